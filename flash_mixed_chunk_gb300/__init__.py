@@ -36,6 +36,8 @@ __all__ = [
     "backward", "flash_mca_gau_project",
     "flash_mca_gau_output",
     "gau_project", "gau_output",
+    "flash_mca_layer_norm", "flash_mca_layer_norm_backward_workspace_bytes",
+    "flash_mca_layer_norm_backward", "layer_norm", "layer_norm_backward",
 ]
 
 FMCA_OK, FMCA_ERR_INVALID_ARG, FMCA_ERR_SHAPE, FMCA_ERR_UNSUPPORTED = 0, 1, 2, 3
@@ -94,6 +96,9 @@ _SIGNATURES = [
     ("flash_mca_backward_workspace_bytes", _sz, [_int] * 6 + [_i32]),
     ("flash_mca_gau_project", _i32, [_vp] * 5 + [_int] * 4 + [_vp]),
     ("flash_mca_gau_output", _i32, [_vp] * 3 + [_int] * 3 + [_vp]),
+    ("flash_mca_layer_norm", _i32, [_vp] * 8 + [_int, _int, ctypes.c_float, _i32, _vp]),
+    ("flash_mca_layer_norm_backward_workspace_bytes", _sz, [_int, _int]),
+    ("flash_mca_layer_norm_backward", _i32, [_vp] * 9 + [_int, _int, _i32, _vp, _sz, _vp]),
     ("flash_mca_backward", _i32, [_vp] * 11 + [_int] * 6 + [_i32, ctypes.POINTER(FmcaOptions),
                                                           _vp, _sz, _vp]),
     ("flash_mca_backward_saved", _i32, [_vp] * 11 + [_int] * 6 +
@@ -507,6 +512,136 @@ def gau_output(Y, Wo_t, stream=None):
     Out = torch.empty((Y.shape[0], Wo_t.shape[0]), dtype=torch.bfloat16, device=Y.device)
     flash_mca_gau_output(Y, Wo_t, Out, stream)
     return Out
+
+
+def _on(name, t, dtype, shape, device) -> int:
+    """The device address of a contiguous tensor of this type and shape on
+    `device`; raises for any other."""
+    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _cuda_device(name, t) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+class _Launch:
+    """Where a call of the training operators runs: the operands' device made
+    current, and `stream` (default: torch's current stream there) made torch's
+    current one, so that what the call allocates belongs to the stream that
+    uses it.  ``with _Launch(device, stream) as ptr``."""
+    __slots__ = ("guards", "ptr")
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is None:
+            self.ptr = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+            elif stream.device != device:
+                raise ValueError(f"stream belongs to {stream.device}, the operands to {device}")
+            self.ptr = stream.cuda_stream
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+        return False
+
+
+def _norm_rows(name, x):
+    """(M, d) of a [..., d] tensor: its leading dimensions are the rows."""
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"{name} must be [..., d] with at least one row")
+    d = x.shape[-1]
+    return x.numel() // d, d
+
+
+def flash_mca_layer_norm(x, res, weight, bias, h, y, mean, rstd, eps: float = 1e-5,
+                         stream=None) -> None:
+    """h = x + res, y = layer norm of h (the C entry point of the same name).
+    x, res, h, y: [..., d] CUDA tensors of one dtype; weight, bias float32 [d];
+    mean, rstd float32 [...] outputs.  res (and then h), mean and rstd may be
+    None; h may be x or res itself."""
+    dev = _cuda_device("x", x)
+    M, d = _norm_rows("x", x)
+    dt, shape, f32 = _dtype_code(x), x.shape, torch.float32
+    if res is not None and h is None:
+        raise ValueError("h must be given with res: the sum is stored there")
+    args = [_on("x", x, x.dtype, shape, dev),
+            None if res is None else _on("res", res, x.dtype, shape, dev),
+            _on("weight", weight, f32, (d,), dev), _on("bias", bias, f32, (d,), dev),
+            None if res is None else _on("h", h, x.dtype, shape, dev),
+            _on("y", y, x.dtype, shape, dev),
+            None if mean is None else _on("mean", mean, f32, shape[:-1], dev),
+            None if rstd is None else _on("rstd", rstd, f32, shape[:-1], dev)]
+    with _Launch(dev, stream) as ptr:
+        st = lib.flash_mca_layer_norm(*args, M, d, eps, dt, ptr)
+    _check(st, "flash_mca_layer_norm")
+
+
+def layer_norm(x, weight, bias, eps: float = 1e-5, residual=None, stream=None):
+    """Allocating wrapper of flash_mca_layer_norm: returns (y, h, mean, rstd),
+    h = x + residual (x itself without a residual)."""
+    with _Launch(_cuda_device("x", x), stream):
+        y = torch.empty_like(x)
+        h = x if residual is None else torch.empty_like(x)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    flash_mca_layer_norm(x, residual, weight, bias, h, y, mean, rstd, eps, stream)
+    return y, h, mean, rstd
+
+
+def flash_mca_layer_norm_backward_workspace_bytes(M: int, d: int) -> int:
+    return int(lib.flash_mca_layer_norm_backward_workspace_bytes(M, d))
+
+
+def flash_mca_layer_norm_backward(dy, h, weight, mean, rstd, dh, dx, dweight, dbias, workspace,
+                                  stream=None) -> None:
+    """Gradients of sum(y * dy) + sum(h * dh) into dx ([..., d]) and dweight,
+    dbias (float32 [d]); h, mean, rstd as flash_mca_layer_norm left them; dh may
+    be None."""
+    dev = _cuda_device("dy", dy)
+    M, d = _norm_rows("dy", dy)
+    dt, shape, f32 = _dtype_code(dy), dy.shape, torch.float32
+    args = [_on("dy", dy, dy.dtype, shape, dev), _on("h", h, dy.dtype, shape, dev),
+            _on("weight", weight, f32, (d,), dev), _on("mean", mean, f32, shape[:-1], dev),
+            _on("rstd", rstd, f32, shape[:-1], dev),
+            None if dh is None else _on("dh", dh, dy.dtype, shape, dev),
+            _on("dx", dx, dy.dtype, shape, dev), _on("dweight", dweight, f32, (d,), dev),
+            _on("dbias", dbias, f32, (d,), dev)]
+    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
+    with _Launch(dev, stream) as ptr:
+        st = lib.flash_mca_layer_norm_backward(*args, M, d, dt, ws, workspace.numel(), ptr)
+    _check(st, "flash_mca_layer_norm_backward")
+
+
+def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, stream=None):
+    """Allocating wrapper of flash_mca_layer_norm_backward: returns
+    (dx, dweight, dbias)."""
+    M, d = _norm_rows("dy", dy)
+    nb = flash_mca_layer_norm_backward_workspace_bytes(M, d)
+    if nb == 0:
+        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_layer_norm_backward_workspace_bytes")
+    with _Launch(_cuda_device("dy", dy), stream):
+        dx = torch.empty_like(dy)
+        dweight = torch.empty(d, dtype=torch.float32, device=dy.device)
+        dbias = torch.empty_like(dweight)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dy.device)
+    flash_mca_layer_norm_backward(dy, h, weight, mean, rstd, dh, dx, dweight, dbias, ws, stream)
+    return dx, dweight, dbias
 
 
 def flash_mca_device_status(stream=None) -> tuple[int, int]:

@@ -1,7 +1,7 @@
 """Build ``libflash_mca.so`` in-tree with nvcc for sm_103a.
 
-Three translation units compile in parallel (the C-ABI layer, the SIMT kernels
-and the tensor-core kernels) and link into one shared library next to this
+The translation units compile in parallel (the C-ABI layer, the SIMT kernels,
+the tensor-core kernels and the layer norm among them) and link into one shared library next to this
 file.  The CUDA runtime is linked statically and the driver's tensor-map
 encoder is looked up at run time, so the library loads on a machine without a
 GPU driver (only calls that touch the device need one).
@@ -24,7 +24,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflash_mca.so")
 
-SOURCES = ["api.cpp", "simt.cu", "tc.cu", "noalloc.cu", "decode.cu", "backward.cu"]
+SOURCES = ["api.cpp", "simt.cu", "tc.cu", "noalloc.cu", "decode.cu", "backward.cu",
+           "api_train.cpp", "norm.cu"]
 HEADERS = ["launch.h", "ptx.cuh", "tc_common.cuh", "tc_prep.cuh", "tc_attn.cuh", "tc_fused.cuh", "tc_walk.cuh", "tc_pair.cuh", "tc_gemm.cuh", "tc_bgemm.cuh", "tc_bwd.cuh", "tc_backward.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

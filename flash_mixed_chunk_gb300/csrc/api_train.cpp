@@ -1,0 +1,110 @@
+// api_train.cpp -- the C ABI of the training operators around the attention
+// core (include/flash_mca.h): argument checks and workspace sizing.  Every
+// check runs before anything is queued; no allocation happens here.
+#include "flash_mca.h"
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "launch.h"
+
+using namespace fmca;
+
+namespace {
+
+struct Span {
+  const void *p;
+  size_t n;
+};
+bool overlap(const Span &a, const Span &b) {
+  if (!a.p || !b.p) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  return a0 < b0 + b.n && b0 < a0 + a.n;
+}
+// outputs must not overlap the inputs or each other
+bool outputs_clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span &o : outs) {
+    for (const Span &i : ins)
+      if (overlap(o, i)) return true;
+    for (const Span &o2 : outs)
+      if (&o2 != &o && overlap(o, o2)) return true;
+  }
+  return false;
+}
+// NULL counts as aligned
+bool aligned(std::initializer_list<const void *> ptrs, uintptr_t to) {
+  for (const void *p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) % to) return false;
+  return true;
+}
+fmca_status done(int rc) { return rc == 0 ? FMCA_OK : FMCA_ERR_CUDA; }
+
+fmca_status norm_sizes(int M, int d) {
+  if (M <= 0 || d <= 0) return FMCA_ERR_INVALID_ARG;
+  if (d > kNormMaxD) return FMCA_ERR_UNSUPPORTED;
+  return FMCA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fmca_status flash_mca_layer_norm(const void *x, const void *res, const float *weight,
+                                 const float *bias, void *h, void *y, float *mean, float *rstd,
+                                 int M, int d, float eps, fmca_dtype dtype,
+                                 fmca_stream_t stream) {
+  const fmca_status st = norm_sizes(M, d);
+  if (st != FMCA_OK) return st;
+  if (dtype != FMCA_F32 && dtype != FMCA_BF16) return FMCA_ERR_INVALID_ARG;
+  if (!x || !weight || !bias || !y || (res && !h)) return FMCA_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.0f) return FMCA_ERR_INVALID_ARG;
+  if (!aligned({x, res, weight, bias, y, mean, rstd}, 16)) return FMCA_ERR_ALIGN;
+  const size_t rows = (size_t)M * d * (dtype == FMCA_BF16 ? 2 : 4);
+  const size_t wb = sizeof(float) * (size_t)d, sb = sizeof(float) * (size_t)M;
+  void *const hh = res ? h : nullptr;  // without a residual branch h is not touched
+  if (!aligned({hh}, 16)) return FMCA_ERR_ALIGN;
+  if (outputs_clash({{y, rows}, {mean, sb}, {rstd, sb}},
+                    {{x, rows}, {res, rows}, {weight, wb}, {bias, wb}, {hh, rows}}))
+    return FMCA_ERR_INVALID_ARG;
+  // h: x or res itself (every thread has read its elements before it writes
+  // them), or apart from every input
+  if (hh && ((hh != x && overlap({hh, rows}, {x, rows})) ||
+             (hh != res && overlap({hh, rows}, {res, rows})) ||
+             overlap({hh, rows}, {weight, wb}) || overlap({hh, rows}, {bias, wb})))
+    return FMCA_ERR_INVALID_ARG;
+  return done(launch_layer_norm(x, res, weight, bias, hh, y, mean, rstd, M, d, eps,
+                                dtype == FMCA_BF16 ? 1 : 0,
+                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t flash_mca_layer_norm_backward_workspace_bytes(int M, int d) {
+  return norm_sizes(M, d) == FMCA_OK ? norm_backward_bytes(M, d) : 0;
+}
+
+fmca_status flash_mca_layer_norm_backward(const void *dy, const void *h, const float *weight,
+                                          const float *mean, const float *rstd, const void *dh,
+                                          void *dx, float *dweight, float *dbias, int M, int d,
+                                          fmca_dtype dtype, void *workspace,
+                                          size_t workspace_bytes_, fmca_stream_t stream) {
+  const fmca_status st = norm_sizes(M, d);
+  if (st != FMCA_OK) return st;
+  if (dtype != FMCA_F32 && dtype != FMCA_BF16) return FMCA_ERR_INVALID_ARG;
+  if (!dy || !h || !weight || !mean || !rstd || !dx || !dweight || !dbias)
+    return FMCA_ERR_INVALID_ARG;
+  if (!aligned({dy, h, weight, mean, rstd, dh, dx, dweight, dbias}, 16)) return FMCA_ERR_ALIGN;
+  if (!workspace || workspace_bytes_ < norm_backward_bytes(M, d)) return FMCA_ERR_WORKSPACE;
+  if (!aligned({workspace}, 256)) return FMCA_ERR_ALIGN;
+  const size_t rows = (size_t)M * d * (dtype == FMCA_BF16 ? 2 : 4);
+  const size_t wb = sizeof(float) * (size_t)d, sb = sizeof(float) * (size_t)M;
+  if (outputs_clash({{dx, rows}, {dweight, wb}, {dbias, wb}, {workspace, workspace_bytes_}},
+                    {{dy, rows}, {h, rows}, {weight, wb}, {mean, sb}, {rstd, sb}, {dh, rows}}))
+    return FMCA_ERR_INVALID_ARG;
+  return done(launch_layer_norm_backward(dy, h, weight, mean, rstd, dh, dx, dweight, dbias, M, d,
+                                         dtype == FMCA_BF16 ? 1 : 0, workspace,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

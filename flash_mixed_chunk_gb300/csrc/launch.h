@@ -269,6 +269,27 @@ int launch_tc_backward(const void *Z, const void *V, const void *U, const float 
                        const Variant &var, void *workspace, cudaStream_t stream,
                        bool saved = false);
 
+// Layer norm (norm.cu).  Rows of up to kNormWarpMaxD elements belong to a
+// warp, longer ones (to kNormMaxD) to a block.  The backward pass deals its
+// rows to norm_backward_blocks blocks, one partial row of dw and db each.
+constexpr int kNormWarpMaxD = 1024, kNormMaxD = 8192;
+constexpr int kNormBackwardBlocks = 304;
+inline int norm_backward_blocks(int M, int d) {
+  const int64_t rows = d <= kNormWarpMaxD ? 8 : 1;
+  const int64_t blocks = ((int64_t)M + rows - 1) / rows;
+  return (int)(blocks < kNormBackwardBlocks ? blocks : kNormBackwardBlocks);
+}
+inline size_t norm_backward_bytes(int M, int d) {
+  return align256(sizeof(float) * 2 * (size_t)d * (size_t)norm_backward_blocks(M, d));
+}
+int launch_layer_norm(const void *x, const void *res, const float *weight, const float *bias,
+                      void *h, void *y, float *mean, float *rstd, int M, int d, float eps,
+                      int dtype_bf16, cudaStream_t stream);
+int launch_layer_norm_backward(const void *dy, const void *h, const float *weight,
+                               const float *mean, const float *rstd, const void *dh, void *dx,
+                               float *dweight, float *dbias, int M, int d, int dtype_bf16,
+                               void *workspace, cudaStream_t stream);
+
 // Shapes the tensor-core path covers.
 bool tc_supported(int B, int n, int s, int e, int C);  // every tensor-core kernel (e % 256)
 bool tc_forward_supported(int B, int n, int s, int e, int C, int lin_norm);  // the forward pass

@@ -1,0 +1,429 @@
+// norm.cu -- layer norm of the residual stream around a GAU layer, forward and
+// backward, for rows [M][d]:
+//
+//   h = x + r (rounded to the I/O type and stored; without r, h = x)
+//   mean = sum_j h_j / d,  var = sum_j (h_j - mean)^2 / d,  rstd = (var + eps)^-1/2
+//   xhat = (h - mean) rstd,  y = xhat w + b
+//
+//   t = dy w,  dx = rstd (t - mean_j t - xhat mean_j (t xhat)) + dh
+//   dw = sum_rows dy xhat,  db = sum_rows dy
+//
+// Bound by the bytes: a forward row is read once and written once (with a
+// residual branch two reads, two writes), so a row lives in registers from its
+// load to its store and the variance is the two-pass one (deviations from the
+// mean, no difference of large squares).  All arithmetic is fp32; h is rounded
+// before its statistics are taken, so that the backward pass, which reads the
+// stored h, differentiates exactly what the forward pass normalised.
+//
+// A row belongs to one warp (d <= 1024) or to one block of 256 threads (d <=
+// 8192): 8, 16, 24 or 32 elements a thread, in 16-byte vectors where d allows
+// it, else 4-byte ones, else single elements.
+//
+// The backward pass keeps dw and db of the rows it has seen in registers, one
+// partial row a block in the workspace, and a second kernel adds the partial
+// rows in a fixed order (no atomics: the same bits every time).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace fmca {
+namespace {
+
+constexpr int kNormThreads = 256;
+
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<16> { using type = uint4; };
+template <>
+struct Raw<4> { using type = uint32_t; };
+template <>
+struct Raw<2> { using type = uint16_t; };
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+template <typename T, int VEC>
+struct Pack {
+  using raw_t = typename Raw<(int)sizeof(T) * VEC>::type;
+  union {
+    raw_t raw;
+    T v[VEC];
+  };
+  __device__ Pack() {}
+};
+
+// One vector of a row through the default cache path, and back.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T *p, float *out) {
+  Pack<T, VEC> k;
+  k.raw = *reinterpret_cast<const typename Pack<T, VEC>::raw_t *>(p);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) out[i] = to_f(k.v[i]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T *p, const float *in) {
+  Pack<T, VEC> k;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) k.v[i] = from_f<T>(in[i]);
+  *reinterpret_cast<typename Pack<T, VEC>::raw_t *>(p) = k.raw;
+}
+// VEC fp32 weights (column offset a multiple of VEC)
+template <int VEC>
+__device__ __forceinline__ void load_w(const float *__restrict__ p, float *out) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(p) + i);
+      out[4 * i] = v.x, out[4 * i + 1] = v.y, out[4 * i + 2] = v.z, out[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) out[i] = __ldg(p + i);
+  }
+}
+
+// Sum of v over the threads of a row's group: a warp, or the whole block (two
+// alternating sets of shared words, so that one barrier a sum is enough).
+template <int GROUP>
+__device__ __forceinline__ float group_sum(float v, float (*red)[kNormThreads / 32], int &turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (GROUP > 32) {
+    float *r = red[turn];
+    turn ^= 1;
+    if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < GROUP / 32; ++i) v += r[i];
+  }
+  return v;
+}
+
+// T: I/O type; VEC elements a vector, N vectors a thread; GROUP threads a row.
+template <typename T, int VEC, int N, int GROUP>
+__global__ void __launch_bounds__(kNormThreads)
+    norm_forward(const T *x, const T *res, const float *__restrict__ weight,
+                 const float *__restrict__ bias, T *h, T *__restrict__ y,
+                 float *__restrict__ mean_out, float *__restrict__ rstd_out, int M, int d,
+                 float eps) {
+  __shared__ float red[2][kNormThreads / 32];
+  int turn = 0;
+  const int lane = threadIdx.x % GROUP;
+  const int64_t row = (int64_t)blockIdx.x * (kNormThreads / GROUP) + threadIdx.x / GROUP;
+  if (row >= M) return;  // whole groups (a block is one row when GROUP is a block)
+  const int nv = d / VEC;
+  const T *xr = x + row * d;
+  float v[N * VEC];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = lane + i * GROUP;
+    if (c < nv) {
+      load_vec<T, VEC>(xr + (int64_t)c * VEC, v + i * VEC);
+    } else {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) v[i * VEC + k] = 0.f;
+    }
+  }
+  if (res != nullptr) {
+    const T *rr = res + row * d;
+    T *hr = h + row * d;
+    float r[N * VEC];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * GROUP;
+      if (c < nv) load_vec<T, VEC>(rr + (int64_t)c * VEC, r + i * VEC);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * GROUP;
+      if (c < nv) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)  // the statistics are those of the stored sum
+          v[i * VEC + k] = to_f(from_f<T>(v[i * VEC + k] + r[i * VEC + k]));
+        store_vec<T, VEC>(hr + (int64_t)c * VEC, v + i * VEC);
+      }
+    }
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < N * VEC; ++i) s += v[i];
+  const float inv_d = 1.0f / (float)d;
+  const float mean = group_sum<GROUP>(s, red, turn) * inv_d;
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = lane + i * GROUP;
+    if (c < nv) {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const float t = v[i * VEC + k] - mean;
+        q += t * t;
+      }
+    }
+  }
+  const float rstd = 1.0f / sqrtf(group_sum<GROUP>(q, red, turn) * inv_d + eps);
+  T *yr = y + row * d;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = lane + i * GROUP;
+    if (c < nv) {
+      float w[VEC], b[VEC], o[VEC];
+      load_w<VEC>(weight + c * VEC, w);
+      load_w<VEC>(bias + c * VEC, b);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) o[k] = (v[i * VEC + k] - mean) * rstd * w[k] + b[k];
+      store_vec<T, VEC>(yr + (int64_t)c * VEC, o);
+    }
+  }
+  if (lane == 0) {
+    if (mean_out != nullptr) mean_out[row] = mean;
+    if (rstd_out != nullptr) rstd_out[row] = rstd;
+  }
+}
+
+// dx, and the block's sums of dw and db: part [blocks][2][d].  Rows are dealt
+// to the groups round-robin.
+template <typename T, int VEC, int N, int GROUP>
+__global__ void __launch_bounds__(kNormThreads)
+    norm_backward(const T *__restrict__ dy, const T *__restrict__ h,
+                  const float *__restrict__ weight, const float *__restrict__ mean_in,
+                  const float *__restrict__ rstd_in, const T *__restrict__ dh,
+                  T *__restrict__ dx, float *__restrict__ part, int M, int d) {
+  __shared__ float red[2][kNormThreads / 32];
+  extern __shared__ float acc_s[];  // [2][d] when a block holds several groups
+  int turn = 0;
+  constexpr int kRows = kNormThreads / GROUP;
+  const int lane = threadIdx.x % GROUP, grp = threadIdx.x / GROUP;
+  const int nv = d / VEC;
+  const float inv_d = 1.0f / (float)d;
+  float dw[N * VEC], db[N * VEC];
+#pragma unroll
+  for (int i = 0; i < N * VEC; ++i) dw[i] = 0.f, db[i] = 0.f;
+  for (int64_t row = (int64_t)blockIdx.x * kRows + grp; row < M;
+       row += (int64_t)gridDim.x * kRows) {
+    const float mean = mean_in[row], rstd = rstd_in[row];
+    float g[N * VEC], xh[N * VEC];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * GROUP;
+      if (c < nv) {
+        load_vec<T, VEC>(dy + row * d + (int64_t)c * VEC, g + i * VEC);
+        load_vec<T, VEC>(h + row * d + (int64_t)c * VEC, xh + i * VEC);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) g[i * VEC + k] = 0.f, xh[i * VEC + k] = mean;
+      }
+    }
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * GROUP;
+      float w[VEC];
+      if (c < nv) {
+        load_w<VEC>(weight + c * VEC, w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) w[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const int e = i * VEC + k;
+        xh[e] = (xh[e] - mean) * rstd;
+        dw[e] += g[e] * xh[e];
+        db[e] += g[e];
+        g[e] *= w[k];
+        s1 += g[e];
+        s2 += g[e] * xh[e];
+      }
+    }
+    const float m1 = group_sum<GROUP>(s1, red, turn) * inv_d;
+    const float m2 = group_sum<GROUP>(s2, red, turn) * inv_d;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * GROUP;
+      if (c < nv) {
+        float o[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          const int e = i * VEC + k;
+          o[k] = rstd * (g[e] - m1 - xh[e] * m2);
+        }
+        if (dh != nullptr) {
+          float r[VEC];
+          load_vec<T, VEC>(dh + row * d + (int64_t)c * VEC, r);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) o[k] += r[k];
+        }
+        store_vec<T, VEC>(dx + row * d + (int64_t)c * VEC, o);
+      }
+    }
+  }
+  float *pw = part + (int64_t)blockIdx.x * 2 * d, *pb = pw + d;
+  if constexpr (GROUP == kNormThreads) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * GROUP;
+      if (c < nv)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          pw[c * VEC + k] = dw[i * VEC + k];
+          pb[c * VEC + k] = db[i * VEC + k];
+        }
+    }
+  } else {
+    // the groups add their sums one after the other (a fixed order)
+    for (int q = 0; q < kRows; ++q) {
+      if (grp == q) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int c = lane + i * GROUP;
+          if (c < nv)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+              const int j = c * VEC + k;
+              acc_s[j] = (q ? acc_s[j] : 0.f) + dw[i * VEC + k];
+              acc_s[d + j] = (q ? acc_s[d + j] : 0.f) + db[i * VEC + k];
+            }
+        }
+      }
+      __syncthreads();
+    }
+    for (int j = threadIdx.x; j < 2 * d; j += kNormThreads) pw[j] = acc_s[j];
+  }
+}
+
+// dw and db from the blocks' partial rows: a block sums 32 columns, 8 row
+// lanes of partial rows each, lanes joined in order.
+constexpr int kNormSumCols = 32, kNormSumLanes = 32;
+__global__ void __launch_bounds__(kNormSumCols *kNormSumLanes)
+    norm_backward_sum(const float *__restrict__ part, float *__restrict__ dweight,
+                      float *__restrict__ dbias, int blocks, int d) {
+  __shared__ float s[kNormSumLanes][kNormSumCols + 1];
+  griddep_wait();
+  const int col = threadIdx.x % kNormSumCols, r = threadIdx.x / kNormSumCols;
+  const int j = blockIdx.x * kNormSumCols + col;
+  float v = 0.f;
+  if (j < 2 * d)
+    for (int b = r; b < blocks; b += kNormSumLanes) v += part[(int64_t)b * 2 * d + j];
+  s[r][col] = v;
+  __syncthreads();
+  if (r == 0 && j < 2 * d) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNormSumLanes; ++i) t += s[i][col];
+    (j < d ? dweight[j] : dbias[j - d]) = t;
+  }
+}
+
+struct NormArgs {
+  const void *a, *b;  // forward: x, res; backward: dy, h
+  const float *weight, *bias, *mean, *rstd;
+  const void *dh;
+  void *o0, *o1;      // forward: h, y; backward: dx, -
+  float *f0, *f1;     // forward: mean, rstd; backward: part, -
+  int M, d;
+  float eps;
+  int blocks;
+};
+
+template <typename T, int VEC, int N, int GROUP>
+cudaError_t launch_fwd(const NormArgs &a, cudaStream_t stream) {
+  norm_forward<T, VEC, N, GROUP><<<a.blocks, kNormThreads, 0, stream>>>(
+      static_cast<const T *>(a.a), static_cast<const T *>(a.b), a.weight, a.bias,
+      static_cast<T *>(a.o0), static_cast<T *>(a.o1), a.f0, a.f1, a.M, a.d, a.eps);
+  return cudaGetLastError();
+}
+template <typename T, int VEC, int N, int GROUP>
+cudaError_t launch_bwd(const NormArgs &a, cudaStream_t stream) {
+  const size_t smem = GROUP < kNormThreads ? 2 * sizeof(float) * (size_t)a.d : 0;
+  norm_backward<T, VEC, N, GROUP><<<a.blocks, kNormThreads, smem, stream>>>(
+      static_cast<const T *>(a.a), static_cast<const T *>(a.b), a.weight, a.mean, a.rstd,
+      static_cast<const T *>(a.dh), static_cast<T *>(a.o0), a.f0, a.M, a.d);
+  return cudaGetLastError();
+}
+
+// Elements a thread: the fewest of 8, 16, 24, 32 that cover the row.
+template <typename T, int VEC, int GROUP, bool kBackward>
+cudaError_t pick_n(const NormArgs &a, cudaStream_t stream) {
+  const int per = (a.d + GROUP * 8 - 1) / (GROUP * 8);  // eights of elements a thread
+#define FMCA_NORM(E)                                                        \
+  return kBackward ? launch_bwd<T, VEC, (E) / VEC, GROUP>(a, stream)        \
+                   : launch_fwd<T, VEC, (E) / VEC, GROUP>(a, stream)
+  switch (per) {
+    case 1: FMCA_NORM(8);
+    case 2: FMCA_NORM(16);
+    case 3: FMCA_NORM(24);
+    default: FMCA_NORM(32);
+  }
+#undef FMCA_NORM
+}
+template <typename T, int VEC, bool kBackward>
+cudaError_t pick_group(const NormArgs &a, cudaStream_t stream) {
+  return a.d <= kNormWarpMaxD ? pick_n<T, VEC, 32, kBackward>(a, stream)
+                              : pick_n<T, VEC, kNormThreads, kBackward>(a, stream);
+}
+template <bool kBackward>
+cudaError_t pick(const NormArgs &a, int bf16, cudaStream_t stream) {
+  if (bf16) {
+    if (a.d % 8 == 0) return pick_group<__nv_bfloat16, 8, kBackward>(a, stream);
+    if (a.d % 2 == 0) return pick_group<__nv_bfloat16, 2, kBackward>(a, stream);
+    return pick_group<__nv_bfloat16, 1, kBackward>(a, stream);
+  }
+  if (a.d % 4 == 0) return pick_group<float, 4, kBackward>(a, stream);
+  return pick_group<float, 1, kBackward>(a, stream);
+}
+
+}  // namespace
+
+int launch_layer_norm(const void *x, const void *res, const float *weight, const float *bias,
+                      void *h, void *y, float *mean, float *rstd, int M, int d, float eps,
+                      int dtype_bf16, cudaStream_t stream) {
+  NormArgs a = {};
+  a.a = x, a.b = res, a.weight = weight, a.bias = bias;
+  a.o0 = h, a.o1 = y, a.f0 = mean, a.f1 = rstd;
+  a.M = M, a.d = d, a.eps = eps;
+  const int rows = d <= kNormWarpMaxD ? kNormThreads / 32 : 1;
+  a.blocks = (int)(((int64_t)M + rows - 1) / rows);
+  return pick<false>(a, dtype_bf16, stream) == cudaSuccess ? 0 : 1;
+}
+
+int launch_layer_norm_backward(const void *dy, const void *h, const float *weight,
+                               const float *mean, const float *rstd, const void *dh, void *dx,
+                               float *dweight, float *dbias, int M, int d, int dtype_bf16,
+                               void *workspace, cudaStream_t stream) {
+  NormArgs a = {};
+  a.a = dy, a.b = h, a.weight = weight, a.mean = mean, a.rstd = rstd, a.dh = dh;
+  a.o0 = dx, a.f0 = static_cast<float *>(workspace);
+  a.M = M, a.d = d;
+  a.blocks = norm_backward_blocks(M, d);
+  if (pick<true>(a, dtype_bf16, stream) != cudaSuccess) return 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((2 * d + kNormSumCols - 1) / kNormSumCols);
+  cfg.blockDim = dim3(kNormSumCols * kNormSumLanes);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_backward_sum, (const float *)a.f0, dweight, dbias, a.blocks,
+                            d) == cudaSuccess
+             ? 0
+             : 1;
+}
+
+}  // namespace fmca

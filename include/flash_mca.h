@@ -369,6 +369,48 @@ fmca_status flash_mca_gau_project(const void *X, const void *Wt, void *U, void *
 fmca_status flash_mca_gau_output(const void *Y, const void *Wo_t, void *Out, int M, int e,
                                  int d, fmca_stream_t stream);
 
+/*
+ * Layer norm of the residual stream around a GAU layer, over rows [M][d]:
+ *   h = x + res (rounded to `dtype` and stored; res NULL: h = x)
+ *   y = (h - mean) * rstd * weight + bias, mean and variance over the row's d
+ *       elements (the variance divided by d), rstd = 1 / sqrt(variance + eps)
+ *   x, res, h, y   device arrays [M][d] of `dtype`, 16-byte aligned; res may
+ *                  be NULL, and h then is not written and may be NULL
+ *   weight, bias   device float32 [d]
+ *   mean, rstd     device float32 [M] outputs, each NULL when not wanted (the
+ *                  backward pass reads both)
+ * h may be x or res itself (the residual stream updated in place); no other
+ * output may overlap an input or another output.  fp32 arithmetic; the
+ * statistics are those of the stored h.  One launch, nothing allocated, any
+ * number of rows (a single decoded token is M = 1).
+ * Sizes: M >= 1, 1 <= d <= 8192; eps finite and >= 0 (a constant row with eps
+ * 0 has rstd infinite and y NaN).
+ */
+fmca_status flash_mca_layer_norm(const void *x, const void *res, const float *weight,
+                                 const float *bias, void *h, void *y, float *mean, float *rstd,
+                                 int M, int d, float eps, fmca_dtype dtype,
+                                 fmca_stream_t stream);
+
+/*
+ * Gradients of sum(y * dy) + sum(h * dh) for that y and h:
+ *   dx       d(x) = d(res) = rstd (t - mean(t) - xhat mean(t xhat)) + dh, with
+ *            t = dy * weight and xhat = (h - mean) * rstd; [M][d] of `dtype`
+ *   dweight  sum over the rows of dy * xhat, float32 [d]
+ *   dbias    sum over the rows of dy, float32 [d]
+ * dy, h and dh [M][d] of `dtype`, mean and rstd as flash_mca_layer_norm left
+ * them; dh (the residual stream's own gradient) may be NULL.  The outputs
+ * must not overlap the inputs, the workspace or each other.  Two launches;
+ * fixed summation order (deterministic).  workspace: at least
+ * flash_mca_layer_norm_backward_workspace_bytes(M, d) bytes, 256-byte aligned
+ * (0 bytes stands for sizes that would be rejected).
+ */
+size_t flash_mca_layer_norm_backward_workspace_bytes(int M, int d);
+fmca_status flash_mca_layer_norm_backward(const void *dy, const void *h, const float *weight,
+                                          const float *mean, const float *rstd, const void *dh,
+                                          void *dx, float *dweight, float *dbias, int M, int d,
+                                          fmca_dtype dtype, void *workspace,
+                                          size_t workspace_bytes, fmca_stream_t stream);
+
 /* Which path FMCA_PATH_AUTO takes for these arguments (FMCA_PATH_SIMT or
  * FMCA_PATH_TCGEN05), or -1 for arguments that would be rejected. */
 int flash_mca_auto_path(int B, int n, int s, int e, int C, int causal, fmca_dtype dtype);

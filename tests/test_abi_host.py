@@ -387,3 +387,61 @@ def test_forward_seq_rejects_before_queueing():
     assert call(1, -256) == fm.FMCA_ERR_INVALID_ARG
     assert call(1, 0, s_in=state + 4) == fm.FMCA_ERR_ALIGN
     assert call(1, 0, s_out=o) == fm.FMCA_ERR_INVALID_ARG             # state_out overlaps O
+
+
+def test_layer_norm_rejects_before_queueing():
+    """flash_mca_layer_norm and its backward pass: argument checks on the host.
+    The pointers here are never dereferenced."""
+    P = 0x7F0000000000
+    x, r, w, b, h, y, mn, rs = [P + (k << 24) for k in range(8)]
+    bf = fm.FMCA_BF16
+
+    def fwd(x=x, r=r, w=w, b=b, h=h, y=y, mn=mn, rs=rs, M=0, d=64, eps=1e-5, dt=bf):
+        return fm.lib.flash_mca_layer_norm(x, r, w, b, h, y, mn, rs, M, d, eps, dt, None)
+    assert fwd() == fm.FMCA_ERR_INVALID_ARG                      # no rows
+    assert fwd(M=4, d=0) == fm.FMCA_ERR_INVALID_ARG
+    assert fwd(M=4, d=8193) == fm.FMCA_ERR_UNSUPPORTED
+    assert fwd(M=4, dt=2) == fm.FMCA_ERR_INVALID_ARG
+    assert fwd(M=4, eps=-1.0) == fm.FMCA_ERR_INVALID_ARG
+    assert fwd(M=4, eps=float("nan")) == fm.FMCA_ERR_INVALID_ARG
+    for k in ("x", "w", "b", "y", "h"):                          # h: needed with a residual
+        assert fwd(M=4, **{k: None}) == fm.FMCA_ERR_INVALID_ARG
+    for k, v in (("x", x), ("r", r), ("w", w), ("b", b), ("h", h), ("y", y), ("mn", mn)):
+        assert fwd(M=4, **{k: v + 8}) == fm.FMCA_ERR_ALIGN
+    for k, v in (("y", x), ("y", r), ("y", h), ("h", x + 128), ("h", r - 128), ("h", w), ("mn", rs),
+                 ("rs", y)):
+        assert fwd(M=4, **{k: v}) == fm.FMCA_ERR_INVALID_ARG     # overlaps
+
+    nb = fm.flash_mca_layer_norm_backward_workspace_bytes
+    # one partial row of dw and db a block: 8 rows a block up to d = 1024, one
+    # beyond, 304 blocks at most
+    up = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    assert nb(1, 768) == up(8 * 768) and nb(17, 768) == up(3 * 8 * 768)
+    assert nb(100000, 768) == up(304 * 8 * 768) and nb(5, 1025) == up(5 * 8 * 1025)
+    assert nb(0, 768) == 0 and nb(4, 0) == 0 and nb(4, 8193) == 0
+
+    dy, hh, dh, dx, dw, db, ws = [P + (k << 24) for k in range(8, 15)]
+
+    def bwd(dy=dy, hh=hh, w=w, mn=mn, rs=rs, dh=dh, dx=dx, dw=dw, db=db, M=4, d=64, dt=bf, ws=ws,
+            size=1 << 20):
+        return fm.lib.flash_mca_layer_norm_backward(dy, hh, w, mn, rs, dh, dx, dw, db, M, d, dt, ws,
+                                                    size, None)
+    assert bwd(M=0) == fm.FMCA_ERR_INVALID_ARG and bwd(d=9000) == fm.FMCA_ERR_UNSUPPORTED
+    assert bwd(dt=7) == fm.FMCA_ERR_INVALID_ARG
+    for k in ("dy", "hh", "w", "mn", "rs", "dx", "dw", "db"):
+        assert bwd(**{k: None}) == fm.FMCA_ERR_INVALID_ARG
+    assert bwd(ws=None) == fm.FMCA_ERR_WORKSPACE and bwd(size=100) == fm.FMCA_ERR_WORKSPACE
+    assert bwd(ws=ws + 16) == fm.FMCA_ERR_ALIGN and bwd(dh=dh + 4) == fm.FMCA_ERR_ALIGN
+    for k, v in (("dx", dy), ("dx", dh), ("dw", db), ("db", ws), ("dx", ws), ("dw", w), ("ws", hh)):
+        assert bwd(**{k: v}) == fm.FMCA_ERR_INVALID_ARG
+
+
+def test_training_wrappers_refuse_host_tensors():
+    import torch
+    x, w = torch.zeros(2, 8), torch.zeros(8)
+    with pytest.raises(ValueError, match="CUDA"):
+        fm.layer_norm(x, w, w)
+    with pytest.raises(ValueError, match="CUDA"):
+        fm.layer_norm_backward(x, x, w, torch.zeros(2), torch.zeros(2))
+    with pytest.raises(ValueError, match="row"):
+        fm.layer_norm_backward(torch.zeros(0, 8), x, w, w, w)
