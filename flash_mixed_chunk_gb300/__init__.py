@@ -38,6 +38,12 @@ __all__ = [
     "gau_project", "gau_output",
     "flash_mca_layer_norm", "flash_mca_layer_norm_backward_workspace_bytes",
     "flash_mca_layer_norm_backward", "layer_norm", "layer_norm_backward",
+    "flash_mca_gau_project_backward_workspace_bytes", "flash_mca_gau_project_backward",
+    "flash_mca_gau_output_backward_workspace_bytes", "flash_mca_gau_output_backward",
+    "gau_project_backward", "gau_output_backward",
+    "flash_mca_vocab_loss_workspace_bytes", "flash_mca_vocab_loss",
+    "flash_mca_vocab_loss_backward_workspace_bytes", "flash_mca_vocab_loss_backward",
+    "vocab_loss", "vocab_loss_backward",
 ]
 
 FMCA_OK, FMCA_ERR_INVALID_ARG, FMCA_ERR_SHAPE, FMCA_ERR_UNSUPPORTED = 0, 1, 2, 3
@@ -96,6 +102,14 @@ _SIGNATURES = [
     ("flash_mca_backward_workspace_bytes", _sz, [_int] * 6 + [_i32]),
     ("flash_mca_gau_project", _i32, [_vp] * 5 + [_int] * 4 + [_vp]),
     ("flash_mca_gau_output", _i32, [_vp] * 3 + [_int] * 3 + [_vp]),
+    ("flash_mca_gau_project_backward_workspace_bytes", _sz, [_int] * 4),
+    ("flash_mca_gau_project_backward", _i32, [_vp] * 7 + [_int] * 4 + [_vp, _sz, _vp]),
+    ("flash_mca_gau_output_backward_workspace_bytes", _sz, [_int] * 3),
+    ("flash_mca_gau_output_backward", _i32, [_vp] * 5 + [_int] * 3 + [_vp, _sz, _vp]),
+    ("flash_mca_vocab_loss_workspace_bytes", _sz, [_int] * 3),
+    ("flash_mca_vocab_loss", _i32, [_vp] * 5 + [_int] * 3 + [_vp, _sz, _vp]),
+    ("flash_mca_vocab_loss_backward_workspace_bytes", _sz, [_int] * 3),
+    ("flash_mca_vocab_loss_backward", _i32, [_vp] * 7 + [_int] * 3 + [_vp, _sz, _vp]),
     ("flash_mca_layer_norm", _i32, [_vp] * 8 + [_int, _int, ctypes.c_float, _i32, _vp]),
     ("flash_mca_layer_norm_backward_workspace_bytes", _sz, [_int, _int]),
     ("flash_mca_layer_norm_backward", _i32, [_vp] * 9 + [_int, _int, _i32, _vp, _sz, _vp]),
@@ -642,6 +656,141 @@ def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, stream=None):
         ws = torch.empty(nb, dtype=torch.uint8, device=dy.device)
     flash_mca_layer_norm_backward(dy, h, weight, mean, rstd, dh, dx, dweight, dbias, ws, stream)
     return dx, dweight, dbias
+
+
+def _matrix(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
+
+
+def flash_mca_gau_project_backward_workspace_bytes(M: int, d: int, e: int, s: int) -> int:
+    return int(lib.flash_mca_gau_project_backward_workspace_bytes(M, d, e, s))
+
+
+def flash_mca_gau_project_backward(X, Wt, dU, dV, dZ, dX, dWt, workspace, stream=None) -> None:
+    """Gradients dX [M, d], dWt [2e+s, d] of flash_mca_gau_project for dU, dV
+    [M, e] and dZ [M, s]; bf16 CUDA tensors."""
+    dev, bf = _cuda_device("X", X), torch.bfloat16
+    (M, d), (_, e), (_, s) = _matrix("X", X), _matrix("dU", dU), _matrix("dZ", dZ)
+    args = [_on("X", X, bf, (M, d), dev), _on("Wt", Wt, bf, (2 * e + s, d), dev),
+            _on("dU", dU, bf, (M, e), dev), _on("dV", dV, bf, (M, e), dev),
+            _on("dZ", dZ, bf, (M, s), dev), _on("dX", dX, bf, (M, d), dev),
+            _on("dWt", dWt, bf, (2 * e + s, d), dev)]
+    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
+    with _Launch(dev, stream) as ptr:
+        st = lib.flash_mca_gau_project_backward(*args, M, d, e, s, ws, workspace.numel(), ptr)
+    _check(st, "flash_mca_gau_project_backward")
+
+
+def gau_project_backward(X, Wt, dU, dV, dZ, stream=None):
+    """Allocating wrapper of flash_mca_gau_project_backward: returns (dX, dWt)."""
+    (M, d), (_, e), (_, s) = _matrix("X", X), _matrix("dU", dU), _matrix("dZ", dZ)
+    nb = flash_mca_gau_project_backward_workspace_bytes(M, d, e, s)
+    if nb == 0:
+        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_gau_project_backward_workspace_bytes")
+    with _Launch(_cuda_device("X", X), stream):
+        dX, dWt = torch.empty_like(X), torch.empty_like(Wt)
+        ws = torch.empty(nb, dtype=torch.uint8, device=X.device)
+    flash_mca_gau_project_backward(X, Wt, dU, dV, dZ, dX, dWt, ws, stream)
+    return dX, dWt
+
+
+def flash_mca_gau_output_backward_workspace_bytes(M: int, e: int, d: int) -> int:
+    return int(lib.flash_mca_gau_output_backward_workspace_bytes(M, e, d))
+
+
+def flash_mca_gau_output_backward(Y, Wo_t, dOut, dY, dWo_t, workspace, stream=None) -> None:
+    """Gradients dY [M, e], dWo_t [d, e] of flash_mca_gau_output for dOut
+    [M, d]; bf16 CUDA tensors."""
+    dev, bf = _cuda_device("Y", Y), torch.bfloat16
+    (M, e), (_, d) = _matrix("Y", Y), _matrix("dOut", dOut)
+    args = [_on("Y", Y, bf, (M, e), dev), _on("Wo_t", Wo_t, bf, (d, e), dev),
+            _on("dOut", dOut, bf, (M, d), dev), _on("dY", dY, bf, (M, e), dev),
+            _on("dWo_t", dWo_t, bf, (d, e), dev)]
+    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
+    with _Launch(dev, stream) as ptr:
+        st = lib.flash_mca_gau_output_backward(*args, M, e, d, ws, workspace.numel(), ptr)
+    _check(st, "flash_mca_gau_output_backward")
+
+
+def gau_output_backward(Y, Wo_t, dOut, stream=None):
+    """Allocating wrapper of flash_mca_gau_output_backward: returns (dY, dWo_t)."""
+    (M, e), (_, d) = _matrix("Y", Y), _matrix("dOut", dOut)
+    nb = flash_mca_gau_output_backward_workspace_bytes(M, e, d)
+    if nb == 0:
+        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_gau_output_backward_workspace_bytes")
+    with _Launch(_cuda_device("Y", Y), stream):
+        dY, dWo_t = torch.empty_like(Y), torch.empty_like(Wo_t)
+        ws = torch.empty(nb, dtype=torch.uint8, device=Y.device)
+    flash_mca_gau_output_backward(Y, Wo_t, dOut, dY, dWo_t, ws, stream)
+    return dY, dWo_t
+
+
+def flash_mca_vocab_loss_workspace_bytes(M: int, V: int, d: int) -> int:
+    return int(lib.flash_mca_vocab_loss_workspace_bytes(M, V, d))
+
+
+def flash_mca_vocab_loss(X, W, target, loss, lse, workspace, stream=None) -> None:
+    """Softmax cross entropy of X [M, d] against the vocabulary W [V, d] (bf16)
+    into loss and lse (float32 [M]); target int64 [M], rows whose target is
+    outside 0 .. V - 1 are ignored (loss and lse 0)."""
+    dev, bf = _cuda_device("X", X), torch.bfloat16
+    (M, d), (V, _) = _matrix("X", X), _matrix("W", W)
+    args = [_on("X", X, bf, (M, d), dev), _on("W", W, bf, (V, d), dev),
+            _on("target", target, torch.int64, (M,), dev),
+            _on("loss", loss, torch.float32, (M,), dev), _on("lse", lse, torch.float32, (M,), dev)]
+    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
+    with _Launch(dev, stream) as ptr:
+        st = lib.flash_mca_vocab_loss(*args, M, V, d, ws, workspace.numel(), ptr)
+    _check(st, "flash_mca_vocab_loss")
+
+
+def vocab_loss(X, W, target, stream=None):
+    """Allocating wrapper of flash_mca_vocab_loss: returns (loss, lse)."""
+    (M, d), (V, _) = _matrix("X", X), _matrix("W", W)
+    nb = flash_mca_vocab_loss_workspace_bytes(M, V, d)
+    if nb == 0:
+        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_vocab_loss_workspace_bytes")
+    with _Launch(_cuda_device("X", X), stream):
+        loss = torch.empty(M, dtype=torch.float32, device=X.device)
+        lse = torch.empty_like(loss)
+        ws = torch.empty(nb, dtype=torch.uint8, device=X.device)
+    flash_mca_vocab_loss(X, W, target, loss, lse, ws, stream)
+    return loss, lse
+
+
+def flash_mca_vocab_loss_backward_workspace_bytes(M: int, V: int, d: int) -> int:
+    return int(lib.flash_mca_vocab_loss_backward_workspace_bytes(M, V, d))
+
+
+def flash_mca_vocab_loss_backward(X, W, target, lse, dloss, dX, dW, workspace,
+                                  stream=None) -> None:
+    """Gradients of sum(loss * dloss) into dX [M, d] and dW [V, d] (bf16); lse
+    as flash_mca_vocab_loss left it, dloss float32 [M]."""
+    dev, bf, f32 = _cuda_device("X", X), torch.bfloat16, torch.float32
+    (M, d), (V, _) = _matrix("X", X), _matrix("W", W)
+    args = [_on("X", X, bf, (M, d), dev), _on("W", W, bf, (V, d), dev),
+            _on("target", target, torch.int64, (M,), dev), _on("lse", lse, f32, (M,), dev),
+            _on("dloss", dloss, f32, (M,), dev), _on("dX", dX, bf, (M, d), dev),
+            _on("dW", dW, bf, (V, d), dev)]
+    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
+    with _Launch(dev, stream) as ptr:
+        st = lib.flash_mca_vocab_loss_backward(*args, M, V, d, ws, workspace.numel(), ptr)
+    _check(st, "flash_mca_vocab_loss_backward")
+
+
+def vocab_loss_backward(X, W, target, lse, dloss, stream=None):
+    """Allocating wrapper of flash_mca_vocab_loss_backward: returns (dX, dW)."""
+    (M, d), (V, _) = _matrix("X", X), _matrix("W", W)
+    nb = flash_mca_vocab_loss_backward_workspace_bytes(M, V, d)
+    if nb == 0:
+        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_vocab_loss_backward_workspace_bytes")
+    with _Launch(_cuda_device("X", X), stream):
+        dX, dW = torch.empty_like(X), torch.empty_like(W)
+        ws = torch.empty(nb, dtype=torch.uint8, device=X.device)
+    flash_mca_vocab_loss_backward(X, W, target, lse, dloss, dX, dW, ws, stream)
+    return dX, dW
 
 
 def flash_mca_device_status(stream=None) -> tuple[int, int]:

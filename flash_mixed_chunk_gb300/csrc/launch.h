@@ -290,6 +290,101 @@ int launch_layer_norm_backward(const void *dy, const void *h, const float *weigh
                                float *dweight, float *dbias, int M, int d, int dtype_bf16,
                                void *workspace, cudaStream_t stream);
 
+// Training operators on the tensor cores (tc_train.cuh).  Their products run
+// on at most kTgMaxCtas CTAs; a product whose depth is split keeps one fp32
+// tile of 128 x 256 a part, no more parts than CTAs.
+constexpr int kTgMaxCtas = 152;
+constexpr size_t kTgSlotBytes = 4 * 128 * 256;
+inline size_t tg_tiles(size_t M, size_t N) {  // 128 x 256 tiles (rows in pairs)
+  return 2 * ((M + 255) / 256) * ((N + 255) / 256);
+}
+inline size_t tg_slot_bytes() { return kTgMaxCtas * kTgSlotBytes; }
+// Boxes of 64 tokens x 64 columns for all N columns of M tokens.
+inline int64_t tg_boxes(int M, int N) {
+  return (int64_t)(((int64_t)M + 255) / 256 * 4) * (((int64_t)N + 255) / 256 * 4);
+}
+
+// Vocabulary loss: header, compact rows (index, target, X), the target's
+// logit, and the partial maxima and sums [2 ceil(V / 256)][M] fp32 pairs.
+struct VocabLossLayout {
+  size_t hdr, idx, tgt, ztgt, Xc, part, total;
+};
+inline VocabLossLayout vocab_loss_layout(int M, int V, int d) {
+  VocabLossLayout L;
+  L.hdr = 0;
+  L.idx = 256;
+  L.tgt = L.idx + align256(4 * (size_t)M);
+  L.ztgt = L.tgt + align256(4 * (size_t)M);
+  L.Xc = L.ztgt + align256(4 * (size_t)M);
+  L.part = L.Xc + align256(2 * (size_t)M * d);
+  L.total = L.part + align256(8 * (size_t)M * 2 * (((size_t)V + 255) / 256));
+  return L;
+}
+
+// Its gradients: the same compact rows with their lse and dloss, the boxes of
+// one piece of the vocabulary and the fp32 tiles (dW's parts; dX's parts, or
+// its sums over the pieces).  A piece's boxes fill kVocabPieceBytes at most,
+// or one 256-column tile of all rows where that is more.
+constexpr size_t kVocabPieceBytes = (size_t)256 << 20;
+struct VocabGradLayout {
+  size_t hdr, idx, tgt, lse, g, Xc, boxes, slots0, slots1, total;
+  int64_t cap_boxes;
+};
+inline VocabGradLayout vocab_grad_layout(int M, int V, int d) {
+  VocabGradLayout L;
+  L.hdr = 0;
+  L.idx = 256;
+  L.tgt = L.idx + align256(4 * (size_t)M);
+  L.lse = L.tgt + align256(4 * (size_t)M);
+  L.g = L.lse + align256(4 * (size_t)M);
+  L.Xc = L.g + align256(4 * (size_t)M);
+  L.boxes = L.Xc + align256(2 * (size_t)M * d);
+  const int64_t all = tg_boxes(M, V), one = tg_boxes(M, 256);
+  int64_t cap = (int64_t)(kVocabPieceBytes / 8192);
+  if (cap < one) cap = one;
+  const bool pieces = cap < all;
+  L.cap_boxes = pieces ? cap : all;
+  L.slots0 = L.boxes + 8192 * (size_t)L.cap_boxes;
+  L.slots1 = L.slots0 + tg_slot_bytes();
+  const size_t sums = pieces ? tg_tiles(M, d) * kTgSlotBytes : 0;
+  L.total = L.slots1 + (sums > tg_slot_bytes() ? sums : tg_slot_bytes());
+  return L;
+}
+
+// Gradients of the GAU projections: the boxes of dpre [M][2e + s], fp32 tiles.
+struct ProjectGradLayout {
+  size_t boxes, slots0, slots1, total;
+  int64_t cap_boxes;
+};
+inline ProjectGradLayout project_grad_layout(int M, int N, int d) {
+  (void)d;
+  ProjectGradLayout L;
+  L.boxes = 0;
+  L.cap_boxes = tg_boxes(M, N);
+  L.slots0 = 8192 * (size_t)L.cap_boxes;
+  L.slots1 = L.slots0 + tg_slot_bytes();
+  L.total = L.slots1 + tg_slot_bytes();
+  return L;
+}
+struct OutputGradLayout {
+  size_t slots0, slots1, total;
+};
+inline OutputGradLayout output_grad_layout(int, int, int) {
+  return OutputGradLayout{0, tg_slot_bytes(), 2 * tg_slot_bytes()};
+}
+
+int launch_vocab_loss(const void *X, const void *W, const int64_t *target, float *loss, float *lse,
+                      int M, int V, int d, void *workspace, cudaStream_t stream);
+int launch_vocab_loss_backward(const void *X, const void *W, const int64_t *target,
+                               const float *lse, const float *dloss, void *dX, void *dW, int M,
+                               int V, int d, void *workspace, cudaStream_t stream);
+int launch_gau_project_backward(const void *X, const void *Wt, const void *dU, const void *dV,
+                                const void *dZ, void *dX, void *dWt, int M, int d, int e, int s,
+                                void *workspace, cudaStream_t stream);
+int launch_gau_output_backward(const void *Y, const void *Wo_t, const void *dOut, void *dY,
+                               void *dWo_t, int M, int e, int d, void *workspace,
+                               cudaStream_t stream);
+
 // Shapes the tensor-core path covers.
 bool tc_supported(int B, int n, int s, int e, int C);  // every tensor-core kernel (e % 256)
 bool tc_forward_supported(int B, int n, int s, int e, int C, int lin_norm);  // the forward pass

@@ -514,4 +514,5 @@ int launch_timeout_selftest(int limit_us, cudaStream_t stream) {
 
 // The tensor-core backward pass (same translation unit: one device status).
 #include "tc_backward.cuh"
-
+// The training operators (the same: one device status).
+#include "tc_train.cuh"

@@ -1,0 +1,736 @@
+// tc_tgemm.cuh -- the matrix products of the training operators around the
+// attention core, on the tensor cores: one persistent tcgen05 kernel, four
+// uses (KIND).  Tokens are rows m, outputs (vocabulary entries or projection
+// features) are columns v, model features are d:
+//
+//   TG_LSE   Z = X W^T           per row the maximum and the sum of
+//                                exp(z - maximum) of every 128 columns, and the
+//                                target's logit; Z itself is not stored
+//   TG_PROB  Z = X W^T           the piece's (softmax(z) - onehot) * g, bf16
+//   TG_SILU  Z = X W^T           dpre = dOut * silu'(z), bf16
+//   TG_GRAD  dW = A^T X, dX = A W   from that bf16 matrix A (or a row-major
+//                                one), two problems in one launch
+//
+// Operands are read by TMA into 128-byte-swizzled tiles, K-major or MN-major
+// by descriptor, so no operand is ever transposed in memory.  The matrix A
+// that TG_PROB and TG_SILU write lies in boxes of 64 tokens x 64 columns (8
+// KB, row after row): box (c, t) of column block c and token block t is number
+// c * n_tok64 + t.  The same box is a K-major tile for dX and an MN-major one
+// for dW, and the width of a piece can be chosen on the device.
+//
+// A unit is a tile of 128 CG x 256 outputs: CG = 1 one CTA, CG = 2 a pair of
+// CTAs on one tcgen05 tile of M = 256 (each holds its 128 rows of A, half of
+// B's 256 rows and the accumulator of its rows).  A pair reads (128 + 128) x 64
+// operands a CTA and k step instead of (128 + 256) x 64, which is what bounds
+// the single-CTA form: its operand traffic from L2.  K runs in 64-deep stages
+// through a ring in shared memory into one of two TMEM accumulators.  Warps: 0
+// TMA producer, 1 MMA issuer (of a pair: the first CTA's), 2-9 epilogue; every
+// warp works out the units by itself, so there is no queue.  Every wait is
+// bounded.  Included by tc.cu (through tc_train.cuh).
+#pragma once
+
+#include "tc_common.cuh"
+
+namespace fmca {
+namespace {
+
+constexpr int TG_EPI_WARPS = 8;
+constexpr int TG_THREADS = 64 + 32 * TG_EPI_WARPS;
+template <int CG>
+struct TgCfg {
+  static constexpr uint32_t A_BYTES = 128 * 64 * 2;              // 16 KB
+  static constexpr uint32_t B_BYTES = (256 / CG) * 64 * 2;       // 32 or 16 KB
+  static constexpr uint32_t SLOT = A_BYTES + B_BYTES;
+  static constexpr int RING = CG == 2 ? 7 : 4;
+  static constexpr uint32_t SMEM = RING * SLOT + 1024;
+};
+static_assert(TgCfg<1>::SMEM + 1024 <= 232448 && TgCfg<2>::SMEM + 1024 <= 232448,
+              "tc_tgemm exceeds 227 KB of shared memory");
+
+enum : int { TG_LSE = 0, TG_PROB = 1, TG_SILU = 2, TG_GRAD = 3 };
+
+// What the rows' preparation leaves on the device: the number of rows that
+// take part and the largest |dloss| among them (1 if that is not finite).
+struct TgHeader {
+  int count;
+  float gmax;
+};
+
+// Pieces of the column axis: as many 256-column tiles a piece as the boxes of
+// all tokens fit the buffer, the pieces equal in length.
+struct TgPieces {
+  int n_tok64, tiles, tp, np;
+};
+__host__ __device__ inline TgPieces tg_pieces(int count, int V, int64_t cap_boxes) {
+  TgPieces r;
+  r.n_tok64 = (count > 0 ? (count + 255) / 256 : 1) * 4;
+  r.tiles = (V + 255) / 256;
+  int64_t tp = cap_boxes / (4 * (int64_t)r.n_tok64);
+  if (tp < 1) tp = 1;
+  if (tp > r.tiles) tp = r.tiles;
+  r.np = (int)((r.tiles + tp - 1) / tp);
+  r.tp = (r.tiles + r.np - 1) / r.np;
+  return r;
+}
+
+// Parts of the k axis for a product of `tiles` tiles: its tiles leave workers
+// without one and every part keeps 16 k steps (1024 deep) at least -- shorter
+// parts cost more in their fp32 partial tiles than they gain.
+__host__ __device__ inline int tg_split(int tiles, int ks, int workers) {
+  if (tiles <= 0) return 1;
+  int S = workers / tiles;
+  if (S > ks / 16) S = ks / 16;
+  return S < 1 ? 1 : S;
+}
+
+struct TgParams {
+  CUtensorMap A, B;    // NT kinds: X [M][K] box {64, 128}, W [N][K] box {64, 256 / CG}
+                       // TG_GRAD: A of problem 0 and (A1) of problem 1, B likewise
+  CUtensorMap A1, B1;
+  int M, N, K;         // NT: rows, columns, depth; TG_GRAD: tokens, columns of A (V), features
+  int blocked;         // TG_GRAD: A lies in boxes
+  int piece;           // piece of the column axis (TG_PROB, TG_GRAD)
+  int64_t cap_boxes;
+  const TgHeader *hdr; // device count of rows (NULL: M)
+  const int *idx;      // compact row -> row (NULL: the same)
+  // TG_LSE
+  float2 *part;        // [2 ceil(N / 256)][M]
+  float *ztgt;         // [M]
+  const int *tgt;      // [M]
+  // TG_PROB
+  const float *lse, *g;
+  // TG_SILU: gradients of the activations, columns [0, n0), [n0, n1), [n1, N)
+  const __nv_bfloat16 *d0, *d1, *d2;
+  int n0, n1;
+  __nv_bfloat16 *boxes;
+  // TG_GRAD
+  __nv_bfloat16 *D0;   // dW [V][K]
+  __nv_bfloat16 *D1;   // dX [tokens][K]
+  float *slots0, *slots1;  // fp32 partial tiles of 128 x 256
+};
+
+// One of TG_GRAD's products as the kernel runs it: rows, tiles of 128 CG rows
+// and of 256 columns, k steps, parts of the k axis, steps a part, and the
+// units that makes.
+struct TgShape {
+  int M, Mt, Nt, ks, S, ksp, units;
+};
+struct TgPlan {
+  int count, col0, width;   // rows; first column and columns of the piece
+  TgPieces pc;
+  TgShape s[2];
+};
+
+// K sets the depth; K_split (>= K) the parts.
+template <int CG>
+__host__ __device__ inline TgShape tg_shape(int M, int N, int K, int K_split, int workers,
+                                            bool split) {
+  TgShape h;
+  h.M = M;
+  h.Mt = (M + 128 * CG - 1) / (128 * CG);
+  h.Nt = (N + 255) / 256;
+  h.ks = (K + 63) / 64;
+  const int ks = (K_split + 63) / 64;
+  h.S = split ? tg_split(h.Mt * h.Nt, ks, workers) : 1;
+  h.ksp = (ks + h.S - 1) / h.S;
+  h.S = h.ksp > 0 ? (ks + h.ksp - 1) / h.ksp : 1;
+  h.units = h.Mt * h.Nt * h.S;
+  return h;
+}
+
+template <int CG, int KIND>
+__host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int count, int workers) {
+  TgPlan p;
+  p.count = count;
+  p.pc = tg_pieces(count, P.N, P.cap_boxes);
+  p.col0 = 0;
+  p.width = P.N;
+  if (KIND == TG_PROB || (KIND == TG_GRAD && P.blocked)) {
+    p.col0 = piece * p.pc.tp * 256;
+    p.width = p.col0 < P.N ? (P.N - p.col0 < p.pc.tp * 256 ? P.N - p.col0 : p.pc.tp * 256) : 0;
+  }
+  const int rows = p.width > 0 ? count : 0;  // no piece left: no units
+  if (KIND == TG_GRAD) {
+    // dW [width][K], depth tokens; dX [tokens][K], depth width, with the same
+    // parts in every piece (their sums go on from piece to piece), of which a
+    // short last piece leaves some without depth
+    p.s[0] = tg_shape<CG>(p.width, P.K, count, count, workers, true);
+    p.s[1] = tg_shape<CG>(rows, P.K, p.width, P.blocked ? p.pc.tp * 256 : P.N, workers, true);
+  } else {
+    p.s[0] = tg_shape<CG>(rows, p.width, P.K, P.K, workers, false);
+    p.s[1] = p.s[0];
+    p.s[1].units = 0;
+  }
+  return p;
+}
+
+// The units of one worker.  The products with their tokens as rows: dealt
+// round-robin, in blocks of 64 row tiles (so that a block's rows and the
+// columns at hand stay in L2), rows first within a block.  TG_GRAD: problem
+// 0's units round-robin, then each worker a run of problem 1's that levels the
+// workers' k steps: the shortest common finish T with room for all of them.
+struct TgWork {
+  int w, W, n0, n1, lo1;
+};
+template <int KIND>
+__host__ __device__ inline TgWork tg_work(const TgPlan &p, int w, int W) {
+  TgWork o;
+  o.w = w;
+  o.W = W;
+  o.n0 = (p.s[0].units - w + W - 1) / W;
+  if (o.n0 < 0) o.n0 = 0;
+  o.n1 = 0;
+  o.lo1 = 0;
+  if (KIND == TG_GRAD && p.s[1].units > 0) {
+    constexpr int kEpilogue = 6;  // an epilogue that is not hidden, in k steps
+    const int c0 = p.s[0].ksp + kEpilogue, c1 = p.s[1].ksp + kEpilogue, n1 = p.s[1].units;
+    const int q = p.s[0].units / W, r = p.s[0].units % W;
+    const int64_t la = (int64_t)(q + 1) * c0, lb = (int64_t)q * c0;
+    int64_t lo = lb, hi = lb + (int64_t)(n1 + 1) * c1 + c0;
+    while (lo < hi) {  // least T with room for n1 units of problem 1
+      const int64_t T = (lo + hi) / 2;
+      const int64_t ka = T > la ? (T - la) / c1 : 0, kb = T > lb ? (T - lb) / c1 : 0;
+      if (r * ka + (W - r) * kb >= n1) hi = T;
+      else lo = T + 1;
+    }
+    const int64_t ka = lo > la ? (lo - la) / c1 : 0, kb = lo > lb ? (lo - lb) / c1 : 0;
+    // the workers with the shorter load first
+    const int64_t i = w >= r ? w - r : w;
+    int64_t a = w >= r ? i * kb : (W - r) * kb + i * ka, b = a + (w >= r ? kb : ka);
+    if (a > n1) a = n1;
+    if (b > n1) b = n1;
+    o.lo1 = (int)a;
+    o.n1 = (int)(b - a);
+  }
+  return o;
+}
+
+struct TgUnit {
+  int pi, mt, nt, s, ks0, nks;
+};
+template <int KIND>
+__host__ __device__ inline bool tg_unit(const TgPlan &p, const TgWork &k, int i, TgUnit &o) {
+  if (i >= k.n0 + k.n1) return false;
+  o.pi = i >= k.n0 ? 1 : 0;
+  const TgShape &h = p.s[o.pi];
+  int u = o.pi ? k.lo1 + (i - k.n0) : k.w + i * k.W;
+  if (KIND == TG_GRAD) {
+    o.nt = u % h.Nt;
+    u /= h.Nt;
+    o.mt = u % h.Mt;
+    o.s = u / h.Mt;
+  } else {
+    constexpr int kBlock = 64;
+    const int per = kBlock * h.Nt, b = u / per, v = u % per;
+    const int rows = min(kBlock, h.Mt - b * kBlock);
+    o.mt = b * kBlock + v % rows;
+    o.nt = v / rows;
+    o.s = 0;
+  }
+  o.ks0 = o.s * h.ksp;
+  o.nks = max(min(h.ksp, h.ks - o.ks0), 0);
+  return true;
+}
+
+// ------------------------------------------------------------- CTA pairs
+template <int CG>
+__device__ __forceinline__ uint32_t tg_rank() {
+  if constexpr (CG == 1) return 0;
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t tg_mapa(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+template <int CG>
+__device__ __forceinline__ void tg_sync_all() {
+  if constexpr (CG == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  }
+}
+// 2-D TMA load into this CTA's shared memory, counted on the barrier at the
+// shared-cluster address `bar` (a pair: the first CTA's).
+template <int CG>
+__device__ __forceinline__ void tg_load(void *dst, const CUtensorMap *map, uint32_t bar, int x,
+                                        int y) {
+  if constexpr (CG == 1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (CG == 1) {
+    mma_bf16_ss(d, a, b, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// Arrive on `bar` (a pair: in both CTAs) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void tg_commit(uint64_t *bar) {
+  if constexpr (CG == 1) {
+    mma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tg_tmem_alloc(uint32_t *dst, uint32_t cols) {
+  if constexpr (CG == 1) {
+    tmem_alloc(dst, cols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(dst)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tg_tmem_dealloc(uint32_t addr, uint32_t cols) {
+  if constexpr (CG == 1)
+    tmem_dealloc(addr, cols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+                 : "memory");
+}
+// mbar_wait on a barrier that threads of the other CTA of a pair arrive on.
+template <int CG>
+__device__ __forceinline__ bool tg_wait_pair(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+  if constexpr (CG == 1) return mbar_wait(bar, parity, limit_ns);
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  }
+}
+// The epilogue's arrival on the MMA issuer's barrier (a pair: the first CTA's).
+template <int CG>
+__device__ __forceinline__ void tg_arrive_leader(uint64_t *bar) {
+  if constexpr (CG == 1)
+    mbar_arrive(bar);
+  else
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                     tg_mapa(smem_u32(bar), 0))
+                 : "memory");
+}
+
+// ------------------------------------------------------------- elementwise
+__device__ __forceinline__ float tg_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 32 bytes to global memory (32-byte aligned), kept in L2: the next kernel
+// reads it.
+__device__ __forceinline__ void tg_store32(void *p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Where chunk c (32 columns) of a warp's half tile of a row lies in the boxes.
+__device__ __forceinline__ __nv_bfloat16 *tg_box(__nv_bfloat16 *boxes, int n_tok64, int m, int nt,
+                                                 int half, int c) {
+  const int64_t vc = nt * 4 + half * 2 + (c >> 1);
+  return boxes + ((vc * n_tok64 + (m >> 6)) * 64 + (m & 63)) * 64 + (c & 1) * 32;
+}
+// 32 values rounded to bf16 into their half row of a box.
+__device__ __forceinline__ void tg_store_box(__nv_bfloat16 *dst, const float (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[16 * q + 2 * i], v[16 * q + 2 * i + 1]);
+    tg_store32(dst + 16 * q, w);
+  }
+}
+// Element offset of 4-column group j of row `row` in an fp32 partial tile of
+// 128 x 256: rows next to each other, so that a warp's 32 rows are 512
+// consecutive bytes.
+__host__ __device__ inline int64_t tg_slot_offset(int row, int j) {
+  return ((int64_t)j * 128 + row) * 4;
+}
+constexpr int64_t kTgSlotFloats = 128 * 256;
+
+template <int CG, int KIND>
+__global__ void __launch_bounds__(TG_THREADS, 1)
+    tc_tgemm(const __grid_constant__ TgParams P) {
+  using Cfg = TgCfg<CG>;
+  constexpr int RING = Cfg::RING;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(8) uint64_t full[RING], empty[RING];
+  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_base;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = tg_rank<CG>();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], TG_EPI_WARPS * CG);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) tg_tmem_alloc<CG>(&tmem_base, 512);
+  tc_fence_before();
+  tg_sync_all<CG>();
+  tc_fence_after();
+  const uint32_t tbase = tmem_base;
+  // a programmatic dependent: nothing below runs before the work ahead on the
+  // stream has completed; what follows may be launched from here on
+  griddep_wait();
+  griddep_launch_dependents();
+  const int count = P.hdr != nullptr ? P.hdr->count : P.M;
+  const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
+  const TgPlan plan = tg_plan<CG, KIND>(P, P.piece, count, workers);
+  const TgWork work = tg_work<KIND>(plan, worker, workers);
+
+  if (warp == 0) {
+    // =========================== TMA producer
+    if (lane == 0) {
+      tma_prefetch_desc(&P.A);
+      tma_prefetch_desc(&P.B);
+      int it = 0;
+      bool ok = true;
+      TgUnit u;
+      for (int i = 0; ok && tg_unit<KIND>(plan, work, i, u); ++i) {
+        const int m0 = u.mt * 128 * CG + (int)rank * 128;
+        const int nb0 = u.nt * 256 + (int)rank * 128;
+        for (int ks = 0; ks < u.nks; ++ks, ++it) {
+          const int slot = it % RING;
+          if (it >= RING && !mbar_wait(&empty[slot], ((it / RING) - 1) & 1, kWaitLimitNs)) {
+            record_timeout(1001);
+            ok = false;
+            break;
+          }
+          uint8_t *sa = smem + slot * Cfg::SLOT, *sb = sa + Cfg::A_BYTES;
+          uint32_t bar = smem_u32(&full[slot]);
+          if constexpr (CG == 2) bar = tg_mapa(bar, 0);
+          // out-of-range rows and columns arrive as zeros; full boxes count
+          if (rank == 0) mbar_arrive_expect_tx(&full[slot], Cfg::SLOT * CG);
+          const int kk = (u.ks0 + ks) * 64;
+          if constexpr (KIND != TG_GRAD) {
+            tg_load<CG>(sa, &P.A, bar, kk, m0);
+            tg_load<CG>(sb, &P.B, bar, kk, plan.col0 + nb0);
+          } else {
+            const CUtensorMap *mB = u.pi ? &P.B1 : &P.B;
+            if (P.blocked) {
+              // problem 0: column blocks m0 / 64 and the next, token block
+              // kk / 64; problem 1: column block kk / 64, two token blocks
+              const int t64 = plan.pc.n_tok64;
+              const int b0 = u.pi ? (kk / 64) * t64 + m0 / 64 : (m0 / 64) * t64 + kk / 64;
+              const int b1 = b0 + (u.pi ? 1 : t64);
+              tg_load<CG>(sa, &P.A, bar, 0, b0 * 64);
+              tg_load<CG>(sa + 8192, &P.A, bar, 0, b1 * 64);
+            } else if (u.pi) {  // rows m, columns k
+              tg_load<CG>(sa, &P.A1, bar, kk, m0);
+              tg_load<CG>(sa + 8192, &P.A1, bar, kk, m0 + 64);
+            } else {            // rows k, columns m
+              tg_load<CG>(sa, &P.A, bar, m0, kk);
+              tg_load<CG>(sa + 8192, &P.A, bar, m0 + 64, kk);
+            }
+            // rows k (problem 1: from the piece's first row of W), columns n
+            const int krow = kk + (u.pi ? plan.col0 : 0);
+#pragma unroll
+            for (int q = 0; q < 4 / CG; ++q)
+              tg_load<CG>(sb + q * 8192, mB, bar, nb0 + 64 * q, krow);
+          }
+        }
+      }
+      // wait (bounded) until every slot's last use is over: its copies have
+      // landed and, in a pair, no arrival is on its way to a CTA that has left
+      for (int q = (it > RING ? it - RING : 0); ok && q < it; ++q)
+        if (!mbar_wait(&empty[q % RING], (q / RING) & 1, kWaitLimitNs)) {
+          record_timeout(1002);
+          break;
+        }
+    }
+  } else if (warp == 1) {
+    // =========================== MMA issuer (of a pair: the first CTA)
+    if (lane == 0 && rank == 0) {
+      constexpr bool kMn = KIND == TG_GRAD;
+      constexpr uint32_t id_k = idesc_bf16_f32(128 * CG, 256, false, kMn);
+      constexpr uint32_t id_mn = idesc_bf16_f32(128 * CG, 256, true, kMn);
+      int it = 0;
+      bool ok = true;
+      TgUnit u;
+      int i = 0;
+      for (; ok && tg_unit<KIND>(plan, work, i, u); ++i) {
+        const int buf = i & 1, use = i >> 1;
+        if (use >= 1 && !tg_wait_pair<CG>(&acc_empty[buf], (use - 1) & 1, kWaitLimitNs)) {
+          record_timeout(1011);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool a_mn = kMn && u.pi == 0;
+        const uint32_t idesc = a_mn ? id_mn : id_k;
+        const uint32_t dcol = tbase + (uint32_t)buf * 256u;
+        for (int ks = 0; ks < u.nks; ++ks, ++it) {
+          const int slot = it % RING;
+          if (!mbar_wait(&full[slot], (it / RING) & 1, kWaitLimitNs)) {
+            record_timeout(1012);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + slot * Cfg::SLOT), sb = sa + Cfg::A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            // K-major: the next 16 k are 32 bytes further along each row;
+            // MN-major: 16 k rows further (LBO: between 64-column boxes)
+            const uint64_t ad = a_mn ? smem_desc_sw128(sa + kk * 2048, 8192, 1024)
+                                     : smem_desc_sw128(sa + kk * 32, 16, 1024);
+            const uint64_t bd = kMn ? smem_desc_sw128(sb + kk * 2048, 8192, 1024)
+                                    : smem_desc_sw128(sb + kk * 32, 16, 1024);
+            tg_mma<CG>(dcol, ad, bd, idesc, (ks | kk) != 0);
+          }
+          tg_commit<CG>(&empty[slot]);
+        }
+        if (!ok) break;
+        tg_commit<CG>(&acc_full[buf]);
+      }
+      // the last accumulators have been read, so every MMA is over
+      for (int q = (i > 2 ? i - 2 : 0); ok && q < i; ++q)
+        if (!tg_wait_pair<CG>(&acc_empty[q & 1], (q >> 1) & 1, kWaitLimitNs)) {
+          record_timeout(1013);
+          break;
+        }
+    }
+  } else {
+    // =========================== epilogue warps
+    // Warp w reads TMEM lanes 32 (w % 4) .. (its 32 rows, one a thread) of
+    // columns 128 half .. + 128.
+    const int quad = warp & 3, half = (warp - 2) / 4;
+    const int row = quad * 32 + lane;
+    TgUnit u;
+    for (int i = 0; tg_unit<KIND>(plan, work, i, u); ++i) {
+      const int buf = i & 1, use = i >> 1;
+      if (!mbar_wait(&acc_full[buf], use & 1, kWaitLimitNs)) {
+        if (lane == 0) record_timeout(1020);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t dcol =
+          tbase + (uint32_t)buf * 256u + (uint32_t)(half * 128) + ((uint32_t)(quad * 32) << 16);
+      const int m = u.mt * 128 * CG + (int)rank * 128 + row;  // row of the product
+      const int c0 = u.nt * 256 + half * 128;                 // first column in the piece
+      uint32_t r[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(dcol + 32 * c, r[c]);
+      tmem_ld_wait();
+      // this warp's last read of the accumulator
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tg_arrive_leader<CG>(&acc_empty[buf]);
+
+      if constexpr (KIND == TG_LSE) {
+        // columns past the vocabulary count as -infinity
+        if (c0 + 128 > P.N) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c0 + 32 * c + j >= P.N) r[c][j] = 0xFF800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mx[c] = fmaxf(mx[c], __uint_as_float(r[c][j]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // a row of -infinities has the sum 0 (not exp(-inf + inf))
+        const float ref = top == -INFINITY ? 0.f : top * kLog2e;
+        float sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            sm[c] += tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -ref));
+        const bool in = m < plan.count;
+        if (in)
+          P.part[(int64_t)(u.nt * 2 + half) * P.M + m] =
+              make_float2(top, (sm[0] + sm[1]) + (sm[2] + sm[3]));
+        const int at = in ? P.tgt[m] - c0 : -1;
+        if (__any_sync(0xffffffffu, at >= 0 && at < 128)) {
+          float z = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (at == 32 * c + j) z = __uint_as_float(r[c][j]);
+          if (at >= 0 && at < 128) P.ztgt[m] = z;
+        }
+      } else if constexpr (KIND == TG_PROB) {
+        const bool in = m < plan.count;
+        const float lse = in ? P.lse[m] * kLog2e : 0.f;
+        const float gmax = P.hdr->gmax;
+        float g = in ? P.g[m] : 0.f;
+        if (gmax > 0.f) g /= gmax;
+        const int at = in ? P.tgt[m] - plan.col0 - c0 : -1;
+        const bool any = __any_sync(0xffffffffu, at >= 0 && at < 128);
+        const int left = plan.width - c0;  // columns of the piece from here on
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -lse)) * g;
+          if (any) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (at == 32 * c + j)  // (p - 1) g, the difference formed first
+                v[j] = (tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -lse)) - 1.f) * g;
+          }
+          if (!in || left < 128) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!in || 32 * c + j >= left) v[j] = 0.f;
+          }
+          tg_store_box(tg_box(P.boxes, plan.pc.n_tok64, m, u.nt, half, c), v);
+        }
+      } else if constexpr (KIND == TG_SILU) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = c0 + 32 * c;  // 32 columns lie in one of the three outputs
+          float v[32];
+          if (m < plan.count && col < P.N) {
+            const __nv_bfloat16 *src = col < P.n0   ? P.d0 + (int64_t)m * P.n0 + col
+                                       : col < P.n1 ? P.d1 + (int64_t)m * (P.n1 - P.n0) + col - P.n0
+                                                    : P.d2 + (int64_t)m * (P.N - P.n1) + col - P.n1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint4 w4 = __ldg(reinterpret_cast<const uint4 *>(src) + q);
+              const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float z = __uint_as_float(r[c][8 * q + k]);
+                const float sig = __fdividef(1.f, 1.f + __expf(-z));
+                const float d = (k & 1) ? bf16_hi(ww[k / 2]) : bf16_lo(ww[k / 2]);
+                v[8 * q + k] = d * sig * fmaf(z, 1.f - sig, 1.f);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+          tg_store_box(tg_box(P.boxes, plan.pc.n_tok64, m, u.nt, half, c), v);
+        }
+      } else {
+        const TgShape &h = plan.s[u.pi];
+        const bool last = !P.blocked || u.pi == 0 || P.piece == plan.pc.np - 1;
+        const bool direct = h.S == 1 && last;
+        // problem 1 over several pieces adds to what the pieces before left
+        const bool add = u.pi == 1 && P.blocked && P.piece > 0;
+        float *slot = (u.pi ? P.slots1 : P.slots0) +
+                      ((int64_t)(u.s * h.Mt * CG + u.mt * CG + (int)rank) * h.Nt + u.nt) *
+                          kTgSlotFloats;
+        const float alpha = P.hdr != nullptr ? P.hdr->gmax : 1.f;
+        const bool in = m < h.M;
+        if (u.nks == 0) {  // no depth, nothing was multiplied: the product is 0
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[c][j] = 0u;
+        }
+        __nv_bfloat16 *out = nullptr;
+        if (direct && in)
+          out = u.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
+                     : P.D0 + (int64_t)(plan.col0 + m) * P.K;
+        const bool wide =
+            P.K % 16 == 0 && (reinterpret_cast<uintptr_t>(u.pi ? P.D1 : P.D0) & 31u) == 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[c][j]);
+          if (add) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 o = *reinterpret_cast<const float4 *>(
+                  slot + tg_slot_offset(row, half * 32 + c * 8 + j));
+              v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
+            }
+          }
+          if (!direct) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4 *>(slot + tg_slot_offset(row, half * 32 + c * 8 + j)) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          } else if (in) {
+            const int col = c0 + 32 * c;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                w[k] = pack_bf16x2(alpha * v[16 * q + 2 * k], alpha * v[16 * q + 2 * k + 1]);
+              const int cq = col + 16 * q;
+              if (wide) {
+                if (cq < P.K) tg_store32(out + cq, w);
+              } else {  // rows start on 16-byte boundaries only
+                if (cq < P.K)
+                  *reinterpret_cast<uint4 *>(out + cq) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (cq + 8 < P.K)
+                  *reinterpret_cast<uint4 *>(out + cq + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+  // the single-lane roles rejoin their warps before the block-wide barrier,
+  // which counts converged warps
+  __syncwarp();
+  tc_fence_before();
+  tg_sync_all<CG>();
+  if (warp == 1) tg_tmem_dealloc<CG>(tbase, 512);
+}
+
+}  // namespace
+}  // namespace fmca

@@ -1,0 +1,449 @@
+// tc_train.cuh -- the training operators on the tensor cores around the
+// products of tc_tgemm: the softmax cross entropy over a vocabulary and its
+// gradients, and the gradients of the GAU projections.
+//
+//   loss_m = log sum_v exp(z_mv) - z_m,t(m),  z = X W^T, for the rows m that
+//            have a target t(m) in 0 .. V - 1
+//   dX_m = g_m sum_v (p_mv - [v = t(m)]) W_v,  dW_v = sum_m g_m (p_mv - [v = t(m)]) X_m
+//
+// The rows with a target are copied next to each other first (vocab_gather),
+// so that a row without one costs nothing in the products and whatever its X
+// holds (NaN included) reaches nothing.  The number of such rows stays on the
+// device; every kernel reads it there, so the calls can be captured.
+//
+// The forward pass keeps, per row and 128 columns, the maximum and the sum of
+// exp(z - maximum), 1/32 of the logits' bytes at bf16; vocab_reduce
+// joins them.  The backward pass forms the logits again, a piece of the
+// vocabulary at a time, as (p - onehot) g / max|g| in bf16 (the scale goes
+// back in fp32 at the end, so that equal weights are not rounded), and takes
+// both gradients of the piece from it in one launch.  dX adds up over the
+// pieces in fp32.
+#pragma once
+
+#include "tc_tgemm.cuh"
+
+namespace fmca {
+namespace {
+
+constexpr int kGatherThreads = 256;
+
+__device__ __forceinline__ bool has_target(int64_t t, int V) { return t >= 0 && t < V; }
+
+// Sum over a block of 256 threads; every thread gets it.
+__device__ __forceinline__ int block_sum(int v, int *red) {
+  __syncthreads();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+  __syncthreads();
+  int t = 0;
+#pragma unroll
+  for (int i = 0; i < kGatherThreads / 32; ++i) t += red[i];
+  return t;
+}
+
+struct GatherArgs {
+  const __nv_bfloat16 *X;   // [M][d]
+  const int64_t *target;    // [M]
+  int M, V, d, per;         // rows a block
+  __nv_bfloat16 *Xc;        // [M][d] compact rows
+  int *idx, *tgt;           // [M] compact
+  TgHeader *hdr;
+  float *loss, *lse_out;    // forward: 0 for rows without a target
+  const float *lse, *dloss; // backward
+  float *lse_c, *g_c;       // backward, compact
+  __nv_bfloat16 *dX;        // backward: rows without a target are 0
+};
+
+// Copies the rows that have a target next to each other, in order.  A block
+// takes `per` rows and counts the targets of all rows before its own by
+// itself: M / 256 loads a thread from L2 instead of a pass over the blocks.
+template <bool kBackward>
+__global__ void __launch_bounds__(kGatherThreads) vocab_gather(GatherArgs a) {
+  __shared__ int red[kGatherThreads / 32];
+  __shared__ float redf[kGatherThreads / 32];
+  __shared__ int pos_s[kGatherThreads];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  griddep_launch_dependents();
+  const int64_t r0 = (int64_t)blockIdx.x * a.per;
+  const int64_t r1 = r0 + a.per < a.M ? r0 + a.per : a.M;
+  int n = 0;
+#pragma unroll 8
+  for (int64_t m = tid; m < r0; m += kGatherThreads) n += has_target(a.target[m], a.V) ? 1 : 0;
+  int base = block_sum(n, red);
+  const int nv = a.d / 8;
+  for (int64_t m0 = r0; m0 < r1; m0 += kGatherThreads) {
+    const int64_t m = m0 + tid;
+    const int64_t t = m < r1 ? a.target[m] : -1;
+    const bool has = has_target(t, a.V);
+    const uint32_t votes = __ballot_sync(0xffffffffu, has);
+    __syncthreads();
+    if (lane == 0) red[warp] = __popc(votes);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kGatherThreads / 32; ++i) {
+      before += i < warp ? red[i] : 0;
+      all += red[i];
+    }
+    const int pos = base + before + __popc(votes & ((1u << lane) - 1));
+    if (has) {
+      a.idx[pos] = (int)m;
+      a.tgt[pos] = (int)t;
+      if constexpr (kBackward) {
+        a.lse_c[pos] = a.lse[m];
+        a.g_c[pos] = a.dloss[m];
+      }
+    } else if (m < r1) {
+      if constexpr (!kBackward) {
+        a.loss[m] = 0.f;
+        a.lse_out[m] = 0.f;
+      }
+    }
+    pos_s[tid] = has ? pos : -1;
+    base += all;
+    __syncthreads();
+    const int rows = (int)(r1 - m0 < kGatherThreads ? r1 - m0 : kGatherThreads);
+    for (int r = warp; r < rows; r += kGatherThreads / 32) {
+      const int p = pos_s[r];
+      if (p >= 0) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.X + (m0 + r) * a.d);
+        uint4 *dst = reinterpret_cast<uint4 *>(a.Xc + (int64_t)p * a.d);
+        for (int v = lane; v < nv; v += 32) dst[v] = __ldg(src + v);
+      } else if constexpr (kBackward) {
+        uint4 *dst = reinterpret_cast<uint4 *>(a.dX + (m0 + r) * a.d);
+        for (int v = lane; v < nv; v += 32) dst[v] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    __syncthreads();
+  }
+  if (blockIdx.x == gridDim.x - 1) {
+    // the last block knows the number of rows; zero rows up to the next
+    // multiple of 64 complete the products' last step over the tokens
+    const int count = base;
+    const int64_t end = min((int64_t)(count + 63) / 64 * 64, (int64_t)a.M);
+    uint4 *dst = reinterpret_cast<uint4 *>(a.Xc);
+    for (int64_t v = (int64_t)count * nv + tid; v < end * nv; v += kGatherThreads)
+      dst[v] = make_uint4(0u, 0u, 0u, 0u);
+    float top = 0.f;
+    if constexpr (kBackward) {
+#pragma unroll 4
+      for (int64_t m = tid; m < a.M; m += kGatherThreads)
+        if (has_target(a.target[m], a.V)) top = fmaxf(top, fabsf(a.dloss[m]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) redf[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kGatherThreads / 32; ++i) top = fmaxf(top, redf[i]);
+      if (top == INFINITY) top = 1.f;  // no scale that the other rows could bear
+    }
+    if (tid == 0) {
+      a.hdr->count = count;
+      a.hdr->gmax = top;
+    }
+  }
+}
+
+// loss and lse of the rows from the products' partial maxima and sums: 32
+// rows a block, 16 lanes of parts each, joined in order.
+constexpr int kReduceLanes = 16;
+__global__ void __launch_bounds__(32 * kReduceLanes)
+    vocab_reduce(const float2 *__restrict__ part, const float *__restrict__ ztgt,
+                 const int *__restrict__ idx, const TgHeader *__restrict__ hdr, float *loss,
+                 float *lse, int parts, int M) {
+  __shared__ float2 s[kReduceLanes][32];
+  griddep_wait();
+  const int count = hdr->count;
+  const int r = threadIdx.x % 32, l = threadIdx.x / 32;
+  const int64_t m = (int64_t)blockIdx.x * 32 + r;
+  if ((int64_t)blockIdx.x * 32 >= count) return;
+  // (top, sum) with sum = sum exp(z - top); (-infinity, 0) is nothing
+  auto join = [](float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x), ref = top == -INFINITY ? 0.f : top;
+    return make_float2(top, a.y * tg_exp2((a.x - ref) * kLog2e) + b.y * tg_exp2((b.x - ref) * kLog2e));
+  };
+  float2 t = make_float2(-INFINITY, 0.f);
+  if (m < count) {
+#pragma unroll 8
+    for (int p = l; p < parts; p += kReduceLanes) t = join(t, __ldg(part + (int64_t)p * M + m));
+  }
+  s[l][r] = t;
+  __syncthreads();
+  if (l == 0 && m < count) {
+#pragma unroll
+    for (int i = 1; i < kReduceLanes; ++i) t = join(t, s[i][r]);
+    const float v = t.x + logf(t.y);
+    const int row = idx[m];
+    lse[row] = v;
+    loss[row] = v - ztgt[m];
+  }
+}
+
+// Products whose k axis was split: the sum of the parts' fp32 tiles, rounded.
+// A thread sums 16 columns of a row (its warp's loads are consecutive).
+template <int CG>
+__global__ void __launch_bounds__(256)
+    tg_join(const __grid_constant__ TgParams P, int workers, int last) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int count = P.hdr != nullptr ? P.hdr->count : P.M;
+  const float alpha = P.hdr != nullptr ? P.hdr->gmax : 1.f;
+#pragma unroll 1
+  for (int pi = 0; pi < 1 + last; ++pi) {
+    // problem 0: this piece's dW; problem 1, after the launches of all pieces:
+    // dX, complete since the last piece that has columns
+    const int np = P.blocked ? tg_pieces(count, P.N, P.cap_boxes).np : 1;
+    const TgPlan plan = tg_plan<CG, TG_GRAD>(P, pi ? np - 1 : P.piece, count, workers);
+    const TgShape &h = plan.s[pi];
+    if (h.S <= 1 || h.units == 0) continue;
+    const int Mt = h.Mt * CG;
+    const int64_t tiles = (int64_t)Mt * h.Nt;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < tiles * 128 * 16;
+         i += (int64_t)gridDim.x * blockDim.x) {
+      const int row = (int)(i % 128), q = (int)(i / 128 % 16);
+      const int64_t tile = i / (128 * 16);
+      const int m = (int)(tile / h.Nt) * 128 + row, col = (int)(tile % h.Nt) * 256 + q * 16;
+      if (m >= h.M || col >= P.K) continue;
+      float v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = 0.f;
+      for (int s = 0; s < h.S; ++s) {
+        const float *slot = (pi ? P.slots1 : P.slots0) + (s * tiles + tile) * kTgSlotFloats;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 o =
+              *reinterpret_cast<const float4 *>(slot + tg_slot_offset(row, q * 4 + j));
+          v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
+        }
+      }
+      __nv_bfloat16 *out = pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
+                              : P.D0 + (int64_t)(plan.col0 + m) * P.K;
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(alpha * v[2 * k], alpha * v[2 * k + 1]);
+      *reinterpret_cast<uint4 *>(out + col) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (col + 8 < P.K)
+        *reinterpret_cast<uint4 *>(out + col + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+template <int CG, int KIND>
+int launch_tgemm_kind(const TgParams &P, int workers, cudaStream_t stream) {
+  static OncePerDevice attrs;
+  if (!attrs.run([] {
+        return cudaFuncSetAttribute(tc_tgemm<CG, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)TgCfg<CG>::SMEM) == cudaSuccess;
+      }))
+    return 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(workers * CG);
+  cfg.blockDim = dim3(TG_THREADS);
+  cfg.dynamicSmemBytes = TgCfg<CG>::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, tc_tgemm<CG, KIND>, P) == cudaSuccess ? 0 : 1;
+}
+
+// Workers of a launch: one CTA (or pair) an SM, no more than there are units
+// with every row taking part, and no more than the workspace was sized for.
+template <int CG, int KIND>
+int tg_workers(const TgParams &P) {
+  const int sms = num_sms();
+  int w = (sms < kTgMaxCtas ? sms : kTgMaxCtas) / CG;
+  if (KIND != TG_GRAD) {
+    const TgPlan p = tg_plan<CG, KIND>(P, P.piece, P.M, w);
+    if (p.s[0].units < w) w = p.s[0].units;
+  }
+  return w < 1 ? 1 : w;
+}
+template <int CG, int KIND>
+int launch_tgemm(const TgParams &P, cudaStream_t stream) {
+  return launch_tgemm_kind<CG, KIND>(P, tg_workers<CG, KIND>(P), stream);
+}
+
+// TG_GRAD on piece P.piece of np and, where a product may have been split, the
+// sum of its parts.  With a device count the rows are not known here, and so
+// neither the split of dX nor, with several pieces, how wide this one is;
+// fewer rows never split dW more often at the same width.
+template <int CG>
+int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
+  const bool last = P.piece == np - 1;
+  const int w = tg_workers<CG, TG_GRAD>(P);
+  if (launch_tgemm_kind<CG, TG_GRAD>(P, w, stream)) return 1;
+  const TgPlan p = tg_plan<CG, TG_GRAD>(P, P.piece, P.M, w);
+  const bool join = p.s[0].S > 1 || np > 1 || (last && (p.s[1].S > 1 || P.hdr != nullptr));
+  if (!join) return 0;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kTgMaxCtas * 2);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tg_join<CG>, P, w, last ? 1 : 0) == cudaSuccess ? 0 : 1;
+}
+
+constexpr int kCG = 1;
+
+// X [M][K] and W [N][K] of the products with tokens as rows
+bool nt_maps(TgParams &P, const void *X, const void *W, int M, int N, int K) {
+  return make_map_bf16(&P.A, X, K, M, 64, 128) && make_map_bf16(&P.B, W, K, N, 64, 256 / kCG);
+}
+
+}  // namespace
+
+int launch_vocab_loss(const void *X, const void *W, const int64_t *target, float *loss, float *lse,
+                      int M, int V, int d, void *workspace, cudaStream_t stream) {
+  const VocabLossLayout L = vocab_loss_layout(M, V, d);
+  char *ws = static_cast<char *>(workspace);
+  GatherArgs a = {};
+  a.X = static_cast<const __nv_bfloat16 *>(X);
+  a.target = target;
+  a.M = M, a.V = V, a.d = d;
+  a.Xc = reinterpret_cast<__nv_bfloat16 *>(ws + L.Xc);
+  a.idx = reinterpret_cast<int *>(ws + L.idx);
+  a.tgt = reinterpret_cast<int *>(ws + L.tgt);
+  a.hdr = reinterpret_cast<TgHeader *>(ws + L.hdr);
+  a.loss = loss, a.lse_out = lse;
+  const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
+  a.per = (M + blocks - 1) / blocks;
+  vocab_gather<false><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return 1;
+
+  TgParams P = {};
+  if (!nt_maps(P, a.Xc, W, M, V, d)) return 2;
+  P.M = M, P.N = V, P.K = d;
+  P.hdr = a.hdr;
+  P.part = reinterpret_cast<float2 *>(ws + L.part);
+  P.ztgt = reinterpret_cast<float *>(ws + L.ztgt);
+  P.tgt = a.tgt;
+  if (int rc = launch_tgemm<kCG, TG_LSE>(P, stream)) return rc;
+
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((M + 31) / 32);
+  cfg.blockDim = dim3(32 * kReduceLanes);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, vocab_reduce, (const float2 *)P.part, (const float *)P.ztgt,
+                            (const int *)a.idx, (const TgHeader *)a.hdr, loss, lse,
+                            2 * ((V + 255) / 256), M) == cudaSuccess
+             ? 0
+             : 1;
+}
+
+int launch_vocab_loss_backward(const void *X, const void *W, const int64_t *target,
+                               const float *lse, const float *dloss, void *dX, void *dW, int M,
+                               int V, int d, void *workspace, cudaStream_t stream) {
+  const VocabGradLayout L = vocab_grad_layout(M, V, d);
+  char *ws = static_cast<char *>(workspace);
+  GatherArgs a = {};
+  a.X = static_cast<const __nv_bfloat16 *>(X);
+  a.target = target;
+  a.M = M, a.V = V, a.d = d;
+  a.Xc = reinterpret_cast<__nv_bfloat16 *>(ws + L.Xc);
+  a.idx = reinterpret_cast<int *>(ws + L.idx);
+  a.tgt = reinterpret_cast<int *>(ws + L.tgt);
+  a.hdr = reinterpret_cast<TgHeader *>(ws + L.hdr);
+  a.lse = lse, a.dloss = dloss;
+  a.lse_c = reinterpret_cast<float *>(ws + L.lse);
+  a.g_c = reinterpret_cast<float *>(ws + L.g);
+  a.dX = static_cast<__nv_bfloat16 *>(dX);
+  const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
+  a.per = (M + blocks - 1) / blocks;
+  vocab_gather<true><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return 1;
+
+  TgParams P = {}, Q = {};
+  if (!nt_maps(P, a.Xc, W, M, V, d)) return 2;
+  P.M = M, P.N = V, P.K = d;
+  P.cap_boxes = L.cap_boxes;
+  P.hdr = a.hdr;
+  P.tgt = a.tgt;
+  P.lse = a.lse_c, P.g = a.g_c;
+  P.boxes = reinterpret_cast<__nv_bfloat16 *>(ws + L.boxes);
+  Q = P;
+  Q.blocked = 1;
+  if (!make_map_bf16(&Q.A, P.boxes, 64, (uint64_t)L.cap_boxes * 64, 64, 64) ||
+      !make_map_bf16(&Q.B, a.Xc, d, M, 64, 64) || !make_map_bf16(&Q.B1, W, d, V, 64, 64))
+    return 2;
+  Q.A1 = Q.A;
+  Q.idx = a.idx;
+  Q.D0 = static_cast<__nv_bfloat16 *>(dW);
+  Q.D1 = static_cast<__nv_bfloat16 *>(dX);
+  Q.slots0 = reinterpret_cast<float *>(ws + L.slots0);
+  Q.slots1 = reinterpret_cast<float *>(ws + L.slots1);
+  const int np = tg_pieces(M, V, L.cap_boxes).np;  // with fewer rows no more pieces
+  for (int k = 0; k < np; ++k) {
+    P.piece = Q.piece = k;
+    if (int rc = launch_tgemm<kCG, TG_PROB>(P, stream)) return rc;
+    if (int rc = launch_grad<kCG>(Q, np, stream)) return rc;
+  }
+  return 0;
+}
+
+int launch_gau_project_backward(const void *X, const void *Wt, const void *dU, const void *dV,
+                                const void *dZ, void *dX, void *dWt, int M, int d, int e, int s,
+                                void *workspace, cudaStream_t stream) {
+  const int N = 2 * e + s;
+  const ProjectGradLayout L = project_grad_layout(M, N, d);
+  char *ws = static_cast<char *>(workspace);
+  TgParams P = {}, Q = {};
+  if (!nt_maps(P, X, Wt, M, N, d)) return 2;
+  P.M = M, P.N = N, P.K = d;
+  P.cap_boxes = L.cap_boxes;
+  P.d0 = static_cast<const __nv_bfloat16 *>(dU);
+  P.d1 = static_cast<const __nv_bfloat16 *>(dV);
+  P.d2 = static_cast<const __nv_bfloat16 *>(dZ);
+  P.n0 = e, P.n1 = 2 * e;
+  P.boxes = reinterpret_cast<__nv_bfloat16 *>(ws + L.boxes);
+  Q = P;
+  Q.blocked = 1;
+  if (!make_map_bf16(&Q.A, P.boxes, 64, (uint64_t)L.cap_boxes * 64, 64, 64) ||
+      !make_map_bf16(&Q.B, X, d, M, 64, 64) || !make_map_bf16(&Q.B1, Wt, d, N, 64, 64))
+    return 2;
+  Q.A1 = Q.A;
+  Q.D0 = static_cast<__nv_bfloat16 *>(dWt);
+  Q.D1 = static_cast<__nv_bfloat16 *>(dX);
+  Q.slots0 = reinterpret_cast<float *>(ws + L.slots0);
+  Q.slots1 = reinterpret_cast<float *>(ws + L.slots1);
+  if (int rc = launch_tgemm<kCG, TG_SILU>(P, stream)) return rc;
+  return launch_grad<kCG>(Q, 1, stream);
+}
+
+int launch_gau_output_backward(const void *Y, const void *Wo_t, const void *dOut, void *dY,
+                               void *dWo_t, int M, int e, int d, void *workspace,
+                               cudaStream_t stream) {
+  const OutputGradLayout L = output_grad_layout(M, d, e);
+  char *ws = static_cast<char *>(workspace);
+  TgParams Q = {};
+  // A = dOut [tokens][d], read by columns for dWo_t [d][e], by rows for dY
+  if (!make_map_bf16(&Q.A, dOut, d, M, 64, 64) || !make_map_bf16(&Q.B, Y, e, M, 64, 64) ||
+      !make_map_bf16(&Q.B1, Wo_t, e, d, 64, 64))
+    return 2;
+  Q.A1 = Q.A;
+  Q.M = M, Q.N = d, Q.K = e;
+  Q.D0 = static_cast<__nv_bfloat16 *>(dWo_t);
+  Q.D1 = static_cast<__nv_bfloat16 *>(dY);
+  Q.slots0 = reinterpret_cast<float *>(ws + L.slots0);
+  Q.slots1 = reinterpret_cast<float *>(ws + L.slots1);
+  return launch_grad<kCG>(Q, 1, stream);
+}
+
+}  // namespace fmca

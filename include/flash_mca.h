@@ -411,6 +411,65 @@ fmca_status flash_mca_layer_norm_backward(const void *dy, const void *h, const f
                                           fmca_dtype dtype, void *workspace,
                                           size_t workspace_bytes, fmca_stream_t stream);
 
+/*
+ * Gradients of the two projections (flash_mca_gau_project, flash_mca_gau_output)
+ * on the tensor cores, bf16 in and out with fp32 accumulation:
+ *   project   pre = X Wt^T (formed again), dpre = [dU | dV | dZ] * silu'(pre)
+ *             (rounded to bf16), dX = dpre Wt [M][d], dWt = dpre^T X [2e + s][d]
+ *   output    dY = dOut Wo_t [M][e], dWo_t = dOut^T Y [d][e]
+ * Arrays, weights and size conditions as for the forward calls (project: d a
+ * multiple of 8, e and s of 64; output: e a multiple of 8, d of 64); dU, dV
+ * [M][e], dZ [M][s], dOut [M][d].  Outputs must not overlap inputs, the
+ * workspace or each other.  Deterministic.  workspace: at least the matching
+ * ..._workspace_bytes (0 for sizes that would be rejected), 256-byte aligned;
+ * project keeps dpre there.
+ */
+size_t flash_mca_gau_project_backward_workspace_bytes(int M, int d, int e, int s);
+fmca_status flash_mca_gau_project_backward(const void *X, const void *Wt, const void *dU,
+                                           const void *dV, const void *dZ, void *dX, void *dWt,
+                                           int M, int d, int e, int s, void *workspace,
+                                           size_t workspace_bytes, fmca_stream_t stream);
+size_t flash_mca_gau_output_backward_workspace_bytes(int M, int e, int d);
+fmca_status flash_mca_gau_output_backward(const void *Y, const void *Wo_t, const void *dOut,
+                                          void *dY, void *dWo_t, int M, int e, int d,
+                                          void *workspace, size_t workspace_bytes,
+                                          fmca_stream_t stream);
+
+/*
+ * Softmax cross entropy of rows X [M][d] against a vocabulary W [V][d] (one
+ * row per entry, as the projections' weights), without storing the logits
+ * z = X W^T:
+ *   loss[m] = lse[m] - z[m][target[m]],  lse[m] = log sum_v exp(z[m][v])
+ * A row whose target lies outside 0 .. V - 1 (an ignored token: -100, say) has
+ * loss 0 and lse 0, takes part in nothing and costs nothing in the products;
+ * what its X holds, NaN included, reaches no output.  No reduction is applied:
+ * dloss [M] of the backward pass carries it (1 / number of targets for their
+ * mean).
+ *   X, W          device bf16, 16-byte aligned; target: device int64 [M]
+ *   loss, lse     device float32 [M] outputs, both needed
+ * The backward pass gives the gradients of sum(loss * dloss):
+ *   dX [M][d], dW [V][d]  bf16 outputs (overwritten; dX is 0 for ignored rows)
+ *   lse           as the forward call left it, for the same X, W and target
+ *   dloss         float32 [M]; not read for ignored rows
+ * It forms the logits again, a piece of the vocabulary at a time: the piece's
+ * probabilities lie in the workspace in bf16, 256 MiB at most (or 256 columns
+ * of all rows where those are more).  fp32 accumulation; fixed summation
+ * orders (deterministic).  The number of rows with a target stays on the
+ * device: the calls do not wait and can be captured.
+ * Sizes: M, V >= 1; d >= 8 a multiple of 8; M d, V d < 2^31.  Outputs must not
+ * overlap inputs, the workspace or each other.  workspace: the matching
+ * ..._workspace_bytes (0 for sizes that would be rejected), 256-byte aligned.
+ */
+size_t flash_mca_vocab_loss_workspace_bytes(int M, int V, int d);
+fmca_status flash_mca_vocab_loss(const void *X, const void *W, const int64_t *target, float *loss,
+                                 float *lse, int M, int V, int d, void *workspace,
+                                 size_t workspace_bytes, fmca_stream_t stream);
+size_t flash_mca_vocab_loss_backward_workspace_bytes(int M, int V, int d);
+fmca_status flash_mca_vocab_loss_backward(const void *X, const void *W, const int64_t *target,
+                                          const float *lse, const float *dloss, void *dX, void *dW,
+                                          int M, int V, int d, void *workspace,
+                                          size_t workspace_bytes, fmca_stream_t stream);
+
 /* Which path FMCA_PATH_AUTO takes for these arguments (FMCA_PATH_SIMT or
  * FMCA_PATH_TCGEN05), or -1 for arguments that would be rejected. */
 int flash_mca_auto_path(int B, int n, int s, int e, int C, int causal, fmca_dtype dtype);

@@ -445,3 +445,101 @@ def test_training_wrappers_refuse_host_tensors():
         fm.layer_norm_backward(x, x, w, torch.zeros(2), torch.zeros(2))
     with pytest.raises(ValueError, match="row"):
         fm.layer_norm_backward(torch.zeros(0, 8), x, w, w, w)
+
+
+def test_projection_gradients_reject_before_queueing():
+    """Argument checks of the projections' gradients; no pointer is
+    dereferenced."""
+    P = 0x7F0000000000
+    a = [P + (k << 28) for k in range(8)]
+    big = 1 << 40
+    nb = fm.flash_mca_gau_project_backward_workspace_bytes
+    slots = 2 * 152 * 128 * 256 * 4  # fp32 tiles of two products
+    # dpre in boxes of 64 x 64, tokens and columns rounded up to 256
+    assert nb(1000, 768, 1536, 128) == 1024 * 3328 * 2 + slots
+    assert nb(1, 64, 64, 64) == 256 * 256 * 2 + slots
+    assert nb(0, 64, 64, 64) == 0 and nb(4, 60, 64, 64) == 0 and nb(4, 64, 32, 64) == 0
+    assert nb(4, 64, 64, 96) == 0 and nb(1 << 21, 768, 1536, 128) == 0
+
+    def proj(X=a[0], Wt=a[1], dU=a[2], dV=a[3], dZ=a[4], dX=a[5], dWt=a[6], M=100, d=64, e=64, s=64,
+             ws=a[7], size=big):
+        return fm.lib.flash_mca_gau_project_backward(X, Wt, dU, dV, dZ, dX, dWt, M, d, e, s, ws,
+                                                     size, None)
+    for k in ("X", "Wt", "dU", "dV", "dZ", "dX", "dWt"):
+        assert proj(**{k: None}) == fm.FMCA_ERR_INVALID_ARG
+        assert proj(**{k: a[0] + (99 << 28) + 2}) == fm.FMCA_ERR_ALIGN
+    assert proj(M=0) == fm.FMCA_ERR_INVALID_ARG and proj(d=12) == fm.FMCA_ERR_UNSUPPORTED
+    assert proj(e=100) == fm.FMCA_ERR_UNSUPPORTED and proj(s=8) == fm.FMCA_ERR_UNSUPPORTED
+    assert proj(ws=None) == fm.FMCA_ERR_WORKSPACE and proj(size=1000) == fm.FMCA_ERR_WORKSPACE
+    assert proj(ws=a[7] + 128) == fm.FMCA_ERR_ALIGN
+    small = nb(100, 64, 64, 64)
+    for k, v in (("dX", a[0]), ("dWt", a[1]), ("dX", a[2]), ("dWt", a[5]), ("ws", a[4]), ("dX", a[7])):
+        assert proj(**{k: v, "size": small}) == fm.FMCA_ERR_INVALID_ARG
+
+    ob = fm.flash_mca_gau_output_backward_workspace_bytes
+    assert ob(100, 64, 64) == slots and ob(0, 64, 64) == 0 and ob(4, 60, 64) == 0
+    assert ob(4, 64, 32) == 0
+
+    def outp(Y=a[0], Wo=a[1], dO=a[2], dY=a[3], dW=a[4], M=100, e=64, d=64, ws=a[5], size=slots):
+        return fm.lib.flash_mca_gau_output_backward(Y, Wo, dO, dY, dW, M, e, d, ws, size, None)
+    for k in ("Y", "Wo", "dO", "dY", "dW"):
+        assert outp(**{k: None}) == fm.FMCA_ERR_INVALID_ARG
+        assert outp(**{k: a[0] + (99 << 28) + 8}) == fm.FMCA_ERR_ALIGN
+    assert outp(M=-1) == fm.FMCA_ERR_INVALID_ARG and outp(e=4) == fm.FMCA_ERR_UNSUPPORTED
+    assert outp(d=8) == fm.FMCA_ERR_UNSUPPORTED and outp(size=slots - 1) == fm.FMCA_ERR_WORKSPACE
+    for k, v in (("dY", a[0]), ("dW", a[2]), ("dY", a[4]), ("ws", a[1])):
+        assert outp(**{k: v}) == fm.FMCA_ERR_INVALID_ARG
+
+
+def test_vocab_loss_rejects_before_queueing():
+    P = 0x7F0000000000
+    a = [P + (k << 28) for k in range(10)]
+    fb, bb = fm.flash_mca_vocab_loss_workspace_bytes, fm.flash_mca_vocab_loss_backward_workspace_bytes
+    for f in (fb, bb):
+        assert f(0, 10, 64) == 0 and f(4, 0, 64) == 0 and f(4, 10, 0) == 0 and f(4, 10, 12) == 0
+        assert f(1 << 22, 10, 512) == 0 and f(4, 1 << 22, 512) == 0
+    up = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    # index, target and logit of a row, X, two fp32 pairs a row and 256 columns
+    assert fb(100, 1000, 64) == 256 + 3 * up(400) + up(100 * 128) + up(100 * 8 * 2 * 4)
+    # the logits never lie in the workspace: a piece of 256 MiB at most
+    assert bb(16384, 250000, 64) < (256 << 20) + (64 << 20)
+    assert fb(16384, 250000, 64) < 16384 * 250000 * 2 / 16
+    nf, nb = fb(100, 1000, 64), bb(100, 1000, 64)
+
+    def fwd(X=a[0], W=a[1], t=a[2], loss=a[3], lse=a[4], M=100, V=1000, d=64, ws=a[5], size=nf):
+        return fm.lib.flash_mca_vocab_loss(X, W, t, loss, lse, M, V, d, ws, size, None)
+
+    def bwd(X=a[0], W=a[1], t=a[2], lse=a[3], g=a[4], dX=a[5], dW=a[6], M=100, V=1000, d=64, ws=a[7],
+            size=nb):
+        return fm.lib.flash_mca_vocab_loss_backward(X, W, t, lse, g, dX, dW, M, V, d, ws, size, None)
+    for f, names in ((fwd, ("X", "W", "t", "loss", "lse")),
+                     (bwd, ("X", "W", "t", "lse", "g", "dX", "dW"))):
+        for k in names:
+            assert f(**{k: None}) == fm.FMCA_ERR_INVALID_ARG
+            assert f(**{k: P + (99 << 28) + 8}) == fm.FMCA_ERR_ALIGN
+        assert f(M=0) == fm.FMCA_ERR_INVALID_ARG and f(V=-5) == fm.FMCA_ERR_INVALID_ARG
+        assert f(d=60) == fm.FMCA_ERR_UNSUPPORTED and f(M=1 << 26) == fm.FMCA_ERR_UNSUPPORTED
+        assert f(ws=None) == fm.FMCA_ERR_WORKSPACE and f(size=255) == fm.FMCA_ERR_WORKSPACE
+        assert f(ws=a[9] + 16) == fm.FMCA_ERR_ALIGN
+    for k, v in (("loss", a[4]), ("lse", a[2]), ("loss", a[0]), ("ws", a[1]), ("lse", a[5])):
+        assert fwd(**{k: v}) == fm.FMCA_ERR_INVALID_ARG
+    for k, v in (("dX", a[0]), ("dW", a[1]), ("dW", a[5]), ("dX", a[4]), ("ws", a[3]), ("dX", a[7])):
+        assert bwd(**{k: v}) == fm.FMCA_ERR_INVALID_ARG
+
+
+def test_training_wrappers_check_shapes_and_types():
+    import torch
+    X, W = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(10, 64, dtype=torch.bfloat16)
+    t = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError, match="CUDA"):
+        fm.vocab_loss(X, W, t)
+    with pytest.raises(ValueError, match="2-D"):
+        fm.vocab_loss(X[0], W, t)
+    with pytest.raises(ValueError, match="2-D"):
+        fm.gau_output_backward(X[0], W, X)
+    with pytest.raises(fm.FmcaError):
+        fm.vocab_loss(X[:, :60], W, t)          # d not a multiple of 8
+    with pytest.raises(fm.FmcaError):
+        fm.gau_project_backward(X, W, X[:, :32], X[:, :32], X)
+    with pytest.raises(ValueError, match="CUDA"):
+        fm.gau_project_backward(X, W, X, X, X)
