@@ -528,59 +528,70 @@ def gau_output(Y, Wo_t, stream=None):
     return Out
 
 
-def _on(name, t, dtype, shape, device) -> int:
-    """The device address of a contiguous tensor of this type and shape on
-    `device`; raises for any other."""
-    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+# The training operators' calls are a few microseconds of device work at their
+# smallest, so their argument checks stay on cheap attribute reads and the
+# stream is fetched as a bare handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+_BF16, _FP32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int64, torch.uint8
+
+
+def _on(name, t, dtype, shape, dev) -> int:
+    """The device address of a contiguous tensor of this type and shape on CUDA
+    device `dev`; raises for any other."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or \
+            not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
     return t.data_ptr()
 
 
-def _cuda_device(name, t) -> torch.device:
-    if not t.is_cuda:
+def _on_or_none(name, t, dtype, shape, dev):
+    return None if t is None else _on(name, t, dtype, shape, dev)
+
+
+def _placed(name, t, stream, fn, *args):
+    """fn(device index, stream handle, *args) with the device of tensor `t`
+    current and `stream` (default: torch's current stream there) torch's
+    current one, so that what fn allocates belongs to the stream that uses it."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
-
-
-class _Launch:
-    """Where a call of the training operators runs: the operands' device made
-    current, and `stream` (default: torch's current stream there) made torch's
-    current one, so that what the call allocates belongs to the stream that
-    uses it.  ``with _Launch(device, stream) as ptr``."""
-    __slots__ = ("guards", "ptr")
-
-    def __init__(self, device, stream):
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is None:
-            self.ptr = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
-            elif stream.device != device:
-                raise ValueError(f"stream belongs to {stream.device}, the operands to {device}")
-            self.ptr = stream.cuda_stream
-            self.guards.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return self.ptr
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
-        return False
+    if stream is None:
+        if dev == torch.cuda.current_device():
+            return fn(dev, _raw_stream(dev), *args)
+        with torch.cuda.device(dev):
+            return fn(dev, _raw_stream(dev), *args)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=t.device)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, {name} to cuda:{dev}")
+    with torch.cuda.stream(stream):
+        return fn(dev, stream.cuda_stream, *args)
 
 
 def _norm_rows(name, x):
     """(M, d) of a [..., d] tensor: its leading dimensions are the rows."""
-    if x.dim() < 1 or x.numel() == 0:
+    n = x.numel()
+    if n == 0 or x.dim() < 1:
         raise ValueError(f"{name} must be [..., d] with at least one row")
     d = x.shape[-1]
-    return x.numel() // d, d
+    return n // d, d
+
+
+def _matrix(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
+
+
+def _workspace(nbytes, what, device):
+    if nbytes == 0:
+        raise FmcaError(FMCA_ERR_UNSUPPORTED, what)
+    return torch.empty(nbytes, dtype=_U8, device=device)
 
 
 def flash_mca_layer_norm(x, res, weight, bias, h, y, mean, rstd, eps: float = 1e-5,
@@ -589,32 +600,43 @@ def flash_mca_layer_norm(x, res, weight, bias, h, y, mean, rstd, eps: float = 1e
     x, res, h, y: [..., d] CUDA tensors of one dtype; weight, bias float32 [d];
     mean, rstd float32 [...] outputs.  res (and then h), mean and rstd may be
     None; h may be x or res itself."""
-    dev = _cuda_device("x", x)
-    M, d = _norm_rows("x", x)
-    dt, shape, f32 = _dtype_code(x), x.shape, torch.float32
     if res is not None and h is None:
         raise ValueError("h must be given with res: the sum is stored there")
-    args = [_on("x", x, x.dtype, shape, dev),
-            None if res is None else _on("res", res, x.dtype, shape, dev),
-            _on("weight", weight, f32, (d,), dev), _on("bias", bias, f32, (d,), dev),
-            None if res is None else _on("h", h, x.dtype, shape, dev),
-            _on("y", y, x.dtype, shape, dev),
-            None if mean is None else _on("mean", mean, f32, shape[:-1], dev),
-            None if rstd is None else _on("rstd", rstd, f32, shape[:-1], dev)]
-    with _Launch(dev, stream) as ptr:
-        st = lib.flash_mca_layer_norm(*args, M, d, eps, dt, ptr)
-    _check(st, "flash_mca_layer_norm")
+    _placed("x", x, stream, _layer_norm, x, res, weight, bias, h, y, mean, rstd, eps)
+
+
+def _layer_norm(dev, ptr, x, res, weight, bias, h, y, mean, rstd, eps):
+    M, d = _norm_rows("x", x)
+    dt, shape, t = _dtype_code(x), x.shape, x.dtype
+    st = lib.flash_mca_layer_norm(
+        _on("x", x, t, shape, dev), _on_or_none("res", res, t, shape, dev),
+        _on("weight", weight, _FP32, (d,), dev), _on("bias", bias, _FP32, (d,), dev),
+        None if res is None else _on("h", h, t, shape, dev), _on("y", y, t, shape, dev),
+        _on_or_none("mean", mean, _FP32, shape[:-1], dev),
+        _on_or_none("rstd", rstd, _FP32, shape[:-1], dev), M, d, eps, dt, ptr)
+    if st:
+        raise FmcaError(st, "flash_mca_layer_norm")
 
 
 def layer_norm(x, weight, bias, eps: float = 1e-5, residual=None, stream=None):
     """Allocating wrapper of flash_mca_layer_norm: returns (y, h, mean, rstd),
     h = x + residual (x itself without a residual)."""
-    with _Launch(_cuda_device("x", x), stream):
-        y = torch.empty_like(x)
-        h = x if residual is None else torch.empty_like(x)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-    flash_mca_layer_norm(x, residual, weight, bias, h, y, mean, rstd, eps, stream)
+    return _placed("x", x, stream, _layer_norm_alloc, x, weight, bias, eps, residual)
+
+
+def _layer_norm_alloc(dev, ptr, x, weight, bias, eps, res):
+    M, d = _norm_rows("x", x)
+    dt, shape, t = _dtype_code(x), x.shape, x.dtype
+    px, pr = _on("x", x, t, shape, dev), _on_or_none("residual", res, t, shape, dev)
+    pw, pb = _on("weight", weight, _FP32, (d,), dev), _on("bias", bias, _FP32, (d,), dev)
+    y = torch.empty_like(x)
+    h = x if res is None else torch.empty_like(x)
+    mean = torch.empty(shape[:-1], dtype=_FP32, device=x.device)
+    rstd = torch.empty_like(mean)
+    st = lib.flash_mca_layer_norm(px, pr, pw, pb, h.data_ptr(), y.data_ptr(), mean.data_ptr(),
+                                  rstd.data_ptr(), M, d, eps, dt, ptr)
+    if st:
+        raise FmcaError(st, "flash_mca_layer_norm")
     return y, h, mean, rstd
 
 
@@ -626,42 +648,42 @@ def flash_mca_layer_norm_backward(dy, h, weight, mean, rstd, dh, dx, dweight, db
                                   stream=None) -> None:
     """Gradients of sum(y * dy) + sum(h * dh) into dx ([..., d]) and dweight,
     dbias (float32 [d]); h, mean, rstd as flash_mca_layer_norm left them; dh may
-    be None."""
-    dev = _cuda_device("dy", dy)
+    be None.  workspace: a uint8 CUDA tensor of at least the bytes that
+    flash_mca_layer_norm_backward_workspace_bytes gives (as for every call
+    below)."""
+    _placed("dy", dy, stream, _layer_norm_backward, dy, h, weight, mean, rstd, dh, dx, dweight,
+            dbias, workspace)
+
+
+def _layer_norm_backward(dev, ptr, dy, h, weight, mean, rstd, dh, dx, dw, db, ws):
     M, d = _norm_rows("dy", dy)
-    dt, shape, f32 = _dtype_code(dy), dy.shape, torch.float32
-    args = [_on("dy", dy, dy.dtype, shape, dev), _on("h", h, dy.dtype, shape, dev),
-            _on("weight", weight, f32, (d,), dev), _on("mean", mean, f32, shape[:-1], dev),
-            _on("rstd", rstd, f32, shape[:-1], dev),
-            None if dh is None else _on("dh", dh, dy.dtype, shape, dev),
-            _on("dx", dx, dy.dtype, shape, dev), _on("dweight", dweight, f32, (d,), dev),
-            _on("dbias", dbias, f32, (d,), dev)]
-    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
-    with _Launch(dev, stream) as ptr:
-        st = lib.flash_mca_layer_norm_backward(*args, M, d, dt, ws, workspace.numel(), ptr)
-    _check(st, "flash_mca_layer_norm_backward")
+    dt, shape, t = _dtype_code(dy), dy.shape, dy.dtype
+    args = (_on("dy", dy, t, shape, dev), _on("h", h, t, shape, dev),
+            _on("weight", weight, _FP32, (d,), dev), _on("mean", mean, _FP32, shape[:-1], dev),
+            _on("rstd", rstd, _FP32, shape[:-1], dev), _on_or_none("dh", dh, t, shape, dev))
+    alloc = dx is None
+    if alloc:
+        ws = _workspace(lib.flash_mca_layer_norm_backward_workspace_bytes(M, d),
+                        "flash_mca_layer_norm_backward_workspace_bytes", dy.device)
+        dx = torch.empty_like(dy)
+        dw = torch.empty(d, dtype=_FP32, device=dy.device)
+        db = torch.empty_like(dw)
+        out = (dx.data_ptr(), dw.data_ptr(), db.data_ptr())
+    else:
+        out = (_on("dx", dx, t, shape, dev), _on("dweight", dw, _FP32, (d,), dev),
+               _on("dbias", db, _FP32, (d,), dev))
+        _on("workspace", ws, _U8, ws.shape, dev)
+    st = lib.flash_mca_layer_norm_backward(*args, *out, M, d, dt, ws.data_ptr(), ws.numel(), ptr)
+    if st:
+        raise FmcaError(st, "flash_mca_layer_norm_backward")
+    return dx, dw, db
 
 
 def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, stream=None):
     """Allocating wrapper of flash_mca_layer_norm_backward: returns
     (dx, dweight, dbias)."""
-    M, d = _norm_rows("dy", dy)
-    nb = flash_mca_layer_norm_backward_workspace_bytes(M, d)
-    if nb == 0:
-        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_layer_norm_backward_workspace_bytes")
-    with _Launch(_cuda_device("dy", dy), stream):
-        dx = torch.empty_like(dy)
-        dweight = torch.empty(d, dtype=torch.float32, device=dy.device)
-        dbias = torch.empty_like(dweight)
-        ws = torch.empty(nb, dtype=torch.uint8, device=dy.device)
-    flash_mca_layer_norm_backward(dy, h, weight, mean, rstd, dh, dx, dweight, dbias, ws, stream)
-    return dx, dweight, dbias
-
-
-def _matrix(name, t):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    return t.shape
+    return _placed("dy", dy, stream, _layer_norm_backward, dy, h, weight, mean, rstd, dh, None,
+                   None, None, None)
 
 
 def flash_mca_gau_project_backward_workspace_bytes(M: int, d: int, e: int, s: int) -> int:
@@ -671,29 +693,33 @@ def flash_mca_gau_project_backward_workspace_bytes(M: int, d: int, e: int, s: in
 def flash_mca_gau_project_backward(X, Wt, dU, dV, dZ, dX, dWt, workspace, stream=None) -> None:
     """Gradients dX [M, d], dWt [2e+s, d] of flash_mca_gau_project for dU, dV
     [M, e] and dZ [M, s]; bf16 CUDA tensors."""
-    dev, bf = _cuda_device("X", X), torch.bfloat16
+    _placed("X", X, stream, _gau_project_backward, X, Wt, dU, dV, dZ, dX, dWt, workspace)
+
+
+def _gau_project_backward(dev, ptr, X, Wt, dU, dV, dZ, dX, dWt, ws):
     (M, d), (_, e), (_, s) = _matrix("X", X), _matrix("dU", dU), _matrix("dZ", dZ)
-    args = [_on("X", X, bf, (M, d), dev), _on("Wt", Wt, bf, (2 * e + s, d), dev),
-            _on("dU", dU, bf, (M, e), dev), _on("dV", dV, bf, (M, e), dev),
-            _on("dZ", dZ, bf, (M, s), dev), _on("dX", dX, bf, (M, d), dev),
-            _on("dWt", dWt, bf, (2 * e + s, d), dev)]
-    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
-    with _Launch(dev, stream) as ptr:
-        st = lib.flash_mca_gau_project_backward(*args, M, d, e, s, ws, workspace.numel(), ptr)
-    _check(st, "flash_mca_gau_project_backward")
+    N = 2 * e + s
+    args = (_on("X", X, _BF16, (M, d), dev), _on("Wt", Wt, _BF16, (N, d), dev),
+            _on("dU", dU, _BF16, (M, e), dev), _on("dV", dV, _BF16, (M, e), dev),
+            _on("dZ", dZ, _BF16, (M, s), dev))
+    if dX is None:
+        ws = _workspace(lib.flash_mca_gau_project_backward_workspace_bytes(M, d, e, s),
+                        "flash_mca_gau_project_backward_workspace_bytes", X.device)
+        dX, dWt = torch.empty_like(X), torch.empty_like(Wt)
+        out = (dX.data_ptr(), dWt.data_ptr())
+    else:
+        out = (_on("dX", dX, _BF16, (M, d), dev), _on("dWt", dWt, _BF16, (N, d), dev))
+        _on("workspace", ws, _U8, ws.shape, dev)
+    st = lib.flash_mca_gau_project_backward(*args, *out, M, d, e, s, ws.data_ptr(), ws.numel(),
+                                            ptr)
+    if st:
+        raise FmcaError(st, "flash_mca_gau_project_backward")
+    return dX, dWt
 
 
 def gau_project_backward(X, Wt, dU, dV, dZ, stream=None):
     """Allocating wrapper of flash_mca_gau_project_backward: returns (dX, dWt)."""
-    (M, d), (_, e), (_, s) = _matrix("X", X), _matrix("dU", dU), _matrix("dZ", dZ)
-    nb = flash_mca_gau_project_backward_workspace_bytes(M, d, e, s)
-    if nb == 0:
-        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_gau_project_backward_workspace_bytes")
-    with _Launch(_cuda_device("X", X), stream):
-        dX, dWt = torch.empty_like(X), torch.empty_like(Wt)
-        ws = torch.empty(nb, dtype=torch.uint8, device=X.device)
-    flash_mca_gau_project_backward(X, Wt, dU, dV, dZ, dX, dWt, ws, stream)
-    return dX, dWt
+    return _placed("X", X, stream, _gau_project_backward, X, Wt, dU, dV, dZ, None, None, None)
 
 
 def flash_mca_gau_output_backward_workspace_bytes(M: int, e: int, d: int) -> int:
@@ -703,28 +729,30 @@ def flash_mca_gau_output_backward_workspace_bytes(M: int, e: int, d: int) -> int
 def flash_mca_gau_output_backward(Y, Wo_t, dOut, dY, dWo_t, workspace, stream=None) -> None:
     """Gradients dY [M, e], dWo_t [d, e] of flash_mca_gau_output for dOut
     [M, d]; bf16 CUDA tensors."""
-    dev, bf = _cuda_device("Y", Y), torch.bfloat16
+    _placed("Y", Y, stream, _gau_output_backward, Y, Wo_t, dOut, dY, dWo_t, workspace)
+
+
+def _gau_output_backward(dev, ptr, Y, Wo_t, dOut, dY, dWo_t, ws):
     (M, e), (_, d) = _matrix("Y", Y), _matrix("dOut", dOut)
-    args = [_on("Y", Y, bf, (M, e), dev), _on("Wo_t", Wo_t, bf, (d, e), dev),
-            _on("dOut", dOut, bf, (M, d), dev), _on("dY", dY, bf, (M, e), dev),
-            _on("dWo_t", dWo_t, bf, (d, e), dev)]
-    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
-    with _Launch(dev, stream) as ptr:
-        st = lib.flash_mca_gau_output_backward(*args, M, e, d, ws, workspace.numel(), ptr)
-    _check(st, "flash_mca_gau_output_backward")
+    args = (_on("Y", Y, _BF16, (M, e), dev), _on("Wo_t", Wo_t, _BF16, (d, e), dev),
+            _on("dOut", dOut, _BF16, (M, d), dev))
+    if dY is None:
+        ws = _workspace(lib.flash_mca_gau_output_backward_workspace_bytes(M, e, d),
+                        "flash_mca_gau_output_backward_workspace_bytes", Y.device)
+        dY, dWo_t = torch.empty_like(Y), torch.empty_like(Wo_t)
+        out = (dY.data_ptr(), dWo_t.data_ptr())
+    else:
+        out = (_on("dY", dY, _BF16, (M, e), dev), _on("dWo_t", dWo_t, _BF16, (d, e), dev))
+        _on("workspace", ws, _U8, ws.shape, dev)
+    st = lib.flash_mca_gau_output_backward(*args, *out, M, e, d, ws.data_ptr(), ws.numel(), ptr)
+    if st:
+        raise FmcaError(st, "flash_mca_gau_output_backward")
+    return dY, dWo_t
 
 
 def gau_output_backward(Y, Wo_t, dOut, stream=None):
     """Allocating wrapper of flash_mca_gau_output_backward: returns (dY, dWo_t)."""
-    (M, e), (_, d) = _matrix("Y", Y), _matrix("dOut", dOut)
-    nb = flash_mca_gau_output_backward_workspace_bytes(M, e, d)
-    if nb == 0:
-        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_gau_output_backward_workspace_bytes")
-    with _Launch(_cuda_device("Y", Y), stream):
-        dY, dWo_t = torch.empty_like(Y), torch.empty_like(Wo_t)
-        ws = torch.empty(nb, dtype=torch.uint8, device=Y.device)
-    flash_mca_gau_output_backward(Y, Wo_t, dOut, dY, dWo_t, ws, stream)
-    return dY, dWo_t
+    return _placed("Y", Y, stream, _gau_output_backward, Y, Wo_t, dOut, None, None, None)
 
 
 def flash_mca_vocab_loss_workspace_bytes(M: int, V: int, d: int) -> int:
@@ -735,29 +763,31 @@ def flash_mca_vocab_loss(X, W, target, loss, lse, workspace, stream=None) -> Non
     """Softmax cross entropy of X [M, d] against the vocabulary W [V, d] (bf16)
     into loss and lse (float32 [M]); target int64 [M], rows whose target is
     outside 0 .. V - 1 are ignored (loss and lse 0)."""
-    dev, bf = _cuda_device("X", X), torch.bfloat16
+    _placed("X", X, stream, _vocab_loss, X, W, target, loss, lse, workspace)
+
+
+def _vocab_loss(dev, ptr, X, W, target, loss, lse, ws):
     (M, d), (V, _) = _matrix("X", X), _matrix("W", W)
-    args = [_on("X", X, bf, (M, d), dev), _on("W", W, bf, (V, d), dev),
-            _on("target", target, torch.int64, (M,), dev),
-            _on("loss", loss, torch.float32, (M,), dev), _on("lse", lse, torch.float32, (M,), dev)]
-    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
-    with _Launch(dev, stream) as ptr:
-        st = lib.flash_mca_vocab_loss(*args, M, V, d, ws, workspace.numel(), ptr)
-    _check(st, "flash_mca_vocab_loss")
+    args = (_on("X", X, _BF16, (M, d), dev), _on("W", W, _BF16, (V, d), dev),
+            _on("target", target, _I64, (M,), dev))
+    if loss is None:
+        ws = _workspace(lib.flash_mca_vocab_loss_workspace_bytes(M, V, d),
+                        "flash_mca_vocab_loss_workspace_bytes", X.device)
+        loss = torch.empty(M, dtype=_FP32, device=X.device)
+        lse = torch.empty_like(loss)
+        out = (loss.data_ptr(), lse.data_ptr())
+    else:
+        out = (_on("loss", loss, _FP32, (M,), dev), _on("lse", lse, _FP32, (M,), dev))
+        _on("workspace", ws, _U8, ws.shape, dev)
+    st = lib.flash_mca_vocab_loss(*args, *out, M, V, d, ws.data_ptr(), ws.numel(), ptr)
+    if st:
+        raise FmcaError(st, "flash_mca_vocab_loss")
+    return loss, lse
 
 
 def vocab_loss(X, W, target, stream=None):
     """Allocating wrapper of flash_mca_vocab_loss: returns (loss, lse)."""
-    (M, d), (V, _) = _matrix("X", X), _matrix("W", W)
-    nb = flash_mca_vocab_loss_workspace_bytes(M, V, d)
-    if nb == 0:
-        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_vocab_loss_workspace_bytes")
-    with _Launch(_cuda_device("X", X), stream):
-        loss = torch.empty(M, dtype=torch.float32, device=X.device)
-        lse = torch.empty_like(loss)
-        ws = torch.empty(nb, dtype=torch.uint8, device=X.device)
-    flash_mca_vocab_loss(X, W, target, loss, lse, ws, stream)
-    return loss, lse
+    return _placed("X", X, stream, _vocab_loss, X, W, target, None, None, None)
 
 
 def flash_mca_vocab_loss_backward_workspace_bytes(M: int, V: int, d: int) -> int:
@@ -768,29 +798,32 @@ def flash_mca_vocab_loss_backward(X, W, target, lse, dloss, dX, dW, workspace,
                                   stream=None) -> None:
     """Gradients of sum(loss * dloss) into dX [M, d] and dW [V, d] (bf16); lse
     as flash_mca_vocab_loss left it, dloss float32 [M]."""
-    dev, bf, f32 = _cuda_device("X", X), torch.bfloat16, torch.float32
+    _placed("X", X, stream, _vocab_loss_backward, X, W, target, lse, dloss, dX, dW, workspace)
+
+
+def _vocab_loss_backward(dev, ptr, X, W, target, lse, dloss, dX, dW, ws):
     (M, d), (V, _) = _matrix("X", X), _matrix("W", W)
-    args = [_on("X", X, bf, (M, d), dev), _on("W", W, bf, (V, d), dev),
-            _on("target", target, torch.int64, (M,), dev), _on("lse", lse, f32, (M,), dev),
-            _on("dloss", dloss, f32, (M,), dev), _on("dX", dX, bf, (M, d), dev),
-            _on("dW", dW, bf, (V, d), dev)]
-    ws = _on("workspace", workspace, torch.uint8, workspace.shape, dev)
-    with _Launch(dev, stream) as ptr:
-        st = lib.flash_mca_vocab_loss_backward(*args, M, V, d, ws, workspace.numel(), ptr)
-    _check(st, "flash_mca_vocab_loss_backward")
+    args = (_on("X", X, _BF16, (M, d), dev), _on("W", W, _BF16, (V, d), dev),
+            _on("target", target, _I64, (M,), dev), _on("lse", lse, _FP32, (M,), dev),
+            _on("dloss", dloss, _FP32, (M,), dev))
+    if dX is None:
+        ws = _workspace(lib.flash_mca_vocab_loss_backward_workspace_bytes(M, V, d),
+                        "flash_mca_vocab_loss_backward_workspace_bytes", X.device)
+        dX, dW = torch.empty_like(X), torch.empty_like(W)
+        out = (dX.data_ptr(), dW.data_ptr())
+    else:
+        out = (_on("dX", dX, _BF16, (M, d), dev), _on("dW", dW, _BF16, (V, d), dev))
+        _on("workspace", ws, _U8, ws.shape, dev)
+    st = lib.flash_mca_vocab_loss_backward(*args, *out, M, V, d, ws.data_ptr(), ws.numel(), ptr)
+    if st:
+        raise FmcaError(st, "flash_mca_vocab_loss_backward")
+    return dX, dW
 
 
 def vocab_loss_backward(X, W, target, lse, dloss, stream=None):
     """Allocating wrapper of flash_mca_vocab_loss_backward: returns (dX, dW)."""
-    (M, d), (V, _) = _matrix("X", X), _matrix("W", W)
-    nb = flash_mca_vocab_loss_backward_workspace_bytes(M, V, d)
-    if nb == 0:
-        raise FmcaError(FMCA_ERR_UNSUPPORTED, "flash_mca_vocab_loss_backward_workspace_bytes")
-    with _Launch(_cuda_device("X", X), stream):
-        dX, dW = torch.empty_like(X), torch.empty_like(W)
-        ws = torch.empty(nb, dtype=torch.uint8, device=X.device)
-    flash_mca_vocab_loss_backward(X, W, target, lse, dloss, dX, dW, ws, stream)
-    return dX, dW
+    return _placed("X", X, stream, _vocab_loss_backward, X, W, target, lse, dloss, None, None,
+                   None)
 
 
 def flash_mca_device_status(stream=None) -> tuple[int, int]:

@@ -34,6 +34,7 @@ namespace fmca {
 namespace {
 
 constexpr int kNormThreads = 256;
+constexpr size_t kNormMaxSmem = 200 << 10;  // of a block of the backward pass
 
 template <int BYTES>
 struct Raw;
@@ -195,59 +196,111 @@ __global__ void __launch_bounds__(kNormThreads)
   }
 }
 
+// Asynchronous copy of one vector to this thread's own place in shared memory;
+// the thread that copied it is the only one to read it, so waiting for its
+// copies (copies_wait) is all the synchronisation there is.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows on their way to a block of the backward pass: the group's current row
+// and the next, three operands (dy, h, dh) each.
+constexpr int kNormStages = 2;
+template <typename T, int VEC, int N>
+constexpr size_t norm_ring_bytes() {
+  // single 2-byte elements cannot be copied asynchronously: read in place
+  return sizeof(T) * VEC >= 4 ? (size_t)kNormStages * 3 * N * kNormThreads * sizeof(T) * VEC : 0;
+}
+
 // dx, and the block's sums of dw and db: part [blocks][2][d].  Rows are dealt
-// to the groups round-robin.
+// to the groups round-robin.  While a row is reduced the next one is on its
+// way to shared memory, which costs no registers: those hold the running dw
+// and db (2 x 24 at d = 768), and what is in flight sets the rate.
 template <typename T, int VEC, int N, int GROUP>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, 2)
     norm_backward(const T *__restrict__ dy, const T *__restrict__ h,
                   const float *__restrict__ weight, const float *__restrict__ mean_in,
                   const float *__restrict__ rstd_in, const T *__restrict__ dh,
                   T *__restrict__ dx, float *__restrict__ part, int M, int d) {
   __shared__ float red[2][kNormThreads / 32];
-  extern __shared__ float acc_s[];  // [2][d] when a block holds several groups
+  extern __shared__ __align__(16) uint8_t ring[];
   int turn = 0;
   constexpr int kRows = kNormThreads / GROUP;
+  constexpr bool kRing = sizeof(T) * VEC >= 4;
   const int lane = threadIdx.x % GROUP, grp = threadIdx.x / GROUP;
   const int nv = d / VEC;
   const float inv_d = 1.0f / (float)d;
+  griddep_launch_dependents();
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  auto place = [&](int stage, int op, int i) {
+    return reinterpret_cast<T *>(ring) +
+           (int64_t)(((stage * 3 + op) * N + i) * kNormThreads + threadIdx.x) * VEC;
+  };
+  auto fetch = [&](int64_t row, int stage) {
+    if constexpr (kRing) {
+      if (row < M) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int c = lane + i * GROUP;
+          if (c < nv) {
+            const int64_t at = row * d + (int64_t)c * VEC;
+            copy_async<(int)sizeof(T) * VEC>(place(stage, 0, i), dy + at);
+            copy_async<(int)sizeof(T) * VEC>(place(stage, 1, i), h + at);
+            if (dh != nullptr) copy_async<(int)sizeof(T) * VEC>(place(stage, 2, i), dh + at);
+          }
+        }
+      }
+      copies_commit();
+    }
+  };
   float dw[N * VEC], db[N * VEC];
 #pragma unroll
   for (int i = 0; i < N * VEC; ++i) dw[i] = 0.f, db[i] = 0.f;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + grp; row < M;
-       row += (int64_t)gridDim.x * kRows) {
+  int64_t row = (int64_t)blockIdx.x * kRows + grp;
+  fetch(row, 0);
+  for (int stage = 0; row < M; row += step, stage ^= 1) {
+    fetch(row + step, stage ^ 1);
     const float mean = mean_in[row], rstd = rstd_in[row];
-    float g[N * VEC], xh[N * VEC];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = lane + i * GROUP;
-      if (c < nv) {
-        load_vec<T, VEC>(dy + row * d + (int64_t)c * VEC, g + i * VEC);
-        load_vec<T, VEC>(h + row * d + (int64_t)c * VEC, xh + i * VEC);
+    // vector i of operand op of this row
+    auto take = [&](int op, int i, float *out) {
+      if constexpr (kRing) {
+        load_vec<T, VEC>(place(stage, op, i), out);
       } else {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) g[i * VEC + k] = 0.f, xh[i * VEC + k] = mean;
+        const T *src = op == 0 ? dy : op == 1 ? h : dh;
+        load_vec<T, VEC>(src + row * d + (int64_t)(lane + i * GROUP) * VEC, out);
       }
-    }
+    };
+    if constexpr (kRing) copies_wait<1>();
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = lane + i * GROUP;
-      float w[VEC];
       if (c < nv) {
+        float g[VEC], xh[VEC], w[VEC];
+        take(0, i, g);
+        take(1, i, xh);
         load_w<VEC>(weight + c * VEC, w);
-      } else {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) w[k] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const int e = i * VEC + k;
-        xh[e] = (xh[e] - mean) * rstd;
-        dw[e] += g[e] * xh[e];
-        db[e] += g[e];
-        g[e] *= w[k];
-        s1 += g[e];
-        s2 += g[e] * xh[e];
+        for (int k = 0; k < VEC; ++k) {
+          const float x = (xh[k] - mean) * rstd, t = g[k] * w[k];
+          dw[i * VEC + k] += g[k] * x;
+          db[i * VEC + k] += g[k];
+          s1 += t;
+          s2 += t * x;
+        }
       }
     }
     const float m1 = group_sum<GROUP>(s1, red, turn) * inv_d;
@@ -256,15 +309,16 @@ __global__ void __launch_bounds__(kNormThreads)
     for (int i = 0; i < N; ++i) {
       const int c = lane + i * GROUP;
       if (c < nv) {
-        float o[VEC];
+        float g[VEC], xh[VEC], w[VEC], o[VEC];
+        take(0, i, g);
+        take(1, i, xh);
+        load_w<VEC>(weight + c * VEC, w);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const int e = i * VEC + k;
-          o[k] = rstd * (g[e] - m1 - xh[e] * m2);
-        }
+        for (int k = 0; k < VEC; ++k)
+          o[k] = rstd * (g[k] * w[k] - m1 - (xh[k] - mean) * rstd * m2);
         if (dh != nullptr) {
           float r[VEC];
-          load_vec<T, VEC>(dh + row * d + (int64_t)c * VEC, r);
+          take(2, i, r);
 #pragma unroll
           for (int k = 0; k < VEC; ++k) o[k] += r[k];
         }
@@ -272,7 +326,7 @@ __global__ void __launch_bounds__(kNormThreads)
       }
     }
   }
-  float *pw = part + (int64_t)blockIdx.x * 2 * d, *pb = pw + d;
+  float *pw = part + (int64_t)blockIdx.x * 2 * d;
   if constexpr (GROUP == kNormThreads) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -281,32 +335,35 @@ __global__ void __launch_bounds__(kNormThreads)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
           pw[c * VEC + k] = dw[i * VEC + k];
-          pb[c * VEC + k] = db[i * VEC + k];
+          pw[d + c * VEC + k] = db[i * VEC + k];
         }
     }
   } else {
-    // the groups add their sums one after the other (a fixed order)
-    for (int q = 0; q < kRows; ++q) {
-      if (grp == q) {
+    // the groups' sums side by side in the ring's place, added in order
+    if constexpr (kRing) copies_wait<0>();
+    __syncthreads();
+    float *acc = reinterpret_cast<float *>(ring);  // [kRows][2][d]
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int c = lane + i * GROUP;
-          if (c < nv)
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * GROUP;
+      if (c < nv)
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-              const int j = c * VEC + k;
-              acc_s[j] = (q ? acc_s[j] : 0.f) + dw[i * VEC + k];
-              acc_s[d + j] = (q ? acc_s[d + j] : 0.f) + db[i * VEC + k];
-            }
+        for (int k = 0; k < VEC; ++k) {
+          acc[grp * 2 * d + c * VEC + k] = dw[i * VEC + k];
+          acc[grp * 2 * d + d + c * VEC + k] = db[i * VEC + k];
         }
-      }
-      __syncthreads();
     }
-    for (int j = threadIdx.x; j < 2 * d; j += kNormThreads) pw[j] = acc_s[j];
+    __syncthreads();
+    for (int j = threadIdx.x; j < 2 * d; j += kNormThreads) {
+      float t = acc[j];
+#pragma unroll
+      for (int q = 1; q < kRows; ++q) t += acc[q * 2 * d + j];
+      pw[j] = t;
+    }
   }
 }
 
-// dw and db from the blocks' partial rows: a block sums 32 columns, 8 row
+// dw and db from the blocks' partial rows: a block sums 32 columns, 32
 // lanes of partial rows each, lanes joined in order.
 constexpr int kNormSumCols = 32, kNormSumLanes = 32;
 __global__ void __launch_bounds__(kNormSumCols *kNormSumLanes)
@@ -317,8 +374,10 @@ __global__ void __launch_bounds__(kNormSumCols *kNormSumLanes)
   const int col = threadIdx.x % kNormSumCols, r = threadIdx.x / kNormSumCols;
   const int j = blockIdx.x * kNormSumCols + col;
   float v = 0.f;
-  if (j < 2 * d)
+  if (j < 2 * d) {
+#pragma unroll 5
     for (int b = r; b < blocks; b += kNormSumLanes) v += part[(int64_t)b * 2 * d + j];
+  }
   s[r][col] = v;
   __syncthreads();
   if (r == 0 && j < 2 * d) {
@@ -347,9 +406,21 @@ cudaError_t launch_fwd(const NormArgs &a, cudaStream_t stream) {
       static_cast<T *>(a.o0), static_cast<T *>(a.o1), a.f0, a.f1, a.M, a.d, a.eps);
   return cudaGetLastError();
 }
+static_assert(norm_ring_bytes<float, 4, 8>() <= kNormMaxSmem, "two rows of every group fit");
 template <typename T, int VEC, int N, int GROUP>
 cudaError_t launch_bwd(const NormArgs &a, cudaStream_t stream) {
-  const size_t smem = GROUP < kNormThreads ? 2 * sizeof(float) * (size_t)a.d : 0;
+  size_t smem = norm_ring_bytes<T, VEC, N>();
+  if (GROUP < kNormThreads) {
+    const size_t sums = 2 * sizeof(float) * (size_t)a.d * (kNormThreads / GROUP);
+    if (sums > smem) smem = sums;
+  }
+  static OncePerDevice attrs;
+  if (!attrs.run([] {
+        return cudaFuncSetAttribute(norm_backward<T, VEC, N, GROUP>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kNormMaxSmem) == cudaSuccess;
+      }))
+    return cudaErrorInvalidValue;
   norm_backward<T, VEC, N, GROUP><<<a.blocks, kNormThreads, smem, stream>>>(
       static_cast<const T *>(a.a), static_cast<const T *>(a.b), a.weight, a.mean, a.rstd,
       static_cast<const T *>(a.dh), static_cast<T *>(a.o0), a.f0, a.M, a.d);

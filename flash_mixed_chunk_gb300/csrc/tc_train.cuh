@@ -230,46 +230,83 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- host side
-template <int CG, int KIND>
-int launch_tgemm_kind(const TgParams &P, int workers, cudaStream_t stream) {
-  static OncePerDevice attrs;
-  if (!attrs.run([] {
-        return cudaFuncSetAttribute(tc_tgemm<CG, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)TgCfg<CG>::SMEM) == cudaSuccess;
-      }))
-    return 1;
+// Launch configuration of one tc_tgemm (its attributes live in the object).
+template <int CG>
+struct TgLaunch {
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(workers * CG);
-  cfg.blockDim = dim3(TG_THREADS);
-  cfg.dynamicSmemBytes = TgCfg<CG>::SMEM;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, tc_tgemm<CG, KIND>, P) == cudaSuccess ? 0 : 1;
+  cudaLaunchConfig_t cfg;
+  TgLaunch(int workers, cudaStream_t stream) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg = cudaLaunchConfig_t{};
+    cfg.gridDim = dim3(workers * CG);
+    cfg.blockDim = dim3(TG_THREADS);
+    cfg.dynamicSmemBytes = TgCfg<CG>::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
+  }
+};
+
+// CTAs (or pairs) that the current device holds at once, 0 on an error.  Pairs
+// sit within a group of SMs, so there can be fewer than half the SMs: the
+// units are dealt to the workers beforehand, and one that had to wait for
+// another to leave would double the time.
+template <int CG, int KIND>
+int tg_resident() {
+  static OncePerDevice once;
+  static int resident[OncePerDevice::kMaxDevices];
+  int dev = 0;
+  if (!once.run([] {
+        int d = 0, n = 0;
+        if (cudaGetDevice(&d) != cudaSuccess ||
+            cudaFuncSetAttribute(tc_tgemm<CG, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)TgCfg<CG>::SMEM) != cudaSuccess)
+          return false;
+        n = num_sms() / CG;
+        if (CG == 2) {
+          TgLaunch<CG> l(n, nullptr);
+          l.cfg.attrs = &l.attr[1];
+          l.cfg.numAttrs = 1;
+          int fit = 0;
+          if (cudaOccupancyMaxActiveClusters(&fit, tc_tgemm<CG, KIND>, &l.cfg) != cudaSuccess)
+            return false;
+          if (fit < n) n = fit;
+        }
+        if (n * CG > kTgMaxCtas) n = kTgMaxCtas / CG;
+        resident[d] = n;
+        return n > 0;
+      }) ||
+      cudaGetDevice(&dev) != cudaSuccess)
+    return 0;
+  return resident[dev];
 }
 
-// Workers of a launch: one CTA (or pair) an SM, no more than there are units
-// with every row taking part, and no more than the workspace was sized for.
+template <int CG, int KIND>
+int launch_tgemm_kind(const TgParams &P, int workers, cudaStream_t stream) {
+  TgLaunch<CG> l(workers, stream);
+  return cudaLaunchKernelEx(&l.cfg, tc_tgemm<CG, KIND>, P) == cudaSuccess ? 0 : 1;
+}
+
+// Workers of a launch: all that are resident at once, no more than there are
+// units with every row taking part.
 template <int CG, int KIND>
 int tg_workers(const TgParams &P) {
-  const int sms = num_sms();
-  int w = (sms < kTgMaxCtas ? sms : kTgMaxCtas) / CG;
-  if (KIND != TG_GRAD) {
+  int w = tg_resident<CG, KIND>();
+  if (KIND != TG_GRAD && w > 0) {
     const TgPlan p = tg_plan<CG, KIND>(P, P.piece, P.M, w);
     if (p.s[0].units < w) w = p.s[0].units;
   }
-  return w < 1 ? 1 : w;
+  return w;
 }
 template <int CG, int KIND>
 int launch_tgemm(const TgParams &P, cudaStream_t stream) {
-  return launch_tgemm_kind<CG, KIND>(P, tg_workers<CG, KIND>(P), stream);
+  const int w = tg_workers<CG, KIND>(P);
+  return w > 0 ? launch_tgemm_kind<CG, KIND>(P, w, stream) : 1;
 }
 
 // TG_GRAD on piece P.piece of np and, where a product may have been split, the
@@ -280,7 +317,7 @@ template <int CG>
 int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
   const bool last = P.piece == np - 1;
   const int w = tg_workers<CG, TG_GRAD>(P);
-  if (launch_tgemm_kind<CG, TG_GRAD>(P, w, stream)) return 1;
+  if (w <= 0 || launch_tgemm_kind<CG, TG_GRAD>(P, w, stream)) return 1;
   const TgPlan p = tg_plan<CG, TG_GRAD>(P, P.piece, P.M, w);
   const bool join = p.s[0].S > 1 || np > 1 || (last && (p.s[1].S > 1 || P.hdr != nullptr));
   if (!join) return 0;
@@ -296,16 +333,18 @@ int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, tg_join<CG>, P, w, last ? 1 : 0) == cudaSuccess ? 0 : 1;
 }
 
-constexpr int kCG = 1;
+// CTA pairs for more rows than one CTA's tile has; up to 128 rows (a short
+// fine-tuning batch, a few tokens) half of a pair's tile would stay empty.
+bool tg_pairs(int M) { return M > 128; }
 
 // X [M][K] and W [N][K] of the products with tokens as rows
+template <int CG>
 bool nt_maps(TgParams &P, const void *X, const void *W, int M, int N, int K) {
-  return make_map_bf16(&P.A, X, K, M, 64, 128) && make_map_bf16(&P.B, W, K, N, 64, 256 / kCG);
+  return make_map_bf16(&P.A, X, K, M, 64, 128) && make_map_bf16(&P.B, W, K, N, 64, 256 / CG);
 }
 
-}  // namespace
-
-int launch_vocab_loss(const void *X, const void *W, const int64_t *target, float *loss, float *lse,
+template <int CG>
+int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *loss, float *lse,
                       int M, int V, int d, void *workspace, cudaStream_t stream) {
   const VocabLossLayout L = vocab_loss_layout(M, V, d);
   char *ws = static_cast<char *>(workspace);
@@ -324,13 +363,13 @@ int launch_vocab_loss(const void *X, const void *W, const int64_t *target, float
   if (cudaGetLastError() != cudaSuccess) return 1;
 
   TgParams P = {};
-  if (!nt_maps(P, a.Xc, W, M, V, d)) return 2;
+  if (!nt_maps<CG>(P, a.Xc, W, M, V, d)) return 2;
   P.M = M, P.N = V, P.K = d;
   P.hdr = a.hdr;
   P.part = reinterpret_cast<float2 *>(ws + L.part);
   P.ztgt = reinterpret_cast<float *>(ws + L.ztgt);
   P.tgt = a.tgt;
-  if (int rc = launch_tgemm<kCG, TG_LSE>(P, stream)) return rc;
+  if (int rc = launch_tgemm<CG, TG_LSE>(P, stream)) return rc;
 
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -348,7 +387,8 @@ int launch_vocab_loss(const void *X, const void *W, const int64_t *target, float
              : 1;
 }
 
-int launch_vocab_loss_backward(const void *X, const void *W, const int64_t *target,
+template <int CG>
+int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
                                const float *lse, const float *dloss, void *dX, void *dW, int M,
                                int V, int d, void *workspace, cudaStream_t stream) {
   const VocabGradLayout L = vocab_grad_layout(M, V, d);
@@ -371,7 +411,7 @@ int launch_vocab_loss_backward(const void *X, const void *W, const int64_t *targ
   if (cudaGetLastError() != cudaSuccess) return 1;
 
   TgParams P = {}, Q = {};
-  if (!nt_maps(P, a.Xc, W, M, V, d)) return 2;
+  if (!nt_maps<CG>(P, a.Xc, W, M, V, d)) return 2;
   P.M = M, P.N = V, P.K = d;
   P.cap_boxes = L.cap_boxes;
   P.hdr = a.hdr;
@@ -392,20 +432,21 @@ int launch_vocab_loss_backward(const void *X, const void *W, const int64_t *targ
   const int np = tg_pieces(M, V, L.cap_boxes).np;  // with fewer rows no more pieces
   for (int k = 0; k < np; ++k) {
     P.piece = Q.piece = k;
-    if (int rc = launch_tgemm<kCG, TG_PROB>(P, stream)) return rc;
-    if (int rc = launch_grad<kCG>(Q, np, stream)) return rc;
+    if (int rc = launch_tgemm<CG, TG_PROB>(P, stream)) return rc;
+    if (int rc = launch_grad<CG>(Q, np, stream)) return rc;
   }
   return 0;
 }
 
-int launch_gau_project_backward(const void *X, const void *Wt, const void *dU, const void *dV,
+template <int CG>
+int gau_project_backward_cg(const void *X, const void *Wt, const void *dU, const void *dV,
                                 const void *dZ, void *dX, void *dWt, int M, int d, int e, int s,
                                 void *workspace, cudaStream_t stream) {
   const int N = 2 * e + s;
   const ProjectGradLayout L = project_grad_layout(M, N, d);
   char *ws = static_cast<char *>(workspace);
   TgParams P = {}, Q = {};
-  if (!nt_maps(P, X, Wt, M, N, d)) return 2;
+  if (!nt_maps<CG>(P, X, Wt, M, N, d)) return 2;
   P.M = M, P.N = N, P.K = d;
   P.cap_boxes = L.cap_boxes;
   P.d0 = static_cast<const __nv_bfloat16 *>(dU);
@@ -423,11 +464,12 @@ int launch_gau_project_backward(const void *X, const void *Wt, const void *dU, c
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
   Q.slots0 = reinterpret_cast<float *>(ws + L.slots0);
   Q.slots1 = reinterpret_cast<float *>(ws + L.slots1);
-  if (int rc = launch_tgemm<kCG, TG_SILU>(P, stream)) return rc;
-  return launch_grad<kCG>(Q, 1, stream);
+  if (int rc = launch_tgemm<CG, TG_SILU>(P, stream)) return rc;
+  return launch_grad<CG>(Q, 1, stream);
 }
 
-int launch_gau_output_backward(const void *Y, const void *Wo_t, const void *dOut, void *dY,
+template <int CG>
+int gau_output_backward_cg(const void *Y, const void *Wo_t, const void *dOut, void *dY,
                                void *dWo_t, int M, int e, int d, void *workspace,
                                cudaStream_t stream) {
   const OutputGradLayout L = output_grad_layout(M, d, e);
@@ -443,7 +485,36 @@ int launch_gau_output_backward(const void *Y, const void *Wo_t, const void *dOut
   Q.D1 = static_cast<__nv_bfloat16 *>(dY);
   Q.slots0 = reinterpret_cast<float *>(ws + L.slots0);
   Q.slots1 = reinterpret_cast<float *>(ws + L.slots1);
-  return launch_grad<kCG>(Q, 1, stream);
+  return launch_grad<CG>(Q, 1, stream);
+}
+
+}  // namespace
+
+int launch_vocab_loss(const void *X, const void *W, const int64_t *target, float *loss, float *lse,
+                      int M, int V, int d, void *workspace, cudaStream_t stream) {
+  return (tg_pairs(M) ? vocab_loss_cg<2> : vocab_loss_cg<1>)(X, W, target, loss, lse, M, V, d,
+                                                            workspace, stream);
+}
+
+int launch_vocab_loss_backward(const void *X, const void *W, const int64_t *target,
+                               const float *lse, const float *dloss, void *dX, void *dW, int M,
+                               int V, int d, void *workspace, cudaStream_t stream) {
+  return (tg_pairs(M) ? vocab_loss_backward_cg<2> : vocab_loss_backward_cg<1>)(
+      X, W, target, lse, dloss, dX, dW, M, V, d, workspace, stream);
+}
+
+int launch_gau_project_backward(const void *X, const void *Wt, const void *dU, const void *dV,
+                                const void *dZ, void *dX, void *dWt, int M, int d, int e, int s,
+                                void *workspace, cudaStream_t stream) {
+  return (tg_pairs(M) ? gau_project_backward_cg<2> : gau_project_backward_cg<1>)(
+      X, Wt, dU, dV, dZ, dX, dWt, M, d, e, s, workspace, stream);
+}
+
+int launch_gau_output_backward(const void *Y, const void *Wo_t, const void *dOut, void *dY,
+                               void *dWo_t, int M, int e, int d, void *workspace,
+                               cudaStream_t stream) {
+  return (tg_pairs(M) ? gau_output_backward_cg<2> : gau_output_backward_cg<1>)(
+      Y, Wo_t, dOut, dY, dWo_t, M, e, d, workspace, stream);
 }
 
 }  // namespace fmca

@@ -187,3 +187,24 @@ def test_more_rows_than_32_bits_of_elements_reach():
     ref = m.layer_norm(tail, w, b, EPS)[0]
     assert torch.equal(y[-200:], ref)
     assert (y[:4] == 0).all()
+
+
+def test_refusals():
+    m = fm()
+    x, res, w, b, dy, dh = cuda(*make(4, 64, BF, 8, True))
+    for bad in (lambda: m.layer_norm(x[:0], w, b), lambda: m.layer_norm(x.t(), w[:4], b[:4]),
+                lambda: m.layer_norm(x, w.to(BF), b), lambda: m.layer_norm(x, w[:32], b),
+                lambda: m.layer_norm(x, w, b, residual=res.float()),
+                lambda: m.layer_norm(x, w, b, residual=res[:2]),
+                lambda: m.layer_norm(x, w, b.cpu()),
+                lambda: m.flash_mca_layer_norm(x, res, w, b, None, torch.empty_like(x), None, None)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        m.layer_norm(x.half(), w, b)
+    big = torch.zeros(2, 8200, device="cuda")
+    for bad in (lambda: m.layer_norm(big, big[0], big[1]),
+                lambda: m.layer_norm(x, w, b, eps=-1.0),
+                lambda: m.flash_mca_layer_norm(x, None, w, b, None, x, None, None)):  # y is x
+        with pytest.raises(m.FmcaError):
+            bad()

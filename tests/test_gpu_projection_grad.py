@@ -139,3 +139,22 @@ def test_streams_and_two_graphs():
             g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for _, out in graphs for a, b in zip(out, ref))
+
+
+def test_refusals():
+    m = fm()
+    X, Wt, g = rand((8, 64), 1).cuda(), rand((192, 64), 2).cuda(), rand((8, 64), 3).cuda()
+    for bad in (lambda: m.gau_project_backward(X, Wt[:128], g, g, g),
+                lambda: m.gau_project_backward(X, Wt, g, g[:4], g),
+                lambda: m.gau_project_backward(X.float(), Wt, g, g, g),
+                lambda: m.gau_project_backward(X, Wt, g, g.cpu(), g),
+                lambda: m.gau_output_backward(X, Wt[:64].t(), g),
+                lambda: m.gau_output_backward(X, Wt, g)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: m.gau_project_backward(X[:0], Wt, g[:0], g[:0], g[:0]),
+                lambda: m.gau_project_backward(X, Wt[:96], g[:, :32].contiguous(),
+                                               g[:, :32].contiguous(), g[:, :32].contiguous()),
+                lambda: m.gau_output_backward(X, Wt[:32], g[:, :32].contiguous())):
+        with pytest.raises(m.FmcaError):
+            bad()

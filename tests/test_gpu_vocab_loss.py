@@ -260,3 +260,30 @@ def test_gradients_are_differences():
             # both roundings (2^-8 of each entry) and the difference's h^2 term
             bound = 2 * R * float((grad.double() * v).abs().sum()) + 1e-4
             assert abs(slope - float((grad.double() * v).sum())) <= bound
+
+
+def test_refusals():
+    m = fm()
+    X, W, t, dloss = make(8, 20, 64, 1.0, 1)
+    lse = torch.zeros(8, device="cuda")
+    for bad in (lambda: m.vocab_loss(X[0], W, t),                       # not a matrix
+                lambda: m.vocab_loss(X, W[:, :56], t),                  # widths differ
+                lambda: m.vocab_loss(X, W.t().contiguous().t(), t),     # not contiguous
+                lambda: m.vocab_loss(X, W, t.int()),
+                lambda: m.vocab_loss(X, W, t[:7]),
+                lambda: m.vocab_loss(X, W, t.cpu()),
+                lambda: m.vocab_loss(X.half(), W.half(), t),
+                lambda: m.vocab_loss_backward(X, W, t, lse[:4], dloss),
+                lambda: m.vocab_loss_backward(X, W, t, lse, dloss.double()),
+                lambda: m.flash_mca_vocab_loss(X, W, t, lse, lse[:4], lse.byte())):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: m.vocab_loss(X[:, :60].contiguous(), W[:, :60].contiguous(), t),
+                lambda: m.vocab_loss(X[:0], W, t[:0]),
+                lambda: m.vocab_loss(X, W[:0], t),
+                lambda: m.flash_mca_vocab_loss(X, W, t, lse, lse, torch.empty(
+                    1 << 20, dtype=torch.uint8, device="cuda")),        # loss is lse
+                lambda: m.flash_mca_vocab_loss(X, W, t, lse, dloss, torch.empty(
+                    16, dtype=torch.uint8, device="cuda"))):            # too small
+        with pytest.raises(m.FmcaError):
+            bad()
