@@ -157,7 +157,7 @@ fmca_status flash_mca_gau_project_backward(const void *X, const void *Wt, const 
 }
 
 size_t flash_mca_gau_output_backward_workspace_bytes(int M, int e, int d) {
-  return output_sizes(M, e, d) == FMCA_OK ? output_grad_layout(M, d, e).total : 0;
+  return output_sizes(M, e, d) == FMCA_OK ? output_grad_layout().total : 0;
 }
 
 fmca_status flash_mca_gau_output_backward(const void *Y, const void *Wo_t, const void *dOut,
@@ -168,7 +168,7 @@ fmca_status flash_mca_gau_output_backward(const void *Y, const void *Wo_t, const
   if (st != FMCA_OK) return st;
   if (!Y || !Wo_t || !dOut || !dY || !dWo_t) return FMCA_ERR_INVALID_ARG;
   if (!aligned({Y, Wo_t, dOut, dY, dWo_t}, 16)) return FMCA_ERR_ALIGN;
-  st = check_workspace(workspace, workspace_bytes_, output_grad_layout(M, d, e).total);
+  st = check_workspace(workspace, workspace_bytes_, output_grad_layout().total);
   if (st != FMCA_OK) return st;
   const size_t yb = 2 * (size_t)M * e, wb = 2 * (size_t)d * e, ob = 2 * (size_t)M * d;
   if (outputs_clash({{dY, yb}, {dWo_t, wb}, {workspace, workspace_bytes_}},

@@ -291,14 +291,14 @@ int launch_layer_norm_backward(const void *dy, const void *h, const float *weigh
                                void *workspace, cudaStream_t stream);
 
 // Training operators on the tensor cores (tc_train.cuh).  Their products run
-// on at most kTgMaxCtas CTAs; a product whose depth is split keeps one fp32
-// tile of 128 x 256 a part, no more parts than CTAs.
+// on at most kTgMaxCtas CTAs; of tiles cut between CTAs each keeps two fp32
+// parts of 128 x 256 at most.
 constexpr int kTgMaxCtas = 152;
 constexpr size_t kTgSlotBytes = 4 * 128 * 256;
 inline size_t tg_tiles(size_t M, size_t N) {  // 128 x 256 tiles (rows in pairs)
   return 2 * ((M + 255) / 256) * ((N + 255) / 256);
 }
-inline size_t tg_slot_bytes() { return kTgMaxCtas * kTgSlotBytes; }
+inline size_t tg_slot_bytes() { return 2 * kTgMaxCtas * kTgSlotBytes; }
 // Boxes of 64 tokens x 64 columns for all N columns of M tokens.
 inline int64_t tg_boxes(int M, int N) {
   return (int64_t)(((int64_t)M + 255) / 256 * 4) * (((int64_t)N + 255) / 256 * 4);
@@ -322,12 +322,12 @@ inline VocabLossLayout vocab_loss_layout(int M, int V, int d) {
 }
 
 // Its gradients: the same compact rows with their lse and dloss, the boxes of
-// one piece of the vocabulary and the fp32 tiles (dW's parts; dX's parts, or
-// its sums over the pieces).  A piece's boxes fill kVocabPieceBytes at most,
+// one piece of the vocabulary, the fp32 parts of cut tiles and, with several
+// pieces, dX's sums over them.  A piece's boxes fill kVocabPieceBytes at most,
 // or one 256-column tile of all rows where that is more.
 constexpr size_t kVocabPieceBytes = (size_t)256 << 20;
 struct VocabGradLayout {
-  size_t hdr, idx, tgt, lse, g, Xc, boxes, slots0, slots1, total;
+  size_t hdr, idx, tgt, lse, g, Xc, boxes, slots, sums, total;
   int64_t cap_boxes;
 };
 inline VocabGradLayout vocab_grad_layout(int M, int V, int d) {
@@ -344,16 +344,15 @@ inline VocabGradLayout vocab_grad_layout(int M, int V, int d) {
   if (cap < one) cap = one;
   const bool pieces = cap < all;
   L.cap_boxes = pieces ? cap : all;
-  L.slots0 = L.boxes + 8192 * (size_t)L.cap_boxes;
-  L.slots1 = L.slots0 + tg_slot_bytes();
-  const size_t sums = pieces ? tg_tiles(M, d) * kTgSlotBytes : 0;
-  L.total = L.slots1 + (sums > tg_slot_bytes() ? sums : tg_slot_bytes());
+  L.slots = L.boxes + 8192 * (size_t)L.cap_boxes;
+  L.sums = L.slots + tg_slot_bytes();
+  L.total = L.sums + (pieces ? tg_tiles(M, d) * kTgSlotBytes : 0);
   return L;
 }
 
 // Gradients of the GAU projections: the boxes of dpre [M][2e + s], fp32 tiles.
 struct ProjectGradLayout {
-  size_t boxes, slots0, slots1, total;
+  size_t boxes, slots, total;
   int64_t cap_boxes;
 };
 inline ProjectGradLayout project_grad_layout(int M, int N, int d) {
@@ -361,17 +360,14 @@ inline ProjectGradLayout project_grad_layout(int M, int N, int d) {
   ProjectGradLayout L;
   L.boxes = 0;
   L.cap_boxes = tg_boxes(M, N);
-  L.slots0 = 8192 * (size_t)L.cap_boxes;
-  L.slots1 = L.slots0 + tg_slot_bytes();
-  L.total = L.slots1 + tg_slot_bytes();
+  L.slots = 8192 * (size_t)L.cap_boxes;
+  L.total = L.slots + tg_slot_bytes();
   return L;
 }
 struct OutputGradLayout {
-  size_t slots0, slots1, total;
+  size_t slots, total;
 };
-inline OutputGradLayout output_grad_layout(int, int, int) {
-  return OutputGradLayout{0, tg_slot_bytes(), 2 * tg_slot_bytes()};
-}
+inline OutputGradLayout output_grad_layout() { return OutputGradLayout{0, tg_slot_bytes()}; }
 
 int launch_vocab_loss(const void *X, const void *W, const int64_t *target, float *loss, float *lse,
                       int M, int V, int d, void *workspace, cudaStream_t stream);

@@ -73,16 +73,6 @@ __host__ __device__ inline TgPieces tg_pieces(int count, int V, int64_t cap_boxe
   return r;
 }
 
-// Parts of the k axis for a product of `tiles` tiles: its tiles leave workers
-// without one and every part keeps 16 k steps (1024 deep) at least -- shorter
-// parts cost more in their fp32 partial tiles than they gain.
-__host__ __device__ inline int tg_split(int tiles, int ks, int workers) {
-  if (tiles <= 0) return 1;
-  int S = workers / tiles;
-  if (S > ks / 16) S = ks / 16;
-  return S < 1 ? 1 : S;
-}
-
 struct TgParams {
   CUtensorMap A, B;    // NT kinds: X [M][K] box {64, 128}, W [N][K] box {64, 256 / CG}
                        // TG_GRAD: A of problem 0 and (A1) of problem 1, B likewise
@@ -106,35 +96,40 @@ struct TgParams {
   // TG_GRAD
   __nv_bfloat16 *D0;   // dW [V][K]
   __nv_bfloat16 *D1;   // dX [tokens][K]
-  float *slots0, *slots1;  // fp32 partial tiles of 128 x 256
+  float *slots;        // two fp32 tiles of 128 x 256 a worker and CTA: its cut tiles
+  float *sums;         // dX's tiles between pieces, fp32
 };
 
-// One of TG_GRAD's products as the kernel runs it: rows, tiles of 128 CG rows
-// and of 256 columns, k steps, parts of the k axis, steps a part, and the
-// units that makes.
+// One of a launch's products: rows that exist, tiles of 128 CG rows and of 256
+// columns, k steps in a full piece and in this one; TG_GRAD: tiles that are
+// dealt out whole, tiles that are cut, the length of one of those.
 struct TgShape {
-  int M, Mt, Nt, ks, S, ksp, units;
+  int M, Mt, Nt, ks, kend, tiles, dealt, cut, len;
 };
 struct TgPlan {
   int count, col0, width;   // rows; first column and columns of the piece
   TgPieces pc;
   TgShape s[2];
+  int base1, total;         // TG_GRAD: where problem 1's cut tiles begin, and end
+  int row_step;             // rows of a tile
 };
 
-// K sets the depth; K_split (>= K) the parts.
+// A tile's epilogue beyond what the next tile's products hide, in k steps.
+constexpr int kTgEpilogue = 3;
+
 template <int CG>
-__host__ __device__ inline TgShape tg_shape(int M, int N, int K, int K_split, int workers,
-                                            bool split) {
+__host__ __device__ inline TgShape tg_shape(int M_exist, int M, int N, int K, int K_full,
+                                            int workers) {
   TgShape h;
-  h.M = M;
+  h.M = M_exist;
   h.Mt = (M + 128 * CG - 1) / (128 * CG);
   h.Nt = (N + 255) / 256;
-  h.ks = (K + 63) / 64;
-  const int ks = (K_split + 63) / 64;
-  h.S = split ? tg_split(h.Mt * h.Nt, ks, workers) : 1;
-  h.ksp = (ks + h.S - 1) / h.S;
-  h.S = h.ksp > 0 ? (ks + h.ksp - 1) / h.ksp : 1;
-  h.units = h.Mt * h.Nt * h.S;
+  h.ks = (K_full + 63) / 64;
+  h.kend = (K + 63) / 64;
+  h.tiles = h.Mt * h.Nt;
+  h.dealt = h.tiles / workers * workers;
+  h.cut = h.tiles - h.dealt;
+  h.len = h.ks + kTgEpilogue;
   return h;
 }
 
@@ -142,95 +137,150 @@ template <int CG, int KIND>
 __host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int count, int workers) {
   TgPlan p;
   p.count = count;
+  p.row_step = 128 * CG;
   p.pc = tg_pieces(count, P.N, P.cap_boxes);
   p.col0 = 0;
   p.width = P.N;
+  int full = P.N;
   if (KIND == TG_PROB || (KIND == TG_GRAD && P.blocked)) {
-    p.col0 = piece * p.pc.tp * 256;
-    p.width = p.col0 < P.N ? (P.N - p.col0 < p.pc.tp * 256 ? P.N - p.col0 : p.pc.tp * 256) : 0;
+    full = p.pc.tp * 256;
+    p.col0 = piece * full;
+    p.width = p.col0 < P.N ? (P.N - p.col0 < full ? P.N - p.col0 : full) : 0;
   }
-  const int rows = p.width > 0 ? count : 0;  // no piece left: no units
   if (KIND == TG_GRAD) {
-    // dW [width][K], depth tokens; dX [tokens][K], depth width, with the same
-    // parts in every piece (their sums go on from piece to piece), of which a
-    // short last piece leaves some without depth
-    p.s[0] = tg_shape<CG>(p.width, P.K, count, count, workers, true);
-    p.s[1] = tg_shape<CG>(rows, P.K, p.width, P.blocked ? p.pc.tp * 256 : P.N, workers, true);
+    // dW [width][K], depth tokens; dX [tokens][K], depth width.  The tiles and
+    // their cuts are those of a full piece in every piece, so that the sums of
+    // dX go on from piece to piece; the last one leaves some without work.
+    p.s[0] = tg_shape<CG>(p.width, full, P.K, count, count, workers);
+    p.s[1] = tg_shape<CG>(count, count, P.K, p.width, full, workers);
+    // fewer cut tiles than workers, 2^22 steps a tile at most: 31 bits hold it
+    p.base1 = p.s[0].cut * p.s[0].len;
+    p.total = p.base1 + p.s[1].cut * p.s[1].len;
   } else {
-    p.s[0] = tg_shape<CG>(rows, p.width, P.K, P.K, workers, false);
+    p.s[0] = tg_shape<CG>(count, p.width > 0 ? count : 0, p.width, P.K, P.K, workers);
     p.s[1] = p.s[0];
-    p.s[1].units = 0;
+    p.base1 = p.total = 0;
   }
   return p;
 }
 
-// The units of one worker.  The products with their tokens as rows: dealt
-// round-robin, in blocks of 64 row tiles (so that a block's rows and the
-// columns at hand stay in L2), rows first within a block.  TG_GRAD: problem
-// 0's units round-robin, then each worker a run of problem 1's that levels the
-// workers' k steps: the shortest common finish T with room for all of them.
-struct TgWork {
-  int w, W, n0, n1, lo1;
+// TG_GRAD's work: of either problem as many tiles as make whole rounds of all
+// workers are dealt out, neighbours at the same time, so that the operands
+// that they share come from L2.  What is left of both is one line of k steps,
+// problem 0's tiles and then problem 1's, cut into equal parts, one a worker:
+// dealt out whole, the last tiles would leave most workers idle (189 tiles of
+// 128 steps and 96 of 252 on 76 pairs: busy 84 % of the time).  A tile that a
+// cut goes through is summed from its parts by a second kernel; a part keeps 8
+// k steps at least, and tiles of less than 16 are not cut.  Where worker w's
+// part of the line begins:
+struct TgCut {
+  int pi, tile, off;  // the tile among the cut ones; k steps of it before the cut
+  int pos;
 };
-template <int KIND>
-__host__ __device__ inline TgWork tg_work(const TgPlan &p, int w, int W) {
-  TgWork o;
-  o.w = w;
-  o.W = W;
-  o.n0 = (p.s[0].units - w + W - 1) / W;
-  if (o.n0 < 0) o.n0 = 0;
-  o.n1 = 0;
-  o.lo1 = 0;
-  if (KIND == TG_GRAD && p.s[1].units > 0) {
-    constexpr int kEpilogue = 6;  // an epilogue that is not hidden, in k steps
-    const int c0 = p.s[0].ksp + kEpilogue, c1 = p.s[1].ksp + kEpilogue, n1 = p.s[1].units;
-    const int q = p.s[0].units / W, r = p.s[0].units % W;
-    const int64_t la = (int64_t)(q + 1) * c0, lb = (int64_t)q * c0;
-    int64_t lo = lb, hi = lb + (int64_t)(n1 + 1) * c1 + c0;
-    while (lo < hi) {  // least T with room for n1 units of problem 1
-      const int64_t T = (lo + hi) / 2;
-      const int64_t ka = T > la ? (T - la) / c1 : 0, kb = T > lb ? (T - lb) / c1 : 0;
-      if (r * ka + (W - r) * kb >= n1) hi = T;
-      else lo = T + 1;
-    }
-    const int64_t ka = lo > la ? (lo - la) / c1 : 0, kb = lo > lb ? (lo - lb) / c1 : 0;
-    // the workers with the shorter load first
-    const int64_t i = w >= r ? w - r : w;
-    int64_t a = w >= r ? i * kb : (W - r) * kb + i * ka, b = a + (w >= r ? kb : ka);
-    if (a > n1) a = n1;
-    if (b > n1) b = n1;
-    o.lo1 = (int)a;
-    o.n1 = (int)(b - a);
+__host__ __device__ inline TgCut tg_cut(const TgPlan &p, int w, int W) {
+  TgCut c;
+  const int b = w <= 0 ? 0 : w >= W ? p.total : w * (p.total / W) + w * (p.total % W) / W;
+  c.pi = b >= p.base1 ? 1 : 0;
+  const int len = c.pi ? p.s[1].len : p.s[0].len, ks = c.pi ? p.s[1].ks : p.s[0].ks;
+  const int at = c.pi ? b - p.base1 : b;
+  c.tile = at / len;
+  int off = at - c.tile * len;
+  if (ks < 16) {
+    off = 2 * off >= len ? len : 0;
+  } else {
+    off = (off + 4) / 8 * 8;
+    if (off > ks - 8) off = len;
   }
-  return o;
+  c.pos = (c.pi ? p.base1 : 0) + c.tile * len + off;
+  if (off == len) {  // the beginning of the next tile
+    ++c.tile;
+    off = 0;
+    if (c.pi == 0 && c.tile == p.s[0].cut) c.pi = 1, c.tile = 0;
+  }
+  c.off = off;
+  return c;
 }
 
 struct TgUnit {
-  int pi, mt, nt, s, ks0, nks;
+  int pi, mt, nt, ks0, nks;
+  bool whole;  // the tile's whole depth
 };
+// A worker's units in order (every role of the kernel walks them by itself).
+// The products with their tokens as rows: dealt round-robin, in blocks of 64
+// row tiles (so that a block's rows and the columns at hand stay in L2), rows
+// first within a block.
 template <int KIND>
-__host__ __device__ inline bool tg_unit(const TgPlan &p, const TgWork &k, int i, TgUnit &o) {
-  if (i >= k.n0 + k.n1) return false;
-  o.pi = i >= k.n0 ? 1 : 0;
-  const TgShape &h = p.s[o.pi];
-  int u = o.pi ? k.lo1 + (i - k.n0) : k.w + i * k.W;
-  if (KIND == TG_GRAD) {
-    o.nt = u % h.Nt;
-    u /= h.Nt;
-    o.mt = u % h.Mt;
-    o.s = u / h.Mt;
-  } else {
-    constexpr int kBlock = 64;
-    const int per = kBlock * h.Nt, b = u / per, v = u % per;
-    const int rows = min(kBlock, h.Mt - b * kBlock);
-    o.mt = b * kBlock + v % rows;
-    o.nt = v / rows;
-    o.s = 0;
+struct TgWalk {
+  const TgPlan &p;
+  int W, pi, u;  // next tile to be dealt
+  TgCut c;       // TG_GRAD: where the next part begins
+  int end;
+  __host__ __device__ TgWalk(const TgPlan &plan, int w, int workers)
+      : p(plan), W(workers), pi(0), u(w) {
+    if (KIND == TG_GRAD) {
+      c = tg_cut(p, w, W);
+      end = tg_cut(p, w + 1, W).pos;
+    }
   }
-  o.ks0 = o.s * h.ksp;
-  o.nks = max(min(h.ksp, h.ks - o.ks0), 0);
-  return true;
-}
+  __host__ __device__ bool next(TgUnit &o) {
+    if (KIND != TG_GRAD) {
+      const TgShape &h = p.s[0];
+      if (u >= h.tiles) return false;
+      constexpr int kBlock = 64;
+      const int per = kBlock * h.Nt, b = u / per, v = u % per;
+      const int rows = h.Mt - b * kBlock < kBlock ? h.Mt - b * kBlock : kBlock;
+      o.pi = 0;
+      o.mt = b * kBlock + v % rows;
+      o.nt = v / rows;
+      o.ks0 = 0;
+      o.nks = h.ks;
+      o.whole = true;
+      u += W;
+      return true;
+    }
+    if (p.width <= 0) return false;  // a piece behind the last
+    while (true) {
+      int tile;
+      if (pi == 0 && u >= p.s[0].dealt) {
+        u -= p.s[0].dealt;  // the rounds are whole: worker w is first in each again
+        pi = 1;
+      }
+      if (pi == 0 || u < p.s[1].dealt) {
+        o.pi = pi;
+        o.ks0 = 0;
+        o.nks = pi ? p.s[1].kend : p.s[0].kend;
+        o.whole = true;
+        tile = u;
+        u += W;
+      } else if (c.pos < end) {
+        const TgShape &h = c.pi ? p.s[1] : p.s[0];
+        o.pi = c.pi;
+        o.ks0 = c.off;
+        tile = h.dealt + c.tile;
+        int k1 = h.ks;
+        if (end - c.pos < h.len - c.off) k1 = c.off + (end - c.pos);
+        o.whole = c.off == 0 && k1 == h.ks;
+        o.nks = (k1 < h.kend ? k1 : h.kend) - c.off;
+        if (o.nks < 0) o.nks = 0;
+        if (k1 < h.ks) {
+          c.pos = end;
+        } else {
+          c.pos += h.len - c.off;
+          c.off = 0;
+          if (++c.tile == h.cut && c.pi == 0) c.pi = 1, c.tile = 0;
+        }
+      } else {
+        return false;
+      }
+      const int Nt = o.pi ? p.s[1].Nt : p.s[0].Nt;
+      o.mt = tile / Nt;
+      o.nt = tile - o.mt * Nt;
+      // rows of dW that a short last piece does not have
+      if (o.pi == 0 && o.mt * p.row_step >= p.s[0].M) continue;
+      return true;
+    }
+  }
+};
 
 // ------------------------------------------------------------- CTA pairs
 template <int CG>
@@ -427,7 +477,6 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
   const int count = P.hdr != nullptr ? P.hdr->count : P.M;
   const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
   const TgPlan plan = tg_plan<CG, KIND>(P, P.piece, count, workers);
-  const TgWork work = tg_work<KIND>(plan, worker, workers);
 
   if (warp == 0) {
     // =========================== TMA producer
@@ -437,7 +486,8 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       int it = 0;
       bool ok = true;
       TgUnit u;
-      for (int i = 0; ok && tg_unit<KIND>(plan, work, i, u); ++i) {
+      TgWalk<KIND> walk(plan, worker, workers);
+      while (ok && walk.next(u)) {
         const int m0 = u.mt * 128 * CG + (int)rank * 128;
         const int nb0 = u.nt * 256 + (int)rank * 128;
         for (int ks = 0; ks < u.nks; ++ks, ++it) {
@@ -498,8 +548,9 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       int it = 0;
       bool ok = true;
       TgUnit u;
+      TgWalk<KIND> walk(plan, worker, workers);
       int i = 0;
-      for (; ok && tg_unit<KIND>(plan, work, i, u); ++i) {
+      for (; ok && walk.next(u); ++i) {
         const int buf = i & 1, use = i >> 1;
         if (use >= 1 && !tg_wait_pair<CG>(&acc_empty[buf], (use - 1) & 1, kWaitLimitNs)) {
           record_timeout(1011);
@@ -548,8 +599,25 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
     const int quad = warp & 3, half = (warp - 2) / 4;
     const int row = quad * 32 + lane;
     TgUnit u;
-    for (int i = 0; tg_unit<KIND>(plan, work, i, u); ++i) {
+    TgWalk<KIND> walk(plan, worker, workers);
+    for (int i = 0; walk.next(u); ++i) {
       const int buf = i & 1, use = i >> 1;
+      const int m = u.mt * 128 * CG + (int)rank * 128 + row;  // row of the product
+      const int c0 = u.nt * 256 + half * 128;                 // first column in the piece
+      // TG_SILU: the row's incoming gradients, 32 columns ahead of their use
+      // (the first before the accumulator is ready)
+      uint4 up[4] = {};
+      auto fetch = [&](int c) {
+        const int col = c0 + 32 * c;  // 32 columns lie in one of the three arrays
+        if (m < plan.count && col < P.N) {
+          const __nv_bfloat16 *src = col < P.n0   ? P.d0 + (int64_t)m * P.n0 + col
+                                     : col < P.n1 ? P.d1 + (int64_t)m * (P.n1 - P.n0) + col - P.n0
+                                                  : P.d2 + (int64_t)m * (P.N - P.n1) + col - P.n1;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) up[q] = __ldg(reinterpret_cast<const uint4 *>(src) + q);
+        }
+      };
+      if constexpr (KIND == TG_SILU) fetch(0);
       if (!mbar_wait(&acc_full[buf], use & 1, kWaitLimitNs)) {
         if (lane == 0) record_timeout(1020);
         break;
@@ -557,8 +625,6 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       tc_fence_after();
       const uint32_t dcol =
           tbase + (uint32_t)buf * 256u + (uint32_t)(half * 128) + ((uint32_t)(quad * 32) << 16);
-      const int m = u.mt * 128 * CG + (int)rank * 128 + row;  // row of the product
-      const int c0 = u.nt * 256 + half * 128;                 // first column in the piece
       uint32_t r[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(dcol + 32 * c, r[c]);
@@ -636,39 +702,35 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       } else if constexpr (KIND == TG_SILU) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int col = c0 + 32 * c;  // 32 columns lie in one of the three outputs
           float v[32];
-          if (m < plan.count && col < P.N) {
-            const __nv_bfloat16 *src = col < P.n0   ? P.d0 + (int64_t)m * P.n0 + col
-                                       : col < P.n1 ? P.d1 + (int64_t)m * (P.n1 - P.n0) + col - P.n0
-                                                    : P.d2 + (int64_t)m * (P.N - P.n1) + col - P.n1;
+          const bool in = m < plan.count && c0 + 32 * c < P.N;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint4 w4 = __ldg(reinterpret_cast<const uint4 *>(src) + q);
-              const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t ww[4] = {up[q].x, up[q].y, up[q].z, up[q].w};
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float z = __uint_as_float(r[c][8 * q + k]);
-                const float sig = __fdividef(1.f, 1.f + __expf(-z));
-                const float d = (k & 1) ? bf16_hi(ww[k / 2]) : bf16_lo(ww[k / 2]);
-                v[8 * q + k] = d * sig * fmaf(z, 1.f - sig, 1.f);
-              }
+            for (int k = 0; k < 8; ++k) {
+              const float z = __uint_as_float(r[c][8 * q + k]);
+              const float sig = __fdividef(1.f, 1.f + __expf(-z));
+              const float d = (k & 1) ? bf16_hi(ww[k / 2]) : bf16_lo(ww[k / 2]);
+              v[8 * q + k] = in ? d * sig * fmaf(z, 1.f - sig, 1.f) : 0.f;
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
           }
+          if (c < 3) fetch(c + 1);
           tg_store_box(tg_box(P.boxes, plan.pc.n_tok64, m, u.nt, half, c), v);
         }
       } else {
         const TgShape &h = plan.s[u.pi];
         const bool last = !P.blocked || u.pi == 0 || P.piece == plan.pc.np - 1;
-        const bool direct = h.S == 1 && last;
+        const bool direct = u.whole && last;
         // problem 1 over several pieces adds to what the pieces before left
         const bool add = u.pi == 1 && P.blocked && P.piece > 0;
-        float *slot = (u.pi ? P.slots1 : P.slots0) +
-                      ((int64_t)(u.s * h.Mt * CG + u.mt * CG + (int)rank) * h.Nt + u.nt) *
-                          kTgSlotFloats;
+        // a cut tile's part: the worker's tile that was begun by another
+        // (its first) or is ended by another (its last)
+        float *slot = u.whole ? P.sums + ((int64_t)(u.mt * CG + (int)rank) * h.Nt + u.nt) *
+                                             kTgSlotFloats
+                              : P.slots + (int64_t)((2 * worker + (u.ks0 > 0 ? 0 : 1)) * CG +
+                                                    (int)rank) *
+                                              kTgSlotFloats;
         const float alpha = P.hdr != nullptr ? P.hdr->gmax : 1.f;
         const bool in = m < h.M;
         if (u.nks == 0) {  // no depth, nothing was multiplied: the product is 0

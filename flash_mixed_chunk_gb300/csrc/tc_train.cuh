@@ -180,53 +180,63 @@ __global__ void __launch_bounds__(32 * kReduceLanes)
   }
 }
 
-// Products whose k axis was split: the sum of the parts' fp32 tiles, rounded.
-// A thread sums 16 columns of a row (its warp's loads are consecutive).
+// The tiles that a cut went through: the sum of their parts, rounded.  A block
+// row is a cut; the first cut of a tile sums it, 16 columns of a row a thread
+// (its warp's loads are consecutive), the parts in order.
+constexpr int kJoinThreads = 256;
+static_assert(kJoinThreads > kTgMaxCtas, "a thread a cut");
 template <int CG>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinThreads)
     tg_join(const __grid_constant__ TgParams P, int workers, int last) {
+  __shared__ int cut_s[kTgMaxCtas + 1], part_s[kTgMaxCtas], parts_s;
   griddep_wait();
   griddep_launch_dependents();
   const int count = P.hdr != nullptr ? P.hdr->count : P.M;
+  const TgPlan plan = tg_plan<CG, TG_GRAD>(P, P.piece, count, workers);
+  const int w = (int)blockIdx.y + 1;
+  const TgCut c = tg_cut(plan, w, workers);
+  const int Nt = c.pi ? plan.s[1].Nt : plan.s[0].Nt, M = c.pi ? plan.s[1].M : plan.s[0].M;
+  const int begin = c.pos - c.off, end = begin + (c.pi ? plan.s[1].len : plan.s[0].len);
+  const int tile = c.tile + (c.pi ? plan.s[1].dealt : plan.s[0].dealt);
+  const int mt = tile / Nt, nt = tile - mt * Nt;
+  if (c.off == 0) return;
+  // dW: this piece's rows; dX: complete once every piece has been
+  if (c.pi == 0 ? mt * plan.row_step >= M : !last) return;
+  if ((int)threadIdx.x <= workers) cut_s[threadIdx.x] = tg_cut(plan, threadIdx.x, workers).pos;
+  __syncthreads();
+  if (cut_s[w - 1] > begin) return;  // not the tile's first cut
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int x = w - 1; cut_s[x] < end; ++x)
+      if (cut_s[x + 1] > cut_s[x]) part_s[n++] = 2 * x + (x == w - 1 ? 1 : 0);
+    parts_s = n;
+  }
+  __syncthreads();
   const float alpha = P.hdr != nullptr ? P.hdr->gmax : 1.f;
-#pragma unroll 1
-  for (int pi = 0; pi < 1 + last; ++pi) {
-    // problem 0: this piece's dW; problem 1, after the launches of all pieces:
-    // dX, complete since the last piece that has columns
-    const int np = P.blocked ? tg_pieces(count, P.N, P.cap_boxes).np : 1;
-    const TgPlan plan = tg_plan<CG, TG_GRAD>(P, pi ? np - 1 : P.piece, count, workers);
-    const TgShape &h = plan.s[pi];
-    if (h.S <= 1 || h.units == 0) continue;
-    const int Mt = h.Mt * CG;
-    const int64_t tiles = (int64_t)Mt * h.Nt;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < tiles * 128 * 16;
-         i += (int64_t)gridDim.x * blockDim.x) {
-      const int row = (int)(i % 128), q = (int)(i / 128 % 16);
-      const int64_t tile = i / (128 * 16);
-      const int m = (int)(tile / h.Nt) * 128 + row, col = (int)(tile % h.Nt) * 256 + q * 16;
-      if (m >= h.M || col >= P.K) continue;
-      float v[16];
+  const int t = (int)(blockIdx.x * kJoinThreads + threadIdx.x);  // < 128 * 16 * CG
+  const int row = t % 128, q = t / 128 % 16, rank = t / (128 * 16);
+  const int m = (mt * CG + rank) * 128 + row, col = nt * 256 + q * 16;
+  if (m >= M || col >= P.K) return;
+  float v[16];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = 0.f;
-      for (int s = 0; s < h.S; ++s) {
-        const float *slot = (pi ? P.slots1 : P.slots0) + (s * tiles + tile) * kTgSlotFloats;
+  for (int k = 0; k < 16; ++k) v[k] = 0.f;
+#pragma unroll 4
+  for (int n = 0; n < parts_s; ++n) {
+    const float *slot = P.slots + (int64_t)(part_s[n] * CG + rank) * kTgSlotFloats;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 o =
-              *reinterpret_cast<const float4 *>(slot + tg_slot_offset(row, q * 4 + j));
-          v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
-        }
-      }
-      __nv_bfloat16 *out = pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
-                              : P.D0 + (int64_t)(plan.col0 + m) * P.K;
-      uint32_t w[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(alpha * v[2 * k], alpha * v[2 * k + 1]);
-      *reinterpret_cast<uint4 *>(out + col) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (col + 8 < P.K)
-        *reinterpret_cast<uint4 *>(out + col + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int j = 0; j < 4; ++j) {
+      const float4 o = *reinterpret_cast<const float4 *>(slot + tg_slot_offset(row, q * 4 + j));
+      v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
     }
   }
+  __nv_bfloat16 *out = c.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
+                            : P.D0 + (int64_t)(plan.col0 + m) * P.K;
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(alpha * v[2 * k], alpha * v[2 * k + 1]);
+  *reinterpret_cast<uint4 *>(out + col) = make_uint4(o[0], o[1], o[2], o[3]);
+  if (col + 8 < P.K)
+    *reinterpret_cast<uint4 *>(out + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // ---------------------------------------------------------------- host side
@@ -299,7 +309,7 @@ int tg_workers(const TgParams &P) {
   int w = tg_resident<CG, KIND>();
   if (KIND != TG_GRAD && w > 0) {
     const TgPlan p = tg_plan<CG, KIND>(P, P.piece, P.M, w);
-    if (p.s[0].units < w) w = p.s[0].units;
+    if (p.s[0].tiles < w) w = p.s[0].tiles;
   }
   return w;
 }
@@ -309,28 +319,31 @@ int launch_tgemm(const TgParams &P, cudaStream_t stream) {
   return w > 0 ? launch_tgemm_kind<CG, KIND>(P, w, stream) : 1;
 }
 
-// TG_GRAD on piece P.piece of np and, where a product may have been split, the
-// sum of its parts.  With a device count the rows are not known here, and so
-// neither the split of dX nor, with several pieces, how wide this one is;
-// fewer rows never split dW more often at the same width.
+// TG_GRAD on piece P.piece of np, and the sums of the tiles that were cut.
+// Without a device count the cuts are known here, and none may go through a
+// tile.
 template <int CG>
 int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
-  const bool last = P.piece == np - 1;
   const int w = tg_workers<CG, TG_GRAD>(P);
   if (w <= 0 || launch_tgemm_kind<CG, TG_GRAD>(P, w, stream)) return 1;
-  const TgPlan p = tg_plan<CG, TG_GRAD>(P, P.piece, P.M, w);
-  const bool join = p.s[0].S > 1 || np > 1 || (last && (p.s[1].S > 1 || P.hdr != nullptr));
-  if (!join) return 0;
+  bool join = P.hdr != nullptr;
+  if (!join) {
+    const TgPlan p = tg_plan<CG, TG_GRAD>(P, P.piece, P.M, w);
+    for (int x = 1; x < w && !join; ++x) join = tg_cut(p, x, w).off != 0;
+  }
+  if (!join || w < 2) return 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kTgMaxCtas * 2);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(128 * 16 * CG / kJoinThreads, w - 1);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tg_join<CG>, P, w, last ? 1 : 0) == cudaSuccess ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, tg_join<CG>, P, w, P.piece == np - 1 ? 1 : 0) == cudaSuccess
+             ? 0
+             : 1;
 }
 
 // CTA pairs for more rows than one CTA's tile has; up to 128 rows (a short
@@ -427,8 +440,8 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   Q.idx = a.idx;
   Q.D0 = static_cast<__nv_bfloat16 *>(dW);
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
-  Q.slots0 = reinterpret_cast<float *>(ws + L.slots0);
-  Q.slots1 = reinterpret_cast<float *>(ws + L.slots1);
+  Q.sums = reinterpret_cast<float *>(ws + L.sums);
+  Q.slots = reinterpret_cast<float *>(ws + L.slots);
   const int np = tg_pieces(M, V, L.cap_boxes).np;  // with fewer rows no more pieces
   for (int k = 0; k < np; ++k) {
     P.piece = Q.piece = k;
@@ -462,8 +475,7 @@ int gau_project_backward_cg(const void *X, const void *Wt, const void *dU, const
   Q.A1 = Q.A;
   Q.D0 = static_cast<__nv_bfloat16 *>(dWt);
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
-  Q.slots0 = reinterpret_cast<float *>(ws + L.slots0);
-  Q.slots1 = reinterpret_cast<float *>(ws + L.slots1);
+  Q.slots = reinterpret_cast<float *>(ws + L.slots);
   if (int rc = launch_tgemm<CG, TG_SILU>(P, stream)) return rc;
   return launch_grad<CG>(Q, 1, stream);
 }
@@ -472,7 +484,7 @@ template <int CG>
 int gau_output_backward_cg(const void *Y, const void *Wo_t, const void *dOut, void *dY,
                                void *dWo_t, int M, int e, int d, void *workspace,
                                cudaStream_t stream) {
-  const OutputGradLayout L = output_grad_layout(M, d, e);
+  const OutputGradLayout L = output_grad_layout();
   char *ws = static_cast<char *>(workspace);
   TgParams Q = {};
   // A = dOut [tokens][d], read by columns for dWo_t [d][e], by rows for dY
@@ -483,8 +495,7 @@ int gau_output_backward_cg(const void *Y, const void *Wo_t, const void *dOut, vo
   Q.M = M, Q.N = d, Q.K = e;
   Q.D0 = static_cast<__nv_bfloat16 *>(dWo_t);
   Q.D1 = static_cast<__nv_bfloat16 *>(dY);
-  Q.slots0 = reinterpret_cast<float *>(ws + L.slots0);
-  Q.slots1 = reinterpret_cast<float *>(ws + L.slots1);
+  Q.slots = reinterpret_cast<float *>(ws + L.slots);
   return launch_grad<CG>(Q, 1, stream);
 }
 

@@ -452,7 +452,7 @@ def test_projection_gradients_reject_before_queueing():
     a = [P + (k << 28) for k in range(8)]
     big = 1 << 40
     nb = fm.flash_mca_gau_project_backward_workspace_bytes
-    slots = 2 * 152 * 128 * 256 * 4  # fp32 tiles of two products
+    slots = 2 * 152 * 128 * 256 * 4  # two fp32 tiles a CTA
     # dpre in boxes of 64 x 64, tokens and columns rounded up to 256
     assert nb(1000, 768, 1536, 128) == 1024 * 3328 * 2 + slots
     assert nb(1, 64, 64, 64) == 256 * 256 * 2 + slots
