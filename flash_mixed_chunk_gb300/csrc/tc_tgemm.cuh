@@ -101,8 +101,8 @@ struct TgParams {
 };
 
 // One of a launch's products: rows that exist, tiles of 128 CG rows and of 256
-// columns, k steps in a full piece and in this one; TG_GRAD: tiles that are
-// dealt out whole, tiles that are cut, the length of one of those.
+// columns, k steps in a full piece and in this one; TG_GRAD: panels that are
+// dealt out whole, panels that are cut, the length of one of those.
 struct TgShape {
   int M, Mt, Nt, ks, kend, tiles, dealt, cut, len;
 };
@@ -110,8 +110,9 @@ struct TgPlan {
   int count, col0, width;   // rows; first column and columns of the piece
   TgPieces pc;
   TgShape s[2];
-  int base1, total;         // TG_GRAD: where problem 1's cut tiles begin, and end
+  int base1, total;         // TG_GRAD: where problem 1's cut panels begin, and end
   int row_step;             // rows of a tile
+  int side, groups;         // tiles of a panel, workers side by side on them
 };
 
 // A tile's epilogue beyond what the next tile's products hide, in k steps.
@@ -119,7 +120,7 @@ constexpr int kTgEpilogue = 3;
 
 template <int CG>
 __host__ __device__ inline TgShape tg_shape(int M_exist, int M, int N, int K, int K_full,
-                                            int workers) {
+                                            int side, int groups) {
   TgShape h;
   h.M = M_exist;
   h.Mt = (M + 128 * CG - 1) / (128 * CG);
@@ -127,8 +128,8 @@ __host__ __device__ inline TgShape tg_shape(int M_exist, int M, int N, int K, in
   h.ks = (K_full + 63) / 64;
   h.kend = (K + 63) / 64;
   h.tiles = h.Mt * h.Nt;
-  h.dealt = h.tiles / workers * workers;
-  h.cut = h.tiles - h.dealt;
+  h.dealt = h.tiles / side / groups * groups;
+  h.cut = h.tiles / side - h.dealt;
   h.len = h.ks + kTgEpilogue;
   return h;
 }
@@ -147,34 +148,47 @@ __host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int coun
     p.col0 = piece * full;
     p.width = p.col0 < P.N ? (P.N - p.col0 < full ? P.N - p.col0 : full) : 0;
   }
+  p.side = 1;
+  if (KIND == TG_GRAD) {
+    // as many tiles of a row panel side by side as leave few workers over;
+    // only where one of the products is all cut
+    const int Nt = (P.K + 255) / 256, rows = 128 * CG;
+    if (((full + rows - 1) / rows) * Nt < workers || ((count + rows - 1) / rows) * Nt < workers)
+      for (int g = 2; g <= 6; ++g)
+        if (Nt % g == 0 && workers % g <= workers / 32) p.side = g;
+  }
+  p.groups = workers / p.side;
   if (KIND == TG_GRAD) {
     // dW [width][K], depth tokens; dX [tokens][K], depth width.  The tiles and
     // their cuts are those of a full piece in every piece, so that the sums of
     // dX go on from piece to piece; the last one leaves some without work.
-    p.s[0] = tg_shape<CG>(p.width, full, P.K, count, count, workers);
-    p.s[1] = tg_shape<CG>(count, count, P.K, p.width, full, workers);
-    // fewer cut tiles than workers, 2^22 steps a tile at most: 31 bits hold it
+    p.s[0] = tg_shape<CG>(p.width, full, P.K, count, count, p.side, p.groups);
+    p.s[1] = tg_shape<CG>(count, count, P.K, p.width, full, p.side, p.groups);
+    // fewer cut panels than workers, 2^22 steps each at most: 31 bits hold it
     p.base1 = p.s[0].cut * p.s[0].len;
     p.total = p.base1 + p.s[1].cut * p.s[1].len;
   } else {
-    p.s[0] = tg_shape<CG>(count, p.width > 0 ? count : 0, p.width, P.K, P.K, workers);
+    p.s[0] = tg_shape<CG>(count, p.width > 0 ? count : 0, p.width, P.K, P.K, 1, workers);
     p.s[1] = p.s[0];
     p.base1 = p.total = 0;
   }
   return p;
 }
 
-// TG_GRAD's work: of either problem as many tiles as make whole rounds of all
-// workers are dealt out, neighbours at the same time, so that the operands
-// that they share come from L2.  What is left of both is one line of k steps,
-// problem 0's tiles and then problem 1's, cut into equal parts, one a worker:
-// dealt out whole, the last tiles would leave most workers idle (189 tiles of
-// 128 steps and 96 of 252 on 76 pairs: busy 84 % of the time).  A tile that a
-// cut goes through is summed from its parts by a second kernel; a part keeps 8
-// k steps at least, and tiles of less than 16 are not cut.  Where worker w's
-// part of the line begins:
+// TG_GRAD's work: a panel is up to 6 tiles side by side (the same rows of A),
+// one for each worker of a group, which read A together at the same time.  Of
+// either problem as many panels as make whole rounds of all groups are dealt
+// out, neighbours at the same time.  What is left of both is one line of k
+// steps, problem 0's panels and then problem 1's, cut into equal parts, one a
+// group: dealt out whole, the last panels would leave most workers idle (189
+// tiles of 128 steps and 96 of 252 on 76 pairs: busy 84 % of the time).  The
+// tiles of a panel that a cut goes through are summed from their parts by a
+// second kernel; a part keeps 8 k steps at least, and panels of less than 16
+// are not cut.  Without panels (each worker on a tile of its own, cut at its
+// own place) A came from DRAM once for every tile beside another: 171 us
+// instead of 142 at 2048 x 50001 x 512.  Where group w's part of the line begins:
 struct TgCut {
-  int pi, tile, off;  // the tile among the cut ones; k steps of it before the cut
+  int pi, tile, off;  // the panel among the cut ones; k steps of it before the cut
   int pos;
 };
 __host__ __device__ inline TgCut tg_cut(const TgPlan &p, int w, int W) {
@@ -192,7 +206,7 @@ __host__ __device__ inline TgCut tg_cut(const TgPlan &p, int w, int W) {
     if (off > ks - 8) off = len;
   }
   c.pos = (c.pi ? p.base1 : 0) + c.tile * len + off;
-  if (off == len) {  // the beginning of the next tile
+  if (off == len) {  // the beginning of the next panel
     ++c.tile;
     off = 0;
     if (c.pi == 0 && c.tile == p.s[0].cut) c.pi = 1, c.tile = 0;
@@ -212,14 +226,20 @@ struct TgUnit {
 template <int KIND>
 struct TgWalk {
   const TgPlan &p;
-  int W, pi, u;  // next tile to be dealt
+  int W, pi, u;  // workers (TG_GRAD: groups); next tile (panel) to be dealt
+  int lane;      // worker of its group
+  bool out = false;
   TgCut c;       // TG_GRAD: where the next part begins
   int end;
   __host__ __device__ TgWalk(const TgPlan &plan, int w, int workers)
-      : p(plan), W(workers), pi(0), u(w) {
+      : p(plan), W(workers), pi(0), u(w), lane(0) {
     if (KIND == TG_GRAD) {
-      c = tg_cut(p, w, W);
-      end = tg_cut(p, w + 1, W).pos;
+      W = p.groups;
+      u = w / p.side;
+      lane = w - u * p.side;
+      out = u >= W;
+      c = tg_cut(p, u, W);
+      end = tg_cut(p, u + 1, W).pos;
     }
   }
   __host__ __device__ bool next(TgUnit &o) {
@@ -238,11 +258,12 @@ struct TgWalk {
       u += W;
       return true;
     }
-    if (p.width <= 0) return false;  // a piece behind the last
+    // a piece behind the last; a worker that belongs to no group
+    if (p.width <= 0 || out) return false;
     while (true) {
       int tile;
       if (pi == 0 && u >= p.s[0].dealt) {
-        u -= p.s[0].dealt;  // the rounds are whole: worker w is first in each again
+        u -= p.s[0].dealt;  // the rounds are whole: the group's place is the same
         pi = 1;
       }
       if (pi == 0 || u < p.s[1].dealt) {
@@ -272,9 +293,9 @@ struct TgWalk {
       } else {
         return false;
       }
-      const int Nt = o.pi ? p.s[1].Nt : p.s[0].Nt;
-      o.mt = tile / Nt;
-      o.nt = tile - o.mt * Nt;
+      const int across = p.s[0].Nt / p.side;  // panels of a row of tiles
+      o.mt = tile / across;
+      o.nt = (tile - o.mt * across) * p.side + lane;
       // rows of dW that a short last piece does not have
       if (o.pi == 0 && o.mt * p.row_step >= p.s[0].M) continue;
       return true;

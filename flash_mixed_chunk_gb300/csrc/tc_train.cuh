@@ -180,9 +180,10 @@ __global__ void __launch_bounds__(32 * kReduceLanes)
   }
 }
 
-// The tiles that a cut went through: the sum of their parts, rounded.  A block
-// row is a cut; the first cut of a tile sums it, 16 columns of a row a thread
-// (its warp's loads are consecutive), the parts in order.
+// The tiles that a cut went through: the sum of their parts, rounded.  The grid
+// is (a tile's blocks, cuts x tiles of a panel); the first cut of a panel sums
+// its tiles, 16 columns of a row a thread (its warp's loads are consecutive),
+// the parts in order.
 constexpr int kJoinThreads = 256;
 static_assert(kJoinThreads > kTgMaxCtas, "a thread a cut");
 template <int CG>
@@ -193,22 +194,26 @@ __global__ void __launch_bounds__(kJoinThreads)
   griddep_launch_dependents();
   const int count = P.hdr != nullptr ? P.hdr->count : P.M;
   const TgPlan plan = tg_plan<CG, TG_GRAD>(P, P.piece, count, workers);
-  const int w = (int)blockIdx.y + 1;
-  const TgCut c = tg_cut(plan, w, workers);
-  const int Nt = c.pi ? plan.s[1].Nt : plan.s[0].Nt, M = c.pi ? plan.s[1].M : plan.s[0].M;
+  // the grid's rows: the cuts between groups, a row for each tile of a panel
+  const int groups = plan.groups, w = (int)blockIdx.y / plan.side + 1;
+  const int lane = (int)blockIdx.y - (w - 1) * plan.side;
+  if (w >= groups) return;
+  const TgCut c = tg_cut(plan, w, groups);
+  const int M = c.pi ? plan.s[1].M : plan.s[0].M;
   const int begin = c.pos - c.off, end = begin + (c.pi ? plan.s[1].len : plan.s[0].len);
-  const int tile = c.tile + (c.pi ? plan.s[1].dealt : plan.s[0].dealt);
-  const int mt = tile / Nt, nt = tile - mt * Nt;
+  const int panel = c.tile + (c.pi ? plan.s[1].dealt : plan.s[0].dealt);
+  const int across = plan.s[0].Nt / plan.side;
+  const int mt = panel / across, nt = (panel - mt * across) * plan.side + lane;
   if (c.off == 0) return;
   // dW: this piece's rows; dX: complete once every piece has been
   if (c.pi == 0 ? mt * plan.row_step >= M : !last) return;
-  if ((int)threadIdx.x <= workers) cut_s[threadIdx.x] = tg_cut(plan, threadIdx.x, workers).pos;
+  if ((int)threadIdx.x <= groups) cut_s[threadIdx.x] = tg_cut(plan, threadIdx.x, groups).pos;
   __syncthreads();
-  if (cut_s[w - 1] > begin) return;  // not the tile's first cut
+  if (cut_s[w - 1] > begin) return;  // not the panel's first cut
   if (threadIdx.x == 0) {
     int n = 0;
     for (int x = w - 1; cut_s[x] < end; ++x)
-      if (cut_s[x + 1] > cut_s[x]) part_s[n++] = 2 * x + (x == w - 1 ? 1 : 0);
+      if (cut_s[x + 1] > cut_s[x]) part_s[n++] = 2 * (x * plan.side + lane) + (x == w - 1 ? 1 : 0);
     parts_s = n;
   }
   __syncthreads();
@@ -326,16 +331,15 @@ template <int CG>
 int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
   const int w = tg_workers<CG, TG_GRAD>(P);
   if (w <= 0 || launch_tgemm_kind<CG, TG_GRAD>(P, w, stream)) return 1;
+  const TgPlan p = tg_plan<CG, TG_GRAD>(P, P.piece, P.M, w);
   bool join = P.hdr != nullptr;
-  if (!join) {
-    const TgPlan p = tg_plan<CG, TG_GRAD>(P, P.piece, P.M, w);
-    for (int x = 1; x < w && !join; ++x) join = tg_cut(p, x, w).off != 0;
-  }
+  for (int x = 1; x < p.groups && !join; ++x) join = tg_cut(p, x, p.groups).off != 0;
   if (!join || w < 2) return 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
+  // the count can change the panels' width: a block row for every tile beside a cut
   cfg.gridDim = dim3(128 * 16 * CG / kJoinThreads, w - 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
