@@ -36,18 +36,22 @@ namespace {
 
 constexpr int TG_EPI_WARPS = 8;
 constexpr int TG_THREADS = 64 + 32 * TG_EPI_WARPS;
-template <int CG>
+enum : int { TG_LSE = 0, TG_PROB = 1, TG_SILU = 2, TG_GRAD = 3 };
+
+// Shared memory of a CTA: the ring, and for the kinds that write A (TG_PROB,
+// TG_SILU) 8 KB a warp to stage its 32 rows x 128 columns.
+template <int CG, int KIND>
 struct TgCfg {
   static constexpr uint32_t A_BYTES = 128 * 64 * 2;              // 16 KB
   static constexpr uint32_t B_BYTES = (256 / CG) * 64 * 2;       // 32 or 16 KB
   static constexpr uint32_t SLOT = A_BYTES + B_BYTES;
-  static constexpr int RING = CG == 2 ? 7 : 4;
-  static constexpr uint32_t SMEM = RING * SLOT + 1024;
+  static constexpr bool STAGED = KIND == TG_PROB || KIND == TG_SILU;
+  static constexpr int RING = STAGED ? (CG == 2 ? 5 : 3) : (CG == 2 ? 7 : 4);
+  static constexpr uint32_t PIECE = 32 * 64 * 2;                 // 32 rows x 64 columns
+  static constexpr uint32_t STAGE = STAGED ? TG_EPI_WARPS * 2 * PIECE : 0;
+  static constexpr uint32_t SMEM = RING * SLOT + STAGE + 1024;
+  static_assert(SMEM + 1024 <= 232448, "tc_tgemm exceeds 227 KB of shared memory");
 };
-static_assert(TgCfg<1>::SMEM + 1024 <= 232448 && TgCfg<2>::SMEM + 1024 <= 232448,
-              "tc_tgemm exceeds 227 KB of shared memory");
-
-enum : int { TG_LSE = 0, TG_PROB = 1, TG_SILU = 2, TG_GRAD = 3 };
 
 // What the rows' preparation leaves on the device: the number of rows that
 // take part and the largest |dloss| among them (1 if that is not finite).
@@ -55,21 +59,25 @@ struct TgHeader {
   int count;
   float gmax;
 };
+// The count as it is in L2 (a kernel may look before the grid ahead is over).
+__device__ __forceinline__ int tg_count(const TgHeader *h) {
+  return (int)ld_acquire_gpu(reinterpret_cast<const unsigned int *>(&h->count));
+}
 
 // Pieces of the column axis: as many 256-column tiles a piece as the boxes of
 // all tokens fit the buffer, the pieces equal in length.
 struct TgPieces {
   int n_tok64, tiles, tp, np;
 };
-__host__ __device__ inline TgPieces tg_pieces(int count, int V, int64_t cap_boxes) {
+__host__ __device__ inline TgPieces tg_pieces(int count, int V, uint32_t cap_boxes) {
   TgPieces r;
-  r.n_tok64 = (count > 0 ? (count + 255) / 256 : 1) * 4;
-  r.tiles = (V + 255) / 256;
-  int64_t tp = cap_boxes / (4 * (int64_t)r.n_tok64);
+  r.n_tok64 = (count > 0 ? (int)(((uint32_t)count + 255) / 256) : 1) * 4;
+  r.tiles = (int)(((uint32_t)V + 255) / 256);
+  uint32_t tp = cap_boxes / (4 * (uint32_t)r.n_tok64);
   if (tp < 1) tp = 1;
-  if (tp > r.tiles) tp = r.tiles;
-  r.np = (int)((r.tiles + tp - 1) / tp);
-  r.tp = (r.tiles + r.np - 1) / r.np;
+  if (tp > (uint32_t)r.tiles) tp = r.tiles;
+  r.np = (int)(((uint32_t)r.tiles + tp - 1) / tp);
+  r.tp = (int)(((uint32_t)r.tiles + r.np - 1) / (uint32_t)r.np);
   return r;
 }
 
@@ -77,10 +85,12 @@ struct TgParams {
   CUtensorMap A, B;    // NT kinds: X [M][K] box {64, 128}, W [N][K] box {64, 256 / CG}
                        // TG_GRAD: A of problem 0 and (A1) of problem 1, B likewise
   CUtensorMap A1, B1;
+  CUtensorMap S;       // TG_PROB, TG_SILU: the boxes as rows of 64, box {64, 32}
+  CUtensorMap U0, U1, U2;  // TG_SILU: the incoming gradients, box {64, 32}
   int M, N, K;         // NT: rows, columns, depth; TG_GRAD: tokens, columns of A (V), features
   int blocked;         // TG_GRAD: A lies in boxes
   int piece;           // piece of the column axis (TG_PROB, TG_GRAD)
-  int64_t cap_boxes;
+  uint32_t cap_boxes;
   const TgHeader *hdr; // device count of rows (NULL: M)
   const int *idx;      // compact row -> row (NULL: the same)
   // TG_LSE
@@ -89,10 +99,9 @@ struct TgParams {
   const int *tgt;      // [M]
   // TG_PROB
   const float *lse, *g;
-  // TG_SILU: gradients of the activations, columns [0, n0), [n0, n1), [n1, N)
-  const __nv_bfloat16 *d0, *d1, *d2;
+  // TG_SILU: gradients of the activations (U0, U1, U2), columns [0, n0), [n0,
+  // n1), [n1, N), multiples of 64
   int n0, n1;
-  __nv_bfloat16 *boxes;
   // TG_GRAD
   __nv_bfloat16 *D0;   // dW [V][K]
   __nv_bfloat16 *D1;   // dX [tokens][K]
@@ -139,7 +148,7 @@ __host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int coun
   TgPlan p;
   p.count = count;
   p.row_step = 128 * CG;
-  p.pc = tg_pieces(count, P.N, P.cap_boxes);
+  if (KIND != TG_LSE) p.pc = tg_pieces(count, P.N, P.cap_boxes);
   p.col0 = 0;
   p.width = P.N;
   int full = P.N;
@@ -344,6 +353,13 @@ __device__ __forceinline__ void tg_load(void *dst, const CUtensorMap *map, uint3
         : "memory");
   }
 }
+// Brings a 2-D box into L2 (no shared memory, no barrier).
+__device__ __forceinline__ void tg_prefetch_l2(const CUtensorMap *map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
 template <int CG>
 __device__ __forceinline__ void tg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -429,29 +445,22 @@ __device__ __forceinline__ float tg_exp2(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 32 bytes to global memory (32-byte aligned), kept in L2: the next kernel
-// reads it.
+// 32 bytes to global memory (32-byte aligned).
 __device__ __forceinline__ void tg_store32(void *p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 
-// Where chunk c (32 columns) of a warp's half tile of a row lies in the boxes.
-__device__ __forceinline__ __nv_bfloat16 *tg_box(__nv_bfloat16 *boxes, int n_tok64, int m, int nt,
-                                                 int half, int c) {
-  const int64_t vc = nt * 4 + half * 2 + (c >> 1);
-  return boxes + ((vc * n_tok64 + (m >> 6)) * 64 + (m & 63)) * 64 + (c & 1) * 32;
-}
-// 32 values rounded to bf16 into their half row of a box.
-__device__ __forceinline__ void tg_store_box(__nv_bfloat16 *dst, const float (&v)[32]) {
+// 32 values of this thread's row rounded to bf16 into half h of its warp's
+// staged piece (32 rows of 128 bytes, 128-byte swizzle).
+__device__ __forceinline__ void tg_stage(uint8_t *piece, int lane, int h, const float (&v)[32]) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[16 * q + 2 * i], v[16 * q + 2 * i + 1]);
-    tg_store32(dst + 16 * q, w);
-  }
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4 *>(piece + sw128_offset(lane, h * 64 + 16 * q)) =
+        make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                   pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                   pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
 }
 // Element offset of 4-column group j of row `row` in an fp32 partial tile of
 // 128 x 256: rows next to each other, so that a warp's 32 rows are 512
@@ -464,13 +473,14 @@ constexpr int64_t kTgSlotFloats = 128 * 256;
 template <int CG, int KIND>
 __global__ void __launch_bounds__(TG_THREADS, 1)
     tc_tgemm(const __grid_constant__ TgParams P) {
-  using Cfg = TgCfg<CG>;
+  using Cfg = TgCfg<CG, KIND>;
   constexpr int RING = Cfg::RING;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t full[RING], empty[RING];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t up_full[2 * TG_EPI_WARPS];  // TG_SILU: gradients staged
   __shared__ uint32_t tmem_base;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -484,6 +494,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], TG_EPI_WARPS * CG);
     }
+    for (int i = 0; i < 2 * TG_EPI_WARPS; ++i) mbar_init(&up_full[i], 1);
     fence_mbar_init();
   }
   if (warp == 1) tg_tmem_alloc<CG>(&tmem_base, 512);
@@ -491,19 +502,30 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
   tg_sync_all<CG>();
   tc_fence_after();
   const uint32_t tbase = tmem_base;
-  // a programmatic dependent: nothing below runs before the work ahead on the
-  // stream has completed; what follows may be launched from here on
+  const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&P.A);
+    tma_prefetch_desc(&P.B);
+    if (KIND == TG_GRAD) {
+      tma_prefetch_desc(&P.A1);
+      tma_prefetch_desc(&P.B1);
+    }
+  }
+  // A programmatic dependent: it may be here while the work ahead on the
+  // stream is still running, and reads none of that work's results before the
+  // wait.  TG_GRAD may look at the row count: it was launched by a TG_PROB that
+  // had waited for the kernel that counts (or has none).
+  TgPlan plan;
+  if (KIND == TG_GRAD || P.hdr == nullptr)
+    plan = tg_plan<CG, KIND>(P, P.piece, P.hdr != nullptr ? tg_count(P.hdr) : P.M, workers);
   griddep_wait();
   griddep_launch_dependents();
-  const int count = P.hdr != nullptr ? P.hdr->count : P.M;
-  const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
-  const TgPlan plan = tg_plan<CG, KIND>(P, P.piece, count, workers);
+  if (KIND != TG_GRAD && P.hdr != nullptr)
+    plan = tg_plan<CG, KIND>(P, P.piece, tg_count(P.hdr), workers);
 
   if (warp == 0) {
     // =========================== TMA producer
     if (lane == 0) {
-      tma_prefetch_desc(&P.A);
-      tma_prefetch_desc(&P.B);
       int it = 0;
       bool ok = true;
       TgUnit u;
@@ -619,26 +641,80 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
     // columns 128 half .. + 128.
     const int quad = warp & 3, half = (warp - 2) / 4;
     const int row = quad * 32 + lane;
-    TgUnit u;
+    uint8_t *stage = smem + RING * Cfg::SLOT + (warp - 2) * 2 * Cfg::PIECE;
+    TgUnit u, ahead;
     TgWalk<KIND> walk(plan, worker, workers);
-    for (int i = 0; walk.next(u); ++i) {
+    bool more = walk.next(ahead);
+    // TG_SILU: the incoming gradients of this warp's rows and 64 columns (piece
+    // q) of a unit, into the piece that it then works on in place
+    uint64_t *up = up_full + 2 * (warp - 2);
+    auto fetch = [&](const TgUnit &f, int q, bool l2_only) {
+      const int row0 = f.mt * 128 * CG + (int)rank * 128 + quad * 32;
+      const int col = f.nt * 256 + half * 128 + 64 * q;
+      // columns past the last array arrive as zeros
+      const CUtensorMap *map = col < P.n0 ? &P.U0 : col < P.n1 ? &P.U1 : &P.U2;
+      const int x = col < P.n0 ? col : col < P.n1 ? col - P.n0 : col - P.n1;
+      if (l2_only) {
+        tg_prefetch_l2(map, x, row0);
+      } else {
+        mbar_arrive_expect_tx(&up[q], Cfg::PIECE);
+        tma_load_2d(stage + q * Cfg::PIECE, map, &up[q], x, row0);
+      }
+    };
+    int fetched[2] = {0, 0}, used[2] = {0, 0};
+    if constexpr (KIND == TG_SILU) {
+      if (more) {
+        if (lane == 0) fetch(ahead, 0, false);
+        ++fetched[0];
+      }
+    }
+    // a finished piece (32 tokens x 64 columns) to its place in the boxes
+    auto store_piece = [&](const TgUnit &f, int q, uint8_t *piece) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int row0 = f.mt * 128 * CG + (int)rank * 128 + quad * 32;
+        const int block = f.nt * 4 + half * 2 + q;
+        tma_store_2d(&P.S, piece, 0, block * plan.pc.n_tok64 * 64 + row0);
+        bulk_commit_group();
+      }
+      __syncwarp();
+    };
+    const float gmax = KIND == TG_PROB ? P.hdr->gmax : 0.f;
+    for (int i = 0; more; ++i) {
+      u = ahead;
+      more = walk.next(ahead);
       const int buf = i & 1, use = i >> 1;
       const int m = u.mt * 128 * CG + (int)rank * 128 + row;  // row of the product
       const int c0 = u.nt * 256 + half * 128;                 // first column in the piece
-      // TG_SILU: the row's incoming gradients, 32 columns ahead of their use
-      // (the first before the accumulator is ready)
-      uint4 up[4] = {};
-      auto fetch = [&](int c) {
-        const int col = c0 + 32 * c;  // 32 columns lie in one of the three arrays
-        if (m < plan.count && col < P.N) {
-          const __nv_bfloat16 *src = col < P.n0   ? P.d0 + (int64_t)m * P.n0 + col
-                                     : col < P.n1 ? P.d1 + (int64_t)m * (P.n1 - P.n0) + col - P.n0
-                                                  : P.d2 + (int64_t)m * (P.N - P.n1) + col - P.n1;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) up[q] = __ldg(reinterpret_cast<const uint4 *>(src) + q);
+      // TG_SILU: piece 0 was fetched as soon as the unit before had left it;
+      // piece 1, stored last, follows now.  The next unit's gradients come to
+      // L2 meanwhile: their pieces are free too late for a trip to DRAM.
+      if constexpr (KIND == TG_SILU) {
+        if (lane == 0) {
+          bulk_wait_group_read<0>();
+          fetch(u, 1, false);
+          if (more) {
+            fetch(ahead, 0, true);
+            fetch(ahead, 1, true);
+          }
         }
-      };
-      if constexpr (KIND == TG_SILU) fetch(0);
+        ++fetched[1];
+        __syncwarp();
+      }
+      // TG_PROB: the row's constants, before the accumulator is ready
+      const bool in_rows = m < plan.count;
+      float row_lse = 0.f, row_g = 0.f;
+      int row_at = -1;
+      if constexpr (KIND == TG_LSE || KIND == TG_PROB) {
+        if (in_rows) row_at = P.tgt[m] - plan.col0 - c0;
+      }
+      if constexpr (KIND == TG_PROB) {
+        if (in_rows) {
+          row_lse = P.lse[m] * kLog2e;
+          row_g = P.g[m];
+        }
+      }
       if (!mbar_wait(&acc_full[buf], use & 1, kWaitLimitNs)) {
         if (lane == 0) record_timeout(1020);
         break;
@@ -678,11 +754,10 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             sm[c] += tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -ref));
-        const bool in = m < plan.count;
-        if (in)
+        if (in_rows)
           P.part[(int64_t)(u.nt * 2 + half) * P.M + m] =
               make_float2(top, (sm[0] + sm[1]) + (sm[2] + sm[3]));
-        const int at = in ? P.tgt[m] - c0 : -1;
+        const int at = row_at;
         if (__any_sync(0xffffffffu, at >= 0 && at < 128)) {
           float z = 0.f;
 #pragma unroll
@@ -693,51 +768,74 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
           if (at >= 0 && at < 128) P.ztgt[m] = z;
         }
       } else if constexpr (KIND == TG_PROB) {
-        const bool in = m < plan.count;
-        const float lse = in ? P.lse[m] * kLog2e : 0.f;
-        const float gmax = P.hdr->gmax;
-        float g = in ? P.g[m] : 0.f;
+        float g = row_g;
         if (gmax > 0.f) g /= gmax;
-        const int at = in ? P.tgt[m] - plan.col0 - c0 : -1;
-        const bool any = __any_sync(0xffffffffu, at >= 0 && at < 128);
+        const bool any = __any_sync(0xffffffffu, row_at >= 0 && row_at < 128);
         const int left = plan.width - c0;  // columns of the piece from here on
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            v[j] = tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -lse)) * g;
+            v[j] = tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -row_lse)) * g;
           if (any) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (at == 32 * c + j)  // (p - 1) g, the difference formed first
-                v[j] = (tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -lse)) - 1.f) * g;
+              if (row_at == 32 * c + j)  // (p - 1) g, the difference formed first
+                v[j] = (tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -row_lse)) - 1.f) * g;
           }
-          if (!in || left < 128) {
+          if (!in_rows || left < 128) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!in || 32 * c + j >= left) v[j] = 0.f;
+              if (!in_rows || 32 * c + j >= left) v[j] = 0.f;
           }
-          tg_store_box(tg_box(P.boxes, plan.pc.n_tok64, m, u.nt, half, c), v);
+          uint8_t *piece = stage + (c >> 1) * Cfg::PIECE;
+          if ((c & 1) == 0) {  // the store from this piece a unit ago has read it
+            if (lane == 0) bulk_wait_group_read<1>();
+            __syncwarp();
+          }
+          tg_stage(piece, lane, c & 1, v);
+          if (c & 1) store_piece(u, c >> 1, piece);
         }
       } else if constexpr (KIND == TG_SILU) {
+        bool ok = true;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          if ((c & 1) == 0) {
+            ok = mbar_wait(&up[c >> 1], i & 1, kWaitLimitNs);
+            if (!ok) break;
+            ++used[c >> 1];
+          }
+          uint8_t *piece = stage + (c >> 1) * Cfg::PIECE;
           float v[32];
-          const bool in = m < plan.count && c0 + 32 * c < P.N;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t ww[4] = {up[q].x, up[q].y, up[q].z, up[q].w};
+            const uint4 g4 =
+                *reinterpret_cast<const uint4 *>(piece + sw128_offset(lane, (c & 1) * 64 + 16 * q));
+            const uint32_t ww[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float z = __uint_as_float(r[c][8 * q + k]);
               const float sig = __fdividef(1.f, 1.f + __expf(-z));
               const float d = (k & 1) ? bf16_hi(ww[k / 2]) : bf16_lo(ww[k / 2]);
-              v[8 * q + k] = in ? d * sig * fmaf(z, 1.f - sig, 1.f) : 0.f;
+              v[8 * q + k] = d * sig * fmaf(z, 1.f - sig, 1.f);
             }
           }
-          if (c < 3) fetch(c + 1);
-          tg_store_box(tg_box(P.boxes, plan.pc.n_tok64, m, u.nt, half, c), v);
+          if (c == 2 && more) {  // the store of piece 0 has read it
+            if (lane == 0) {
+              bulk_wait_group_read<0>();
+              fetch(ahead, 0, false);
+            }
+            ++fetched[0];
+          }
+          // rows past the last and columns past the last array: z and the
+          // gradient both came in as zeros, so these are zeros
+          tg_stage(piece, lane, c & 1, v);
+          if (c & 1) store_piece(u, c >> 1, piece);
+        }
+        if (!ok) {
+          if (lane == 0) record_timeout(1021);
+          break;
         }
       } else {
         const TgShape &h = plan.s[u.pi];
@@ -805,6 +903,17 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
           }
         }
       }
+    }
+    // a wait that ran out may have left gradients on their way
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (fetched[q] > used[q] && !mbar_wait(&up[q], (fetched[q] - 1) & 1, kWaitLimitNs) &&
+          lane == 0)
+        record_timeout(1022);
+    // staged pieces have been read (and, before the kernel ends, written)
+    if constexpr (Cfg::STAGED) {
+      if (lane == 0) bulk_wait_group<0>();
+      __syncwarp();
     }
   }
   // the single-lane roles rejoin their warps before the block-wide barrier,

@@ -190,26 +190,31 @@ template <int CG>
 __global__ void __launch_bounds__(kJoinThreads)
     tg_join(const __grid_constant__ TgParams P, int workers, int last) {
   __shared__ int cut_s[kTgMaxCtas + 1], part_s[kTgMaxCtas], parts_s;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int count = P.hdr != nullptr ? P.hdr->count : P.M;
+  // launched by a TG_GRAD that had waited for what wrote the header: the plan
+  // is made while that kernel still runs
+  const int count = P.hdr != nullptr ? tg_count(P.hdr) : P.M;
   const TgPlan plan = tg_plan<CG, TG_GRAD>(P, P.piece, count, workers);
   // the grid's rows: the cuts between groups, a row for each tile of a panel
   const int groups = plan.groups, w = (int)blockIdx.y / plan.side + 1;
   const int lane = (int)blockIdx.y - (w - 1) * plan.side;
-  if (w >= groups) return;
   const TgCut c = tg_cut(plan, w, groups);
   const int M = c.pi ? plan.s[1].M : plan.s[0].M;
   const int begin = c.pos - c.off, end = begin + (c.pi ? plan.s[1].len : plan.s[0].len);
   const int panel = c.tile + (c.pi ? plan.s[1].dealt : plan.s[0].dealt);
   const int across = plan.s[0].Nt / plan.side;
   const int mt = panel / across, nt = (panel - mt * across) * plan.side + lane;
-  if (c.off == 0) return;
-  // dW: this piece's rows; dX: complete once every piece has been
-  if (c.pi == 0 ? mt * plan.row_step >= M : !last) return;
+  // a panel's first cut; dW: this piece's rows; dX: complete once every piece
+  // has been
+  const bool mine = w < groups && c.off != 0 && tg_cut(plan, w - 1, groups).pos <= begin &&
+                    (c.pi == 0 ? mt * plan.row_step < M : last != 0);
+  if (!mine) {
+    // the grid must not be over before the one ahead of it: what follows on
+    // the stream waits for this one alone
+    if (blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();
+    return;
+  }
   if ((int)threadIdx.x <= groups) cut_s[threadIdx.x] = tg_cut(plan, threadIdx.x, groups).pos;
   __syncthreads();
-  if (cut_s[w - 1] > begin) return;  // not the panel's first cut
   if (threadIdx.x == 0) {
     int n = 0;
     for (int x = w - 1; cut_s[x] < end; ++x)
@@ -217,6 +222,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     parts_s = n;
   }
   __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
   const float alpha = P.hdr != nullptr ? P.hdr->gmax : 1.f;
   const int t = (int)(blockIdx.x * kJoinThreads + threadIdx.x);  // < 128 * 16 * CG
   const int row = t % 128, q = t / 128 % 16, rank = t / (128 * 16);
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   float v[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) v[k] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int n = 0; n < parts_s; ++n) {
     const float *slot = P.slots + (int64_t)(part_s[n] * CG + rank) * kTgSlotFloats;
 #pragma unroll
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // ---------------------------------------------------------------- host side
 // Launch configuration of one tc_tgemm (its attributes live in the object).
-template <int CG>
+template <int CG, int KIND>
 struct TgLaunch {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg;
@@ -260,7 +267,7 @@ struct TgLaunch {
     cfg = cudaLaunchConfig_t{};
     cfg.gridDim = dim3(workers * CG);
     cfg.blockDim = dim3(TG_THREADS);
-    cfg.dynamicSmemBytes = TgCfg<CG>::SMEM;
+    cfg.dynamicSmemBytes = TgCfg<CG, KIND>::SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
@@ -280,11 +287,11 @@ int tg_resident() {
         int d = 0, n = 0;
         if (cudaGetDevice(&d) != cudaSuccess ||
             cudaFuncSetAttribute(tc_tgemm<CG, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)TgCfg<CG>::SMEM) != cudaSuccess)
+                                 (int)TgCfg<CG, KIND>::SMEM) != cudaSuccess)
           return false;
         n = num_sms() / CG;
         if (CG == 2) {
-          TgLaunch<CG> l(n, nullptr);
+          TgLaunch<CG, KIND> l(n, nullptr);
           l.cfg.attrs = &l.attr[1];
           l.cfg.numAttrs = 1;
           int fit = 0;
@@ -303,7 +310,7 @@ int tg_resident() {
 
 template <int CG, int KIND>
 int launch_tgemm_kind(const TgParams &P, int workers, cudaStream_t stream) {
-  TgLaunch<CG> l(workers, stream);
+  TgLaunch<CG, KIND> l(workers, stream);
   return cudaLaunchKernelEx(&l.cfg, tc_tgemm<CG, KIND>, P) == cudaSuccess ? 0 : 1;
 }
 
@@ -434,10 +441,11 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   P.hdr = a.hdr;
   P.tgt = a.tgt;
   P.lse = a.lse_c, P.g = a.g_c;
-  P.boxes = reinterpret_cast<__nv_bfloat16 *>(ws + L.boxes);
+  const uint64_t box_rows = (uint64_t)L.cap_boxes * 64;
+  if (!make_map_bf16(&P.S, ws + L.boxes, 64, box_rows, 64, 32)) return 2;
   Q = P;
   Q.blocked = 1;
-  if (!make_map_bf16(&Q.A, P.boxes, 64, (uint64_t)L.cap_boxes * 64, 64, 64) ||
+  if (!make_map_bf16(&Q.A, ws + L.boxes, 64, box_rows, 64, 64) ||
       !make_map_bf16(&Q.B, a.Xc, d, M, 64, 64) || !make_map_bf16(&Q.B1, W, d, V, 64, 64))
     return 2;
   Q.A1 = Q.A;
@@ -466,14 +474,15 @@ int gau_project_backward_cg(const void *X, const void *Wt, const void *dU, const
   if (!nt_maps<CG>(P, X, Wt, M, N, d)) return 2;
   P.M = M, P.N = N, P.K = d;
   P.cap_boxes = L.cap_boxes;
-  P.d0 = static_cast<const __nv_bfloat16 *>(dU);
-  P.d1 = static_cast<const __nv_bfloat16 *>(dV);
-  P.d2 = static_cast<const __nv_bfloat16 *>(dZ);
   P.n0 = e, P.n1 = 2 * e;
-  P.boxes = reinterpret_cast<__nv_bfloat16 *>(ws + L.boxes);
+  const uint64_t box_rows = (uint64_t)L.cap_boxes * 64;
+  if (!make_map_bf16(&P.S, ws + L.boxes, 64, box_rows, 64, 32) ||
+      !make_map_bf16(&P.U0, dU, e, M, 64, 32) || !make_map_bf16(&P.U1, dV, e, M, 64, 32) ||
+      !make_map_bf16(&P.U2, dZ, s, M, 64, 32))
+    return 2;
   Q = P;
   Q.blocked = 1;
-  if (!make_map_bf16(&Q.A, P.boxes, 64, (uint64_t)L.cap_boxes * 64, 64, 64) ||
+  if (!make_map_bf16(&Q.A, ws + L.boxes, 64, box_rows, 64, 64) ||
       !make_map_bf16(&Q.B, X, d, M, 64, 64) || !make_map_bf16(&Q.B1, Wt, d, N, 64, 64))
     return 2;
   Q.A1 = Q.A;
