@@ -9,6 +9,7 @@ shared library is missing or fails to load, importing this package raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -145,6 +146,12 @@ class FmcaError(RuntimeError):
         self.status = int(status)
         msg = lib.flash_mca_status_string(self.status).decode()
         super().__init__(f"{what}: {msg}" if what else msg)
+
+
+# The training operators' allocating wrappers (csrc/binding.cpp).
+from . import _binding  # noqa: E402
+
+_binding.set_error(FmcaError)
 
 
 def _check(status: int, what: str) -> None:
@@ -528,13 +535,6 @@ def gau_output(Y, Wo_t, stream=None):
     return Out
 
 
-# The training operators' calls are a few microseconds of device work at their
-# smallest, so their argument checks stay on cheap attribute reads and the
-# stream is fetched as a bare handle.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-if _raw_stream is None:
-    def _raw_stream(index):
-        return torch.cuda.current_stream(index).cuda_stream
 _BF16, _FP32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int64, torch.uint8
 
 
@@ -555,22 +555,29 @@ def _on_or_none(name, t, dtype, shape, dev):
 
 def _placed(name, t, stream, fn, *args):
     """fn(device index, stream handle, *args) with the device of tensor `t`
-    current and `stream` (default: torch's current stream there) torch's
-    current one, so that what fn allocates belongs to the stream that uses it."""
+    current; `stream` defaults to torch's current stream there."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if stream is None:
-        if dev == torch.cuda.current_device():
-            return fn(dev, _raw_stream(dev), *args)
         with torch.cuda.device(dev):
-            return fn(dev, _raw_stream(dev), *args)
+            return fn(dev, torch.cuda.current_stream(dev).cuda_stream, *args)
+    with _on_stream(name, t, stream) as s:
+        return fn(dev, s.cuda_stream, *args)
+
+
+@contextlib.contextmanager
+def _on_stream(name, t, stream):
+    """`stream` (a torch stream or a handle) as torch's current stream on the
+    device of tensor `t`."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=t.device)
-    elif stream.device_index != dev:
-        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, {name} to cuda:{dev}")
+    elif stream.device != t.device:
+        raise ValueError(f"the stream belongs to {stream.device}, {name} to {t.device}")
     with torch.cuda.stream(stream):
-        return fn(dev, stream.cuda_stream, *args)
+        yield stream
 
 
 def _norm_rows(name, x):
@@ -586,12 +593,6 @@ def _matrix(name, t):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     return t.shape
-
-
-def _workspace(nbytes, what, device):
-    if nbytes == 0:
-        raise FmcaError(FMCA_ERR_UNSUPPORTED, what)
-    return torch.empty(nbytes, dtype=_U8, device=device)
 
 
 def flash_mca_layer_norm(x, res, weight, bias, h, y, mean, rstd, eps: float = 1e-5,
@@ -614,30 +615,16 @@ def _layer_norm(dev, ptr, x, res, weight, bias, h, y, mean, rstd, eps):
         None if res is None else _on("h", h, t, shape, dev), _on("y", y, t, shape, dev),
         _on_or_none("mean", mean, _FP32, shape[:-1], dev),
         _on_or_none("rstd", rstd, _FP32, shape[:-1], dev), M, d, eps, dt, ptr)
-    if st:
-        raise FmcaError(st, "flash_mca_layer_norm")
+    _check(st, "flash_mca_layer_norm")
 
 
 def layer_norm(x, weight, bias, eps: float = 1e-5, residual=None, stream=None):
     """Allocating wrapper of flash_mca_layer_norm: returns (y, h, mean, rstd),
     h = x + residual (x itself without a residual)."""
-    return _placed("x", x, stream, _layer_norm_alloc, x, weight, bias, eps, residual)
-
-
-def _layer_norm_alloc(dev, ptr, x, weight, bias, eps, res):
-    M, d = _norm_rows("x", x)
-    dt, shape, t = _dtype_code(x), x.shape, x.dtype
-    px, pr = _on("x", x, t, shape, dev), _on_or_none("residual", res, t, shape, dev)
-    pw, pb = _on("weight", weight, _FP32, (d,), dev), _on("bias", bias, _FP32, (d,), dev)
-    y = torch.empty_like(x)
-    h = x if res is None else torch.empty_like(x)
-    mean = torch.empty(shape[:-1], dtype=_FP32, device=x.device)
-    rstd = torch.empty_like(mean)
-    st = lib.flash_mca_layer_norm(px, pr, pw, pb, h.data_ptr(), y.data_ptr(), mean.data_ptr(),
-                                  rstd.data_ptr(), M, d, eps, dt, ptr)
-    if st:
-        raise FmcaError(st, "flash_mca_layer_norm")
-    return y, h, mean, rstd
+    if stream is None:
+        return _binding.layer_norm(x, weight, bias, eps, residual)
+    with _on_stream("x", x, stream):
+        return _binding.layer_norm(x, weight, bias, eps, residual)
 
 
 def flash_mca_layer_norm_backward_workspace_bytes(M: int, d: int) -> int:
@@ -661,29 +648,20 @@ def _layer_norm_backward(dev, ptr, dy, h, weight, mean, rstd, dh, dx, dw, db, ws
     args = (_on("dy", dy, t, shape, dev), _on("h", h, t, shape, dev),
             _on("weight", weight, _FP32, (d,), dev), _on("mean", mean, _FP32, shape[:-1], dev),
             _on("rstd", rstd, _FP32, shape[:-1], dev), _on_or_none("dh", dh, t, shape, dev))
-    alloc = dx is None
-    if alloc:
-        ws = _workspace(lib.flash_mca_layer_norm_backward_workspace_bytes(M, d),
-                        "flash_mca_layer_norm_backward_workspace_bytes", dy.device)
-        dx = torch.empty_like(dy)
-        dw = torch.empty(d, dtype=_FP32, device=dy.device)
-        db = torch.empty_like(dw)
-        out = (dx.data_ptr(), dw.data_ptr(), db.data_ptr())
-    else:
-        out = (_on("dx", dx, t, shape, dev), _on("dweight", dw, _FP32, (d,), dev),
-               _on("dbias", db, _FP32, (d,), dev))
-        _on("workspace", ws, _U8, ws.shape, dev)
-    st = lib.flash_mca_layer_norm_backward(*args, *out, M, d, dt, ws.data_ptr(), ws.numel(), ptr)
-    if st:
-        raise FmcaError(st, "flash_mca_layer_norm_backward")
-    return dx, dw, db
+    out = (_on("dx", dx, t, shape, dev), _on("dweight", dw, _FP32, (d,), dev),
+           _on("dbias", db, _FP32, (d,), dev))
+    ws_ptr = _on("workspace", ws, _U8, ws.shape, dev)
+    _check(lib.flash_mca_layer_norm_backward(*args, *out, M, d, dt, ws_ptr, ws.numel(), ptr),
+           "flash_mca_layer_norm_backward")
 
 
 def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, stream=None):
     """Allocating wrapper of flash_mca_layer_norm_backward: returns
     (dx, dweight, dbias)."""
-    return _placed("dy", dy, stream, _layer_norm_backward, dy, h, weight, mean, rstd, dh, None,
-                   None, None, None)
+    if stream is None:
+        return _binding.layer_norm_backward(dy, h, weight, mean, rstd, dh)
+    with _on_stream("dy", dy, stream):
+        return _binding.layer_norm_backward(dy, h, weight, mean, rstd, dh)
 
 
 def flash_mca_gau_project_backward_workspace_bytes(M: int, d: int, e: int, s: int) -> int:
@@ -702,24 +680,18 @@ def _gau_project_backward(dev, ptr, X, Wt, dU, dV, dZ, dX, dWt, ws):
     args = (_on("X", X, _BF16, (M, d), dev), _on("Wt", Wt, _BF16, (N, d), dev),
             _on("dU", dU, _BF16, (M, e), dev), _on("dV", dV, _BF16, (M, e), dev),
             _on("dZ", dZ, _BF16, (M, s), dev))
-    if dX is None:
-        ws = _workspace(lib.flash_mca_gau_project_backward_workspace_bytes(M, d, e, s),
-                        "flash_mca_gau_project_backward_workspace_bytes", X.device)
-        dX, dWt = torch.empty_like(X), torch.empty_like(Wt)
-        out = (dX.data_ptr(), dWt.data_ptr())
-    else:
-        out = (_on("dX", dX, _BF16, (M, d), dev), _on("dWt", dWt, _BF16, (N, d), dev))
-        _on("workspace", ws, _U8, ws.shape, dev)
-    st = lib.flash_mca_gau_project_backward(*args, *out, M, d, e, s, ws.data_ptr(), ws.numel(),
-                                            ptr)
-    if st:
-        raise FmcaError(st, "flash_mca_gau_project_backward")
-    return dX, dWt
+    out = (_on("dX", dX, _BF16, (M, d), dev), _on("dWt", dWt, _BF16, (N, d), dev))
+    ws_ptr = _on("workspace", ws, _U8, ws.shape, dev)
+    _check(lib.flash_mca_gau_project_backward(*args, *out, M, d, e, s, ws_ptr, ws.numel(), ptr),
+           "flash_mca_gau_project_backward")
 
 
 def gau_project_backward(X, Wt, dU, dV, dZ, stream=None):
     """Allocating wrapper of flash_mca_gau_project_backward: returns (dX, dWt)."""
-    return _placed("X", X, stream, _gau_project_backward, X, Wt, dU, dV, dZ, None, None, None)
+    if stream is None:
+        return _binding.gau_project_backward(X, Wt, dU, dV, dZ)
+    with _on_stream("X", X, stream):
+        return _binding.gau_project_backward(X, Wt, dU, dV, dZ)
 
 
 def flash_mca_gau_output_backward_workspace_bytes(M: int, e: int, d: int) -> int:
@@ -736,23 +708,18 @@ def _gau_output_backward(dev, ptr, Y, Wo_t, dOut, dY, dWo_t, ws):
     (M, e), (_, d) = _matrix("Y", Y), _matrix("dOut", dOut)
     args = (_on("Y", Y, _BF16, (M, e), dev), _on("Wo_t", Wo_t, _BF16, (d, e), dev),
             _on("dOut", dOut, _BF16, (M, d), dev))
-    if dY is None:
-        ws = _workspace(lib.flash_mca_gau_output_backward_workspace_bytes(M, e, d),
-                        "flash_mca_gau_output_backward_workspace_bytes", Y.device)
-        dY, dWo_t = torch.empty_like(Y), torch.empty_like(Wo_t)
-        out = (dY.data_ptr(), dWo_t.data_ptr())
-    else:
-        out = (_on("dY", dY, _BF16, (M, e), dev), _on("dWo_t", dWo_t, _BF16, (d, e), dev))
-        _on("workspace", ws, _U8, ws.shape, dev)
-    st = lib.flash_mca_gau_output_backward(*args, *out, M, e, d, ws.data_ptr(), ws.numel(), ptr)
-    if st:
-        raise FmcaError(st, "flash_mca_gau_output_backward")
-    return dY, dWo_t
+    out = (_on("dY", dY, _BF16, (M, e), dev), _on("dWo_t", dWo_t, _BF16, (d, e), dev))
+    ws_ptr = _on("workspace", ws, _U8, ws.shape, dev)
+    _check(lib.flash_mca_gau_output_backward(*args, *out, M, e, d, ws_ptr, ws.numel(), ptr),
+           "flash_mca_gau_output_backward")
 
 
 def gau_output_backward(Y, Wo_t, dOut, stream=None):
     """Allocating wrapper of flash_mca_gau_output_backward: returns (dY, dWo_t)."""
-    return _placed("Y", Y, stream, _gau_output_backward, Y, Wo_t, dOut, None, None, None)
+    if stream is None:
+        return _binding.gau_output_backward(Y, Wo_t, dOut)
+    with _on_stream("Y", Y, stream):
+        return _binding.gau_output_backward(Y, Wo_t, dOut)
 
 
 def flash_mca_vocab_loss_workspace_bytes(M: int, V: int, d: int) -> int:
@@ -770,24 +737,18 @@ def _vocab_loss(dev, ptr, X, W, target, loss, lse, ws):
     (M, d), (V, _) = _matrix("X", X), _matrix("W", W)
     args = (_on("X", X, _BF16, (M, d), dev), _on("W", W, _BF16, (V, d), dev),
             _on("target", target, _I64, (M,), dev))
-    if loss is None:
-        ws = _workspace(lib.flash_mca_vocab_loss_workspace_bytes(M, V, d),
-                        "flash_mca_vocab_loss_workspace_bytes", X.device)
-        loss = torch.empty(M, dtype=_FP32, device=X.device)
-        lse = torch.empty_like(loss)
-        out = (loss.data_ptr(), lse.data_ptr())
-    else:
-        out = (_on("loss", loss, _FP32, (M,), dev), _on("lse", lse, _FP32, (M,), dev))
-        _on("workspace", ws, _U8, ws.shape, dev)
-    st = lib.flash_mca_vocab_loss(*args, *out, M, V, d, ws.data_ptr(), ws.numel(), ptr)
-    if st:
-        raise FmcaError(st, "flash_mca_vocab_loss")
-    return loss, lse
+    out = (_on("loss", loss, _FP32, (M,), dev), _on("lse", lse, _FP32, (M,), dev))
+    ws_ptr = _on("workspace", ws, _U8, ws.shape, dev)
+    _check(lib.flash_mca_vocab_loss(*args, *out, M, V, d, ws_ptr, ws.numel(), ptr),
+           "flash_mca_vocab_loss")
 
 
 def vocab_loss(X, W, target, stream=None):
     """Allocating wrapper of flash_mca_vocab_loss: returns (loss, lse)."""
-    return _placed("X", X, stream, _vocab_loss, X, W, target, None, None, None)
+    if stream is None:
+        return _binding.vocab_loss(X, W, target)
+    with _on_stream("X", X, stream):
+        return _binding.vocab_loss(X, W, target)
 
 
 def flash_mca_vocab_loss_backward_workspace_bytes(M: int, V: int, d: int) -> int:
@@ -806,24 +767,18 @@ def _vocab_loss_backward(dev, ptr, X, W, target, lse, dloss, dX, dW, ws):
     args = (_on("X", X, _BF16, (M, d), dev), _on("W", W, _BF16, (V, d), dev),
             _on("target", target, _I64, (M,), dev), _on("lse", lse, _FP32, (M,), dev),
             _on("dloss", dloss, _FP32, (M,), dev))
-    if dX is None:
-        ws = _workspace(lib.flash_mca_vocab_loss_backward_workspace_bytes(M, V, d),
-                        "flash_mca_vocab_loss_backward_workspace_bytes", X.device)
-        dX, dW = torch.empty_like(X), torch.empty_like(W)
-        out = (dX.data_ptr(), dW.data_ptr())
-    else:
-        out = (_on("dX", dX, _BF16, (M, d), dev), _on("dW", dW, _BF16, (V, d), dev))
-        _on("workspace", ws, _U8, ws.shape, dev)
-    st = lib.flash_mca_vocab_loss_backward(*args, *out, M, V, d, ws.data_ptr(), ws.numel(), ptr)
-    if st:
-        raise FmcaError(st, "flash_mca_vocab_loss_backward")
-    return dX, dW
+    out = (_on("dX", dX, _BF16, (M, d), dev), _on("dW", dW, _BF16, (V, d), dev))
+    ws_ptr = _on("workspace", ws, _U8, ws.shape, dev)
+    _check(lib.flash_mca_vocab_loss_backward(*args, *out, M, V, d, ws_ptr, ws.numel(), ptr),
+           "flash_mca_vocab_loss_backward")
 
 
 def vocab_loss_backward(X, W, target, lse, dloss, stream=None):
     """Allocating wrapper of flash_mca_vocab_loss_backward: returns (dX, dW)."""
-    return _placed("X", X, stream, _vocab_loss_backward, X, W, target, lse, dloss, None, None,
-                   None)
+    if stream is None:
+        return _binding.vocab_loss_backward(X, W, target, lse, dloss)
+    with _on_stream("X", X, stream):
+        return _binding.vocab_loss_backward(X, W, target, lse, dloss)
 
 
 def flash_mca_device_status(stream=None) -> tuple[int, int]:

@@ -2,7 +2,8 @@
 
 The translation units compile in parallel (the C-ABI layer, the SIMT kernels,
 the tensor-core kernels and the layer norm among them) and link into one shared library next to this
-file.  The CUDA runtime is linked statically and the driver's tensor-map
+file; the Python module with the training operators' wrappers (host code over
+torch's headers) compiles beside them.  The CUDA runtime is linked statically and the driver's tensor-map
 encoder is looked up at run time, so the library loads on a machine without a
 GPU driver (only calls that touch the device need one).
 
@@ -23,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflash_mca.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 SOURCES = ["api.cpp", "simt.cu", "tc.cu", "noalloc.cu", "decode.cu", "backward.cu",
            "api_train.cpp", "norm.cu"]
@@ -39,24 +41,59 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libflash_mca.so")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _older(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps.append(os.path.join(INCLUDE, "flash_mca.h"))
-    deps.append(os.path.abspath(__file__))
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _stale() -> bool:
+    return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS] +
+                  [os.path.join(INCLUDE, "flash_mca.h"), os.path.abspath(__file__)])
+
+
+def _binding_stale() -> bool:
+    import torch
+    return _older(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "flash_mca.h"),
+                            os.path.abspath(__file__), torch.__file__])
+
+
+def _binding_compile():
+    """Starts the compiler on binding.cpp (host code over torch's C++ headers)."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    paths = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+             sysconfig.get_paths()["include"],
+             os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for p in paths for x in ("-isystem", p)], "-c", os.path.join(CSRC, "binding.cpp"),
+           "-o", os.path.join(BUILD, "binding.o")]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _binding_link() -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-shared", "-o", tmp, os.path.join(BUILD, "binding.o"), "-L", PKG,
+                    "-l:libflash_mca.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python",
+                    "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
+    lib, binding = force or _stale(), force or _binding_stale()
     os.makedirs(BUILD, exist_ok=True)
-    cc = nvcc()
+    cc = nvcc() if lib or binding else ""
     procs = []
     objs = []
-    for src in SOURCES:
+    if binding:
+        procs.append(("binding.cpp", _binding_compile()))
+    for src in SOURCES if lib else []:
         obj = os.path.join(BUILD, src.rsplit(".", 1)[0] + ".o")
         objs.append(obj)
         cmd = [cc, *ARCH, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -71,10 +108,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
-    tmp = LIB + f".tmp{os.getpid()}"
-    link = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    subprocess.run(link, check=True)
-    os.replace(tmp, LIB)
+        raise RuntimeError(f"compilation failed for {failed}")
+    if lib:
+        tmp = LIB + f".tmp{os.getpid()}"
+        link = [cc, *ARCH, "-shared", "-o", tmp, *objs]
+        subprocess.run(link, check=True)
+        os.replace(tmp, LIB)
+    if binding:
+        _binding_link()
     return LIB
 

@@ -482,9 +482,26 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
   __shared__ __align__(8) uint64_t up_full[2 * TG_EPI_WARPS];  // TG_SILU: gradients staged
   __shared__ uint32_t tmem_base;
+  __shared__ TgPlan plan;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = tg_rank<CG>();
+  const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
+  // A programmatic dependent: it may be here while the work ahead on the
+  // stream is still running, and reads none of that work's results before the
+  // grid wait.  TG_GRAD may look at the row count: it was launched by a TG_PROB
+  // that had waited for the kernel that counts (or has none).
+  const bool early = KIND == TG_GRAD || P.hdr == nullptr;
+  if (threadIdx.x == 96) {
+    tma_prefetch_desc(&P.A);
+    tma_prefetch_desc(&P.B);
+    if (KIND == TG_GRAD) {
+      tma_prefetch_desc(&P.A1);
+      tma_prefetch_desc(&P.B1);
+    }
+    if (early)
+      plan = tg_plan<CG, KIND>(P, P.piece, P.hdr != nullptr ? tg_count(P.hdr) : P.M, workers);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < RING; ++i) {
       mbar_init(&full[i], 1);
@@ -502,26 +519,13 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
   tg_sync_all<CG>();
   tc_fence_after();
   const uint32_t tbase = tmem_base;
-  const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
-  if (threadIdx.x == 0) {
-    tma_prefetch_desc(&P.A);
-    tma_prefetch_desc(&P.B);
-    if (KIND == TG_GRAD) {
-      tma_prefetch_desc(&P.A1);
-      tma_prefetch_desc(&P.B1);
-    }
-  }
-  // A programmatic dependent: it may be here while the work ahead on the
-  // stream is still running, and reads none of that work's results before the
-  // wait.  TG_GRAD may look at the row count: it was launched by a TG_PROB that
-  // had waited for the kernel that counts (or has none).
-  TgPlan plan;
-  if (KIND == TG_GRAD || P.hdr == nullptr)
-    plan = tg_plan<CG, KIND>(P, P.piece, P.hdr != nullptr ? tg_count(P.hdr) : P.M, workers);
   griddep_wait();
   griddep_launch_dependents();
-  if (KIND != TG_GRAD && P.hdr != nullptr)
-    plan = tg_plan<CG, KIND>(P, P.piece, tg_count(P.hdr), workers);
+  if (!early) {
+    if (threadIdx.x == 96) plan = tg_plan<CG, KIND>(P, P.piece, tg_count(P.hdr), workers);
+    __syncthreads();
+  }
+  const int count = plan.count, col0 = plan.col0, n_tok64 = plan.pc.n_tok64;
 
   if (warp == 0) {
     // =========================== TMA producer
@@ -548,13 +552,13 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
           const int kk = (u.ks0 + ks) * 64;
           if constexpr (KIND != TG_GRAD) {
             tg_load<CG>(sa, &P.A, bar, kk, m0);
-            tg_load<CG>(sb, &P.B, bar, kk, plan.col0 + nb0);
+            tg_load<CG>(sb, &P.B, bar, kk, col0 + nb0);
           } else {
             const CUtensorMap *mB = u.pi ? &P.B1 : &P.B;
             if (P.blocked) {
               // problem 0: column blocks m0 / 64 and the next, token block
               // kk / 64; problem 1: column block kk / 64, two token blocks
-              const int t64 = plan.pc.n_tok64;
+              const int t64 = n_tok64;
               const int b0 = u.pi ? (kk / 64) * t64 + m0 / 64 : (m0 / 64) * t64 + kk / 64;
               const int b1 = b0 + (u.pi ? 1 : t64);
               tg_load<CG>(sa, &P.A, bar, 0, b0 * 64);
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
               tg_load<CG>(sa + 8192, &P.A, bar, m0 + 64, kk);
             }
             // rows k (problem 1: from the piece's first row of W), columns n
-            const int krow = kk + (u.pi ? plan.col0 : 0);
+            const int krow = kk + (u.pi ? col0 : 0);
 #pragma unroll
             for (int q = 0; q < 4 / CG; ++q)
               tg_load<CG>(sb + q * 8192, mB, bar, nb0 + 64 * q, krow);
@@ -675,7 +679,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       if (lane == 0) {
         const int row0 = f.mt * 128 * CG + (int)rank * 128 + quad * 32;
         const int block = f.nt * 4 + half * 2 + q;
-        tma_store_2d(&P.S, piece, 0, block * plan.pc.n_tok64 * 64 + row0);
+        tma_store_2d(&P.S, piece, 0, block * n_tok64 * 64 + row0);
         bulk_commit_group();
       }
       __syncwarp();
@@ -703,11 +707,11 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
         __syncwarp();
       }
       // TG_PROB: the row's constants, before the accumulator is ready
-      const bool in_rows = m < plan.count;
+      const bool in_rows = m < count;
       float row_lse = 0.f, row_g = 0.f;
       int row_at = -1;
       if constexpr (KIND == TG_LSE || KIND == TG_PROB) {
-        if (in_rows) row_at = P.tgt[m] - plan.col0 - c0;
+        if (in_rows) row_at = P.tgt[m] - col0 - c0;
       }
       if constexpr (KIND == TG_PROB) {
         if (in_rows) {
@@ -722,16 +726,18 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       tc_fence_after();
       const uint32_t dcol =
           tbase + (uint32_t)buf * 256u + (uint32_t)(half * 128) + ((uint32_t)(quad * 32) << 16);
-      uint32_t r[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(dcol + 32 * c, r[c]);
-      tmem_ld_wait();
       // this warp's last read of the accumulator
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tg_arrive_leader<CG>(&acc_empty[buf]);
-
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tg_arrive_leader<CG>(&acc_empty[buf]);
+      };
       if constexpr (KIND == TG_LSE) {
+        uint32_t r[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(dcol + 32 * c, r[c]);
+        tmem_ld_wait();
+        release();
         // columns past the vocabulary count as -infinity
         if (c0 + 128 > P.N) {
 #pragma unroll
@@ -767,140 +773,143 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
               if (at == 32 * c + j) z = __uint_as_float(r[c][j]);
           if (at >= 0 && at < 128) P.ztgt[m] = z;
         }
-      } else if constexpr (KIND == TG_PROB) {
-        float g = row_g;
-        if (gmax > 0.f) g /= gmax;
-        const bool any = __any_sync(0xffffffffu, row_at >= 0 && row_at < 128);
-        const int left = plan.width - c0;  // columns of the piece from here on
+      } else {
+        // 64 columns at a time, in chunks of 32
+        const float g = KIND == TG_PROB && gmax > 0.f ? row_g / gmax : row_g;
+        const bool any = KIND == TG_PROB && __any_sync(0xffffffffu, row_at >= 0 && row_at < 128);
+        const int left = plan.width - c0;  // TG_PROB: columns of the piece from here on
+        // TG_GRAD: problem 1 over several pieces adds to what the pieces before
+        // left; a cut tile's part goes to the place of the worker's tile that
+        // was begun by another (its first) or is ended by another (its last)
+        const TgShape &h = plan.s[KIND == TG_GRAD ? u.pi : 0];
+        const bool last = !P.blocked || u.pi == 0 || P.piece == plan.pc.np - 1;
+        const bool direct = u.whole && last;
+        const bool add = u.pi == 1 && P.blocked && P.piece > 0;
+        const bool in = m < h.M;
+        float *slot = nullptr;
+        __nv_bfloat16 *out = nullptr;
+        float alpha = 1.f;
+        bool wide = false;
+        if constexpr (KIND == TG_GRAD) {
+          slot = u.whole ? P.sums + ((int64_t)(u.mt * CG + (int)rank) * h.Nt + u.nt) * kTgSlotFloats
+                         : P.slots + (int64_t)((2 * worker + (u.ks0 > 0 ? 0 : 1)) * CG + (int)rank) *
+                                         kTgSlotFloats;
+          if (P.hdr != nullptr) alpha = P.hdr->gmax;
+          wide = P.K % 16 == 0 && (reinterpret_cast<uintptr_t>(u.pi ? P.D1 : P.D0) & 31u) == 0;
+          if (direct && in)
+            out = u.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
+                       : P.D0 + (int64_t)(col0 + m) * P.K;
+        }
+        bool ok = true;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            v[j] = tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -row_lse)) * g;
-          if (any) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (row_at == 32 * c + j)  // (p - 1) g, the difference formed first
-                v[j] = (tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -row_lse)) - 1.f) * g;
-          }
-          if (!in_rows || left < 128) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!in_rows || 32 * c + j >= left) v[j] = 0.f;
-          }
-          uint8_t *piece = stage + (c >> 1) * Cfg::PIECE;
-          if ((c & 1) == 0) {  // the store from this piece a unit ago has read it
+        for (int q2 = 0; q2 < 2; ++q2) {
+          uint32_t r[2][32];
+          tmem_ld32(dcol + 64 * q2, r[0]);
+          tmem_ld32(dcol + 64 * q2 + 32, r[1]);
+          uint8_t *piece = stage + q2 * Cfg::PIECE;
+          if constexpr (KIND == TG_PROB) {  // the store from this piece a unit ago has read it
             if (lane == 0) bulk_wait_group_read<1>();
             __syncwarp();
           }
-          tg_stage(piece, lane, c & 1, v);
-          if (c & 1) store_piece(u, c >> 1, piece);
-        }
-      } else if constexpr (KIND == TG_SILU) {
-        bool ok = true;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if ((c & 1) == 0) {
-            ok = mbar_wait(&up[c >> 1], i & 1, kWaitLimitNs);
-            if (!ok) break;
-            ++used[c >> 1];
+          if constexpr (KIND == TG_SILU) {
+            ok = mbar_wait(&up[q2], i & 1, kWaitLimitNs);
           }
-          uint8_t *piece = stage + (c >> 1) * Cfg::PIECE;
-          float v[32];
+          tmem_ld_wait();
+          if (!ok) break;
+          if constexpr (KIND == TG_SILU) ++used[q2];
+          if (q2 == 1) release();
+          if (KIND == TG_GRAD && u.nks == 0) {  // nothing was multiplied: the product is 0
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 g4 =
-                *reinterpret_cast<const uint4 *>(piece + sw128_offset(lane, (c & 1) * 64 + 16 * q));
-            const uint32_t ww[4] = {g4.x, g4.y, g4.z, g4.w};
+            for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float z = __uint_as_float(r[c][8 * q + k]);
-              const float sig = __fdividef(1.f, 1.f + __expf(-z));
-              const float d = (k & 1) ? bf16_hi(ww[k / 2]) : bf16_lo(ww[k / 2]);
-              v[8 * q + k] = d * sig * fmaf(z, 1.f - sig, 1.f);
+              for (int j = 0; j < 32; ++j) r[c2][j] = 0u;
+          }
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            const int c = 2 * q2 + c2;
+            float v[32];
+            if constexpr (KIND == TG_PROB) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                v[j] = tg_exp2(fmaf(__uint_as_float(r[c2][j]), kLog2e, -row_lse)) * g;
+              if (any) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (row_at == 32 * c + j)  // (p - 1) g, the difference formed first
+                    v[j] = (tg_exp2(fmaf(__uint_as_float(r[c2][j]), kLog2e, -row_lse)) - 1.f) * g;
+              }
+              if (!in_rows || left < 128) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!in_rows || 32 * c + j >= left) v[j] = 0.f;
+              }
+            } else if constexpr (KIND == TG_SILU) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint4 g4 =
+                    *reinterpret_cast<const uint4 *>(piece + sw128_offset(lane, c2 * 64 + 16 * q));
+                const uint32_t ww[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float z = __uint_as_float(r[c2][8 * q + k]);
+                  const float sig = __fdividef(1.f, 1.f + __expf(-z));
+                  const float d = (k & 1) ? bf16_hi(ww[k / 2]) : bf16_lo(ww[k / 2]);
+                  v[8 * q + k] = d * sig * fmaf(z, 1.f - sig, 1.f);
+                }
+              }
+              if (c == 2 && more) {  // the store of piece 0 has read it
+                if (lane == 0) {
+                  bulk_wait_group_read<0>();
+                  fetch(ahead, 0, false);
+                }
+                ++fetched[0];
+              }
+              // rows past the last and columns past the last array: z and the
+              // gradient both came in as zeros, so these are zeros
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[c2][j]);
+              if (add) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float4 o = *reinterpret_cast<const float4 *>(
+                      slot + tg_slot_offset(row, half * 32 + c * 8 + j));
+                  v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
+                }
+              }
+              if (!direct) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  *reinterpret_cast<float4 *>(slot + tg_slot_offset(row, half * 32 + c * 8 + j)) =
+                      make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              } else if (in) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  uint32_t w[8];
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    w[k] = pack_bf16x2(alpha * v[16 * q + 2 * k], alpha * v[16 * q + 2 * k + 1]);
+                  const int cq = c0 + 32 * c + 16 * q;
+                  if (wide) {
+                    if (cq < P.K) tg_store32(out + cq, w);
+                  } else {  // rows start on 16-byte boundaries only
+                    if (cq < P.K)
+                      *reinterpret_cast<uint4 *>(out + cq) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (cq + 8 < P.K)
+                      *reinterpret_cast<uint4 *>(out + cq + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                  }
+                }
+              }
+            }
+            if constexpr (Cfg::STAGED) {
+              tg_stage(piece, lane, c2, v);
+              if (c2 == 1) store_piece(u, q2, piece);
             }
           }
-          if (c == 2 && more) {  // the store of piece 0 has read it
-            if (lane == 0) {
-              bulk_wait_group_read<0>();
-              fetch(ahead, 0, false);
-            }
-            ++fetched[0];
-          }
-          // rows past the last and columns past the last array: z and the
-          // gradient both came in as zeros, so these are zeros
-          tg_stage(piece, lane, c & 1, v);
-          if (c & 1) store_piece(u, c >> 1, piece);
         }
         if (!ok) {
           if (lane == 0) record_timeout(1021);
           break;
-        }
-      } else {
-        const TgShape &h = plan.s[u.pi];
-        const bool last = !P.blocked || u.pi == 0 || P.piece == plan.pc.np - 1;
-        const bool direct = u.whole && last;
-        // problem 1 over several pieces adds to what the pieces before left
-        const bool add = u.pi == 1 && P.blocked && P.piece > 0;
-        // a cut tile's part: the worker's tile that was begun by another
-        // (its first) or is ended by another (its last)
-        float *slot = u.whole ? P.sums + ((int64_t)(u.mt * CG + (int)rank) * h.Nt + u.nt) *
-                                             kTgSlotFloats
-                              : P.slots + (int64_t)((2 * worker + (u.ks0 > 0 ? 0 : 1)) * CG +
-                                                    (int)rank) *
-                                              kTgSlotFloats;
-        const float alpha = P.hdr != nullptr ? P.hdr->gmax : 1.f;
-        const bool in = m < h.M;
-        if (u.nks == 0) {  // no depth, nothing was multiplied: the product is 0
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[c][j] = 0u;
-        }
-        __nv_bfloat16 *out = nullptr;
-        if (direct && in)
-          out = u.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
-                     : P.D0 + (int64_t)(plan.col0 + m) * P.K;
-        const bool wide =
-            P.K % 16 == 0 && (reinterpret_cast<uintptr_t>(u.pi ? P.D1 : P.D0) & 31u) == 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[c][j]);
-          if (add) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 o = *reinterpret_cast<const float4 *>(
-                  slot + tg_slot_offset(row, half * 32 + c * 8 + j));
-              v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
-            }
-          }
-          if (!direct) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<float4 *>(slot + tg_slot_offset(row, half * 32 + c * 8 + j)) =
-                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          } else if (in) {
-            const int col = c0 + 32 * c;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                w[k] = pack_bf16x2(alpha * v[16 * q + 2 * k], alpha * v[16 * q + 2 * k + 1]);
-              const int cq = col + 16 * q;
-              if (wide) {
-                if (cq < P.K) tg_store32(out + cq, w);
-              } else {  // rows start on 16-byte boundaries only
-                if (cq < P.K)
-                  *reinterpret_cast<uint4 *>(out + cq) = make_uint4(w[0], w[1], w[2], w[3]);
-                if (cq + 8 < P.K)
-                  *reinterpret_cast<uint4 *>(out + cq + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-              }
-            }
-          }
         }
       }
     }
