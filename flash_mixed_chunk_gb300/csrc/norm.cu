@@ -17,7 +17,9 @@
 //
 // A row belongs to one warp (d <= 1024) or to one block of 256 threads (d <=
 // 8192): 8, 16, 24 or 32 elements a thread, in 16-byte vectors where d allows
-// it, else 4-byte ones, else single elements.
+// it, else 4-byte ones, else single elements.  Backward rows that would fill a
+// warp's registers and shared memory with few threads (fp32 beyond 512
+// elements, narrow vectors beyond 256) belong to half a block instead.
 //
 // The backward pass keeps dw and db of the rows it has seen in registers, one
 // partial row a block in the workspace, and a second kernel adds the partial
@@ -225,6 +227,36 @@ constexpr size_t norm_ring_bytes() {
   return sizeof(T) * VEC >= 4 ? (size_t)kNormStages * 3 * N * kNormThreads * sizeof(T) * VEC : 0;
 }
 
+// The sums of a.x and a.y over a row's group, as group_sum; a quarter or half
+// block meets at a barrier of its own.
+template <int GROUP>
+__device__ __forceinline__ float2 group_sum2(float2 a, float2 (*red)[kNormThreads / 32],
+                                             int &turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+    a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+  }
+  if constexpr (GROUP > 32) {
+    float2 *r = red[turn];
+    turn ^= 1;
+    if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = a;
+    const int grp = threadIdx.x / GROUP;
+    if constexpr (GROUP == kNormThreads)
+      __syncthreads();
+    else
+      named_bar_sync(1 + grp, GROUP);
+    a = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < GROUP / 32; ++i) {
+      const float2 v = r[grp * (GROUP / 32) + i];
+      a.x += v.x;
+      a.y += v.y;
+    }
+  }
+  return a;
+}
+
 // dx, and the block's sums of dw and db: part [blocks][2][d].  Rows are dealt
 // to the groups round-robin.  While a row is reduced the next one is on its
 // way to shared memory, which costs no registers: those hold the running dw
@@ -235,7 +267,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
                   const float *__restrict__ weight, const float *__restrict__ mean_in,
                   const float *__restrict__ rstd_in, const T *__restrict__ dh,
                   T *__restrict__ dx, float *__restrict__ part, int M, int d) {
-  __shared__ float red[2][kNormThreads / 32];
+  __shared__ float2 red[2][kNormThreads / 32];
   extern __shared__ __align__(16) uint8_t ring[];
   int turn = 0;
   constexpr int kRows = kNormThreads / GROUP;
@@ -303,8 +335,8 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         }
       }
     }
-    const float m1 = group_sum<GROUP>(s1, red, turn) * inv_d;
-    const float m2 = group_sum<GROUP>(s2, red, turn) * inv_d;
+    const float2 sums = group_sum2<GROUP>(make_float2(s1, s2), red, turn);
+    const float m1 = sums.x * inv_d, m2 = sums.y * inv_d;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = lane + i * GROUP;
@@ -444,6 +476,10 @@ cudaError_t pick_n(const NormArgs &a, cudaStream_t stream) {
 }
 template <typename T, int VEC, bool kBackward>
 cudaError_t pick_group(const NormArgs &a, cudaStream_t stream) {
+  if constexpr (kBackward) {
+    if (norm_backward_half(a.d, sizeof(T), sizeof(T) * VEC))
+      return launch_bwd<T, VEC, 8 / VEC, 128>(a, stream);
+  }
   return a.d <= kNormWarpMaxD ? pick_n<T, VEC, 32, kBackward>(a, stream)
                               : pick_n<T, VEC, kNormThreads, kBackward>(a, stream);
 }
@@ -480,7 +516,11 @@ int launch_layer_norm_backward(const void *dy, const void *h, const float *weigh
   a.a = dy, a.b = h, a.weight = weight, a.mean = mean, a.rstd = rstd, a.dh = dh;
   a.o0 = dx, a.f0 = static_cast<float *>(workspace);
   a.M = M, a.d = d;
-  a.blocks = norm_backward_blocks(M, d);
+  const int es = dtype_bf16 ? 2 : 4;
+  const int vec = d * es % 16 == 0 ? 16 : d * es % 4 == 0 ? 4 : 2;
+  const int rows = norm_backward_half(d, es, vec) ? 2 : d <= kNormWarpMaxD ? 8 : 1;
+  const int64_t blocks = ((int64_t)M + rows - 1) / rows;
+  a.blocks = (int)(blocks < kNormBackwardBlocks ? blocks : kNormBackwardBlocks);
   if (pick<true>(a, dtype_bf16, stream) != cudaSuccess) return 1;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

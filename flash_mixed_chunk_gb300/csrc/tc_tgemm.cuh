@@ -46,7 +46,7 @@ struct TgCfg {
   static constexpr uint32_t B_BYTES = (256 / CG) * 64 * 2;       // 32 or 16 KB
   static constexpr uint32_t SLOT = A_BYTES + B_BYTES;
   static constexpr bool STAGED = KIND == TG_PROB || KIND == TG_SILU;
-  static constexpr int RING = STAGED ? (CG == 2 ? 5 : 3) : (CG == 2 ? 7 : 4);
+  static constexpr int RING = STAGED ? (CG == 2 ? 5 : 3) : (CG == 2 ? 6 : 4);
   static constexpr uint32_t PIECE = 32 * 64 * 2;                 // 32 rows x 64 columns
   static constexpr uint32_t STAGE = STAGED ? TG_EPI_WARPS * 2 * PIECE : 0;
   static constexpr uint32_t SMEM = RING * SLOT + STAGE + 1024;

@@ -180,75 +180,100 @@ __global__ void __launch_bounds__(32 * kReduceLanes)
   }
 }
 
-// The tiles that a cut went through: the sum of their parts, rounded.  The grid
-// is (a tile's blocks, cuts x tiles of a panel); the first cut of a panel sums
-// its tiles, 16 columns of a row a thread (its warp's loads are consecutive),
-// the parts in order.
+// The tiles that a cut went through: the sum of their parts, rounded.  Every
+// block makes the list of those tiles while the products still run (a ring of
+// 6 leaves room for a block beside them), then the blocks share the tiles in
+// pieces of 256 threads, 16 columns of a row a thread (a warp's loads are
+// consecutive), the parts in order.
 constexpr int kJoinThreads = 256;
 static_assert(kJoinThreads > kTgMaxCtas, "a thread a cut");
 template <int CG>
 __global__ void __launch_bounds__(kJoinThreads)
     tg_join(const __grid_constant__ TgParams P, int workers, int last) {
-  __shared__ int cut_s[kTgMaxCtas + 1], part_s[kTgMaxCtas], parts_s;
-  // launched by a TG_GRAD that had waited for what wrote the header: the plan
-  // is made while that kernel still runs
-  const int count = P.hdr != nullptr ? tg_count(P.hdr) : P.M;
-  const TgPlan plan = tg_plan<CG, TG_GRAD>(P, P.piece, count, workers);
-  // the grid's rows: the cuts between groups, a row for each tile of a panel
-  const int groups = plan.groups, w = (int)blockIdx.y / plan.side + 1;
-  const int lane = (int)blockIdx.y - (w - 1) * plan.side;
-  const TgCut c = tg_cut(plan, w, groups);
-  const int M = c.pi ? plan.s[1].M : plan.s[0].M;
-  const int begin = c.pos - c.off, end = begin + (c.pi ? plan.s[1].len : plan.s[0].len);
-  const int panel = c.tile + (c.pi ? plan.s[1].dealt : plan.s[0].dealt);
-  const int across = plan.s[0].Nt / plan.side;
-  const int mt = panel / across, nt = (panel - mt * across) * plan.side + lane;
-  // a panel's first cut; dW: this piece's rows; dX: complete once every piece
-  // has been
-  const bool mine = w < groups && c.off != 0 && tg_cut(plan, w - 1, groups).pos <= begin &&
-                    (c.pi == 0 ? mt * plan.row_step < M : last != 0);
-  if (!mine) {
-    // the grid must not be over before the one ahead of it: what follows on
-    // the stream waits for this one alone
-    if (blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();
-    return;
-  }
-  if ((int)threadIdx.x <= groups) cut_s[threadIdx.x] = tg_cut(plan, threadIdx.x, groups).pos;
+  __shared__ TgPlan plan;
+  __shared__ int cut_s[kTgMaxCtas + 1];        // where the groups' parts begin
+  __shared__ int part_s[kTgMaxCtas + 1];                // groups that have a part
+  __shared__ int2 warp_s[kJoinThreads / 32];
+  __shared__ int list_s[kTgMaxCtas], list_a[kTgMaxCtas], list_b[kTgMaxCtas], list_n;
+  // launched by a TG_GRAD that had waited for what wrote the header
+  if (threadIdx.x == 0)
+    plan = tg_plan<CG, TG_GRAD>(P, P.piece, P.hdr != nullptr ? tg_count(P.hdr) : P.M, workers);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int x = w - 1; cut_s[x] < end; ++x)
-      if (cut_s[x + 1] > cut_s[x]) part_s[n++] = 2 * (x * plan.side + lane) + (x == w - 1 ? 1 : 0);
-    parts_s = n;
+  const int groups = plan.groups, w = (int)threadIdx.x;
+  TgCut c = {};
+  if (w <= groups) {
+    c = tg_cut(plan, w, groups);
+    cut_s[w] = c.pos;
+  }
+  __syncthreads();
+  // the groups that have a part, and the cuts that are a panel's first, each
+  // numbered in order (the same in every block)
+  const bool has = w < groups && cut_s[w + 1] > cut_s[w];
+  bool first_cut = w > 0 && w < groups && c.off != 0 && cut_s[w - 1] <= c.pos - c.off;
+  if (first_cut) {  // dW: this piece's rows; dX: complete once every piece has been
+    const int panel = c.tile + plan.s[c.pi].dealt, mt = panel / (plan.s[0].Nt / plan.side);
+    first_cut = c.pi == 0 ? mt * plan.row_step < plan.s[0].M : last != 0;
+  }
+  const uint32_t votes = __ballot_sync(0xffffffffu, has);
+  const uint32_t votes2 = __ballot_sync(0xffffffffu, first_cut);
+  const uint32_t below = (1u << (w % 32)) - 1;
+  if (w % 32 == 0) warp_s[w / 32] = make_int2(__popc(votes), __popc(votes2));
+  __syncthreads();
+  int at = __popc(votes & below), item_at = __popc(votes2 & below);
+  for (int i = 0; i < w / 32; ++i) at += warp_s[i].x, item_at += warp_s[i].y;
+  if (has || w == groups) part_s[at] = w;  // (groups: the end)
+  if (w == groups) list_n = item_at;
+  __syncthreads();
+  if (first_cut) {
+    const int end = c.pos - c.off + plan.s[c.pi].len;
+    int b = at;
+    while (part_s[b] < groups && cut_s[part_s[b]] < end) ++b;
+    list_s[item_at] = w;
+    list_a[item_at] = at - 1;  // the group before the cut
+    list_b[item_at] = b;
   }
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   const float alpha = P.hdr != nullptr ? P.hdr->gmax : 1.f;
-  const int t = (int)(blockIdx.x * kJoinThreads + threadIdx.x);  // < 128 * 16 * CG
-  const int row = t % 128, q = t / 128 % 16, rank = t / (128 * 16);
-  const int m = (mt * CG + rank) * 128 + row, col = nt * 256 + q * 16;
-  if (m >= M || col >= P.K) return;
-  float v[16];
+  constexpr int kPieces = 128 * 16 * CG / kJoinThreads;
+  const int tasks = list_n * plan.side * kPieces;
+  for (int task = (int)blockIdx.x; task < tasks; task += (int)gridDim.x) {
+    const int lane = task / kPieces % plan.side, item = task / (kPieces * plan.side);
+    const int first = list_s[item], n1 = list_b[item];
+    const TgCut f = tg_cut(plan, first, groups);
+    const TgShape &h = plan.s[f.pi];
+    const int across = h.Nt / plan.side, panel = f.tile + h.dealt;
+    const int mt = panel / across, nt = (panel - mt * across) * plan.side + lane;
+    const int t = task % kPieces * kJoinThreads + (int)threadIdx.x;
+    const int row = t % 128, q = t / 128 % 16, rank = t / (128 * 16);
+    const int m = (mt * CG + rank) * 128 + row, col = nt * 256 + q * 16;
+    if (m >= h.M || col >= P.K) continue;
+    float v[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = 0.f;
-#pragma unroll 8
-  for (int n = 0; n < parts_s; ++n) {
-    const float *slot = P.slots + (int64_t)(part_s[n] * CG + rank) * kTgSlotFloats;
+    for (int k = 0; k < 16; ++k) v[k] = 0.f;
+#pragma unroll 4
+    for (int n = list_a[item]; n < n1; ++n) {
+      const int x = part_s[n];
+      // the tile's first part is the last one of its worker, the others first
+      const float *slot =
+          P.slots +
+          (int64_t)((2 * (x * plan.side + lane) + (x < first ? 1 : 0)) * CG + rank) * kTgSlotFloats;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 o = *reinterpret_cast<const float4 *>(slot + tg_slot_offset(row, q * 4 + j));
-      v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
+      for (int j = 0; j < 4; ++j) {
+        const float4 o = *reinterpret_cast<const float4 *>(slot + tg_slot_offset(row, q * 4 + j));
+        v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
+      }
     }
-  }
-  __nv_bfloat16 *out = c.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
-                            : P.D0 + (int64_t)(plan.col0 + m) * P.K;
-  uint32_t o[8];
+    __nv_bfloat16 *out = f.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
+                              : P.D0 + (int64_t)(plan.col0 + m) * P.K;
+    uint32_t o[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(alpha * v[2 * k], alpha * v[2 * k + 1]);
-  *reinterpret_cast<uint4 *>(out + col) = make_uint4(o[0], o[1], o[2], o[3]);
-  if (col + 8 < P.K)
-    *reinterpret_cast<uint4 *>(out + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(alpha * v[2 * k], alpha * v[2 * k + 1]);
+    *reinterpret_cast<uint4 *>(out + col) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (col + 8 < P.K)
+      *reinterpret_cast<uint4 *>(out + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -346,8 +371,7 @@ int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // the count can change the panels' width: a block row for every tile beside a cut
-  cfg.gridDim = dim3(128 * 16 * CG / kJoinThreads, w - 1);
+  cfg.gridDim = dim3(3 * kTgMaxCtas);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = attr;

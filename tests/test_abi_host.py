@@ -413,10 +413,11 @@ def test_layer_norm_rejects_before_queueing():
         assert fwd(M=4, **{k: v}) == fm.FMCA_ERR_INVALID_ARG     # overlaps
 
     nb = fm.flash_mca_layer_norm_backward_workspace_bytes
-    # one partial row of dw and db a block: 8 rows a block up to d = 1024, one
-    # beyond, 304 blocks at most
+    # one partial row of dw and db a block: at least 8 rows a block up to d =
+    # 256, 2 up to 1024, one beyond; 304 blocks at most
     up = lambda v: (v + 255) // 256 * 256  # noqa: E731
-    assert nb(1, 768) == up(8 * 768) and nb(17, 768) == up(3 * 8 * 768)
+    assert nb(1, 768) == up(8 * 768) and nb(17, 768) == up(9 * 8 * 768)
+    assert nb(17, 256) == up(3 * 8 * 256)
     assert nb(100000, 768) == up(304 * 8 * 768) and nb(5, 1025) == up(5 * 8 * 1025)
     assert nb(0, 768) == 0 and nb(4, 0) == 0 and nb(4, 8193) == 0
 
