@@ -560,6 +560,8 @@ def _placed(name, t, stream, fn, *args):
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if stream is None:
+        if dev == torch.cuda.current_device():
+            return fn(dev, torch.cuda.current_stream(dev).cuda_stream, *args)
         with torch.cuda.device(dev):
             return fn(dev, torch.cuda.current_stream(dev).cuda_stream, *args)
     with _on_stream(name, t, stream) as s:

@@ -81,7 +81,7 @@ def _binding_link() -> None:
     tmp = BINDING + f".tmp{os.getpid()}"
     subprocess.run(["g++", "-shared", "-o", tmp, os.path.join(BUILD, "binding.o"), "-L", PKG,
                     "-l:libflash_mca.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python",
-                    "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
+                    "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], check=True)
     os.replace(tmp, BINDING)
 
 

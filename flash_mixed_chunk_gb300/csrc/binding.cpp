@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -82,8 +82,9 @@ int size_of(const char *what, int64_t v) {
   return (int)v;
 }
 
+// torch.empty without its dispatcher
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Device &dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 at::Tensor workspace(size_t bytes, const char *what, const at::Device &dev) {
   if (bytes == 0) check(FMCA_ERR_UNSUPPORTED, what);

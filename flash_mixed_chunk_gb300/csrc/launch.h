@@ -270,13 +270,12 @@ int launch_tc_backward(const void *Z, const void *V, const void *U, const float 
                        bool saved = false);
 
 // Layer norm (norm.cu).  Rows of up to kNormWarpMaxD elements belong to a
-// warp, longer ones (to kNormMaxD) to a block; in the backward pass some of the
-// first to half a block (norm_backward_half: element and vector bytes).  The
-// backward pass deals its rows to norm_backward_blocks blocks at most, one
-// partial row of dw and db each.
+// warp or (norm_half: element and vector bytes) to half a block, longer ones
+// (to kNormMaxD) to a block.  The backward pass deals its rows to
+// norm_backward_blocks blocks at most, one partial row of dw and db each.
 constexpr int kNormWarpMaxD = 1024, kNormMaxD = 8192;
 constexpr int kNormBackwardBlocks = 304;
-inline bool norm_backward_half(int d, size_t elem, size_t vec) {
+inline bool norm_half(int d, size_t elem, size_t vec) {
   return d <= kNormWarpMaxD && d > (vec == 16 ? 512 : 256) && (elem == 4 || vec < 16);
 }
 inline int norm_backward_blocks(int M, int d) {

@@ -17,9 +17,10 @@
 //
 // A row belongs to one warp (d <= 1024) or to one block of 256 threads (d <=
 // 8192): 8, 16, 24 or 32 elements a thread, in 16-byte vectors where d allows
-// it, else 4-byte ones, else single elements.  Backward rows that would fill a
-// warp's registers and shared memory with few threads (fp32 beyond 512
-// elements, narrow vectors beyond 256) belong to half a block instead.
+// it, else 4-byte ones, else single elements.  Rows that would fill a warp's
+// registers (and, backward, its shared memory) with few threads at work (fp32
+// beyond 512 elements, narrow vectors beyond 256) belong to half a block: 5001
+// fp32 rows of 1001 take 17 us backward instead of 32.
 //
 // The backward pass keeps dw and db of the rows it has seen in registers, one
 // partial row a block in the workspace, and a second kernel adds the partial
@@ -98,22 +99,39 @@ __device__ __forceinline__ void load_w(const float *__restrict__ p, float *out) 
   }
 }
 
-// Sum of v over the threads of a row's group: a warp, or the whole block (two
-// alternating sets of shared words, so that one barrier a sum is enough).
+// The sums of a.x and a.y over the threads of a row's group: a warp, half a
+// block or the block (two sets of shared words in turn, so that one barrier a
+// sum is enough; half a block meets at a barrier of its own).
 template <int GROUP>
-__device__ __forceinline__ float group_sum(float v, float (*red)[kNormThreads / 32], int &turn) {
+__device__ __forceinline__ float2 group_sum2(float2 a, float2 (*red)[kNormThreads / 32],
+                                             int &turn) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (GROUP > 32) {
-    float *r = red[turn];
-    turn ^= 1;
-    if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < GROUP / 32; ++i) v += r[i];
+  for (int o = 16; o > 0; o >>= 1) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+    a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
   }
-  return v;
+  if constexpr (GROUP > 32) {
+    float2 *r = red[turn];
+    turn ^= 1;
+    if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = a;
+    const int grp = threadIdx.x / GROUP;
+    if constexpr (GROUP == kNormThreads)
+      __syncthreads();
+    else
+      named_bar_sync(1 + grp, GROUP);
+    a = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < GROUP / 32; ++i) {
+      const float2 v = r[grp * (GROUP / 32) + i];
+      a.x += v.x;
+      a.y += v.y;
+    }
+  }
+  return a;
+}
+template <int GROUP>
+__device__ __forceinline__ float group_sum(float v, float2 (*red)[kNormThreads / 32], int &turn) {
+  return group_sum2<GROUP>(make_float2(v, 0.f), red, turn).x;
 }
 
 // T: I/O type; VEC elements a vector, N vectors a thread; GROUP threads a row.
@@ -123,47 +141,40 @@ __global__ void __launch_bounds__(kNormThreads)
                  const float *__restrict__ bias, T *h, T *__restrict__ y,
                  float *__restrict__ mean_out, float *__restrict__ rstd_out, int M, int d,
                  float eps) {
-  __shared__ float red[2][kNormThreads / 32];
+  __shared__ float2 red[2][kNormThreads / 32];
   int turn = 0;
   const int lane = threadIdx.x % GROUP;
   const int64_t row = (int64_t)blockIdx.x * (kNormThreads / GROUP) + threadIdx.x / GROUP;
   if (row >= M) return;  // whole groups (a block is one row when GROUP is a block)
   const int nv = d / VEC;
   const T *xr = x + row * d;
-  float v[N * VEC];
+  // the row stays in its own type: half the registers, twice the rows in flight
+  using P = Pack<T, VEC>;
+  P v[N], r[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int c = lane + i * GROUP;
     if (c < nv) {
-      load_vec<T, VEC>(xr + (int64_t)c * VEC, v + i * VEC);
-    } else {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) v[i * VEC + k] = 0.f;
-    }
-  }
-  if (res != nullptr) {
-    const T *rr = res + row * d;
-    T *hr = h + row * d;
-    float r[N * VEC];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = lane + i * GROUP;
-      if (c < nv) load_vec<T, VEC>(rr + (int64_t)c * VEC, r + i * VEC);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = lane + i * GROUP;
-      if (c < nv) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k)  // the statistics are those of the stored sum
-          v[i * VEC + k] = to_f(from_f<T>(v[i * VEC + k] + r[i * VEC + k]));
-        store_vec<T, VEC>(hr + (int64_t)c * VEC, v + i * VEC);
-      }
+      v[i].raw = *reinterpret_cast<const typename P::raw_t *>(xr + (int64_t)c * VEC);
+      if (res != nullptr)
+        r[i].raw = *reinterpret_cast<const typename P::raw_t *>(res + row * d + (int64_t)c * VEC);
     }
   }
   float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < N * VEC; ++i) s += v[i];
+  for (int i = 0; i < N; ++i) {
+    const int c = lane + i * GROUP;
+    if (c < nv) {
+      if (res != nullptr) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)  // the statistics are those of the stored sum
+          v[i].v[k] = from_f<T>(to_f(v[i].v[k]) + to_f(r[i].v[k]));
+        *reinterpret_cast<typename P::raw_t *>(h + row * d + (int64_t)c * VEC) = v[i].raw;
+      }
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) s += to_f(v[i].v[k]);
+    }
+  }
   const float inv_d = 1.0f / (float)d;
   const float mean = group_sum<GROUP>(s, red, turn) * inv_d;
   float q = 0.f;
@@ -173,7 +184,7 @@ __global__ void __launch_bounds__(kNormThreads)
     if (c < nv) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        const float t = v[i * VEC + k] - mean;
+        const float t = to_f(v[i].v[k]) - mean;
         q += t * t;
       }
     }
@@ -188,7 +199,7 @@ __global__ void __launch_bounds__(kNormThreads)
       load_w<VEC>(weight + c * VEC, w);
       load_w<VEC>(bias + c * VEC, b);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) o[k] = (v[i * VEC + k] - mean) * rstd * w[k] + b[k];
+      for (int k = 0; k < VEC; ++k) o[k] = (to_f(v[i].v[k]) - mean) * rstd * w[k] + b[k];
       store_vec<T, VEC>(yr + (int64_t)c * VEC, o);
     }
   }
@@ -225,36 +236,6 @@ template <typename T, int VEC, int N>
 constexpr size_t norm_ring_bytes() {
   // single 2-byte elements cannot be copied asynchronously: read in place
   return sizeof(T) * VEC >= 4 ? (size_t)kNormStages * 3 * N * kNormThreads * sizeof(T) * VEC : 0;
-}
-
-// The sums of a.x and a.y over a row's group, as group_sum; a quarter or half
-// block meets at a barrier of its own.
-template <int GROUP>
-__device__ __forceinline__ float2 group_sum2(float2 a, float2 (*red)[kNormThreads / 32],
-                                             int &turn) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
-    a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
-  }
-  if constexpr (GROUP > 32) {
-    float2 *r = red[turn];
-    turn ^= 1;
-    if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = a;
-    const int grp = threadIdx.x / GROUP;
-    if constexpr (GROUP == kNormThreads)
-      __syncthreads();
-    else
-      named_bar_sync(1 + grp, GROUP);
-    a = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < GROUP / 32; ++i) {
-      const float2 v = r[grp * (GROUP / 32) + i];
-      a.x += v.x;
-      a.y += v.y;
-    }
-  }
-  return a;
 }
 
 // dx, and the block's sums of dw and db: part [blocks][2][d].  Rows are dealt
@@ -476,10 +457,9 @@ cudaError_t pick_n(const NormArgs &a, cudaStream_t stream) {
 }
 template <typename T, int VEC, bool kBackward>
 cudaError_t pick_group(const NormArgs &a, cudaStream_t stream) {
-  if constexpr (kBackward) {
-    if (norm_backward_half(a.d, sizeof(T), sizeof(T) * VEC))
-      return launch_bwd<T, VEC, 8 / VEC, 128>(a, stream);
-  }
+  if (norm_half(a.d, sizeof(T), sizeof(T) * VEC))
+    return kBackward ? launch_bwd<T, VEC, 8 / VEC, 128>(a, stream)
+                     : launch_fwd<T, VEC, 8 / VEC, 128>(a, stream);
   return a.d <= kNormWarpMaxD ? pick_n<T, VEC, 32, kBackward>(a, stream)
                               : pick_n<T, VEC, kNormThreads, kBackward>(a, stream);
 }
@@ -494,6 +474,12 @@ cudaError_t pick(const NormArgs &a, int bf16, cudaStream_t stream) {
   return pick_group<float, 1, kBackward>(a, stream);
 }
 
+// Rows a block works on at a time.
+int norm_rows(int d, int elem) {
+  const int vec = d * elem % 16 == 0 ? 16 : d * elem % 4 == 0 ? 4 : 2;
+  return norm_half(d, elem, vec) ? 2 : d <= kNormWarpMaxD ? kNormThreads / 32 : 1;
+}
+
 }  // namespace
 
 int launch_layer_norm(const void *x, const void *res, const float *weight, const float *bias,
@@ -503,7 +489,7 @@ int launch_layer_norm(const void *x, const void *res, const float *weight, const
   a.a = x, a.b = res, a.weight = weight, a.bias = bias;
   a.o0 = h, a.o1 = y, a.f0 = mean, a.f1 = rstd;
   a.M = M, a.d = d, a.eps = eps;
-  const int rows = d <= kNormWarpMaxD ? kNormThreads / 32 : 1;
+  const int rows = norm_rows(d, dtype_bf16 ? 2 : 4);
   a.blocks = (int)(((int64_t)M + rows - 1) / rows);
   return pick<false>(a, dtype_bf16, stream) == cudaSuccess ? 0 : 1;
 }
@@ -516,9 +502,7 @@ int launch_layer_norm_backward(const void *dy, const void *h, const float *weigh
   a.a = dy, a.b = h, a.weight = weight, a.mean = mean, a.rstd = rstd, a.dh = dh;
   a.o0 = dx, a.f0 = static_cast<float *>(workspace);
   a.M = M, a.d = d;
-  const int es = dtype_bf16 ? 2 : 4;
-  const int vec = d * es % 16 == 0 ? 16 : d * es % 4 == 0 ? 4 : 2;
-  const int rows = norm_backward_half(d, es, vec) ? 2 : d <= kNormWarpMaxD ? 8 : 1;
+  const int rows = norm_rows(d, dtype_bf16 ? 2 : 4);
   const int64_t blocks = ((int64_t)M + rows - 1) / rows;
   a.blocks = (int)(blocks < kNormBackwardBlocks ? blocks : kNormBackwardBlocks);
   if (pick<true>(a, dtype_bf16, stream) != cudaSuccess) return 1;

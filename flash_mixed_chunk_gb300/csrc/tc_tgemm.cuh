@@ -92,7 +92,15 @@ struct TgParams {
   int piece;           // piece of the column axis (TG_PROB, TG_GRAD)
   uint32_t cap_boxes;
   const TgHeader *hdr; // device count of rows (NULL: M)
+  const float *gmax;   // scale of dW and dX (NULL: 1)
   const int *idx;      // compact row -> row (NULL: the same)
+  // few rows, taken as they are: their targets (TG_LSE, TG_PROB), and what
+  // TG_PROB leaves for TG_GRAD: whether a row has one, X with 0 in the others
+  const int64_t *target;
+  const __nv_bfloat16 *X;
+  __nv_bfloat16 *Xz;
+  int *keep;
+  float *gmax_out;
   // TG_LSE
   float2 *part;        // [2 ceil(N / 256)][M]
   float *ztgt;         // [M]
@@ -470,6 +478,32 @@ __host__ __device__ inline int64_t tg_slot_offset(int row, int j) {
 }
 constexpr int64_t kTgSlotFloats = 128 * 256;
 
+// TG_PROB on rows as they are (128 at most): the largest |dloss| of those that
+// have a target, the same in every warp of the launch, and, shared between the
+// warps, what TG_GRAD needs: the rows' marks and X without the others' contents
+// (0 times NaN would be NaN).
+__device__ __forceinline__ float tg_rows_as_they_are(const TgParams &P, int count, int w, int W,
+                                                     int lane) {
+  float top = 0.f;
+  for (int r = lane; r < count; r += 32) {
+    const int64_t t = P.target[r];
+    if (t >= 0 && t < P.N) top = fmaxf(top, fabsf(P.g[r]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (top == INFINITY) top = 1.f;  // no scale that the other rows could bear
+  if (w == 0 && lane == 0) *P.gmax_out = top;
+  for (int r = w; r < count; r += W) {
+    const int64_t t = P.target[r];
+    const bool has = t >= 0 && t < P.N;
+    if (lane == 0) P.keep[r] = has ? 1 : 0;
+    const uint4 *src = reinterpret_cast<const uint4 *>(P.X + (int64_t)r * P.K);
+    uint4 *dst = reinterpret_cast<uint4 *>(P.Xz + (int64_t)r * P.K);
+    for (int v = lane; v < P.K / 8; v += 32) dst[v] = has ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  return top;
+}
+
 template <int CG, int KIND>
 __global__ void __launch_bounds__(TG_THREADS, 1)
     tc_tgemm(const __grid_constant__ TgParams P) {
@@ -684,7 +718,15 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       }
       __syncwarp();
     };
-    const float gmax = KIND == TG_PROB ? P.hdr->gmax : 0.f;
+    float gmax = 0.f;
+    if constexpr (KIND == TG_PROB) {
+      if (P.target == nullptr) {
+        gmax = *P.gmax;
+      } else {
+        gmax = tg_rows_as_they_are(P, count, (int)blockIdx.x * TG_EPI_WARPS + warp - 2,
+                                   (int)gridDim.x * TG_EPI_WARPS, lane);
+      }
+    }
     for (int i = 0; more; ++i) {
       u = ahead;
       more = walk.next(ahead);
@@ -706,12 +748,18 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
         ++fetched[1];
         __syncwarp();
       }
-      // TG_PROB: the row's constants, before the accumulator is ready
-      const bool in_rows = m < count;
+      // TG_LSE, TG_PROB: the row's constants, before the accumulator is ready
+      bool in_rows = m < count;
       float row_lse = 0.f, row_g = 0.f;
       int row_at = -1;
       if constexpr (KIND == TG_LSE || KIND == TG_PROB) {
-        if (in_rows) row_at = P.tgt[m] - col0 - c0;
+        if (P.target == nullptr) {
+          if (in_rows) row_at = P.tgt[m] - col0 - c0;
+        } else {
+          const int64_t t = in_rows ? P.target[m] : -1;
+          in_rows = t >= 0 && t < P.N;
+          if (in_rows) row_at = (int)t - col0 - c0;
+        }
       }
       if constexpr (KIND == TG_PROB) {
         if (in_rows) {
@@ -789,12 +837,13 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
         float *slot = nullptr;
         __nv_bfloat16 *out = nullptr;
         float alpha = 1.f;
-        bool wide = false;
+        bool wide = false, live = true;  // dX of a row without a target is 0, whatever W holds
         if constexpr (KIND == TG_GRAD) {
           slot = u.whole ? P.sums + ((int64_t)(u.mt * CG + (int)rank) * h.Nt + u.nt) * kTgSlotFloats
                          : P.slots + (int64_t)((2 * worker + (u.ks0 > 0 ? 0 : 1)) * CG + (int)rank) *
                                          kTgSlotFloats;
-          if (P.hdr != nullptr) alpha = P.hdr->gmax;
+          if (P.gmax != nullptr) alpha = *P.gmax;
+          live = u.pi == 0 || P.keep == nullptr || (in && P.keep[m] != 0);
           wide = P.K % 16 == 0 && (reinterpret_cast<uintptr_t>(u.pi ? P.D1 : P.D0) & 31u) == 0;
           if (direct && in)
             out = u.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
@@ -888,7 +937,9 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
                   uint32_t w[8];
 #pragma unroll
                   for (int k = 0; k < 8; ++k)
-                    w[k] = pack_bf16x2(alpha * v[16 * q + 2 * k], alpha * v[16 * q + 2 * k + 1]);
+                    w[k] = live ? pack_bf16x2(alpha * v[16 * q + 2 * k],
+                                              alpha * v[16 * q + 2 * k + 1])
+                                : 0u;
                   const int cq = c0 + 32 * c + 16 * q;
                   if (wide) {
                     if (cq < P.K) tg_store32(out + cq, w);

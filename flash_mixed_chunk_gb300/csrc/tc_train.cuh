@@ -9,7 +9,9 @@
 // The rows with a target are copied next to each other first (vocab_gather),
 // so that a row without one costs nothing in the products and whatever its X
 // holds (NaN included) reaches nothing.  The number of such rows stays on the
-// device; every kernel reads it there, so the calls can be captured.
+// device; every kernel reads it there, so the calls can be captured.  Up to 128
+// rows, one tile, there is nothing to save: they are taken as they are, a
+// launch fewer in either direction.
 //
 // The forward pass keeps, per row and 128 columns, the maximum and the sum of
 // exp(z - maximum), 1/32 of the logits' bytes at bf16; vocab_reduce
@@ -146,15 +148,17 @@ __global__ void __launch_bounds__(kGatherThreads) vocab_gather(GatherArgs a) {
 }
 
 // loss and lse of the rows from the products' partial maxima and sums: 32
-// rows a block, 16 lanes of parts each, joined in order.
+// rows a block, 16 lanes of parts each, joined in order.  The rows are compact
+// (idx, hdr), or as they are (target; one without a target has loss and lse 0).
 constexpr int kReduceLanes = 16;
 __global__ void __launch_bounds__(32 * kReduceLanes)
     vocab_reduce(const float2 *__restrict__ part, const float *__restrict__ ztgt,
-                 const int *__restrict__ idx, const TgHeader *__restrict__ hdr, float *loss,
-                 float *lse, int parts, int M) {
+                 const int *__restrict__ idx, const TgHeader *__restrict__ hdr,
+                 const int64_t *__restrict__ target, float *loss, float *lse, int parts, int M,
+                 int V) {
   __shared__ float2 s[kReduceLanes][32];
   griddep_wait();
-  const int count = hdr->count;
+  const int count = hdr != nullptr ? hdr->count : M;
   const int r = threadIdx.x % 32, l = threadIdx.x / 32;
   const int64_t m = (int64_t)blockIdx.x * 32 + r;
   if ((int64_t)blockIdx.x * 32 >= count) return;
@@ -174,19 +178,79 @@ __global__ void __launch_bounds__(32 * kReduceLanes)
 #pragma unroll
     for (int i = 1; i < kReduceLanes; ++i) t = join(t, s[i][r]);
     const float v = t.x + logf(t.y);
-    const int row = idx[m];
-    lse[row] = v;
-    loss[row] = v - ztgt[m];
+    if (target == nullptr) {
+      const int row = idx[m];
+      lse[row] = v;
+      loss[row] = v - ztgt[m];
+    } else {
+      const bool has = has_target(target[m], V);
+      lse[m] = has ? v : 0.f;
+      loss[m] = has ? v - ztgt[m] : 0.f;
+    }
   }
 }
 
 // The tiles that a cut went through: the sum of their parts, rounded.  Every
 // block makes the list of those tiles while the products still run (a ring of
 // 6 leaves room for a block beside them), then the blocks share the tiles in
-// pieces of 256 threads, 16 columns of a row a thread (a warp's loads are
-// consecutive), the parts in order.
+// pieces of 256 threads (a warp's loads are consecutive), the parts in order.
 constexpr int kJoinThreads = 256;
 static_assert(kJoinThreads > kTgMaxCtas, "a thread a cut");
+
+// The listed tiles, COLS columns of a row a thread: list_s the first cut,
+// list_a .. list_b the numbers of its parts' groups in part_s.
+template <int CG, int COLS>
+__device__ __forceinline__ void tg_join_tiles(const TgParams &P, const TgPlan &plan,
+                                              const int *list_s, const int *list_a,
+                                              const int *list_b, const int *part_s, int list_n,
+                                              float alpha) {
+  constexpr int kAcross = 256 / COLS, kPieces = 128 * kAcross * CG / kJoinThreads;
+  const int tasks = list_n * plan.side * kPieces;
+  for (int task = (int)blockIdx.x; task < tasks; task += (int)gridDim.x) {
+    const int lane = task / kPieces % plan.side, item = task / (kPieces * plan.side);
+    const int first = list_s[item], n1 = list_b[item];
+    const TgCut f = tg_cut(plan, first, plan.groups);
+    const TgShape &h = plan.s[f.pi];
+    const int across = h.Nt / plan.side, panel = f.tile + h.dealt;
+    const int mt = panel / across, nt = (panel - mt * across) * plan.side + lane;
+    const int t = task % kPieces * kJoinThreads + (int)threadIdx.x;
+    const int row = t % 128, q = t / 128 % kAcross, rank = t / (128 * kAcross);
+    const int m = (mt * CG + rank) * 128 + row, col = nt * 256 + q * COLS;
+    if (m >= h.M || col >= P.K) continue;
+    float v[COLS];
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) v[k] = 0.f;
+#pragma unroll(COLS == 4 ? 16 : 4)
+    for (int n = list_a[item]; n < n1; ++n) {
+      const int x = part_s[n];
+      // the tile's first part is the last one of its worker, the others first
+      const float *slot =
+          P.slots +
+          (int64_t)((2 * (x * plan.side + lane) + (x < first ? 1 : 0)) * CG + rank) * kTgSlotFloats;
+#pragma unroll
+      for (int j = 0; j < COLS / 4; ++j) {
+        const float4 o = *reinterpret_cast<const float4 *>(
+            slot + tg_slot_offset(row, q * (COLS / 4) + j));
+        v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
+      }
+    }
+    __nv_bfloat16 *out = f.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
+                              : P.D0 + (int64_t)(plan.col0 + m) * P.K;
+    uint32_t o[COLS / 2];
+    const bool live = f.pi == 0 || P.keep == nullptr || P.keep[m] != 0;
+#pragma unroll
+    for (int k = 0; k < COLS / 2; ++k)
+      o[k] = live ? pack_bf16x2(alpha * v[2 * k], alpha * v[2 * k + 1]) : 0u;
+    if constexpr (COLS == 4) {
+      *reinterpret_cast<uint2 *>(out + col) = make_uint2(o[0], o[1]);
+    } else {
+      *reinterpret_cast<uint4 *>(out + col) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (col + 8 < P.K)
+        *reinterpret_cast<uint4 *>(out + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
 template <int CG>
 __global__ void __launch_bounds__(kJoinThreads)
     tg_join(const __grid_constant__ TgParams P, int workers, int last) {
@@ -235,45 +299,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  const float alpha = P.hdr != nullptr ? P.hdr->gmax : 1.f;
-  constexpr int kPieces = 128 * 16 * CG / kJoinThreads;
-  const int tasks = list_n * plan.side * kPieces;
-  for (int task = (int)blockIdx.x; task < tasks; task += (int)gridDim.x) {
-    const int lane = task / kPieces % plan.side, item = task / (kPieces * plan.side);
-    const int first = list_s[item], n1 = list_b[item];
-    const TgCut f = tg_cut(plan, first, groups);
-    const TgShape &h = plan.s[f.pi];
-    const int across = h.Nt / plan.side, panel = f.tile + h.dealt;
-    const int mt = panel / across, nt = (panel - mt * across) * plan.side + lane;
-    const int t = task % kPieces * kJoinThreads + (int)threadIdx.x;
-    const int row = t % 128, q = t / 128 % 16, rank = t / (128 * 16);
-    const int m = (mt * CG + rank) * 128 + row, col = nt * 256 + q * 16;
-    if (m >= h.M || col >= P.K) continue;
-    float v[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = 0.f;
-#pragma unroll 4
-    for (int n = list_a[item]; n < n1; ++n) {
-      const int x = part_s[n];
-      // the tile's first part is the last one of its worker, the others first
-      const float *slot =
-          P.slots +
-          (int64_t)((2 * (x * plan.side + lane) + (x < first ? 1 : 0)) * CG + rank) * kTgSlotFloats;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 o = *reinterpret_cast<const float4 *>(slot + tg_slot_offset(row, q * 4 + j));
-        v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
-      }
-    }
-    __nv_bfloat16 *out = f.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
-                              : P.D0 + (int64_t)(plan.col0 + m) * P.K;
-    uint32_t o[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(alpha * v[2 * k], alpha * v[2 * k + 1]);
-    *reinterpret_cast<uint4 *>(out + col) = make_uint4(o[0], o[1], o[2], o[3]);
-    if (col + 8 < P.K)
-      *reinterpret_cast<uint4 *>(out + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-  }
+  const float alpha = P.gmax != nullptr ? *P.gmax : 1.f;
+  // 16 columns a thread; of few tiles (each of many parts) 4, so that the
+  // parts are read at the same time
+  if (list_n * plan.side > 4)
+    tg_join_tiles<CG, 16>(P, plan, list_s, list_a, list_b, part_s, list_n, alpha);
+  else
+    tg_join_tiles<CG, 4>(P, plan, list_s, list_a, list_b, part_s, list_n, alpha);
 }
 
 // ---------------------------------------------------------------- host side
@@ -357,14 +389,13 @@ int launch_tgemm(const TgParams &P, cudaStream_t stream) {
 }
 
 // TG_GRAD on piece P.piece of np, and the sums of the tiles that were cut.
-// Without a device count the cuts are known here, and none may go through a
-// tile.
+// Without a device count the cuts are known here, and there may be none.
 template <int CG>
 int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
   const int w = tg_workers<CG, TG_GRAD>(P);
   if (w <= 0 || launch_tgemm_kind<CG, TG_GRAD>(P, w, stream)) return 1;
   const TgPlan p = tg_plan<CG, TG_GRAD>(P, P.piece, P.M, w);
-  bool join = P.hdr != nullptr;
+  bool join = P.hdr != nullptr;  // the cuts are not known here
   for (int x = 1; x < p.groups && !join; ++x) join = tg_cut(p, x, p.groups).off != 0;
   if (!join || w < 2) return 0;
   cudaLaunchAttribute attr[1];
@@ -405,15 +436,19 @@ int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *lo
   a.tgt = reinterpret_cast<int *>(ws + L.tgt);
   a.hdr = reinterpret_cast<TgHeader *>(ws + L.hdr);
   a.loss = loss, a.lse_out = lse;
-  const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
-  a.per = (M + blocks - 1) / blocks;
-  vocab_gather<false><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return 1;
+  constexpr bool kCompact = CG == 2;
+  if (kCompact) {
+    const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
+    a.per = (M + blocks - 1) / blocks;
+    vocab_gather<false><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return 1;
+  }
 
   TgParams P = {};
-  if (!nt_maps<CG>(P, a.Xc, W, M, V, d)) return 2;
+  if (!nt_maps<CG>(P, kCompact ? a.Xc : a.X, W, M, V, d)) return 2;
   P.M = M, P.N = V, P.K = d;
-  P.hdr = a.hdr;
+  P.hdr = kCompact ? a.hdr : nullptr;
+  P.target = kCompact ? nullptr : target;
   P.part = reinterpret_cast<float2 *>(ws + L.part);
   P.ztgt = reinterpret_cast<float *>(ws + L.ztgt);
   P.tgt = a.tgt;
@@ -429,8 +464,8 @@ int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *lo
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, vocab_reduce, (const float2 *)P.part, (const float *)P.ztgt,
-                            (const int *)a.idx, (const TgHeader *)a.hdr, loss, lse,
-                            2 * ((V + 255) / 256), M) == cudaSuccess
+                            (const int *)a.idx, P.hdr, P.target, loss, lse,
+                            2 * ((V + 255) / 256), M, V) == cudaSuccess
              ? 0
              : 1;
 }
@@ -453,18 +488,30 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   a.lse_c = reinterpret_cast<float *>(ws + L.lse);
   a.g_c = reinterpret_cast<float *>(ws + L.g);
   a.dX = static_cast<__nv_bfloat16 *>(dX);
-  const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
-  a.per = (M + blocks - 1) / blocks;
-  vocab_gather<true><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return 1;
+  constexpr bool kCompact = CG == 2;
+  if (kCompact) {
+    const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
+    a.per = (M + blocks - 1) / blocks;
+    vocab_gather<true><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return 1;
+  }
 
   TgParams P = {}, Q = {};
-  if (!nt_maps<CG>(P, a.Xc, W, M, V, d)) return 2;
+  if (!nt_maps<CG>(P, kCompact ? a.Xc : a.X, W, M, V, d)) return 2;
   P.M = M, P.N = V, P.K = d;
   P.cap_boxes = L.cap_boxes;
-  P.hdr = a.hdr;
-  P.tgt = a.tgt;
-  P.lse = a.lse_c, P.g = a.g_c;
+  P.gmax = &a.hdr->gmax;
+  if (kCompact) {
+    P.hdr = a.hdr;
+    P.tgt = a.tgt;
+    P.lse = a.lse_c, P.g = a.g_c;
+  } else {
+    P.target = target;
+    P.lse = lse, P.g = dloss;
+    P.X = a.X, P.Xz = a.Xc;
+    P.keep = a.idx;
+    P.gmax_out = &a.hdr->gmax;
+  }
   const uint64_t box_rows = (uint64_t)L.cap_boxes * 64;
   if (!make_map_bf16(&P.S, ws + L.boxes, 64, box_rows, 64, 32)) return 2;
   Q = P;
@@ -473,7 +520,7 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
       !make_map_bf16(&Q.B, a.Xc, d, M, 64, 64) || !make_map_bf16(&Q.B1, W, d, V, 64, 64))
     return 2;
   Q.A1 = Q.A;
-  Q.idx = a.idx;
+  Q.idx = kCompact ? a.idx : nullptr;
   Q.D0 = static_cast<__nv_bfloat16 *>(dW);
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
   Q.sums = reinterpret_cast<float *>(ws + L.sums);

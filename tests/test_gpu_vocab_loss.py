@@ -130,10 +130,11 @@ def test_sharp_and_flat_rows():
     check(m, X, W, t, dloss)
 
 
-def test_rows_without_target_reach_nothing():
+@pytest.mark.parametrize("M", [300, 90])
+def test_rows_without_target_reach_nothing(M):
     """NaN and infinities in ignored rows of X, and in their dloss."""
     m = fm()
-    X, W, t, dloss = make(300, 1000, 128, 0.5, 31)
+    X, W, t, dloss = make(M, 1000, 128, 0.5, 31)
     clean = run(m, X, W, t, dloss)
     out = (t < 0) | (t >= 1000)
     X2, g2 = X.clone(), dloss.clone()
@@ -155,14 +156,15 @@ def test_no_row_has_a_target(M):
         assert (a == 0).all()
 
 
-def test_nan_stays_in_its_row_and_weights_of_zero():
+@pytest.mark.parametrize("M", [200, 100])
+def test_nan_stays_in_its_row_and_weights_of_zero(M):
     m = fm()
-    X, W, t, dloss = make(200, 600, 64, 1.0, 51)
+    X, W, t, dloss = make(M, 600, 64, 1.0, 51)
     ref = run(m, X, W, t, dloss)
     X2 = X.clone()
     X2[17, 3] = float("nan")
     loss, lse, dX, dW = run(m, X2, W, t, dloss)
-    keep = torch.arange(200, device="cuda") != 17
+    keep = torch.arange(M, device="cuda") != 17
     assert torch.isnan(loss[17]) and torch.isnan(dX[17]).all() and torch.isnan(dW).all()
     assert torch.equal(loss[keep], ref[0][keep]) and torch.equal(dX[keep], ref[2][keep])
     for a in m.vocab_loss_backward(X, W, t, ref[1], torch.zeros_like(dloss)):
@@ -171,15 +173,16 @@ def test_nan_stays_in_its_row_and_weights_of_zero():
     g2 = dloss.clone()
     g2[5] = float("inf")
     dX, dW = m.vocab_loss_backward(X, W, t, ref[1], g2)
-    keep = torch.arange(200, device="cuda") != 5
+    keep = torch.arange(M, device="cuda") != 5
     assert torch.isfinite(dX[keep]).all() and not torch.isfinite(dX[5]).any()
 
 
-def test_tiny_and_huge_weights_scale_the_gradients():
+@pytest.mark.parametrize("M", [150, 128])
+def test_tiny_and_huge_weights_scale_the_gradients(M):
     """dloss times a power of two gives the gradients times it, bit for bit
     (no overflow or underflow in between)."""
     m = fm()
-    X, W, t, dloss = make(150, 400, 64, 0.8, 61)
+    X, W, t, dloss = make(M, 400, 64, 0.8, 61)
     _, lse = m.vocab_loss(X, W, t)
     base = m.vocab_loss_backward(X, W, t, lse, dloss)
     for k in (-60, 60):
@@ -213,12 +216,13 @@ def test_same_bits_again_on_streams_and_behind_the_last_row():
         assert torch.equal(a[:n], b) and (a[n:] == 3.0).all()
 
 
-def test_captured_calls_follow_the_targets():
+@pytest.mark.parametrize("M", [500, 77])
+def test_captured_calls_follow_the_targets(M):
     """Two graphs over the same inputs; the targets change between replays, so
     that the number of rows that take part does."""
     m = fm()
-    X, W, t, dloss = make(500, 1500, 64, 1.0, 81)
-    targets = [make(500, 1500, 64, k, 82)[2] for k in (1.0, 0.4, 0.0, 0.7)]
+    X, W, t, dloss = make(M, 1500, 64, 1.0, 81)
+    targets = [make(M, 1500, 64, k, 82)[2] for k in (1.0, 0.4, 0.0, 0.7)]
     refs = [run(m, X, W, v, dloss) for v in targets]
     graphs = []
     for _ in range(2):
@@ -287,3 +291,14 @@ def test_refusals():
                     16, dtype=torch.uint8, device="cuda"))):            # too small
         with pytest.raises(m.FmcaError):
             bad()
+
+
+@pytest.mark.parametrize("M", [40, 300])
+def test_nan_in_the_vocabulary_leaves_ignored_rows_zero(M):
+    m = fm()
+    X, W, t, dloss = make(M, 3000, 64, 0.5, 95)
+    W[11, 3] = float("nan")
+    loss, lse, dX, dW = run(m, X, W, t, dloss)
+    out = (t < 0) | (t >= 3000)
+    assert (loss[out] == 0).all() and (lse[out] == 0).all() and (dX[out] == 0).all()
+    assert torch.isnan(loss[~out]).all() and torch.isnan(dX[~out]).all()
