@@ -83,7 +83,8 @@ __host__ __device__ inline TgPieces tg_pieces(int count, int V, uint32_t cap_box
 
 struct TgParams {
   CUtensorMap A, B;    // NT kinds: X [M][K] box {64, 128}, W [N][K] box {64, 256 / CG}
-                       // TG_GRAD: A of problem 0 and (A1) of problem 1, B likewise
+                       // TG_GRAD: A of problem 0, box {64, 64}, and (A1) of
+                       // problem 1, box {64, 128}; B and B1, box {64, 64}
   CUtensorMap A1, B1;
   CUtensorMap S;       // TG_PROB, TG_SILU: the boxes as rows of 64, box {64, 32}
   CUtensorMap U0, U1, U2;  // TG_SILU: the incoming gradients, box {64, 32}
@@ -589,18 +590,19 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
             tg_load<CG>(sb, &P.B, bar, kk, col0 + nb0);
           } else {
             const CUtensorMap *mB = u.pi ? &P.B1 : &P.B;
-            if (P.blocked) {
-              // problem 0: column blocks m0 / 64 and the next, token block
-              // kk / 64; problem 1: column block kk / 64, two token blocks
-              const int t64 = n_tok64;
-              const int b0 = u.pi ? (kk / 64) * t64 + m0 / 64 : (m0 / 64) * t64 + kk / 64;
-              const int b1 = b0 + (u.pi ? 1 : t64);
-              tg_load<CG>(sa, &P.A, bar, 0, b0 * 64);
-              tg_load<CG>(sa + 8192, &P.A, bar, 0, b1 * 64);
-            } else if (u.pi) {  // rows m, columns k
-              tg_load<CG>(sa, &P.A1, bar, kk, m0);
-              tg_load<CG>(sa + 8192, &P.A1, bar, kk, m0 + 64);
-            } else {            // rows k, columns m
+            if (u.pi) {
+              // rows m, columns k (in the boxes: column block kk / 64, two token
+              // blocks, one behind the other)
+              if (P.blocked)
+                tg_load<CG>(sa, &P.A1, bar, 0, (kk / 64) * n_tok64 * 64 + m0);
+              else
+                tg_load<CG>(sa, &P.A1, bar, kk, m0);
+            } else if (P.blocked) {
+              // columns m: column blocks m0 / 64 and the next, token block kk / 64
+              const int row0 = (m0 / 64) * n_tok64 * 64 + kk;
+              tg_load<CG>(sa, &P.A, bar, 0, row0);
+              tg_load<CG>(sa + 8192, &P.A, bar, 0, row0 + n_tok64 * 64);
+            } else {  // rows k, columns m
               tg_load<CG>(sa, &P.A, bar, m0, kk);
               tg_load<CG>(sa + 8192, &P.A, bar, m0 + 64, kk);
             }

@@ -517,9 +517,9 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   Q = P;
   Q.blocked = 1;
   if (!make_map_bf16(&Q.A, ws + L.boxes, 64, box_rows, 64, 64) ||
+      !make_map_bf16(&Q.A1, ws + L.boxes, 64, box_rows, 64, 128) ||
       !make_map_bf16(&Q.B, a.Xc, d, M, 64, 64) || !make_map_bf16(&Q.B1, W, d, V, 64, 64))
     return 2;
-  Q.A1 = Q.A;
   Q.idx = kCompact ? a.idx : nullptr;
   Q.D0 = static_cast<__nv_bfloat16 *>(dW);
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
@@ -554,9 +554,9 @@ int gau_project_backward_cg(const void *X, const void *Wt, const void *dU, const
   Q = P;
   Q.blocked = 1;
   if (!make_map_bf16(&Q.A, ws + L.boxes, 64, box_rows, 64, 64) ||
+      !make_map_bf16(&Q.A1, ws + L.boxes, 64, box_rows, 64, 128) ||
       !make_map_bf16(&Q.B, X, d, M, 64, 64) || !make_map_bf16(&Q.B1, Wt, d, N, 64, 64))
     return 2;
-  Q.A1 = Q.A;
   Q.D0 = static_cast<__nv_bfloat16 *>(dWt);
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
   Q.slots = reinterpret_cast<float *>(ws + L.slots);
@@ -572,10 +572,10 @@ int gau_output_backward_cg(const void *Y, const void *Wo_t, const void *dOut, vo
   char *ws = static_cast<char *>(workspace);
   TgParams Q = {};
   // A = dOut [tokens][d], read by columns for dWo_t [d][e], by rows for dY
-  if (!make_map_bf16(&Q.A, dOut, d, M, 64, 64) || !make_map_bf16(&Q.B, Y, e, M, 64, 64) ||
+  if (!make_map_bf16(&Q.A, dOut, d, M, 64, 64) || !make_map_bf16(&Q.A1, dOut, d, M, 64, 128) ||
+      !make_map_bf16(&Q.B, Y, e, M, 64, 64) ||
       !make_map_bf16(&Q.B1, Wo_t, e, d, 64, 64))
     return 2;
-  Q.A1 = Q.A;
   Q.M = M, Q.N = d, Q.K = e;
   Q.D0 = static_cast<__nv_bfloat16 *>(dWo_t);
   Q.D1 = static_cast<__nv_bfloat16 *>(dY);
