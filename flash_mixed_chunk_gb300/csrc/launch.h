@@ -325,19 +325,21 @@ inline VocabLossLayout vocab_loss_layout(int M, int V, int d) {
   return L;
 }
 
-// Its gradients: the same compact rows with their lse and dloss, the boxes of
+// Its gradients: the same compact rows with their lse and dloss (and the
+// largest |dloss| of the blocks that prepare them), the boxes of
 // one piece of the vocabulary, the fp32 parts of cut tiles and, with several
 // pieces, dX's sums over them.  A piece's boxes fill kVocabPieceBytes at most,
 // or one 256-column tile of all rows where that is more.
 constexpr size_t kVocabPieceBytes = (size_t)256 << 20;
 struct VocabGradLayout {
-  size_t hdr, idx, tgt, lse, g, Xc, boxes, slots, sums, total;
+  size_t hdr, tops, idx, tgt, lse, g, Xc, boxes, slots, sums, total;
   int64_t cap_boxes;
 };
 inline VocabGradLayout vocab_grad_layout(int M, int V, int d) {
   VocabGradLayout L;
   L.hdr = 0;
-  L.idx = 256;
+  L.tops = 256;
+  L.idx = L.tops + align256(4 * 2 * kTgMaxCtas);
   L.tgt = L.idx + align256(4 * (size_t)M);
   L.lse = L.tgt + align256(4 * (size_t)M);
   L.g = L.lse + align256(4 * (size_t)M);

@@ -53,8 +53,8 @@ struct TgCfg {
   static_assert(SMEM + 1024 <= 232448, "tc_tgemm exceeds 227 KB of shared memory");
 };
 
-// What the rows' preparation leaves on the device: the number of rows that
-// take part and the largest |dloss| among them (1 if that is not finite).
+// What stays on the device: the number of rows that take part (the rows'
+// preparation) and the largest |dloss| among them (TG_PROB; 1 if not finite).
 struct TgHeader {
   int count;
   float gmax;
@@ -101,6 +101,9 @@ struct TgParams {
   const __nv_bfloat16 *X;
   __nv_bfloat16 *Xz;
   int *keep;
+  // TG_PROB: the largest |dloss| of the rows' blocks, and where it goes
+  const float *tops;
+  int n_tops;
   float *gmax_out;
   // TG_LSE
   float2 *part;        // [2 ceil(N / 256)][M]
@@ -479,6 +482,14 @@ __host__ __device__ inline int64_t tg_slot_offset(int row, int j) {
 }
 constexpr int64_t kTgSlotFloats = 128 * 256;
 
+// The scale of dW and dX from a warp's largest |dloss| (1 for an infinite one,
+// which the other rows could not bear).
+__device__ __forceinline__ float tg_scale(float top) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return top == INFINITY ? 1.f : top;
+}
+
 // TG_PROB on rows as they are (128 at most): the largest |dloss| of those that
 // have a target, the same in every warp of the launch, and, shared between the
 // warps, what TG_GRAD needs: the rows' marks and X without the others' contents
@@ -490,9 +501,7 @@ __device__ __forceinline__ float tg_rows_as_they_are(const TgParams &P, int coun
     const int64_t t = P.target[r];
     if (t >= 0 && t < P.N) top = fmaxf(top, fabsf(P.g[r]));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (top == INFINITY) top = 1.f;  // no scale that the other rows could bear
+  top = tg_scale(top);
   if (w == 0 && lane == 0) *P.gmax_out = top;
   for (int r = w; r < count; r += W) {
     const int64_t t = P.target[r];
@@ -723,7 +732,9 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
     float gmax = 0.f;
     if constexpr (KIND == TG_PROB) {
       if (P.target == nullptr) {
-        gmax = *P.gmax;
+        for (int b = lane; b < P.n_tops; b += 32) gmax = fmaxf(gmax, P.tops[b]);
+        gmax = tg_scale(gmax);
+        if (blockIdx.x == 0 && warp == 2 && lane == 0) *P.gmax_out = gmax;
       } else {
         gmax = tg_rows_as_they_are(P, count, (int)blockIdx.x * TG_EPI_WARPS + warp - 2,
                                    (int)gridDim.x * TG_EPI_WARPS, lane);

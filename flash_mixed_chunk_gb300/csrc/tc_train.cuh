@@ -54,12 +54,14 @@ struct GatherArgs {
   float *loss, *lse_out;    // forward: 0 for rows without a target
   const float *lse, *dloss; // backward
   float *lse_c, *g_c;       // backward, compact
+  float *tops;              // backward: the blocks' largest |dloss|
   __nv_bfloat16 *dX;        // backward: rows without a target are 0
 };
 
 // Copies the rows that have a target next to each other, in order.  A block
-// takes `per` rows and counts the targets of all rows before its own by
-// itself: M / 256 loads a thread from L2 instead of a pass over the blocks.
+// takes `per` rows (an even number) and counts the targets of all rows before
+// its own by itself: M / 512 loads a thread from L2 instead of a pass over the
+// blocks.
 template <bool kBackward>
 __global__ void __launch_bounds__(kGatherThreads) vocab_gather(GatherArgs a) {
   __shared__ int red[kGatherThreads / 32];
@@ -71,9 +73,13 @@ __global__ void __launch_bounds__(kGatherThreads) vocab_gather(GatherArgs a) {
   const int64_t r1 = r0 + a.per < a.M ? r0 + a.per : a.M;
   int n = 0;
 #pragma unroll 8
-  for (int64_t m = tid; m < r0; m += kGatherThreads) n += has_target(a.target[m], a.V) ? 1 : 0;
+  for (int64_t m = 2 * tid; m < r0; m += 2 * kGatherThreads) {
+    const longlong2 t = *reinterpret_cast<const longlong2 *>(a.target + m);
+    n += (has_target(t.x, a.V) ? 1 : 0) + (has_target(t.y, a.V) ? 1 : 0);
+  }
   int base = block_sum(n, red);
   const int nv = a.d / 8;
+  float top = 0.f;
   for (int64_t m0 = r0; m0 < r1; m0 += kGatherThreads) {
     const int64_t m = m0 + tid;
     const int64_t t = m < r1 ? a.target[m] : -1;
@@ -93,8 +99,10 @@ __global__ void __launch_bounds__(kGatherThreads) vocab_gather(GatherArgs a) {
       a.idx[pos] = (int)m;
       a.tgt[pos] = (int)t;
       if constexpr (kBackward) {
+        const float g = a.dloss[m];
         a.lse_c[pos] = a.lse[m];
-        a.g_c[pos] = a.dloss[m];
+        a.g_c[pos] = g;
+        top = fmaxf(top, fabsf(g));
       }
     } else if (m < r1) {
       if constexpr (!kBackward) {
@@ -111,7 +119,15 @@ __global__ void __launch_bounds__(kGatherThreads) vocab_gather(GatherArgs a) {
       if (p >= 0) {
         const uint4 *src = reinterpret_cast<const uint4 *>(a.X + (m0 + r) * a.d);
         uint4 *dst = reinterpret_cast<uint4 *>(a.Xc + (int64_t)p * a.d);
-        for (int v = lane; v < nv; v += 32) dst[v] = __ldg(src + v);
+        for (int v = lane; v < nv; v += 128) {  // four loads on their way at once
+          uint4 x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (v + 32 * k < nv) x[k] = __ldg(src + v + 32 * k);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (v + 32 * k < nv) dst[v + 32 * k] = x[k];
+        }
       } else if constexpr (kBackward) {
         uint4 *dst = reinterpret_cast<uint4 *>(a.dX + (m0 + r) * a.d);
         for (int v = lane; v < nv; v += 32) dst[v] = make_uint4(0u, 0u, 0u, 0u);
@@ -127,30 +143,25 @@ __global__ void __launch_bounds__(kGatherThreads) vocab_gather(GatherArgs a) {
     uint4 *dst = reinterpret_cast<uint4 *>(a.Xc);
     for (int64_t v = (int64_t)count * nv + tid; v < end * nv; v += kGatherThreads)
       dst[v] = make_uint4(0u, 0u, 0u, 0u);
-    float top = 0.f;
-    if constexpr (kBackward) {
-#pragma unroll 4
-      for (int64_t m = tid; m < a.M; m += kGatherThreads)
-        if (has_target(a.target[m], a.V)) top = fmaxf(top, fabsf(a.dloss[m]));
+    if (tid == 0) a.hdr->count = count;
+  }
+  if constexpr (kBackward) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) redf[warp] = top;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kGatherThreads / 32; ++i) top = fmaxf(top, redf[i]);
-      if (top == INFINITY) top = 1.f;  // no scale that the other rows could bear
-    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) redf[warp] = top;
+    __syncthreads();
     if (tid == 0) {
-      a.hdr->count = count;
-      a.hdr->gmax = top;
+#pragma unroll
+      for (int i = 1; i < kGatherThreads / 32; ++i) top = fmaxf(top, redf[i]);
+      a.tops[blockIdx.x] = top;
     }
   }
 }
 
 // loss and lse of the rows from the products' partial maxima and sums: 32
-// rows a block, 16 lanes of parts each, joined in order.  The rows are compact
+// rows a block, 32 lanes of parts each, joined in order.  The rows are compact
 // (idx, hdr), or as they are (target; one without a target has loss and lse 0).
-constexpr int kReduceLanes = 16;
+constexpr int kReduceLanes = 32;
 __global__ void __launch_bounds__(32 * kReduceLanes)
     vocab_reduce(const float2 *__restrict__ part, const float *__restrict__ ztgt,
                  const int *__restrict__ idx, const TgHeader *__restrict__ hdr,
@@ -439,7 +450,7 @@ int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *lo
   constexpr bool kCompact = CG == 2;
   if (kCompact) {
     const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
-    a.per = (M + blocks - 1) / blocks;
+    a.per = ((M + blocks - 1) / blocks + 1) / 2 * 2;
     vocab_gather<false><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return 1;
   }
@@ -487,11 +498,12 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   a.lse = lse, a.dloss = dloss;
   a.lse_c = reinterpret_cast<float *>(ws + L.lse);
   a.g_c = reinterpret_cast<float *>(ws + L.g);
+  a.tops = reinterpret_cast<float *>(ws + L.tops);
   a.dX = static_cast<__nv_bfloat16 *>(dX);
   constexpr bool kCompact = CG == 2;
   if (kCompact) {
     const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
-    a.per = (M + blocks - 1) / blocks;
+    a.per = ((M + blocks - 1) / blocks + 1) / 2 * 2;
     vocab_gather<true><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return 1;
   }
@@ -501,6 +513,9 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   P.M = M, P.N = V, P.K = d;
   P.cap_boxes = L.cap_boxes;
   P.gmax = &a.hdr->gmax;
+  P.gmax_out = &a.hdr->gmax;
+  P.tops = a.tops;
+  P.n_tops = kCompact ? (M + a.per - 1) / a.per : 0;
   if (kCompact) {
     P.hdr = a.hdr;
     P.tgt = a.tgt;
@@ -510,7 +525,6 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
     P.lse = lse, P.g = dloss;
     P.X = a.X, P.Xz = a.Xc;
     P.keep = a.idx;
-    P.gmax_out = &a.hdr->gmax;
   }
   const uint64_t box_rows = (uint64_t)L.cap_boxes * 64;
   if (!make_map_bf16(&P.S, ws + L.boxes, 64, box_rows, 64, 32)) return 2;
