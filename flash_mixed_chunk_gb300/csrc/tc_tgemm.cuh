@@ -519,6 +519,13 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
     tc_tgemm(const __grid_constant__ TgParams P) {
   using Cfg = TgCfg<CG, KIND>;
   constexpr int RING = Cfg::RING;
+  // With few of the rows taking part the pieces are wide and the last launches
+  // have none (every kernel ahead has waited for the one that counts).
+  if ((KIND == TG_PROB || KIND == TG_GRAD) && P.hdr != nullptr && P.piece > 0 &&
+      P.piece >= tg_pieces(tg_count(P.hdr), P.N, P.cap_boxes).np) {
+    griddep_wait();
+    return;
+  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));

@@ -271,6 +271,11 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ int2 warp_s[kJoinThreads / 32];
   __shared__ int list_s[kTgMaxCtas], list_a[kTgMaxCtas], list_b[kTgMaxCtas], list_n;
   // launched by a TG_GRAD that had waited for what wrote the header
+  if (P.hdr != nullptr && P.piece > 0 && last == 0 &&
+      P.piece >= tg_pieces(tg_count(P.hdr), P.N, P.cap_boxes).np) {
+    griddep_wait();
+    return;
+  }
   if (threadIdx.x == 0)
     plan = tg_plan<CG, TG_GRAD>(P, P.piece, P.hdr != nullptr ? tg_count(P.hdr) : P.M, workers);
   __syncthreads();
