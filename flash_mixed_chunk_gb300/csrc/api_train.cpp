@@ -87,7 +87,7 @@ fmca_status flash_mca_layer_norm(const void *x, const void *res, const float *we
   if (dtype != FMCA_F32 && dtype != FMCA_BF16) return FMCA_ERR_INVALID_ARG;
   if (!x || !weight || !bias || !y || (res && !h)) return FMCA_ERR_INVALID_ARG;
   if (!std::isfinite(eps) || eps < 0.0f) return FMCA_ERR_INVALID_ARG;
-  if (!aligned({x, res, weight, bias, y, mean, rstd}, 16)) return FMCA_ERR_ALIGN;
+  if (!aligned({x, res, weight, bias, y}, 16) || !aligned({mean, rstd}, 4)) return FMCA_ERR_ALIGN;
   const size_t rows = (size_t)M * d * (dtype == FMCA_BF16 ? 2 : 4);
   const size_t wb = sizeof(float) * (size_t)d, sb = sizeof(float) * (size_t)M;
   void *const hh = res ? h : nullptr;  // without a residual branch h is not touched
@@ -120,7 +120,8 @@ fmca_status flash_mca_layer_norm_backward(const void *dy, const void *h, const f
   if (dtype != FMCA_F32 && dtype != FMCA_BF16) return FMCA_ERR_INVALID_ARG;
   if (!dy || !h || !weight || !mean || !rstd || !dx || !dweight || !dbias)
     return FMCA_ERR_INVALID_ARG;
-  if (!aligned({dy, h, weight, mean, rstd, dh, dx, dweight, dbias}, 16)) return FMCA_ERR_ALIGN;
+  if (!aligned({dy, h, weight, dh, dx, dweight, dbias}, 16) || !aligned({mean, rstd}, 4))
+    return FMCA_ERR_ALIGN;
   if (!workspace || workspace_bytes_ < norm_backward_bytes(M, d)) return FMCA_ERR_WORKSPACE;
   if (!aligned({workspace}, 256)) return FMCA_ERR_ALIGN;
   const size_t rows = (size_t)M * d * (dtype == FMCA_BF16 ? 2 : 4);
@@ -188,7 +189,8 @@ fmca_status flash_mca_vocab_loss(const void *X, const void *W, const int64_t *ta
   fmca_status st = vocab_sizes(M, V, d);
   if (st != FMCA_OK) return st;
   if (!X || !W || !target || !loss || !lse) return FMCA_ERR_INVALID_ARG;
-  if (!aligned({X, W, target, loss, lse}, 16)) return FMCA_ERR_ALIGN;
+  if (!aligned({X, W}, 16) || !aligned({target}, 8) || !aligned({loss, lse}, 4))
+    return FMCA_ERR_ALIGN;
   st = check_workspace(workspace, workspace_bytes_, vocab_loss_layout(M, V, d).total);
   if (st != FMCA_OK) return st;
   const size_t xb = 2 * (size_t)M * d, wb = 2 * (size_t)V * d, rb = 4 * (size_t)M;
@@ -210,7 +212,8 @@ fmca_status flash_mca_vocab_loss_backward(const void *X, const void *W, const in
   fmca_status st = vocab_sizes(M, V, d);
   if (st != FMCA_OK) return st;
   if (!X || !W || !target || !lse || !dloss || !dX || !dW) return FMCA_ERR_INVALID_ARG;
-  if (!aligned({X, W, target, lse, dloss, dX, dW}, 16)) return FMCA_ERR_ALIGN;
+  if (!aligned({X, W, dX, dW}, 16) || !aligned({target}, 8) || !aligned({lse, dloss}, 4))
+    return FMCA_ERR_ALIGN;
   st = check_workspace(workspace, workspace_bytes_, vocab_grad_layout(M, V, d).total);
   if (st != FMCA_OK) return st;
   const size_t xb = 2 * (size_t)M * d, wb = 2 * (size_t)V * d, rb = 4 * (size_t)M;

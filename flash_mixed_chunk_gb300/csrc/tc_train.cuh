@@ -72,10 +72,15 @@ __global__ void __launch_bounds__(kGatherThreads) vocab_gather(GatherArgs a) {
   const int64_t r0 = (int64_t)blockIdx.x * a.per;
   const int64_t r1 = r0 + a.per < a.M ? r0 + a.per : a.M;
   int n = 0;
+  if ((reinterpret_cast<uintptr_t>(a.target) & 15u) == 0) {
 #pragma unroll 8
-  for (int64_t m = 2 * tid; m < r0; m += 2 * kGatherThreads) {
-    const longlong2 t = *reinterpret_cast<const longlong2 *>(a.target + m);
-    n += (has_target(t.x, a.V) ? 1 : 0) + (has_target(t.y, a.V) ? 1 : 0);
+    for (int64_t m = 2 * tid; m < r0; m += 2 * kGatherThreads) {
+      const longlong2 t = *reinterpret_cast<const longlong2 *>(a.target + m);
+      n += (has_target(t.x, a.V) ? 1 : 0) + (has_target(t.y, a.V) ? 1 : 0);
+    }
+  } else {  // labels shifted by one token
+#pragma unroll 8
+    for (int64_t m = tid; m < r0; m += kGatherThreads) n += has_target(a.target[m], a.V) ? 1 : 0;
   }
   int base = block_sum(n, red);
   const int nv = a.d / 8;

@@ -376,9 +376,9 @@ fmca_status flash_mca_gau_output(const void *Y, const void *Wo_t, void *Out, int
  *       elements (the variance divided by d), rstd = 1 / sqrt(variance + eps)
  *   x, res, h, y   device arrays [M][d] of `dtype`, 16-byte aligned; res may
  *                  be NULL, and h then is not written and may be NULL
- *   weight, bias   device float32 [d]
- *   mean, rstd     device float32 [M] outputs, each NULL when not wanted (the
- *                  backward pass reads both)
+ *   weight, bias   device float32 [d], 16-byte aligned
+ *   mean, rstd     device float32 [M] outputs (4-byte aligned), each NULL when
+ *                  not wanted (the backward pass reads both)
  * h may be x or res itself (the residual stream updated in place); no other
  * output may overlap an input or another output.  fp32 arithmetic; the
  * statistics are those of the stored h.  One launch, nothing allocated, any
@@ -445,10 +445,12 @@ fmca_status flash_mca_gau_output_backward(const void *Y, const void *Wo_t, const
  * what its X holds, NaN included, reaches no output.  No reduction is applied:
  * dloss [M] of the backward pass carries it (1 / number of targets for their
  * mean).
- *   X, W          device bf16, 16-byte aligned; target: device int64 [M]
- *   loss, lse     device float32 [M] outputs, both needed
+ *   X, W          device bf16, 16-byte aligned; target: device int64 [M], 8-byte
+ *                 aligned (labels shifted by a token are)
+ *   loss, lse     device float32 [M] outputs, 4-byte aligned, both needed
  * The backward pass gives the gradients of sum(loss * dloss):
- *   dX [M][d], dW [V][d]  bf16 outputs (overwritten; dX is 0 for ignored rows)
+ *   dX [M][d], dW [V][d]  bf16 outputs, 16-byte aligned (overwritten; dX is 0
+ *                 for ignored rows)
  *   lse           as the forward call left it, for the same X, W and target
  *   dloss         float32 [M]; not read for ignored rows
  * It forms the logits again, a piece of the vocabulary at a time: the piece's

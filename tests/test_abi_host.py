@@ -406,8 +406,9 @@ def test_layer_norm_rejects_before_queueing():
     assert fwd(M=4, eps=float("nan")) == fm.FMCA_ERR_INVALID_ARG
     for k in ("x", "w", "b", "y", "h"):                          # h: needed with a residual
         assert fwd(M=4, **{k: None}) == fm.FMCA_ERR_INVALID_ARG
-    for k, v in (("x", x), ("r", r), ("w", w), ("b", b), ("h", h), ("y", y), ("mn", mn)):
+    for k, v in (("x", x), ("r", r), ("w", w), ("b", b), ("h", h), ("y", y)):
         assert fwd(M=4, **{k: v + 8}) == fm.FMCA_ERR_ALIGN
+    assert fwd(M=4, mn=mn + 2) == fm.FMCA_ERR_ALIGN and fwd(M=4, rs=rs + 1) == fm.FMCA_ERR_ALIGN
     for k, v in (("y", x), ("y", r), ("y", h), ("h", x + 128), ("h", r - 128), ("h", w), ("mn", rs),
                  ("rs", y)):
         assert fwd(M=4, **{k: v}) == fm.FMCA_ERR_INVALID_ARG     # overlaps
@@ -515,7 +516,8 @@ def test_vocab_loss_rejects_before_queueing():
                      (bwd, ("X", "W", "t", "lse", "g", "dX", "dW"))):
         for k in names:
             assert f(**{k: None}) == fm.FMCA_ERR_INVALID_ARG
-            assert f(**{k: P + (99 << 28) + 8}) == fm.FMCA_ERR_ALIGN
+            off = 4 if k == "t" else 2 if k in ("loss", "lse", "g") else 8
+            assert f(**{k: P + (99 << 28) + off}) == fm.FMCA_ERR_ALIGN
         assert f(M=0) == fm.FMCA_ERR_INVALID_ARG and f(V=-5) == fm.FMCA_ERR_INVALID_ARG
         assert f(d=60) == fm.FMCA_ERR_UNSUPPORTED and f(M=1 << 26) == fm.FMCA_ERR_UNSUPPORTED
         assert f(ws=None) == fm.FMCA_ERR_WORKSPACE and f(size=255) == fm.FMCA_ERR_WORKSPACE

@@ -302,3 +302,18 @@ def test_nan_in_the_vocabulary_leaves_ignored_rows_zero(M):
     out = (t < 0) | (t >= 3000)
     assert (loss[out] == 0).all() and (lse[out] == 0).all() and (dX[out] == 0).all()
     assert torch.isnan(loss[~out]).all() and torch.isnan(dX[~out]).all()
+
+
+@pytest.mark.parametrize("M", [5000, 100])
+def test_shifted_labels(M):
+    """The next token's label for each token: target, dloss and lse start where
+    only their own type is aligned."""
+    m = fm()
+    X, W, t, dloss = make(M, 300, 64, 0.7, 97)
+    ref = run(m, X, W, t, dloss)
+    pad = lambda v: torch.cat([v[:1], v])[1:]  # noqa: E731
+    t1, g1, l1 = pad(t), pad(dloss), pad(ref[1])
+    assert t1.data_ptr() % 16 == 8 and g1.data_ptr() % 16 == 4
+    loss, lse = m.vocab_loss(X, W, t1)
+    got = (loss, lse) + m.vocab_loss_backward(X, W, t1, l1, g1)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
