@@ -252,8 +252,16 @@ struct TgWalk {
   bool out = false;
   TgCut c;       // TG_GRAD: where the next part begins
   int end;
-  __host__ __device__ TgWalk(const TgPlan &plan, int w, int workers)
-      : p(plan), W(workers), pi(0), u(w), lane(0) {
+  __host__ __device__ TgWalk(const TgPlan &plan, int w, int workers) : p(plan) {
+    start(w, workers);
+  }
+  // (one that is started later)
+  __host__ __device__ explicit TgWalk(const TgPlan &plan) : p(plan) {}
+  __host__ __device__ void start(int w, int workers) {
+    W = workers;
+    pi = 0;
+    u = w;
+    lane = 0;
     if (KIND == TG_GRAD) {
       W = p.groups;
       u = w / p.side;
@@ -570,11 +578,22 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
   tg_sync_all<CG>();
   tc_fence_after();
   const uint32_t tbase = tmem_base;
+  // every warp walks the units by itself; the first one is found ahead of the
+  // grid wait where the plan was made there
+  TgWalk<KIND> walk(plan);
+  TgUnit ahead;
+  bool more = false;
+  if (early) {
+    walk.start(worker, workers);
+    more = walk.next(ahead);
+  }
   griddep_wait();
   griddep_launch_dependents();
   if (!early) {
     if (threadIdx.x == 96) plan = tg_plan<CG, KIND>(P, P.piece, tg_count(P.hdr), workers);
     __syncthreads();
+    walk.start(worker, workers);
+    more = walk.next(ahead);
   }
   const int count = plan.count, col0 = plan.col0, n_tok64 = plan.pc.n_tok64;
 
@@ -583,9 +602,8 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
     if (lane == 0) {
       int it = 0;
       bool ok = true;
-      TgUnit u;
-      TgWalk<KIND> walk(plan, worker, workers);
-      while (ok && walk.next(u)) {
+      for (TgUnit u; ok && more; more = walk.next(ahead)) {
+        u = ahead;
         const int m0 = u.mt * 128 * CG + (int)rank * 128;
         const int nb0 = u.nt * 256 + (int)rank * 128;
         for (int ks = 0; ks < u.nks; ++ks, ++it) {
@@ -647,9 +665,9 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       int it = 0;
       bool ok = true;
       TgUnit u;
-      TgWalk<KIND> walk(plan, worker, workers);
       int i = 0;
-      for (; ok && walk.next(u); ++i) {
+      for (; ok && more; ++i, more = walk.next(ahead)) {
+        u = ahead;
         const int buf = i & 1, use = i >> 1;
         if (use >= 1 && !tg_wait_pair<CG>(&acc_empty[buf], (use - 1) & 1, kWaitLimitNs)) {
           record_timeout(1011);
@@ -698,9 +716,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
     const int quad = warp & 3, half = (warp - 2) / 4;
     const int row = quad * 32 + lane;
     uint8_t *stage = smem + RING * Cfg::SLOT + (warp - 2) * 2 * Cfg::PIECE;
-    TgUnit u, ahead;
-    TgWalk<KIND> walk(plan, worker, workers);
-    bool more = walk.next(ahead);
+    TgUnit u;
     // TG_SILU: the incoming gradients of this warp's rows and 64 columns (piece
     // q) of a unit, into the piece that it then works on in place
     uint64_t *up = up_full + 2 * (warp - 2);
@@ -737,6 +753,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       __syncwarp();
     };
     float gmax = 0.f;
+    const float alpha = KIND == TG_GRAD && P.gmax != nullptr ? *P.gmax : 1.f;
     if constexpr (KIND == TG_PROB) {
       if (P.target == nullptr) {
         for (int b = lane; b < P.n_tops; b += 32) gmax = fmaxf(gmax, P.tops[b]);
@@ -785,6 +802,19 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
         if (in_rows) {
           row_lse = P.lse[m] * kLog2e;
           row_g = P.g[m];
+        }
+      }
+      // TG_GRAD: where the row goes
+      bool live = true;  // dX of a row without a target is 0, whatever W holds
+      __nv_bfloat16 *out = nullptr;
+      if constexpr (KIND == TG_GRAD) {
+        if (m < plan.s[u.pi].M) {
+          if (u.pi) {
+            if (P.keep != nullptr) live = P.keep[m] != 0;
+            out = P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K;
+          } else {
+            out = P.D0 + (int64_t)(col0 + m) * P.K;
+          }
         }
       }
       if (!mbar_wait(&acc_full[buf], use & 1, kWaitLimitNs)) {
@@ -853,21 +883,13 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
         const bool last = !P.blocked || u.pi == 0 || P.piece == plan.pc.np - 1;
         const bool direct = u.whole && last;
         const bool add = u.pi == 1 && P.blocked && P.piece > 0;
-        const bool in = m < h.M;
         float *slot = nullptr;
-        __nv_bfloat16 *out = nullptr;
-        float alpha = 1.f;
-        bool wide = false, live = true;  // dX of a row without a target is 0, whatever W holds
+        bool wide = false;
         if constexpr (KIND == TG_GRAD) {
           slot = u.whole ? P.sums + ((int64_t)(u.mt * CG + (int)rank) * h.Nt + u.nt) * kTgSlotFloats
                          : P.slots + (int64_t)((2 * worker + (u.ks0 > 0 ? 0 : 1)) * CG + (int)rank) *
                                          kTgSlotFloats;
-          if (P.gmax != nullptr) alpha = *P.gmax;
-          live = u.pi == 0 || P.keep == nullptr || (in && P.keep[m] != 0);
           wide = P.K % 16 == 0 && (reinterpret_cast<uintptr_t>(u.pi ? P.D1 : P.D0) & 31u) == 0;
-          if (direct && in)
-            out = u.pi ? P.D1 + (int64_t)(P.idx != nullptr ? P.idx[m] : m) * P.K
-                       : P.D0 + (int64_t)(col0 + m) * P.K;
         }
         bool ok = true;
 #pragma unroll
@@ -951,7 +973,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
                 for (int j = 0; j < 8; ++j)
                   *reinterpret_cast<float4 *>(slot + tg_slot_offset(row, half * 32 + c * 8 + j)) =
                       make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-              } else if (in) {
+              } else if (out != nullptr) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                   uint32_t w[8];

@@ -393,13 +393,18 @@ int launch_tgemm_kind(const TgParams &P, int workers, cudaStream_t stream) {
 }
 
 // Workers of a launch: all that are resident at once, no more than there are
-// units with every row taking part.
+// units (parts of 8 k steps) with every row taking part.
 template <int CG, int KIND>
 int tg_workers(const TgParams &P) {
   int w = tg_resident<CG, KIND>();
-  if (KIND != TG_GRAD && w > 0) {
+  if (w > 0) {
     const TgPlan p = tg_plan<CG, KIND>(P, P.piece, P.M, w);
-    if (p.s[0].tiles < w) w = p.s[0].tiles;
+    int64_t units = p.s[0].tiles;
+    if (KIND == TG_GRAD) {
+      units = 0;
+      for (const TgShape &h : p.s) units += (int64_t)h.tiles * (h.ks < 16 ? 1 : h.ks / 8);
+    }
+    if (units < w) w = (int)units;
   }
   return w;
 }
