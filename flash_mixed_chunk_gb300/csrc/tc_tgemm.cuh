@@ -498,13 +498,14 @@ __device__ __forceinline__ float tg_scale(float top) {
   return top == INFINITY ? 1.f : top;
 }
 
-// TG_PROB on rows as they are (128 at most): the largest |dloss| of those that
+// TG_PROB on rows as they are (512 at most): the largest |dloss| of those that
 // have a target, the same in every warp of the launch, and, shared between the
 // warps, what TG_GRAD needs: the rows' marks and X without the others' contents
 // (0 times NaN would be NaN).
 __device__ __forceinline__ float tg_rows_as_they_are(const TgParams &P, int count, int w, int W,
                                                      int lane) {
   float top = 0.f;
+#pragma unroll 4
   for (int r = lane; r < count; r += 32) {
     const int64_t t = P.target[r];
     if (t >= 0 && t < P.N) top = fmaxf(top, fabsf(P.g[r]));

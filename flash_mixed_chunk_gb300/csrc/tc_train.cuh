@@ -9,9 +9,8 @@
 // The rows with a target are copied next to each other first (vocab_gather),
 // so that a row without one costs nothing in the products and whatever its X
 // holds (NaN included) reaches nothing.  The number of such rows stays on the
-// device; every kernel reads it there, so the calls can be captured.  Up to 128
-// rows, one tile, there is nothing to save: they are taken as they are, a
-// launch fewer in either direction.
+// device; every kernel reads it there, so the calls can be captured.  Few rows
+// are taken as they are (vocab_compact), a launch fewer in either direction.
 //
 // The forward pass keeps, per row and 128 columns, the maximum and the sum of
 // exp(z - maximum), 1/32 of the logits' bytes at bf16; vocab_reduce
@@ -438,6 +437,14 @@ int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
              : 1;
 }
 
+// Whether the vocabulary loss makes its rows compact.  Not up to 128 rows (one
+// tile in any case), nor up to 512 while all of them cost less in the products
+// (8 GFLOP, 5 us) than the launch that would sort them out: 455 rows against
+// 2245 x 680 take 40 us forward and backward as they are, 51 compact.
+bool vocab_compact(int M, int V, int d) {
+  return M > 512 || (M > 128 && 2.0 * M * V * d > 8e9);
+}
+
 // CTA pairs for more rows than one CTA's tile has; up to 128 rows (a short
 // fine-tuning batch, a few tokens) half of a pair's tile would stay empty.
 bool tg_pairs(int M) { return M > 128; }
@@ -462,8 +469,8 @@ int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *lo
   a.tgt = reinterpret_cast<int *>(ws + L.tgt);
   a.hdr = reinterpret_cast<TgHeader *>(ws + L.hdr);
   a.loss = loss, a.lse_out = lse;
-  constexpr bool kCompact = CG == 2;
-  if (kCompact) {
+  const bool compact = vocab_compact(M, V, d);
+  if (compact) {
     const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
     a.per = ((M + blocks - 1) / blocks + 1) / 2 * 2;
     vocab_gather<false><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
@@ -471,10 +478,10 @@ int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *lo
   }
 
   TgParams P = {};
-  if (!nt_maps<CG>(P, kCompact ? a.Xc : a.X, W, M, V, d)) return 2;
+  if (!nt_maps<CG>(P, compact ? a.Xc : a.X, W, M, V, d)) return 2;
   P.M = M, P.N = V, P.K = d;
-  P.hdr = kCompact ? a.hdr : nullptr;
-  P.target = kCompact ? nullptr : target;
+  P.hdr = compact ? a.hdr : nullptr;
+  P.target = compact ? nullptr : target;
   P.part = reinterpret_cast<float2 *>(ws + L.part);
   P.ztgt = reinterpret_cast<float *>(ws + L.ztgt);
   P.tgt = a.tgt;
@@ -515,8 +522,8 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   a.g_c = reinterpret_cast<float *>(ws + L.g);
   a.tops = reinterpret_cast<float *>(ws + L.tops);
   a.dX = static_cast<__nv_bfloat16 *>(dX);
-  constexpr bool kCompact = CG == 2;
-  if (kCompact) {
+  const bool compact = vocab_compact(M, V, d);
+  if (compact) {
     const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
     a.per = ((M + blocks - 1) / blocks + 1) / 2 * 2;
     vocab_gather<true><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
@@ -524,14 +531,14 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   }
 
   TgParams P = {}, Q = {};
-  if (!nt_maps<CG>(P, kCompact ? a.Xc : a.X, W, M, V, d)) return 2;
+  if (!nt_maps<CG>(P, compact ? a.Xc : a.X, W, M, V, d)) return 2;
   P.M = M, P.N = V, P.K = d;
   P.cap_boxes = L.cap_boxes;
   P.gmax = &a.hdr->gmax;
   P.gmax_out = &a.hdr->gmax;
   P.tops = a.tops;
-  P.n_tops = kCompact ? (M + a.per - 1) / a.per : 0;
-  if (kCompact) {
+  P.n_tops = compact ? (M + a.per - 1) / a.per : 0;
+  if (compact) {
     P.hdr = a.hdr;
     P.tgt = a.tgt;
     P.lse = a.lse_c, P.g = a.g_c;
@@ -549,7 +556,7 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
       !make_map_bf16(&Q.A1, ws + L.boxes, 64, box_rows, 64, 128) ||
       !make_map_bf16(&Q.B, a.Xc, d, M, 64, 64) || !make_map_bf16(&Q.B1, W, d, V, 64, 64))
     return 2;
-  Q.idx = kCompact ? a.idx : nullptr;
+  Q.idx = compact ? a.idx : nullptr;
   Q.D0 = static_cast<__nv_bfloat16 *>(dW);
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
   Q.sums = reinterpret_cast<float *>(ws + L.sums);

@@ -208,3 +208,20 @@ def test_refusals():
                 lambda: m.flash_mca_layer_norm(x, None, w, b, None, x, None, None)):  # y is x
         with pytest.raises(m.FmcaError):
             bad()
+
+
+def test_outputs_are_tensors_of_their_own():
+    """What the wrappers return: fresh, contiguous, aligned, and apart from each
+    other (writing one leaves the rest)."""
+    m = fm()
+    x, res, w, b, dy, dh = cuda(*make(7, 65, F32, 9, True))
+    y, h, mean, rstd = m.layer_norm(x, w, b, residual=res)
+    dx, dw, db = m.layer_norm_backward(dy, h, w, mean, rstd, dh)
+    outs = [y, h, mean, rstd, dx, dw, db]
+    assert [tuple(t.shape) for t in outs] == [(7, 65), (7, 65), (7,), (7,), (7, 65), (65,), (65,)]
+    keep = [t.clone() for t in outs]
+    for i, t in enumerate(outs):
+        assert t.is_contiguous() and t.data_ptr() % 16 == 0 and not t.requires_grad
+        t.fill_(-1.0)
+        assert all(torch.equal(a, c) for a, c in zip(outs[i + 1:], keep[i + 1:]))
+        assert (t == -1.0).all()

@@ -90,7 +90,8 @@ def check(m, X, W, t, dloss):
 SIZES = [(1, 1, 8), (1, 2, 64), (2, 300, 64), (31, 256, 72), (33, 255, 64), (64, 257, 136),
          (65, 511, 256), (127, 1000, 64), (128, 513, 768), (129, 769, 520), (200, 128, 64),
          (256, 2048, 256), (257, 129, 1000), (37, 8191, 256), (5, 40001, 64), (3000, 100, 64),
-         (9000, 17, 96), (700, 5003, 200)]
+         (9000, 17, 96), (700, 5003, 200),
+         (512, 600, 64), (513, 600, 64), (400, 16000, 768)]  # the rows' two forms meet here
 
 
 @pytest.mark.parametrize("keep", [1.0, 0.3])
@@ -130,7 +131,7 @@ def test_sharp_and_flat_rows():
     check(m, X, W, t, dloss)
 
 
-@pytest.mark.parametrize("M", [300, 90])
+@pytest.mark.parametrize("M", [900, 300, 90])
 def test_rows_without_target_reach_nothing(M):
     """NaN and infinities in ignored rows of X, and in their dloss."""
     m = fm()
@@ -146,7 +147,7 @@ def test_rows_without_target_reach_nothing(M):
     assert (dirty[0][out] == 0).all() and (dirty[1][out] == 0).all() and (dirty[2][out] == 0).all()
 
 
-@pytest.mark.parametrize("M", [1, 64, 300])
+@pytest.mark.parametrize("M", [1, 64, 300, 1000])
 def test_no_row_has_a_target(M):
     m = fm()
     X, W, t, dloss = make(M, 500, 64, 1.0, 41)
@@ -156,7 +157,7 @@ def test_no_row_has_a_target(M):
         assert (a == 0).all()
 
 
-@pytest.mark.parametrize("M", [200, 100])
+@pytest.mark.parametrize("M", [600, 200, 100])
 def test_nan_stays_in_its_row_and_weights_of_zero(M):
     m = fm()
     X, W, t, dloss = make(M, 600, 64, 1.0, 51)
@@ -177,7 +178,7 @@ def test_nan_stays_in_its_row_and_weights_of_zero(M):
     assert torch.isfinite(dX[keep]).all() and not torch.isfinite(dX[5]).any()
 
 
-@pytest.mark.parametrize("M", [150, 128])
+@pytest.mark.parametrize("M", [600, 150, 128])
 def test_tiny_and_huge_weights_scale_the_gradients(M):
     """dloss times a power of two gives the gradients times it, bit for bit
     (no overflow or underflow in between)."""
@@ -216,7 +217,7 @@ def test_same_bits_again_on_streams_and_behind_the_last_row():
         assert torch.equal(a[:n], b) and (a[n:] == 3.0).all()
 
 
-@pytest.mark.parametrize("M", [500, 77])
+@pytest.mark.parametrize("M", [800, 500, 77])
 def test_captured_calls_follow_the_targets(M):
     """Two graphs over the same inputs; the targets change between replays, so
     that the number of rows that take part does."""
@@ -293,7 +294,7 @@ def test_refusals():
             bad()
 
 
-@pytest.mark.parametrize("M", [40, 300])
+@pytest.mark.parametrize("M", [40, 300, 700])
 def test_nan_in_the_vocabulary_leaves_ignored_rows_zero(M):
     m = fm()
     X, W, t, dloss = make(M, 3000, 64, 0.5, 95)
