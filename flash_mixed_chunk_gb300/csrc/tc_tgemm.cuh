@@ -132,12 +132,15 @@ struct TgPlan {
   TgPieces pc;
   TgShape s[2];
   int base1, total;         // TG_GRAD: where problem 1's cut panels begin, and end
+  bool apart;               // the panels left over are not cut: one a group
   int row_step;             // rows of a tile
   int side, groups;         // tiles of a panel, workers side by side on them
 };
 
 // A tile's epilogue beyond what the next tile's products hide, in k steps.
 constexpr int kTgEpilogue = 3;
+// The launch that joins the parts of cut tiles (5 us), in k steps.
+constexpr int kTgJoin = 14;
 
 template <int CG>
 __host__ __device__ inline TgShape tg_shape(int M_exist, int M, int N, int K, int K_full,
@@ -188,10 +191,15 @@ __host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int coun
     // fewer cut panels than workers, 2^22 steps each at most: 31 bits hold it
     p.base1 = p.s[0].cut * p.s[0].len;
     p.total = p.base1 + p.s[1].cut * p.s[1].len;
+    // no cuts where they would save less than joining the parts takes
+    const int len0 = p.s[0].cut ? p.s[0].len : 0, len1 = p.s[1].cut ? p.s[1].len : 0;
+    p.apart = p.s[0].cut + p.s[1].cut <= p.groups &&
+              (len0 > len1 ? len0 : len1) <= p.total / p.groups + kTgJoin;
   } else {
     p.s[0] = tg_shape<CG>(count, p.width > 0 ? count : 0, p.width, P.K, P.K, 1, workers);
     p.s[1] = p.s[0];
     p.base1 = p.total = 0;
+    p.apart = false;
   }
   return p;
 }
@@ -205,7 +213,7 @@ __host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int coun
 // tiles of 128 steps and 96 of 252 on 76 pairs: busy 84 % of the time).  The
 // tiles of a panel that a cut goes through are summed from their parts by a
 // second kernel; a part keeps 8 k steps at least, and panels of less than 16
-// are not cut.  Without panels (each worker on a tile of its own, cut at its
+// are not cut, nor any where that kernel costs more than the cuts save.  Without panels (each worker on a tile of its own, cut at its
 // own place) A came from DRAM once for every tile beside another: 171 us
 // instead of 142 at 2048 x 50001 x 512.  Where group w's part of the line begins:
 struct TgCut {
@@ -214,6 +222,15 @@ struct TgCut {
 };
 __host__ __device__ inline TgCut tg_cut(const TgPlan &p, int w, int W) {
   TgCut c;
+  if (p.apart) {
+    const int n0 = p.s[0].cut, n = n0 + p.s[1].cut;
+    if (w > n) w = n;
+    c.pi = w >= n0 ? 1 : 0;
+    c.tile = c.pi ? w - n0 : w;
+    c.off = 0;
+    c.pos = c.pi ? p.base1 + c.tile * p.s[1].len : w * p.s[0].len;
+    return c;
+  }
   const int b = w <= 0 ? 0 : w >= W ? p.total : w * (p.total / W) + w * (p.total % W) / W;
   c.pi = b >= p.base1 ? 1 : 0;
   const int len = c.pi ? p.s[1].len : p.s[0].len, ks = c.pi ? p.s[1].ks : p.s[0].ks;
