@@ -86,26 +86,60 @@ int size_of(const char *what, int64_t v) {
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Device &dev) {
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
-// Two float32 tensors of a shape in one allocation (they are small and go
-// together; an allocation and its release are 0.8 us), 16-byte aligned both.
-struct Pair {
-  at::Tensor a, b;
+// The tensors of one call.  While they are small together they are parts of one
+// allocation: an allocation and its release are 0.8 us, of a call of 5 for one
+// token, and what one result can hold back of the others' memory is small.  A
+// large one is an allocation of its own.
+class Results {
+ public:
+  explicit Results(const at::Device &dev) : dev_(dev) {}
+  int add(at::IntArrayRef shape, at::ScalarType type) {
+    Item &it = items_[n_];
+    it.shape = shape;
+    it.type = type;
+    it.at = total_;
+    total_ += (c10::multiply_integers(shape) * (int64_t)c10::elementSize(type) + 255) / 256 * 256;
+    return n_++;
+  }
+  // `bytes` as a ..._workspace_bytes function gave them
+  int add_workspace(size_t bytes, const char *what) {
+    if (bytes == 0) check(FMCA_ERR_UNSUPPORTED, what);
+    items_[n_].bytes = (int64_t)bytes;
+    return add(at::IntArrayRef(&items_[n_].bytes, 1), at::kByte);
+  }
+  void make() {
+    if (total_ > kShared) {
+      for (int i = 0; i < n_; ++i) t_[i] = ::make(items_[i].shape, items_[i].type, dev_);
+      return;
+    }
+    const at::Tensor all = ::make({total_}, at::kByte, dev_);
+    for (int i = 0; i < n_; ++i) {
+      t_[i] = at::detail::make_tensor<c10::TensorImpl>(
+          c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(items_[i].type));
+      t_[i].unsafeGetTensorImpl()->set_storage_offset(
+          items_[i].at / (int64_t)c10::elementSize(items_[i].type));
+      t_[i].unsafeGetTensorImpl()->set_sizes_contiguous(items_[i].shape);
+    }
+  }
+  const at::Tensor &operator[](int i) const { return t_[i]; }
+  template <typename T = void>
+  T *ptr(int i) const {
+    return static_cast<T *>(t_[i].data_ptr());
+  }
+
+ private:
+  static constexpr int64_t kShared = 256 << 10;
+  struct Item {
+    at::IntArrayRef shape;  // of an operand, or of `bytes`
+    int64_t bytes, at;
+    at::ScalarType type;
+  };
+  at::Device dev_;
+  Item items_[4];
+  at::Tensor t_[4];
+  int n_ = 0;
+  int64_t total_ = 0;
 };
-Pair make_pair(at::IntArrayRef shape, const at::Device &dev) {
-  const int64_t n = (c10::multiply_integers(shape) + 3) / 4 * 4;
-  Pair p;
-  p.a = make({2 * n}, at::kFloat, dev);
-  p.b = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(p.a.storage()), p.a.key_set(),
-                                                 p.a.dtype());
-  p.b.unsafeGetTensorImpl()->set_storage_offset(n);
-  p.b.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-  p.a.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-  return p;
-}
-at::Tensor workspace(size_t bytes, const char *what, const at::Device &dev) {
-  if (bytes == 0) check(FMCA_ERR_UNSUPPORTED, what);
-  return make({(int64_t)bytes}, at::kByte, dev);
-}
 fmca_stream_t stream_of(const at::Device &dev) {
   return reinterpret_cast<fmca_stream_t>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
 }
@@ -149,15 +183,16 @@ PyObject *layer_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const float *pb = (const float *)on("bias", a[2], at::kFloat, {d}, dev);
   const int M = size_of("the number of rows", x.numel() / d);
   c10::cuda::CUDAGuard guard(dev);
-  at::Tensor y = make(x.sizes(), type, dev), h = has ? make(x.sizes(), type, dev) : x;
-  const Pair stats = make_pair(rows, dev);
-  const at::Tensor &mean = stats.a, &rstd = stats.b;
-  check(flash_mca_layer_norm(px, pr, pw, pb, has ? h.data_ptr() : nullptr, y.data_ptr(),
-                             (float *)mean.data_ptr(), (float *)rstd.data_ptr(), M,
-                             size_of("d", d), (float)eps, dt, stream_of(dev)),
+  Results t(dev);
+  const int y = t.add(x.sizes(), type), mean = t.add(rows, at::kFloat);
+  const int rstd = t.add(rows, at::kFloat), h = has ? t.add(x.sizes(), type) : y;
+  t.make();
+  check(flash_mca_layer_norm(px, pr, pw, pb, has ? t.ptr(h) : nullptr, t.ptr(y), t.ptr<float>(mean),
+                             t.ptr<float>(rstd), M, size_of("d", d), (float)eps, dt,
+                             stream_of(dev)),
         "flash_mca_layer_norm");
-  if (has) return pack(y, h, mean, rstd);
-  PyObject *r = pack(y, y, mean, rstd);  // h is the caller's x itself
+  if (has) return pack(t[y], t[h], t[mean], t[rstd]);
+  PyObject *r = pack(t[y], t[y], t[mean], t[rstd]);  // h is the caller's x itself
   Py_DECREF(PyTuple_GET_ITEM(r, 1));
   Py_INCREF(a[0]);
   PyTuple_SET_ITEM(r, 1, a[0]);
@@ -185,16 +220,17 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const void *pd = a[5] != Py_None ? on("dh", a[5], type, dy.sizes(), dev) : nullptr;
   const int M = size_of("the number of rows", dy.numel() / d), di = size_of("d", d);
   c10::cuda::CUDAGuard guard(dev);
-  at::Tensor ws = workspace(flash_mca_layer_norm_backward_workspace_bytes(M, di),
-                            "flash_mca_layer_norm_backward_workspace_bytes", dev);
-  at::Tensor dx = make(dy.sizes(), type, dev);
-  const Pair sums = make_pair({d}, dev);
-  const at::Tensor &dw = sums.a, &db = sums.b;
-  check(flash_mca_layer_norm_backward(py, ph, pw, pm, pr, pd, dx.data_ptr(),
-                                      (float *)dw.data_ptr(), (float *)db.data_ptr(), M, di, dt,
-                                      ws.data_ptr(), (size_t)ws.numel(), stream_of(dev)),
+  Results t(dev);
+  const int ws = t.add_workspace(flash_mca_layer_norm_backward_workspace_bytes(M, di),
+                                 "flash_mca_layer_norm_backward_workspace_bytes");
+  const int64_t vec[1] = {d};
+  const int dx = t.add(dy.sizes(), type), dw = t.add(vec, at::kFloat), db = t.add(vec, at::kFloat);
+  t.make();
+  check(flash_mca_layer_norm_backward(py, ph, pw, pm, pr, pd, t.ptr(dx), t.ptr<float>(dw),
+                                      t.ptr<float>(db), M, di, dt, t.ptr(ws),
+                                      (size_t)t[ws].numel(), stream_of(dev)),
         "flash_mca_layer_norm_backward");
-  return pack(dx, dw, db);
+  return pack(t[dx], t[dw], t[db]);
   END_HANDLE_TH_ERRORS
 }
 
@@ -214,13 +250,16 @@ PyObject *gau_project_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const void *pz = on("dZ", a[4], bf, {M, s}, dev);
   const int Mi = size_of("M", M), di = size_of("d", d), ei = size_of("e", e), si = size_of("s", s);
   c10::cuda::CUDAGuard guard(dev);
-  at::Tensor ws = workspace(flash_mca_gau_project_backward_workspace_bytes(Mi, di, ei, si),
-                            "flash_mca_gau_project_backward_workspace_bytes", dev);
-  at::Tensor dX = make({M, d}, bf, dev), dWt = make({N, d}, bf, dev);
-  check(flash_mca_gau_project_backward(px, pw, pu, pv, pz, dX.data_ptr(), dWt.data_ptr(), Mi, di,
-                                       ei, si, ws.data_ptr(), (size_t)ws.numel(), stream_of(dev)),
+  const int64_t wshape[2] = {N, d};
+  Results t(dev);
+  const int ws = t.add_workspace(flash_mca_gau_project_backward_workspace_bytes(Mi, di, ei, si),
+                                 "flash_mca_gau_project_backward_workspace_bytes");
+  const int dX = t.add(X.sizes(), bf), dWt = t.add(wshape, bf);
+  t.make();
+  check(flash_mca_gau_project_backward(px, pw, pu, pv, pz, t.ptr(dX), t.ptr(dWt), Mi, di, ei, si,
+                                       t.ptr(ws), (size_t)t[ws].numel(), stream_of(dev)),
         "flash_mca_gau_project_backward");
-  return pack(dX, dWt);
+  return pack(t[dX], t[dWt]);
   END_HANDLE_TH_ERRORS
 }
 
@@ -237,13 +276,16 @@ PyObject *gau_output_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const void *po = on("dOut", a[2], bf, {M, d}, dev);
   const int Mi = size_of("M", M), ei = size_of("e", e), di = size_of("d", d);
   c10::cuda::CUDAGuard guard(dev);
-  at::Tensor ws = workspace(flash_mca_gau_output_backward_workspace_bytes(Mi, ei, di),
-                            "flash_mca_gau_output_backward_workspace_bytes", dev);
-  at::Tensor dY = make({M, e}, bf, dev), dW = make({d, e}, bf, dev);
-  check(flash_mca_gau_output_backward(py, pw, po, dY.data_ptr(), dW.data_ptr(), Mi, ei, di,
-                                      ws.data_ptr(), (size_t)ws.numel(), stream_of(dev)),
+  const int64_t wshape[2] = {d, e};
+  Results t(dev);
+  const int ws = t.add_workspace(flash_mca_gau_output_backward_workspace_bytes(Mi, ei, di),
+                                 "flash_mca_gau_output_backward_workspace_bytes");
+  const int dY = t.add(Y.sizes(), bf), dW = t.add(wshape, bf);
+  t.make();
+  check(flash_mca_gau_output_backward(py, pw, po, t.ptr(dY), t.ptr(dW), Mi, ei, di, t.ptr(ws),
+                                      (size_t)t[ws].numel(), stream_of(dev)),
         "flash_mca_gau_output_backward");
-  return pack(dY, dW);
+  return pack(t[dY], t[dW]);
   END_HANDLE_TH_ERRORS
 }
 
@@ -260,14 +302,16 @@ PyObject *vocab_loss(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int64_t *pt = (const int64_t *)on("target", a[2], at::kLong, {M}, dev);
   const int Mi = size_of("M", M), Vi = size_of("V", V), di = size_of("d", d);
   c10::cuda::CUDAGuard guard(dev);
-  at::Tensor ws = workspace(flash_mca_vocab_loss_workspace_bytes(Mi, Vi, di),
-                            "flash_mca_vocab_loss_workspace_bytes", dev);
-  const Pair out = make_pair({M}, dev);
-  const at::Tensor &loss = out.a, &lse = out.b;
-  check(flash_mca_vocab_loss(px, pw, pt, (float *)loss.data_ptr(), (float *)lse.data_ptr(), Mi, Vi,
-                             di, ws.data_ptr(), (size_t)ws.numel(), stream_of(dev)),
+  const int64_t rows[1] = {M};
+  Results t(dev);
+  const int ws = t.add_workspace(flash_mca_vocab_loss_workspace_bytes(Mi, Vi, di),
+                                 "flash_mca_vocab_loss_workspace_bytes");
+  const int loss = t.add(rows, at::kFloat), lse = t.add(rows, at::kFloat);
+  t.make();
+  check(flash_mca_vocab_loss(px, pw, pt, t.ptr<float>(loss), t.ptr<float>(lse), Mi, Vi, di,
+                             t.ptr(ws), (size_t)t[ws].numel(), stream_of(dev)),
         "flash_mca_vocab_loss");
-  return pack(loss, lse);
+  return pack(t[loss], t[lse]);
   END_HANDLE_TH_ERRORS
 }
 
@@ -286,13 +330,16 @@ PyObject *vocab_loss_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const float *pg = (const float *)on("dloss", a[4], at::kFloat, {M}, dev);
   const int Mi = size_of("M", M), Vi = size_of("V", V), di = size_of("d", d);
   c10::cuda::CUDAGuard guard(dev);
-  at::Tensor ws = workspace(flash_mca_vocab_loss_backward_workspace_bytes(Mi, Vi, di),
-                            "flash_mca_vocab_loss_backward_workspace_bytes", dev);
-  at::Tensor dX = make({M, d}, at::kBFloat16, dev), dW = make({V, d}, at::kBFloat16, dev);
-  check(flash_mca_vocab_loss_backward(px, pw, pt, pl, pg, dX.data_ptr(), dW.data_ptr(), Mi, Vi, di,
-                                      ws.data_ptr(), (size_t)ws.numel(), stream_of(dev)),
+  const int64_t wshape[2] = {V, d};
+  Results t(dev);
+  const int ws = t.add_workspace(flash_mca_vocab_loss_backward_workspace_bytes(Mi, Vi, di),
+                                 "flash_mca_vocab_loss_backward_workspace_bytes");
+  const int dX = t.add(X.sizes(), at::kBFloat16), dW = t.add(wshape, at::kBFloat16);
+  t.make();
+  check(flash_mca_vocab_loss_backward(px, pw, pt, pl, pg, t.ptr(dX), t.ptr(dW), Mi, Vi, di,
+                                      t.ptr(ws), (size_t)t[ws].numel(), stream_of(dev)),
         "flash_mca_vocab_loss_backward");
-  return pack(dX, dW);
+  return pack(t[dX], t[dW]);
   END_HANDLE_TH_ERRORS
 }
 
