@@ -86,10 +86,22 @@ int size_of(const char *what, int64_t v) {
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Device &dev) {
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
+// Other threads run while a call allocates (which may wait for the device) and
+// queues its kernels (which waits while the stream's queue is full).
+class WithoutGil {
+ public:
+  WithoutGil() : state_(PyEval_SaveThread()) {}
+  ~WithoutGil() { PyEval_RestoreThread(state_); }
+  WithoutGil(const WithoutGil &) = delete;
+
+ private:
+  PyThreadState *state_;
+};
 // The tensors of one call.  While they are small together they are parts of one
 // allocation: an allocation and its release are 0.8 us, of a call of 5 for one
-// token, and what one result can hold back of the others' memory is small.  A
-// large one is an allocation of its own.
+// token.  One result that is kept keeps the others' memory with it, which is of
+// its own order; a workspace of more than 16 KB, which no caller knows of, and
+// anything large are allocations of their own.
 class Results {
  public:
   explicit Results(const at::Device &dev) : dev_(dev) {}
@@ -97,29 +109,25 @@ class Results {
     Item &it = items_[n_];
     it.shape = shape;
     it.type = type;
-    it.at = total_;
-    total_ += (c10::multiply_integers(shape) * (int64_t)c10::elementSize(type) + 255) / 256 * 256;
+    place(it, c10::multiply_integers(shape) * (int64_t)c10::elementSize(type), kShared);
     return n_++;
   }
   // `bytes` as a ..._workspace_bytes function gave them
   int add_workspace(size_t bytes, const char *what) {
     if (bytes == 0) check(FMCA_ERR_UNSUPPORTED, what);
-    items_[n_].bytes = (int64_t)bytes;
-    return add(at::IntArrayRef(&items_[n_].bytes, 1), at::kByte);
+    Item &it = items_[n_];
+    it.bytes = (int64_t)bytes;
+    it.shape = at::IntArrayRef(&it.bytes, 1);
+    it.type = at::kByte;
+    place(it, it.bytes, kSharedWorkspace);
+    return n_++;
   }
-  void make() {
-    if (total_ > kShared) {
-      for (int i = 0; i < n_; ++i) t_[i] = ::make(items_[i].shape, items_[i].type, dev_);
-      return;
-    }
-    const at::Tensor all = ::make({total_}, at::kByte, dev_);
-    for (int i = 0; i < n_; ++i) {
-      t_[i] = at::detail::make_tensor<c10::TensorImpl>(
-          c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(items_[i].type));
-      t_[i].unsafeGetTensorImpl()->set_storage_offset(
-          items_[i].at / (int64_t)c10::elementSize(items_[i].type));
-      t_[i].unsafeGetTensorImpl()->set_sizes_contiguous(items_[i].shape);
-    }
+  // makes the tensors and queues the call that writes them
+  template <typename F>
+  fmca_status queue(const F &call) {
+    const WithoutGil other_threads_run;
+    make();
+    return call();
   }
   const at::Tensor &operator[](int i) const { return t_[i]; }
   template <typename T = void>
@@ -128,12 +136,33 @@ class Results {
   }
 
  private:
-  static constexpr int64_t kShared = 256 << 10;
+  void make() {
+    const bool shared = total_ > 0 && total_ <= kShared;
+    const at::Tensor all = shared ? ::make({total_}, at::kByte, dev_) : at::Tensor();
+    for (int i = 0; i < n_; ++i) {
+      if (!shared || items_[i].at < 0) {
+        t_[i] = ::make(items_[i].shape, items_[i].type, dev_);
+        continue;
+      }
+      t_[i] = at::detail::make_tensor<c10::TensorImpl>(
+          c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(items_[i].type));
+      t_[i].unsafeGetTensorImpl()->set_storage_offset(
+          items_[i].at / (int64_t)c10::elementSize(items_[i].type));
+      t_[i].unsafeGetTensorImpl()->set_sizes_contiguous(items_[i].shape);
+    }
+  }
+  static constexpr int64_t kShared = 256 << 10, kSharedWorkspace = 16 << 10;
   struct Item {
     at::IntArrayRef shape;  // of an operand, or of `bytes`
-    int64_t bytes, at;
+    int64_t bytes, at;      // at < 0: an allocation of its own
     at::ScalarType type;
   };
+  void place(Item &it, int64_t bytes, int64_t limit) {
+    it.at = -1;
+    if (bytes > limit) return;
+    it.at = total_;
+    total_ += (bytes + 255) / 256 * 256;
+  }
   at::Device dev_;
   Item items_[4];
   at::Tensor t_[4];
@@ -159,6 +188,11 @@ PyObject *pack(const T &...t) {
   if (r == nullptr) throw python_error();
   Py_ssize_t i = 0;
   (PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t)), ...);
+  for (i = 0; i < (Py_ssize_t)sizeof...(t); ++i)
+    if (PyTuple_GET_ITEM(r, i) == nullptr) {
+      Py_DECREF(r);
+      throw python_error();
+    }
   return r;
 }
 
@@ -181,15 +215,16 @@ PyObject *layer_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const void *pr = has ? on("residual", a[4], type, x.sizes(), dev) : nullptr;
   const float *pw = (const float *)on("weight", a[1], at::kFloat, {d}, dev);
   const float *pb = (const float *)on("bias", a[2], at::kFloat, {d}, dev);
-  const int M = size_of("the number of rows", x.numel() / d);
+  const int M = size_of("the number of rows", x.numel() / d), di = size_of("d", d);
   c10::cuda::CUDAGuard guard(dev);
   Results t(dev);
   const int y = t.add(x.sizes(), type), mean = t.add(rows, at::kFloat);
   const int rstd = t.add(rows, at::kFloat), h = has ? t.add(x.sizes(), type) : y;
-  t.make();
-  check(flash_mca_layer_norm(px, pr, pw, pb, has ? t.ptr(h) : nullptr, t.ptr(y), t.ptr<float>(mean),
-                             t.ptr<float>(rstd), M, size_of("d", d), (float)eps, dt,
-                             stream_of(dev)),
+  check(t.queue([&] {
+          return flash_mca_layer_norm(px, pr, pw, pb, has ? t.ptr(h) : nullptr, t.ptr(y),
+                                      t.ptr<float>(mean), t.ptr<float>(rstd), M, di, (float)eps,
+                                      dt, stream_of(dev));
+        }),
         "flash_mca_layer_norm");
   if (has) return pack(t[y], t[h], t[mean], t[rstd]);
   PyObject *r = pack(t[y], t[y], t[mean], t[rstd]);  // h is the caller's x itself
@@ -225,10 +260,11 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                  "flash_mca_layer_norm_backward_workspace_bytes");
   const int64_t vec[1] = {d};
   const int dx = t.add(dy.sizes(), type), dw = t.add(vec, at::kFloat), db = t.add(vec, at::kFloat);
-  t.make();
-  check(flash_mca_layer_norm_backward(py, ph, pw, pm, pr, pd, t.ptr(dx), t.ptr<float>(dw),
-                                      t.ptr<float>(db), M, di, dt, t.ptr(ws),
-                                      (size_t)t[ws].numel(), stream_of(dev)),
+  check(t.queue([&] {
+          return flash_mca_layer_norm_backward(py, ph, pw, pm, pr, pd, t.ptr(dx), t.ptr<float>(dw),
+                                               t.ptr<float>(db), M, di, dt, t.ptr(ws),
+                                               (size_t)t[ws].numel(), stream_of(dev));
+        }),
         "flash_mca_layer_norm_backward");
   return pack(t[dx], t[dw], t[db]);
   END_HANDLE_TH_ERRORS
@@ -255,9 +291,11 @@ PyObject *gau_project_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int ws = t.add_workspace(flash_mca_gau_project_backward_workspace_bytes(Mi, di, ei, si),
                                  "flash_mca_gau_project_backward_workspace_bytes");
   const int dX = t.add(X.sizes(), bf), dWt = t.add(wshape, bf);
-  t.make();
-  check(flash_mca_gau_project_backward(px, pw, pu, pv, pz, t.ptr(dX), t.ptr(dWt), Mi, di, ei, si,
-                                       t.ptr(ws), (size_t)t[ws].numel(), stream_of(dev)),
+  check(t.queue([&] {
+          return flash_mca_gau_project_backward(px, pw, pu, pv, pz, t.ptr(dX), t.ptr(dWt), Mi, di,
+                                                ei, si, t.ptr(ws), (size_t)t[ws].numel(),
+                                                stream_of(dev));
+        }),
         "flash_mca_gau_project_backward");
   return pack(t[dX], t[dWt]);
   END_HANDLE_TH_ERRORS
@@ -281,9 +319,10 @@ PyObject *gau_output_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int ws = t.add_workspace(flash_mca_gau_output_backward_workspace_bytes(Mi, ei, di),
                                  "flash_mca_gau_output_backward_workspace_bytes");
   const int dY = t.add(Y.sizes(), bf), dW = t.add(wshape, bf);
-  t.make();
-  check(flash_mca_gau_output_backward(py, pw, po, t.ptr(dY), t.ptr(dW), Mi, ei, di, t.ptr(ws),
-                                      (size_t)t[ws].numel(), stream_of(dev)),
+  check(t.queue([&] {
+          return flash_mca_gau_output_backward(py, pw, po, t.ptr(dY), t.ptr(dW), Mi, ei, di,
+                                               t.ptr(ws), (size_t)t[ws].numel(), stream_of(dev));
+        }),
         "flash_mca_gau_output_backward");
   return pack(t[dY], t[dW]);
   END_HANDLE_TH_ERRORS
@@ -307,9 +346,10 @@ PyObject *vocab_loss(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int ws = t.add_workspace(flash_mca_vocab_loss_workspace_bytes(Mi, Vi, di),
                                  "flash_mca_vocab_loss_workspace_bytes");
   const int loss = t.add(rows, at::kFloat), lse = t.add(rows, at::kFloat);
-  t.make();
-  check(flash_mca_vocab_loss(px, pw, pt, t.ptr<float>(loss), t.ptr<float>(lse), Mi, Vi, di,
-                             t.ptr(ws), (size_t)t[ws].numel(), stream_of(dev)),
+  check(t.queue([&] {
+          return flash_mca_vocab_loss(px, pw, pt, t.ptr<float>(loss), t.ptr<float>(lse), Mi, Vi, di,
+                                      t.ptr(ws), (size_t)t[ws].numel(), stream_of(dev));
+        }),
         "flash_mca_vocab_loss");
   return pack(t[loss], t[lse]);
   END_HANDLE_TH_ERRORS
@@ -335,9 +375,10 @@ PyObject *vocab_loss_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int ws = t.add_workspace(flash_mca_vocab_loss_backward_workspace_bytes(Mi, Vi, di),
                                  "flash_mca_vocab_loss_backward_workspace_bytes");
   const int dX = t.add(X.sizes(), at::kBFloat16), dW = t.add(wshape, at::kBFloat16);
-  t.make();
-  check(flash_mca_vocab_loss_backward(px, pw, pt, pl, pg, t.ptr(dX), t.ptr(dW), Mi, Vi, di,
-                                      t.ptr(ws), (size_t)t[ws].numel(), stream_of(dev)),
+  check(t.queue([&] {
+          return flash_mca_vocab_loss_backward(px, pw, pt, pl, pg, t.ptr(dX), t.ptr(dW), Mi, Vi, di,
+                                               t.ptr(ws), (size_t)t[ws].numel(), stream_of(dev));
+        }),
         "flash_mca_vocab_loss_backward");
   return pack(t[dX], t[dW]);
   END_HANDLE_TH_ERRORS

@@ -1,0 +1,102 @@
+"""The allocating wrappers of the training operators as calls: what their
+results keep alive, other Python threads, a process whose first calls are
+captured."""
+from __future__ import annotations
+
+import os
+import subprocess
+import sys
+import threading
+import time
+
+import pytest
+import torch
+
+from tests.test_gpu_parity import fm
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def test_small_results_keep_little_memory_and_versions_of_their_own():
+    """A loss that is kept (for a log) keeps no workspace with it, and the
+    results of a call are not views of one another for autograd."""
+    m = fm()
+    X, W = torch.randn(100, 64, device="cuda").to(BF), torch.randn(5000, 64, device="cuda").to(BF)
+    t = torch.randint(0, 5000, (100,), device="cuda")
+    loss, lse = m.vocab_loss(X, W, t)
+    # 2 x 400 bytes at multiples of 256, and 16 KB of a workspace at most
+    assert loss.untyped_storage().nbytes() <= 2 * 512 + (16 << 10)
+    assert m.flash_mca_vocab_loss_workspace_bytes(100, 5000, 64) > 16 << 10
+    before = lse._version
+    loss.mul_(2.0)
+    assert lse._version == before and not loss._is_view() and not lse._is_view()
+    with torch.inference_mode():
+        loss2, lse2 = m.vocab_loss(X, W, t)
+    assert torch.equal(loss2 * 2.0, loss) and torch.equal(lse2, lse) and loss2.is_inference()
+
+
+def test_other_threads_run_while_a_stream_is_full():
+    """Calls that wait for room in the stream's queue let other Python threads
+    run (the device is kept busy for half a second, ahead of 3000 calls)."""
+    m = fm()
+    x, w = torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    m.layer_norm(x, w, w)
+    torch.cuda.synchronize()
+    gaps, stop = [], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.002)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    ticker = threading.Thread(target=tick)
+    ticker.start()
+    try:
+        torch.cuda._sleep(1_000_000_000)
+        for _ in range(3000):
+            m.layer_norm(x, w, w)
+    finally:
+        stop.set()
+        ticker.join()
+    torch.cuda.synchronize()
+    assert max(gaps) < 0.25
+
+
+def test_first_calls_of_a_process_are_captured():
+    """The kernels' attributes and residencies are looked up in the first call:
+    that call may be one that is being captured."""
+    code = """
+import torch, flash_mixed_chunk_gb300 as m
+torch.manual_seed(0)
+g = torch.Generator("cuda").manual_seed(1)
+r = lambda *s: (torch.randn(*s, device="cuda", generator=g) / 8).to(torch.bfloat16)
+res = {}
+for M in (100, 700):
+    X, W, Y, Wo, dOut = r(M, 128), r(900, 128), r(M, 256), r(128, 256), r(M, 128)
+    Wt, dU, dV, dZ = r(2 * 256 + 64, 128), r(M, 256), r(M, 256), r(M, 64)
+    t = torch.randint(0, 900, (M,), device="cuda", generator=g)
+    w, dl = torch.ones(128, device="cuda"), torch.rand(M, device="cuda", generator=g)
+    def step():
+        y, h, mean, rstd = m.layer_norm(X, w, w)
+        loss, lse = m.vocab_loss(X, W, t)
+        return (y, *m.layer_norm_backward(dOut, h, w, mean, rstd), loss,
+                *m.vocab_loss_backward(X, W, t, lse, dl),
+                *m.gau_output_backward(Y, Wo, dOut), *m.gau_project_backward(X, Wt, dU, dV, dZ))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    graph.replay()
+    for a, b in zip(out, step()):
+        assert torch.equal(a, b)
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert p.returncode == 0 and "same" in p.stdout, p.stderr[-2000:]
