@@ -20,7 +20,7 @@
 // it, else 4-byte ones, else single elements.  Rows that would fill a warp's
 // registers (and, backward, its shared memory) with few threads at work (fp32
 // beyond 512 elements, narrow vectors beyond 256) belong to half a block: 5001
-// fp32 rows of 1001 take 17 us backward instead of 32.
+// fp32 rows of 1001 took 17 us backward instead of 32 (13 since, held).
 //
 // The backward pass keeps dw and db of the rows it has seen in registers, one
 // partial row a block in the workspace, and a second kernel adds the partial
@@ -99,12 +99,11 @@ __device__ __forceinline__ void load_w(const float *__restrict__ p, float *out) 
   }
 }
 
-// The sums of a.x and a.y over the threads of a row's group: a warp, half a
-// block or the block (two sets of shared words in turn, so that one barrier a
-// sum is enough; half a block meets at a barrier of its own).
-template <int GROUP>
-__device__ __forceinline__ float2 group_sum2(float2 a, float2 (*red)[kNormThreads / 32],
-                                             int &turn) {
+// The sums of a.x and a.y over the threads of a row's group: a warp, some warps
+// of a block or the block (two sets of shared words in turn, so that one barrier
+// a sum is enough; some warps meet at a barrier of their own).
+template <int GROUP, int THREADS>
+__device__ __forceinline__ float2 group_sum2(float2 a, float2 (*red)[THREADS / 32], int &turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
@@ -115,7 +114,7 @@ __device__ __forceinline__ float2 group_sum2(float2 a, float2 (*red)[kNormThread
     turn ^= 1;
     if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = a;
     const int grp = threadIdx.x / GROUP;
-    if constexpr (GROUP == kNormThreads)
+    if constexpr (GROUP == THREADS)
       __syncthreads();
     else
       named_bar_sync(1 + grp, GROUP);
@@ -131,7 +130,7 @@ __device__ __forceinline__ float2 group_sum2(float2 a, float2 (*red)[kNormThread
 }
 template <int GROUP>
 __device__ __forceinline__ float group_sum(float v, float2 (*red)[kNormThreads / 32], int &turn) {
-  return group_sum2<GROUP>(make_float2(v, 0.f), red, turn).x;
+  return group_sum2<GROUP, kNormThreads>(make_float2(v, 0.f), red, turn).x;
 }
 
 // T: I/O type; VEC elements a vector, N vectors a thread; GROUP threads a row.
@@ -229,30 +228,45 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Rows on their way to a block of the backward pass: the group's current row
-// and the next, three operands (dy, h, dh) each.
+// How the backward pass brings its rows: with up to 8 elements a thread it holds
+// the weights and the row's dy and h in registers (N * VEC <= 8), else it reads
+// them twice.  16-byte vectors come through a ring in shared memory (copied
+// asynchronously, which costs no registers: the group's current row and the
+// next, three operands each); 4-byte ones too, or, held, one row ahead in
+// registers (5001 fp32 rows of 1001 with a residual: 14.3 us, through the ring
+// 18.1; 16-byte vectors the other way round, 16384 bf16 rows of 1024: 37.2 and
+// 32.8); single 2-byte elements are read in place (ahead, they spill: 16.0 us
+// instead of 13.4 for 5001 rows of 1001).
 constexpr int kNormStages = 2;
 template <typename T, int VEC, int N>
+struct NormFeed {
+  static constexpr size_t kBytes = sizeof(T) * VEC;
+  static constexpr bool kHold = N * VEC <= 8;
+  static constexpr bool kAhead = kHold && kBytes == 4;
+  static constexpr bool kRing = kBytes >= 4 && !kAhead;
+};
+template <typename T, int VEC, int N, int THREADS>
 constexpr size_t norm_ring_bytes() {
-  // single 2-byte elements cannot be copied asynchronously: read in place
-  return sizeof(T) * VEC >= 4 ? (size_t)kNormStages * 3 * N * kNormThreads * sizeof(T) * VEC : 0;
+  return NormFeed<T, VEC, N>::kRing ? (size_t)kNormStages * 3 * N * THREADS * sizeof(T) * VEC : 0;
 }
 
 // dx, and the block's sums of dw and db: part [blocks][2][d].  Rows are dealt
 // to the groups round-robin.  While a row is reduced the next one is on its
-// way to shared memory, which costs no registers: those hold the running dw
-// and db (2 x 24 at d = 768), and what is in flight sets the rate.
-template <typename T, int VEC, int N, int GROUP>
-__global__ void __launch_bounds__(kNormThreads, 2)
+// way; registers hold the running dw and db (2 x 24 at d = 768), and what is in
+// flight sets the rate.
+template <typename T, int VEC, int N, int GROUP, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2)
     norm_backward(const T *__restrict__ dy, const T *__restrict__ h,
                   const float *__restrict__ weight, const float *__restrict__ mean_in,
                   const float *__restrict__ rstd_in, const T *__restrict__ dh,
                   T *__restrict__ dx, float *__restrict__ part, int M, int d) {
-  __shared__ float2 red[2][kNormThreads / 32];
+  __shared__ float2 red[2][THREADS / 32];
   extern __shared__ __align__(16) uint8_t ring[];
   int turn = 0;
-  constexpr int kRows = kNormThreads / GROUP;
-  constexpr bool kRing = sizeof(T) * VEC >= 4;
+  using Feed = NormFeed<T, VEC, N>;
+  using P = Pack<T, VEC>;
+  constexpr int kRows = THREADS / GROUP;
+  constexpr bool kHold = Feed::kHold, kAhead = Feed::kAhead, kRing = Feed::kRing;
   const int lane = threadIdx.x % GROUP, grp = threadIdx.x / GROUP;
   const int nv = d / VEC;
   const float inv_d = 1.0f / (float)d;
@@ -260,87 +274,117 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   const int64_t step = (int64_t)gridDim.x * kRows;
   auto place = [&](int stage, int op, int i) {
     return reinterpret_cast<T *>(ring) +
-           (int64_t)(((stage * 3 + op) * N + i) * kNormThreads + threadIdx.x) * VEC;
+           (int64_t)(((stage * 3 + op) * N + i) * THREADS + threadIdx.x) * VEC;
   };
+  auto source = [&](int op, int64_t row, int i) {
+    return (op == 0 ? dy : op == 1 ? h : dh) + row * d + (int64_t)(lane + i * GROUP) * VEC;
+  };
+  P ahead[kAhead ? 3 : 1][kAhead ? N : 1];
   auto fetch = [&](int64_t row, int stage) {
-    if constexpr (kRing) {
-      if (row < M) {
+    if (row < M) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int c = lane + i * GROUP;
-          if (c < nv) {
-            const int64_t at = row * d + (int64_t)c * VEC;
-            copy_async<(int)sizeof(T) * VEC>(place(stage, 0, i), dy + at);
-            copy_async<(int)sizeof(T) * VEC>(place(stage, 1, i), h + at);
-            if (dh != nullptr) copy_async<(int)sizeof(T) * VEC>(place(stage, 2, i), dh + at);
+      for (int i = 0; i < N; ++i) {
+        if (lane + i * GROUP < nv) {
+#pragma unroll
+          for (int op = 0; op < 3; ++op) {
+            if (op == 2 && dh == nullptr) continue;
+            if constexpr (kRing)
+              copy_async<(int)Feed::kBytes>(place(stage, op, i), source(op, row, i));
+            else if constexpr (kAhead)
+              ahead[op][i].raw =
+                  __ldg(reinterpret_cast<const typename P::raw_t *>(source(op, row, i)));
           }
         }
       }
-      copies_commit();
     }
+    if constexpr (kRing) copies_commit();
   };
-  float dw[N * VEC], db[N * VEC];
+  float dw[N * VEC], db[N * VEC], held_w[kHold ? N * VEC : 1];
 #pragma unroll
   for (int i = 0; i < N * VEC; ++i) dw[i] = 0.f, db[i] = 0.f;
+  if constexpr (kHold) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + i * GROUP < nv) load_w<VEC>(weight + (lane + i * GROUP) * VEC, held_w + i * VEC);
+  }
   int64_t row = (int64_t)blockIdx.x * kRows + grp;
   fetch(row, 0);
   for (int stage = 0; row < M; row += step, stage ^= 1) {
+    P held[kHold ? 3 : 1][kHold ? N : 1];  // dy, h and, of a row fetched ahead, dh
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int op = 0; op < 3; ++op)
+#pragma unroll
+        for (int i = 0; i < N; ++i) held[op][i] = ahead[op][i];
+    }
     fetch(row + step, stage ^ 1);
     const float mean = mean_in[row], rstd = rstd_in[row];
     // vector i of operand op of this row
-    auto take = [&](int op, int i, float *out) {
-      if constexpr (kRing) {
-        load_vec<T, VEC>(place(stage, op, i), out);
+    auto take = [&](int op, int i, P &out) {
+      if constexpr (kAhead)
+        out = held[op][i];
+      else
+        out.raw = *reinterpret_cast<const typename P::raw_t *>(kRing ? place(stage, op, i)
+                                                                     : source(op, row, i));
+    };
+    auto weights = [&](int i, float *w) {
+      if constexpr (kHold) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) w[k] = held_w[i * VEC + k];
       } else {
-        const T *src = op == 0 ? dy : op == 1 ? h : dh;
-        load_vec<T, VEC>(src + row * d + (int64_t)(lane + i * GROUP) * VEC, out);
+        load_w<VEC>(weight + (lane + i * GROUP) * VEC, w);
       }
     };
     if constexpr (kRing) copies_wait<1>();
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = lane + i * GROUP;
-      if (c < nv) {
-        float g[VEC], xh[VEC], w[VEC];
+      if (lane + i * GROUP < nv) {
+        P g, xh;
+        float w[VEC];
         take(0, i, g);
         take(1, i, xh);
-        load_w<VEC>(weight + c * VEC, w);
+        if constexpr (kHold) held[0][i] = g, held[1][i] = xh;
+        weights(i, w);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-          const float x = (xh[k] - mean) * rstd, t = g[k] * w[k];
-          dw[i * VEC + k] += g[k] * x;
-          db[i * VEC + k] += g[k];
+          const float gk = to_f(g.v[k]), x = (to_f(xh.v[k]) - mean) * rstd, t = gk * w[k];
+          dw[i * VEC + k] += gk * x;
+          db[i * VEC + k] += gk;
           s1 += t;
           s2 += t * x;
         }
       }
     }
-    const float2 sums = group_sum2<GROUP>(make_float2(s1, s2), red, turn);
+    const float2 sums = group_sum2<GROUP, THREADS>(make_float2(s1, s2), red, turn);
     const float m1 = sums.x * inv_d, m2 = sums.y * inv_d;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = lane + i * GROUP;
-      if (c < nv) {
-        float g[VEC], xh[VEC], w[VEC], o[VEC];
-        take(0, i, g);
-        take(1, i, xh);
-        load_w<VEC>(weight + c * VEC, w);
+      if (lane + i * GROUP < nv) {
+        P g, xh;
+        float w[VEC], o[VEC];
+        if constexpr (kHold) {
+          g = held[0][i], xh = held[1][i];
+        } else {
+          take(0, i, g);
+          take(1, i, xh);
+        }
+        weights(i, w);
 #pragma unroll
         for (int k = 0; k < VEC; ++k)
-          o[k] = rstd * (g[k] * w[k] - m1 - (xh[k] - mean) * rstd * m2);
+          o[k] = rstd * (to_f(g.v[k]) * w[k] - m1 - (to_f(xh.v[k]) - mean) * rstd * m2);
         if (dh != nullptr) {
-          float r[VEC];
+          P r;
           take(2, i, r);
 #pragma unroll
-          for (int k = 0; k < VEC; ++k) o[k] += r[k];
+          for (int k = 0; k < VEC; ++k) o[k] += to_f(r.v[k]);
         }
-        store_vec<T, VEC>(dx + row * d + (int64_t)c * VEC, o);
+        store_vec<T, VEC>(dx + row * d + (int64_t)(lane + i * GROUP) * VEC, o);
       }
     }
   }
   float *pw = part + (int64_t)blockIdx.x * 2 * d;
-  if constexpr (GROUP == kNormThreads) {
+  if constexpr (GROUP == THREADS) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = lane + i * GROUP;
@@ -367,7 +411,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
         }
     }
     __syncthreads();
-    for (int j = threadIdx.x; j < 2 * d; j += kNormThreads) {
+    for (int j = threadIdx.x; j < 2 * d; j += THREADS) {
       float t = acc[j];
 #pragma unroll
       for (int q = 1; q < kRows; ++q) t += acc[q * 2 * d + j];
@@ -419,47 +463,70 @@ cudaError_t launch_fwd(const NormArgs &a, cudaStream_t stream) {
       static_cast<T *>(a.o0), static_cast<T *>(a.o1), a.f0, a.f1, a.M, a.d, a.eps);
   return cudaGetLastError();
 }
-static_assert(norm_ring_bytes<float, 4, 8>() <= kNormMaxSmem, "two rows of every group fit");
-template <typename T, int VEC, int N, int GROUP>
+static_assert(norm_ring_bytes<float, 4, 8, kNormThreads>() <= kNormMaxSmem,
+              "two rows of every group fit");
+template <typename T, int VEC, int N, int GROUP, int THREADS = kNormThreads>
 cudaError_t launch_bwd(const NormArgs &a, cudaStream_t stream) {
-  size_t smem = norm_ring_bytes<T, VEC, N>();
-  if (GROUP < kNormThreads) {
-    const size_t sums = 2 * sizeof(float) * (size_t)a.d * (kNormThreads / GROUP);
+  size_t smem = norm_ring_bytes<T, VEC, N, THREADS>();
+  if (GROUP < THREADS) {
+    const size_t sums = 2 * sizeof(float) * (size_t)a.d * (THREADS / GROUP);
     if (sums > smem) smem = sums;
   }
   static OncePerDevice attrs;
   if (!attrs.run([] {
-        return cudaFuncSetAttribute(norm_backward<T, VEC, N, GROUP>,
+        return cudaFuncSetAttribute(norm_backward<T, VEC, N, GROUP, THREADS>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kNormMaxSmem) == cudaSuccess;
       }))
     return cudaErrorInvalidValue;
-  norm_backward<T, VEC, N, GROUP><<<a.blocks, kNormThreads, smem, stream>>>(
+  norm_backward<T, VEC, N, GROUP, THREADS><<<a.blocks, THREADS, smem, stream>>>(
       static_cast<const T *>(a.a), static_cast<const T *>(a.b), a.weight, a.mean, a.rstd,
       static_cast<const T *>(a.dh), static_cast<T *>(a.o0), a.f0, a.M, a.d);
   return cudaGetLastError();
 }
 
-// Elements a thread: the fewest of 8, 16, 24, 32 that cover the row.
+// Elements a thread: the fewest of 8, 16, 24, 32 that cover the row.  A warp's
+// rows are no longer than pick_group lets them be.
 template <typename T, int VEC, int GROUP, bool kBackward>
 cudaError_t pick_n(const NormArgs &a, cudaStream_t stream) {
+  constexpr int kMost = GROUP > 32              ? 32
+                        : sizeof(T) * VEC < 16 ? 8
+                        : sizeof(T) == 4       ? 16
+                        : kBackward            ? 24
+                                               : 32;
   const int per = (a.d + GROUP * 8 - 1) / (GROUP * 8);  // eights of elements a thread
-#define FMCA_NORM(E)                                                        \
-  return kBackward ? launch_bwd<T, VEC, (E) / VEC, GROUP>(a, stream)        \
-                   : launch_fwd<T, VEC, (E) / VEC, GROUP>(a, stream)
-  switch (per) {
-    case 1: FMCA_NORM(8);
-    case 2: FMCA_NORM(16);
-    case 3: FMCA_NORM(24);
-    default: FMCA_NORM(32);
-  }
+#define FMCA_NORM(E)                                                            \
+  if constexpr ((E) <= kMost)                                                   \
+    if (per * 8 <= (E))                                                         \
+      return kBackward ? launch_bwd<T, VEC, (E) / VEC, GROUP>(a, stream)        \
+                       : launch_fwd<T, VEC, (E) / VEC, GROUP>(a, stream)
+  FMCA_NORM(8);
+  FMCA_NORM(16);
+  FMCA_NORM(24);
+  FMCA_NORM(32);
 #undef FMCA_NORM
+  return cudaErrorInvalidValue;
+}
+// Warps a row of the backward pass has where one warp would be short of
+// registers: bf16 rows of more than 768 in 16-byte vectors (16384 x 1024: 35.8 us
+// with a warp a row, 31.1 with 4), and of more than 512 while there are few of
+// them for all the groups (4096 x 768: 11.9 and 10.3 with 3, 8192: 15.2 and
+// 14.4, 16384: 23.4 and 24.0).  0: as in the forward pass.
+constexpr int kNormWideRows = 4;
+int norm_wide(int M, int d, int elem) {
+  if (elem != 2 || d % 8 || d > kNormWarpMaxD) return 0;
+  return d > 768 ? 4 : d > 512 && M <= 8192 ? 3 : 0;
 }
 template <typename T, int VEC, bool kBackward>
 cudaError_t pick_group(const NormArgs &a, cudaStream_t stream) {
   if (norm_half(a.d, sizeof(T), sizeof(T) * VEC))
     return kBackward ? launch_bwd<T, VEC, 8 / VEC, 128>(a, stream)
                      : launch_fwd<T, VEC, 8 / VEC, 128>(a, stream);
+  if constexpr (kBackward && VEC == 8) {
+    const int warps = norm_wide(a.M, a.d, sizeof(T));
+    if (warps == 4) return launch_bwd<T, VEC, 1, 128, 128 * kNormWideRows>(a, stream);
+    if (warps == 3) return launch_bwd<T, VEC, 1, 96, 96 * kNormWideRows>(a, stream);
+  }
   return a.d <= kNormWarpMaxD ? pick_n<T, VEC, 32, kBackward>(a, stream)
                               : pick_n<T, VEC, kNormThreads, kBackward>(a, stream);
 }
@@ -478,6 +545,9 @@ cudaError_t pick(const NormArgs &a, int bf16, cudaStream_t stream) {
 int norm_rows(int d, int elem) {
   const int vec = d * elem % 16 == 0 ? 16 : d * elem % 4 == 0 ? 4 : 2;
   return norm_half(d, elem, vec) ? 2 : d <= kNormWarpMaxD ? kNormThreads / 32 : 1;
+}
+int norm_rows_backward(int M, int d, int elem) {
+  return norm_wide(M, d, elem) ? kNormWideRows : norm_rows(d, elem);
 }
 
 }  // namespace
@@ -502,7 +572,7 @@ int launch_layer_norm_backward(const void *dy, const void *h, const float *weigh
   a.a = dy, a.b = h, a.weight = weight, a.mean = mean, a.rstd = rstd, a.dh = dh;
   a.o0 = dx, a.f0 = static_cast<float *>(workspace);
   a.M = M, a.d = d;
-  const int rows = norm_rows(d, dtype_bf16 ? 2 : 4);
+  const int rows = norm_rows_backward(M, d, dtype_bf16 ? 2 : 4);
   const int64_t blocks = ((int64_t)M + rows - 1) / rows;
   a.blocks = (int)(blocks < kNormBackwardBlocks ? blocks : kNormBackwardBlocks);
   if (pick<true>(a, dtype_bf16, stream) != cudaSuccess) return 1;

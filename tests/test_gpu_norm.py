@@ -225,3 +225,21 @@ def test_outputs_are_tensors_of_their_own():
         t.fill_(-1.0)
         assert all(torch.equal(a, c) for a, c in zip(outs[i + 1:], keep[i + 1:]))
         assert (t == -1.0).all()
+
+
+# rows of several warps, and several rows a group, at both sides of the number of
+# rows up to which the backward pass spreads a row over more warps
+MANY = [(8192, 640, BF), (8193, 640, BF), (3000, 776, BF), (4099, 1002, BF), (4099, 1001, BF),
+        (4099, 1001, F32), (2600, 201, F32), (2000, 2001, F32), (1, 776, BF), (5, 640, BF)]
+
+
+@pytest.mark.parametrize("M,d,dt", MANY, ids=lambda v: str(v).removeprefix("torch."))
+@pytest.mark.parametrize("residual", [False, True])
+def test_backward_of_many_rows(M, d, dt, residual):
+    m = fm()
+    x, _, w, b, dy, dh = cuda(*make(M, d, dt, M + d, residual))
+    _, h, mean, rstd = m.layer_norm(x, w, b, EPS)
+    dx, dw, db = m.layer_norm_backward(dy, h, w, mean, rstd, dh)
+    check_backward(dy, h, w, dh, dx, dw, db, dt)
+    again = m.layer_norm_backward(dy, h, w, mean, rstd, dh)
+    assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))
