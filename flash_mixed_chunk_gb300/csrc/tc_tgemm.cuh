@@ -40,13 +40,13 @@ enum : int { TG_LSE = 0, TG_PROB = 1, TG_SILU = 2, TG_GRAD = 3 };
 
 // Shared memory of a CTA: the ring, and for the kinds that write A (TG_PROB,
 // TG_SILU) 8 KB a warp to stage its 32 rows x 128 columns.
-template <int CG, int KIND>
+template <int CG, int KIND, int NT>
 struct TgCfg {
   static constexpr uint32_t A_BYTES = 128 * 64 * 2;              // 16 KB
-  static constexpr uint32_t B_BYTES = (256 / CG) * 64 * 2;       // 32 or 16 KB
+  static constexpr uint32_t B_BYTES = (NT / CG) * 64 * 2;        // 32 or 16 KB
   static constexpr uint32_t SLOT = A_BYTES + B_BYTES;
   static constexpr bool STAGED = KIND == TG_PROB || KIND == TG_SILU;
-  static constexpr int RING = STAGED ? (CG == 2 ? 5 : 3) : (CG == 2 ? 6 : 4);
+  static constexpr int RING = STAGED ? (NT / CG == 128 ? 5 : 3) : (NT / CG == 128 ? 6 : 4);
   static constexpr uint32_t PIECE = 32 * 64 * 2;                 // 32 rows x 64 columns
   static constexpr uint32_t STAGE = STAGED ? TG_EPI_WARPS * 2 * PIECE : 0;
   static constexpr uint32_t SMEM = RING * SLOT + STAGE + 1024;
@@ -142,13 +142,13 @@ constexpr int kTgEpilogue = 3;
 // The launch that joins the parts of cut tiles (5 us), in k steps.
 constexpr int kTgJoin = 14;
 
-template <int CG>
+template <int CG, int NT>
 __host__ __device__ inline TgShape tg_shape(int M_exist, int M, int N, int K, int K_full,
                                             int side, int groups) {
   TgShape h;
   h.M = M_exist;
   h.Mt = (M + 128 * CG - 1) / (128 * CG);
-  h.Nt = (N + 255) / 256;
+  h.Nt = (N + NT - 1) / NT;
   h.ks = (K_full + 63) / 64;
   h.kend = (K + 63) / 64;
   h.tiles = h.Mt * h.Nt;
@@ -158,7 +158,7 @@ __host__ __device__ inline TgShape tg_shape(int M_exist, int M, int N, int K, in
   return h;
 }
 
-template <int CG, int KIND>
+template <int CG, int KIND, int NT = 256>
 __host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int count, int workers) {
   TgPlan p;
   p.count = count;
@@ -173,7 +173,7 @@ __host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int coun
     p.width = p.col0 < P.N ? (P.N - p.col0 < full ? P.N - p.col0 : full) : 0;
   }
   p.side = 1;
-  if (KIND == TG_GRAD) {
+  if (KIND == TG_GRAD && NT == 256) {
     // as many tiles of a row panel side by side as leave few workers over;
     // only where one of the products is all cut
     const int Nt = (P.K + 255) / 256, rows = 128 * CG;
@@ -186,17 +186,17 @@ __host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int coun
     // dW [width][K], depth tokens; dX [tokens][K], depth width.  The tiles and
     // their cuts are those of a full piece in every piece, so that the sums of
     // dX go on from piece to piece; the last one leaves some without work.
-    p.s[0] = tg_shape<CG>(p.width, full, P.K, count, count, p.side, p.groups);
-    p.s[1] = tg_shape<CG>(count, count, P.K, p.width, full, p.side, p.groups);
+    p.s[0] = tg_shape<CG, NT>(p.width, full, P.K, count, count, p.side, p.groups);
+    p.s[1] = tg_shape<CG, NT>(count, count, P.K, p.width, full, p.side, p.groups);
     // fewer cut panels than workers, 2^22 steps each at most: 31 bits hold it
     p.base1 = p.s[0].cut * p.s[0].len;
     p.total = p.base1 + p.s[1].cut * p.s[1].len;
     // no cuts where they would save less than joining the parts takes
     const int len0 = p.s[0].cut ? p.s[0].len : 0, len1 = p.s[1].cut ? p.s[1].len : 0;
-    p.apart = p.s[0].cut + p.s[1].cut <= p.groups &&
-              (len0 > len1 ? len0 : len1) <= p.total / p.groups + kTgJoin;
+    p.apart = NT < 256 || (p.s[0].cut + p.s[1].cut <= p.groups &&
+                           (len0 > len1 ? len0 : len1) <= p.total / p.groups + kTgJoin);
   } else {
-    p.s[0] = tg_shape<CG>(count, p.width > 0 ? count : 0, p.width, P.K, P.K, 1, workers);
+    p.s[0] = tg_shape<CG, NT>(count, p.width > 0 ? count : 0, p.width, P.K, P.K, 1, workers);
     p.s[1] = p.s[0];
     p.base1 = p.total = 0;
     p.apart = false;
@@ -540,10 +540,11 @@ __device__ __forceinline__ float tg_rows_as_they_are(const TgParams &P, int coun
   return top;
 }
 
-template <int CG, int KIND>
+template <int CG, int KIND, int NT>
 __global__ void __launch_bounds__(TG_THREADS, 1)
     tc_tgemm(const __grid_constant__ TgParams P) {
-  using Cfg = TgCfg<CG, KIND>;
+  using Cfg = TgCfg<CG, KIND, NT>;
+  static_assert(NT == 256 || (CG == 1 && (KIND == TG_SILU || KIND == TG_GRAD)));
   constexpr int RING = Cfg::RING;
   // With few of the rows taking part the pieces are wide and the last launches
   // have none (every kernel ahead has waited for the one that counts).
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       tma_prefetch_desc(&P.B1);
     }
     if (early)
-      plan = tg_plan<CG, KIND>(P, P.piece, P.hdr != nullptr ? tg_count(P.hdr) : P.M, workers);
+      plan = tg_plan<CG, KIND, NT>(P, P.piece, P.hdr != nullptr ? tg_count(P.hdr) : P.M, workers);
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < RING; ++i) {
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
   griddep_wait();
   griddep_launch_dependents();
   if (!early) {
-    if (threadIdx.x == 96) plan = tg_plan<CG, KIND>(P, P.piece, tg_count(P.hdr), workers);
+    if (threadIdx.x == 96) plan = tg_plan<CG, KIND, NT>(P, P.piece, tg_count(P.hdr), workers);
     __syncthreads();
     walk.start(worker, workers);
     more = walk.next(ahead);
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       for (TgUnit u; ok && more; more = walk.next(ahead)) {
         u = ahead;
         const int m0 = u.mt * 128 * CG + (int)rank * 128;
-        const int nb0 = u.nt * 256 + (int)rank * 128;
+        const int nb0 = u.nt * NT + (int)rank * 128;
         for (int ks = 0; ks < u.nks; ++ks, ++it) {
           const int slot = it % RING;
           if (it >= RING && !mbar_wait(&empty[slot], ((it / RING) - 1) & 1, kWaitLimitNs)) {
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
             // rows k (problem 1: from the piece's first row of W), columns n
             const int krow = kk + (u.pi ? col0 : 0);
 #pragma unroll
-            for (int q = 0; q < 4 / CG; ++q)
+            for (int q = 0; q < NT / 64 / CG; ++q)
               tg_load<CG>(sb + q * 8192, mB, bar, nb0 + 64 * q, krow);
           }
         }
@@ -678,8 +679,8 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
     // =========================== MMA issuer (of a pair: the first CTA)
     if (lane == 0 && rank == 0) {
       constexpr bool kMn = KIND == TG_GRAD;
-      constexpr uint32_t id_k = idesc_bf16_f32(128 * CG, 256, false, kMn);
-      constexpr uint32_t id_mn = idesc_bf16_f32(128 * CG, 256, true, kMn);
+      constexpr uint32_t id_k = idesc_bf16_f32(128 * CG, NT, false, kMn);
+      constexpr uint32_t id_mn = idesc_bf16_f32(128 * CG, NT, true, kMn);
       int it = 0;
       bool ok = true;
       TgUnit u;
@@ -730,7 +731,8 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
   } else {
     // =========================== epilogue warps
     // Warp w reads TMEM lanes 32 (w % 4) .. (its 32 rows, one a thread) of
-    // columns 128 half .. + 128.
+    // columns kHalf half .. + kHalf, 64 at a time (NQ pieces).
+    constexpr int kHalf = NT / 2, NQ = kHalf / 64;
     const int quad = warp & 3, half = (warp - 2) / 4;
     const int row = quad * 32 + lane;
     uint8_t *stage = smem + RING * Cfg::SLOT + (warp - 2) * 2 * Cfg::PIECE;
@@ -740,7 +742,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
     uint64_t *up = up_full + 2 * (warp - 2);
     auto fetch = [&](const TgUnit &f, int q, bool l2_only) {
       const int row0 = f.mt * 128 * CG + (int)rank * 128 + quad * 32;
-      const int col = f.nt * 256 + half * 128 + 64 * q;
+      const int col = f.nt * NT + half * kHalf + 64 * q;
       // columns past the last array arrive as zeros
       const CUtensorMap *map = col < P.n0 ? &P.U0 : col < P.n1 ? &P.U1 : &P.U2;
       const int x = col < P.n0 ? col : col < P.n1 ? col - P.n0 : col - P.n1;
@@ -764,7 +766,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         const int row0 = f.mt * 128 * CG + (int)rank * 128 + quad * 32;
-        const int block = f.nt * 4 + half * 2 + q;
+        const int block = (f.nt * NT + half * kHalf) / 64 + q;
         tma_store_2d(&P.S, piece, 0, block * n_tok64 * 64 + row0);
         bulk_commit_group();
       }
@@ -787,11 +789,11 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       more = walk.next(ahead);
       const int buf = i & 1, use = i >> 1;
       const int m = u.mt * 128 * CG + (int)rank * 128 + row;  // row of the product
-      const int c0 = u.nt * 256 + half * 128;                 // first column in the piece
+      const int c0 = u.nt * NT + half * kHalf;                // first column in the piece
       // TG_SILU: piece 0 was fetched as soon as the unit before had left it;
       // piece 1, stored last, follows now.  The next unit's gradients come to
       // L2 meanwhile: their pieces are free too late for a trip to DRAM.
-      if constexpr (KIND == TG_SILU) {
+      if constexpr (KIND == TG_SILU && NQ == 2) {
         if (lane == 0) {
           bulk_wait_group_read<0>();
           fetch(u, 1, false);
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
       }
       tc_fence_after();
       const uint32_t dcol =
-          tbase + (uint32_t)buf * 256u + (uint32_t)(half * 128) + ((uint32_t)(quad * 32) << 16);
+          tbase + (uint32_t)buf * 256u + (uint32_t)(half * kHalf) + ((uint32_t)(quad * 32) << 16);
       // this warp's last read of the accumulator
       auto release = [&] {
         tc_fence_before();
@@ -911,7 +913,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
         }
         bool ok = true;
 #pragma unroll
-        for (int q2 = 0; q2 < 2; ++q2) {
+        for (int q2 = 0; q2 < NQ; ++q2) {
           uint32_t r[2][32];
           tmem_ld32(dcol + 64 * q2, r[0]);
           tmem_ld32(dcol + 64 * q2 + 32, r[1]);
@@ -926,7 +928,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
           tmem_ld_wait();
           if (!ok) break;
           if constexpr (KIND == TG_SILU) ++used[q2];
-          if (q2 == 1) release();
+          if (q2 == NQ - 1) release();
           if (KIND == TG_GRAD && u.nks == 0) {  // nothing was multiplied: the product is 0
 #pragma unroll
             for (int c2 = 0; c2 < 2; ++c2)
@@ -966,7 +968,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
                   v[8 * q + k] = d * sig * fmaf(z, 1.f - sig, 1.f);
                 }
               }
-              if (c == 2 && more) {  // the store of piece 0 has read it
+              if (NQ == 2 && c == 2 && more) {  // the store of piece 0 has read it
                 if (lane == 0) {
                   bulk_wait_group_read<0>();
                   fetch(ahead, 0, false);
@@ -982,14 +984,14 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                   const float4 o = *reinterpret_cast<const float4 *>(
-                      slot + tg_slot_offset(row, half * 32 + c * 8 + j));
+                      slot + tg_slot_offset(row, half * (kHalf / 4) + c * 8 + j));
                   v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
                 }
               }
               if (!direct) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                  *reinterpret_cast<float4 *>(slot + tg_slot_offset(row, half * 32 + c * 8 + j)) =
+                  *reinterpret_cast<float4 *>(slot + tg_slot_offset(row, half * (kHalf / 4) + c * 8 + j)) =
                       make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
               } else if (out != nullptr) {
 #pragma unroll
@@ -1016,6 +1018,15 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
               tg_stage(piece, lane, c2, v);
               if (c2 == 1) store_piece(u, q2, piece);
             }
+          }
+        }
+        if constexpr (KIND == TG_SILU && NQ == 1) {
+          if (ok && more) {  // the only piece is free once its store has read it
+            if (lane == 0) {
+              bulk_wait_group_read<0>();
+              fetch(ahead, 0, false);
+            }
+            ++fetched[0];
           }
         }
         if (!ok) {

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // ---------------------------------------------------------------- host side
 // Launch configuration of one tc_tgemm (its attributes live in the object).
-template <int CG, int KIND>
+template <int CG, int KIND, int NT>
 struct TgLaunch {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg;
@@ -344,7 +344,7 @@ struct TgLaunch {
     cfg = cudaLaunchConfig_t{};
     cfg.gridDim = dim3(workers * CG);
     cfg.blockDim = dim3(TG_THREADS);
-    cfg.dynamicSmemBytes = TgCfg<CG, KIND>::SMEM;
+    cfg.dynamicSmemBytes = TgCfg<CG, KIND, NT>::SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
@@ -355,7 +355,7 @@ struct TgLaunch {
 // sit within a group of SMs, so there can be fewer than half the SMs: the
 // units are dealt to the workers beforehand, and one that had to wait for
 // another to leave would double the time.
-template <int CG, int KIND>
+template <int CG, int KIND, int NT>
 int tg_resident() {
   static OncePerDevice once;
   static int resident[OncePerDevice::kMaxDevices];
@@ -363,16 +363,16 @@ int tg_resident() {
   if (!once.run([] {
         int d = 0, n = 0;
         if (cudaGetDevice(&d) != cudaSuccess ||
-            cudaFuncSetAttribute(tc_tgemm<CG, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)TgCfg<CG, KIND>::SMEM) != cudaSuccess)
+            cudaFuncSetAttribute(tc_tgemm<CG, KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)TgCfg<CG, KIND, NT>::SMEM) != cudaSuccess)
           return false;
         n = num_sms() / CG;
         if (CG == 2) {
-          TgLaunch<CG, KIND> l(n, nullptr);
+          TgLaunch<CG, KIND, NT> l(n, nullptr);
           l.cfg.attrs = &l.attr[1];
           l.cfg.numAttrs = 1;
           int fit = 0;
-          if (cudaOccupancyMaxActiveClusters(&fit, tc_tgemm<CG, KIND>, &l.cfg) != cudaSuccess)
+          if (cudaOccupancyMaxActiveClusters(&fit, tc_tgemm<CG, KIND, NT>, &l.cfg) != cudaSuccess)
             return false;
           if (fit < n) n = fit;
         }
@@ -385,19 +385,19 @@ int tg_resident() {
   return resident[dev];
 }
 
-template <int CG, int KIND>
+template <int CG, int KIND, int NT>
 int launch_tgemm_kind(const TgParams &P, int workers, cudaStream_t stream) {
-  TgLaunch<CG, KIND> l(workers, stream);
-  return cudaLaunchKernelEx(&l.cfg, tc_tgemm<CG, KIND>, P) == cudaSuccess ? 0 : 1;
+  TgLaunch<CG, KIND, NT> l(workers, stream);
+  return cudaLaunchKernelEx(&l.cfg, tc_tgemm<CG, KIND, NT>, P) == cudaSuccess ? 0 : 1;
 }
 
 // Workers of a launch: all that are resident at once, no more than there are
 // units (parts of 8 k steps) with every row taking part.
-template <int CG, int KIND>
+template <int CG, int KIND, int NT>
 int tg_workers(const TgParams &P) {
-  int w = tg_resident<CG, KIND>();
+  int w = tg_resident<CG, KIND, NT>();
   if (w > 0) {
-    const TgPlan p = tg_plan<CG, KIND>(P, P.piece, P.M, w);
+    const TgPlan p = tg_plan<CG, KIND, NT>(P, P.piece, P.M, w);
     int64_t units = p.s[0].tiles;
     if (KIND == TG_GRAD) {
       units = 0;
@@ -407,19 +407,37 @@ int tg_workers(const TgParams &P) {
   }
   return w;
 }
-template <int CG, int KIND>
+template <int CG, int KIND, int NT = 256>
 int launch_tgemm(const TgParams &P, cudaStream_t stream) {
-  const int w = tg_workers<CG, KIND>(P);
-  return w > 0 ? launch_tgemm_kind<CG, KIND>(P, w, stream) : 1;
+  const int w = tg_workers<CG, KIND, NT>(P);
+  return w > 0 ? launch_tgemm_kind<CG, KIND, NT>(P, w, stream) : 1;
+}
+
+// 128 x 128 tiles of a product.
+int64_t tg_small_tiles(int M, int N) {
+  return (int64_t)((M + 127) / 128) * ((N + 127) / 128);
+}
+
+// Whether the gradients of a single piece, not cut in any case (plan), go in
+// 128 x 128 tiles: while those fit on the CTAs at once.  A tile's k steps and
+// epilogue take half the time then.
+bool tg_small_grad(const TgParams &P, const TgPlan &plan) {
+  const int r = tg_resident<1, TG_GRAD, 128>();
+  if (P.hdr != nullptr || r <= 0 || !plan.apart || plan.s[0].dealt + plan.s[1].dealt > 0)
+    return false;
+  const TgPlan p = tg_plan<1, TG_GRAD, 128>(P, 0, P.M, r);
+  return (int64_t)p.s[0].tiles + p.s[1].tiles <= r;
 }
 
 // TG_GRAD on piece P.piece of np, and the sums of the tiles that were cut.
 // Without a device count the cuts are known here, and there may be none.
 template <int CG>
 int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
-  const int w = tg_workers<CG, TG_GRAD>(P);
-  if (w <= 0 || launch_tgemm_kind<CG, TG_GRAD>(P, w, stream)) return 1;
+  const int w = tg_workers<CG, TG_GRAD, 256>(P);
+  if (w <= 0) return 1;
   const TgPlan p = tg_plan<CG, TG_GRAD>(P, P.piece, P.M, w);
+  if (np == 1 && tg_small_grad(P, p)) return launch_tgemm<1, TG_GRAD, 128>(P, stream);
+  if (launch_tgemm_kind<CG, TG_GRAD, 256>(P, w, stream)) return 1;
   bool join = P.hdr != nullptr;  // the cuts are not known here
   for (int x = 1; x < p.groups && !join; ++x) join = tg_cut(p, x, p.groups).off != 0;
   if (!join || w < 2) return 0;
@@ -451,8 +469,8 @@ bool tg_pairs(int M) { return M > 128; }
 
 // X [M][K] and W [N][K] of the products with tokens as rows
 template <int CG>
-bool nt_maps(TgParams &P, const void *X, const void *W, int M, int N, int K) {
-  return make_map_bf16(&P.A, X, K, M, 64, 128) && make_map_bf16(&P.B, W, K, N, 64, 256 / CG);
+bool nt_maps(TgParams &P, const void *X, const void *W, int M, int N, int K, int NT = 256) {
+  return make_map_bf16(&P.A, X, K, M, 64, 128) && make_map_bf16(&P.B, W, K, N, 64, NT / CG);
 }
 
 template <int CG>
@@ -578,7 +596,8 @@ int gau_project_backward_cg(const void *X, const void *Wt, const void *dU, const
   const ProjectGradLayout L = project_grad_layout(M, N, d);
   char *ws = static_cast<char *>(workspace);
   TgParams P = {}, Q = {};
-  if (!nt_maps<CG>(P, X, Wt, M, N, d)) return 2;
+  const bool small = tg_small_tiles(M, N) <= tg_resident<1, TG_SILU, 128>();
+  if (!(small ? nt_maps<1>(P, X, Wt, M, N, d, 128) : nt_maps<CG>(P, X, Wt, M, N, d))) return 2;
   P.M = M, P.N = N, P.K = d;
   P.cap_boxes = L.cap_boxes;
   P.n0 = e, P.n1 = 2 * e;
@@ -596,7 +615,9 @@ int gau_project_backward_cg(const void *X, const void *Wt, const void *dU, const
   Q.D0 = static_cast<__nv_bfloat16 *>(dWt);
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
   Q.slots = reinterpret_cast<float *>(ws + L.slots);
-  if (int rc = launch_tgemm<CG, TG_SILU>(P, stream)) return rc;
+  if (int rc = small ? launch_tgemm<1, TG_SILU, 128>(P, stream)
+                     : launch_tgemm<CG, TG_SILU>(P, stream))
+    return rc;
   return launch_grad<CG>(Q, 1, stream);
 }
 
