@@ -302,6 +302,10 @@ constexpr size_t kTgSlotBytes = 4 * 128 * 256;
 inline size_t tg_tiles(size_t M, size_t N) {  // 128 x 256 tiles (rows in pairs)
   return 2 * ((M + 255) / 256) * ((N + 255) / 256);
 }
+// 128 x 128 tiles, of products small enough for all of them to run at once.
+inline int64_t tg_small_tiles(int M, int N) {
+  return (((int64_t)M + 127) / 128) * (((int64_t)N + 127) / 128);
+}
 inline size_t tg_slot_bytes() { return 2 * kTgMaxCtas * kTgSlotBytes; }
 // Boxes of 64 tokens x 64 columns for all N columns of M tokens.
 inline int64_t tg_boxes(int M, int N) {
@@ -309,7 +313,8 @@ inline int64_t tg_boxes(int M, int N) {
 }
 
 // Vocabulary loss: header, compact rows (index, target, X), the target's
-// logit, and the partial maxima and sums [2 ceil(V / 256)][M] fp32 pairs.
+// logit, and the partial maxima and sums [2 ceil(V / 256)][M] fp32 pairs (of
+// half as many columns each where 128 x 128 tiles may be taken).
 struct VocabLossLayout {
   size_t hdr, idx, tgt, ztgt, Xc, part, total;
 };
@@ -321,7 +326,8 @@ inline VocabLossLayout vocab_loss_layout(int M, int V, int d) {
   L.ztgt = L.tgt + align256(4 * (size_t)M);
   L.Xc = L.ztgt + align256(4 * (size_t)M);
   L.part = L.Xc + align256(2 * (size_t)M * d);
-  L.total = L.part + align256(8 * (size_t)M * 2 * (((size_t)V + 255) / 256));
+  const size_t cols = tg_small_tiles(M, V) <= kTgMaxCtas ? 128 : 256;
+  L.total = L.part + align256(8 * (size_t)M * 2 * (((size_t)V + cols - 1) / cols));
   return L;
 }
 

@@ -4,7 +4,7 @@
 // features) are columns v, model features are d:
 //
 //   TG_LSE   Z = X W^T           per row the maximum and the sum of
-//                                exp(z - maximum) of every 128 columns, and the
+//                                exp(z - maximum) of every NT / 2 columns, and the
 //                                target's logit; Z itself is not stored
 //   TG_PROB  Z = X W^T           the piece's (softmax(z) - onehot) * g, bf16
 //   TG_SILU  Z = X W^T           dpre = dOut * silu'(z), bf16
@@ -18,7 +18,8 @@
 // c * n_tok64 + t.  The same box is a K-major tile for dX and an MN-major one
 // for dW, and the width of a piece can be chosen on the device.
 //
-// A unit is a tile of 128 CG x 256 outputs: CG = 1 one CTA, CG = 2 a pair of
+// A unit is a tile of 128 CG x NT outputs: NT = 256, or 128 (with CG = 1) for
+// products of so few tiles that all run at once; CG = 1 one CTA, CG = 2 a pair of
 // CTAs on one tcgen05 tile of M = 256 (each holds its 128 rows of A, half of
 // B's 256 rows and the accumulator of its rows).  A pair reads (128 + 128) x 64
 // operands a CTA and k step instead of (128 + 256) x 64, which is what bounds
@@ -106,7 +107,7 @@ struct TgParams {
   int n_tops;
   float *gmax_out;
   // TG_LSE
-  float2 *part;        // [2 ceil(N / 256)][M]
+  float2 *part;        // [2 ceil(N / NT)][M]
   float *ztgt;         // [M]
   const int *tgt;      // [M]
   // TG_PROB
@@ -213,9 +214,10 @@ __host__ __device__ inline TgPlan tg_plan(const TgParams &P, int piece, int coun
 // tiles of 128 steps and 96 of 252 on 76 pairs: busy 84 % of the time).  The
 // tiles of a panel that a cut goes through are summed from their parts by a
 // second kernel; a part keeps 8 k steps at least, and panels of less than 16
-// are not cut, nor any where that kernel costs more than the cuts save.  Without panels (each worker on a tile of its own, cut at its
-// own place) A came from DRAM once for every tile beside another: 171 us
-// instead of 142 at 2048 x 50001 x 512.  Where group w's part of the line begins:
+// are not cut, nor any where that kernel costs more than the cuts save.  Without
+// panels (each worker on a tile of its own, cut at its own place) A came from
+// DRAM once for every tile beside another: 171 us instead of 142 at 2048 x 50001
+// x 512.  Where group w's part of the line begins:
 struct TgCut {
   int pi, tile, off;  // the panel among the cut ones; k steps of it before the cut
   int pos;
@@ -535,7 +537,8 @@ __device__ __forceinline__ float tg_rows_as_they_are(const TgParams &P, int coun
     if (lane == 0) P.keep[r] = has ? 1 : 0;
     const uint4 *src = reinterpret_cast<const uint4 *>(P.X + (int64_t)r * P.K);
     uint4 *dst = reinterpret_cast<uint4 *>(P.Xz + (int64_t)r * P.K);
-    for (int v = lane; v < P.K / 8; v += 32) dst[v] = has ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
+    for (int v = lane; v < P.K / 8; v += 32)
+      dst[v] = has ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
   }
   return top;
 }
@@ -544,7 +547,7 @@ template <int CG, int KIND, int NT>
 __global__ void __launch_bounds__(TG_THREADS, 1)
     tc_tgemm(const __grid_constant__ TgParams P) {
   using Cfg = TgCfg<CG, KIND, NT>;
-  static_assert(NT == 256 || (CG == 1 && (KIND == TG_SILU || KIND == TG_GRAD)));
+  static_assert(NT == 256 || CG == 1);
   constexpr int RING = Cfg::RING;
   // With few of the rows taking part the pieces are wide and the last launches
   // have none (every kernel ahead has waited for the one that counts).
@@ -851,50 +854,53 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
         if (lane == 0) tg_arrive_leader<CG>(&acc_empty[buf]);
       };
       if constexpr (KIND == TG_LSE) {
-        uint32_t r[4][32];
+        constexpr int NC = kHalf / 32;
+        uint32_t r[NC][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(dcol + 32 * c, r[c]);
+        for (int c = 0; c < NC; ++c) tmem_ld32(dcol + 32 * c, r[c]);
         tmem_ld_wait();
         release();
         // columns past the vocabulary count as -infinity
-        if (c0 + 128 > P.N) {
+        if (c0 + kHalf > P.N) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (c0 + 32 * c + j >= P.N) r[c][j] = 0xFF800000u;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[NC], sm[NC];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < NC; ++c) mx[c] = -INFINITY, sm[c] = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) mx[c] = fmaxf(mx[c], __uint_as_float(r[c][j]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        float top = fmaxf(mx[0], mx[1]);
+        if constexpr (NC == 4) top = fmaxf(top, fmaxf(mx[2], mx[3]));
         // a row of -infinities has the sum 0 (not exp(-inf + inf))
         const float ref = top == -INFINITY ? 0.f : top * kLog2e;
-        float sm[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             sm[c] += tg_exp2(fmaf(__uint_as_float(r[c][j]), kLog2e, -ref));
-        if (in_rows)
-          P.part[(int64_t)(u.nt * 2 + half) * P.M + m] =
-              make_float2(top, (sm[0] + sm[1]) + (sm[2] + sm[3]));
+        float sum = sm[0] + sm[1];
+        if constexpr (NC == 4) sum += sm[2] + sm[3];
+        if (in_rows) P.part[(int64_t)(u.nt * 2 + half) * P.M + m] = make_float2(top, sum);
         const int at = row_at;
-        if (__any_sync(0xffffffffu, at >= 0 && at < 128)) {
+        if (__any_sync(0xffffffffu, at >= 0 && at < kHalf)) {
           float z = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (at == 32 * c + j) z = __uint_as_float(r[c][j]);
-          if (at >= 0 && at < 128) P.ztgt[m] = z;
+          if (at >= 0 && at < kHalf) P.ztgt[m] = z;
         }
       } else {
         // 64 columns at a time, in chunks of 32
         const float g = KIND == TG_PROB && gmax > 0.f ? row_g / gmax : row_g;
-        const bool any = KIND == TG_PROB && __any_sync(0xffffffffu, row_at >= 0 && row_at < 128);
+        const bool any = KIND == TG_PROB && __any_sync(0xffffffffu, row_at >= 0 && row_at < kHalf);
         const int left = plan.width - c0;  // TG_PROB: columns of the piece from here on
         // TG_GRAD: problem 1 over several pieces adds to what the pieces before
         // left; a cut tile's part goes to the place of the worker's tile that
@@ -906,9 +912,9 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
         float *slot = nullptr;
         bool wide = false;
         if constexpr (KIND == TG_GRAD) {
+          const int cut = (2 * worker + (u.ks0 > 0 ? 0 : 1)) * CG + (int)rank;
           slot = u.whole ? P.sums + ((int64_t)(u.mt * CG + (int)rank) * h.Nt + u.nt) * kTgSlotFloats
-                         : P.slots + (int64_t)((2 * worker + (u.ks0 > 0 ? 0 : 1)) * CG + (int)rank) *
-                                         kTgSlotFloats;
+                         : P.slots + (int64_t)cut * kTgSlotFloats;
           wide = P.K % 16 == 0 && (reinterpret_cast<uintptr_t>(u.pi ? P.D1 : P.D0) & 31u) == 0;
         }
         bool ok = true;
@@ -919,7 +925,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
           tmem_ld32(dcol + 64 * q2 + 32, r[1]);
           uint8_t *piece = stage + q2 * Cfg::PIECE;
           if constexpr (KIND == TG_PROB) {  // the store from this piece a unit ago has read it
-            if (lane == 0) bulk_wait_group_read<1>();
+            if (lane == 0) bulk_wait_group_read<NQ - 1>();
             __syncwarp();
           }
           if constexpr (KIND == TG_SILU) {
@@ -949,7 +955,7 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
                   if (row_at == 32 * c + j)  // (p - 1) g, the difference formed first
                     v[j] = (tg_exp2(fmaf(__uint_as_float(r[c2][j]), kLog2e, -row_lse)) - 1.f) * g;
               }
-              if (!in_rows || left < 128) {
+              if (!in_rows || left < kHalf) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                   if (!in_rows || 32 * c + j >= left) v[j] = 0.f;
@@ -991,7 +997,8 @@ __global__ void __launch_bounds__(TG_THREADS, 1)
               if (!direct) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                  *reinterpret_cast<float4 *>(slot + tg_slot_offset(row, half * (kHalf / 4) + c * 8 + j)) =
+                  *reinterpret_cast<float4 *>(
+                      slot + tg_slot_offset(row, half * (kHalf / 4) + c * 8 + j)) =
                       make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
               } else if (out != nullptr) {
 #pragma unroll

@@ -12,9 +12,9 @@
 // device; every kernel reads it there, so the calls can be captured.  Few rows
 // are taken as they are (vocab_compact), a launch fewer in either direction.
 //
-// The forward pass keeps, per row and 128 columns, the maximum and the sum of
-// exp(z - maximum), 1/32 of the logits' bytes at bf16; vocab_reduce
-// joins them.  The backward pass forms the logits again, a piece of the
+// The forward pass keeps, per row and 128 columns (64 of a small product), the
+// maximum and the sum of exp(z - maximum), 1/32 of the logits' bytes at bf16;
+// vocab_reduce joins them.  The backward pass forms the logits again, a piece of the
 // vocabulary at a time, as (p - onehot) g / max|g| in bf16 (the scale goes
 // back in fp32 at the end, so that equal weights are not rounded), and takes
 // both gradients of the piece from it in one launch.  dX adds up over the
@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(32 * kReduceLanes)
   // (top, sum) with sum = sum exp(z - top); (-infinity, 0) is nothing
   auto join = [](float2 a, float2 b) {
     const float top = fmaxf(a.x, b.x), ref = top == -INFINITY ? 0.f : top;
-    return make_float2(top, a.y * tg_exp2((a.x - ref) * kLog2e) + b.y * tg_exp2((b.x - ref) * kLog2e));
+    return make_float2(
+        top, a.y * tg_exp2((a.x - ref) * kLog2e) + b.y * tg_exp2((b.x - ref) * kLog2e));
   };
   float2 t = make_float2(-INFINITY, 0.f);
   if (m < count) {
@@ -363,7 +364,8 @@ int tg_resident() {
   if (!once.run([] {
         int d = 0, n = 0;
         if (cudaGetDevice(&d) != cudaSuccess ||
-            cudaFuncSetAttribute(tc_tgemm<CG, KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            cudaFuncSetAttribute(tc_tgemm<CG, KIND, NT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)TgCfg<CG, KIND, NT>::SMEM) != cudaSuccess)
           return false;
         n = num_sms() / CG;
@@ -413,9 +415,17 @@ int launch_tgemm(const TgParams &P, cudaStream_t stream) {
   return w > 0 ? launch_tgemm_kind<CG, KIND, NT>(P, w, stream) : 1;
 }
 
-// 128 x 128 tiles of a product.
-int64_t tg_small_tiles(int M, int N) {
-  return (int64_t)((M + 127) / 128) * ((N + 127) / 128);
+// Whether a product with its tokens as rows goes in 128 x 128 tiles: while those
+// fit on the CTAs at once.  A tile's k steps and epilogue take half the time
+// then: projection gradients of 1001 x 520, e 448, s 64 16.6 us (CTA pairs
+// 22.1), the loss's gradients of 88 x 164 x 560 13.1 (18.8).
+template <int KIND>
+bool tg_small(int M, int N) {
+  return tg_small_tiles(M, N) <= tg_resident<1, KIND, 128>();
+}
+template <int CG, int KIND>
+int launch_nt(const TgParams &P, bool small, cudaStream_t stream) {
+  return small ? launch_tgemm<1, KIND, 128>(P, stream) : launch_tgemm<CG, KIND>(P, stream);
 }
 
 // Whether the gradients of a single piece, not cut in any case (plan), go in
@@ -458,7 +468,7 @@ int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
 // Whether the vocabulary loss makes its rows compact.  Not up to 128 rows (one
 // tile in any case), nor up to 512 while all of them cost less in the products
 // (8 GFLOP, 5 us) than the launch that would sort them out: 455 rows against
-// 2245 x 680 take 40 us forward and backward as they are, 51 compact.
+// 2245 x 680 took 40 us forward and backward as they are, 51 compact.
 bool vocab_compact(int M, int V, int d) {
   return M > 512 || (M > 128 && 2.0 * M * V * d > 8e9);
 }
@@ -469,8 +479,9 @@ bool tg_pairs(int M) { return M > 128; }
 
 // X [M][K] and W [N][K] of the products with tokens as rows
 template <int CG>
-bool nt_maps(TgParams &P, const void *X, const void *W, int M, int N, int K, int NT = 256) {
-  return make_map_bf16(&P.A, X, K, M, 64, 128) && make_map_bf16(&P.B, W, K, N, 64, NT / CG);
+bool nt_maps(TgParams &P, const void *X, const void *W, int M, int N, int K, bool small) {
+  return make_map_bf16(&P.A, X, K, M, 64, 128) &&
+         make_map_bf16(&P.B, W, K, N, 64, small ? 128 : 256 / CG);
 }
 
 template <int CG>
@@ -496,14 +507,15 @@ int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *lo
   }
 
   TgParams P = {};
-  if (!nt_maps<CG>(P, compact ? a.Xc : a.X, W, M, V, d)) return 2;
+  const bool small = tg_small<TG_LSE>(M, V);
+  if (!nt_maps<CG>(P, compact ? a.Xc : a.X, W, M, V, d, small)) return 2;
   P.M = M, P.N = V, P.K = d;
   P.hdr = compact ? a.hdr : nullptr;
   P.target = compact ? nullptr : target;
   P.part = reinterpret_cast<float2 *>(ws + L.part);
   P.ztgt = reinterpret_cast<float *>(ws + L.ztgt);
   P.tgt = a.tgt;
-  if (int rc = launch_tgemm<CG, TG_LSE>(P, stream)) return rc;
+  if (int rc = launch_nt<CG, TG_LSE>(P, small, stream)) return rc;
 
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -516,7 +528,8 @@ int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *lo
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, vocab_reduce, (const float2 *)P.part, (const float *)P.ztgt,
                             (const int *)a.idx, P.hdr, P.target, loss, lse,
-                            2 * ((V + 255) / 256), M, V) == cudaSuccess
+                            small ? 2 * ((V + 127) / 128) : 2 * ((V + 255) / 256), M,
+                            V) == cudaSuccess
              ? 0
              : 1;
 }
@@ -549,7 +562,9 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   }
 
   TgParams P = {}, Q = {};
-  if (!nt_maps<CG>(P, compact ? a.Xc : a.X, W, M, V, d)) return 2;
+  const TgPieces pieces = tg_pieces(M, V, L.cap_boxes);  // with fewer rows no more of them
+  const bool small = tg_small<TG_PROB>(M, pieces.tp * 256);
+  if (!nt_maps<CG>(P, compact ? a.Xc : a.X, W, M, V, d, small)) return 2;
   P.M = M, P.N = V, P.K = d;
   P.cap_boxes = L.cap_boxes;
   P.gmax = &a.hdr->gmax;
@@ -579,11 +594,10 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
   Q.sums = reinterpret_cast<float *>(ws + L.sums);
   Q.slots = reinterpret_cast<float *>(ws + L.slots);
-  const int np = tg_pieces(M, V, L.cap_boxes).np;  // with fewer rows no more pieces
-  for (int k = 0; k < np; ++k) {
+  for (int k = 0; k < pieces.np; ++k) {
     P.piece = Q.piece = k;
-    if (int rc = launch_tgemm<CG, TG_PROB>(P, stream)) return rc;
-    if (int rc = launch_grad<CG>(Q, np, stream)) return rc;
+    if (int rc = launch_nt<CG, TG_PROB>(P, small, stream)) return rc;
+    if (int rc = launch_grad<CG>(Q, pieces.np, stream)) return rc;
   }
   return 0;
 }
@@ -596,8 +610,8 @@ int gau_project_backward_cg(const void *X, const void *Wt, const void *dU, const
   const ProjectGradLayout L = project_grad_layout(M, N, d);
   char *ws = static_cast<char *>(workspace);
   TgParams P = {}, Q = {};
-  const bool small = tg_small_tiles(M, N) <= tg_resident<1, TG_SILU, 128>();
-  if (!(small ? nt_maps<1>(P, X, Wt, M, N, d, 128) : nt_maps<CG>(P, X, Wt, M, N, d))) return 2;
+  const bool small = tg_small<TG_SILU>(M, N);
+  if (!nt_maps<CG>(P, X, Wt, M, N, d, small)) return 2;
   P.M = M, P.N = N, P.K = d;
   P.cap_boxes = L.cap_boxes;
   P.n0 = e, P.n1 = 2 * e;
@@ -615,9 +629,7 @@ int gau_project_backward_cg(const void *X, const void *Wt, const void *dU, const
   Q.D0 = static_cast<__nv_bfloat16 *>(dWt);
   Q.D1 = static_cast<__nv_bfloat16 *>(dX);
   Q.slots = reinterpret_cast<float *>(ws + L.slots);
-  if (int rc = small ? launch_tgemm<1, TG_SILU, 128>(P, stream)
-                     : launch_tgemm<CG, TG_SILU>(P, stream))
-    return rc;
+  if (int rc = launch_nt<CG, TG_SILU>(P, small, stream)) return rc;
   return launch_grad<CG>(Q, 1, stream);
 }
 

@@ -158,3 +158,20 @@ def test_refusals():
                 lambda: m.gau_output_backward(X, Wt[:32], g[:, :32].contiguous())):
         with pytest.raises(m.FmcaError):
             bad()
+
+
+# both sides of the sizes up to which a product goes in 128 x 128 tiles, and the
+# two launches of a call on different ones
+TILES = [(100, 64, 9664, 64), (100, 64, 9728, 64), (1200, 512, 960, 64), (1001, 2000, 448, 64),
+         (300, 2600, 192, 64), (300, 2696, 192, 64)]
+
+
+@pytest.mark.parametrize("M,d,e,s", TILES)
+def test_project_backward_in_either_tile(M, d, e, s):
+    test_project_backward(M, d, e, s)
+
+
+@pytest.mark.parametrize("M,e,d", [(1000, 1152, 1024), (1000, 1224, 1024), (129, 4864, 384),
+                                   (129, 4872, 384)])
+def test_output_backward_in_either_tile(M, e, d):
+    test_output_backward(M, e, d)

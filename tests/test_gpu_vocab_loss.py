@@ -318,3 +318,12 @@ def test_shifted_labels(M):
     loss, lse = m.vocab_loss(X, W, t1)
     got = (loss, lse) + m.vocab_loss_backward(X, W, t1, l1, g1)
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("keep", [1.0, 0.3])
+@pytest.mark.parametrize("M,V,d", [(100, 19456, 64), (100, 19457, 64), (300, 6400, 64),
+                                   (300, 6401, 64), (600, 3840, 72), (600, 3841, 72),
+                                   (2000, 1150, 64)])
+def test_both_sides_of_the_small_tiles(M, V, d, keep):
+    """Products go in 128 x 128 tiles while those fit on the CTAs at once."""
+    check(fm(), *make(M, V, d, keep, M + V))
