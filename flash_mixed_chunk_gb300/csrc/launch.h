@@ -8,6 +8,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 namespace fmca {
 
@@ -268,6 +269,31 @@ int launch_tc_backward(const void *Z, const void *V, const void *U, const float 
                        float *dgamma, float *dbeta, int B, int n, int s, int e, int C, int causal,
                        const Variant &var, void *workspace, cudaStream_t stream,
                        bool saved = false);
+
+#ifdef __CUDACC__
+// Launches `kernel` as a programmatic dependent of the work before it on
+// `stream`: it may start launching (and run its prologue) while its
+// predecessor drains.  Every such kernel waits (griddepcontrol.wait), in one
+// thread at least, for its predecessor to complete before it reads or writes,
+// so each one's completion implies all earlier ones'; the ones that let their
+// own dependents launch do so after that wait, unless they are ordinary
+// launches.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, Args &&...args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+#endif
 
 // Layer norm (norm.cu).  Rows of up to kNormWarpMaxD elements belong to a
 // warp or (norm_half: element and vector bytes) to half a block, longer ones

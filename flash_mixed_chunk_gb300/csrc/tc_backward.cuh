@@ -54,27 +54,6 @@ bool fill_problem(BgProblem &p, const BgSpec &s) {
   return true;
 }
 
-// Launches `kernel` as a programmatic dependent of the work before it on
-// `stream`: it may start launching (and run its prologue) while its
-// predecessor drains.  Every kernel of the backward pass waits
-// (griddepcontrol.wait) for its predecessor to complete before it reads, so
-// each one's completion implies all earlier ones'.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                             cudaStream_t stream, Args &&...args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
 // One tc_bgemm launch over n (1..3) independent products.
 int launch_bgemm(const BgSpec *specs, int n, cudaStream_t stream) {
   BgParams P;

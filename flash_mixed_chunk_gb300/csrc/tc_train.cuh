@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kGatherThreads) vocab_gather(GatherArgs a) {
   __shared__ float redf[kGatherThreads / 32];
   __shared__ int pos_s[kGatherThreads];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  griddep_wait();
   griddep_launch_dependents();
   const int64_t r0 = (int64_t)blockIdx.x * a.per;
   const int64_t r1 = r0 + a.per < a.M ? r0 + a.per : a.M;
@@ -451,16 +452,8 @@ int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
   bool join = P.hdr != nullptr;  // the cuts are not known here
   for (int x = 1; x < p.groups && !join; ++x) join = tg_cut(p, x, p.groups).off != 0;
   if (!join || w < 2) return 0;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(3 * kTgMaxCtas);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tg_join<CG>, P, w, P.piece == np - 1 ? 1 : 0) == cudaSuccess
+  return launch_dependent(tg_join<CG>, 3 * kTgMaxCtas, kJoinThreads, 0, stream, P, w,
+                          P.piece == np - 1 ? 1 : 0) == cudaSuccess
              ? 0
              : 1;
 }
@@ -502,8 +495,9 @@ int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *lo
   if (compact) {
     const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
     a.per = ((M + blocks - 1) / blocks + 1) / 2 * 2;
-    vocab_gather<false><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return 1;
+    if (launch_dependent(vocab_gather<false>, (M + a.per - 1) / a.per, kGatherThreads, 0, stream,
+                         a) != cudaSuccess)
+      return 1;
   }
 
   TgParams P = {};
@@ -517,19 +511,10 @@ int vocab_loss_cg(const void *X, const void *W, const int64_t *target, float *lo
   P.tgt = a.tgt;
   if (int rc = launch_nt<CG, TG_LSE>(P, small, stream)) return rc;
 
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((M + 31) / 32);
-  cfg.blockDim = dim3(32 * kReduceLanes);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, vocab_reduce, (const float2 *)P.part, (const float *)P.ztgt,
-                            (const int *)a.idx, P.hdr, P.target, loss, lse,
-                            small ? 2 * ((V + 127) / 128) : 2 * ((V + 255) / 256), M,
-                            V) == cudaSuccess
+  return launch_dependent(vocab_reduce, (M + 31) / 32, 32 * kReduceLanes, 0, stream,
+                          (const float2 *)P.part, (const float *)P.ztgt, (const int *)a.idx, P.hdr,
+                          P.target, loss, lse, 2 * (small ? (V + 127) / 128 : (V + 255) / 256), M,
+                          V) == cudaSuccess
              ? 0
              : 1;
 }
@@ -557,8 +542,9 @@ int vocab_loss_backward_cg(const void *X, const void *W, const int64_t *target,
   if (compact) {
     const int blocks = M < kTgMaxCtas * 2 ? M : kTgMaxCtas * 2;
     a.per = ((M + blocks - 1) / blocks + 1) / 2 * 2;
-    vocab_gather<true><<<(M + a.per - 1) / a.per, kGatherThreads, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return 1;
+    if (launch_dependent(vocab_gather<true>, (M + a.per - 1) / a.per, kGatherThreads, 0, stream,
+                         a) != cudaSuccess)
+      return 1;
   }
 
   TgParams P = {}, Q = {};
