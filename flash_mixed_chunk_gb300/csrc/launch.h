@@ -300,14 +300,16 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
 // (to kNormMaxD) to a block.  The backward pass deals its rows to
 // norm_backward_blocks blocks at most, one partial row of dw and db each.
 constexpr int kNormWarpMaxD = 1024, kNormMaxD = 8192;
-constexpr int kNormBackwardBlocks = 304;
+constexpr int kNormSms = 152;
 inline bool norm_half(int d, size_t elem, size_t vec) {
   return d <= kNormWarpMaxD && d > (vec == 16 ? 512 : 256) && (elem == 4 || vec < 16);
 }
 inline int norm_backward_blocks(int M, int d) {
   const int64_t rows = d <= 256 ? 8 : d <= kNormWarpMaxD ? 2 : 1;
   const int64_t blocks = ((int64_t)M + rows - 1) / rows;
-  return (int)(blocks < kNormBackwardBlocks ? blocks : kNormBackwardBlocks);
+  // three on an SM of rows with up to 8 elements a thread in a warp or a block
+  const int64_t most = kNormSms * (d <= 256 || (d > kNormWarpMaxD && d <= 2048) ? 3 : 2);
+  return (int)(blocks < most ? blocks : most);
 }
 inline size_t norm_backward_bytes(int M, int d) {
   return align256(sizeof(float) * 2 * (size_t)d * (size_t)norm_backward_blocks(M, d));

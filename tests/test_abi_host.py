@@ -415,11 +415,14 @@ def test_layer_norm_rejects_before_queueing():
 
     nb = fm.flash_mca_layer_norm_backward_workspace_bytes
     # one partial row of dw and db a block: at least 8 rows a block up to d =
-    # 256, 2 up to 1024, one beyond; 304 blocks at most
+    # 256, 2 up to 1024, one beyond; 304 blocks at most (456 up to d = 256 and
+    # from 1025 to 2048)
     up = lambda v: (v + 255) // 256 * 256  # noqa: E731
     assert nb(1, 768) == up(8 * 768) and nb(17, 768) == up(9 * 8 * 768)
     assert nb(17, 256) == up(3 * 8 * 256)
     assert nb(100000, 768) == up(304 * 8 * 768) and nb(5, 1025) == up(5 * 8 * 1025)
+    assert nb(100000, 256) == up(456 * 8 * 256) and nb(100000, 2048) == up(456 * 8 * 2048)
+    assert nb(100000, 257) == up(304 * 8 * 257) and nb(100000, 2049) == up(304 * 8 * 2049)
     assert nb(0, 768) == 0 and nb(4, 0) == 0 and nb(4, 8193) == 0
 
     dy, hh, dh, dx, dw, db, ws = [P + (k << 24) for k in range(8, 15)]
@@ -499,8 +502,11 @@ def test_vocab_loss_rejects_before_queueing():
         assert f(0, 10, 64) == 0 and f(4, 0, 64) == 0 and f(4, 10, 0) == 0 and f(4, 10, 12) == 0
         assert f(1 << 22, 10, 512) == 0 and f(4, 1 << 22, 512) == 0
     up = lambda v: (v + 255) // 256 * 256  # noqa: E731
-    # index, target and logit of a row, X, two fp32 pairs a row and 256 columns
-    assert fb(100, 1000, 64) == 256 + 3 * up(400) + up(100 * 128) + up(100 * 8 * 2 * 4)
+    # index, target and logit of a row, X, two fp32 pairs a row and 256 columns (128
+    # while the tiles of 128 x 128 are 152 at most)
+    assert fb(100, 1000, 64) == 256 + 3 * up(400) + up(100 * 128) + up(100 * 8 * 2 * 8)
+    assert fb(100, 19456, 64) == 256 + 3 * up(400) + up(100 * 128) + up(100 * 8 * 2 * 152)
+    assert fb(100, 19457, 64) == 256 + 3 * up(400) + up(100 * 128) + up(100 * 8 * 2 * 77)
     # the logits never lie in the workspace: a piece of 256 MiB at most
     assert bb(16384, 250000, 64) < (256 << 20) + (64 << 20)
     assert fb(16384, 250000, 64) < 16384 * 250000 * 2 / 16

@@ -243,3 +243,10 @@ def test_backward_of_many_rows(M, d, dt, residual):
     check_backward(dy, h, w, dh, dx, dw, db, dt)
     again = m.layer_norm_backward(dy, h, w, mean, rstd, dh)
     assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))
+
+
+@pytest.mark.parametrize("M,d,dt", [(5000, 256, BF), (5000, 1536, BF), (3000, 2048, BF),
+                                    (5000, 256, F32), (1000, 1028, F32)],
+                         ids=lambda v: str(v).removeprefix("torch."))
+def test_backward_with_three_blocks_an_sm(M, d, dt):
+    test_backward_of_many_rows(M, d, dt, True)
