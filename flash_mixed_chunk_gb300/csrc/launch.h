@@ -296,13 +296,14 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
 #endif
 
 // Layer norm (norm.cu).  Rows of up to kNormWarpMaxD elements belong to a
-// warp or (norm_half: element and vector bytes) to half a block, longer ones
-// (to kNormMaxD) to a block.  The backward pass deals its rows to
+// warp or (norm_part, of element and vector bytes: its threads, else 0) to a part
+// of a block, longer ones (to kNormMaxD) to a block.  The backward pass deals its rows to
 // norm_backward_blocks blocks at most, one partial row of dw and db each.
 constexpr int kNormWarpMaxD = 1024, kNormMaxD = 8192;
 constexpr int kNormSms = 152;
-inline bool norm_half(int d, size_t elem, size_t vec) {
-  return d <= kNormWarpMaxD && d > (vec == 16 ? 512 : 256) && (elem == 4 || vec < 16);
+inline int norm_part(int d, size_t elem, size_t vec) {
+  if (d > kNormWarpMaxD || d <= 256) return 0;
+  return vec == 16 ? (elem == 4 && d > 512 ? 128 : 0) : d > 512 ? 128 : 64;
 }
 inline int norm_backward_blocks(int M, int d) {
   const int64_t rows = d <= 256 ? 8 : d <= kNormWarpMaxD ? 2 : 1;

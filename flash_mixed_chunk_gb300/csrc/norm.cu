@@ -19,8 +19,9 @@
 // 8192): 8, 16, 24 or 32 elements a thread, in 16-byte vectors where d allows
 // it, else 4-byte ones, else single elements.  Rows that would fill a warp's
 // registers (and, backward, its shared memory) with few threads at work (fp32
-// beyond 512 elements, narrow vectors beyond 256) belong to half a block: 5001
-// fp32 rows of 1001 took 17 us backward instead of 32 (13 since, held).
+// beyond 512 elements, narrow vectors beyond 256) belong to half a block or (up
+// to 512) a quarter: 5001 fp32 rows of 1001 took 17 us backward instead of 32, and
+// 9001 of 301 13.4 with a quarter instead of 17.3.
 //
 // Every kernel is a programmatic dependent of what runs ahead of it on the
 // stream: its blocks are on their way while that ends, and read nothing before
@@ -42,6 +43,7 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr size_t kNormMaxSmem = 200 << 10;  // of a block of the backward pass
+constexpr size_t kNormSmSmem = 220 << 10;   // of an SM's blocks
 
 template <int BYTES>
 struct Raw;
@@ -107,6 +109,15 @@ __device__ __forceinline__ void load_w(const float *__restrict__ p, float *out) 
 // of a block or the block (two sets of shared words in turn, so that one barrier
 // a sum is enough; some warps meet at a barrier of their own).
 template <int GROUP, int THREADS>
+__device__ __forceinline__ void group_sync() {
+  if constexpr (GROUP == 32)
+    __syncwarp();
+  else if constexpr (GROUP == THREADS)
+    __syncthreads();
+  else
+    named_bar_sync(1 + threadIdx.x / GROUP, GROUP);
+}
+template <int GROUP, int THREADS>
 __device__ __forceinline__ float2 group_sum2(float2 a, float2 (*red)[THREADS / 32], int &turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -118,10 +129,7 @@ __device__ __forceinline__ float2 group_sum2(float2 a, float2 (*red)[THREADS / 3
     turn ^= 1;
     if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = a;
     const int grp = threadIdx.x / GROUP;
-    if constexpr (GROUP == THREADS)
-      __syncthreads();
-    else
-      named_bar_sync(1 + grp, GROUP);
+    group_sync<GROUP, THREADS>();
     a = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < GROUP / 32; ++i) {
@@ -226,6 +234,12 @@ __device__ __forceinline__ void copy_async(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
                  : "memory");
 }
+// 16 bytes of which the first n exist (the others are written as 0)
+__device__ __forceinline__ void copy_async_n(void *dst, const void *src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(n)
+               : "memory");
+}
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -234,26 +248,60 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// How the backward pass brings its rows: with up to 8 elements a thread it holds
-// the weights and the row's dy and h in registers (N * VEC <= 8), else it reads
-// them twice.  16-byte vectors come through a ring in shared memory (copied
-// asynchronously, which costs no registers: the group's current row and the
-// next, three operands each); 4-byte ones too, or, held, one row ahead in
-// registers (5001 fp32 rows of 1001 with a residual: 14.3 us, through the ring
-// 18.1; 16-byte vectors the other way round, 16384 bf16 rows of 1024: 37.2 and
-// 32.8); single 2-byte elements are read in place (ahead, they spill: 16.0 us
-// instead of 13.4 for 5001 rows of 1001).
-constexpr int kNormStages = 2;
+// How the backward pass brings its rows.  With up to 8 elements a thread it
+// holds the weights and the row's dy and h in registers (N * VEC <= 8), else it
+// reads them twice.
+//   ring   each thread copies its own vectors asynchronously to its own places in
+//          shared memory, which costs no registers and needs no barrier: the
+//          row at hand and the next
+//   ahead  the next row waits in registers: 4-byte vectors that are held (5001
+//          fp32 rows of 1001 with a residual: 14.6 us, through the ring 18.1;
+//          16-byte vectors the other way round, 16384 bf16 rows of 1024: 37.2
+//          and 32.8)
+//   rows   2-byte elements, which cannot be copied one by one: the group copies
+//          whole rows, from the 16 bytes that a row's start lies in to those of
+//          its end, and reads its elements there (2000 rows of 4001: 26.9 us,
+//          read in place 73; 4-byte ones are better off as above, 18.6 and 16.4
+//          for 5001 fp32 rows of 1001)
+constexpr int kNormStages = 2, kNormRowStages = 3;
 template <typename T, int VEC, int N>
 struct NormFeed {
   static constexpr size_t kBytes = sizeof(T) * VEC;
   static constexpr bool kHold = N * VEC <= 8;
   static constexpr bool kAhead = kHold && kBytes == 4;
   static constexpr bool kRing = kBytes >= 4 && !kAhead;
+  static constexpr bool kWhole = kBytes == 2;
 };
 template <typename T, int VEC, int N, int THREADS>
 constexpr size_t norm_ring_bytes() {
   return NormFeed<T, VEC, N>::kRing ? (size_t)kNormStages * 3 * N * THREADS * sizeof(T) * VEC : 0;
+}
+// Room for a row from the 16 bytes that its start lies in to those of its end.
+__host__ __device__ inline int norm_row_bytes(int d, int elem) {
+  return (d * elem + 31) / 16 * 16;
+}
+
+// The first element of row `row` in its copy, and the copies of dy, h and dh (by
+// the threads of a group) themselves, next to each other: the elements around
+// the row come along, none beyond the last row.
+template <typename T>
+__device__ __forceinline__ int norm_row_first(int64_t row, int d) {
+  return (int)(row * d % (16 / (int)sizeof(T)));
+}
+template <typename T, int GROUP>
+__device__ __forceinline__ void norm_copy_row(uint8_t *dst, const T *dy, const T *h, const T *dh,
+                                              int64_t row, int M, int d) {
+  constexpr int kVec = 16 / (int)sizeof(T);
+  const int first = norm_row_first<T>(row, d), n = (first + d + kVec - 1) / kVec;
+  const int stride = norm_row_bytes(d, sizeof(T));
+  const int64_t begin = row * d - first, end = (int64_t)M * d;
+  for (int c = (int)threadIdx.x % GROUP; c < n; c += GROUP) {
+    const int64_t at = begin + (int64_t)c * kVec;
+    const int bytes = end - at < kVec ? (int)(end - at) * (int)sizeof(T) : 16;
+    copy_async_n(dst + 16 * c, dy + at, bytes);
+    copy_async_n(dst + stride + 16 * c, h + at, bytes);
+    if (dh != nullptr) copy_async_n(dst + 2 * stride + 16 * c, dh + at, bytes);
+  }
 }
 
 // Blocks on an SM: three where the registers allow it (held 16-byte vectors, 80 a
@@ -281,6 +329,7 @@ __global__ void __launch_bounds__(THREADS, (norm_backward_per_sm<T, VEC, N, GROU
   using P = Pack<T, VEC>;
   constexpr int kRows = THREADS / GROUP;
   constexpr bool kHold = Feed::kHold, kAhead = Feed::kAhead, kRing = Feed::kRing;
+  constexpr bool kWhole = Feed::kWhole;
   const int lane = threadIdx.x % GROUP, grp = threadIdx.x / GROUP;
   const int nv = d / VEC;
   const float inv_d = 1.0f / (float)d;
@@ -293,6 +342,14 @@ __global__ void __launch_bounds__(THREADS, (norm_backward_per_sm<T, VEC, N, GROU
   };
   auto source = [&](int op, int64_t row, int i) {
     return (op == 0 ? dy : op == 1 ? h : dh) + row * d + (int64_t)(lane + i * GROUP) * VEC;
+  };
+  // whole rows: stage, operand; and how they come
+  auto copy_of = [&](int stage, int op) {
+    return ring + ((grp * kNormRowStages + stage) * 3 + op) * norm_row_bytes(d, sizeof(T));
+  };
+  auto fetch_whole = [&](int64_t row, int stage) {
+    if (row < M) norm_copy_row<T, GROUP>(copy_of(stage, 0), dy, h, dh, row, M, d);
+    copies_commit();
   };
   P ahead[kAhead ? 3 : 1][kAhead ? N : 1];
   auto fetch = [&](int64_t row, int stage) {
@@ -323,8 +380,22 @@ __global__ void __launch_bounds__(THREADS, (norm_backward_per_sm<T, VEC, N, GROU
       if (lane + i * GROUP < nv) load_w<VEC>(weight + (lane + i * GROUP) * VEC, held_w + i * VEC);
   }
   int64_t row = (int64_t)blockIdx.x * kRows + grp;
-  fetch(row, 0);
-  for (int stage = 0; row < M; row += step, stage ^= 1) {
+  if constexpr (kWhole) {
+    fetch_whole(row, 0);
+    fetch_whole(row + step, 1);
+  } else {
+    fetch(row, 0);
+  }
+  // the row's, a row ahead like the rest of it (8192 x 1536: 27.8 us, now 24.1)
+  float next_mean = 0.f, next_rstd = 0.f;
+  if (row < M) next_mean = mean_in[row], next_rstd = rstd_in[row];
+  if constexpr (kWhole) {
+    copies_wait<1>();
+    group_sync<GROUP, THREADS>();
+  }
+  // two stages (three of whole rows) in turn
+  for (int stage = 0; row < M;
+       row += step, stage = kWhole ? (stage == 2 ? 0 : stage + 1) : stage ^ 1) {
     P held[kHold ? 3 : 1][kHold ? N : 1];  // dy, h and, of a row fetched ahead, dh
     if constexpr (kAhead) {
 #pragma unroll
@@ -332,15 +403,25 @@ __global__ void __launch_bounds__(THREADS, (norm_backward_per_sm<T, VEC, N, GROU
 #pragma unroll
         for (int i = 0; i < N; ++i) held[op][i] = ahead[op][i];
     }
-    fetch(row + step, stage ^ 1);
-    const float mean = mean_in[row], rstd = rstd_in[row];
+    if constexpr (!kWhole) fetch(row + step, stage ^ 1);
+    const float mean = next_mean, rstd = next_rstd;
+    if (row + step < M) next_mean = mean_in[row + step], next_rstd = rstd_in[row + step];
+    const T *mine[kWhole ? 3 : 1];  // whole rows: this thread's first element
+    if constexpr (kWhole) {
+#pragma unroll
+      for (int op = 0; op < 3; ++op)
+        mine[op] = reinterpret_cast<const T *>(copy_of(stage, op)) + norm_row_first<T>(row, d) +
+                   lane;
+    }
     // vector i of operand op of this row
     auto take = [&](int op, int i, P &out) {
-      if constexpr (kAhead)
+      if constexpr (kAhead) {
         out = held[op][i];
-      else
-        out.raw = *reinterpret_cast<const typename P::raw_t *>(kRing ? place(stage, op, i)
-                                                                     : source(op, row, i));
+      } else if constexpr (kRing) {
+        out.raw = *reinterpret_cast<const typename P::raw_t *>(place(stage, op, i));
+      } else {
+        out.v[0] = mine[op][i * GROUP];
+      }
     };
     auto weights = [&](int i, float *w) {
       if constexpr (kHold) {
@@ -371,7 +452,14 @@ __global__ void __launch_bounds__(THREADS, (norm_backward_per_sm<T, VEC, N, GROU
         }
       }
     }
+    if constexpr (kWhole) {
+      // the next row has come: to the whole group, once it has met
+      copies_wait<0>();
+      if constexpr (GROUP == 32) __syncwarp();
+    }
     const float2 sums = group_sum2<GROUP, THREADS>(make_float2(s1, s2), red, turn);
+    // and it has left the row before this one
+    if constexpr (kWhole) fetch_whole(row + 2 * step, stage == 0 ? 2 : stage - 1);
     const float m1 = sums.x * inv_d, m2 = sums.y * inv_d;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -415,7 +503,7 @@ __global__ void __launch_bounds__(THREADS, (norm_backward_per_sm<T, VEC, N, GROU
     }
   } else {
     // the groups' sums side by side in the ring's place, added in order
-    if constexpr (kRing) copies_wait<0>();
+    if constexpr (kRing || kWhole) copies_wait<0>();
     __syncthreads();
     float *acc = reinterpret_cast<float *>(ring);  // [kRows][2][d]
 #pragma unroll
@@ -486,17 +574,21 @@ static_assert(norm_ring_bytes<float, 4, 8, kNormThreads>() <= kNormMaxSmem,
               "two rows of every group fit");
 template <typename T, int VEC, int N, int GROUP, int THREADS = kNormThreads>
 cudaError_t launch_bwd(NormArgs &a, cudaStream_t stream) {
-  // groups of the grid: all that are resident at once, no more than rows
   constexpr int kRows = THREADS / GROUP;
-  constexpr int kMost = kNormSms * norm_backward_per_sm<T, VEC, N, GROUP, THREADS>();
-  const int64_t blocks = ((int64_t)a.M + kRows - 1) / kRows;
-  a.blocks = (int)(blocks < kMost ? blocks : kMost);
-  if (a.blocks > norm_backward_blocks(a.M, a.d)) return cudaErrorInvalidValue;  // the workspace's
   size_t smem = norm_ring_bytes<T, VEC, N, THREADS>();
+  if (NormFeed<T, VEC, N>::kWhole)
+    smem = (size_t)kRows * kNormRowStages * 3 * norm_row_bytes(a.d, sizeof(T));
   if (GROUP < THREADS) {
     const size_t sums = 2 * sizeof(float) * (size_t)a.d * kRows;
     if (sums > smem) smem = sums;
   }
+  // groups of the grid: all that are resident at once, no more than rows
+  constexpr int kPerSm = norm_backward_per_sm<T, VEC, N, GROUP, THREADS>();
+  const int most = kNormSms * (kPerSm * smem > kNormSmSmem ? 1 : kPerSm);
+  const int64_t blocks = ((int64_t)a.M + kRows - 1) / kRows;
+  a.blocks = (int)(blocks < most ? blocks : most);
+  if (a.blocks > norm_backward_blocks(a.M, a.d) || smem > kNormMaxSmem)
+    return cudaErrorInvalidValue;  // more than the workspace or the attribute below holds
   static OncePerDevice attrs;
   if (!attrs.run([] {
         return cudaFuncSetAttribute(norm_backward<T, VEC, N, GROUP, THREADS>,
@@ -544,9 +636,15 @@ int norm_wide(int M, int d, int elem) {
 }
 template <typename T, int VEC, bool kBackward>
 cudaError_t pick_group(NormArgs &a, cudaStream_t stream) {
-  if (norm_half(a.d, sizeof(T), sizeof(T) * VEC))
-    return kBackward ? launch_bwd<T, VEC, 8 / VEC, 128>(a, stream)
-                     : launch_fwd<T, VEC, 8 / VEC, 128>(a, stream);
+  const int part = norm_part(a.d, sizeof(T), sizeof(T) * VEC);
+  if constexpr (sizeof(T) * VEC < 16)
+    if (part == 64)
+      return kBackward ? launch_bwd<T, VEC, 8 / VEC, 64>(a, stream)
+                       : launch_fwd<T, VEC, 8 / VEC, 64>(a, stream);
+  if constexpr (sizeof(T) * VEC < 16 || sizeof(T) == 4)
+    if (part == 128)
+      return kBackward ? launch_bwd<T, VEC, 8 / VEC, 128>(a, stream)
+                       : launch_fwd<T, VEC, 8 / VEC, 128>(a, stream);
   if constexpr (kBackward && VEC == 8) {
     const int warps = norm_wide(a.M, a.d, sizeof(T));
     if (warps == 4) return launch_bwd<T, VEC, 1, 128, 128 * kNormWideRows>(a, stream);
@@ -570,7 +668,8 @@ cudaError_t pick(NormArgs &a, int bf16, cudaStream_t stream) {
 int norm_vec(int d, int elem) { return d * elem % 16 == 0 ? 16 : d * elem % 4 == 0 ? 4 : 2; }
 // Rows of a block of the forward pass.
 int norm_rows(int d, int elem) {
-  return norm_half(d, elem, norm_vec(d, elem)) ? 2 : d <= kNormWarpMaxD ? kNormThreads / 32 : 1;
+  const int part = norm_part(d, elem, norm_vec(d, elem));
+  return kNormThreads / (part ? part : d <= kNormWarpMaxD ? 32 : kNormThreads);
 }
 
 }  // namespace

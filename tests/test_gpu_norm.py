@@ -250,3 +250,28 @@ def test_backward_of_many_rows(M, d, dt, residual):
                          ids=lambda v: str(v).removeprefix("torch."))
 def test_backward_with_three_blocks_an_sm(M, d, dt):
     test_backward_of_many_rows(M, d, dt, True)
+
+
+# bf16 rows of odd lengths, each starting somewhere else within 16 bytes, come
+# whole: up to the longest, the last row ending with the array, rows behind it
+WHOLE = [(1, 1), (7, 3), (900, 17), (2000, 255), (1300, 257), (700, 1023), (1301, 1025),
+         (311, 4001), (200, 8191)]
+
+
+@pytest.mark.parametrize("M,d", WHOLE)
+@pytest.mark.parametrize("residual", [False, True])
+def test_backward_of_rows_that_start_anywhere(M, d, residual):
+    m = fm()
+    x, _, w, b, dy, dh = cuda(*make(M, d, BF, M + d, residual))
+    _, h, mean, rstd = m.layer_norm(x, w, b, EPS)
+    want = m.layer_norm_backward(dy, h, w, mean, rstd, dh)
+    check_backward(dy, h, w, dh, *want, BF)
+    # the same rows ahead of others that hold NaN
+    more = torch.full((M + 1, d), float("nan"), device="cuda", dtype=BF)
+    parts = [None if t is None else more.clone() for t in (dy, h, dh)]
+    for p, t in zip(parts, (dy, h, dh)):
+        if t is not None:
+            p[:M] = t
+    got = m.layer_norm_backward(parts[0][:M], parts[1][:M], w, mean, rstd,
+                                None if dh is None else parts[2][:M])
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
