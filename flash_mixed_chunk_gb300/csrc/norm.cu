@@ -309,6 +309,7 @@ __device__ __forceinline__ void norm_copy_row(uint8_t *dst, const T *dy, const T
 template <typename T, int VEC, int N, int GROUP, int THREADS>
 constexpr int norm_backward_per_sm() {
   using Feed = NormFeed<T, VEC, N>;
+  if (Feed::kAhead && THREADS > kNormThreads) return 1;  // the registers of a row ahead
   return Feed::kHold && Feed::kRing && (GROUP == 32 || GROUP == kNormThreads) ? 3 : 2;
 }
 
@@ -602,10 +603,19 @@ cudaError_t launch_bwd(NormArgs &a, cudaStream_t stream) {
                           static_cast<T *>(a.o0), a.f0, a.M, a.d);
 }
 
-// Elements a thread: the fewest of 8, 16, 24, 32 that cover the row.  A warp's
-// rows are no longer than pick_group lets them be.
+// Whether the backward pass takes rows of 2049 to 4096 elements with 512 threads,
+// so that they can be held: fp32 (2000 x 4001: 38.4 us, held 23.9; 4000 x 4000:
+// 52.6 and 45.6) and pairs of bf16 (2000 x 4002: 30.0 and 20.9), not the other
+// bf16 rows (9001 x 4000: 64.5 and 69.0, 6000 x 2561: 48.1 and 56.9).
+template <typename T, int VEC>
+constexpr bool norm_long_held() {
+  return sizeof(T) == 4 || VEC == 2;
+}
+// Elements a thread: the fewest of 8, 16, 24, 32 that cover the row.  A part of a
+// block's rows are no longer than pick_group lets them be.
 template <typename T, int VEC, int GROUP, bool kBackward>
 cudaError_t pick_n(NormArgs &a, cudaStream_t stream) {
+  constexpr int kNot = kBackward && GROUP == kNormThreads && norm_long_held<T, VEC>() ? 16 : 0;
   constexpr int kMost = GROUP > 32              ? 32
                         : sizeof(T) * VEC < 16 ? 8
                         : sizeof(T) == 4       ? 16
@@ -613,7 +623,7 @@ cudaError_t pick_n(NormArgs &a, cudaStream_t stream) {
                                                : 32;
   const int per = (a.d + GROUP * 8 - 1) / (GROUP * 8);  // eights of elements a thread
 #define FMCA_NORM(E)                                                            \
-  if constexpr ((E) <= kMost)                                                   \
+  if constexpr ((E) <= kMost && (E) != kNot)                                    \
     if (per * 8 <= (E))                                                         \
       return kBackward ? launch_bwd<T, VEC, (E) / VEC, GROUP>(a, stream)        \
                        : launch_fwd<T, VEC, (E) / VEC, GROUP>(a, stream)
@@ -636,6 +646,9 @@ int norm_wide(int M, int d, int elem) {
 }
 template <typename T, int VEC, bool kBackward>
 cudaError_t pick_group(NormArgs &a, cudaStream_t stream) {
+  if constexpr (kBackward && norm_long_held<T, VEC>())
+    if (a.d > 2048 && a.d <= 4096)
+      return launch_bwd<T, VEC, 8 / VEC, 2 * kNormThreads, 2 * kNormThreads>(a, stream);
   const int part = norm_part(a.d, sizeof(T), sizeof(T) * VEC);
   if constexpr (sizeof(T) * VEC < 16)
     if (part == 64)

@@ -275,3 +275,14 @@ def test_backward_of_rows_that_start_anywhere(M, d, residual):
     got = m.layer_norm_backward(parts[0][:M], parts[1][:M], w, mean, rstd,
                                 None if dh is None else parts[2][:M])
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("M,d,dt", [(700, 2049, F32), (500, 2052, F32), (300, 4096, F32),
+                                    (300, 4095, F32), (200, 4097, F32), (100, 5700, F32),
+                                    (700, 2050, BF), (300, 4094, BF), (200, 4098, BF),
+                                    (500, 2056, BF), (600, 511, F32), (600, 513, F32),
+                                    (600, 510, BF), (600, 514, BF), (600, 511, BF)],
+                         ids=lambda v: str(v).removeprefix("torch."))
+def test_long_rows_and_quarter_blocks(M, d, dt):
+    test_layer_norm(M, d, dt)
+    test_backward_of_many_rows(M, d, dt, True)
