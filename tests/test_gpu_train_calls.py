@@ -100,3 +100,62 @@ print("same")
     p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert p.returncode == 0 and "same" in p.stdout, p.stderr[-2000:]
+
+
+def all_calls(m, r, M):
+    """Every operator once, on inputs of the generator r; a list of results."""
+    X, W, Y, Wo, dOut = r(M, 128), r(900, 128), r(M, 256), r(128, 256), r(M, 128)
+    Wt, dU, dV, dZ = r(2 * 256 + 64, 128), r(M, 256), r(M, 256), r(M, 64)
+    t = torch.arange(M, device="cuda") % 900
+    w, dl = torch.ones(128, device="cuda"), torch.full((M,), 1.0 / M, device="cuda")
+
+    def step(first):
+        y, h, mean, rstd = m.layer_norm(X, w, w)
+        loss, lse = m.vocab_loss(X, W, t)
+        calls = {"norm": lambda: m.layer_norm(X, w, w)[:1],
+                 "norm backward": lambda: m.layer_norm_backward(dOut, h, w, mean, rstd),
+                 "loss": lambda: m.vocab_loss(X, W, t),
+                 "loss backward": lambda: m.vocab_loss_backward(X, W, t, lse, dl),
+                 "output": lambda: m.gau_output_backward(Y, Wo, dOut),
+                 "project": lambda: m.gau_project_backward(X, Wt, dU, dV, dZ)}
+        return calls[first]
+
+    return X, step
+
+
+@pytest.mark.parametrize("M", [100, 700])
+@pytest.mark.parametrize("first", ["norm", "norm backward", "loss", "loss backward", "output",
+                                   "project"])
+def test_calls_behind_copies_and_joined_streams(first, M):
+    """A call's first kernel behind a copy, a memset and the join of two streams,
+    captured and not: what it reads was written there just before."""
+    m = fm()
+    g = torch.Generator("cuda").manual_seed(3)
+    X, step = all_calls(m, lambda *s: (torch.randn(*s, device="cuda", generator=g) / 8).to(BF), M)
+    call = step(first)
+    keep = X.clone()
+    want = [o.clone() for o in call()]
+    side = torch.cuda.Stream()
+
+    def joined():
+        main = torch.cuda.current_stream()
+        X.zero_()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            half = keep.float().mul_(0.5)
+        X.copy_(keep)                       # a copy, and a kernel on the other stream
+        main.wait_stream(side)
+        return half, call()
+
+    half, got = joined()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        half, got = joined()
+    for _ in range(3):
+        X.fill_(7.0)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(half, keep.float() * 0.5)
