@@ -243,7 +243,7 @@ __device__ __forceinline__ void tg_join_tiles(const TgParams &P, const TgPlan &p
       // the tile's first part is the last one of its worker, the others first
       const float *slot =
           P.slots +
-          (int64_t)((2 * (x * plan.side + lane) + (x < first ? 1 : 0)) * CG + rank) * kTgSlotFloats;
+          (int64_t)tg_part(x * plan.side + lane, x >= first, CG, rank) * kTgSlotFloats;
 #pragma unroll
       for (int j = 0; j < COLS / 4; ++j) {
         const float4 o = *reinterpret_cast<const float4 *>(
@@ -295,11 +295,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   // the groups that have a part, and the cuts that are a panel's first, each
   // numbered in order (the same in every block)
   const bool has = w < groups && cut_s[w + 1] > cut_s[w];
-  bool first_cut = w > 0 && w < groups && c.off != 0 && cut_s[w - 1] <= c.pos - c.off;
-  if (first_cut) {  // dW: this piece's rows; dX: complete once every piece has been
-    const int panel = c.tile + plan.s[c.pi].dealt, mt = panel / (plan.s[0].Nt / plan.side);
-    first_cut = c.pi == 0 ? mt * plan.row_step < plan.s[0].M : last != 0;
-  }
+  const bool first_cut =
+      w > 0 && w < groups && tg_first_cut(plan, c, cut_s[w - 1], last != 0);
   const uint32_t votes = __ballot_sync(0xffffffffu, has);
   const uint32_t votes2 = __ballot_sync(0xffffffffu, first_cut);
   const uint32_t below = (1u << (w % 32)) - 1;
