@@ -64,9 +64,13 @@ fmca_status output_sizes(int M, int e, int d) {
     return FMCA_ERR_UNSUPPORTED;
   return FMCA_OK;
 }
+// The logits' depth is not cut: 2^24 features are 2^18 k steps of a tile, 0.2 s at
+// a CTA's share of the memory's rate, of the second that a wait may take.
+constexpr int kVocabMaxD = 1 << 24;
 fmca_status vocab_sizes(int M, int V, int d) {
   if (M <= 0 || V <= 0 || d <= 0) return FMCA_ERR_INVALID_ARG;
-  if (d % 8 || (int64_t)M * d >= kLimit || (int64_t)V * d >= kLimit) return FMCA_ERR_UNSUPPORTED;
+  if (d % 8 || d > kVocabMaxD || (int64_t)M * d >= kLimit || (int64_t)V * d >= kLimit)
+    return FMCA_ERR_UNSUPPORTED;
   return FMCA_OK;
 }
 fmca_status check_workspace(const void *workspace, size_t have, size_t need) {

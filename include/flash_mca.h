@@ -458,8 +458,8 @@ fmca_status flash_mca_gau_output_backward(const void *Y, const void *Wo_t, const
  * of all rows where those are more).  fp32 accumulation; fixed summation
  * orders (deterministic).  The number of rows with a target stays on the
  * device: the calls do not wait and can be captured.
- * Sizes: M, V >= 1; d >= 8 a multiple of 8; M d, V d < 2^31.  Outputs must not
- * overlap inputs, the workspace or each other.  workspace: the matching
+ * Sizes: M, V >= 1; d a multiple of 8, 8 <= d <= 2^24; M d, V d < 2^31.  Outputs
+ * must not overlap inputs, the workspace or each other.  workspace: the matching
  * ..._workspace_bytes (0 for sizes that would be rejected), 256-byte aligned.
  */
 size_t flash_mca_vocab_loss_workspace_bytes(int M, int V, int d);

@@ -543,3 +543,21 @@ def test_tensor_core_training_wrappers_refuse_host_tensors():
                  lambda: fm.gau_output_backward(X, W, X)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_vocab_loss_refuses_depths_beyond_its_products():
+    """A product's depth is one tile's k steps: up to 2^24 they stay well within a
+    second (the waits' limit) and their number within 32 bits, which ceil(d / 64)
+    left at d = 2^31 - 8."""
+    for f in (fm.flash_mca_vocab_loss_workspace_bytes,
+              fm.flash_mca_vocab_loss_backward_workspace_bytes):
+        assert f(1, 1, 1 << 24) > 0 and f(100, 127, 1 << 24) > 0
+        for d in ((1 << 24) + 8, 1 << 28, 2 ** 31 - 64, 2 ** 31 - 8):
+            assert f(1, 1, d) == 0
+    P = 0x7F0000000000
+    a = [P + (k << 36) for k in range(8)]
+    for d in ((1 << 24) + 8, 2 ** 31 - 8):
+        assert fm.lib.flash_mca_vocab_loss(*a[:5], 1, 1, d, a[5], 0, None) == \
+            fm.FMCA_ERR_UNSUPPORTED
+        assert fm.lib.flash_mca_vocab_loss_backward(*a[:7], 1, 1, d, a[7], 0, None) == \
+            fm.FMCA_ERR_UNSUPPORTED
