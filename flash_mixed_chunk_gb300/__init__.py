@@ -575,7 +575,11 @@ def _on_stream(name, t, stream):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=t.device)
+        handle = _stream_ptr(stream)
+        # 0 and 1 are the default stream's; torch would take 0 for "any stream of
+        # its pool" and does not know 1
+        stream = torch.cuda.default_stream(t.device) if handle in (0, 1) else \
+            torch.cuda.ExternalStream(handle, device=t.device)
     elif stream.device != t.device:
         raise ValueError(f"the stream belongs to {stream.device}, {name} to {t.device}")
     with torch.cuda.stream(stream):

@@ -159,3 +159,35 @@ def test_calls_behind_copies_and_joined_streams(first, M):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert torch.equal(half, keep.float() * 0.5)
+
+
+@pytest.mark.parametrize("explicit", [False, True], ids=["allocating", "into outputs"])
+@pytest.mark.parametrize("kind", ["0", "1", "default", "side handle", "side"])
+def test_streams_by_handle(kind, explicit):
+    """`stream` may be a handle: 0 and 1 are the device's default stream.  The call
+    is ordered behind what that stream holds (a delay, then the inputs)."""
+    m = fm()
+    keep, w = torch.randn(300, 64, device="cuda"), torch.ones(64, device="cuda")
+    X, W = torch.randn(300, 64, device="cuda").to(BF), torch.randn(900, 64, device="cuda").to(BF)
+    t = torch.arange(300, device="cuda")
+    want, (wloss, wlse) = m.layer_norm(keep, w, w)[0], m.vocab_loss(X, W, t)
+    x, Xs = torch.zeros_like(keep), torch.zeros_like(X)
+    y, loss, lse = torch.empty_like(x), torch.empty_like(wloss), torch.empty_like(wlse)
+    ws = torch.empty(m.flash_mca_vocab_loss_workspace_bytes(300, 900, 64), dtype=torch.uint8,
+                     device="cuda")
+    side = torch.cuda.Stream()
+    on = side if kind.startswith("side") else torch.cuda.default_stream()
+    stream = {"0": 0, "1": 1, "default": on, "side handle": side.cuda_stream, "side": side}[kind]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(on):
+        torch.cuda._sleep(20_000_000)
+        x.copy_(keep)
+        Xs.copy_(X)
+    if explicit:
+        m.flash_mca_layer_norm(x, None, w, w, None, y, None, None, stream=stream)
+        m.flash_mca_vocab_loss(Xs, W, t, loss, lse, ws, stream=stream)
+    else:
+        y = m.layer_norm(x, w, w, stream=stream)[0]
+        loss, lse = m.vocab_loss(Xs, W, t, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(loss, wloss) and torch.equal(lse, wlse)
