@@ -586,19 +586,30 @@ def _on_stream(name, t, stream):
         yield stream
 
 
+_INT_MAX = 2 ** 31 - 1  # the C ABI's sizes are ints, to which ctypes cuts a larger one
+
+
 def _norm_rows(name, x):
     """(M, d) of a [..., d] tensor: its leading dimensions are the rows."""
     n = x.numel()
     if n == 0 or x.dim() < 1:
         raise ValueError(f"{name} must be [..., d] with at least one row")
     d = x.shape[-1]
+    if n // d > _INT_MAX or d > _INT_MAX:
+        raise ValueError(f"the sizes of {name}, {n // d} x {d}, do not fit 32 bits")
     return n // d, d
 
 
 def _matrix(name, t):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
+    if max(t.shape) > _INT_MAX:
+        raise ValueError(f"the sizes of {name}, {t.shape[0]} x {t.shape[1]}, do not fit 32 bits")
     return t.shape
+
+
+def _workspace_bytes(fn, *sizes) -> int:
+    return int(fn(*sizes)) if max(map(abs, sizes)) <= _INT_MAX else 0
 
 
 def flash_mca_layer_norm(x, res, weight, bias, h, y, mean, rstd, eps: float = 1e-5,
@@ -634,7 +645,7 @@ def layer_norm(x, weight, bias, eps: float = 1e-5, residual=None, stream=None):
 
 
 def flash_mca_layer_norm_backward_workspace_bytes(M: int, d: int) -> int:
-    return int(lib.flash_mca_layer_norm_backward_workspace_bytes(M, d))
+    return _workspace_bytes(lib.flash_mca_layer_norm_backward_workspace_bytes, M, d)
 
 
 def flash_mca_layer_norm_backward(dy, h, weight, mean, rstd, dh, dx, dweight, dbias, workspace,
@@ -671,7 +682,7 @@ def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, stream=None):
 
 
 def flash_mca_gau_project_backward_workspace_bytes(M: int, d: int, e: int, s: int) -> int:
-    return int(lib.flash_mca_gau_project_backward_workspace_bytes(M, d, e, s))
+    return _workspace_bytes(lib.flash_mca_gau_project_backward_workspace_bytes, M, d, e, s)
 
 
 def flash_mca_gau_project_backward(X, Wt, dU, dV, dZ, dX, dWt, workspace, stream=None) -> None:
@@ -701,7 +712,7 @@ def gau_project_backward(X, Wt, dU, dV, dZ, stream=None):
 
 
 def flash_mca_gau_output_backward_workspace_bytes(M: int, e: int, d: int) -> int:
-    return int(lib.flash_mca_gau_output_backward_workspace_bytes(M, e, d))
+    return _workspace_bytes(lib.flash_mca_gau_output_backward_workspace_bytes, M, e, d)
 
 
 def flash_mca_gau_output_backward(Y, Wo_t, dOut, dY, dWo_t, workspace, stream=None) -> None:
@@ -729,7 +740,7 @@ def gau_output_backward(Y, Wo_t, dOut, stream=None):
 
 
 def flash_mca_vocab_loss_workspace_bytes(M: int, V: int, d: int) -> int:
-    return int(lib.flash_mca_vocab_loss_workspace_bytes(M, V, d))
+    return _workspace_bytes(lib.flash_mca_vocab_loss_workspace_bytes, M, V, d)
 
 
 def flash_mca_vocab_loss(X, W, target, loss, lse, workspace, stream=None) -> None:
@@ -758,7 +769,7 @@ def vocab_loss(X, W, target, stream=None):
 
 
 def flash_mca_vocab_loss_backward_workspace_bytes(M: int, V: int, d: int) -> int:
-    return int(lib.flash_mca_vocab_loss_backward_workspace_bytes(M, V, d))
+    return _workspace_bytes(lib.flash_mca_vocab_loss_backward_workspace_bytes, M, V, d)
 
 
 def flash_mca_vocab_loss_backward(X, W, target, lse, dloss, dX, dW, workspace,

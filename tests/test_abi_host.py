@@ -561,3 +561,36 @@ def test_vocab_loss_refuses_depths_beyond_its_products():
             fm.FMCA_ERR_UNSUPPORTED
         assert fm.lib.flash_mca_vocab_loss_backward(*a[:7], 1, 1, d, a[7], 0, None) == \
             fm.FMCA_ERR_UNSUPPORTED
+
+
+def test_training_sizes_beyond_32_bits_are_refused():
+    """The C ABI takes sizes as int: 2^32 + 4 rows are not 4 rows."""
+    import torch
+    big = (1 << 32) + 4
+    assert fm.flash_mca_layer_norm_backward_workspace_bytes(4, 8) > 0
+    assert fm.flash_mca_layer_norm_backward_workspace_bytes(big, 8) == 0
+    assert fm.flash_mca_layer_norm_backward_workspace_bytes(4, (1 << 32) + 8) == 0
+    assert fm.flash_mca_gau_project_backward_workspace_bytes(big, 64, 64, 64) == 0
+    assert fm.flash_mca_gau_project_backward_workspace_bytes(4, 64, 64, (1 << 32) + 64) == 0
+    assert fm.flash_mca_gau_output_backward_workspace_bytes(big, 64, 64) == 0
+    assert fm.flash_mca_vocab_loss_workspace_bytes(big, 10, 64) == 0
+    assert fm.flash_mca_vocab_loss_backward_workspace_bytes(4, (1 << 33) + 10, 64) == 0
+    # the calls themselves, on tensors without memory
+    bf, f32 = torch.bfloat16, torch.float32
+    t = lambda *shape, dtype=bf: torch.empty(*shape, dtype=dtype, device="meta")  # noqa: E731
+    dev = t(1).get_device()
+    v = t(8, dtype=f32)
+    rows = t(big, dtype=f32)
+    x, ws = t(big, 8), t(1 << 20, dtype=torch.uint8)
+    y = t(big, 64)
+    for call in (
+            lambda: fm._layer_norm(dev, None, x, None, v, v, None, x, None, None, 1e-5),
+            lambda: fm._layer_norm_backward(dev, None, x, x, v, rows, rows, None, x, v, v, ws),
+            lambda: fm._gau_project_backward(dev, None, y, t(192, 64), y, y, y, y, t(192, 64), ws),
+            lambda: fm._gau_output_backward(dev, None, y, t(64, 64), y, y, t(64, 64), ws),
+            lambda: fm._vocab_loss(dev, None, x, t(10, 8), t(big, dtype=torch.int64), rows, rows,
+                                   ws),
+            lambda: fm._vocab_loss_backward(dev, None, t(4, 8), x, t(4, dtype=torch.int64),
+                                            t(4, dtype=f32), t(4, dtype=f32), t(4, 8), x, ws)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
