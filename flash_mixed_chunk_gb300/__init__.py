@@ -61,8 +61,11 @@ library_path = _build.LIB
 
 # Build (or rebuild, when a source is newer) the in-tree library; without it
 # the package does not import -- there is no CPU fallback.
+_binding_error = None
 try:
     _build.build()
+except _build.BindingError as exc:  # the library is there
+    _binding_error = exc
 except Exception as exc:  # nvcc missing or the build failed
     if not os.path.exists(library_path):
         raise ImportError(f"{library_path} is missing and could not be built: {exc}") from exc
@@ -148,10 +151,26 @@ class FmcaError(RuntimeError):
         super().__init__(f"{what}: {msg}" if what else msg)
 
 
-# The training operators' allocating wrappers (csrc/binding.cpp).
-from . import _binding  # noqa: E402
+class _NoBinding:
+    """In the place of the module that is missing: its functions raise."""
 
-_binding.set_error(FmcaError)
+    def __init__(self, why: Exception):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs the package's binding module (the flash_mca_* calls "
+                          f"with given outputs do not): {self._why}") from self._why
+
+
+# The training operators' allocating wrappers (csrc/binding.cpp).
+if _binding_error is None:
+    try:
+        from . import _binding
+        _binding.set_error(FmcaError)
+    except ImportError as exc:
+        _binding_error = exc
+if _binding_error is not None:
+    _binding = _NoBinding(_binding_error)
 
 
 def _check(status: int, what: str) -> None:

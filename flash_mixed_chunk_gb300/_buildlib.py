@@ -1,15 +1,16 @@
 """Build ``libflash_mca.so`` in-tree with nvcc for sm_103a.
 
 The translation units compile in parallel (the C-ABI layer, the SIMT kernels,
-the tensor-core kernels and the layer norm among them) and link into one shared library next to this
-file; the Python module with the training operators' wrappers (host code over
-torch's headers) compiles beside them.  The CUDA runtime is linked statically and the driver's tensor-map
-encoder is looked up at run time, so the library loads on a machine without a
-GPU driver (only calls that touch the device need one).
+the tensor-core kernels and the layer norm among them) and link into one shared
+library next to this file.  The CUDA runtime is linked statically and the driver's
+tensor-map encoder is looked up at run time, so the library loads on a machine
+without a GPU driver (only calls that touch the device need one).  The Python
+module with the training operators' wrappers (host code over torch's headers, by
+g++) compiles beside them; where it cannot, the rest of the package works.
 
-The package runs ``build()`` on import (a no-op when the library is newer than
-its sources); ``python -m flash_mixed_chunk_gb300.build [--force] [-v]`` runs
-it by hand.
+The package runs ``build()`` on import (a no-op when both are newer than their
+sources); ``python -m flash_mixed_chunk_gb300.build [--force] [-v]`` runs it by
+hand.
 """
 from __future__ import annotations
 
@@ -85,15 +86,44 @@ def _binding_link() -> None:
     os.replace(tmp, BINDING)
 
 
+class BindingError(RuntimeError):
+    """The library is there, the module with the training operators' wrappers is not."""
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is out of date; raises BindingError where that fails for the
+    module alone."""
     lib, binding = force or _stale(), force or _binding_stale()
     os.makedirs(BUILD, exist_ok=True)
-    cc = nvcc() if lib or binding else ""
+    binding_proc = binding_error = None
+    if binding:
+        try:
+            binding_proc = _binding_compile()
+        except Exception as exc:  # no host compiler
+            binding_error = exc
+    if lib:
+        _build_library(verbose)
+    if binding_proc is not None:
+        out = binding_proc.communicate()[0].decode(errors="replace")
+        if verbose or binding_proc.returncode != 0:
+            sys.stdout.write(out)
+        try:
+            if binding_proc.returncode != 0:
+                raise RuntimeError("compilation failed for binding.cpp")
+            _binding_link()
+        except Exception as exc:
+            binding_error = exc
+    if binding_error is not None:
+        raise BindingError(f"{BINDING} could not be built (it needs g++, Python's and torch's "
+                           f"headers): {binding_error}") from binding_error
+    return LIB
+
+
+def _build_library(verbose: bool) -> None:
+    cc = nvcc()
     procs = []
     objs = []
-    if binding:
-        procs.append(("binding.cpp", _binding_compile()))
-    for src in SOURCES if lib else []:
+    for src in SOURCES:
         obj = os.path.join(BUILD, src.rsplit(".", 1)[0] + ".o")
         objs.append(obj)
         cmd = [cc, *ARCH, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -109,12 +139,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
             failed.append(src)
     if failed:
         raise RuntimeError(f"compilation failed for {failed}")
-    if lib:
-        tmp = LIB + f".tmp{os.getpid()}"
-        link = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-        subprocess.run(link, check=True)
-        os.replace(tmp, LIB)
-    if binding:
-        _binding_link()
-    return LIB
-
+    tmp = LIB + f".tmp{os.getpid()}"
+    subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
+    os.replace(tmp, LIB)
