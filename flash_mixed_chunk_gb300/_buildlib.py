@@ -18,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,7 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflash_mca.so")
-BINDING = os.path.join(PKG, "_binding.so")
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_STAMP = os.path.join(BUILD, "binding.stamp")
 
 SOURCES = ["api.cpp", "simt.cu", "tc.cu", "noalloc.cu", "decode.cu", "backward.cu",
            "api_train.cpp", "norm.cu"]
@@ -54,16 +56,26 @@ def _stale() -> bool:
                   [os.path.join(INCLUDE, "flash_mca.h"), os.path.abspath(__file__)])
 
 
-def _binding_stale() -> bool:
+def _binding_against() -> str:
+    """What the module is compiled against: another Python or torch may lay out its
+    objects otherwise, whatever the files' times say."""
     import torch
+    return f"{sys.version}\n{torch.__version__} {torch._C._GLIBCXX_USE_CXX11_ABI}\n"
+
+
+def _binding_stale() -> bool:
+    try:
+        with open(BINDING_STAMP) as f:
+            if f.read() != _binding_against():
+                return True
+    except OSError:
+        return True
     return _older(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "flash_mca.h"),
-                            os.path.abspath(__file__), torch.__file__])
+                            os.path.abspath(__file__)])
 
 
 def _binding_compile():
     """Starts the compiler on binding.cpp (host code over torch's C++ headers)."""
-    import sysconfig
-
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     paths = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"),
@@ -84,6 +96,8 @@ def _binding_link() -> None:
                     "-l:libflash_mca.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python",
                     "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], check=True)
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_against())
 
 
 class BindingError(RuntimeError):

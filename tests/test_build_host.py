@@ -40,3 +40,21 @@ def test_the_core_needs_the_library_alone(tmp_path):
     p = subprocess.run([sys.executable, "-c", CODE], cwd=tmp_path, env=env, capture_output=True,
                        text=True, timeout=300)
     assert p.returncode == 0 and "fine" in p.stdout, p.stderr[-2000:]
+
+
+def test_the_module_belongs_to_one_python_and_torch(monkeypatch):
+    """Its file carries Python's ABI tag, and another torch makes it out of date
+    whatever the files' times are."""
+    import sysconfig
+
+    import torch
+    assert os.path.basename(_buildlib.BINDING) == "_binding" + sysconfig.get_config_var("EXT_SUFFIX")
+    _buildlib.build()
+    assert not _buildlib._binding_stale()
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    assert _buildlib._binding_stale()
+    monkeypatch.undo()
+    monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)
+    assert _buildlib._binding_stale()
+    monkeypatch.undo()
+    assert not _buildlib._binding_stale()
