@@ -139,7 +139,7 @@ fmca_status flash_mca_layer_norm_backward(const void *dy, const void *h, const f
 }
 
 size_t flash_mca_gau_project_backward_workspace_bytes(int M, int d, int e, int s) {
-  return project_sizes(M, d, e, s) == FMCA_OK ? project_grad_layout(M, 2 * e + s, d).total : 0;
+  return project_sizes(M, d, e, s) == FMCA_OK ? project_grad_layout(M, 2 * e + s).total : 0;
 }
 
 fmca_status flash_mca_gau_project_backward(const void *X, const void *Wt, const void *dU,
@@ -150,7 +150,7 @@ fmca_status flash_mca_gau_project_backward(const void *X, const void *Wt, const 
   if (st != FMCA_OK) return st;
   if (!X || !Wt || !dU || !dV || !dZ || !dX || !dWt) return FMCA_ERR_INVALID_ARG;
   if (!aligned({X, Wt, dU, dV, dZ, dX, dWt}, 16)) return FMCA_ERR_ALIGN;
-  st = check_workspace(workspace, workspace_bytes_, project_grad_layout(M, 2 * e + s, d).total);
+  st = check_workspace(workspace, workspace_bytes_, project_grad_layout(M, 2 * e + s).total);
   if (st != FMCA_OK) return st;
   const size_t xb = 2 * (size_t)M * d, wb = 2 * (size_t)(2 * (int64_t)e + s) * d;
   const size_t eb = 2 * (size_t)M * e, zb = 2 * (size_t)M * s;

@@ -396,8 +396,7 @@ struct ProjectGradLayout {
   size_t boxes, slots, total;
   int64_t cap_boxes;
 };
-inline ProjectGradLayout project_grad_layout(int M, int N, int d) {
-  (void)d;
+inline ProjectGradLayout project_grad_layout(int M, int N) {
   ProjectGradLayout L;
   L.boxes = 0;
   L.cap_boxes = tg_boxes(M, N);

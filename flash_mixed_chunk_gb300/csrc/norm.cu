@@ -75,14 +75,6 @@ struct Pack {
   __device__ Pack() {}
 };
 
-// One vector of a row through the default cache path, and back.
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float *out) {
-  Pack<T, VEC> k;
-  k.raw = *reinterpret_cast<const typename Pack<T, VEC>::raw_t *>(p);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) out[i] = to_f(k.v[i]);
-}
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float *in) {
   Pack<T, VEC> k;

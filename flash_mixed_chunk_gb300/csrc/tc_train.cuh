@@ -590,7 +590,7 @@ int gau_project_backward_cg(const void *X, const void *Wt, const void *dU, const
                                 const void *dZ, void *dX, void *dWt, int M, int d, int e, int s,
                                 void *workspace, cudaStream_t stream) {
   const int N = 2 * e + s;
-  const ProjectGradLayout L = project_grad_layout(M, N, d);
+  const ProjectGradLayout L = project_grad_layout(M, N);
   char *ws = static_cast<char *>(workspace);
   TgParams P = {}, Q = {};
   const bool small = tg_small<TG_SILU>(M, N);

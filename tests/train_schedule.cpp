@@ -281,7 +281,7 @@ const char *check_vocab_gradients(int cg, int M, int V, int d, int count, int wo
 const char *check_projection_gradients(int cg, int M, int N, int d, int blocked, int workers) {
   TgSizes S = {};
   S.M = M, S.N = N, S.K = d, S.blocked = blocked;
-  S.cap_boxes = blocked ? (uint32_t)project_grad_layout(M, N, d).cap_boxes : 0;
+  S.cap_boxes = blocked ? (uint32_t)project_grad_layout(M, N).cap_boxes : 0;
   std::string e = cg == 1 ? gradients<1, 256>(S, M, workers, false)
                           : gradients<2, 256>(S, M, workers, false);
   if (e.empty()) e = small_gradients(S);
