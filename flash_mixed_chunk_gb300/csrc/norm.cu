@@ -608,11 +608,10 @@ constexpr bool norm_long_held() {
 template <typename T, int VEC, int GROUP, bool kBackward>
 cudaError_t pick_n(NormArgs &a, cudaStream_t stream) {
   constexpr int kNot = kBackward && GROUP == kNormThreads && norm_long_held<T, VEC>() ? 16 : 0;
-  constexpr int kMost = GROUP > 32              ? 32
-                        : sizeof(T) * VEC < 16 ? 8
-                        : sizeof(T) == 4       ? 16
-                        : kBackward            ? 24
-                                               : 32;
+  constexpr int kMost = GROUP > 32                    ? 32
+                        : sizeof(T) * VEC < 16        ? 8
+                        : sizeof(T) == 4 || kBackward ? 16
+                                                      : 32;
   const int per = (a.d + GROUP * 8 - 1) / (GROUP * 8);  // eights of elements a thread
 #define FMCA_NORM(E)                                                            \
   if constexpr ((E) <= kMost && (E) != kNot)                                    \
@@ -627,14 +626,14 @@ cudaError_t pick_n(NormArgs &a, cudaStream_t stream) {
   return cudaErrorInvalidValue;
 }
 // Warps a row of the backward pass has where one warp would be short of
-// registers: bf16 rows of more than 768 in 16-byte vectors (16384 x 1024: 35.8 us
-// with a warp a row, 31.1 with 4), and of more than 512 while there are few of
-// them for all the groups (4096 x 768: 11.9 and 10.3 with 3, 8192: 15.2 and
-// 14.4, 16384: 23.4 and 24.0).  0: as in the forward pass.
+// registers: bf16 rows of more than 768 in 16-byte vectors four (16384 x 1024:
+// 28.1 us, with a warp a row 34.8), of more than 512 three (4096 x 768: 8.9 and
+// 9.3, 16384 x 768: 22.0 and 25.7, 32768 x 768: 37.4 and 43.8, 16384 x 520: 21.0
+// and 22.0).  0: as in the forward pass.
 constexpr int kNormWideRows = 4;
-int norm_wide(int M, int d, int elem) {
+int norm_wide(int d, int elem) {
   if (elem != 2 || d % 8 || d > kNormWarpMaxD) return 0;
-  return d > 768 ? 4 : d > 512 && M <= 8192 ? 3 : 0;
+  return d > 768 ? 4 : d > 512 ? 3 : 0;
 }
 template <typename T, int VEC, bool kBackward>
 cudaError_t pick_group(NormArgs &a, cudaStream_t stream) {
@@ -651,7 +650,7 @@ cudaError_t pick_group(NormArgs &a, cudaStream_t stream) {
       return kBackward ? launch_bwd<T, VEC, 8 / VEC, 128>(a, stream)
                        : launch_fwd<T, VEC, 8 / VEC, 128>(a, stream);
   if constexpr (kBackward && VEC == 8) {
-    const int warps = norm_wide(a.M, a.d, sizeof(T));
+    const int warps = norm_wide(a.d, sizeof(T));
     if (warps == 4) return launch_bwd<T, VEC, 1, 128, 128 * kNormWideRows>(a, stream);
     if (warps == 3) return launch_bwd<T, VEC, 1, 96, 96 * kNormWideRows>(a, stream);
   }
