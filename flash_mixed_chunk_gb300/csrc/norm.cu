@@ -20,12 +20,22 @@
 // it, else 4-byte ones, else single elements.  Rows that would fill a warp's
 // registers (and, backward, its shared memory) with few threads at work (fp32
 // beyond 512 elements, narrow vectors beyond 256) belong to half a block or (up
-// to 512) a quarter: 5001 fp32 rows of 1001 took 17 us backward instead of 32, and
-// 9001 of 301 13.4 with a quarter instead of 17.3.
+// to 512) a quarter: 5001 fp32 rows of 1001 take 16.5 us backward (34.6 with a
+// warp a row) and 10.9 forward (14.3), 9001 of 301 11.4 (14.2); forward the short
+// ones of many rows would be better off with a warp (9001 of 301: 7.2 and 6.2,
+// 300 rows 2.1 and 2.4).  Backward, bf16 rows in 16-byte vectors have three warps
+// from 513 elements on and four from 769 (norm_wide), and fp32 rows and rows of
+// pairs of bf16 512 threads from 2049 to 4096 (norm_long_held).
+//
+// Times in this file: calls in a captured loop over three sets of inputs, the
+// backward pass with both its launches; rows with a residual branch (backward: its
+// gradient) unless they are called plain.  The fp32 rows of 1001 and 301 just above
+// are plain.
 //
 // Every kernel is a programmatic dependent of what runs ahead of it on the
 // stream: its blocks are on their way while that ends, and read nothing before
-// the grid wait (a pass forward and backward: 4096 x 768 19.0 us, so 14.9).
+// the grid wait (a pass forward and backward of 4096 x 768, calls queued one by
+// one: 20.7 us, so 15.0; captured the same either way).
 //
 // The backward pass keeps dw and db of the rows it has seen in registers, one
 // partial row a block in the workspace, and a second kernel adds the partial
@@ -247,13 +257,12 @@ __device__ __forceinline__ void copies_wait() {
 //          shared memory, which costs no registers and needs no barrier: the
 //          row at hand and the next
 //   ahead  the next row waits in registers: 4-byte vectors that are held (5001
-//          fp32 rows of 1001 with a residual: 14.6 us, through the ring 18.1;
-//          16-byte vectors the other way round, 16384 bf16 rows of 1024: 37.2
-//          and 32.8)
+//          fp32 rows of 1001: 18.4 us, through the ring 21.8; 16-byte vectors the
+//          other way round, 16384 bf16 rows of 1024: 43.3 and 28.1)
 //   rows   2-byte elements, which cannot be copied one by one: the group copies
 //          whole rows, from the 16 bytes that a row's start lies in to those of
-//          its end, and reads its elements there (2000 rows of 4001: 26.9 us,
-//          read in place 73; 4-byte ones are better off as above, 18.6 and 16.4
+//          its end, and reads its elements there (2000 rows of 4001: 27.1 us,
+//          read in place 80.6; 4-byte ones are better off as above, 20.5 and 18.4
 //          for 5001 fp32 rows of 1001)
 constexpr int kNormStages = 2, kNormRowStages = 3;
 template <typename T, int VEC, int N>
@@ -297,7 +306,7 @@ __device__ __forceinline__ void norm_copy_row(uint8_t *dst, const T *dy, const T
 }
 
 // Blocks on an SM: three where the registers allow it (held 16-byte vectors, 80 a
-// thread), 8192 x 1536 28.0 us instead of 32.7 with two.
+// thread), 8192 x 1536 24.3 us instead of 27.1 with two.
 template <typename T, int VEC, int N, int GROUP, int THREADS>
 constexpr int norm_backward_per_sm() {
   using Feed = NormFeed<T, VEC, N>;
@@ -307,8 +316,8 @@ constexpr int norm_backward_per_sm() {
 
 // dx, and the block's sums of dw and db: part [blocks][2][d].  Rows are dealt
 // to the groups round-robin.  While a row is reduced the next one is on its
-// way; registers hold the running dw and db (2 x 24 at d = 768), and what is in
-// flight sets the rate.
+// way; registers hold the running dw and db (2 x 8 at d = 768, three warps a row), and
+// what is in flight sets the rate.
 template <typename T, int VEC, int N, int GROUP, int THREADS>
 __global__ void __launch_bounds__(THREADS, (norm_backward_per_sm<T, VEC, N, GROUP, THREADS>()))
     norm_backward(const T *__restrict__ dy, const T *__restrict__ h,
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, (norm_backward_per_sm<T, VEC, N, GROU
   } else {
     fetch(row, 0);
   }
-  // the row's, a row ahead like the rest of it (8192 x 1536: 27.8 us, now 24.1)
+  // the row's, a row ahead like the rest of it (8192 x 1536: 24.3 us, with the row 27.8)
   float next_mean = 0.f, next_rstd = 0.f;
   if (row < M) next_mean = mean_in[row], next_rstd = rstd_in[row];
   if constexpr (kWhole) {
@@ -481,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, (norm_backward_per_sm<T, VEC, N, GROU
   }
   // dw and db of a block lie element k of every vector next to each other
   // (k nv + c), so that a warp's stores are consecutive: in the rows' own order
-  // eight lanes meet in each bank of shared memory (16384 x 768: 27.3 us, now 25.4)
+  // eight lanes meet in each bank of shared memory (8192 x 1536: 29.0 us, so 24.3)
   float *pw = part + (int64_t)blockIdx.x * 2 * d;
   if constexpr (GROUP == THREADS) {
 #pragma unroll
@@ -596,9 +605,9 @@ cudaError_t launch_bwd(NormArgs &a, cudaStream_t stream) {
 }
 
 // Whether the backward pass takes rows of 2049 to 4096 elements with 512 threads,
-// so that they can be held: fp32 (2000 x 4001: 38.4 us, held 23.9; 4000 x 4000:
-// 52.6 and 45.6) and pairs of bf16 (2000 x 4002: 30.0 and 20.9), not the other
-// bf16 rows (9001 x 4000: 64.5 and 69.0, 6000 x 2561: 48.1 and 56.9).
+// so that they can be held: fp32 (2000 x 4001: 44.1 us, held 27.5; 4000 x 4000:
+// 52.1 and 45.7) and pairs of bf16 (2000 x 4002: 30.4 and 21.0), not the other
+// bf16 rows (9001 x 4000: 64.6 and 69.0, 6000 x 2561: 47.9 and 49.6).
 template <typename T, int VEC>
 constexpr bool norm_long_held() {
   return sizeof(T) == 4 || VEC == 2;

@@ -415,8 +415,8 @@ int launch_tgemm(const TgParams &P, cudaStream_t stream) {
 
 // Whether a product with its tokens as rows goes in 128 x 128 tiles: while those
 // fit on the CTAs at once.  A tile's k steps and epilogue take half the time
-// then: projection gradients of 1001 x 520, e 448, s 64 16.6 us (CTA pairs
-// 22.1), the loss's gradients of 88 x 164 x 560 13.1 (18.8).
+// then: projection gradients of 1001 x 520, e 448, s 64 16.7 us (CTA pairs
+// 21.2), the loss's gradients of 88 x 164 x 560 13.5 (19.3).
 template <int KIND>
 bool tg_small(int M, int N) {
   return tg_small_tiles(M, N) <= tg_resident<1, KIND, 128>();
@@ -458,7 +458,7 @@ int launch_grad(const TgParams &P, int np, cudaStream_t stream) {
 // Whether the vocabulary loss makes its rows compact.  Not up to 128 rows (one
 // tile in any case), nor up to 512 while all of them cost less in the products
 // (8 GFLOP, 5 us) than the launch that would sort them out: 455 rows against
-// 2245 x 680 took 40 us forward and backward as they are, 51 compact.
+// 2245 x 680 take 35.4 us forward and backward as they are, 40.7 compact.
 bool vocab_compact(int M, int V, int d) {
   return M > 512 || (M > 128 && 2.0 * M * V * d > 8e9);
 }

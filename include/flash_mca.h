@@ -440,9 +440,11 @@ fmca_status flash_mca_gau_output_backward(const void *Y, const void *Wo_t, const
  * row per entry, as the projections' weights), without storing the logits
  * z = X W^T:
  *   loss[m] = lse[m] - z[m][target[m]],  lse[m] = log sum_v exp(z[m][v])
- * A row whose target lies outside 0 .. V - 1 (an ignored token: -100, say) has
- * loss 0 and lse 0, takes part in nothing and costs nothing in the products;
- * what its X holds, NaN included, reaches no output.  No reduction is applied:
+ * A row whose target lies outside 0 .. V - 1 (an ignored token: -100, say; a
+ * label too large is one too, without an error) has loss 0 and lse 0, takes part
+ * in nothing and, in calls of more than 512 rows, costs nothing in the products;
+ * what its X holds, NaN included, reaches no output.  A logit that overflows fp32
+ * makes its row's loss infinite or NaN.  No reduction is applied:
  * dloss [M] of the backward pass carries it (1 / number of targets for their
  * mean).
  *   X, W          device bf16, 16-byte aligned; target: device int64 [M], 8-byte
