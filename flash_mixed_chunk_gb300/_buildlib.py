@@ -27,7 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libflash_mca.so")
 BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
-BINDING_STAMP = os.path.join(BUILD, "binding.stamp")
+BINDING_STAMP = os.path.join(PKG, "_binding.stamp")
 
 SOURCES = ["api.cpp", "simt.cu", "tc.cu", "noalloc.cu", "decode.cu", "backward.cu",
            "api_train.cpp", "norm.cu"]
@@ -77,6 +77,7 @@ def _binding_stale() -> bool:
 def _binding_compile():
     """Starts the compiler on binding.cpp (host code over torch's C++ headers)."""
     import torch
+    os.makedirs(BUILD, exist_ok=True)
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     paths = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"),
              sysconfig.get_paths()["include"],
@@ -108,12 +109,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Builds what is out of date; raises BindingError where that fails for the
     module alone."""
     lib, binding = force or _stale(), force or _binding_stale()
-    os.makedirs(BUILD, exist_ok=True)
     binding_proc = binding_error = None
     if binding:
         try:
             binding_proc = _binding_compile()
-        except Exception as exc:  # no host compiler
+        except Exception as exc:  # no host compiler, nowhere to write
             binding_error = exc
     if lib:
         _build_library(verbose)
@@ -135,6 +135,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def _build_library(verbose: bool) -> None:
     cc = nvcc()
+    os.makedirs(BUILD, exist_ok=True)
     procs = []
     objs = []
     for src in SOURCES:

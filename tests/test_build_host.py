@@ -58,3 +58,42 @@ def test_the_module_belongs_to_one_python_and_torch(monkeypatch):
     assert _buildlib._binding_stale()
     monkeypatch.undo()
     assert not _buildlib._binding_stale()
+
+
+def copied(tmp_path, ignore):
+    root = os.path.dirname(_buildlib.PKG)
+    for part in ("flash_mixed_chunk_gb300", "include"):
+        shutil.copytree(os.path.join(root, part), tmp_path / part,
+                        ignore=shutil.ignore_patterns("__pycache__", *ignore))
+    (tmp_path / "bin").mkdir()
+    env = {**os.environ, "PATH": str(tmp_path / "bin")}
+    env.pop("PYTHONPATH", None)
+
+    def python(code):
+        return subprocess.run([sys.executable, "-c", code], cwd=tmp_path, env=env,
+                              capture_output=True, text=True, timeout=300)
+    return python
+
+
+def test_a_tree_without_its_build_folder_is_not_built_again(tmp_path):
+    """Both binaries and what they were built against are all that a copy of the
+    package needs: no compiler, no folder of objects."""
+    _buildlib.build()
+    p = copied(tmp_path, ["_build"])("""
+import torch
+import flash_mixed_chunk_gb300 as fm
+try:
+    fm.layer_norm(torch.zeros(2, 8), torch.zeros(8), torch.zeros(8))
+except ValueError as e:
+    assert "CUDA" in str(e)
+    print("fine")
+""")
+    assert p.returncode == 0 and "fine" in p.stdout, p.stderr[-2000:]
+    assert not (tmp_path / "flash_mixed_chunk_gb300" / "_build").exists()
+
+
+def test_a_module_that_cannot_be_built_for_want_of_a_folder(tmp_path):
+    python = copied(tmp_path, ["_build", "_binding*"])
+    (tmp_path / "flash_mixed_chunk_gb300" / "_build").write_text("not a folder")
+    p = python(CODE)
+    assert p.returncode == 0 and "fine" in p.stdout, p.stderr[-2000:]
