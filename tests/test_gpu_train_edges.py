@@ -252,3 +252,79 @@ def test_gradients_are_differences_along_directions(scaled):
             elif along:
                 outside += off > bound
     assert scaled == 1.0 or outside == 2
+
+
+# ------------------------------------------------------- several calls at once
+
+def small_step(m, M, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *k: (torch.randn(*k, device="cuda", generator=g) / 8).to(BF)  # noqa: E731
+    X, W, Y, Wo, dOut = r(M, 136), r(1500, 136), r(M, 264), r(128, 264), r(M, 128)
+    Wt, dU, dV, dZ = r(2 * 256 + 64, 136), r(M, 256), r(M, 256), r(M, 64)
+    t = torch.randint(-200, 1500, (M,), device="cuda", generator=g)
+    w, dl = torch.rand(136, device="cuda", generator=g), torch.rand(M, device="cuda", generator=g)
+
+    def step():
+        y, h, mean, rstd = m.layer_norm(X, w, w)
+        loss, lse = m.vocab_loss(y, W, t)
+        dX, dW = m.vocab_loss_backward(y, W, t, lse, dl)
+        return (y, loss, dX, dW, *m.layer_norm_backward(dX, h, w, mean, rstd),
+                *m.gau_output_backward(Y, Wo, dOut), *m.gau_project_backward(X, Wt, dU, dV, dZ))
+    return step
+
+
+def test_threads_with_a_stream_each():
+    import threading
+    m = fm()
+    steps = [small_step(m, M, M) for M in (90, 700, 1300)]
+    want = [[o.clone() for o in s()] for s in steps]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = steps[k]()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[k])):
+                    wrong.append(k)
+        stream.synchronize()
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and m.flash_mca_device_status()[0] == m.FMCA_OK
+
+
+def test_graphs_replayed_side_by_side():
+    m = fm()
+    steps = [small_step(m, M, M) for M in (90, 700, 1300)]
+    want = [[o.clone() for o in s()] for s in steps]
+    torch.cuda.synchronize()
+    graphs = []
+    for s in steps:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = s()
+        graphs.append((graph, out, torch.cuda.Stream()))
+    for _ in range(20):
+        for graph, _, stream in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, out, _), ref in zip(graphs, want):
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    assert m.flash_mca_device_status()[0] == m.FMCA_OK
+
+
+def test_a_single_row_without_leading_dimensions():
+    m = fm()
+    x, w = torch.randn(301, device="cuda"), torch.rand(301, device="cuda")
+    y, h, mean, rstd = m.layer_norm(x, w, w, residual=x)
+    y2, h2, mean2, rstd2 = m.layer_norm(x[None], w, w, residual=x[None])
+    assert mean.shape == () and torch.equal(y, y2[0]) and torch.equal(h, 2 * x)
+    got = m.layer_norm_backward(x, h, w, mean, rstd, x)
+    want = m.layer_norm_backward(x[None], h2, w, mean2, rstd2, x[None])
+    assert torch.equal(got[0], want[0][0]) and all(torch.equal(a, b) for a, b in
+                                                  zip(got[1:], want[1:]))
