@@ -29,8 +29,8 @@
 //
 // Times in this file: calls in a captured loop over three sets of inputs, the
 // backward pass with both its launches; rows with a residual branch (backward: its
-// gradient) unless they are called plain.  The fp32 rows of 1001 and 301 just above
-// are plain.
+// gradient), but for the fp32 rows of 1001 and the 9001 of 301 just above, which
+// have none.
 //
 // Every kernel is a programmatic dependent of what runs ahead of it on the
 // stream: its blocks are on their way while that ends, and read nothing before
