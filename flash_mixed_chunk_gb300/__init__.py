@@ -45,6 +45,11 @@ __all__ = [
     "flash_mca_vocab_loss_workspace_bytes", "flash_mca_vocab_loss",
     "flash_mca_vocab_loss_backward_workspace_bytes", "flash_mca_vocab_loss_backward",
     "vocab_loss", "vocab_loss_backward",
+    "FmcaDecayShape", "FmcaBeamPiece",
+    "flash_mca_decay_workspace_bytes", "flash_mca_decay_attention", "flash_mca_decay_step",
+    "decay_attention", "decay_step",
+    "flash_mca_beam_select", "beam_select", "flash_mca_beam_reorder", "beam_reorder",
+    "flash_mca_decode_reorder",
 ]
 
 FMCA_OK, FMCA_ERR_INVALID_ARG, FMCA_ERR_SHAPE, FMCA_ERR_UNSUPPORTED = 0, 1, 2, 3
@@ -91,6 +96,19 @@ class FmcaSeq(ctypes.Structure):
                 ("n_norm", ctypes.c_int64)]
 
 
+class FmcaDecayShape(ctypes.Structure):
+    """``fmca_decay_shape`` of the header: the sizes of a call of linear attention
+    with a decay, and the strides (batch, token, head) of q, k and v in elements."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "H", "Hq", "Hk", "Hv", "dk", "dv")] + \
+        [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride")]
+
+
+class FmcaBeamPiece(ctypes.Structure):
+    """``fmca_beam_piece`` of the header: B K rows of ``bytes`` bytes, ``row`` bytes
+    apart."""
+    _fields_ = [("base", _vp), ("row", ctypes.c_int64), ("bytes", ctypes.c_int64)]
+
+
 # (name, restype, argtypes) for every symbol the header declares
 _SIGNATURES = [
     ("flash_mca_workspace_bytes", _sz, [_int] * 6 + [_i32]),
@@ -117,6 +135,16 @@ _SIGNATURES = [
     ("flash_mca_layer_norm", _i32, [_vp] * 8 + [_int, _int, ctypes.c_float, _i32, _vp]),
     ("flash_mca_layer_norm_backward_workspace_bytes", _sz, [_int, _int]),
     ("flash_mca_layer_norm_backward", _i32, [_vp] * 9 + [_int, _int, _i32, _vp, _sz, _vp]),
+    ("flash_mca_decay_workspace_bytes", _sz, [ctypes.POINTER(FmcaDecayShape), _i32]),
+    ("flash_mca_decay_attention", _i32, [_vp] * 8 + [ctypes.POINTER(FmcaDecayShape),
+                                                     ctypes.c_float, _i32, _vp, _sz, _vp]),
+    ("flash_mca_decay_step", _i32, [_vp] * 6 + [ctypes.POINTER(FmcaDecayShape), ctypes.c_float,
+                                                _i32, _vp]),
+    ("flash_mca_beam_select", _i32, [_vp, ctypes.c_int64] + [_vp] * 5 + [_int] * 5 +
+     [_i32, _vp]),
+    ("flash_mca_beam_reorder", _i32, [ctypes.POINTER(FmcaBeamPiece), _int, _vp, _int, _int,
+                                      _vp]),
+    ("flash_mca_decode_reorder", _i32, [_vp, _sz, _vp] + [_int] * 6 + [_i32, _vp]),
     ("flash_mca_backward", _i32, [_vp] * 11 + [_int] * 6 + [_i32, ctypes.POINTER(FmcaOptions),
                                                           _vp, _sz, _vp]),
     ("flash_mca_backward_saved", _i32, [_vp] * 11 + [_int] * 6 +
@@ -162,7 +190,7 @@ class _NoBinding:
                           f"with given outputs do not): {self._why}") from self._why
 
 
-# The training operators' allocating wrappers (csrc/binding.cpp).
+# The wrappers of the training operators and of generation with states (csrc/binding.cpp).
 if _binding_error is None:
     try:
         from . import _binding
@@ -815,6 +843,209 @@ def vocab_loss_backward(X, W, target, lse, dloss, stream=None):
         return _binding.vocab_loss_backward(X, W, target, lse, dloss)
     with _on_stream("X", X, stream):
         return _binding.vocab_loss_backward(X, W, target, lse, dloss)
+
+
+def _decay_strides(name, t, lead):
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return (t.stride(0), t.stride(1) if lead == 2 else 0, t.stride(-2))
+
+
+def _decay_shape(q, k, v, log_decay, lead, dev):
+    """``fmca_decay_shape`` of q, k [B, (T,) heads, dk] and v [B, (T,) heads, dv]."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != lead + 2:
+            raise ValueError(f"{name} must be [B, {'T, ' if lead == 2 else ''}heads, d]")
+        if t.dtype is not q.dtype or t.get_device() != dev:
+            raise ValueError("q, k and v must share one dtype and device")
+        if t.shape[:lead] != q.shape[:lead]:
+            raise ValueError(f"{name} must have q's batch{' and length' if lead == 2 else ''}")
+    if k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and k must share their last size")
+    if log_decay.dim() != 1:
+        raise ValueError("log_decay must be [H]")
+    s = FmcaDecayShape()
+    sizes = (q.shape[0], q.shape[1] if lead == 2 else 1, log_decay.shape[0], q.shape[-2],
+             k.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1])
+    if max(sizes) > _INT_MAX:
+        raise ValueError(f"the sizes {sizes} do not fit 32 bits")
+    s.B, s.T, s.H, s.Hq, s.Hk, s.Hv, s.dk, s.dv = sizes
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        getattr(s, f"{name}_stride")[:] = _decay_strides(name, t, lead)
+    return s
+
+
+def flash_mca_decay_workspace_bytes(q, k, v, log_decay) -> int:
+    """Bytes of workspace that flash_mca_decay_attention needs for these operands (0:
+    none); -1 for sizes that would be rejected."""
+    s = _decay_shape(q, k, v, log_decay, 2, q.get_device())
+    n = int(lib.flash_mca_decay_workspace_bytes(ctypes.byref(s), _dtype_code(q)))
+    return -1 if n == _sz(-1).value else n
+
+
+def flash_mca_decay_attention(q, k, v, log_decay, lengths, state_in, o, state_out, workspace,
+                              scale: float = 1.0, stream=None) -> None:
+    """Linear attention with a decay for each head over whole prompts: S_t =
+    exp(log_decay) S_{t-1} + k_t^T v_t, o_t = scale q_t S_t.  q [B, T, Hq, dk], k
+    [B, T, Hk, dk], v [B, T, Hv, dv] CUDA tensors of one dtype, contiguous in their
+    last dimension; log_decay float32 [H], of which Hq, Hk and Hv are divisors; lengths
+    int32 [B] or None; state_in, state_out float32 [B, H, dk, dv] or None (state_out
+    may be state_in); o [B, T, H, dv].  workspace: a uint8 CUDA tensor of at least the
+    bytes that flash_mca_decay_workspace_bytes gives, None where that is 0."""
+    _placed("q", q, stream, _decay_attention, q, k, v, log_decay, lengths, state_in, o, state_out,
+            workspace, scale)
+
+
+def _decay_attention(dev, ptr, q, k, v, log_decay, lengths, state_in, o, state_out, ws, scale):
+    s, dt = _decay_shape(q, k, v, log_decay, 2, dev), _dtype_code(q)
+    state = (s.B, s.H, s.dk, s.dv)
+    st = lib.flash_mca_decay_attention(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _on("log_decay", log_decay, _FP32, (s.H,), dev),
+        _on_or_none("lengths", lengths, torch.int32, (s.B,), dev),
+        _on_or_none("state_in", state_in, _FP32, state, dev),
+        _on("o", o, q.dtype, (s.B, s.T, s.H, s.dv), dev),
+        _on_or_none("state_out", state_out, _FP32, state, dev), ctypes.byref(s), scale, dt,
+        None if ws is None else _on("workspace", ws, _U8, ws.shape, dev),
+        0 if ws is None else ws.numel(), ptr)
+    _check(st, "flash_mca_decay_attention")
+
+
+def decay_attention(q, k, v, log_decay, state=None, scale: float = 1.0, lengths=None,
+                    stream=None):
+    """Allocating wrapper of flash_mca_decay_attention: returns (o, state), the state
+    behind each sequence's last token; the state that is given stays as it is."""
+    if stream is None:
+        return _binding.decay_attention(q, k, v, log_decay, state, scale, lengths)
+    with _on_stream("q", q, stream):
+        return _binding.decay_attention(q, k, v, log_decay, state, scale, lengths)
+
+
+def flash_mca_decay_step(q, k, v, log_decay, state, o, scale: float = 1.0, stream=None) -> None:
+    """One token of every sequence: state = exp(log_decay) state + k^T v in place, o =
+    scale q state.  q [B, Hq, dk], k [B, Hk, dk], v [B, Hv, dv], o [B, H, dv], state
+    float32 [B, H, dk, dv], as for flash_mca_decay_attention."""
+    _placed("q", q, stream, _decay_step, q, k, v, log_decay, state, o, scale)
+
+
+def _decay_step(dev, ptr, q, k, v, log_decay, state, o, scale):
+    s, dt = _decay_shape(q, k, v, log_decay, 1, dev), _dtype_code(q)
+    st = lib.flash_mca_decay_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _on("log_decay", log_decay, _FP32, (s.H,), dev),
+        _on("state", state, _FP32, (s.B, s.H, s.dk, s.dv), dev),
+        _on("o", o, q.dtype, (s.B, s.H, s.dv), dev), ctypes.byref(s), scale, dt, ptr)
+    _check(st, "flash_mca_decay_step")
+
+
+def decay_step(q, k, v, log_decay, state, scale: float = 1.0, stream=None):
+    """Allocating wrapper of flash_mca_decay_step: returns o; the state in place."""
+    if stream is None:
+        return _binding.decay_step(q, k, v, log_decay, state, scale)
+    with _on_stream("q", q, stream):
+        return _binding.decay_step(q, k, v, log_decay, state, scale)
+
+
+def _row_stride(name, t, B, K) -> int:
+    """Elements between the rows of [B, K, ...] or [B K, ...], each contiguous."""
+    two = t.dim() >= 2 and t.shape[:2] == (B, K)
+    if not two and not (t.dim() >= 1 and t.shape[0] == B * K):
+        raise ValueError(f"{name} must be [B, K, ...] or [B K, ...], got {tuple(t.shape)}")
+    lead, inner = 2 if two else 1, 1
+    for size, stride in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        inner *= size
+    if B * K == 1:
+        return inner
+    if not two or K == 1:
+        return t.stride(0)
+    if B > 1 and t.stride(0) != K * t.stride(1):
+        raise ValueError(f"{name}'s rows must be evenly spaced")
+    return t.stride(1)
+
+
+def flash_mca_beam_select(logits, scores, finished, score, parent, token, pad: int = 0,
+                          stream=None) -> None:
+    """Of the candidates scores[k] + log softmax(logits[k])[v] of every batch element the
+    n largest, in their order, equal ones by the lowest k V + v, into score (float32),
+    parent and token (int64), all [B, n].  logits [B, K, V] or [B K, V] (rows evenly
+    spaced), scores float32 [B, K], finished bool [B, K] or None: a finished beam offers
+    its score alone, with token `pad`."""
+    _placed("logits", logits, stream, _beam_select, logits, scores, finished, score, parent, token,
+            pad)
+
+
+def _beam_select(dev, ptr, logits, scores, finished, score, parent, token, pad):
+    (B, K), (_, n) = _matrix("scores", scores), _matrix("score", score)
+    if logits.dim() not in (2, 3) or logits.dim() == 3 and logits.shape[:2] != (B, K):
+        raise ValueError("logits must be [B, K, V] or [B K, V] with scores [B, K]")
+    row, V = _row_stride("logits", logits, B, K), logits.shape[-1]
+    if V > _INT_MAX or not 0 <= pad <= _INT_MAX:
+        raise ValueError("the vocabulary and pad must fit 32 bits")
+    st = lib.flash_mca_beam_select(
+        logits.data_ptr(), row, _on("scores", scores, _FP32, (B, K), dev),
+        _on_or_none("finished", finished, torch.bool, (B, K), dev),
+        _on("score", score, _FP32, (B, n), dev), _on("parent", parent, _I64, (B, n), dev),
+        _on("token", token, _I64, (B, n), dev), B, K, V, n, pad, _dtype_code(logits), ptr)
+    _check(st, "flash_mca_beam_select")
+
+
+def beam_select(logits, scores, n: int | None = None, finished=None, pad: int = 0, stream=None):
+    """Allocating wrapper of flash_mca_beam_select: returns (score, parent, token); n
+    candidates of every batch element, as many as beams by default."""
+    if stream is None:
+        return _binding.beam_select(logits, scores, n, finished, pad)
+    with _on_stream("logits", logits, stream):
+        return _binding.beam_select(logits, scores, n, finished, pad)
+
+
+def flash_mca_beam_reorder(tensors, parent, stream=None) -> None:
+    """Row (b, k) of every tensor becomes what row (b, parent[b, k]) was, in place.
+    tensors: CUDA tensors [B, K, ...] or [B K, ...] of any types, rows contiguous and
+    evenly spaced; parent int64 [B, K]."""
+    tensors = list(tensors)
+    _placed("parent", parent, stream, _beam_reorder, tensors, parent)
+
+
+def _beam_reorder(dev, ptr, tensors, parent):
+    B, K = _matrix("parent", parent)
+    pieces = (FmcaBeamPiece * len(tensors))()
+    for i, t in enumerate(tensors):
+        if t.get_device() != dev:
+            raise ValueError(f"tensor {i} must be on cuda:{dev}")
+        row = _row_stride(f"tensor {i}", t, B, K)
+        el = t.element_size()
+        pieces[i] = FmcaBeamPiece(t.data_ptr(), row * el, t.numel() // max(B * K, 1) * el)
+    st = lib.flash_mca_beam_reorder(pieces, len(tensors), _on("parent", parent, _I64, (B, K), dev),
+                                    B, K, ptr)
+    _check(st, "flash_mca_beam_reorder")
+
+
+def beam_reorder(tensors, parent, stream=None) -> None:
+    """flash_mca_beam_reorder, with less of the host's time for each call."""
+    if stream is None:
+        return _binding.beam_reorder(tensors, parent)
+    with _on_stream("parent", parent, stream):
+        return _binding.beam_reorder(tensors, parent)
+
+
+def flash_mca_decode_reorder(state, parent, s: int, e: int, C: int, t: int, dtype: int,
+                             stream=None) -> None:
+    """flash_mca_beam_reorder for the state of flash_mca_decode_step of B K sequences
+    (sequence b K + k is beam k) ahead of position t; parent int64 [B, K], the sizes and
+    dtype those of flash_mca_decode_state_bytes(B K, ...)."""
+    _placed("state", state, stream, _decode_reorder, state, parent, s, e, C, t, dtype)
+
+
+def _decode_reorder(dev, ptr, state, parent, s, e, C, t, dtype):
+    B, K = _matrix("parent", parent)
+    if not state.is_contiguous():
+        raise ValueError("state must be contiguous")
+    if max(map(abs, (s, e, C, t))) > _INT_MAX:
+        raise ValueError("the sizes do not fit 32 bits")
+    st = lib.flash_mca_decode_reorder(state.data_ptr(), state.numel() * state.element_size(),
+                                      _on("parent", parent, _I64, (B, K), dev), B, K, s, e, C, t,
+                                      dtype, ptr)
+    _check(st, "flash_mca_decode_reorder")
 
 
 def flash_mca_device_status(stream=None) -> tuple[int, int]:

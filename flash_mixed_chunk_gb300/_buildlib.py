@@ -30,9 +30,9 @@ BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 BINDING_STAMP = os.path.join(PKG, "_binding.stamp")
 
 SOURCES = ["api.cpp", "simt.cu", "tc.cu", "noalloc.cu", "decode.cu", "backward.cu",
-           "api_train.cpp", "norm.cu"]
+           "api_train.cpp", "norm.cu", "api_serve.cpp", "decay.cu", "beam.cu"]
 HEADERS = ["launch.h", "ptx.cuh", "tc_common.cuh", "tc_prep.cuh", "tc_attn.cuh", "tc_fused.cuh", "tc_walk.cuh", "tc_pair.cuh", "tc_gemm.cuh", "tc_bgemm.cuh", "tc_bwd.cuh", "tc_backward.cuh",
-           "tg_plan.h", "tc_tgemm.cuh", "tc_train.cuh"]
+           "tg_plan.h", "tc_tgemm.cuh", "tc_train.cuh", "decay.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -1,6 +1,7 @@
 // binding.cpp -- the allocating Python wrappers of the training operators
 // (layer_norm, layer_norm_backward, gau_project_backward, gau_output_backward,
-// vocab_loss, vocab_loss_backward) as a CPython module.
+// vocab_loss, vocab_loss_backward) and of generation with states (decay_attention,
+// decay_step, beam_select, beam_reorder) as a CPython module.
 //
 // A call is checks, up to four tensors from torch's allocator and one call of
 // the C ABI (include/flash_mca.h): at one token the device work is 3 us and the
@@ -16,7 +17,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <memory>
 #include <string>
+#include <vector>
 
 #include "flash_mca.h"
 
@@ -384,6 +387,221 @@ PyObject *vocab_loss_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------- generation with states
+
+// The strides (batch, token, head) of q, k or v; `lead` dimensions ahead of (heads,
+// d): 2, or 1 without tokens.
+void strides_of(const char *name, const at::Tensor &t, int lead, int64_t *out) {
+  const int n = (int)t.dim();
+  if (t.size(n - 1) > 1 && t.stride(n - 1) != 1)
+    fail(PyExc_ValueError, std::string(name) + " must be contiguous in its last dimension");
+  out[0] = t.stride(0);
+  out[1] = lead == 2 ? t.stride(1) : 0;
+  out[2] = t.stride(n - 2);
+}
+// The shape of a call from q, k [B, (T,) heads, dk] and v [B, (T,) heads, dv].
+fmca_decay_shape decay_shape(const at::Tensor &q, PyObject *ko, PyObject *vo, PyObject *ro,
+                             int lead) {
+  const at::Tensor &k = tensor("k", ko), &v = tensor("v", vo), &r = tensor("log_decay", ro);
+  const int n = lead + 2;
+  const char *const want = lead == 2 ? " must be [B, T, heads, d]" : " must be [B, heads, d]";
+  const struct {
+    const char *name;
+    const at::Tensor &t;
+  } all[3] = {{"q", q}, {"k", k}, {"v", v}};
+  for (const auto &x : all) {
+    if (x.t.dim() != n) fail(PyExc_ValueError, x.name + std::string(want));
+    if (x.t.scalar_type() != q.scalar_type() || x.t.device() != q.device())
+      fail(PyExc_ValueError, std::string("q, k and v must share one dtype and device"));
+    for (int i = 0; i < lead; ++i)
+      if (x.t.size(i) != q.size(i))
+        fail(PyExc_ValueError, std::string(x.name) + " must have q's batch" +
+                                   (lead == 2 ? " and length" : ""));
+  }
+  if (k.size(n - 1) != q.size(n - 1)) fail(PyExc_ValueError, "q and k must share their last size");
+  if (r.dim() != 1) fail(PyExc_ValueError, "log_decay must be [H]");
+  fmca_decay_shape s;
+  s.B = size_of("the batch", q.size(0));
+  s.T = lead == 2 ? size_of("the length", q.size(1)) : 1;
+  s.H = size_of("the number of heads", r.size(0));
+  s.Hq = size_of("q's heads", q.size(n - 2));
+  s.Hk = size_of("k's heads", k.size(n - 2));
+  s.Hv = size_of("v's heads", v.size(n - 2));
+  s.dk = size_of("dk", q.size(n - 1));
+  s.dv = size_of("dv", v.size(n - 1));
+  strides_of("q", q, lead, s.q_stride);
+  strides_of("k", k, lead, s.k_stride);
+  strides_of("v", v, lead, s.v_stride);
+  return s;
+}
+double number(PyObject *o) {
+  const double x = PyFloat_AsDouble(o);
+  if (x == -1.0 && PyErr_Occurred()) throw python_error();
+  return x;
+}
+int64_t whole(PyObject *o) {
+  const int64_t x = PyLong_AsLongLong(o);
+  if (x == -1 && PyErr_Occurred()) throw python_error();
+  return x;
+}
+
+// (q, k, v, log_decay, state or None, scale, lengths or None) -> (o, state)
+PyObject *decay_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 7);
+  const at::Tensor &q = cuda_tensor("q", a[0]);
+  const fmca_dtype dt = dtype_of(q);
+  const fmca_decay_shape s = decay_shape(q, a[1], a[2], a[3], 2);
+  const at::Device dev = q.device();
+  const int64_t oshape[4] = {s.B, s.T, s.H, s.dv}, sshape[4] = {s.B, s.H, s.dk, s.dv};
+  const float *pr = (const float *)on("log_decay", a[3], at::kFloat, {s.H}, dev);
+  const float *ps =
+      a[4] != Py_None ? (const float *)on("state", a[4], at::kFloat, sshape, dev) : nullptr;
+  const double scale = number(a[5]);
+  const int32_t *pl =
+      a[6] != Py_None ? (const int32_t *)on("lengths", a[6], at::kInt, {s.B}, dev) : nullptr;
+  const void *pq = q.data_ptr(), *pk = tensor("k", a[1]).data_ptr();
+  const void *pv = tensor("v", a[2]).data_ptr();
+  c10::cuda::CUDAGuard guard(dev);
+  Results t(dev);
+  const size_t bytes = flash_mca_decay_workspace_bytes(&s, dt);
+  const bool fits = bytes != (size_t)-1;  // if not the call says why
+  const int o = t.add(oshape, q.scalar_type()), out = t.add(sshape, at::kFloat);
+  const int ws =
+      fits && bytes > 0 ? t.add_workspace(bytes, "flash_mca_decay_workspace_bytes") : -1;
+  const auto call = [&](void *po, float *pout, void *w) {
+    return flash_mca_decay_attention(pq, pk, pv, pr, pl, ps, po, pout, &s, (float)scale, dt, w,
+                                     w != nullptr ? bytes : 0, stream_of(dev));
+  };
+  if (!fits) check(call(nullptr, nullptr, nullptr), "flash_mca_decay_attention");
+  check(t.queue([&] { return call(t.ptr(o), t.ptr<float>(out), ws < 0 ? nullptr : t.ptr(ws)); }),
+        "flash_mca_decay_attention");
+  return pack(t[o], t[out]);
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, k, v, log_decay, state, scale) -> o; the state in place
+PyObject *decay_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 6);
+  const at::Tensor &q = cuda_tensor("q", a[0]);
+  const fmca_dtype dt = dtype_of(q);
+  const fmca_decay_shape s = decay_shape(q, a[1], a[2], a[3], 1);
+  const at::Device dev = q.device();
+  const int64_t oshape[3] = {s.B, s.H, s.dv}, sshape[4] = {s.B, s.H, s.dk, s.dv};
+  const float *pr = (const float *)on("log_decay", a[3], at::kFloat, {s.H}, dev);
+  float *ps = (float *)on("state", a[4], at::kFloat, sshape, dev);
+  const double scale = number(a[5]);
+  const void *pq = q.data_ptr(), *pk = tensor("k", a[1]).data_ptr();
+  const void *pv = tensor("v", a[2]).data_ptr();
+  c10::cuda::CUDAGuard guard(dev);
+  Results t(dev);
+  const int o = t.add(oshape, q.scalar_type());
+  check(t.queue([&] {
+          return flash_mca_decay_step(pq, pk, pv, pr, ps, t.ptr(o), &s, (float)scale, dt,
+                                      stream_of(dev));
+        }),
+        "flash_mca_decay_step");
+  return THPVariable_Wrap(t[o]);
+  END_HANDLE_TH_ERRORS
+}
+
+// The elements between the rows of a tensor of B K rows: [B, K, ...] or [B K, ...],
+// a row contiguous, the rows evenly spaced.
+int64_t row_stride(const char *name, const at::Tensor &t, int64_t B, int64_t K) {
+  const bool two = t.dim() >= 2 && t.size(0) == B && t.size(1) == K;
+  if (!two && !(t.dim() >= 1 && t.size(0) == B * K))
+    fail(PyExc_ValueError, std::string(name) + " must be [B, K, ...] or [B K, ...], got " +
+                               shape_text(t.sizes()));
+  const int lead = two ? 2 : 1;
+  int64_t inner = 1;
+  for (int i = (int)t.dim() - 1; i >= lead; --i) {
+    if (t.size(i) != 1 && t.stride(i) != inner)
+      fail(PyExc_ValueError, std::string(name) + "'s rows must be contiguous");
+    inner *= t.size(i);
+  }
+  if (B * K == 1) return inner;
+  if (!two) return t.stride(0);
+  if (K == 1) return t.stride(0);
+  if (B > 1 && t.stride(0) != K * t.stride(1))
+    fail(PyExc_ValueError, std::string(name) + "'s rows must be evenly spaced");
+  return t.stride(1);
+}
+
+// (logits, scores, n or None, finished or None, pad) -> (score, parent, token)
+PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  arguments(n_args, 5);
+  const at::Tensor &logits = cuda_tensor("logits", a[0]);
+  const at::Tensor &scores = matrix("scores", a[1]);
+  const at::Device dev = logits.device();
+  const fmca_dtype dt = dtype_of(logits);
+  const int64_t B = scores.size(0), K = scores.size(1);
+  const float *ps = (const float *)on("scores", scores, at::kFloat, {B, K}, dev);
+  const int64_t row = row_stride("logits", logits, B, K);
+  const bool two = logits.dim() == 3;
+  if (!two && logits.dim() != 2) fail(PyExc_ValueError, "logits must be [B, K, V] or [B K, V]");
+  if (two && (logits.size(0) != B || logits.size(1) != K))
+    fail(PyExc_ValueError, "logits must be [B, K, V] with scores [B, K]");
+  const int V = size_of("the vocabulary", logits.size(logits.dim() - 1));
+  const int64_t n = a[2] == Py_None ? K : whole(a[2]), pad = whole(a[4]);
+  if (n < 1 || n > INT32_MAX || pad < 0 || pad > INT32_MAX)
+    fail(PyExc_ValueError, "n must be at least 1, pad a token");
+  const uint8_t *pf =
+      a[3] != Py_None ? (const uint8_t *)on("finished", a[3], at::kBool, {B, K}, dev) : nullptr;
+  const void *pl = logits.data_ptr();
+  const int Bi = size_of("B", B), Ki = size_of("K", K);
+  c10::cuda::CUDAGuard guard(dev);
+  const int64_t shape[2] = {B, n};
+  Results t(dev);
+  const int score = t.add(shape, at::kFloat), parent = t.add(shape, at::kLong);
+  const int token = t.add(shape, at::kLong);
+  check(t.queue([&] {
+          return flash_mca_beam_select(pl, row, ps, pf, t.ptr<float>(score), t.ptr<int64_t>(parent),
+                                       t.ptr<int64_t>(token), Bi, Ki, V, (int)n, (int)pad, dt,
+                                       stream_of(dev));
+        }),
+        "flash_mca_beam_select");
+  return pack(t[score], t[parent], t[token]);
+  END_HANDLE_TH_ERRORS
+}
+
+// (a sequence of tensors, parent) -> None; the tensors in place
+PyObject *beam_reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+  HANDLE_TH_ERRORS
+  arguments(n_args, 2);
+  const at::Tensor &parent = cuda_tensor("parent", a[1]);
+  matrix("parent", a[1]);
+  const at::Device dev = parent.device();
+  const int64_t B = parent.size(0), K = parent.size(1);
+  const int64_t *pp = (const int64_t *)on("parent", parent, at::kLong, {B, K}, dev);
+  PyObject *all = PySequence_Fast(a[0], "the tensors must be a sequence");
+  if (all == nullptr) throw python_error();
+  std::unique_ptr<PyObject, void (*)(PyObject *)> held(all, [](PyObject *o) { Py_DECREF(o); });
+  std::vector<fmca_beam_piece> pieces;
+  for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(all); ++i) {
+    const std::string name = "tensor " + std::to_string(i);
+    const at::Tensor &t = tensor(name.c_str(), PySequence_Fast_GET_ITEM(all, i));
+    if (t.device() != dev) fail(PyExc_ValueError, name + " must be on " + dev.str());
+    const int64_t row = row_stride(name.c_str(), t, B, K), el = (int64_t)t.element_size();
+    const int64_t rows = B * K;
+    pieces.push_back(fmca_beam_piece{t.data_ptr(), row * el,
+                                     rows > 0 ? t.numel() / rows * el : 0});
+  }
+  if (pieces.empty()) fail(PyExc_ValueError, "no tensors");
+  const int Bi = size_of("B", B), Ki = size_of("K", K);
+  const int count = size_of("the number of tensors", (int64_t)pieces.size());
+  c10::cuda::CUDAGuard guard(dev);
+  fmca_status st;
+  {
+    const WithoutGil other_threads_run;
+    st = flash_mca_beam_reorder(pieces.data(), count, pp, Bi, Ki, stream_of(dev));
+  }
+  check(st, "flash_mca_beam_reorder");
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // (FmcaError): the class that a refused call raises
 PyObject *set_error(PyObject *, PyObject *type) {
   Py_XINCREF(type);
@@ -396,10 +614,12 @@ PyMethodDef kMethods[] = {
     FMCA_FAST(layer_norm),          FMCA_FAST(layer_norm_backward),
     FMCA_FAST(gau_project_backward), FMCA_FAST(gau_output_backward),
     FMCA_FAST(vocab_loss),          FMCA_FAST(vocab_loss_backward),
+    FMCA_FAST(decay_attention),     FMCA_FAST(decay_step),
+    FMCA_FAST(beam_select),         FMCA_FAST(beam_reorder),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding",
-                       "Allocating wrappers of the training operators.", -1, kMethods};
+                       "Wrappers of the training operators and of generation with states.", -1, kMethods};
 
 }  // namespace
 

@@ -1,0 +1,336 @@
+// decay.cu -- linear attention with a decay for each head, on the CUDA cores:
+//
+//   S_t = lam S_{t-1} + k_t^T v_t,   o_t = scale q_t S_t,   lam = exp(log_decay)
+//
+// decay_step runs one token of every sequence (the recurrence itself); decay_prompt
+// whole prompts in the chunked form, for 32-bit operands and for the sizes and
+// strides that the tensor-core kernel (tc_decay.cuh) does not take:
+//
+//   o_i = scale (sum_{j <= i} lam^(i-j) (q_i k_j) v_j + lam^(i+1) q_i S)   rows of a chunk
+//   S   = lam^n S + sum_j lam^(n-1-j) k_j^T v_j                            its n tokens
+//
+// Every power has an exponent >= 0, so that a strong decay underflows and never
+// overflows.  A sequence is cut into segments where there are fewer heads than SMs:
+// a first launch forms what each segment adds to the state, a second one starts
+// every segment from the sum of those before it.
+//
+// All kernels are programmatic dependents of what runs ahead of them on the stream
+// and wait for it before they read or write.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "decay.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace fmca {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int C = 32;         // tokens of a chunk
+constexpr int DVT = 64;       // columns of v of a unit
+constexpr int VS = DVT + 4;   // row of the v tile in shared memory
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// ------------------------------------------------------------------- prompts
+
+// Shared memory, in floats: q and k [C][dk + 4], v [C][VS], the chunk's weights
+// [C][C + 1], the powers 0 .. C, the state [dk][DVT].
+__host__ __device__ constexpr int prompt_floats(int dk) {
+  return 2 * C * (dk + 4) + C * VS + C * (C + 1) + (C + 4) + dk * DVT;
+}
+
+// A block is one unit.  LOCAL: what segments 0 .. S-2 add to the state, into
+// slots 1 .. S-1 of the workspace (segment 0 starts from the carried state, a copy
+// of which goes to slot 0: the second launch may overwrite it in place).
+template <typename T, bool LOCAL>
+__global__ void __launch_bounds__(kThreads)
+    decay_prompt(const __grid_constant__ DecayArgs a, const DecaySplit sp,
+                 float *__restrict__ slots) {
+  extern __shared__ float4 smem4[];
+  float *sm = reinterpret_cast<float *>(smem4);
+  const int dk = a.dk, ks = dk + 4;
+  float *sq = sm, *sk = sq + C * ks, *sv = sk + C * ks, *st = sv + C * VS;
+  float *sw = st + dk * DVT, *pw = sw + C * (C + 1);
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+
+  griddep_wait();
+  griddep_launch_dependents();
+  const int segs = LOCAL ? sp.S - 1 : sp.S;
+  const DecayUnit w = decay_unit(a, sp, segs, blockIdx.x);
+  const int v0 = w.vt * DVT, nv = a.dv - v0 < DVT ? a.dv - v0 : DVT;
+  const size_t slot = (size_t)dk * DVT;
+  float *own = slots + (((size_t)w.b * a.H + w.h) * sp.nvt + w.vt) * sp.S * slot;
+  const double rate = decay_rate(a.log_decay[w.h]);
+  if (tid <= C) pw[tid] = decay_power(rate, tid);
+  const float2 whole = decay_power2(rate, C);
+
+  // the state at the segment's start
+  const size_t at = ((size_t)w.b * a.H + w.h) * dk * (size_t)a.dv + v0;
+  for (int i = tid; i < dk * DVT; i += kThreads) {
+    const int d = i / DVT, c = i % DVT;
+    float x = 0.f;
+    if (sp.S == 1 || (LOCAL && w.s == 0)) {
+      if (a.state_in != nullptr && c < nv) x = a.state_in[at + (size_t)d * a.dv + c];
+      if (LOCAL) own[i] = x;
+    } else if (!LOCAL) {
+      if (w.s == 0) {
+        x = own[i];
+      } else if (w.t0 < w.len) {
+        for (int s = 1; s <= w.s; ++s)
+          x = fmaf(decay_power(rate, w.t0 - (int64_t)s * sp.L), own[s * slot + i], x);
+      }
+    }
+    st[i] = x;
+  }
+  // a segment that nothing comes behind is nobody's start
+  const int64_t end = w.t1 < w.len ? w.t1 : w.len;
+  if (LOCAL && w.t1 >= w.len) return;
+
+  const T *q = static_cast<const T *>(a.q) + w.b * a.qs[0] + (w.h / (a.H / a.Hq)) * a.qs[2];
+  const T *k = static_cast<const T *>(a.k) + w.b * a.ks[0] + (w.h / (a.H / a.Hk)) * a.ks[2];
+  const T *v = static_cast<const T *>(a.v) + w.b * a.vs[0] + (w.h / (a.H / a.Hv)) * a.vs[2] + v0;
+  T *o = static_cast<T *>(a.o) + ((size_t)w.b * a.T * a.H + w.h) * (size_t)a.dv + v0;
+  const size_t orow = (size_t)a.H * a.dv;
+
+  for (int64_t t = w.t0; t < end; t += C) {
+    const int n = end - t < C ? (int)(end - t) : C;
+    __syncthreads();  // the last chunk's reads of the tiles
+    // tokens behind the end are zeros, whatever the arrays hold there
+    for (int i = tid; i < C * dk; i += kThreads) {
+      const int r = i / dk, d = i % dk;
+      if (!LOCAL) sq[r * ks + d] = r < n ? to_f(q[(t + r) * a.qs[1] + d]) : 0.f;
+      sk[r * ks + d] = r < n ? to_f(k[(t + r) * a.ks[1] + d]) : 0.f;
+    }
+    for (int i = tid; i < C * DVT; i += kThreads) {
+      const int r = i / DVT, c = i % DVT;
+      sv[r * VS + c] = r < n && c < nv ? to_f(v[(t + r) * a.vs[1] + c]) : 0.f;
+    }
+    __syncthreads();
+    if (!LOCAL) {
+      float acc[2][2] = {};
+      for (int d = 0; d < dk; ++d) {
+        const float q0 = sq[2 * ty * ks + d], q1 = sq[(2 * ty + 1) * ks + d];
+        const float k0 = sk[2 * tx * ks + d], k1 = sk[(2 * tx + 1) * ks + d];
+        acc[0][0] = fmaf(q0, k0, acc[0][0]);
+        acc[0][1] = fmaf(q0, k1, acc[0][1]);
+        acc[1][0] = fmaf(q1, k0, acc[1][0]);
+        acc[1][1] = fmaf(q1, k1, acc[1][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int gap = 2 * ty + i - (2 * tx + j);
+          sw[(2 * ty + i) * (C + 1) + 2 * tx + j] = gap >= 0 ? acc[i][j] * pw[gap] : 0.f;
+        }
+      __syncthreads();
+      float4 near[2] = {}, far[2] = {};
+      auto fma4 = [](float x, const float4 &y, float4 &z) {
+        z.x = fmaf(x, y.x, z.x), z.y = fmaf(x, y.y, z.y);
+        z.z = fmaf(x, y.z, z.z), z.w = fmaf(x, y.w, z.w);
+      };
+      for (int j = 0; j <= 2 * ty + 1; ++j) {
+        const float4 x = *reinterpret_cast<const float4 *>(sv + j * VS + 4 * tx);
+        fma4(sw[2 * ty * (C + 1) + j], x, near[0]);
+        fma4(sw[(2 * ty + 1) * (C + 1) + j], x, near[1]);
+      }
+      for (int d = 0; d < dk; ++d) {
+        const float4 x = *reinterpret_cast<const float4 *>(st + d * DVT + 4 * tx);
+        fma4(sq[2 * ty * ks + d], x, far[0]);
+        fma4(sq[(2 * ty + 1) * ks + d], x, far[1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 2 * ty + i;
+        if (r >= n) continue;
+        const float *x = &near[i].x, *y = &far[i].x;
+        T *row = o + (size_t)(t + r) * orow;
+        for (int c = 0; c < 4; ++c)
+          if (4 * tx + c < nv) put(row + 4 * tx + c, a.scale * fmaf(pw[r + 1], y[c], x[c]));
+      }
+    }
+    // k_j's weight in the state
+    for (int i = tid; i < n * dk; i += kThreads) sk[(i / dk) * ks + i % dk] *= pw[n - 1 - i / dk];
+    __syncthreads();
+    const float2 g = n == C ? whole : make_float2(pw[n], 0.f);
+    for (int d = ty; d < dk; d += 16) {
+      float4 add = {};
+      for (int j = 0; j < n; ++j) {
+        const float x = sk[j * ks + d];
+        const float4 y = *reinterpret_cast<const float4 *>(sv + j * VS + 4 * tx);
+        add.x = fmaf(x, y.x, add.x), add.y = fmaf(x, y.y, add.y);
+        add.z = fmaf(x, y.z, add.z), add.w = fmaf(x, y.w, add.w);
+      }
+      float4 *p = reinterpret_cast<float4 *>(st + d * DVT + 4 * tx);
+      const float4 s = *p;
+      *p = make_float4(fmaf(s.x, g.x, fmaf(s.x, g.y, add.x)), fmaf(s.y, g.x, fmaf(s.y, g.y, add.y)),
+                       fmaf(s.z, g.x, fmaf(s.z, g.y, add.z)), fmaf(s.w, g.x, fmaf(s.w, g.y, add.w)));
+    }
+  }
+  __syncthreads();
+  if (LOCAL) {
+    for (int i = tid; i < dk * DVT; i += kThreads) own[(w.s + 1) * slot + i] = st[i];
+    return;
+  }
+  // outputs behind the sequence's end
+  const int64_t z0 = w.t0 > w.len ? w.t0 : w.len;
+  for (int64_t i = tid; i < (w.t1 - z0) * nv; i += kThreads)
+    put(o + (size_t)(z0 + i / nv) * orow + i % nv, 0.f);
+  if (a.state_out != nullptr && decay_last(w, sp.L))
+    for (int i = tid; i < dk * DVT; i += kThreads)
+      if (i % DVT < nv) a.state_out[at + (size_t)(i / DVT) * a.dv + i % DVT] = st[i];
+}
+
+// -------------------------------------------------------------- single tokens
+
+// A block is W = LR VEC columns of one head's state.  LR threads side by side have a
+// row of them, 256 / LR rows at a time; a thread reads, scales, adds to and writes
+// its places of the state, and adds q_d S_d to its columns' sums, which the rows'
+// threads join in a fixed order.  Bound by the state, read once and written once.
+template <typename T, int VEC, int LR>
+__global__ void __launch_bounds__(kThreads)
+    decay_step(const __grid_constant__ DecayArgs a, float *__restrict__ state) {
+  constexpr int W = LR * VEC, RP = kThreads / LR, U = 8;
+  __shared__ float sq[kDecayMaxK], sk[kDecayMaxK];
+  __shared__ float part[RP][W];
+  const int nvt = (a.dv + W - 1) / W;
+  const int vt = (int)(blockIdx.x % nvt);
+  const int64_t bh = blockIdx.x / nvt;
+  const int h = (int)(bh % a.H);
+  const int64_t b = bh / a.H;
+  const int tid = threadIdx.x, rp = tid / LR, c = vt * W + (tid % LR) * VEC;
+  const bool in = c < a.dv;
+  using V = typename std::conditional<VEC == 4, float4, float>::type;
+
+  griddep_wait();
+  griddep_launch_dependents();
+  float *p = state + (bh * a.dk) * (int64_t)a.dv + c;
+  const T *q = static_cast<const T *>(a.q) + b * a.qs[0] + (h / (a.H / a.Hq)) * a.qs[2];
+  const T *k = static_cast<const T *>(a.k) + b * a.ks[0] + (h / (a.H / a.Hk)) * a.ks[2];
+  const T *v = static_cast<const T *>(a.v) + b * a.vs[0] + (h / (a.H / a.Hv)) * a.vs[2] + c;
+  V s[U];
+  // the first rows are on their way while q and k come in
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (in && rp + u * RP < a.dk)
+      s[u] = *reinterpret_cast<const V *>(p + (int64_t)(rp + u * RP) * a.dv);
+  if (tid < a.dk) {
+    sq[tid] = to_f(q[tid]);
+    sk[tid] = to_f(k[tid]);
+  }
+  float x[VEC], sum[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    x[i] = in ? to_f(v[i]) : 0.f;
+    sum[i] = 0.f;
+  }
+  const float lam = decay_power(decay_rate(a.log_decay[h]), 1);
+  __syncthreads();
+  for (int r0 = rp; r0 < a.dk; r0 += U * RP) {
+    if (r0 != rp) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (in && r0 + u * RP < a.dk)
+          s[u] = *reinterpret_cast<const V *>(p + (int64_t)(r0 + u * RP) * a.dv);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RP;
+      if (!in || r >= a.dk) continue;
+      float *e = reinterpret_cast<float *>(&s[u]);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        e[i] = fmaf(lam, e[i], sk[r] * x[i]);
+        sum[i] = fmaf(sq[r], e[i], sum[i]);
+      }
+      *reinterpret_cast<V *>(p + (int64_t)r * a.dv) = s[u];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) part[rp][(tid % LR) * VEC + i] = sum[i];
+  __syncthreads();
+  if (tid < W && vt * W + tid < a.dv) {
+    float y = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < RP; ++i) y += part[i][tid];
+    put(static_cast<T *>(a.o) + bh * a.dv + vt * W + tid, a.scale * y);
+  }
+}
+
+template <typename T>
+int step(const DecayArgs &a, float *state, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kThreads);
+  const int64_t bh = (int64_t)a.B * a.H;
+  const auto blocks = [&](int W) { return bh * ((a.dv + W - 1) / W); };
+  if (a.dv % 4) {
+    cfg.gridDim = dim3((unsigned)blocks(32));
+    return cudaLaunchKernelEx(&cfg, decay_step<T, 1, 32>, a, state) == cudaSuccess ? 0 : 1;
+  }
+  // the widest rows that leave two blocks an SM
+  auto *kern = decay_step<T, 4, 32>;
+  int W = 128;
+  if (blocks(128) < 2 * kDecaySms) kern = decay_step<T, 4, 16>, W = 64;
+  if (blocks(64) < 2 * kDecaySms) kern = decay_step<T, 4, 8>, W = 32;
+  cfg.gridDim = dim3((unsigned)blocks(W));
+  return cudaLaunchKernelEx(&cfg, kern, a, state) == cudaSuccess ? 0 : 1;
+}
+
+template <typename T>
+int prompt(const DecayArgs &a, float *slots, cudaStream_t stream) {
+  const DecaySplit sp = decay_split_simt(a.B, a.T, a.H, a.dv);
+  const size_t smem = sizeof(float) * (size_t)prompt_floats(a.dk);
+  static OncePerDevice attrs;
+  if (!attrs.run([] {
+        const int most = (int)sizeof(float) * prompt_floats(kDecayMaxK);
+        return cudaFuncSetAttribute(decay_prompt<T, true>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    most) == cudaSuccess &&
+               cudaFuncSetAttribute(decay_prompt<T, false>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    most) == cudaSuccess;
+      }))
+    return 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  const int64_t heads = (int64_t)a.B * a.H * sp.nvt;
+  if (sp.S > 1) {
+    cfg.gridDim = dim3((unsigned)(heads * (sp.S - 1)));
+    if (cudaLaunchKernelEx(&cfg, decay_prompt<T, true>, a, sp, slots) != cudaSuccess) return 1;
+  }
+  cfg.gridDim = dim3((unsigned)(heads * sp.S));
+  return cudaLaunchKernelEx(&cfg, decay_prompt<T, false>, a, sp, slots) == cudaSuccess ? 0 : 1;
+}
+
+}  // namespace
+
+int launch_decay_simt(const DecayArgs &a, void *workspace, cudaStream_t stream) {
+  float *slots = static_cast<float *>(workspace);
+  return a.bf16 ? prompt<__nv_bfloat16>(a, slots, stream) : prompt<float>(a, slots, stream);
+}
+
+int launch_decay_step(const DecayArgs &a, float *state, cudaStream_t stream) {
+  return a.bf16 ? step<__nv_bfloat16>(a, state, stream) : step<float>(a, state, stream);
+}
+
+}  // namespace fmca

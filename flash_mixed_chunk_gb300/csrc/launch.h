@@ -421,6 +421,58 @@ int launch_gau_output_backward(const void *Y, const void *Wo_t, const void *dOut
                                void *dWo_t, int M, int e, int d, void *workspace,
                                cudaStream_t stream);
 
+// Linear attention with a decay for each head (decay.cu, tc_decay.cuh): the
+// operands of a call, strides in elements (batch, token, head).
+constexpr int kDecayMaxK = 256;  // dk that the kernels take
+constexpr int kDecaySms = 152;
+struct DecayArgs {
+  const void *q, *k, *v;
+  const float *log_decay;
+  const int32_t *lengths;   // or null
+  const float *state_in;    // or null
+  void *o;
+  float *state_out;         // or null
+  int B, T, H, Hq, Hk, Hv, dk, dv;
+  int64_t qs[3], ks[3], vs[3];
+  float scale;
+  int bf16;
+};
+// A head's tokens in S segments of L, its dv in nvt tiles.
+struct DecaySplit {
+  int S, L, nvt;
+};
+// CUDA cores: about two units an SM, segments of 256 tokens at least.
+inline DecaySplit decay_split_simt(int B, int T, int H, int dv) {
+  const int nvt = (dv + 63) / 64;
+  const int64_t heads = (int64_t)B * H * nvt;
+  int64_t S = heads < 2 * kDecaySms ? 2 * kDecaySms / heads : 1;
+  const int64_t most = ((int64_t)T + 255) / 256;
+  S = S < most ? S : most;
+  const int64_t L = ((T + S - 1) / S + 31) / 32 * 32;
+  return DecaySplit{(int)((T + L - 1) / L), (int)L, nvt};
+}
+inline size_t decay_bytes_simt(int B, int T, int H, int dk, int dv) {
+  const DecaySplit sp = decay_split_simt(B, T, H, dv);
+  return sp.S > 1 ? align256(sizeof(float) * (size_t)B * H * sp.nvt * sp.S * (size_t)dk * 64) : 0;
+}
+int launch_decay_simt(const DecayArgs &a, void *workspace, cudaStream_t stream);
+int launch_decay_step(const DecayArgs &a, float *state, cudaStream_t stream);
+
+// Beam search (beam.cu).
+constexpr int kBeamMax = 32;      // beams, and candidates, of a batch element
+constexpr int kBeamPieces = 16;   // arrays that one launch reorders
+constexpr int kBeamCluster = 8;   // blocks of a batch element, at most
+struct BeamPiece {  // rows [B K] of `bytes` bytes, `row` bytes apart; vec: of the launch
+  void *base;
+  int64_t row, bytes;
+  int vec;
+};
+int launch_beam_select(const void *logits, int64_t row, const float *scores,
+                       const uint8_t *finished, float *score, int64_t *parent, int64_t *token,
+                       int B, int K, int V, int n, int pad, int bf16, cudaStream_t stream);
+int launch_beam_reorder(const BeamPiece *pieces, int n, const int64_t *parent, int B, int K,
+                        cudaStream_t stream);
+
 // Shapes the tensor-core path covers.
 bool tc_supported(int B, int n, int s, int e, int C);  // every tensor-core kernel (e % 256)
 bool tc_forward_supported(int B, int n, int s, int e, int C, int lin_norm);  // the forward pass

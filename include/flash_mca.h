@@ -474,6 +474,102 @@ fmca_status flash_mca_vocab_loss_backward(const void *X, const void *W, const in
                                           int M, int V, int d, void *workspace,
                                           size_t workspace_bytes, fmca_stream_t stream);
 
+/*
+ * Linear attention with a decay for each head (the linear-attention recurrence of
+ * "大模型训练之加速篇 -attention优化", section 1.4, whose state forgets): for every
+ * sequence and head h of H, with lam = exp(log_decay[h]),
+ *
+ *   S_t = lam S_{t-1} + k_t^T v_t  (dk x dv),   o_t = scale q_t S_t
+ *
+ * flash_mca_decay_attention runs whole prompts (chunks of tokens on the tensor
+ * cores), flash_mca_decay_step one token of every sequence with the state updated
+ * in place; a prompt's last state is the first step's.
+ *   q [B][T][Hq][dk], k [B][T][Hk][dk], v [B][T][Hv][dv]
+ *            device arrays of `dtype` (a step: without T), the last dimension
+ *            contiguous, the others at the strides that `shape` gives (columns of
+ *            one projection's output, say; 0 and overlapping rows are allowed).
+ *            Hq, Hk and Hv divide H: head h reads heads h / (H / Hq) and so on.
+ *   log_decay  device float32 [H], <= 0 (-inf: nothing is kept; above 0 the state
+ *            grows, and overflows as the formula does)
+ *   lengths  device int32 [B] or NULL: sequence b has its first lengths[b] tokens
+ *            (cut to 0 .. T); what lies behind, NaN included, reaches nothing, its
+ *            outputs are 0, and the state is the one after lengths[b] tokens
+ *   state_in, state_out, state  device float32 [B][H][dk][dv], contiguous;
+ *            state_in NULL: zero; state_out NULL: not wanted, or state_in itself
+ *   o        device [B][T][H][dv] of `dtype`, contiguous (a step: [B][H][dv])
+ * States, sums and powers of the decay are held in 32 bits or more.  In a prompt of
+ * FMCA_BF16 with dk and dv multiples of 8, dk <= 128 and strides (in elements) that
+ * are multiples of 8, products run on the tensor cores: the weights of a chunk's
+ * pairs of tokens and the state as an operand of its outputs are rounded to bf16,
+ * the state itself is not.  Every other prompt runs in fp32 on the CUDA cores.
+ * Sizes: B, T, H >= 1; 1 <= dk <= 256; dv >= 1.  log_decay, lengths and states are
+ * aligned to 4 bytes (states to 16 for a dv that is a multiple of 4), q, k, v and o
+ * to their elements.  Outputs must not overlap inputs (but state_out state_in), the
+ * workspace or each other.  Deterministic.  workspace: at least
+ * flash_mca_decay_workspace_bytes (it may be 0; (size_t)-1 for sizes that would be
+ * rejected), 256-byte aligned.
+ */
+typedef struct {
+  int B, T, H, Hq, Hk, Hv, dk, dv;
+  int64_t q_stride[3], k_stride[3], v_stride[3]; /* batch, token, head; in elements */
+} fmca_decay_shape;
+size_t flash_mca_decay_workspace_bytes(const fmca_decay_shape *shape, fmca_dtype dtype);
+fmca_status flash_mca_decay_attention(const void *q, const void *k, const void *v,
+                                      const float *log_decay, const int32_t *lengths,
+                                      const float *state_in, void *o, float *state_out,
+                                      const fmca_decay_shape *shape, float scale,
+                                      fmca_dtype dtype, void *workspace, size_t workspace_bytes,
+                                      fmca_stream_t stream);
+/* shape->T must be 1; the token strides are not used. */
+fmca_status flash_mca_decay_step(const void *q, const void *k, const void *v,
+                                 const float *log_decay, float *state, void *o,
+                                 const fmca_decay_shape *shape, float scale, fmca_dtype dtype,
+                                 fmca_stream_t stream);
+
+/*
+ * Beam search's selection: of the candidates (beam k, token v) of each of B batch
+ * elements,
+ *
+ *   c[k][v] = scores[k] + z[k][v] - log sum_w exp(z[k][w])
+ *
+ * the n largest, in their order, equal ones by the lowest k V + v.
+ *   logits    device [B K rows][V] of `dtype`, `row` elements between rows (>= V)
+ *   scores    device float32 [B][K]
+ *   finished  device bytes [B][K] or NULL: a beam marked by other than 0 has one
+ *             candidate, token `pad` at its score; its logits are not read
+ *   score     device float32 [B][n];  parent, token  device int64 [B][n]
+ * A beam whose score is not finite, or whose logits hold a NaN, +inf or nothing above
+ * -inf, has no candidate, nor has a logit of -inf.  Places without a candidate (the
+ * last ones) hold score -inf, parent (place mod K) and token `pad`.  Candidates are
+ * compared in 64 bits.  One launch, nothing allocated; deterministic.
+ * Sizes: B, V >= 1, 1 <= K, n <= 32, 0 <= pad < V.  Arrays are aligned to their
+ * elements; outputs must not overlap inputs or each other.
+ */
+fmca_status flash_mca_beam_select(const void *logits, int64_t row, const float *scores,
+                                  const uint8_t *finished, float *score, int64_t *parent,
+                                  int64_t *token, int B, int K, int V, int n, int pad,
+                                  fmca_dtype dtype, fmca_stream_t stream);
+
+/*
+ * Rows of any arrays after a selection, in place: row (b, k) becomes what row
+ * (b, parent[b][k]) was.  A piece is an array of B K rows of `bytes` bytes, `row`
+ * bytes (>= bytes) apart; what lies between is not touched.  A parent outside
+ * 0 .. K - 1 leaves its beam as it is.  One launch for up to 16 pieces; pieces must
+ * not overlap each other or parent.  Sizes: B, n_pieces >= 1, 1 <= K <= 32.
+ */
+typedef struct {
+  void *base;
+  int64_t row, bytes;
+} fmca_beam_piece;
+fmca_status flash_mca_beam_reorder(const fmca_beam_piece *pieces, int n_pieces,
+                                   const int64_t *parent, int B, int K, fmca_stream_t stream);
+/* The same for the state of flash_mca_decode_step of B K sequences (sequence b K + k
+ * is beam k) ahead of position t: the carried sums and the current chunk's rows so
+ * far.  s, e, C, dtype: as for flash_mca_decode_state_bytes(B K, ...). */
+fmca_status flash_mca_decode_reorder(void *state, size_t state_bytes, const int64_t *parent,
+                                     int B, int K, int s, int e, int C, int t, fmca_dtype dtype,
+                                     fmca_stream_t stream);
+
 /* Which path FMCA_PATH_AUTO takes for these arguments (FMCA_PATH_SIMT or
  * FMCA_PATH_TCGEN05), or -1 for arguments that would be rejected. */
 int flash_mca_auto_path(int B, int n, int s, int e, int C, int causal, fmca_dtype dtype);
