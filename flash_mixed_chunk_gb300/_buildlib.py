@@ -32,7 +32,8 @@ BINDING_STAMP = os.path.join(PKG, "_binding.stamp")
 SOURCES = ["api.cpp", "simt.cu", "tc.cu", "noalloc.cu", "decode.cu", "backward.cu",
            "api_train.cpp", "norm.cu", "api_serve.cpp", "decay.cu", "beam.cu"]
 HEADERS = ["launch.h", "ptx.cuh", "tc_common.cuh", "tc_prep.cuh", "tc_attn.cuh", "tc_fused.cuh", "tc_walk.cuh", "tc_pair.cuh", "tc_gemm.cuh", "tc_bgemm.cuh", "tc_bwd.cuh", "tc_backward.cuh",
-           "tg_plan.h", "tc_tgemm.cuh", "tc_train.cuh", "decay.cuh"]
+           "tg_plan.h", "tc_tgemm.cuh", "tc_train.cuh", "decay.cuh",
+           "tc_decay.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

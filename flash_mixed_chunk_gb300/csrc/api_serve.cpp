@@ -117,7 +117,12 @@ fmca_status decay_pointers(const DecayArgs &a, const void *state) {
   return aligned({a.state_in, a.state_out, state}, a.dv % 4 ? 4 : 16) ? FMCA_OK : FMCA_ERR_ALIGN;
 }
 
-size_t decay_bytes(const DecayArgs &a) { return decay_bytes_simt(a.B, a.T, a.H, a.dk, a.dv); }
+// Of either kernel: which one runs goes by the operands' addresses too.
+size_t decay_bytes(const DecayArgs &a) {
+  const size_t s = decay_bytes_simt(a.B, a.T, a.H, a.dk, a.dv);
+  const size_t t = a.bf16 && a.dk <= 128 ? decay_bytes_tc(a.B, a.T, a.H, a.dv) : 0;
+  return s > t ? s : t;
+}
 
 fmca_status pieces_check(const fmca_beam_piece *p, int n, const int64_t *parent, int B, int K) {
   if (!p || n <= 0 || !parent || B <= 0 || K <= 0) return FMCA_ERR_INVALID_ARG;
@@ -195,7 +200,9 @@ fmca_status flash_mca_decay_attention(const void *q, const void *k, const void *
   if (outputs_clash({out, so, ws}, {sq, sk, sv, rates, lens, si}) ||
       overlap(out, Span{state_in, states}) || overlap(ws, Span{state_in, states}))
     return FMCA_ERR_INVALID_ARG;
-  return done(launch_decay_simt(a, workspace, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  return done(decay_tc(a) ? launch_tc_decay(a, workspace, cs)
+                          : launch_decay_simt(a, workspace, cs));
 }
 
 fmca_status flash_mca_decay_step(const void *q, const void *k, const void *v,

@@ -455,6 +455,40 @@ inline size_t decay_bytes_simt(int B, int T, int H, int dk, int dv) {
   const DecaySplit sp = decay_split_simt(B, T, H, dv);
   return sp.S > 1 ? align256(sizeof(float) * (size_t)B * H * sp.nvt * sp.S * (size_t)dk * 64) : 0;
 }
+// Tensor cores: tiles of 128 columns, chunks of 128 tokens; a slot of the workspace
+// holds a unit's state of 128 x 128.
+constexpr size_t kDecaySlot = 128 * 128;
+inline bool decay_tc(const DecayArgs &a) {
+  if (!a.bf16 || a.dk % 8 || a.dv % 8 || a.dk > 128) return false;
+  const auto fits = [](const void *p, const int64_t *s, int B, int T, int heads) {
+    const int n[3] = {B, T, heads};
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && (s[i] % 8 || s[i] == 0 || s[i] >= (int64_t)1 << 39)) return false;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  };
+  return fits(a.q, a.qs, a.B, a.T, a.Hq) && fits(a.k, a.ks, a.B, a.T, a.Hk) &&
+         fits(a.v, a.vs, a.B, a.T, a.Hv) && reinterpret_cast<uintptr_t>(a.o) % 16 == 0;
+}
+// As many segments as make the two launches shortest, a chunk of the first (k and v
+// alone) counted as half of one of the second, a launch's start as three.
+inline DecaySplit decay_split_tc(int B, int T, int H, int dv) {
+  const int nvt = (dv + 127) / 128;
+  const int64_t heads = (int64_t)B * H * nvt, chunks = ((int64_t)T + 127) / 128;
+  const auto waves = [](int64_t units) { return (units + kDecaySms - 1) / kDecaySms; };
+  int64_t best = 1, least = 2 * waves(heads) * (chunks + 3);
+  for (int64_t S = 2; S <= chunks && S <= 64 && heads * S < 4 * kDecaySms; ++S) {
+    const int64_t L = (chunks + S - 1) / S;
+    const int64_t cost = waves(heads * (S - 1)) * (L + 6) + 2 * waves(heads * S) * (L + 3);
+    if (cost < least) least = cost, best = S;
+  }
+  const int64_t L = (chunks + best - 1) / best * 128;
+  return DecaySplit{(int)((T + L - 1) / L), (int)L, nvt};
+}
+inline size_t decay_bytes_tc(int B, int T, int H, int dv) {
+  const DecaySplit sp = decay_split_tc(B, T, H, dv);
+  return sp.S > 1 ? sizeof(float) * (size_t)B * H * sp.nvt * sp.S * kDecaySlot : 0;
+}
+int launch_tc_decay(const DecayArgs &a, void *workspace, cudaStream_t stream);
 int launch_decay_simt(const DecayArgs &a, void *workspace, cudaStream_t stream);
 int launch_decay_step(const DecayArgs &a, float *state, cudaStream_t stream);
 

@@ -516,3 +516,5 @@ int launch_timeout_selftest(int limit_us, cudaStream_t stream) {
 #include "tc_backward.cuh"
 // The training operators (the same: one device status).
 #include "tc_train.cuh"
+// Linear attention with a decay for each head (the same).
+#include "tc_decay.cuh"
