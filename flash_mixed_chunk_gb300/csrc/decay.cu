@@ -84,13 +84,13 @@ __global__ void __launch_bounds__(kThreads)
         x = own[i];
       } else if (w.t0 < w.len) {
         for (int s = 1; s <= w.s; ++s)
-          x = fmaf(decay_power(rate, w.t0 - (int64_t)s * sp.L), own[s * slot + i], x);
+          x = fmaf(decay_power(rate, w.t0 - s * sp.L), own[s * slot + i], x);
       }
     }
     st[i] = x;
   }
   // a segment that nothing comes behind is nobody's start
-  const int64_t end = w.t1 < w.len ? w.t1 : w.len;
+  const int end = w.t1 < w.len ? w.t1 : w.len;
   if (LOCAL && w.t1 >= w.len) return;
 
   const T *q = static_cast<const T *>(a.q) + w.b * a.qs[0] + (w.h / (a.H / a.Hq)) * a.qs[2];
@@ -99,18 +99,18 @@ __global__ void __launch_bounds__(kThreads)
   T *o = static_cast<T *>(a.o) + ((size_t)w.b * a.T * a.H + w.h) * (size_t)a.dv + v0;
   const size_t orow = (size_t)a.H * a.dv;
 
-  for (int64_t t = w.t0; t < end; t += C) {
-    const int n = end - t < C ? (int)(end - t) : C;
+  for (int t = w.t0; t < end; t += C) {
+    const int n = end - t < C ? end - t : C;
     __syncthreads();  // the last chunk's reads of the tiles
     // tokens behind the end are zeros, whatever the arrays hold there
     for (int i = tid; i < C * dk; i += kThreads) {
       const int r = i / dk, d = i % dk;
-      if (!LOCAL) sq[r * ks + d] = r < n ? to_f(q[(t + r) * a.qs[1] + d]) : 0.f;
-      sk[r * ks + d] = r < n ? to_f(k[(t + r) * a.ks[1] + d]) : 0.f;
+      if (!LOCAL) sq[r * ks + d] = r < n ? to_f(q[(int64_t)(t + r) * a.qs[1] + d]) : 0.f;
+      sk[r * ks + d] = r < n ? to_f(k[(int64_t)(t + r) * a.ks[1] + d]) : 0.f;
     }
     for (int i = tid; i < C * DVT; i += kThreads) {
       const int r = i / DVT, c = i % DVT;
-      sv[r * VS + c] = r < n && c < nv ? to_f(v[(t + r) * a.vs[1] + c]) : 0.f;
+      sv[r * VS + c] = r < n && c < nv ? to_f(v[(int64_t)(t + r) * a.vs[1] + c]) : 0.f;
     }
     __syncthreads();
     if (!LOCAL) {
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(kThreads)
     return;
   }
   // outputs behind the sequence's end
-  const int64_t z0 = w.t0 > w.len ? w.t0 : w.len;
-  for (int64_t i = tid; i < (w.t1 - z0) * nv; i += kThreads)
+  const int z0 = w.t0 > w.len ? w.t0 : w.len;
+  for (int64_t i = tid; i < (int64_t)(w.t1 - z0) * nv; i += kThreads)
     put(o + (size_t)(z0 + i / nv) * orow + i % nv, 0.f);
   if (a.state_out != nullptr && decay_last(w, sp.L))
     for (int i = tid; i < dk * DVT; i += kThreads)

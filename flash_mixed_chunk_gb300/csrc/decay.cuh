@@ -35,8 +35,8 @@ __device__ __forceinline__ float2 decay_power2(double rate, int n) {
 // A unit of work: one head of one sequence, a tile of dv, a segment of tokens.
 struct DecayUnit {
   int b, h, vt, s;
-  int64_t t0, t1;  // the segment's tokens
-  int64_t len;     // of the sequence
+  int t0, t1;  // the segment's tokens
+  int len;     // of the sequence
 };
 // Units of `segs` segments each, the segments of a head next to each other.
 __device__ __forceinline__ DecayUnit decay_unit(const DecayArgs &a, const DecaySplit &sp, int segs,
@@ -48,20 +48,19 @@ __device__ __forceinline__ DecayUnit decay_unit(const DecayArgs &a, const DecayS
   u /= sp.nvt;
   w.h = (int)(u % a.H);
   w.b = (int)(u / a.H);
-  w.t0 = (int64_t)w.s * sp.L;
-  w.t1 = w.t0 + sp.L < a.T ? w.t0 + sp.L : a.T;
-  int64_t len = a.T;
+  w.t0 = w.s * sp.L;
+  w.t1 = a.T - w.t0 < sp.L ? a.T : w.t0 + sp.L;
+  w.len = a.T;
   if (a.lengths != nullptr) {
     const int32_t l = a.lengths[w.b];
-    len = l < 0 ? 0 : l < a.T ? l : a.T;
+    w.len = l < 0 ? 0 : l < a.T ? l : a.T;
   }
-  w.len = len;
   return w;
 }
 // Whether this segment's unit has the sequence's last token, and with it the state
 // that is returned (a sequence without tokens: its first segment's).
 __device__ __forceinline__ bool decay_last(const DecayUnit &w, int L) {
-  return w.s == (w.len == 0 ? 0 : (int)((w.len - 1) / L));
+  return w.s == (w.len == 0 ? 0 : (w.len - 1) / L);
 }
 
 }  // namespace

@@ -9,9 +9,10 @@
 // registers, fp32.  Of each chunk four products, accumulators in TMEM:
 //
 //   Sc = Q K^T          then P = Sc lam^(i-j), masked, bf16, back into TMEM
-//   O1 = P V,  O2 = Q S     S: the state before the chunk, rounded to bf16
+//   O  = Q S            S: the state before the chunk, rounded to bf16
+//   O  = lam^(i+1) O + P V      (the rows scaled in place in between)
 //   D  = K~^T V         K~_j = lam^(n-1-j) k_j
-//   o = scale (O1 + lam^(i+1) O2),   S = lam^n S + D
+//   o = scale O,   S = lam^n S + D
 //
 // What is rounded: P and the operand S, half a step of bf16 each, as is the output.
 // K~ is not: a product of a weight in 24 bits and a key in 8 goes in as three bf16
@@ -24,10 +25,10 @@
 // launch (LOCAL) forms only the segments' states, a second starts every segment from
 // the sum of those before it.
 //
-// Warps (576 threads): 0 TMA, 1 MMA issuer, 2-5 P, 6-9 outputs, 10-17 the state: K~'s
-// terms from K in place (the first term) and through two buffers of 32 tokens (the
-// others), then D from TMEM into the state and its bf16 copy in shared memory.  P
-// takes Sc's columns; the issuer forms the next Sc when PV is through.
+// Warps (640 threads): 0 TMA, 1 MMA issuer, 4-11 P and the outputs, 12-19 the state:
+// K~'s terms from K in place (the first term) and through two buffers of 32 tokens (the
+// others), then D from TMEM into the state and its bf16 copy in shared memory.  P takes
+// the columns of the scores that its own warp has read, of one of two buffers.
 #pragma once
 
 #include "decay.cuh"
@@ -36,12 +37,17 @@
 namespace fmca {
 namespace {
 
-constexpr int DA_THREADS = 576;
+constexpr int DA_THREADS = 640;
 constexpr int DA_SLOTS = 12;             // ring slots at most
 constexpr uint32_t DA_ATOM = 16384;      // 64 columns of 128 tokens
 constexpr uint32_t DA_SMEM = 229376;     // ring, state, terms
-constexpr uint32_t DA_COL_SC = 0, DA_COL_O1 = 128, DA_COL_O2 = 256, DA_COL_D = 384;
-constexpr int DA_STATE_WARP = 10;
+constexpr uint32_t DA_COL_SC = 0, DA_COL_O = 256, DA_COL_D = 384;  // two of Sc
+constexpr int DA_OUT_WARP = 4, DA_STATE_WARP = 12;
+// Registers of a thread: 96 at the launch, 640 of them; the state's 64 places need more,
+// the first four warps little.
+constexpr int DA_REG_ISSUE = 64, DA_REG_OUT = 88, DA_REG_STATE = 120;
+static_assert(128 * DA_REG_ISSUE + 256 * DA_REG_OUT + 256 * DA_REG_STATE <= 96 * DA_THREADS,
+              "tc_decay's warps would wait for registers that the block has not");
 
 // Shared memory by the 64-column blocks of dk (ka) and of the unit's dv (va).
 __host__ __device__ inline uint32_t da_slot(int ka, int va) {
@@ -56,28 +62,58 @@ __host__ __device__ inline int da_slots(int ka, int va) {
   return n < DA_SLOTS ? n : DA_SLOTS;
 }
 
-// One 16-byte vector of keys times w as three bf16 terms.
-__device__ __forceinline__ void key_terms(const uint4 &raw, float w, uint4 &t0, uint4 &t1,
-                                          uint4 &t2) {
-  const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t a[4], b[4], c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x = bf16_lo(in[i]) * w, y = bf16_hi(in[i]) * w;
-    a[i] = pack_bf16x2(x, y);
-    x -= bf16_lo(a[i]), y -= bf16_hi(a[i]);
-    b[i] = pack_bf16x2(x, y);
-    x -= bf16_lo(b[i]), y -= bf16_hi(b[i]);
-    c[i] = pack_bf16x2(x, y);
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A place in the ring and how often it has been used before, kept step by step: a
+// division by the ring's length takes a role longer than its products.
+struct RingAt {
+  int slot = 0, use = 0;
+  __device__ __forceinline__ RingAt ahead(int by, int n) const {  // by <= n
+    RingAt r = *this;
+    r.slot += by;
+    if (r.slot >= n) r.slot -= n, ++r.use;
+    return r;
   }
-  t0 = make_uint4(a[0], a[1], a[2], a[3]);
-  t1 = make_uint4(b[0], b[1], b[2], b[3]);
-  t2 = make_uint4(c[0], c[1], c[2], c[3]);
+};
+
+// Two floats in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// Two keys times w as three bf16 terms.
+__device__ __forceinline__ void key_terms(uint32_t k, float2 w, uint32_t &t0, uint32_t &t1,
+                                          uint32_t &t2) {
+  const float2 minus = make_float2(-1.f, -1.f);
+  float2 x = mul2(make_float2(bf16_lo(k), bf16_hi(k)), w);
+  t0 = pack_bf16x2(x.x, x.y);
+  x = fma2(make_float2(bf16_lo(t0), bf16_hi(t0)), minus, x);
+  t1 = pack_bf16x2(x.x, x.y);
+  x = fma2(make_float2(bf16_lo(t1), bf16_hi(t1)), minus, x);
+  t2 = pack_bf16x2(x.x, x.y);
 }
 
 // first: this launch is the call's first (it waits for the work ahead; the second one
 // waits for the first before it reads a state).
-template <bool LOCAL>
+// ka: the 64-column blocks of dk.
+template <bool LOCAL, int ka>
 __global__ void __launch_bounds__(DA_THREADS, 1)
     tc_decay(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
              const __grid_constant__ CUtensorMap mapV, const __grid_constant__ DecayArgs a,
@@ -86,8 +122,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t full[DA_SLOTS], empty[DA_SLOTS], x_ready[2], x_free[2];
-  __shared__ __align__(8) uint64_t sc_full, p_ready, o_full, o_free, s_ready, d_full, mma_done;
-  __shared__ __align__(16) float back[32];  // lam^(31 - j)
+  __shared__ __align__(8) uint64_t sc_full[2], qs_full, p_ready, o_full, o_free, s_ready, d_full,
+      mma_done;
+  __shared__ __align__(16) float back[16];  // lam^(15 - j)
   __shared__ float power[129];              // lam^j
   __shared__ uint32_t tmem_base;
 
@@ -96,21 +133,21 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   if (LOCAL || first) griddep_launch_dependents();
   const DecayUnit w = decay_unit(a, sp, LOCAL ? sp.S - 1 : sp.S, blockIdx.x);
   const int v0 = w.vt * 128, nv = a.dv - v0 < 128 ? a.dv - v0 : 128;
-  const int ka = a.dk > 64 ? 2 : 1, va = nv > 64 ? 2 : 1;
+  const int va = nv > 64 ? 2 : 1;
   const int va_all = a.dv > 64 ? 2 : 1;  // the ring's, of every unit
   const uint32_t slot_bytes = da_slot(ka, va_all);
   const int n_slots = da_slots(ka, va_all);
   uint8_t *const s_tile = smem + n_slots * slot_bytes;
   uint8_t *const terms = s_tile + da_state_bytes(ka, va_all);
   const double rate = decay_rate(a.log_decay[w.h]);
-  const int64_t end = w.t1 < w.len ? w.t1 : w.len;
+  const int end = w.t1 < w.len ? w.t1 : w.len;
   // (LOCAL: a segment that nothing comes behind is nobody's start)
   const int chunks = end <= w.t0 || (LOCAL && w.t1 >= w.len)
                          ? 0
-                         : (int)((end - w.t0 + 127) / 128);
+                         : (end - w.t0 + 127) / 128;
   const auto tokens = [&](int g) {
-    const int64_t n = end - w.t0 - 128 * (int64_t)g;
-    return n < 128 ? (int)n : 128;
+    const int n = end - w.t0 - 128 * g;
+    return n < 128 ? n : 128;
   };
   constexpr int PER = LOCAL ? 2 : 3;  // ring items of a chunk: (Q,) K, V
 
@@ -120,13 +157,15 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&x_ready[i], 8);
+      mbar_init(&x_ready[i], 4);
       mbar_init(&x_free[i], 1);
     }
-    mbar_init(&sc_full, 1);
-    mbar_init(&p_ready, 4);
+    mbar_init(&sc_full[0], 1);
+    mbar_init(&sc_full[1], 1);
+    mbar_init(&qs_full, 1);
+    mbar_init(&p_ready, 8);
     mbar_init(&o_full, 1);
-    mbar_init(&o_free, 4);
+    mbar_init(&o_free, 8);
     mbar_init(&s_ready, 8);
     mbar_init(&d_full, 1);
     mbar_init(&mma_done, 1);
@@ -136,7 +175,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     const int j = (int)threadIdx.x - 64;
     const float p = decay_power(rate, j);
     power[j] = p;
-    if (j < 32) back[31 - j] = p;
+    if (j < 16) back[15 - j] = p;
   }
   if (warp == 1) {
     tmem_alloc(&tmem_base, 512);
@@ -147,208 +186,264 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   tc_fence_after();
   const uint32_t tbase = tmem_base;
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-  // all of a warp's lanes, or none
+  // After a wait that ran out a thread waits no more: it goes through its chunks without
+  // (what it writes is no result), arrives where others wait, and ends.
+  bool dead = false;
   const auto wait = [&](uint64_t *bar, int use, int code) {
-    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, (uint32_t)use & 1u, kWaitLimitNs));
-    if (!ok && lane == 0) record_timeout(code);
-    return ok;
+    if (!dead && !mbar_wait(bar, (uint32_t)use & 1u, kWaitLimitNs)) {
+      record_timeout(code);
+      dead = true;
+    }
   };
 
-  if (warp == 0) {
-    // =========================== TMA
-    if (lane == 0) {
+  if (warp < DA_OUT_WARP) {
+    regs_dec<DA_REG_ISSUE>();
+    if (warp == 0 && lane == 0) {
+      // =========================== TMA
       if (!LOCAL) tma_prefetch_desc(&mapQ);
       tma_prefetch_desc(&mapK);
       tma_prefetch_desc(&mapV);
       const int hq = w.h / (a.H / a.Hq), hk = w.h / (a.H / a.Hk), hv = w.h / (a.H / a.Hv);
-      int it = 0;
-      for (int g = 0; g < chunks; ++g) {
-        const int t = (int)(w.t0 + 128 * (int64_t)g);
-        bool ok = true;
-        for (int i = 3 - PER; i < 3; ++i, ++it) {
-          const int slot = it % n_slots;
-          if (it >= n_slots && !mbar_wait(&empty[slot], ((it / n_slots) - 1) & 1, kWaitLimitNs)) {
+      RingAt at;
+      bool ok = true;
+      for (int g = 0; ok && g < chunks; ++g) {
+        const int t = w.t0 + 128 * g;
+        for (int i = 3 - PER; i < 3; ++i, at = at.ahead(1, n_slots)) {
+          if (at.use > 0 && !mbar_wait(&empty[at.slot], (uint32_t)(at.use - 1) & 1u, kWaitLimitNs)) {
             record_timeout(1101);
             ok = false;
             break;
           }
           const int atoms = i == 2 ? va : ka;
-          mbar_arrive_expect_tx(&full[slot], DA_ATOM * (uint32_t)atoms);
+          mbar_arrive_expect_tx(&full[at.slot], DA_ATOM * (uint32_t)atoms);
           for (int x = 0; x < atoms; ++x)
-            tma_load_4d(smem + slot * slot_bytes + x * DA_ATOM,
-                        i == 0 ? &mapQ : i == 1 ? &mapK : &mapV, &full[slot],
+            tma_load_4d(smem + at.slot * slot_bytes + x * DA_ATOM,
+                        i == 0 ? &mapQ : i == 1 ? &mapK : &mapV, &full[at.slot],
                         (i == 2 ? v0 : 0) + 64 * x, i == 0 ? hq : i == 1 ? hk : hv, t, w.b);
         }
-        if (!ok) break;
       }
       // the last copy issued into each slot has landed
-      for (int q = it > n_slots ? it - n_slots : 0; q < it; ++q)
-        if (!mbar_wait(&full[q % n_slots], (q / n_slots) & 1, kWaitLimitNs)) record_timeout(1102);
+      for (int i = 0; i < n_slots; ++i) {
+        const int uses = at.use + (i < at.slot ? 1 : 0);
+        if (uses > 0 && !mbar_wait(&full[i], (uint32_t)(uses - 1) & 1u, kWaitLimitNs)) record_timeout(1102);
+      }
     }
-  } else if (warp == 1) {
-    // =========================== MMA issuer
-    if (lane == 0) {
+    if (warp == 1 && lane == 0) {
+      // =========================== MMA issuer
       const uint32_t nvc = 64u * (uint32_t)va;
       const uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
       const uint32_t id_o = idesc_bf16_f32(128, nvc, false, true);
       const uint32_t id_d = idesc_bf16_f32(128, nvc, true, true);
-      const uint32_t lbo_k = ka == 2 ? DA_ATOM : 0, lbo_x = ka == 2 ? 4096 : 0;
-      const uint32_t st = smem_u32(s_tile), lbo_s = 8192u * (uint32_t)ka;
-      const auto slot_of = [&](int it) { return smem_u32(smem + (it % n_slots) * slot_bytes); };
+      // descriptors: 16-byte steps in their low bits
+      const uint32_t lbo_k = ka == 2 ? DA_ATOM : 0;
+      const uint64_t x_desc = smem_desc_sw128(smem_u32(terms), ka == 2 ? 4096 : 0, 1024);
+      const uint64_t s_desc = smem_desc_sw128(smem_u32(s_tile), 8192u * (uint32_t)ka, 1024);
+      const auto slot_of = [&](const RingAt &r) { return smem_u32(smem + r.slot * slot_bytes); };
       const auto got = [&](uint64_t *bar, int use, int code) {
         if (mbar_wait(bar, (uint32_t)use & 1u, kWaitLimitNs)) return true;
         record_timeout(code);
         return false;
       };
-      int xn = 0;
-      for (int g = 0; g < chunks; ++g) {
-        const int n = tokens(g), it0 = g * PER;
-        const int ik = it0 + PER - 2, iv = it0 + PER - 1;
-        const uint32_t k = slot_of(ik), v = slot_of(iv), q = slot_of(it0);
-        if (!LOCAL) {
-          if (!got(&full[it0 % n_slots], it0 / n_slots, 1110) ||
-              !got(&full[ik % n_slots], ik / n_slots, 1111) ||
-              (g > 0 && !got(&o_full, g - 1, 1112)))
-            break;
-          tc_fence_after();
-          for (int i = 0; i < 4 * ka; ++i) {
-            const uint32_t off = (uint32_t)(i / 4) * DA_ATOM + (uint32_t)(i % 4) * 32;
-            mma_bf16_ss(tbase + DA_COL_SC, smem_desc_sw128(q + off, 0, 1024),
-                        smem_desc_sw128(k + off, 0, 1024), id_sc, i > 0);
-          }
-          mma_commit(&sc_full);
-          if (!got(&s_ready, g, 1113) || (g > 0 && !got(&o_free, g - 1, 1114))) break;
-          tc_fence_after();
-          for (int i = 0; i < 4 * ka; ++i) {
-            const uint32_t off = (uint32_t)(i / 4) * DA_ATOM + (uint32_t)(i % 4) * 32;
-            mma_bf16_ss(tbase + DA_COL_O2, smem_desc_sw128(q + off, 0, 1024),
-                        smem_desc_sw128(st + (uint32_t)i * 2048, lbo_s, 1024), id_o, i > 0);
-          }
-          mma_commit(&empty[it0 % n_slots]);
+      // The scores of chunk g, into the buffer whose weights the products of chunk g - 2
+      // have read (o_free of that chunk, waited for ahead of Q S of chunk g - 1).
+      const auto scores = [&](int g, const RingAt &rq) {
+        const RingAt rk = rq.ahead(1, n_slots);
+        if (!got(&full[rq.slot], rq.use, 1110) || !got(&full[rk.slot], rk.use, 1111)) return false;
+        tc_fence_after();
+        uint64_t q = smem_desc_sw128(slot_of(rq), 0, 1024);
+        uint64_t k = smem_desc_sw128(slot_of(rk), 0, 1024);
+        const uint32_t sc = tbase + DA_COL_SC + 128u * (uint32_t)(g & 1);
+#pragma unroll
+        for (int x = 0; x < ka; ++x, q += DA_ATOM / 16, k += DA_ATOM / 16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // 16 of dk: 32 bytes of the rows
+            mma_bf16_ss(sc, q + 2u * i, k + 2u * i, id_sc, (x | i) > 0);
         }
-        if (!got(&full[iv % n_slots], iv / n_slots, 1115)) break;
-        bool ok = true;
+        mma_commit(&sc_full[g & 1]);
+        return true;
+      };
+      int xn = 0;
+      RingAt r0;  // the chunk's first item
+      bool ok = LOCAL || chunks == 0 || scores(0, r0);
+      for (int g = 0; ok && g < chunks; ++g) {
+        const int n = tokens(g);
+        const RingAt rk = r0.ahead(PER - 2, n_slots), rv = r0.ahead(PER - 1, n_slots);
+        const uint64_t kd = smem_desc_sw128(slot_of(rk), lbo_k, 1024);
+        const uint64_t vd = smem_desc_sw128(slot_of(rv), DA_ATOM, 1024);
+        if (!got(&s_ready, g, 1113)) break;
+        if (!LOCAL) {
+          if (g > 0 && !got(&o_free, g - 1, 1114)) break;
+          tc_fence_after();
+          uint64_t qd = smem_desc_sw128(slot_of(r0), 0, 1024), sd = s_desc;
+#pragma unroll
+          for (int x = 0; x < ka; ++x, qd += DA_ATOM / 16, sd += 8192 / 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // 16 rows of the state
+              mma_bf16_ss(tbase + DA_COL_O, qd + 2u * i, sd + 128u * i, id_o, (x | i) > 0);
+          }
+          mma_commit(&qs_full);
+          mma_commit(&empty[r0.slot]);
+        }
+        if (!got(&full[rv.slot], rv.use, 1115)) break;
+        const RingAt next = r0.ahead(PER, n_slots);
+#pragma unroll 1
         for (int qt = 0; qt < (n + 31) / 32; ++qt, ++xn) {
-          if (!got(&x_ready[xn & 1], xn >> 1, 1116)) {
+          // the next chunk's scores ahead of half of these products: its keys' terms and
+          // its weights can be on their way
+          if (!LOCAL && qt == 2 && g + 1 < chunks && !scores(g + 1, next)) ok = false;
+          if (!ok || !got(&x_ready[xn & 1], xn >> 1, 1116)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t x = smem_u32(terms) + (uint32_t)(xn & 1) * 2 * (uint32_t)ka * 4096;
+          const uint64_t x1 = x_desc + (uint32_t)(xn & 1) * (uint32_t)ka * (2 * 4096 / 16);
+          const uint64_t x2 = x1 + (uint32_t)ka * (4096 / 16);
+          const uint64_t k1 = kd + (uint32_t)qt * (4096 / 16), v1 = vd + (uint32_t)qt * (4096 / 16);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {  // 16 tokens
-            const uint32_t off = (uint32_t)qt * 4096 + (uint32_t)i * 2048;
-            const uint64_t bd = smem_desc_sw128(v + off, DA_ATOM, 1024);
-            mma_bf16_ss(tbase + DA_COL_D,
-                        smem_desc_sw128(x + (uint32_t)ka * 4096 + (uint32_t)i * 2048, lbo_x, 1024),
-                        bd, id_d, (qt | i) > 0);
-            mma_bf16_ss(tbase + DA_COL_D, smem_desc_sw128(x + (uint32_t)i * 2048, lbo_x, 1024), bd,
-                        id_d, 1);
-            mma_bf16_ss(tbase + DA_COL_D, smem_desc_sw128(k + off, lbo_k, 1024), bd, id_d, 1);
+            mma_bf16_ss(tbase + DA_COL_D, x2 + 128u * i, v1 + 128u * i, id_d, (qt | i) > 0);
+            mma_bf16_ss(tbase + DA_COL_D, x1 + 128u * i, v1 + 128u * i, id_d, 1);
+            mma_bf16_ss(tbase + DA_COL_D, k1 + 128u * i, v1 + 128u * i, id_d, 1);
           }
           mma_commit(&x_free[xn & 1]);
         }
         if (!ok) break;
         mma_commit(&d_full);
-        mma_commit(&empty[ik % n_slots]);
+        mma_commit(&empty[rk.slot]);
         if (!LOCAL) {
           if (!got(&p_ready, g, 1117)) break;
           tc_fence_after();
-          for (int i = 0; i < (n + 15) / 16; ++i)
-            mma_bf16_ts(tbase + DA_COL_O1, tbase + DA_COL_SC + (uint32_t)i * 8,
-                        smem_desc_sw128(v + (uint32_t)i * 2048, DA_ATOM, 1024), id_o, i > 0);
+          const uint32_t pc = tbase + DA_COL_SC + 128u * (uint32_t)(g & 1);
+          const int steps = (n + 15) / 16;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < steps)
+              mma_bf16_ts(tbase + DA_COL_O, pc + (uint32_t)(i / 4) * 64 + (uint32_t)(i % 4) * 8,
+                          vd + 128u * i, id_o, 1);
           mma_commit(&o_full);
         }
-        mma_commit(&empty[iv % n_slots]);
+        mma_commit(&empty[rv.slot]);
+        r0 = next;
       }
       mma_commit(&mma_done);
       if (!mbar_wait(&mma_done, 0, kWaitLimitNs)) record_timeout(1118);
     }
-  } else if (warp < 6) {
-    // =========================== P: a row of Sc a thread
-    const int quad = warp & 3;
-    for (int g = 0; !LOCAL && g < chunks; ++g) {
-      if (!wait(&sc_full, g, 1120)) break;
+  } else if (warp < DA_STATE_WARP) {
+    // =========================== P and the outputs: a row and 64 columns a thread
+    regs_dec<DA_REG_OUT>();
+    const int quad = warp & 3, half = (warp - DA_OUT_WARP) >> 2, row = quad * 32 + lane;
+    const float ahead = power[row + 1], rate_f = (float)rate;
+    const size_t orow = (size_t)a.H * a.dv;
+    const uint32_t ocol = tbase + lane_off + DA_COL_O + 64u * (uint32_t)half;
+    const int cols = nv - 64 * half;
+    const bool wide = a.dv % 16 == 0 && reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) +
+                       (((size_t)w.b * a.T + w.t0 + row) * a.H + w.h) * (size_t)a.dv + v0 +
+                       64 * half;
+    for (int g = 0; !LOCAL && g < chunks; ++g, o += 128 * orow) {
+      wait(&sc_full[g & 1], g >> 1, 1120);
+      __syncwarp();
       tc_fence_after();
+      const uint32_t sc = tbase + lane_off + DA_COL_SC + 128u * (uint32_t)(g & 1) +
+                          64u * (uint32_t)half;
+      // opaque: their products would be kept for all chunks, in registers that are not there
+      float rf = rate_f;
+      int ln = lane;
+      asm volatile("" : "+f"(rf), "+r"(ln));
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {  // 64 keys
-        uint32_t p[32];
-#pragma unroll
-        for (int c2 = 0; c2 < 2; ++c2) {
-          const int c = 2 * h + c2;  // 32 keys: all before the warp's rows, or on the diagonal
-          uint32_t r[32];
-          if (c <= quad) {
-            tmem_ld32(tbase + lane_off + DA_COL_SC + 32u * (uint32_t)c, r);
-            tmem_ld_wait();
-          }
-          if (c < quad) {
-            const float f = power[32 * (quad - c) + lane - 31];
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 d = *reinterpret_cast<const float4 *>(&back[j]);
-              p[16 * c2 + j / 2] = pack_bf16x2(__uint_as_float(r[j]) * (f * d.x),
-                                               __uint_as_float(r[j + 1]) * (f * d.y));
-              p[16 * c2 + j / 2 + 1] = pack_bf16x2(__uint_as_float(r[j + 2]) * (f * d.z),
-                                                   __uint_as_float(r[j + 3]) * (f * d.w));
-            }
-          } else if (c == quad) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float x = j <= lane ? __uint_as_float(r[j]) * power[lane - j] : 0.f;
-              const float y = j < lane ? __uint_as_float(r[j + 1]) * power[lane - j - 1] : 0.f;
-              p[16 * c2 + j / 2] = pack_bf16x2(x, y);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) p[16 * c2 + j] = 0u;
-          }
+      for (int c = 0; c < 4; ++c) {  // 16 keys: all before the warp's rows, or on the diagonal
+        const int at = 64 * half + 16 * c - 32 * quad;  // the first, from the warp's first row
+        uint32_t r[16], p[8];
+        if (at < 32) {
+          tmem_ld16(sc + 16u * (uint32_t)c, r);
+          tmem_ld_wait();
         }
-        tmem_st32(tbase + lane_off + DA_COL_SC + 32u * (uint32_t)h, p);
+        if (at < 0) {
+          const float f = power[ln - at - 15];
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 d = *reinterpret_cast<const float4 *>(&back[j]);
+            p[j / 2] = pack_bf16x2(__uint_as_float(r[j]) * (f * d.x),
+                                   __uint_as_float(r[j + 1]) * (f * d.y));
+            p[j / 2 + 1] = pack_bf16x2(__uint_as_float(r[j + 2]) * (f * d.z),
+                                       __uint_as_float(r[j + 3]) * (f * d.w));
+          }
+        } else if (at < 32) {
+          const int gap = ln - at;
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {  // (a power with an exponent below 0 is dropped)
+            const float x = __uint_as_float(r[j]) * exp2_fast(rf * (float)(gap - j));
+            const float y = __uint_as_float(r[j + 1]) * exp2_fast(rf * (float)(gap - j - 1));
+            p[j / 2] = pack_bf16x2(j <= gap ? x : 0.f, j < gap ? y : 0.f);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) p[j] = 0u;
+        }
+        tmem_st8(sc + 8u * (uint32_t)c, p);  // of 64 scores' columns the first 32
+      }
+      // Q S times each row's power, in place: the weights' products are added to it
+      wait(&qs_full, g, 1121);
+      __syncwarp();
+      tc_fence_after();
+      if (half < va) {
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(ocol + (uint32_t)c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * ahead);
+          tmem_st16(ocol + (uint32_t)c, r);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_ready);
-    }
-  } else if (warp < DA_STATE_WARP) {
-    // =========================== outputs: a row a thread
-    const int row = (warp & 3) * 32 + lane;
-    const float ahead = power[row + 1];
-    const size_t orow = (size_t)a.H * a.dv;
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) +
-                       (((size_t)w.b * a.T + w.t0 + row) * a.H + w.h) * (size_t)a.dv + v0;
-    for (int g = 0; !LOCAL && g < chunks; ++g, o += 128 * orow) {
-      if (!wait(&o_full, g, 1130)) break;
+
+      wait(&o_full, g, 1130);
+      __syncwarp();
       tc_fence_after();
       const bool in = row < tokens(g);
-#pragma unroll 1
-      for (int c = 0; c < 64 * va; c += 32) {
-        uint32_t x[32], y[32];
-        tmem_ld32(tbase + lane_off + DA_COL_O1 + (uint32_t)c, x);
-        tmem_ld32(tbase + lane_off + DA_COL_O2 + (uint32_t)c, y);
+      uint32_t x[32];
+      if (half < va) {
+        uint32_t r[32];
+        tmem_ld32(ocol, r);
         tmem_ld_wait();
-        if (c + 32 >= 64 * va) {  // the next chunk's products may take the columns
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&o_free);
-        }
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint32_t r[4];
+        for (int j = 0; j < 16; ++j)
+          x[j] = pack_bf16x2(a.scale * __uint_as_float(r[2 * j]),
+                             a.scale * __uint_as_float(r[2 * j + 1]));
+        tmem_ld32(ocol + 32, r);
+        tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = j + 2 * i;
-            r[i] = pack_bf16x2(
-                a.scale * fmaf(ahead, __uint_as_float(y[e]), __uint_as_float(x[e])),
-                a.scale * fmaf(ahead, __uint_as_float(y[e + 1]), __uint_as_float(x[e + 1])));
-          }
-          if (in && c + j < nv)
-            *reinterpret_cast<uint4 *>(o + c + j) = make_uint4(r[0], r[1], r[2], r[3]);
-        }
+        for (int j = 0; j < 16; ++j)
+          x[16 + j] = pack_bf16x2(a.scale * __uint_as_float(r[2 * j]),
+                                  a.scale * __uint_as_float(r[2 * j + 1]));
+      }
+      tc_fence_before();  // the next chunk's products may take the columns
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free);
+      if (half >= va || !in) continue;
+      // a whole sector of 32 bytes at once where the rows allow it: the stores of a chunk
+      // are bound by the lines that each of them touches
+      if (wide) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8)
+          if (2 * j < cols)
+            stg_32(o + 2 * j, make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]),
+                   make_uint4(x[j + 4], x[j + 5], x[j + 6], x[j + 7]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          if (2 * j < cols)
+            *reinterpret_cast<uint4 *>(o + 2 * j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
       }
     }
   } else {
     // =========================== the state: row `row`, 64 columns a thread
+    regs_inc<DA_REG_STATE>();
     const int sw = warp - DA_STATE_WARP, half = sw >> 2, row = (warp & 3) * 32 + lane;
     const int st = sw * 32 + lane;
     const bool mine = row < a.dk && half < va;
@@ -379,7 +474,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       }
     } else if (!LOCAL && (w.s == 0 || chunks > 0)) {
       for (int s = w.s == 0 ? 0 : 1; s <= w.s; ++s) {
-        const float f = w.s == 0 ? 1.f : decay_power(rate, w.t0 - (int64_t)s * sp.L);
+        const float f = w.s == 0 ? 1.f : decay_power(rate, w.t0 - s * sp.L);
         const float4 *p = own + (size_t)s * (kDecaySlot / 4);
 #pragma unroll
         for (int j = 0; j < 64; j += 4) {
@@ -392,8 +487,10 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       }
     }
     const float2 whole = decay_power2(rate, 128);
-    const auto publish = [&]() {  // the operand of the next chunk's Q S
-      if (row < 64 * ka && half < va) {
+    // D's columns have been read, and (LOCAL: not) the operand of the next chunk's Q S is
+    // there
+    const auto publish = [&]() {
+      if (!LOCAL && row < 64 * ka && half < va) {
         uint8_t *p = s_tile + (uint32_t)(half * ka) * 8192u;
 #pragma unroll
         for (int j = 0; j < 64; j += 8)
@@ -402,63 +499,83 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                          pack_bf16x2(S[j + 4], S[j + 5]), pack_bf16x2(S[j + 6], S[j + 7]));
       }
       fence_proxy_async_smem();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_ready);
     };
-    if (!LOCAL && chunks > 0) publish();
-    const int r = st >> 3, p16 = (st & 7) * 16;  // of 32 tokens, of a row's 128 bytes
+    if (chunks > 0) publish();
+    const int r = (st & 127) >> 3, p16 = (st & 7) * 16;  // of 16 tokens, of a row's 128 bytes
     int xn = 0;
-    for (int g = 0; g < chunks; ++g) {
-      const int n = tokens(g), ik = g * PER + PER - 2, iv = ik + 1;
+    RingAt rk = RingAt{}.ahead(PER - 2, n_slots);
+    for (int g = 0; g < chunks; ++g, rk = rk.ahead(PER, n_slots)) {
+      const int n = tokens(g);
       // the first term replaces K, which Sc has read by then
-      if ((!LOCAL && !wait(&sc_full, g, 1140)) || !wait(&full[ik % n_slots], ik / n_slots, 1141))
-        break;
-      uint8_t *const k = smem + (ik % n_slots) * slot_bytes;
+      if (!LOCAL) wait(&sc_full[g & 1], g >> 1, 1140);
+      wait(&full[rk.slot], rk.use, 1141);
+      uint8_t *const k = smem + rk.slot * slot_bytes;
       if (n < 128) {  // rows behind the end are zeros, whatever they hold
-        if (!wait(&full[iv % n_slots], iv / n_slots, 1142)) break;
-        uint8_t *const v = smem + (iv % n_slots) * slot_bytes;
-        for (int i = st; i < (128 - n) * 8; i += 256)
+        const RingAt rv = rk.ahead(1, n_slots);
+        wait(&full[rv.slot], rv.use, 1142);
+        uint8_t *const v = smem + rv.slot * slot_bytes;
+        // (by the first four warps, whose first tokens the products wait for)
+        for (int i = st; half == 0 && i < (128 - n) * 8; i += 128)
           for (int x = 0; x < va; ++x)
             *reinterpret_cast<uint4 *>(v + x * DA_ATOM + n * 128 + i * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
       }
-      bool ok = true;
-      for (int qt = 0; qt < (n + 31) / 32; ++qt, ++xn) {
-        if (xn >= 2 && !wait(&x_free[xn & 1], (xn >> 1) - 1, 1143)) {
-          ok = false;
-          break;
-        }
-        const int j = qt * 32 + r;
-        uint8_t *const x = terms + (uint32_t)(xn & 1) * 2 * (uint32_t)ka * 4096 + r * 128 + p16;
-        for (int i = 0; i < ka; ++i) {
-          uint4 *const kp = reinterpret_cast<uint4 *>(k + i * DA_ATOM + j * 128 + p16);
-          uint4 t0 = make_uint4(0u, 0u, 0u, 0u), t1 = t0, t2 = t0;
-          if (j < n) key_terms(*kp, power[n - 1 - j], t0, t1, t2);
-          *kp = t0;
-          *reinterpret_cast<uint4 *>(x + i * 4096) = t1;
-          *reinterpret_cast<uint4 *>(x + (ka + i) * 4096) = t2;
+      // 32 tokens at a time, four warps the even ones and four the odd: a warp's vectors
+      // are few and their terms one long chain
+#pragma unroll 1
+      for (int qt = half; qt < (n + 31) / 32; qt += 2, ++xn) {
+        if (xn >= 1) wait(&x_free[half], xn - 1, 1143);
+        uint8_t *const x = terms + (uint32_t)half * 2 * (uint32_t)ka * 4096 + r * 128 + p16;
+        uint8_t *const kp = k + (qt * 32 + r) * 128 + p16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // 16 tokens
+          const int j = qt * 32 + 16 * h + r;
+          const bool in = j < n;
+          const float wj = in ? power[n - 1 - j] : 0.f;
+          const float2 w2 = make_float2(wj, wj);
+          uint4 raw[ka];
+#pragma unroll
+          for (int i = 0; i < ka; ++i) {
+            raw[i] = *reinterpret_cast<const uint4 *>(kp + i * DA_ATOM + h * 2048);
+            if (!in) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < ka; ++i) {
+            uint4 t0, t1, t2;
+            key_terms(raw[i].x, w2, t0.x, t1.x, t2.x);
+            key_terms(raw[i].y, w2, t0.y, t1.y, t2.y);
+            key_terms(raw[i].z, w2, t0.z, t1.z, t2.z);
+            key_terms(raw[i].w, w2, t0.w, t1.w, t2.w);
+            *reinterpret_cast<uint4 *>(kp + i * DA_ATOM + h * 2048) = t0;
+            *reinterpret_cast<uint4 *>(x + i * 4096 + h * 2048) = t1;
+            *reinterpret_cast<uint4 *>(x + (ka + i) * 4096 + h * 2048) = t2;
+          }
         }
         fence_proxy_async_smem();
-        tc_fence_before();  // D's columns have been read
         __syncwarp();
-        if (lane == 0) mbar_arrive(&x_ready[xn & 1]);
+        if (lane == 0) mbar_arrive(&x_ready[half]);
       }
-      if (!ok || !wait(&d_full, g, 1144)) break;
+      wait(&d_full, g, 1144);
+      __syncwarp();
       tc_fence_after();
       const float2 f = n == 128 ? whole : make_float2(power[n], 0.f);
       if (half < va) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t d[32];
-          tmem_ld32(tbase + lane_off + DA_COL_D + (uint32_t)(64 * half + 32 * c), d);
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t d[2][16];
+          tmem_ld16(tbase + lane_off + DA_COL_D + (uint32_t)(64 * half + 16 * c), d[0]);
+          tmem_ld16(tbase + lane_off + DA_COL_D + (uint32_t)(64 * half + 16 * c + 16), d[1]);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            S[32 * c + j] = fmaf(S[32 * c + j], f.x,
-                                 fmaf(S[32 * c + j], f.y, __uint_as_float(d[j])));
+            S[16 * c + j] = fmaf(S[16 * c + j], f.x,
+                                 fmaf(S[16 * c + j], f.y, __uint_as_float(d[j / 16][j % 16])));
         }
       }
-      if (!LOCAL && g + 1 < chunks) publish();
+      if (g + 1 < chunks) publish();
     }
     if (LOCAL) {
       if (chunks > 0) {
@@ -477,11 +594,11 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   }
   if (!LOCAL) {
     // outputs behind the sequence's end
-    const int64_t z0 = w.t0 > w.len ? w.t0 : w.len;
+    const int z0 = w.t0 > w.len ? w.t0 : w.len;
     const int per = nv / 8;
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) +
                        (((size_t)w.b * a.T + z0) * a.H + w.h) * (size_t)a.dv + v0;
-    for (int64_t i = threadIdx.x; i < (w.t1 - z0) * per; i += DA_THREADS)
+    for (int64_t i = threadIdx.x; i < (int64_t)(w.t1 - z0) * per; i += DA_THREADS)
       *reinterpret_cast<uint4 *>(o + (size_t)(i / per) * a.H * a.dv + (i % per) * 8) =
           make_uint4(0u, 0u, 0u, 0u);
   }
@@ -518,10 +635,12 @@ int launch_tc_decay(const DecayArgs &a, void *workspace, cudaStream_t stream) {
     return 2;
   static OncePerDevice attrs;
   if (!attrs.run([] {
-        return cudaFuncSetAttribute(tc_decay<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)DA_SMEM + 1024) == cudaSuccess &&
-               cudaFuncSetAttribute(tc_decay<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)DA_SMEM + 1024) == cudaSuccess;
+        const auto set = [](auto *kern) {
+          return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)DA_SMEM + 1024) == cudaSuccess;
+        };
+        return set(tc_decay<true, 1>) && set(tc_decay<true, 2>) && set(tc_decay<false, 1>) &&
+               set(tc_decay<false, 2>);
       }))
     return 1;
   const DecaySplit sp = decay_split_tc(a.B, a.T, a.H, a.dv);
@@ -532,12 +651,13 @@ int launch_tc_decay(const DecayArgs &a, void *workspace, cudaStream_t stream) {
   cfg.cfg.dynamicSmemBytes = DA_SMEM + 1024;
   if (sp.S > 1) {
     cfg.cfg.gridDim = dim3((unsigned)(heads * (sp.S - 1)));
-    if (cudaLaunchKernelEx(&cfg.cfg, tc_decay<true>, mQ, mK, mV, a, sp, slots, 1) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg.cfg, a.dk > 64 ? tc_decay<true, 2> : tc_decay<true, 1>, mQ, mK, mV,
+                           a, sp, slots, 1) != cudaSuccess)
       return 1;
   }
   cfg.cfg.gridDim = dim3((unsigned)(heads * sp.S));
-  return cudaLaunchKernelEx(&cfg.cfg, tc_decay<false>, mQ, mK, mV, a, sp, slots,
-                            sp.S > 1 ? 0 : 1) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg.cfg, a.dk > 64 ? tc_decay<false, 2> : tc_decay<false, 1>, mQ, mK,
+                            mV, a, sp, slots, sp.S > 1 ? 0 : 1) == cudaSuccess
              ? 0
              : 1;
 }
