@@ -46,19 +46,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Whether the phase has completed; the thread is not suspended.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Same as mbar_try_wait, but the thread may sleep until the phase completes or about
+// Same, but the thread may sleep until the phase completes or about
 // `hint_ns` have passed, leaving its issue slots to the other warps.
 __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t *bar, uint32_t parity,
                                                     uint32_t hint_ns) {
@@ -179,6 +167,15 @@ __device__ __forceinline__ void tma_store_3d_hint(const CUtensorMap *map, const 
       "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "l"(policy)
       : "memory");
 }
+// 4-D tiled store.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int32_t x,
+                                             int32_t y, int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::
+          "l"(reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(src))
+      : "memory");
+}
 // Untiled bulk copies (both addresses 16-byte aligned, size % 16 == 0).
 __device__ __forceinline__ void bulk_load(void *dst, const void *gsrc, uint32_t bytes,
                                           uint64_t *bar) {
@@ -288,6 +285,16 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bo
   return r != 0;
 }
 
+// One lane of a converged warp (the same every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 // Registers of a warpgroup's threads (all four warps execute these; the sum over the
 // block's warpgroups must stay within what the block was launched with).
 template <int N>
@@ -482,13 +489,6 @@ __device__ __forceinline__ void stg_stream(void *p, const u32x8 &v) {
       "r"(v.lo.x), "r"(v.lo.y), "r"(v.lo.z), "r"(v.lo.w), "r"(v.hi.x), "r"(v.hi.y), "r"(v.hi.z),
       "r"(v.hi.w)
       : "memory");
-}
-
-// 32-byte global store.
-__device__ __forceinline__ void stg_32(void *p, const uint4 &a, const uint4 &b) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
-               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

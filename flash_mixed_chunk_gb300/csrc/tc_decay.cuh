@@ -10,9 +10,9 @@
 //
 //   Sc = Q K^T          then P = Sc lam^(i-j), masked, bf16, back into TMEM
 //   O  = Q S            S: the state before the chunk, rounded to bf16
-//   O  = lam^(i+1) O + P V      (the rows scaled in place in between)
+//   O  = lam^(i+1) O + P V      (the rows scaled in place in between, P and they by scale)
 //   D  = K~^T V         K~_j = lam^(n-1-j) k_j
-//   o = scale O,   S = lam^n S + D
+//   o = O,   S = lam^n S + D
 //
 // What is rounded: P and the operand S, half a step of bf16 each, as is the output.
 // K~ is not: a product of a weight in 24 bits and a key in 8 goes in as three bf16
@@ -25,9 +25,9 @@
 // launch (LOCAL) forms only the segments' states, a second starts every segment from
 // the sum of those before it.
 //
-// Warps (640 threads): 0 TMA, 1 MMA issuer, 4-11 P and the outputs, 12-19 the state:
-// K~'s terms from K in place (the first term) and through two buffers of 32 tokens (the
-// others), then D from TMEM into the state and its bf16 copy in shared memory.  P takes
+// Warps (768 threads): 0 TMA, 1 MMA issuer, 2 output stores; 4-11 P and the outputs; 12-15
+// K~'s terms, from K in place (the first term) and through two buffers of 32 tokens (the
+// others); 16-23 the state, from D in TMEM, and its bf16 copy in shared memory.  P takes
 // the columns of the scores that its own warp has read, of one of two buffers.
 #pragma once
 
@@ -37,16 +37,17 @@
 namespace fmca {
 namespace {
 
-constexpr int DA_THREADS = 640;
+constexpr int DA_THREADS = 768;
 constexpr int DA_SLOTS = 12;             // ring slots at most
 constexpr uint32_t DA_ATOM = 16384;      // 64 columns of 128 tokens
 constexpr uint32_t DA_SMEM = 229376;     // ring, state, terms
 constexpr uint32_t DA_COL_SC = 0, DA_COL_O = 256, DA_COL_D = 384;  // two of Sc
-constexpr int DA_OUT_WARP = 4, DA_STATE_WARP = 12;
-// Registers of a thread: 96 at the launch, 640 of them; the state's 64 places need more,
-// the first four warps little.
-constexpr int DA_REG_ISSUE = 64, DA_REG_OUT = 88, DA_REG_STATE = 120;
-static_assert(128 * DA_REG_ISSUE + 256 * DA_REG_OUT + 256 * DA_REG_STATE <= 96 * DA_THREADS,
+constexpr int DA_OUT_WARP = 4, DA_KEY_WARP = 12, DA_STATE_WARP = 16;
+// Registers of a thread: 80 at the launch of 768; the state's 64 places need more, the
+// first four warps and the keys' less.
+constexpr int DA_REG_ISSUE = 56, DA_REG_OUT = 80, DA_REG_KEYS = 56, DA_REG_STATE = 104;
+static_assert(128 * DA_REG_ISSUE + 256 * DA_REG_OUT + 128 * DA_REG_KEYS + 256 * DA_REG_STATE <=
+                  80 * DA_THREADS,
               "tc_decay's warps would wait for registers that the block has not");
 
 // Shared memory by the 64-column blocks of dk (ka) and of the unit's dv (va).
@@ -66,6 +67,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// A wait with a limit of turns (each suspends the thread for a while; about a second in
+// all), without a look at the clock: the roles' loops of a chunk share the instruction
+// caches, and what is not in a warp's nearest one costs it more than its products.
+__device__ __forceinline__ bool da_wait(uint64_t *bar, int use) {
+#pragma unroll 1
+  for (int i = 0; !mbar_try_wait_sleep(bar, (uint32_t)use & 1u, 1000u); ++i)
+    if (i > (1 << 23)) return false;
+  return true;
 }
 
 // A place in the ring and how often it has been used before, kept step by step: a
@@ -116,19 +127,23 @@ __device__ __forceinline__ void key_terms(uint32_t k, float2 w, uint32_t &t0, ui
 template <bool LOCAL, int ka>
 __global__ void __launch_bounds__(DA_THREADS, 1)
     tc_decay(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-             const __grid_constant__ CUtensorMap mapV, const __grid_constant__ DecayArgs a,
+             const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO,
+             const __grid_constant__ DecayArgs a,
              const DecaySplit sp, float *__restrict__ slots, int first) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t full[DA_SLOTS], empty[DA_SLOTS], x_ready[2], x_free[2];
+  __shared__ __align__(8) uint64_t staged[2], stored[2];
   __shared__ __align__(8) uint64_t sc_full[2], qs_full, p_ready, o_full, o_free, s_ready, d_full,
       mma_done;
   __shared__ __align__(16) float back[16];  // lam^(15 - j)
   __shared__ float power[129];              // lam^j
   __shared__ uint32_t tmem_base;
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // (the same in all of a warp's lanes, for the compiler too: the products' operands then
+  // come straight from uniform registers)
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   if (first) griddep_wait();
   if (LOCAL || first) griddep_launch_dependents();
   const DecayUnit w = decay_unit(a, sp, LOCAL ? sp.S - 1 : sp.S, blockIdx.x);
@@ -159,6 +174,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&x_ready[i], 4);
       mbar_init(&x_free[i], 1);
+      mbar_init(&staged[i], 8);
+      mbar_init(&stored[i], 1);
     }
     mbar_init(&sc_full[0], 1);
     mbar_init(&sc_full[1], 1);
@@ -190,7 +207,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   // (what it writes is no result), arrives where others wait, and ends.
   bool dead = false;
   const auto wait = [&](uint64_t *bar, int use, int code) {
-    if (!dead && !mbar_wait(bar, (uint32_t)use & 1u, kWaitLimitNs)) {
+    if (!dead && !da_wait(bar, use)) {
       record_timeout(code);
       dead = true;
     }
@@ -209,7 +226,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       for (int g = 0; ok && g < chunks; ++g) {
         const int t = w.t0 + 128 * g;
         for (int i = 3 - PER; i < 3; ++i, at = at.ahead(1, n_slots)) {
-          if (at.use > 0 && !mbar_wait(&empty[at.slot], (uint32_t)(at.use - 1) & 1u, kWaitLimitNs)) {
+          if (at.use > 0 && !da_wait(&empty[at.slot], at.use - 1)) {
             record_timeout(1101);
             ok = false;
             break;
@@ -225,11 +242,12 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       // the last copy issued into each slot has landed
       for (int i = 0; i < n_slots; ++i) {
         const int uses = at.use + (i < at.slot ? 1 : 0);
-        if (uses > 0 && !mbar_wait(&full[i], (uint32_t)(uses - 1) & 1u, kWaitLimitNs)) record_timeout(1102);
+        if (uses > 0 && !da_wait(&full[i], uses - 1)) record_timeout(1102);
       }
     }
-    if (warp == 1 && lane == 0) {
-      // =========================== MMA issuer
+    if (warp == 1) {
+      // =========================== MMA issuer: all lanes go through, one issues
+      const bool lead = elect_one();
       const uint32_t nvc = 64u * (uint32_t)va;
       const uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
       const uint32_t id_o = idesc_bf16_f32(128, nvc, false, true);
@@ -240,8 +258,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       const uint64_t s_desc = smem_desc_sw128(smem_u32(s_tile), 8192u * (uint32_t)ka, 1024);
       const auto slot_of = [&](const RingAt &r) { return smem_u32(smem + r.slot * slot_bytes); };
       const auto got = [&](uint64_t *bar, int use, int code) {
-        if (mbar_wait(bar, (uint32_t)use & 1u, kWaitLimitNs)) return true;
-        record_timeout(code);
+        if (__all_sync(0xFFFFFFFFu, da_wait(bar, use))) return true;
+        if (lead) record_timeout(code);
         return false;
       };
       // The scores of chunk g, into the buffer whose weights the products of chunk g - 2
@@ -253,13 +271,15 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         uint64_t q = smem_desc_sw128(slot_of(rq), 0, 1024);
         uint64_t k = smem_desc_sw128(slot_of(rk), 0, 1024);
         const uint32_t sc = tbase + DA_COL_SC + 128u * (uint32_t)(g & 1);
+        if (lead) {
 #pragma unroll
-        for (int x = 0; x < ka; ++x, q += DA_ATOM / 16, k += DA_ATOM / 16) {
+          for (int x = 0; x < ka; ++x, q += DA_ATOM / 16, k += DA_ATOM / 16) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)  // 16 of dk: 32 bytes of the rows
-            mma_bf16_ss(sc, q + 2u * i, k + 2u * i, id_sc, (x | i) > 0);
+            for (int i = 0; i < 4; ++i)  // 16 of dk: 32 bytes of the rows
+              mma_bf16_ss(sc, q + 2u * i, k + 2u * i, id_sc, (x | i) > 0);
+          }
+          mma_commit(&sc_full[g & 1]);
         }
-        mma_commit(&sc_full[g & 1]);
         return true;
       };
       int xn = 0;
@@ -275,14 +295,16 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           if (g > 0 && !got(&o_free, g - 1, 1114)) break;
           tc_fence_after();
           uint64_t qd = smem_desc_sw128(slot_of(r0), 0, 1024), sd = s_desc;
+          if (lead) {
 #pragma unroll
-          for (int x = 0; x < ka; ++x, qd += DA_ATOM / 16, sd += 8192 / 16) {
+            for (int x = 0; x < ka; ++x, qd += DA_ATOM / 16, sd += 8192 / 16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)  // 16 rows of the state
-              mma_bf16_ss(tbase + DA_COL_O, qd + 2u * i, sd + 128u * i, id_o, (x | i) > 0);
+              for (int i = 0; i < 4; ++i)  // 16 rows of the state
+                mma_bf16_ss(tbase + DA_COL_O, qd + 2u * i, sd + 128u * i, id_o, (x | i) > 0);
+            }
+            mma_commit(&qs_full);
+            mma_commit(&empty[r0.slot]);
           }
-          mma_commit(&qs_full);
-          mma_commit(&empty[r0.slot]);
         }
         if (!got(&full[rv.slot], rv.use, 1115)) break;
         const RingAt next = r0.ahead(PER, n_slots);
@@ -299,48 +321,68 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           const uint64_t x1 = x_desc + (uint32_t)(xn & 1) * (uint32_t)ka * (2 * 4096 / 16);
           const uint64_t x2 = x1 + (uint32_t)ka * (4096 / 16);
           const uint64_t k1 = kd + (uint32_t)qt * (4096 / 16), v1 = vd + (uint32_t)qt * (4096 / 16);
+          if (lead) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {  // 16 tokens
-            mma_bf16_ss(tbase + DA_COL_D, x2 + 128u * i, v1 + 128u * i, id_d, (qt | i) > 0);
-            mma_bf16_ss(tbase + DA_COL_D, x1 + 128u * i, v1 + 128u * i, id_d, 1);
-            mma_bf16_ss(tbase + DA_COL_D, k1 + 128u * i, v1 + 128u * i, id_d, 1);
+            for (int i = 0; i < 2; ++i) {  // 16 tokens
+              mma_bf16_ss(tbase + DA_COL_D, x2 + 128u * i, v1 + 128u * i, id_d, (qt | i) > 0);
+              mma_bf16_ss(tbase + DA_COL_D, x1 + 128u * i, v1 + 128u * i, id_d, 1);
+              mma_bf16_ss(tbase + DA_COL_D, k1 + 128u * i, v1 + 128u * i, id_d, 1);
+            }
+            mma_commit(&x_free[xn & 1]);
           }
-          mma_commit(&x_free[xn & 1]);
         }
         if (!ok) break;
-        mma_commit(&d_full);
-        mma_commit(&empty[rk.slot]);
+        if (lead) {
+          mma_commit(&d_full);
+          mma_commit(&empty[rk.slot]);
+        }
         if (!LOCAL) {
           if (!got(&p_ready, g, 1117)) break;
           tc_fence_after();
           const uint32_t pc = tbase + DA_COL_SC + 128u * (uint32_t)(g & 1);
           const int steps = (n + 15) / 16;
+          if (lead) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < steps)
-              mma_bf16_ts(tbase + DA_COL_O, pc + (uint32_t)(i / 4) * 64 + (uint32_t)(i % 4) * 8,
-                          vd + 128u * i, id_o, 1);
-          mma_commit(&o_full);
+            for (int i = 0; i < 8; ++i)
+              if (i < steps)
+                mma_bf16_ts(tbase + DA_COL_O, pc + (uint32_t)(i / 4) * 64 + (uint32_t)(i % 4) * 8,
+                            vd + 128u * i, id_o, 1);
+            mma_commit(&o_full);
+          }
         }
-        mma_commit(&empty[rv.slot]);
+        if (LOCAL && lead) mma_commit(&empty[rv.slot]);
         r0 = next;
       }
-      mma_commit(&mma_done);
-      if (!mbar_wait(&mma_done, 0, kWaitLimitNs)) record_timeout(1118);
+      if (lead) mma_commit(&mma_done);
+      got(&mma_done, 0, 1118);
     }
-  } else if (warp < DA_STATE_WARP) {
+    if (!LOCAL && warp == 2 && lane == 0) {
+      // =========================== output stores
+      RingAt rv = RingAt{}.ahead(PER - 1, n_slots);
+      bool ok = true;
+      for (int g = 0; ok && g < chunks; ++g, rv = rv.ahead(PER, n_slots)) {
+        if (!da_wait(&staged[g & 1], g >> 1)) {
+          record_timeout(1150);
+          ok = false;
+          break;
+        }
+        for (int x = 0; x < va; ++x)
+          tma_store_4d(&mapO, smem + rv.slot * slot_bytes + x * DA_ATOM, v0 + 64 * x, w.h,
+                       w.t0 + 128 * g, w.b);
+        bulk_commit_group();
+        bulk_wait_group_read<0>();
+        mbar_arrive(&empty[rv.slot]);
+        mbar_arrive(&stored[g & 1]);
+      }
+      bulk_wait_group<0>();
+    }
+  } else if (warp < DA_KEY_WARP) {
     // =========================== P and the outputs: a row and 64 columns a thread
-    regs_dec<DA_REG_OUT>();
     const int quad = warp & 3, half = (warp - DA_OUT_WARP) >> 2, row = quad * 32 + lane;
-    const float ahead = power[row + 1], rate_f = (float)rate;
-    const size_t orow = (size_t)a.H * a.dv;
+    const float ahead = a.scale * power[row + 1], rate_f = (float)rate;
     const uint32_t ocol = tbase + lane_off + DA_COL_O + 64u * (uint32_t)half;
-    const int cols = nv - 64 * half;
-    const bool wide = a.dv % 16 == 0 && reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) +
-                       (((size_t)w.b * a.T + w.t0 + row) * a.H + w.h) * (size_t)a.dv + v0 +
-                       64 * half;
-    for (int g = 0; !LOCAL && g < chunks; ++g, o += 128 * orow) {
+    RingAt rv = RingAt{}.ahead(PER - 1, n_slots);
+    for (int g = 0; !LOCAL && g < chunks; ++g, rv = rv.ahead(PER, n_slots)) {
       wait(&sc_full[g & 1], g >> 1, 1120);
       __syncwarp();
       tc_fence_after();
@@ -359,7 +401,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           tmem_ld_wait();
         }
         if (at < 0) {
-          const float f = power[ln - at - 15];
+          const float f = a.scale * power[ln - at - 15];
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float4 d = *reinterpret_cast<const float4 *>(&back[j]);
@@ -372,8 +414,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           const int gap = ln - at;
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {  // (a power with an exponent below 0 is dropped)
-            const float x = __uint_as_float(r[j]) * exp2_fast(rf * (float)(gap - j));
-            const float y = __uint_as_float(r[j + 1]) * exp2_fast(rf * (float)(gap - j - 1));
+            const float x = __uint_as_float(r[j]) * (a.scale * exp2_fast(rf * (float)(gap - j)));
+            const float y = __uint_as_float(r[j + 1]) * (a.scale * exp2_fast(rf * (float)(gap - j - 1)));
             p[j / 2] = pack_bf16x2(j <= gap ? x : 0.f, j < gap ? y : 0.f);
           }
         } else {
@@ -405,40 +447,91 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       wait(&o_full, g, 1130);
       __syncwarp();
       tc_fence_after();
+      if (g > 1) wait(&stored[g & 1], (g >> 1) - 1, 1131);
+      // Through v's place in the ring, which its products have left, and out by TMA: 32-byte
+      // stores from the registers hold the SM's other shared memory traffic up for 1800 of
+      // 10000 cycles a chunk.  Rows behind the end are zeros.
       const bool in = row < tokens(g);
-      uint32_t x[32];
       if (half < va) {
-        uint32_t r[32];
-        tmem_ld32(ocol, r);
-        tmem_ld_wait();
+        uint8_t *const out = smem + rv.slot * slot_bytes + (uint32_t)half * DA_ATOM;
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(ocol + (uint32_t)c, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          x[j] = pack_bf16x2(a.scale * __uint_as_float(r[2 * j]),
-                             a.scale * __uint_as_float(r[2 * j + 1]));
-        tmem_ld32(ocol + 32, r);
-        tmem_ld_wait();
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t x = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            r[j] = in ? x : 0u;
+          }
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          x[16 + j] = pack_bf16x2(a.scale * __uint_as_float(r[2 * j]),
-                                  a.scale * __uint_as_float(r[2 * j + 1]));
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<uint4 *>(out + sw128_offset((uint32_t)row, 2u * c + 16u * j)) =
+                make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        }
+        fence_proxy_async_smem();
       }
       tc_fence_before();  // the next chunk's products may take the columns
       __syncwarp();
-      if (lane == 0) mbar_arrive(&o_free);
-      if (half >= va || !in) continue;
-      // a whole sector of 32 bytes at once where the rows allow it: the stores of a chunk
-      // are bound by the lines that each of them touches
-      if (wide) {
+      if (lane == 0) {
+        mbar_arrive(&o_free);
+        mbar_arrive(&staged[g & 1]);
+      }
+    }
+  } else if (warp < DA_STATE_WARP) {
+    // =========================== the keys' terms, 32 tokens at a time
+    regs_dec<DA_REG_KEYS>();
+    const int kt = (int)threadIdx.x - 32 * DA_KEY_WARP;
+    const int r = kt >> 3, p16 = (kt & 7) * 16;  // of 16 tokens, of a row's 128 bytes
+    int xn = 0;
+    RingAt rk = RingAt{}.ahead(PER - 2, n_slots);
+    for (int g = 0; g < chunks; ++g, rk = rk.ahead(PER, n_slots)) {
+      const int n = tokens(g);
+      // the first term replaces K, which Sc has read by then
+      if (!LOCAL) wait(&sc_full[g & 1], g >> 1, 1140);
+      wait(&full[rk.slot], rk.use, 1141);
+      uint8_t *const k = smem + rk.slot * slot_bytes;
+      if (n < 128) {  // rows behind the end are zeros, whatever they hold
+        const RingAt rv = rk.ahead(1, n_slots);
+        wait(&full[rv.slot], rv.use, 1142);
+        uint8_t *const v = smem + rv.slot * slot_bytes;
+        for (int i = kt; i < (128 - n) * 8; i += 128)
+          for (int x = 0; x < va; ++x)
+            *reinterpret_cast<uint4 *>(v + x * DA_ATOM + n * 128 + i * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll 1
+      for (int qt = 0; qt < (n + 31) / 32; ++qt, ++xn) {
+        if (xn > 1) wait(&x_free[xn & 1], (xn >> 1) - 1, 1143);
+        uint8_t *const x = terms + (uint32_t)(xn & 1) * 2 * (uint32_t)ka * 4096 + r * 128 + p16;
+        uint8_t *const kp = k + (qt * 32 + r) * 128 + p16;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {  // 16 tokens
+          const int j = qt * 32 + 16 * h + r;
+          const float wj = j < n ? power[n - 1 - j] : 0.f;
+          const float2 w2 = make_float2(wj, wj);
+          uint4 raw[ka];
 #pragma unroll
-        for (int j = 0; j < 32; j += 8)
-          if (2 * j < cols)
-            stg_32(o + 2 * j, make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]),
-                   make_uint4(x[j + 4], x[j + 5], x[j + 6], x[j + 7]));
-      } else {
+          for (int i = 0; i < ka; ++i) {
+            raw[i] = *reinterpret_cast<const uint4 *>(kp + i * DA_ATOM + h * 2048);
+            if (j >= n) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          if (2 * j < cols)
-            *reinterpret_cast<uint4 *>(o + 2 * j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+          for (int i = 0; i < ka; ++i) {
+            uint4 t0, t1, t2;
+            key_terms(raw[i].x, w2, t0.x, t1.x, t2.x);
+            key_terms(raw[i].y, w2, t0.y, t1.y, t2.y);
+            key_terms(raw[i].z, w2, t0.z, t1.z, t2.z);
+            key_terms(raw[i].w, w2, t0.w, t1.w, t2.w);
+            *reinterpret_cast<uint4 *>(kp + i * DA_ATOM + h * 2048) = t0;
+            *reinterpret_cast<uint4 *>(x + i * 4096 + h * 2048) = t1;
+            *reinterpret_cast<uint4 *>(x + (ka + i) * 4096 + h * 2048) = t2;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_ready[xn & 1]);
       }
     }
   } else {
@@ -504,60 +597,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       if (lane == 0) mbar_arrive(&s_ready);
     };
     if (chunks > 0) publish();
-    const int r = (st & 127) >> 3, p16 = (st & 7) * 16;  // of 16 tokens, of a row's 128 bytes
-    int xn = 0;
-    RingAt rk = RingAt{}.ahead(PER - 2, n_slots);
-    for (int g = 0; g < chunks; ++g, rk = rk.ahead(PER, n_slots)) {
+    for (int g = 0; g < chunks; ++g) {
       const int n = tokens(g);
-      // the first term replaces K, which Sc has read by then
-      if (!LOCAL) wait(&sc_full[g & 1], g >> 1, 1140);
-      wait(&full[rk.slot], rk.use, 1141);
-      uint8_t *const k = smem + rk.slot * slot_bytes;
-      if (n < 128) {  // rows behind the end are zeros, whatever they hold
-        const RingAt rv = rk.ahead(1, n_slots);
-        wait(&full[rv.slot], rv.use, 1142);
-        uint8_t *const v = smem + rv.slot * slot_bytes;
-        // (by the first four warps, whose first tokens the products wait for)
-        for (int i = st; half == 0 && i < (128 - n) * 8; i += 128)
-          for (int x = 0; x < va; ++x)
-            *reinterpret_cast<uint4 *>(v + x * DA_ATOM + n * 128 + i * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-      }
-      // 32 tokens at a time, four warps the even ones and four the odd: a warp's vectors
-      // are few and their terms one long chain
-#pragma unroll 1
-      for (int qt = half; qt < (n + 31) / 32; qt += 2, ++xn) {
-        if (xn >= 1) wait(&x_free[half], xn - 1, 1143);
-        uint8_t *const x = terms + (uint32_t)half * 2 * (uint32_t)ka * 4096 + r * 128 + p16;
-        uint8_t *const kp = k + (qt * 32 + r) * 128 + p16;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 16 tokens
-          const int j = qt * 32 + 16 * h + r;
-          const bool in = j < n;
-          const float wj = in ? power[n - 1 - j] : 0.f;
-          const float2 w2 = make_float2(wj, wj);
-          uint4 raw[ka];
-#pragma unroll
-          for (int i = 0; i < ka; ++i) {
-            raw[i] = *reinterpret_cast<const uint4 *>(kp + i * DA_ATOM + h * 2048);
-            if (!in) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int i = 0; i < ka; ++i) {
-            uint4 t0, t1, t2;
-            key_terms(raw[i].x, w2, t0.x, t1.x, t2.x);
-            key_terms(raw[i].y, w2, t0.y, t1.y, t2.y);
-            key_terms(raw[i].z, w2, t0.z, t1.z, t2.z);
-            key_terms(raw[i].w, w2, t0.w, t1.w, t2.w);
-            *reinterpret_cast<uint4 *>(kp + i * DA_ATOM + h * 2048) = t0;
-            *reinterpret_cast<uint4 *>(x + i * 4096 + h * 2048) = t1;
-            *reinterpret_cast<uint4 *>(x + (ka + i) * 4096 + h * 2048) = t2;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x_ready[half]);
-      }
       wait(&d_full, g, 1144);
       __syncwarp();
       tc_fence_after();
@@ -570,9 +611,15 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           tmem_ld16(tbase + lane_off + DA_COL_D + (uint32_t)(64 * half + 16 * c + 16), d[1]);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            S[16 * c + j] = fmaf(S[16 * c + j], f.x,
-                                 fmaf(S[16 * c + j], f.y, __uint_as_float(d[j / 16][j % 16])));
+          for (int j = 0; j < 32; j += 2) {
+            float *const s = S + 16 * c + j;
+            const float2 o = make_float2(s[0], s[1]);
+            const float2 y = fma2(o, make_float2(f.x, f.x),
+                                  fma2(o, make_float2(f.y, f.y),
+                                       make_float2(__uint_as_float(d[j / 16][j % 16]),
+                                                   __uint_as_float(d[j / 16][j % 16 + 1]))));
+            s[0] = y.x, s[1] = y.y;
+          }
         }
       }
       if (g + 1 < chunks) publish();
@@ -593,8 +640,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     }
   }
   if (!LOCAL) {
-    // outputs behind the sequence's end
-    const int z0 = w.t0 > w.len ? w.t0 : w.len;
+    // outputs behind the sequence's last chunk
+    const int z0 = w.t0 + 128 * chunks;
     const int per = nv / 8;
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) +
                        (((size_t)w.b * a.T + z0) * a.H + w.h) * (size_t)a.dv + v0;
@@ -628,10 +675,12 @@ bool make_map_decay(CUtensorMap *m, const void *base, int d, int heads, int T, i
 }  // namespace
 
 int launch_tc_decay(const DecayArgs &a, void *workspace, cudaStream_t stream) {
-  CUtensorMap mQ, mK, mV;
+  CUtensorMap mQ, mK, mV, mO;
+  const int64_t os[3] = {(int64_t)a.T * a.H * a.dv, (int64_t)a.H * a.dv, a.dv};
   if (!make_map_decay(&mQ, a.q, a.dk, a.Hq, a.T, a.B, a.qs) ||
       !make_map_decay(&mK, a.k, a.dk, a.Hk, a.T, a.B, a.ks) ||
-      !make_map_decay(&mV, a.v, a.dv, a.Hv, a.T, a.B, a.vs))
+      !make_map_decay(&mV, a.v, a.dv, a.Hv, a.T, a.B, a.vs) ||
+      !make_map_decay(&mO, a.o, a.dv, a.H, a.T, a.B, os))
     return 2;
   static OncePerDevice attrs;
   if (!attrs.run([] {
@@ -652,12 +701,12 @@ int launch_tc_decay(const DecayArgs &a, void *workspace, cudaStream_t stream) {
   if (sp.S > 1) {
     cfg.cfg.gridDim = dim3((unsigned)(heads * (sp.S - 1)));
     if (cudaLaunchKernelEx(&cfg.cfg, a.dk > 64 ? tc_decay<true, 2> : tc_decay<true, 1>, mQ, mK, mV,
-                           a, sp, slots, 1) != cudaSuccess)
+                           mO, a, sp, slots, 1) != cudaSuccess)
       return 1;
   }
   cfg.cfg.gridDim = dim3((unsigned)(heads * sp.S));
   return cudaLaunchKernelEx(&cfg.cfg, a.dk > 64 ? tc_decay<false, 2> : tc_decay<false, 1>, mQ, mK,
-                            mV, a, sp, slots, sp.S > 1 ? 0 : 1) == cudaSuccess
+                            mV, mO, a, sp, slots, sp.S > 1 ? 0 : 1) == cudaSuccess
              ? 0
              : 1;
 }
