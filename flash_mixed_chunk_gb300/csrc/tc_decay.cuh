@@ -45,7 +45,7 @@ constexpr uint32_t DA_COL_SC = 0, DA_COL_O = 256, DA_COL_D = 384;  // two of Sc
 constexpr int DA_OUT_WARP = 4, DA_KEY_WARP = 12, DA_STATE_WARP = 16;
 // Registers of a thread: 80 at the launch of 768; the state's 64 places need more, the
 // first four warps and the keys' less.
-constexpr int DA_REG_ISSUE = 56, DA_REG_OUT = 80, DA_REG_KEYS = 56, DA_REG_STATE = 104;
+constexpr int DA_REG_ISSUE = 48, DA_REG_OUT = 80, DA_REG_KEYS = 64, DA_REG_STATE = 104;
 static_assert(128 * DA_REG_ISSUE + 256 * DA_REG_OUT + 128 * DA_REG_KEYS + 256 * DA_REG_STATE <=
                   80 * DA_THREADS,
               "tc_decay's warps would wait for registers that the block has not");
@@ -58,9 +58,16 @@ __host__ __device__ inline uint32_t da_state_bytes(int ka, int va) {
   return 8192u * (uint32_t)(ka * va);
 }
 __host__ __device__ inline uint32_t da_term_bytes(int ka) { return DA_ATOM * (uint32_t)ka; }
-__host__ __device__ inline int da_slots(int ka, int va) {
-  const int n = (int)((DA_SMEM - da_state_bytes(ka, va) - da_term_bytes(ka)) / da_slot(ka, va));
-  return n < DA_SLOTS ? n : DA_SLOTS;
+// The places of a ring each of q, k and v tiles (LOCAL: of k and v, and no state tile).
+// One ring of all three in turn would have k wait for the place that outputs leave last.
+struct DaRings {
+  int q, k, v;
+};
+__host__ __device__ inline DaRings da_rings(bool local, int ka, int va) {
+  const uint32_t room = DA_SMEM - da_term_bytes(ka) - (local ? 0 : da_state_bytes(ka, va));
+  int n = (int)(room / da_slot(ka, va));
+  n = n < DA_SLOTS ? n : DA_SLOTS;
+  return local ? DaRings{0, n / 2, n / 2} : DaRings{n / 3, (n + 1) / 3, (n + 2) / 3};
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -79,15 +86,13 @@ __device__ __forceinline__ bool da_wait(uint64_t *bar, int use) {
   return true;
 }
 
-// A place in the ring and how often it has been used before, kept step by step: a
-// division by the ring's length takes a role longer than its products.
+// A place in a ring and how often it has been used before, kept step by step: a division
+// by the ring's length takes a role longer than its products.
 struct RingAt {
-  int slot = 0, use = 0;
-  __device__ __forceinline__ RingAt ahead(int by, int n) const {  // by <= n
-    RingAt r = *this;
-    r.slot += by;
-    if (r.slot >= n) r.slot -= n, ++r.use;
-    return r;
+  int slot, use;
+  __device__ __forceinline__ explicit RingAt(int first) : slot(first), use(0) {}
+  __device__ __forceinline__ void step(int first, int n) {
+    if (++slot == first + n) slot = first, ++use;
   }
 };
 
@@ -151,9 +156,10 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   const int va = nv > 64 ? 2 : 1;
   const int va_all = a.dv > 64 ? 2 : 1;  // the ring's, of every unit
   const uint32_t slot_bytes = da_slot(ka, va_all);
-  const int n_slots = da_slots(ka, va_all);
-  uint8_t *const s_tile = smem + n_slots * slot_bytes;
-  uint8_t *const terms = s_tile + da_state_bytes(ka, va_all);
+  const DaRings rings = da_rings(LOCAL, ka, va_all);
+  const int k0 = rings.q, v0s = rings.q + rings.k, n_slots = v0s + rings.v;  // first places
+  uint8_t *const terms = smem + n_slots * slot_bytes;
+  uint8_t *const s_tile = terms + da_term_bytes(ka);
   const double rate = decay_rate(a.log_decay[w.h]);
   const int end = w.t1 < w.len ? w.t1 : w.len;
   // (LOCAL: a segment that nothing comes behind is nobody's start)
@@ -164,7 +170,6 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     const int n = end - w.t0 - 128 * g;
     return n < 128 ? n : 128;
   };
-  constexpr int PER = LOCAL ? 2 : 3;  // ring items of a chunk: (Q,) K, V
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < n_slots; ++i) {
@@ -221,27 +226,36 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       tma_prefetch_desc(&mapK);
       tma_prefetch_desc(&mapV);
       const int hq = w.h / (a.H / a.Hq), hk = w.h / (a.H / a.Hk), hv = w.h / (a.H / a.Hv);
-      RingAt at;
+      RingAt rq(0), rk(k0), rv(v0s);
       bool ok = true;
+      const auto load = [&](RingAt &r, int from, int n, const CUtensorMap *map, int atoms, int x0,
+                            int head, int t) {
+        if (!ok) return;
+        if (r.use > 0 && !da_wait(&empty[r.slot], r.use - 1)) {
+          record_timeout(1101);
+          ok = false;
+          return;
+        }
+        mbar_arrive_expect_tx(&full[r.slot], DA_ATOM * (uint32_t)atoms);
+        for (int x = 0; x < atoms; ++x)
+          tma_load_4d(smem + r.slot * slot_bytes + x * DA_ATOM, map, &full[r.slot], x0 + 64 * x, head,
+                      t, w.b);
+        r.step(from, n);
+      };
+#pragma unroll 1
       for (int g = 0; ok && g < chunks; ++g) {
         const int t = w.t0 + 128 * g;
-        for (int i = 3 - PER; i < 3; ++i, at = at.ahead(1, n_slots)) {
-          if (at.use > 0 && !da_wait(&empty[at.slot], at.use - 1)) {
-            record_timeout(1101);
-            ok = false;
-            break;
-          }
-          const int atoms = i == 2 ? va : ka;
-          mbar_arrive_expect_tx(&full[at.slot], DA_ATOM * (uint32_t)atoms);
-          for (int x = 0; x < atoms; ++x)
-            tma_load_4d(smem + at.slot * slot_bytes + x * DA_ATOM,
-                        i == 0 ? &mapQ : i == 1 ? &mapK : &mapV, &full[at.slot],
-                        (i == 2 ? v0 : 0) + 64 * x, i == 0 ? hq : i == 1 ? hk : hv, t, w.b);
-        }
+        load(rk, k0, rings.k, &mapK, ka, 0, hk, t);
+        // q's place is free late and its scores are due soon: from L2
+        if (!LOCAL && g + 1 < chunks)
+          for (int x = 0; x < ka; ++x) tma_prefetch_l2_4d(&mapQ, 64 * x, hq, t + 128, w.b);
+        if (!LOCAL) load(rq, 0, rings.q, &mapQ, ka, 0, hq, t);
+        load(rv, v0s, rings.v, &mapV, va, v0, hv, t);
       }
-      // the last copy issued into each slot has landed
+      // the last copy issued into each place has landed
       for (int i = 0; i < n_slots; ++i) {
-        const int uses = at.use + (i < at.slot ? 1 : 0);
+        const RingAt &r = i < k0 ? rq : i < v0s ? rk : rv;
+        const int uses = r.use + (i < r.slot ? 1 : 0);
         if (uses > 0 && !da_wait(&full[i], uses - 1)) record_timeout(1102);
       }
     }
@@ -264,8 +278,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       };
       // The scores of chunk g, into the buffer whose weights the products of chunk g - 2
       // have read (o_free of that chunk, waited for ahead of Q S of chunk g - 1).
-      const auto scores = [&](int g, const RingAt &rq) {
-        const RingAt rk = rq.ahead(1, n_slots);
+      RingAt rq(0), rk(k0), rv(v0s);  // of the next scores' q and k, and the chunk's v
+      const auto scores = [&](int g) {
         if (!got(&full[rq.slot], rq.use, 1110) || !got(&full[rk.slot], rk.use, 1111)) return false;
         tc_fence_after();
         uint64_t q = smem_desc_sw128(slot_of(rq), 0, 1024);
@@ -280,21 +294,22 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           }
           mma_commit(&sc_full[g & 1]);
         }
+        rq.step(0, rings.q);
+        rk.step(k0, rings.k);
         return true;
       };
       int xn = 0;
-      RingAt r0;  // the chunk's first item
-      bool ok = LOCAL || chunks == 0 || scores(0, r0);
+      RingAt cq(0), ck(k0);  // of the chunk's q and k
+      bool ok = LOCAL || chunks == 0 || scores(0);
       for (int g = 0; ok && g < chunks; ++g) {
         const int n = tokens(g);
-        const RingAt rk = r0.ahead(PER - 2, n_slots), rv = r0.ahead(PER - 1, n_slots);
-        const uint64_t kd = smem_desc_sw128(slot_of(rk), lbo_k, 1024);
+        const uint64_t kd = smem_desc_sw128(slot_of(ck), lbo_k, 1024);
         const uint64_t vd = smem_desc_sw128(slot_of(rv), DA_ATOM, 1024);
         if (!got(&s_ready, g, 1113)) break;
         if (!LOCAL) {
           if (g > 0 && !got(&o_free, g - 1, 1114)) break;
           tc_fence_after();
-          uint64_t qd = smem_desc_sw128(slot_of(r0), 0, 1024), sd = s_desc;
+          uint64_t qd = smem_desc_sw128(slot_of(cq), 0, 1024), sd = s_desc;
           if (lead) {
 #pragma unroll
             for (int x = 0; x < ka; ++x, qd += DA_ATOM / 16, sd += 8192 / 16) {
@@ -303,17 +318,13 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                 mma_bf16_ss(tbase + DA_COL_O, qd + 2u * i, sd + 128u * i, id_o, (x | i) > 0);
             }
             mma_commit(&qs_full);
-            mma_commit(&empty[r0.slot]);
+            mma_commit(&empty[cq.slot]);
           }
         }
         if (!got(&full[rv.slot], rv.use, 1115)) break;
-        const RingAt next = r0.ahead(PER, n_slots);
 #pragma unroll 1
         for (int qt = 0; qt < (n + 31) / 32; ++qt, ++xn) {
-          // the next chunk's scores ahead of half of these products: its keys' terms and
-          // its weights can be on their way
-          if (!LOCAL && qt == 2 && g + 1 < chunks && !scores(g + 1, next)) ok = false;
-          if (!ok || !got(&x_ready[xn & 1], xn >> 1, 1116)) {
+          if (!got(&x_ready[xn & 1], xn >> 1, 1116)) {
             ok = false;
             break;
           }
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         if (!ok) break;
         if (lead) {
           mma_commit(&d_full);
-          mma_commit(&empty[rk.slot]);
+          mma_commit(&empty[ck.slot]);
         }
         if (!LOCAL) {
           if (!got(&p_ready, g, 1117)) break;
@@ -351,16 +362,19 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           }
         }
         if (LOCAL && lead) mma_commit(&empty[rv.slot]);
-        r0 = next;
+        if (!LOCAL) cq.step(0, rings.q);
+        ck.step(k0, rings.k);
+        rv.step(v0s, rings.v);
+        if (!LOCAL && g + 1 < chunks) ok = scores(g + 1);
       }
       if (lead) mma_commit(&mma_done);
       got(&mma_done, 0, 1118);
     }
     if (!LOCAL && warp == 2 && lane == 0) {
       // =========================== output stores
-      RingAt rv = RingAt{}.ahead(PER - 1, n_slots);
+      RingAt rv(v0s);
       bool ok = true;
-      for (int g = 0; ok && g < chunks; ++g, rv = rv.ahead(PER, n_slots)) {
+      for (int g = 0; ok && g < chunks; ++g, rv.step(v0s, rings.v)) {
         if (!da_wait(&staged[g & 1], g >> 1)) {
           record_timeout(1150);
           ok = false;
@@ -381,8 +395,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     const int quad = warp & 3, half = (warp - DA_OUT_WARP) >> 2, row = quad * 32 + lane;
     const float ahead = a.scale * power[row + 1], rate_f = (float)rate;
     const uint32_t ocol = tbase + lane_off + DA_COL_O + 64u * (uint32_t)half;
-    RingAt rv = RingAt{}.ahead(PER - 1, n_slots);
-    for (int g = 0; !LOCAL && g < chunks; ++g, rv = rv.ahead(PER, n_slots)) {
+    RingAt rv(v0s);
+    for (int g = 0; !LOCAL && g < chunks; ++g, rv.step(v0s, rings.v)) {
       wait(&sc_full[g & 1], g >> 1, 1120);
       __syncwarp();
       tc_fence_after();
@@ -456,17 +470,17 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         uint8_t *const out = smem + rv.slot * slot_bytes + (uint32_t)half * DA_ATOM;
         __syncwarp();
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 16) {
-          uint32_t r[16];
-          tmem_ld16(ocol + (uint32_t)c, r);
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(ocol + (uint32_t)c, r);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 16; ++j) {
             const uint32_t x = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
             r[j] = in ? x : 0u;
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4 *>(out + sw128_offset((uint32_t)row, 2u * c + 16u * j)) =
                 make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
         }
@@ -485,15 +499,14 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     const int kt = (int)threadIdx.x - 32 * DA_KEY_WARP;
     const int r = kt >> 3, p16 = (kt & 7) * 16;  // of 16 tokens, of a row's 128 bytes
     int xn = 0;
-    RingAt rk = RingAt{}.ahead(PER - 2, n_slots);
-    for (int g = 0; g < chunks; ++g, rk = rk.ahead(PER, n_slots)) {
+    RingAt rk(k0), rv(v0s);
+    for (int g = 0; g < chunks; ++g, rk.step(k0, rings.k), rv.step(v0s, rings.v)) {
       const int n = tokens(g);
       // the first term replaces K, which Sc has read by then
       if (!LOCAL) wait(&sc_full[g & 1], g >> 1, 1140);
       wait(&full[rk.slot], rk.use, 1141);
       uint8_t *const k = smem + rk.slot * slot_bytes;
       if (n < 128) {  // rows behind the end are zeros, whatever they hold
-        const RingAt rv = rk.ahead(1, n_slots);
         wait(&full[rv.slot], rv.use, 1142);
         uint8_t *const v = smem + rv.slot * slot_bytes;
         for (int i = kt; i < (128 - n) * 8; i += 128)
