@@ -25,7 +25,7 @@
 // launch (LOCAL) forms only the segments' states, a second starts every segment from
 // the sum of those before it.
 //
-// Warps (768 threads): 0 TMA, 1 MMA issuer, 2 output stores; 4-11 P and the outputs; 12-15
+// Warps (768 threads): 0 TMA, 1 and 3 MMA issuers, 2 output stores; 4-11 P and the outputs; 12-15
 // K~'s terms, from K in place (the first term) and through two buffers of 32 tokens (the
 // others); 16-23 the state, from D in TMEM, and its bf16 copy in shared memory.  P takes
 // the columns of the scores that its own warp has read, of one of two buffers.
@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ __align__(8) uint64_t full[DA_SLOTS], empty[DA_SLOTS], x_ready[2], x_free[2];
   __shared__ __align__(8) uint64_t staged[2], stored[2];
-  __shared__ __align__(8) uint64_t sc_full[2], qs_full, p_ready, o_full, o_free, s_ready, d_full,
-      mma_done;
+  __shared__ __align__(8) uint64_t sc_full[2], qs_full, p_ready, o_full, o_free, s_ready, d_full[2],
+      d_free, v_ready, mma_done[2];
   __shared__ __align__(16) float back[16];  // lam^(15 - j)
   __shared__ float power[129];              // lam^j
   __shared__ uint32_t tmem_base;
@@ -189,8 +189,12 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     mbar_init(&o_full, 1);
     mbar_init(&o_free, 8);
     mbar_init(&s_ready, 8);
-    mbar_init(&d_full, 1);
-    mbar_init(&mma_done, 1);
+    mbar_init(&d_full[0], 1);
+    mbar_init(&d_full[1], 1);
+    mbar_init(&v_ready, 4);
+    mbar_init(&d_free, 8);
+    mbar_init(&mma_done[0], 1);
+    mbar_init(&mma_done[1], 1);
     fence_mbar_init();
   }
   if (threadIdx.x >= 64 && threadIdx.x < 64 + 129) {
@@ -228,29 +232,32 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       const int hq = w.h / (a.H / a.Hq), hk = w.h / (a.H / a.Hk), hv = w.h / (a.H / a.Hv);
       RingAt rq(0), rk(k0), rv(v0s);
       bool ok = true;
-      const auto load = [&](RingAt &r, int from, int n, const CUtensorMap *map, int atoms, int x0,
-                            int head, int t) {
-        if (!ok) return;
-        if (r.use > 0 && !da_wait(&empty[r.slot], r.use - 1)) {
-          record_timeout(1101);
-          ok = false;
-          return;
-        }
-        mbar_arrive_expect_tx(&full[r.slot], DA_ATOM * (uint32_t)atoms);
-        for (int x = 0; x < atoms; ++x)
-          tma_load_4d(smem + r.slot * slot_bytes + x * DA_ATOM, map, &full[r.slot], x0 + 64 * x, head,
-                      t, w.b);
-        r.step(from, n);
-      };
 #pragma unroll 1
       for (int g = 0; ok && g < chunks; ++g) {
         const int t = w.t0 + 128 * g;
-        load(rk, k0, rings.k, &mapK, ka, 0, hk, t);
-        // q's place is free late and its scores are due soon: from L2
-        if (!LOCAL && g + 1 < chunks)
-          for (int x = 0; x < ka; ++x) tma_prefetch_l2_4d(&mapQ, 64 * x, hq, t + 128, w.b);
-        if (!LOCAL) load(rq, 0, rings.q, &mapQ, ka, 0, hq, t);
-        load(rv, v0s, rings.v, &mapV, va, v0, hv, t);
+#pragma unroll 1
+        for (int i = 0; ok && i < (LOCAL ? 2 : 3); ++i) {  // k, (q,) v
+          const bool isk = i == 0, isv = i == (LOCAL ? 1 : 2), isq = !isk && !isv;
+          RingAt r = isv ? rv : isq ? rq : rk;
+          if (r.use > 0 && !da_wait(&empty[r.slot], r.use - 1)) {
+            record_timeout(1101);
+            ok = false;
+            break;
+          }
+          const int atoms = isv ? va : ka;
+          mbar_arrive_expect_tx(&full[r.slot], DA_ATOM * (uint32_t)atoms);
+#pragma unroll 1
+          for (int x = 0; x < atoms; ++x)
+            tma_load_4d(smem + r.slot * slot_bytes + x * DA_ATOM, isv ? &mapV : isq ? &mapQ : &mapK,
+                        &full[r.slot], (isv ? v0 : 0) + 64 * x, isv ? hv : isq ? hq : hk, t, w.b);
+          r.step(isv ? v0s : isq ? 0 : k0, isv ? rings.v : isq ? rings.q : rings.k);
+          if (isv)
+            rv = r;
+          else if (isk)
+            rk = r;
+          else
+            rq = r;
+        }
       }
       // the last copy issued into each place has landed
       for (int i = 0; i < n_slots; ++i) {
@@ -259,116 +266,121 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         if (uses > 0 && !da_wait(&full[i], uses - 1)) record_timeout(1102);
       }
     }
-    if (warp == 1) {
-      // =========================== MMA issuer: all lanes go through, one issues
+    // Two warps issue products, the state's (1) and the outputs' (3): either's waits are the
+    // other's time.  All of a warp's lanes go through, one issues.
+    if (warp == 1 || (!LOCAL && warp == 3)) {
       const bool lead = elect_one();
       const uint32_t nvc = 64u * (uint32_t)va;
-      const uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
-      const uint32_t id_o = idesc_bf16_f32(128, nvc, false, true);
-      const uint32_t id_d = idesc_bf16_f32(128, nvc, true, true);
       // descriptors: 16-byte steps in their low bits
-      const uint32_t lbo_k = ka == 2 ? DA_ATOM : 0;
-      const uint64_t x_desc = smem_desc_sw128(smem_u32(terms), ka == 2 ? 4096 : 0, 1024);
-      const uint64_t s_desc = smem_desc_sw128(smem_u32(s_tile), 8192u * (uint32_t)ka, 1024);
       const auto slot_of = [&](const RingAt &r) { return smem_u32(smem + r.slot * slot_bytes); };
       const auto got = [&](uint64_t *bar, int use, int code) {
         if (__all_sync(0xFFFFFFFFu, da_wait(bar, use))) return true;
         if (lead) record_timeout(code);
         return false;
       };
-      // The scores of chunk g, into the buffer whose weights the products of chunk g - 2
-      // have read (o_free of that chunk, waited for ahead of Q S of chunk g - 1).
-      RingAt rq(0), rk(k0), rv(v0s);  // of the next scores' q and k, and the chunk's v
-      const auto scores = [&](int g) {
-        if (!got(&full[rq.slot], rq.use, 1110) || !got(&full[rk.slot], rk.use, 1111)) return false;
-        tc_fence_after();
-        uint64_t q = smem_desc_sw128(slot_of(rq), 0, 1024);
-        uint64_t k = smem_desc_sw128(slot_of(rk), 0, 1024);
-        const uint32_t sc = tbase + DA_COL_SC + 128u * (uint32_t)(g & 1);
-        if (lead) {
-#pragma unroll
-          for (int x = 0; x < ka; ++x, q += DA_ATOM / 16, k += DA_ATOM / 16) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)  // 16 of dk: 32 bytes of the rows
-              mma_bf16_ss(sc, q + 2u * i, k + 2u * i, id_sc, (x | i) > 0);
-          }
-          mma_commit(&sc_full[g & 1]);
-        }
-        rq.step(0, rings.q);
-        rk.step(k0, rings.k);
-        return true;
-      };
-      int xn = 0;
-      RingAt cq(0), ck(k0);  // of the chunk's q and k
-      bool ok = LOCAL || chunks == 0 || scores(0);
-      for (int g = 0; ok && g < chunks; ++g) {
-        const int n = tokens(g);
-        const uint64_t kd = smem_desc_sw128(slot_of(ck), lbo_k, 1024);
-        const uint64_t vd = smem_desc_sw128(slot_of(rv), DA_ATOM, 1024);
-        if (!got(&s_ready, g, 1113)) break;
-        if (!LOCAL) {
-          if (g > 0 && !got(&o_free, g - 1, 1114)) break;
-          tc_fence_after();
-          uint64_t qd = smem_desc_sw128(slot_of(cq), 0, 1024), sd = s_desc;
-          if (lead) {
-#pragma unroll
-            for (int x = 0; x < ka; ++x, qd += DA_ATOM / 16, sd += 8192 / 16) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)  // 16 rows of the state
-                mma_bf16_ss(tbase + DA_COL_O, qd + 2u * i, sd + 128u * i, id_o, (x | i) > 0);
-            }
-            mma_commit(&qs_full);
-            mma_commit(&empty[cq.slot]);
-          }
-        }
-        if (!got(&full[rv.slot], rv.use, 1115)) break;
+      bool ok = true;
+      if (warp == 1) {
+        // =========================== D = K~^T V
+        const uint32_t id_d = idesc_bf16_f32(128, nvc, true, true);
+        const uint32_t lbo_k = ka == 2 ? DA_ATOM : 0;
+        const uint64_t x_desc = smem_desc_sw128(smem_u32(terms), ka == 2 ? 4096 : 0, 1024);
+        RingAt rk(k0), rv(v0s);
+        int xn = 0;
+        for (int g = 0; ok && g < chunks; ++g, rk.step(k0, rings.k), rv.step(v0s, rings.v)) {
+          const int n = tokens(g);
+          const uint64_t kd = smem_desc_sw128(slot_of(rk), lbo_k, 1024);
+          const uint64_t vd = smem_desc_sw128(slot_of(rv), DA_ATOM, 1024);
+          if ((g > 0 && !got(&d_free, g - 1, 1119)) || !got(&full[rv.slot], rv.use, 1115)) break;
 #pragma unroll 1
-        for (int qt = 0; qt < (n + 31) / 32; ++qt, ++xn) {
-          if (!got(&x_ready[xn & 1], xn >> 1, 1116)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t x1 = x_desc + (uint32_t)(xn & 1) * (uint32_t)ka * (2 * 4096 / 16);
-          const uint64_t x2 = x1 + (uint32_t)ka * (4096 / 16);
-          const uint64_t k1 = kd + (uint32_t)qt * (4096 / 16), v1 = vd + (uint32_t)qt * (4096 / 16);
-          if (lead) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {  // 16 tokens
-              mma_bf16_ss(tbase + DA_COL_D, x2 + 128u * i, v1 + 128u * i, id_d, (qt | i) > 0);
-              mma_bf16_ss(tbase + DA_COL_D, x1 + 128u * i, v1 + 128u * i, id_d, 1);
-              mma_bf16_ss(tbase + DA_COL_D, k1 + 128u * i, v1 + 128u * i, id_d, 1);
+          for (int qt = 0; 32 * qt < n; ++qt, ++xn) {
+            if (!got(&x_ready[xn & 1], xn >> 1, 1116)) {
+              ok = false;
+              break;
             }
-            mma_commit(&x_free[xn & 1]);
+            tc_fence_after();
+            const uint64_t x1 = x_desc + (uint32_t)(xn & 1) * (uint32_t)ka * (2 * 4096 / 16);
+            const uint64_t x2 = x1 + (uint32_t)ka * (4096 / 16);
+            const uint64_t k1 = kd + (uint32_t)qt * (4096 / 16);
+            const uint64_t v1 = vd + (uint32_t)qt * (4096 / 16);
+            if (lead) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {  // 16 tokens
+                mma_bf16_ss(tbase + DA_COL_D, x2 + 128u * i, v1 + 128u * i, id_d, (qt | i) > 0);
+                mma_bf16_ss(tbase + DA_COL_D, x1 + 128u * i, v1 + 128u * i, id_d, 1);
+                mma_bf16_ss(tbase + DA_COL_D, k1 + 128u * i, v1 + 128u * i, id_d, 1);
+              }
+              mma_commit(&x_free[xn & 1]);
+            }
+          }
+          if (ok && lead) {
+            mma_commit(&d_full[g & 1]);
+            mma_commit(&empty[rk.slot]);
+            if (LOCAL) mma_commit(&empty[rv.slot]);
           }
         }
-        if (!ok) break;
-        if (lead) {
-          mma_commit(&d_full);
-          mma_commit(&empty[ck.slot]);
-        }
-        if (!LOCAL) {
-          if (!got(&p_ready, g, 1117)) break;
+        if (lead) mma_commit(&mma_done[0]);
+        got(&mma_done[0], 0, 1118);
+      } else {
+        // =========================== Sc, Q S and P V
+        const uint32_t id_sc = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t id_o = idesc_bf16_f32(128, nvc, false, true);
+        const uint64_t s_desc = smem_desc_sw128(smem_u32(s_tile), 8192u * (uint32_t)ka, 1024);
+        RingAt rq(0), rk(k0), rv(v0s);  // of the next scores, and the chunk's v
+        RingAt cq(0);                   // of the chunk's q
+        for (int g = -1; ok && g < chunks; ++g) {
+          if (g >= 0) {
+            if (!got(&s_ready, g, 1113) || (g > 0 && !got(&o_free, g - 1, 1114))) break;
+            tc_fence_after();
+            uint64_t qd = smem_desc_sw128(slot_of(cq), 0, 1024), sd = s_desc;
+            if (lead) {
+#pragma unroll
+              for (int x = 0; x < ka; ++x, qd += DA_ATOM / 16, sd += 8192 / 16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)  // 16 rows of the state
+                  mma_bf16_ss(tbase + DA_COL_O, qd + 2u * i, sd + 128u * i, id_o, (x | i) > 0);
+              }
+              mma_commit(&qs_full);
+              mma_commit(&empty[cq.slot]);
+            }
+            cq.step(0, rings.q);
+            if (!got(&p_ready, g, 1117) || !got(&v_ready, g, 1112)) break;
+            tc_fence_after();
+            const uint32_t pc = tbase + DA_COL_SC + 128u * (uint32_t)(g & 1);
+            const uint64_t vd = smem_desc_sw128(slot_of(rv), DA_ATOM, 1024);
+            const int steps = (tokens(g) + 15) / 16;
+            if (lead) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (i < steps)
+                  mma_bf16_ts(tbase + DA_COL_O, pc + (uint32_t)(i / 4) * 64 + (uint32_t)(i % 4) * 8,
+                              vd + 128u * i, id_o, 1);
+              mma_commit(&o_full);
+            }
+            rv.step(v0s, rings.v);
+          }
+          if (g + 1 == chunks) break;
+          // the next scores, into the buffer whose weights the products of chunk g - 1 have
+          // read (o_free of that chunk)
+          if (!got(&full[rq.slot], rq.use, 1110) || !got(&full[rk.slot], rk.use, 1111)) break;
           tc_fence_after();
-          const uint32_t pc = tbase + DA_COL_SC + 128u * (uint32_t)(g & 1);
-          const int steps = (n + 15) / 16;
+          uint64_t q = smem_desc_sw128(slot_of(rq), 0, 1024);
+          uint64_t k = smem_desc_sw128(slot_of(rk), 0, 1024);
+          const uint32_t sc = tbase + DA_COL_SC + 128u * (uint32_t)((g + 1) & 1);
           if (lead) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < steps)
-                mma_bf16_ts(tbase + DA_COL_O, pc + (uint32_t)(i / 4) * 64 + (uint32_t)(i % 4) * 8,
-                            vd + 128u * i, id_o, 1);
-            mma_commit(&o_full);
+            for (int x = 0; x < ka; ++x, q += DA_ATOM / 16, k += DA_ATOM / 16) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)  // 16 of dk: 32 bytes of the rows
+                mma_bf16_ss(sc, q + 2u * i, k + 2u * i, id_sc, (x | i) > 0);
+            }
+            mma_commit(&sc_full[(g + 1) & 1]);
           }
+          rq.step(0, rings.q);
+          rk.step(k0, rings.k);
         }
-        if (LOCAL && lead) mma_commit(&empty[rv.slot]);
-        if (!LOCAL) cq.step(0, rings.q);
-        ck.step(k0, rings.k);
-        rv.step(v0s, rings.v);
-        if (!LOCAL && g + 1 < chunks) ok = scores(g + 1);
+        if (lead) mma_commit(&mma_done[1]);
+        got(&mma_done[1], 0, 1118);
       }
-      if (lead) mma_commit(&mma_done);
-      got(&mma_done, 0, 1118);
     }
     if (!LOCAL && warp == 2 && lane == 0) {
       // =========================== output stores
@@ -461,6 +473,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       wait(&o_full, g, 1130);
       __syncwarp();
       tc_fence_after();
+      wait(&d_full[g & 1], g >> 1, 1132);  // D has read v too
       if (g > 1) wait(&stored[g & 1], (g >> 1) - 1, 1131);
       // Through v's place in the ring, which its products have left, and out by TMA: 32-byte
       // stores from the registers hold the SM's other shared memory traffic up for 1800 of
@@ -506,14 +519,17 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       if (!LOCAL) wait(&sc_full[g & 1], g >> 1, 1140);
       wait(&full[rk.slot], rk.use, 1141);
       uint8_t *const k = smem + rk.slot * slot_bytes;
+      if (!LOCAL || n < 128) wait(&full[rv.slot], rv.use, 1142);
       if (n < 128) {  // rows behind the end are zeros, whatever they hold
-        wait(&full[rv.slot], rv.use, 1142);
         uint8_t *const v = smem + rv.slot * slot_bytes;
         for (int i = kt; i < (128 - n) * 8; i += 128)
           for (int x = 0; x < va; ++x)
             *reinterpret_cast<uint4 *>(v + x * DA_ATOM + n * 128 + i * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
       }
+      __syncwarp();
+      if (!LOCAL && lane == 0) mbar_arrive(&v_ready);
 #pragma unroll 1
       for (int qt = 0; qt < (n + 31) / 32; ++qt, ++xn) {
         if (xn > 1) wait(&x_free[xn & 1], (xn >> 1) - 1, 1143);
@@ -593,10 +609,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       }
     }
     const float2 whole = decay_power2(rate, 128);
-    // D's columns have been read, and (LOCAL: not) the operand of the next chunk's Q S is
-    // there
-    const auto publish = [&]() {
-      if (!LOCAL && row < 64 * ka && half < va) {
+    const auto publish = [&]() {  // the operand of the next chunk's Q S
+      if (row < 64 * ka && half < va) {
         uint8_t *p = s_tile + (uint32_t)(half * ka) * 8192u;
 #pragma unroll
         for (int j = 0; j < 64; j += 8)
@@ -605,14 +619,13 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                          pack_bf16x2(S[j + 4], S[j + 5]), pack_bf16x2(S[j + 6], S[j + 7]));
       }
       fence_proxy_async_smem();
-      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_ready);
     };
-    if (chunks > 0) publish();
+    if (!LOCAL && chunks > 0) publish();
     for (int g = 0; g < chunks; ++g) {
       const int n = tokens(g);
-      wait(&d_full, g, 1144);
+      wait(&d_full[g & 1], g >> 1, 1144);
       __syncwarp();
       tc_fence_after();
       const float2 f = n == 128 ? whole : make_float2(power[n], 0.f);
@@ -635,7 +648,14 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           }
         }
       }
-      if (g + 1 < chunks) publish();
+      tc_fence_before();  // the next chunk's products may take D's columns
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_free);
+      if (!LOCAL && g + 1 < chunks) {
+        wait(&qs_full, g, 1145);  // Q S has read the tile
+        __syncwarp();
+        publish();
+      }
     }
     if (LOCAL) {
       if (chunks > 0) {
@@ -658,9 +678,11 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     const int per = nv / 8;
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) +
                        (((size_t)w.b * a.T + z0) * a.H + w.h) * (size_t)a.dv + v0;
-    for (int64_t i = threadIdx.x; i < (int64_t)(w.t1 - z0) * per; i += DA_THREADS)
-      *reinterpret_cast<uint4 *>(o + (size_t)(i / per) * a.H * a.dv + (i % per) * 8) =
-          make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+    for (int r = warp; r < w.t1 - z0; r += DA_THREADS / 32)
+#pragma unroll 1
+      for (int i = lane; i < per; i += 32)
+        *reinterpret_cast<uint4 *>(o + (size_t)r * a.H * a.dv + i * 8) = make_uint4(0u, 0u, 0u, 0u);
   }
   // the single-lane roles rejoin their warps before the block-wide barrier
   __syncwarp();
