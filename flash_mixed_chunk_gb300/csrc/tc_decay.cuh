@@ -402,13 +402,13 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       }
       bulk_wait_group<0>();
     }
-  } else if (warp < DA_KEY_WARP) {
+  } else if (!LOCAL && warp < DA_KEY_WARP) {
     // =========================== P and the outputs: a row and 64 columns a thread
     const int quad = warp & 3, half = (warp - DA_OUT_WARP) >> 2, row = quad * 32 + lane;
     const float ahead = a.scale * power[row + 1], rate_f = (float)rate;
     const uint32_t ocol = tbase + lane_off + DA_COL_O + 64u * (uint32_t)half;
     RingAt rv(v0s);
-    for (int g = 0; !LOCAL && g < chunks; ++g, rv.step(v0s, rings.v)) {
+    for (int g = 0; g < chunks; ++g, rv.step(v0s, rings.v)) {
       wait(&sc_full[g & 1], g >> 1, 1120);
       __syncwarp();
       tc_fence_after();
@@ -507,13 +507,16 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       }
     }
   } else if (warp < DA_STATE_WARP) {
-    // =========================== the keys' terms, 32 tokens at a time
+    // =========================== the keys' terms, 32 tokens at a time by four warps
+    // (LOCAL: the warps that have no outputs are four more; they take turns)
     regs_dec<DA_REG_KEYS>();
-    const int kt = (int)threadIdx.x - 32 * DA_KEY_WARP;
+    constexpr int GROUPS = LOCAL ? 2 : 1;
+    const int kt = (int)threadIdx.x & 127, group = LOCAL ? (DA_STATE_WARP - 1 - warp) >> 2 : 0;
     const int r = kt >> 3, p16 = (kt & 7) * 16;  // of 16 tokens, of a row's 128 bytes
-    int xn = 0;
+    int xn = 0;  // uses of the buffer ahead (of both, by one group)
     RingAt rk(k0), rv(v0s);
-    for (int g = 0; g < chunks; ++g, rk.step(k0, rings.k), rv.step(v0s, rings.v)) {
+    for (int g = group < GROUPS ? 0 : chunks; g < chunks;
+         ++g, rk.step(k0, rings.k), rv.step(v0s, rings.v)) {
       const int n = tokens(g);
       // the first term replaces K, which Sc has read by then
       if (!LOCAL) wait(&sc_full[g & 1], g >> 1, 1140);
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       if (!LOCAL || n < 128) wait(&full[rv.slot], rv.use, 1142);
       if (n < 128) {  // rows behind the end are zeros, whatever they hold
         uint8_t *const v = smem + rv.slot * slot_bytes;
-        for (int i = kt; i < (128 - n) * 8; i += 128)
+        for (int i = kt; group == 0 && i < (128 - n) * 8; i += 128)
           for (int x = 0; x < va; ++x)
             *reinterpret_cast<uint4 *>(v + x * DA_ATOM + n * 128 + i * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
@@ -531,9 +534,10 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       __syncwarp();
       if (!LOCAL && lane == 0) mbar_arrive(&v_ready);
 #pragma unroll 1
-      for (int qt = 0; qt < (n + 31) / 32; ++qt, ++xn) {
-        if (xn > 1) wait(&x_free[xn & 1], (xn >> 1) - 1, 1143);
-        uint8_t *const x = terms + (uint32_t)(xn & 1) * 2 * (uint32_t)ka * 4096 + r * 128 + p16;
+      for (int qt = group; 32 * qt < n; qt += GROUPS, ++xn) {
+        const int buf = LOCAL ? group : xn & 1, use = LOCAL ? xn : xn >> 1;
+        if (use > 0) wait(&x_free[buf], use - 1, 1143);
+        uint8_t *const x = terms + (uint32_t)buf * 2 * (uint32_t)ka * 4096 + r * 128 + p16;
         uint8_t *const kp = k + (qt * 32 + r) * 128 + p16;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {  // 16 tokens
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&x_ready[xn & 1]);
+        if (lane == 0) mbar_arrive(&x_ready[buf]);
       }
     }
   } else {
