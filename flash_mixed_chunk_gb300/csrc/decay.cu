@@ -67,9 +67,10 @@ __global__ void __launch_bounds__(kThreads)
   const int v0 = w.vt * DVT, nv = a.dv - v0 < DVT ? a.dv - v0 : DVT;
   const size_t slot = (size_t)dk * DVT;
   float *own = slots + (((size_t)w.b * a.H + w.h) * sp.nvt + w.vt) * sp.S * slot;
-  const double rate = decay_rate(a.log_decay[w.h]);
+  const DecayRate rate = decay_rate(a.log_decay[w.h]);
   if (tid <= C) pw[tid] = decay_power(rate, tid);
-  const float2 whole = decay_power2(rate, C);
+  __shared__ float2 whole;
+  if (tid == 64) whole = decay_power2(rate, C);  // (read behind the first chunk's barriers)
 
   // the state at the segment's start
   const size_t at = ((size_t)w.b * a.H + w.h) * dk * (size_t)a.dv + v0;

@@ -11,23 +11,37 @@
 namespace fmca {
 namespace {
 
-// log2 of a head's decay.  Held in 64 bits: the exponent of a far position is a
-// product with up to 2^31.  A log decay of -inf (nothing is kept) becomes one whose
-// first power is 0 already, so that the power 0 is 1 and not a NaN.
-__device__ __forceinline__ double decay_rate(float log_decay) {
-  return (double)(log_decay < -1e6f ? -1e6f : log_decay) * 1.4426950408889634074;
+// log2 of a head's decay, as a sum of two floats: the exponent of a far position is a
+// product with up to 2^31.  (64-bit arithmetic, whose pipe is a trickle here, costs a
+// block whose warps all form powers microseconds.)  A log decay of -inf (nothing is kept)
+// becomes one whose first power is 0 already, so that the power 0 is 1 and not a NaN.
+struct DecayRate {
+  float hi, lo;
+};
+__device__ __forceinline__ DecayRate decay_rate(float log_decay) {
+  const float x = log_decay < -1e6f ? -1e6f : log_decay;
+  constexpr float kHi = 1.44269502162933349609f, kLo = 1.92596299112661746887e-8f;  // log2(e)
+  DecayRate r;
+  r.hi = x * kHi;
+  r.lo = fmaf(x, kLo, fmaf(x, kHi, -r.hi));
+  if (isinf(r.hi)) r.lo = 0.f;
+  return r;
 }
-// 2^(rate n) in 32 bits: the exponent's rounding goes back in as a factor.
-__device__ __forceinline__ float decay_power(double rate, int64_t n) {
-  const double e = rate * (double)n;
-  const float hi = (float)e;
-  const float p = exp2f(hi);
-  return isinf(hi) ? p : p + p * ((float)(e - (double)hi) * 0.693147180559945f);
+// 2^(rate n), n >= 0: the exponent's rounding goes back in as a factor.
+__device__ __forceinline__ float decay_power(const DecayRate &r, int n) {
+  const float a = (float)(n & ~4095), b = (float)(n & 4095);  // exactly
+  const float pa = a * r.hi, pb = b * r.hi;
+  const float e = pa + pb, back = e - pa;
+  const float rest = (pa - (e - back)) + (pb - back) + fmaf(a, r.hi, -pa) + fmaf(b, r.hi, -pb) +
+                     (float)n * r.lo;
+  const float p = exp2f(e);
+  return isinf(e) ? p : fmaf(p, rest * 0.693147180559945f, p);
 }
 // The same as a sum of two floats: a state is multiplied by one power once a chunk,
-// and a factor in 32 bits would be off by half a step in every one of them.
-__device__ __forceinline__ float2 decay_power2(double rate, int n) {
-  const double p = exp2(rate * (double)n);
+// and a factor in 32 bits would be off by half a step in every one of them.  (In 64 bits:
+// for one warp of a block.)
+__device__ __forceinline__ float2 decay_power2(const DecayRate &r, int n) {
+  const double p = exp2(((double)r.hi + (double)r.lo) * (double)n);
   const float hi = (float)p;
   return make_float2(hi, isinf(hi) ? 0.f : (float)(p - (double)hi));
 }

@@ -144,6 +144,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       d_free, v_ready, mma_done[2];
   __shared__ __align__(16) float back[16];  // lam^(15 - j)
   __shared__ float power[129];              // lam^j
+  __shared__ float from[64];                // the segments' powers at this one's start
+  __shared__ float2 whole_s;                // lam^128
   __shared__ uint32_t tmem_base;
 
   // (the same in all of a warp's lanes, for the compiler too: the products' operands then
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   const int k0 = rings.q, v0s = rings.q + rings.k, n_slots = v0s + rings.v;  // first places
   uint8_t *const terms = smem + n_slots * slot_bytes;
   uint8_t *const s_tile = terms + da_term_bytes(ka);
-  const double rate = decay_rate(a.log_decay[w.h]);
+  const DecayRate rate = decay_rate(a.log_decay[w.h]);
   const int end = w.t1 < w.len ? w.t1 : w.len;
   // (LOCAL: a segment that nothing comes behind is nobody's start)
   const int chunks = end <= w.t0 || (LOCAL && w.t1 >= w.len)
@@ -203,6 +205,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     power[j] = p;
     if (j < 16) back[15 - j] = p;
   }
+  if (warp == 12 && lane == 0) whole_s = decay_power2(rate, 128);
+  if (!LOCAL && threadIdx.x >= 512 && (int)threadIdx.x - 512 <= w.s)
+    from[threadIdx.x - 512] = decay_power(rate, w.t0 - ((int)threadIdx.x - 512) * sp.L);
   if (warp == 1) {
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   } else if (!LOCAL && warp < DA_KEY_WARP) {
     // =========================== P and the outputs: a row and 64 columns a thread
     const int quad = warp & 3, half = (warp - DA_OUT_WARP) >> 2, row = quad * 32 + lane;
-    const float ahead = a.scale * power[row + 1], rate_f = (float)rate;
+    const float ahead = a.scale * power[row + 1], rate_f = rate.hi;
     const uint32_t ocol = tbase + lane_off + DA_COL_O + 64u * (uint32_t)half;
     RingAt rv(v0s);
     for (int g = 0; g < chunks; ++g, rv.step(v0s, rings.v)) {
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       }
     } else if (!LOCAL && (w.s == 0 || chunks > 0)) {
       for (int s = w.s == 0 ? 0 : 1; s <= w.s; ++s) {
-        const float f = w.s == 0 ? 1.f : decay_power(rate, w.t0 - s * sp.L);
+        const float f = from[s];
         const float4 *p = own + (size_t)s * (kDecaySlot / 4);
 #pragma unroll
         for (int j = 0; j < 64; j += 4) {
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         }
       }
     }
-    const float2 whole = decay_power2(rate, 128);
+    const float2 whole = whole_s;
     const auto publish = [&]() {  // the operand of the next chunk's Q S
       if (row < 64 * ka && half < va) {
         uint8_t *p = s_tile + (uint32_t)(half * ka) * 8192u;
