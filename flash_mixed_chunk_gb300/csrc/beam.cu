@@ -57,6 +57,16 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 }
 __device__ __forceinline__ uint32_t key_index(uint64_t k) { return ~(uint32_t)k; }
 
+// 64-bit values in an order of unsigned numbers (comparisons of doubles go through a
+// pipe of two a clock), larger than 0.
+__device__ __forceinline__ uint64_t order_of(double c) {
+  const uint64_t u = (uint64_t)__double_as_longlong(c + 0.0);
+  return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double value_of(uint64_t o) {
+  return __longlong_as_double((long long)(o >> 63 ? o & 0x7FFFFFFFFFFFFFFFull : ~o));
+}
+
 // One step of a bitonic network: lanes off apart, the larger to the lower lane
 // (down) or to the upper.
 template <typename K>
@@ -84,10 +94,43 @@ __device__ __forceinline__ uint64_t merge32(uint64_t a, uint64_t b, int lane) {
   return a;
 }
 
+// Of two lists of (value, index), largest value and of equal ones the lowest index
+// first, the 32 first, into the first list.
+__device__ __forceinline__ void merge_pairs(uint64_t &c, uint64_t &at, uint64_t c2, uint64_t at2,
+                                            int lane) {
+  const auto ahead = [](uint64_t x, uint64_t i, uint64_t y, uint64_t j) {
+    return x > y || (x == y && i < j);
+  };
+  c2 = __shfl_sync(kAll, c2, 31 - lane);
+  at2 = __shfl_sync(kAll, at2, 31 - lane);
+  if (ahead(c2, at2, c, at)) c = c2, at = at2;
+#pragma unroll
+  for (int off = 16; off > 0; off /= 2) {
+    const uint64_t x = __shfl_xor_sync(kAll, c, off), i = __shfl_xor_sync(kAll, at, off);
+    if (((lane & off) == 0) == ahead(x, i, c, at)) c = x, at = i;
+  }
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {
   float m;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
   return m;
+}
+
+// The 32 largest of `count` lists of n keys, largest first each, `stride` keys apart:
+// short ones several at a time, as one sort of 32.
+__device__ __forceinline__ uint64_t merge_lists(const uint64_t *lists, int count, int stride, int n,
+                                                int lane) {
+  uint64_t list = 0;
+  const int per = n <= 8 ? 32 / n : 1;
+  for (int w = 0; w < count; w += per) {
+    const int at = w + lane / n;
+    uint64_t o = 0;
+    if (lane / n < per && at < count) o = lists[at * stride + lane % n];
+    if (!__any_sync(kAll, o != 0)) continue;
+    list = merge32(list, per > 1 ? sort32(o, lane) : o, lane);
+  }
+  return list;
 }
 
 // (maximum, sum of exp(z - maximum)) of two parts; a maximum that is -inf has
@@ -115,30 +158,34 @@ struct Vec<2> { using type = uint16_t; };
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// A lane's logits of one task; -inf behind the row's end.  Vectors of BYTES bytes:
-// those of a call, so that all its rows are cut the same way.
+// A lane's logits of one task, as they are in memory.  Vectors of BYTES bytes: those of
+// a call, so that all its rows are cut the same way.
 template <typename T, int BYTES>
-__device__ __forceinline__ void load_task(const T *__restrict__ row, int V, int t, int lane,
-                                          float (&z)[E]) {
-  constexpr int EV = BYTES / (int)sizeof(T), NV = E / EV;
+struct Task {
+  static constexpr int EV = BYTES / (int)sizeof(T), NV = E / EV;
   using raw_t = typename Vec<BYTES>::type;
   union Raw {
     raw_t raw;
     T v[EV];
     __device__ Raw() {}
   } r[NV];
+  __device__ __forceinline__ void load(const T *__restrict__ row, int V, int t, int lane) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int64_t at = (int64_t)t * TASK + (j * 32 + lane) * EV;
-    if (at < V) r[j].raw = __ldg(reinterpret_cast<const raw_t *>(row + at));
+    for (int j = 0; j < NV; ++j) {
+      const int64_t at = (int64_t)t * TASK + (j * 32 + lane) * EV;
+      if (at < V) r[j].raw = __ldg(reinterpret_cast<const raw_t *>(row + at));
+    }
   }
+  // -inf behind the row's end
+  __device__ __forceinline__ void get(int V, int t, int lane, float (&z)[E]) const {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const bool in = (int64_t)t * TASK + (j * 32 + lane) * EV < V;
+    for (int j = 0; j < NV; ++j) {
+      const bool in = (int64_t)t * TASK + (j * 32 + lane) * EV < V;
 #pragma unroll
-    for (int i = 0; i < EV; ++i) z[j * EV + i] = in ? to_f(r[j].v[i]) : -kInf;
+      for (int i = 0; i < EV; ++i) z[j * EV + i] = in ? to_f(r[j].v[i]) : -kInf;
+    }
   }
-}
+};
 // Index of a lane's logit i.
 template <typename T, int BYTES>
 __device__ __forceinline__ uint32_t index_of(int t, int lane, int i) {
@@ -158,20 +205,26 @@ struct SelectArgs {
 };
 
 // Shared memory of a block: the n keys and the part of every (beam, warp), and the
-// same of every beam joined over the block's warps.
-__host__ __device__ inline size_t select_smem(int K, int n) {
-  return (size_t)K * (kWarps + 1) * (8 * (size_t)n + 8);
+// same of every beam joined over the block's warps (later half the warps' lists of
+// pairs).
+__host__ __device__ inline size_t select_joined(int K, int n) {
+  const size_t pairs = 2 * (kWarps / 2) * 32;
+  return (size_t)K * n > pairs ? (size_t)K * n : pairs;
 }
+__host__ __device__ inline size_t select_smem(int K, int n) {
+  return 8 * ((size_t)K * kWarps * n + select_joined(K, n) + (size_t)K * kWarps + K);
+}
+static_assert(kBeamCluster <= kWarps, "the blocks' lists take the place of the warps'");
 
 template <typename T, int BYTES>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     beam_select(const __grid_constant__ SelectArgs a) {
   extern __shared__ uint64_t sm64[];
   __shared__ uint64_t pool[kWarps][kPool];
   const int K = a.K, n = a.n;
   uint64_t *keys = sm64;                                        // [K][kWarps][n]
   uint64_t *keys_all = keys + (size_t)K * kWarps * n;           // [K][n]
-  Part *parts = reinterpret_cast<Part *>(keys_all + (size_t)K * n);  // [K][kWarps]
+  Part *parts = reinterpret_cast<Part *>(keys_all + select_joined(K, n));  // [K][kWarps]
   Part *part_all = parts + K * kWarps;                          // [K]
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -194,9 +247,13 @@ __global__ void __launch_bounds__(kThreads)
                     k % groups == me / a.group;
     if (on) {
       const T *row = static_cast<const T *>(a.logits) + (b * K + k) * a.row;
+      Task<T, BYTES> task;
+      if (in_group < NT) task.load(row, a.V, in_group, lane);
       for (int t = in_group; t < NT; t += a.group) {
         float z[E];
-        load_task<T, BYTES>(row, a.V, t, lane, z);
+        task.get(a.V, t, lane, z);
+        // the next ones are on their way while these are gone through
+        if (t + a.group < NT) task.load(row, a.V, t + a.group, lane);
         float top = z[0];
 #pragma unroll
         for (int i = 1; i < E; ++i) top = max_nan(top, z[i]);
@@ -231,6 +288,14 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
           for (int i = 0; i < E; ++i) mask |= z[i] >= v && z[i] > -kInf ? 1u << i : 0u;
         }
+        // a lane's first that may, read again: a register of a place known at run time is
+        // none
+        const auto pop = [&]() -> uint64_t {
+          if (mask == 0) return 0;
+          const uint32_t at = index_of<T, BYTES>(t, lane, __ffs(mask) - 1);
+          mask &= mask - 1;
+          return key_of(to_f(__ldg(row + at)), at);
+        };
         int before = __popc(mask);
 #pragma unroll
         for (int off = 1; off < 32; off *= 2) {
@@ -239,10 +304,20 @@ __global__ void __launch_bounds__(kThreads)
         }
         const int count = __shfl_sync(kAll, before, 31);
         before -= __popc(mask);
-        if (count <= kPool) {
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (mask >> i & 1) pool[warp][before++] = key_of(z[i], index_of<T, BYTES>(t, lane, i));
+        if (count <= 6) {  // one by one into their places
+          uint64_t mine = pop();
+          for (unsigned act; (act = __ballot_sync(kAll, mine != 0)) != 0;) {
+            const int from = __ffs(act) - 1;
+            const uint64_t key = __shfl_sync(kAll, mine, from);
+            const uint64_t up = __shfl_up_sync(kAll, list, 1);
+            if (list < key) list = lane == 0 || up > key ? key : up;
+            if (lane == from) mine = pop();
+          }
+        } else if (count <= kPool) {
+          while (mask != 0) {
+            const int to = before++;
+            pool[warp][to] = pop();
+          }
           __syncwarp();
           for (int i = 0; i < count; i += 32) {
             const uint64_t k1 = i + lane < count ? pool[warp][i + lane] : 0;
@@ -250,12 +325,8 @@ __global__ void __launch_bounds__(kThreads)
           }
           __syncwarp();
         } else {  // many equal values, or few lanes with any
-#pragma unroll 1
-          for (int i = 0; i < E; ++i) {
-            float v = -kInf;
-#pragma unroll
-            for (int j = 0; j < E; ++j) v = i == j ? z[j] : v;
-            const uint64_t k1 = mask >> i & 1 ? key_of(v, index_of<T, BYTES>(t, lane, i)) : 0;
+          while (__any_sync(kAll, mask != 0)) {
+            const uint64_t k1 = pop();
             if (__any_sync(kAll, k1 > __shfl_sync(kAll, list, n - 1)))
               list = merge32(list, sort32(k1, lane), lane);
           }
@@ -269,71 +340,68 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   for (int k = warp; k < K; k += kWarps) {
-    uint64_t list = 0;
+    const uint64_t list = merge_lists(keys + (size_t)k * kWarps * n, kWarps, n, n, lane);
     Part sum{-kInf, 0.f};
     for (int w = 0; w < kWarps; ++w) {
-      const uint64_t o = lane < n ? keys[(k * kWarps + w) * n + lane] : 0;
-      if (__any_sync(kAll, o != 0)) list = merge32(list, o, lane);
-      sum = join(sum, parts[k * kWarps + w]);
+      const Part p = parts[k * kWarps + w];
+      if (p.m != -kInf) sum = join(sum, p);  // (else a warp without a part of this row)
     }
     if (lane < n) keys_all[k * n + lane] = list;
     if (lane == 0) part_all[k] = sum;
   }
   cluster.sync();
   if (rank == 0) {
-    // the n best of every beam as candidates, over the lists of the block's warps
-    double *cand = reinterpret_cast<double *>(keys);  // [K][n]
-    int64_t *flat = reinterpret_cast<int64_t *>(keys + (size_t)K * n);
+    // all blocks' lists into this one's memory (over its own warps'), in one trip
+    uint64_t *got = keys;  // [K][kBeamCluster][n]
+    for (int i = tid; i < K * NC * n; i += kThreads) {
+      const int r = i / n % NC, k = i / n / NC;
+      got[(k * kBeamCluster + r) * n + i % n] =
+          cluster.map_shared_rank(keys_all, r)[k * n + i % n];
+    }
+    for (int i = tid; i < K * NC; i += kThreads)
+      parts[(i / NC) * kBeamCluster + i % NC] = cluster.map_shared_rank(part_all, i % NC)[i / NC];
+    __syncthreads();
+    // a warp's beams: the n best of each as candidates, and of them the n best
+    uint64_t best = 0, where = 0;  // a lane's place in the list, by value, then the lower index
     for (int k = warp; k < K; k += kWarps) {
-      uint64_t list = 0;
+      const uint64_t list = merge_lists(got + (size_t)k * kBeamCluster * n, NC, n, n, lane);
       Part sum{-kInf, 0.f};
       for (int r = 0; r < NC; ++r) {
-        const uint64_t *o = cluster.map_shared_rank(keys_all, r);
-        const Part *p = cluster.map_shared_rank(part_all, r);
-        list = merge32(list, lane < n ? o[k * n + lane] : 0, lane);
-        sum = join(sum, p[k]);
+        const Part p = parts[k * kBeamCluster + r];
+        if (p.m != -kInf) sum = join(sum, p);
       }
-      const double score = (double)scores[k];
-      bool some = list != 0 && isfinite(sum.m);
-      double c = some ? score + ((double)key_value(list) - ((double)sum.m + log((double)sum.s)))
-                      : 0.0;
-      uint32_t token = key_index(list);
-      if (isfinite(scores[k]) && finished != nullptr && finished[k]) {
-        some = lane == 0;
-        c = score;
-        token = (uint32_t)a.pad;
+      uint64_t c = 0, at = (uint64_t)k * a.V + key_index(list);
+      if (finished != nullptr && finished[k]) {
+        if (lane == 0 && isfinite(scores[k])) c = order_of((double)scores[k]);
+        at = (uint64_t)k * a.V + a.pad;
+      } else if (list != 0 && isfinite(sum.m)) {
+        c = order_of((double)scores[k] +
+                     ((double)key_value(list) - ((double)sum.m + log((double)sum.s))));
       }
-      if (lane < n) {
-        cand[k * n + lane] = c;
-        flat[k * n + lane] = some ? (int64_t)k * a.V + token : -1;
-      }
+      if (lane >= n) c = 0;
+      merge_pairs(best, where, c, at, lane);
     }
-    __syncthreads();
-    int some = 0;
-    for (int i = tid; i < K * n; i += kThreads) {
-      const int64_t f = flat[i];
-      if (f < 0) continue;
-      ++some;
-      const double c = cand[i];
-      int better = 0;
-      for (int j = 0; j < K * n; ++j)
-        better += flat[j] >= 0 && (cand[j] > c || (cand[j] == c && flat[j] < f)) ? 1 : 0;
-      if (better < n) {
-        a.score[b * n + better] = (float)c;
-        a.parent[b * n + better] = f / a.V;
-        a.token[b * n + better] = f % a.V;
+    // the warps' lists, pair by pair
+    uint64_t *list_c = keys_all, *list_at = keys_all + kWarps / 2 * 32;
+    for (int half = kWarps / 2; half > 0; half /= 2) {
+      __syncthreads();
+      if (warp >= half && warp < 2 * half) {
+        list_c[(warp - half) * 32 + lane] = best;
+        list_at[(warp - half) * 32 + lane] = where;
       }
+      __syncthreads();
+      if (warp < half) merge_pairs(best, where, list_c[warp * 32 + lane], list_at[warp * 32 + lane], lane);
     }
-    // places without a candidate
-    int *count = reinterpret_cast<int *>(pool);
-    if (tid == 0) *count = 0;
-    __syncthreads();
-    if (some > 0) atomicAdd(count, some);
-    __syncthreads();
-    for (int i = *count + tid; i < n; i += kThreads) {
-      a.score[b * n + i] = -kInf;
-      a.parent[b * n + i] = i % K;
-      a.token[b * n + i] = a.pad;
+    if (warp == 0) {
+      if (best != 0 && lane < n) {
+        a.score[b * n + lane] = (float)value_of(best);
+        a.parent[b * n + lane] = (int64_t)(where / (uint32_t)a.V);
+        a.token[b * n + lane] = (int64_t)(where % (uint32_t)a.V);
+      } else if (lane < n) {  // a place without a candidate
+        a.score[b * n + lane] = -kInf;
+        a.parent[b * n + lane] = lane % K;
+        a.token[b * n + lane] = a.pad;
+      }
     }
   }
   cluster.sync();  // the other blocks' lists stay until they are read
@@ -423,9 +491,14 @@ int launch_beam_select(const void *logits, int64_t row, const float *scores,
   const int64_t NT = ((int64_t)V + TASK - 1) / TASK;
   int NC = 1;
   while (NC < kBeamCluster && (int64_t)B * NC * kWarps < 24 * 152 && NC * kWarps < NT * K) NC *= 2;
-  int group = 1;
-  while (group < NC * kWarps && group < NT) group *= 2;
-  a.group = group;
+  // warps that share a beam: a warp's first task of a row costs about twice the others'
+  // (its list begins)
+  int64_t least = INT64_MAX;
+  for (int group = 1; group <= NC * kWarps; group *= 2) {
+    const int64_t groups = NC * kWarps / group;
+    const int64_t cost = (K + groups - 1) / groups * ((NT + group - 1) / group + 1);
+    if (cost < least) least = cost, a.group = group;
+  }
   const int el = bf16 ? 2 : 4;
   const uintptr_t at = reinterpret_cast<uintptr_t>(logits);
   const auto fits = [&](int bytes) {
