@@ -111,6 +111,13 @@ __device__ __forceinline__ void merge_pairs(uint64_t &c, uint64_t &at, uint64_t 
   }
 }
 
+// exp(x), x <= 0 (what is under 2^-126 is 0)
+__device__ __forceinline__ float exp_below(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+  return y;
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {
   float m;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
@@ -178,6 +185,13 @@ struct Task {
   }
   // -inf behind the row's end
   __device__ __forceinline__ void get(int V, int t, int lane, float (&z)[E]) const {
+    if ((int64_t)(t + 1) * TASK <= V) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < EV; ++i) z[j * EV + i] = to_f(r[j].v[i]);
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const bool in = (int64_t)t * TASK + (j * 32 + lane) * EV < V;
@@ -204,17 +218,37 @@ struct SelectArgs {
   int group;  // warps of a cluster that share a beam (a power of 2)
 };
 
-// Shared memory of a block: the n keys and the part of every (beam, warp), and the
-// same of every beam joined over the block's warps (later half the warps' lists of
-// pairs).
-__host__ __device__ inline size_t select_joined(int K, int n) {
-  const size_t pairs = 2 * (kWarps / 2) * 32;
-  return (size_t)K * n > pairs ? (size_t)K * n : pairs;
+// Shared memory of a block, in words of 64 bits: the n keys and the part of every (beam,
+// warp), the same of every (beam, block) in the cluster's first block, and the nth
+// largest value of every (beam, warp) so far.
+struct SelectSmem {
+  int keys, parts, got, got_parts, tops, total;
+};
+__host__ __device__ inline SelectSmem select_smem(int K, int n) {
+  SelectSmem s;
+  s.keys = 0;
+  s.parts = s.keys + K * kWarps * n;
+  s.got = s.parts + K * kWarps;
+  s.got_parts = s.got + K * kBeamCluster * n;
+  s.tops = s.got_parts + K * kBeamCluster;
+  s.total = s.tops + K * kWarps / 2;
+  return s;
 }
-__host__ __device__ inline size_t select_smem(int K, int n) {
-  return 8 * ((size_t)K * kWarps * n + select_joined(K, n) + (size_t)K * kWarps + K);
+static_assert(kWarps * kPool >= 2 * (kWarps / 2) * 32, "half the warps' lists of pairs");
+
+// The two halves of a barrier over the cluster's threads (those that have ended do not
+// count); what was written before the first is there behind the second.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-static_assert(kBeamCluster <= kWarps, "the blocks' lists take the place of the warps'");
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The next float above v (finite).
+__device__ __forceinline__ float nextafter_up(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return __uint_as_float(u >> 31 ? u - 1 : u + 1);
+}
 
 template <typename T, int BYTES>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -222,30 +256,41 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint64_t sm64[];
   __shared__ uint64_t pool[kWarps][kPool];
   const int K = a.K, n = a.n;
-  uint64_t *keys = sm64;                                        // [K][kWarps][n]
-  uint64_t *keys_all = keys + (size_t)K * kWarps * n;           // [K][n]
-  Part *parts = reinterpret_cast<Part *>(keys_all + select_joined(K, n));  // [K][kWarps]
-  Part *part_all = parts + K * kWarps;                          // [K]
+  const SelectSmem at = select_smem(K, n);
+  uint64_t *keys = sm64 + at.keys;                               // [K][kWarps][n]
+  Part *parts = reinterpret_cast<Part *>(sm64 + at.parts);       // [K][kWarps]
+  uint64_t *keys_got = sm64 + at.got;                            // [K][kBeamCluster][n]
+  Part *parts_got = reinterpret_cast<Part *>(sm64 + at.got_parts);  // [K][kBeamCluster]
+  volatile uint32_t *tops = reinterpret_cast<uint32_t *>(sm64 + at.tops);  // [K][kWarps]
 
   cg::cluster_group cluster = cg::this_cluster();
   const int NC = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  cluster_arrive();  // this block's shared memory is there
   const int64_t b = blockIdx.x / NC;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int NT = (a.V + TASK - 1) / TASK;
+  // nothing yet
+  for (int i = tid; i < K * kWarps * n; i += kThreads) keys[i] = 0;
+  for (int i = tid; i < K * kWarps; i += kThreads) {
+    parts[i] = Part{-kInf, 0.f};
+    tops[i] = 0;
+  }
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
 
   const float *scores = a.scores + b * K;
   const uint8_t *finished = a.finished == nullptr ? nullptr : a.finished + b * K;
-  const int all = NC * kWarps, me = rank * kWarps + warp;
-  const int groups = all / a.group, in_group = me % a.group;
+  const int me = rank * kWarps + warp;
+  const int groups = NC * kWarps / a.group, in_group = me % a.group;
+  // the warps of this block that share a beam, and how many of its n a warp answers for
+  const int near = a.group < kWarps ? a.group : kWarps, nth = (n + near - 1) / near;
+  const int first = warp & ~(near - 1);
 
-  for (int k = 0; k < K; ++k) {
+  for (int k = me / a.group; k < K; k += groups) {
     uint64_t list = 0;  // 0: no key
     Part sum{-kInf, 0.f};
-    const bool on = isfinite(scores[k]) && !(finished != nullptr && finished[k]) &&
-                    k % groups == me / a.group;
-    if (on) {
+    if (isfinite(scores[k]) && !(finished != nullptr && finished[k])) {
       const T *row = static_cast<const T *>(a.logits) + (b * K + k) * a.row;
       Task<T, BYTES> task;
       if (in_group < NT) task.load(row, a.V, in_group, lane);
@@ -269,24 +314,33 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (m == -kInf) continue;
         float add = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) add += __expf(z[i] - m);
-        sum.s = (sum.s == 0.f ? 0.f : sum.s * __expf(sum.m - m)) + add;
+        for (int i = 0; i < E; ++i) add += exp_below(z[i] - m);
+        sum.s = (sum.s == 0.f ? 0.f : sum.s * exp_below(sum.m - m)) + add;
         sum.m = m;
 
         // What may enter the list: with a full one whatever is above its last (an
         // equal value here has a higher index); before that whatever reaches the
-        // n-th largest of the lanes' maxima, n of the values do.
+        // n-th largest of the lanes' maxima, n of the values do.  And nothing below what
+        // the block's warps of this beam have together: each its nth largest (as read at
+        // any time; they only rise, and where they stand the answer does not depend on).
         const uint64_t last = __shfl_sync(kAll, list, n - 1);
-        uint32_t mask = 0;
-        if (last != 0) {
-          const float v = key_value(last);
+        const uint32_t seen = lane < near ? tops[k * kWarps + first + lane] : 0xFFFFFFFFu;
+        const uint32_t floor = __reduce_min_sync(kAll, seen);
+        float v = floor != 0 ? key_value((uint64_t)floor << 32) : -kInf;
+        if (last != 0 && !(v > key_value(last))) {
+          v = key_value(last);
           if (!(most > v)) continue;
+          v = nextafter_up(v);
+        } else if (last == 0) {
+          v = fmaxf(v, __shfl_sync(kAll, sort32(top, lane), n - 1));
+        }
+        if (most < v) continue;
+        uint32_t mask = 0;
 #pragma unroll
-          for (int i = 0; i < E; ++i) mask |= z[i] > v ? 1u << i : 0u;
-        } else {
-          const float v = __shfl_sync(kAll, sort32(top, lane), n - 1);
+        for (int i = 0; i < E; ++i) mask |= z[i] >= v ? 1u << i : 0u;
+        if (v == -kInf) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) mask |= z[i] >= v && z[i] > -kInf ? 1u << i : 0u;
+          for (int i = 0; i < E; ++i) mask &= z[i] > -kInf ? ~0u : ~(1u << i);
         }
         // a lane's first that may, read again: a register of a place known at run time is
         // none
@@ -331,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               list = merge32(list, sort32(k1, lane), lane);
           }
         }
+        const uint64_t own = __shfl_sync(kAll, list, nth - 1);
+        if (lane == 0) tops[k * kWarps + warp] = (uint32_t)(own >> 32);
       }
     }
 #pragma unroll
@@ -339,6 +395,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) parts[k * kWarps + warp] = sum;
   }
   __syncthreads();
+  // the block's list of every beam, into the first block's memory
+  cluster_wait();
   for (int k = warp; k < K; k += kWarps) {
     const uint64_t list = merge_lists(keys + (size_t)k * kWarps * n, kWarps, n, n, lane);
     Part sum{-kInf, 0.f};
@@ -346,43 +404,37 @@ __global__ void __launch_bounds__(kThreads, 2)
       const Part p = parts[k * kWarps + w];
       if (p.m != -kInf) sum = join(sum, p);  // (else a warp without a part of this row)
     }
-    if (lane < n) keys_all[k * n + lane] = list;
-    if (lane == 0) part_all[k] = sum;
+    if (lane < n)
+      cluster.map_shared_rank(keys_got, 0)[(k * kBeamCluster + rank) * n + lane] = list;
+    if (lane == 0) cluster.map_shared_rank(parts_got, 0)[k * kBeamCluster + rank] = sum;
   }
-  cluster.sync();
-  if (rank == 0) {
-    // all blocks' lists into this one's memory (over its own warps'), in one trip
-    uint64_t *got = keys;  // [K][kBeamCluster][n]
-    for (int i = tid; i < K * NC * n; i += kThreads) {
-      const int r = i / n % NC, k = i / n / NC;
-      got[(k * kBeamCluster + r) * n + i % n] =
-          cluster.map_shared_rank(keys_all, r)[k * n + i % n];
-    }
-    for (int i = tid; i < K * NC; i += kThreads)
-      parts[(i / NC) * kBeamCluster + i % NC] = cluster.map_shared_rank(part_all, i % NC)[i / NC];
-    __syncthreads();
+  __syncwarp();
+  cluster_arrive();
+  if (rank != 0) return;  // nobody reads this block's memory
+  cluster_wait();
+  {
     // a warp's beams: the n best of each as candidates, and of them the n best
     uint64_t best = 0, where = 0;  // a lane's place in the list, by value, then the lower index
     for (int k = warp; k < K; k += kWarps) {
-      const uint64_t list = merge_lists(got + (size_t)k * kBeamCluster * n, NC, n, n, lane);
+      const uint64_t list = merge_lists(keys_got + (size_t)k * kBeamCluster * n, NC, n, n, lane);
       Part sum{-kInf, 0.f};
       for (int r = 0; r < NC; ++r) {
-        const Part p = parts[k * kBeamCluster + r];
+        const Part p = parts_got[k * kBeamCluster + r];
         if (p.m != -kInf) sum = join(sum, p);
       }
-      uint64_t c = 0, at = (uint64_t)k * a.V + key_index(list);
+      uint64_t c = 0, flat = (uint64_t)k * a.V + key_index(list);
       if (finished != nullptr && finished[k]) {
         if (lane == 0 && isfinite(scores[k])) c = order_of((double)scores[k]);
-        at = (uint64_t)k * a.V + a.pad;
+        flat = (uint64_t)k * a.V + a.pad;
       } else if (list != 0 && isfinite(sum.m)) {
         c = order_of((double)scores[k] +
                      ((double)key_value(list) - ((double)sum.m + log((double)sum.s))));
       }
       if (lane >= n) c = 0;
-      merge_pairs(best, where, c, at, lane);
+      merge_pairs(best, where, c, flat, lane);
     }
     // the warps' lists, pair by pair
-    uint64_t *list_c = keys_all, *list_at = keys_all + kWarps / 2 * 32;
+    uint64_t *list_c = &pool[0][0], *list_at = list_c + kWarps / 2 * 32;
     for (int half = kWarps / 2; half > 0; half /= 2) {
       __syncthreads();
       if (warp >= half && warp < 2 * half) {
@@ -404,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-  cluster.sync();  // the other blocks' lists stay until they are read
 }
 
 // ------------------------------------------------------------------- reordering
@@ -461,7 +512,7 @@ int select(const SelectArgs &a, int B, int NC, cudaStream_t stream) {
   if (!attrs.run([] {
         return cudaFuncSetAttribute(beam_select<T, BYTES>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)select_smem(kBeamMax, kBeamMax)) == cudaSuccess;
+                                    8 * select_smem(kBeamMax, kBeamMax).total) == cudaSuccess;
       }))
     return 1;
   cudaLaunchAttribute attr[2];
@@ -476,7 +527,7 @@ int select(const SelectArgs &a, int B, int NC, cudaStream_t stream) {
   cfg.numAttrs = 2;
   cfg.gridDim = dim3((unsigned)((int64_t)B * NC));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = select_smem(a.K, a.n);
+  cfg.dynamicSmemBytes = 8 * (size_t)select_smem(a.K, a.n).total;
   return cudaLaunchKernelEx(&cfg, beam_select<T, BYTES>, a) == cudaSuccess ? 0 : 1;
 }
 
