@@ -40,7 +40,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int E = 32;           // logits of a lane
 constexpr int TASK = 32 * E;    // of a warp at a time
-constexpr int kPool = 128;      // keys that a warp gathers before it sorts them
+constexpr int kPool = 256;      // keys that a warp gathers before it sorts them
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -537,11 +537,11 @@ int launch_beam_select(const void *logits, int64_t row, const float *scores,
                        const uint8_t *finished, float *score, int64_t *parent, int64_t *token,
                        int B, int K, int V, int n, int pad, int bf16, cudaStream_t stream) {
   SelectArgs a{logits, row, scores, finished, score, parent, token, K, V, n, pad, 0};
-  // a beam's row has NT warps' work; as many blocks as give about 24 warps an SM,
-  // no more than have any
+  // a beam's row has NT warps' work; as many blocks as run at once (two an SM), no more
+  // than have any
   const int64_t NT = ((int64_t)V + TASK - 1) / TASK;
   int NC = 1;
-  while (NC < kBeamCluster && (int64_t)B * NC * kWarps < 24 * 152 && NC * kWarps < NT * K) NC *= 2;
+  while (NC < kBeamCluster && (int64_t)B * 2 * NC <= 2 * 152 && NC * kWarps < NT * K) NC *= 2;
   // warps that share a beam: a warp's first task of a row costs about twice the others'
   // (its list begins)
   int64_t least = INT64_MAX;

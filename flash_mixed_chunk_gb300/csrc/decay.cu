@@ -70,10 +70,14 @@ __global__ void __launch_bounds__(kThreads)
   const DecayRate rate = decay_rate(a.log_decay[w.h]);
   if (tid <= C) pw[tid] = decay_power(rate, tid);
   __shared__ float2 whole;
+  __shared__ float from[64];  // the segments' powers at this one's start
+  if (!LOCAL && tid >= 128 && tid - 128 <= w.s) from[tid - 128] = decay_power(rate, w.t0 - (tid - 128) * sp.L);
   if (tid == 64) whole = decay_power2(rate, C);  // (read behind the first chunk's barriers)
 
   // the state at the segment's start
   const size_t at = ((size_t)w.b * a.H + w.h) * dk * (size_t)a.dv + v0;
+  __syncthreads();
+  const int warp = tid / 32, lane = tid % 32;
   for (int i = tid; i < dk * DVT; i += kThreads) {
     const int d = i / DVT, c = i % DVT;
     float x = 0.f;
@@ -84,8 +88,8 @@ __global__ void __launch_bounds__(kThreads)
       if (w.s == 0) {
         x = own[i];
       } else if (w.t0 < w.len) {
-        for (int s = 1; s <= w.s; ++s)
-          x = fmaf(decay_power(rate, w.t0 - s * sp.L), own[s * slot + i], x);
+#pragma unroll 4
+        for (int s = 1; s <= w.s; ++s) x = fmaf(from[s], own[s * slot + i], x);
       }
     }
     st[i] = x;
@@ -104,14 +108,16 @@ __global__ void __launch_bounds__(kThreads)
     const int n = end - t < C ? end - t : C;
     __syncthreads();  // the last chunk's reads of the tiles
     // tokens behind the end are zeros, whatever the arrays hold there
-    for (int i = tid; i < C * dk; i += kThreads) {
-      const int r = i / dk, d = i % dk;
-      if (!LOCAL) sq[r * ks + d] = r < n ? to_f(q[(int64_t)(t + r) * a.qs[1] + d]) : 0.f;
-      sk[r * ks + d] = r < n ? to_f(k[(int64_t)(t + r) * a.ks[1] + d]) : 0.f;
-    }
-    for (int i = tid; i < C * DVT; i += kThreads) {
-      const int r = i / DVT, c = i % DVT;
-      sv[r * VS + c] = r < n && c < nv ? to_f(v[(int64_t)(t + r) * a.vs[1] + c]) : 0.f;
+#pragma unroll 1
+    for (int r = warp; r < C; r += kThreads / 32) {
+      const int64_t row = t + r;
+      for (int d = lane; d < dk; d += 32) {
+        if (!LOCAL) sq[r * ks + d] = r < n ? to_f(q[row * a.qs[1] + d]) : 0.f;
+        sk[r * ks + d] = r < n ? to_f(k[row * a.ks[1] + d]) : 0.f;
+      }
+#pragma unroll
+      for (int c = lane; c < DVT; c += 32)
+        sv[r * VS + c] = r < n && c < nv ? to_f(v[row * a.vs[1] + c]) : 0.f;
     }
     __syncthreads();
     if (!LOCAL) {
@@ -158,7 +164,8 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     // k_j's weight in the state
-    for (int i = tid; i < n * dk; i += kThreads) sk[(i / dk) * ks + i % dk] *= pw[n - 1 - i / dk];
+    for (int r = warp; r < n; r += kThreads / 32)
+      for (int d = lane; d < dk; d += 32) sk[r * ks + d] *= pw[n - 1 - r];
     __syncthreads();
     const float2 g = n == C ? whole : make_float2(pw[n], 0.f);
     for (int d = ty; d < dk; d += 16) {
@@ -182,8 +189,8 @@ __global__ void __launch_bounds__(kThreads)
   }
   // outputs behind the sequence's end
   const int z0 = w.t0 > w.len ? w.t0 : w.len;
-  for (int64_t i = tid; i < (int64_t)(w.t1 - z0) * nv; i += kThreads)
-    put(o + (size_t)(z0 + i / nv) * orow + i % nv, 0.f);
+  for (int r = z0 + warp; r < w.t1; r += kThreads / 32)
+    for (int c = lane; c < nv; c += 32) put(o + (size_t)r * orow + c, 0.f);
   if (a.state_out != nullptr && decay_last(w, sp.L))
     for (int i = tid; i < dk * DVT; i += kThreads)
       if (i % DVT < nv) a.state_out[at + (size_t)(i / DVT) * a.dv + i % DVT] = st[i];

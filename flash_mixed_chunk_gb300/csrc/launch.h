@@ -441,12 +441,12 @@ struct DecayArgs {
 struct DecaySplit {
   int S, L, nvt;
 };
-// CUDA cores: about two units an SM, segments of 256 tokens at least.
+// CUDA cores: about two units an SM, segments of 64 tokens at least and 64 at most.
 inline DecaySplit decay_split_simt(int B, int T, int H, int dv) {
   const int nvt = (dv + 63) / 64;
   const int64_t heads = (int64_t)B * H * nvt;
   int64_t S = heads < 2 * kDecaySms ? 2 * kDecaySms / heads : 1;
-  const int64_t most = ((int64_t)T + 255) / 256;
+  const int64_t most = ((int64_t)T + 63) / 64 < 64 ? ((int64_t)T + 63) / 64 : 64;
   S = S < most ? S : most;
   const int64_t L = ((T + S - 1) / S + 31) / 32 * 32;
   return DecaySplit{(int)((T + L - 1) / L), (int)L, nvt};
