@@ -40,10 +40,22 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 
 // ------------------------------------------------------------------- prompts
 
-// Shared memory, in floats: q and k [C][dk + 4], v [C][VS], the chunk's weights
-// [C][C + 1], the powers 0 .. C, the state [dk][DVT].
+// dk in whole float4s (zeros behind it), and a row of q or k: an odd number of float4s,
+// so that the rows that eight threads read at once lie in different banks.
+__host__ __device__ constexpr int padded(int dk) { return (dk + 3) / 4 * 4; }
+__host__ __device__ constexpr int row_of(int dk) {
+  return padded(dk) + (padded(dk) / 4 % 2 ? 8 : 4);
+}
+constexpr int WS = C + 4;  // row of the weights
+// Shared memory, in floats: q and k [C][row_of(dk)], v [C][VS], the state
+// [padded(dk)][DVT], the chunk's weights [C][WS], the powers 0 .. C.
 __host__ __device__ constexpr int prompt_floats(int dk) {
-  return 2 * C * (dk + 4) + C * VS + C * (C + 1) + (C + 4) + dk * DVT;
+  return 2 * C * row_of(dk) + C * VS + padded(dk) * DVT + C * WS + C + 4;
+}
+__device__ __forceinline__ float4 &at4(float *p) { return *reinterpret_cast<float4 *>(p); }
+__device__ __forceinline__ void fma4(float x, const float4 &y, float4 &z) {
+  z.x = fmaf(x, y.x, z.x), z.y = fmaf(x, y.y, z.y);
+  z.z = fmaf(x, y.z, z.z), z.w = fmaf(x, y.w, z.w);
 }
 
 // A block is one unit.  LOCAL: what segments 0 .. S-2 add to the state, into
@@ -55,9 +67,9 @@ __global__ void __launch_bounds__(kThreads)
                  float *__restrict__ slots) {
   extern __shared__ float4 smem4[];
   float *sm = reinterpret_cast<float *>(smem4);
-  const int dk = a.dk, ks = dk + 4;
+  const int dk = a.dk, dkp = padded(dk), ks = row_of(dk);
   float *sq = sm, *sk = sq + C * ks, *sv = sk + C * ks, *st = sv + C * VS;
-  float *sw = st + dk * DVT, *pw = sw + C * (C + 1);
+  float *sw = st + dkp * DVT, *pw = sw + C * WS;
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
 
   griddep_wait();
@@ -78,10 +90,11 @@ __global__ void __launch_bounds__(kThreads)
   const size_t at = ((size_t)w.b * a.H + w.h) * dk * (size_t)a.dv + v0;
   __syncthreads();
   const int warp = tid / 32, lane = tid % 32;
-  for (int i = tid; i < dk * DVT; i += kThreads) {
+  for (int i = tid; i < dkp * DVT; i += kThreads) {
     const int d = i / DVT, c = i % DVT;
     float x = 0.f;
-    if (sp.S == 1 || (LOCAL && w.s == 0)) {
+    if (d >= dk) {
+    } else if (sp.S == 1 || (LOCAL && w.s == 0)) {
       if (a.state_in != nullptr && c < nv) x = a.state_in[at + (size_t)d * a.dv + c];
       if (LOCAL) own[i] = x;
     } else if (!LOCAL) {
@@ -108,50 +121,81 @@ __global__ void __launch_bounds__(kThreads)
     const int n = end - t < C ? end - t : C;
     __syncthreads();  // the last chunk's reads of the tiles
     // tokens behind the end are zeros, whatever the arrays hold there
-#pragma unroll 1
-    for (int r = warp; r < C; r += kThreads / 32) {
-      const int64_t row = t + r;
-      for (int d = lane; d < dk; d += 32) {
-        if (!LOCAL) sq[r * ks + d] = r < n ? to_f(q[row * a.qs[1] + d]) : 0.f;
-        sk[r * ks + d] = r < n ? to_f(k[row * a.ks[1] + d]) : 0.f;
+    // (a warp's four rows, loads ahead of stores: one trip to memory for all of them)
+    constexpr int R = C / (kThreads / 32);
+    T y[2 * R];
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) {
+      const int r = warp + kThreads / 32 * (i % R), c = lane + 32 * (i / R);
+      if (r < n && c < nv) y[i] = v[(int64_t)(t + r) * a.vs[1] + c];
+    }
+    for (int d = lane; d < dkp; d += 32) {
+      T x[2 * R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int r = warp + kThreads / 32 * i;
+        if (r >= n || d >= dk) continue;
+        if (!LOCAL) x[i] = q[(int64_t)(t + r) * a.qs[1] + d];
+        x[R + i] = k[(int64_t)(t + r) * a.ks[1] + d];
       }
 #pragma unroll
-      for (int c = lane; c < DVT; c += 32)
-        sv[r * VS + c] = r < n && c < nv ? to_f(v[row * a.vs[1] + c]) : 0.f;
+      for (int i = 0; i < R; ++i) {
+        const int r = warp + kThreads / 32 * i;
+        const bool in = r < n && d < dk;
+        if (!LOCAL) sq[r * ks + d] = in ? to_f(x[i]) : 0.f;
+        sk[r * ks + d] = in ? to_f(x[R + i]) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) {
+      const int r = warp + kThreads / 32 * (i % R), c = lane + 32 * (i / R);
+      sv[r * VS + c] = r < n && c < nv ? to_f(y[i]) : 0.f;
     }
     __syncthreads();
     if (!LOCAL) {
+      // rows 2 ty and 2 ty + 1, keys tx and tx + 16
       float acc[2][2] = {};
-      for (int d = 0; d < dk; ++d) {
-        const float q0 = sq[2 * ty * ks + d], q1 = sq[(2 * ty + 1) * ks + d];
-        const float k0 = sk[2 * tx * ks + d], k1 = sk[(2 * tx + 1) * ks + d];
-        acc[0][0] = fmaf(q0, k0, acc[0][0]);
-        acc[0][1] = fmaf(q0, k1, acc[0][1]);
-        acc[1][0] = fmaf(q1, k0, acc[1][0]);
-        acc[1][1] = fmaf(q1, k1, acc[1][1]);
+#pragma unroll 2
+      for (int d = 0; d < dkp; d += 4) {
+        const float4 x[2] = {at4(sq + 2 * ty * ks + d), at4(sq + (2 * ty + 1) * ks + d)};
+        const float4 y[2] = {at4(sk + tx * ks + d), at4(sk + (tx + 16) * ks + d)};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y,
+                        fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int gap = 2 * ty + i - (2 * tx + j);
-          sw[(2 * ty + i) * (C + 1) + 2 * tx + j] = gap >= 0 ? acc[i][j] * pw[gap] : 0.f;
+          const int gap = 2 * ty + i - (tx + 16 * j);
+          sw[(2 * ty + i) * WS + tx + 16 * j] = gap >= 0 ? acc[i][j] * pw[gap] : 0.f;
         }
       __syncthreads();
       float4 near[2] = {}, far[2] = {};
-      auto fma4 = [](float x, const float4 &y, float4 &z) {
-        z.x = fmaf(x, y.x, z.x), z.y = fmaf(x, y.y, z.y);
-        z.z = fmaf(x, y.z, z.z), z.w = fmaf(x, y.w, z.w);
-      };
-      for (int j = 0; j <= 2 * ty + 1; ++j) {
-        const float4 x = *reinterpret_cast<const float4 *>(sv + j * VS + 4 * tx);
-        fma4(sw[2 * ty * (C + 1) + j], x, near[0]);
-        fma4(sw[(2 * ty + 1) * (C + 1) + j], x, near[1]);
+#pragma unroll 2
+      for (int j = 0; j <= 2 * ty + 1; j += 4) {
+        const float4 x0 = at4(sw + 2 * ty * WS + j), x1 = at4(sw + (2 * ty + 1) * WS + j);
+        const float *p0 = &x0.x, *p1 = &x1.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 y = at4(sv + (j + i) * VS + 4 * tx);
+          fma4(p0[i], y, near[0]);
+          fma4(p1[i], y, near[1]);
+        }
       }
-      for (int d = 0; d < dk; ++d) {
-        const float4 x = *reinterpret_cast<const float4 *>(st + d * DVT + 4 * tx);
-        fma4(sq[2 * ty * ks + d], x, far[0]);
-        fma4(sq[(2 * ty + 1) * ks + d], x, far[1]);
+#pragma unroll 2
+      for (int d = 0; d < dkp; d += 4) {
+        const float4 x0 = at4(sq + 2 * ty * ks + d), x1 = at4(sq + (2 * ty + 1) * ks + d);
+        const float *p0 = &x0.x, *p1 = &x1.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 y = at4(st + (d + i) * DVT + 4 * tx);
+          fma4(p0[i], y, far[0]);
+          fma4(p1[i], y, far[1]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -168,18 +212,26 @@ __global__ void __launch_bounds__(kThreads)
       for (int d = lane; d < dk; d += 32) sk[r * ks + d] *= pw[n - 1 - r];
     __syncthreads();
     const float2 g = n == C ? whole : make_float2(pw[n], 0.f);
-    for (int d = ty; d < dk; d += 16) {
-      float4 add = {};
+    // places 4 ty .. 4 ty + 3 of dk, columns 4 tx .. 4 tx + 3
+    for (int d = 4 * ty; d < dkp; d += 64) {
+      float4 add[4] = {};
+#pragma unroll 4
       for (int j = 0; j < n; ++j) {
-        const float x = sk[j * ks + d];
-        const float4 y = *reinterpret_cast<const float4 *>(sv + j * VS + 4 * tx);
-        add.x = fmaf(x, y.x, add.x), add.y = fmaf(x, y.y, add.y);
-        add.z = fmaf(x, y.z, add.z), add.w = fmaf(x, y.w, add.w);
+        const float4 x = at4(sk + j * ks + d), y = at4(sv + j * VS + 4 * tx);
+        fma4(x.x, y, add[0]);
+        fma4(x.y, y, add[1]);
+        fma4(x.z, y, add[2]);
+        fma4(x.w, y, add[3]);
       }
-      float4 *p = reinterpret_cast<float4 *>(st + d * DVT + 4 * tx);
-      const float4 s = *p;
-      *p = make_float4(fmaf(s.x, g.x, fmaf(s.x, g.y, add.x)), fmaf(s.y, g.x, fmaf(s.y, g.y, add.y)),
-                       fmaf(s.z, g.x, fmaf(s.z, g.y, add.z)), fmaf(s.w, g.x, fmaf(s.w, g.y, add.w)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float4 &p = at4(st + (d + i) * DVT + 4 * tx);
+        const float4 s = p;
+        p = make_float4(fmaf(s.x, g.x, fmaf(s.x, g.y, add[i].x)),
+                        fmaf(s.y, g.x, fmaf(s.y, g.y, add[i].y)),
+                        fmaf(s.z, g.x, fmaf(s.z, g.y, add[i].z)),
+                        fmaf(s.w, g.x, fmaf(s.w, g.y, add[i].w)));
+      }
     }
   }
   __syncthreads();
