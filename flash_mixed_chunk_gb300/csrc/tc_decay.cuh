@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   __shared__ __align__(8) uint64_t full[DA_SLOTS], empty[DA_SLOTS], x_ready[2], x_free[2];
   __shared__ __align__(8) uint64_t staged[2], stored[2];
   __shared__ __align__(8) uint64_t sc_full[2], qs_full, p_ready, o_full, o_free, s_ready, d_full[2],
-      d_free, v_ready, mma_done[2];
+      d_free[2], v_ready, mma_done[2];
   __shared__ __align__(16) float back[16];  // lam^(15 - j)
   __shared__ float power[129];              // lam^j
   __shared__ float from[64];                // the segments' powers at this one's start
@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   const int chunks = end <= w.t0 || (LOCAL && w.t1 >= w.len)
                          ? 0
                          : (end - w.t0 + 127) / 128;
+  constexpr int DBUF = LOCAL ? 2 : 1;  // of D (LOCAL: O's columns are free)
   const auto tokens = [&](int g) {
     const int n = end - w.t0 - 128 * g;
     return n < 128 ? n : 128;
@@ -194,7 +195,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     mbar_init(&d_full[0], 1);
     mbar_init(&d_full[1], 1);
     mbar_init(&v_ready, 4);
-    mbar_init(&d_free, 8);
+    mbar_init(&d_free[0], 8);
+    mbar_init(&d_free[1], 8);
     mbar_init(&mma_done[0], 1);
     mbar_init(&mma_done[1], 1);
     fence_mbar_init();
@@ -295,7 +297,10 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           const int n = tokens(g);
           const uint64_t kd = smem_desc_sw128(slot_of(rk), lbo_k, 1024);
           const uint64_t vd = smem_desc_sw128(slot_of(rv), DA_ATOM, 1024);
-          if ((g > 0 && !got(&d_free, g - 1, 1119)) || !got(&full[rv.slot], rv.use, 1115)) break;
+          if ((g >= DBUF && !got(&d_free[g % DBUF], g / DBUF - 1, 1119)) ||
+              !got(&full[rv.slot], rv.use, 1115))
+            break;
+          const uint32_t dcol = tbase + DA_COL_D - 128u * (uint32_t)(g % DBUF);
 #pragma unroll 1
           for (int qt = 0; 32 * qt < n; ++qt, ++xn) {
             if (!got(&x_ready[xn & 1], xn >> 1, 1116)) {
@@ -310,9 +315,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
             if (lead) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {  // 16 tokens
-                mma_bf16_ss(tbase + DA_COL_D, x2 + 128u * i, v1 + 128u * i, id_d, (qt | i) > 0);
-                mma_bf16_ss(tbase + DA_COL_D, x1 + 128u * i, v1 + 128u * i, id_d, 1);
-                mma_bf16_ss(tbase + DA_COL_D, k1 + 128u * i, v1 + 128u * i, id_d, 1);
+                mma_bf16_ss(dcol, x2 + 128u * i, v1 + 128u * i, id_d, (qt | i) > 0);
+                mma_bf16_ss(dcol, x1 + 128u * i, v1 + 128u * i, id_d, 1);
+                mma_bf16_ss(dcol, k1 + 128u * i, v1 + 128u * i, id_d, 1);
               }
               mma_commit(&x_free[xn & 1]);
             }
@@ -637,13 +642,15 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       wait(&d_full[g & 1], g >> 1, 1144);
       __syncwarp();
       tc_fence_after();
+      const uint32_t dcol = tbase + lane_off + DA_COL_D - 128u * (uint32_t)(g % DBUF) +
+                            64u * (uint32_t)half;
       const float2 f = n == 128 ? whole : make_float2(power[n], 0.f);
       if (half < va) {
 #pragma unroll
         for (int c = 0; c < 4; c += 2) {
           uint32_t d[2][16];
-          tmem_ld16(tbase + lane_off + DA_COL_D + (uint32_t)(64 * half + 16 * c), d[0]);
-          tmem_ld16(tbase + lane_off + DA_COL_D + (uint32_t)(64 * half + 16 * c + 16), d[1]);
+          tmem_ld16(dcol + (uint32_t)(16 * c), d[0]);
+          tmem_ld16(dcol + (uint32_t)(16 * c + 16), d[1]);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
@@ -659,7 +666,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       }
       tc_fence_before();  // the next chunk's products may take D's columns
       __syncwarp();
-      if (lane == 0) mbar_arrive(&d_free);
+      if (lane == 0) mbar_arrive(&d_free[g % DBUF]);
       if (!LOCAL && g + 1 < chunks) {
         wait(&qs_full, g, 1145);  // Q S has read the tile
         __syncwarp();
