@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_arrive();  // this block's shared memory is there
   const int64_t b = blockIdx.x / NC;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int NT = (a.V + TASK - 1) / TASK;
+  const int NT = (a.V - 1) / TASK + 1;
   // nothing yet
   for (int i = tid; i < K * kWarps * n; i += kThreads) keys[i] = 0;
   for (int i = tid; i < K * kWarps; i += kThreads) {

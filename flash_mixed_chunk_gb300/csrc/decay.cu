@@ -180,10 +180,10 @@ __global__ void __launch_bounds__(kThreads)
         const float4 x0 = at4(sw + 2 * ty * WS + j), x1 = at4(sw + (2 * ty + 1) * WS + j);
         const float *p0 = &x0.x, *p1 = &x1.x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {  // (a weight of 0 would not keep an infinity or a NaN out)
           const float4 y = at4(sv + (j + i) * VS + 4 * tx);
-          fma4(p0[i], y, near[0]);
-          fma4(p1[i], y, near[1]);
+          if (j + i <= 2 * ty) fma4(p0[i], y, near[0]);
+          if (j + i <= 2 * ty + 1) fma4(p1[i], y, near[1]);
         }
       }
 #pragma unroll 2

@@ -25,7 +25,7 @@
 // launch (LOCAL) forms only the segments' states, a second starts every segment from
 // the sum of those before it.
 //
-// Warps (768 threads): 0 TMA, 1 and 3 MMA issuers, 2 output stores; 4-11 P and the outputs; 12-15
+// Warps (768 threads): 0 TMA, 1 and 3 MMA issuers, 2 a look at v and the output stores; 4-11 P and the outputs; 12-15
 // K~'s terms, from K in place (the first term) and through two buffers of 32 tokens (the
 // others); 16-23 the state, from D in TMEM, and its bf16 copy in shared memory.  P takes
 // the columns of the scores that its own warp has read, of one of two buffers.
@@ -114,6 +114,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
+// Two bf16 times 0, plus `sum`: 0 until one is infinite or a NaN.
+__device__ __forceinline__ uint32_t zero_unless_wild(uint32_t x, uint32_t sum) {
+  uint32_t y;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0u), "r"(sum));
+  return y;
+}
+
 // Two keys times w as three bf16 terms.
 __device__ __forceinline__ void key_terms(uint32_t k, float2 w, uint32_t &t0, uint32_t &t1,
                                           uint32_t &t2) {
@@ -141,11 +148,13 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   __shared__ __align__(8) uint64_t full[DA_SLOTS], empty[DA_SLOTS], x_ready[2], x_free[2];
   __shared__ __align__(8) uint64_t staged[2], stored[2];
   __shared__ __align__(8) uint64_t sc_full[2], qs_full, p_ready, o_full, o_free, s_ready, d_full[2],
-      d_free[2], v_ready, mma_done[2];
+      d_free[2], v_ready[2], mma_done[2];
   __shared__ __align__(16) float back[16];  // lam^(15 - j)
   __shared__ float power[129];              // lam^j
   __shared__ float from[64];                // the segments' powers at this one's start
   __shared__ float2 whole_s;                // lam^128
+  // whether a chunk's v holds a value that is not finite, and each column's first such row
+  __shared__ uint8_t wild[2], wild_row[2][128];
   __shared__ uint32_t tmem_base;
 
   // (the same in all of a warp's lanes, for the compiler too: the products' operands then
@@ -194,7 +203,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     mbar_init(&s_ready, 8);
     mbar_init(&d_full[0], 1);
     mbar_init(&d_full[1], 1);
-    mbar_init(&v_ready, 4);
+    mbar_init(&v_ready[0], 5);
+    mbar_init(&v_ready[1], 5);
     mbar_init(&d_free[0], 8);
     mbar_init(&d_free[1], 8);
     mbar_init(&mma_done[0], 1);
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
               mma_commit(&empty[cq.slot]);
             }
             cq.step(0, rings.q);
-            if (!got(&p_ready, g, 1117) || !got(&v_ready, g, 1112)) break;
+            if (!got(&p_ready, g, 1117) || !got(&v_ready[g & 1], g >> 1, 1112)) break;
             tc_fence_after();
             const uint32_t pc = tbase + DA_COL_SC + 128u * (uint32_t)(g & 1);
             const uint64_t vd = smem_desc_sw128(slot_of(rv), DA_ATOM, 1024);
@@ -392,25 +402,76 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         got(&mma_done[1], 0, 1118);
       }
     }
-    if (!LOCAL && warp == 2 && lane == 0) {
-      // =========================== output stores
-      RingAt rv(v0s);
-      bool ok = true;
-      for (int g = 0; ok && g < chunks; ++g, rv.step(v0s, rings.v)) {
-        if (!da_wait(&staged[g & 1], g >> 1)) {
-          record_timeout(1150);
-          ok = false;
-          break;
+    if (!LOCAL && warp == 2) {
+      // =========================== a look at v a chunk ahead, and output stores
+      // A weight of 0 keeps no infinity or NaN of a later token out of a row's sum.  So v is
+      // looked through; where it holds one, it is taken out once the state's product has had
+      // it, and the rows from there on become NaN.
+      RingAt rv(v0s), ro(v0s);
+      const auto got = [&](uint64_t *bar, int use, int code) {
+        if (__all_sync(0xFFFFFFFFu, da_wait(bar, use))) return true;
+        if (lane == 0) record_timeout(code);
+        return false;
+      };
+#pragma unroll 1
+      for (int g = -1; g < chunks; ++g) {
+        if (g + 1 < chunks) {
+          if (!got(&full[rv.slot], rv.use, 1151)) break;
+          uint8_t *const v = smem + rv.slot * slot_bytes;
+          const int n = tokens(g + 1), buf = (g + 1) & 1;
+          uint32_t zero[4] = {};
+          for (int x = 0; x < va; ++x)
+#pragma unroll 8
+            for (int i = lane; i < 8 * n; i += 32) {
+              const uint4 y = *reinterpret_cast<const uint4 *>(v + x * DA_ATOM + 16 * i);
+              zero[0] = zero_unless_wild(y.x, zero[0]);
+              zero[1] = zero_unless_wild(y.y, zero[1]);
+              zero[2] = zero_unless_wild(y.z, zero[2]);
+              zero[3] = zero_unless_wild(y.w, zero[3]);
+            }
+          const bool any = __any_sync(
+              0xFFFFFFFFu, ((zero[0] | zero[1] | zero[2] | zero[3]) & 0x7FFF7FFFu) != 0u);
+          if (any) {
+            if (!got(&d_full[buf], (g + 1) >> 1, 1152)) break;
+#pragma unroll 1
+            for (int x = 0; x < va; ++x) {  // two columns a lane
+              int at[2] = {128, 128};
+#pragma unroll 1
+              for (int i = 0; i < n; ++i) {
+                uint32_t *const p =
+                    reinterpret_cast<uint32_t *>(v + x * DA_ATOM + sw128_offset(i, 4u * lane));
+                const uint32_t y = *p;
+                const bool lo = (y & 0x7F80u) == 0x7F80u, hi = (y & 0x7F800000u) == 0x7F800000u;
+                if (lo && at[0] > i) at[0] = i;
+                if (hi && at[1] > i) at[1] = i;
+                if (lo || hi) *p = y & (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
+              }
+              wild_row[buf][64 * x + 2 * lane] = (uint8_t)at[0];
+              wild_row[buf][64 * x + 2 * lane + 1] = (uint8_t)at[1];
+            }
+            fence_proxy_async_smem();
+          }
+          if (lane == 0) wild[buf] = any;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_ready[buf]);
+          rv.step(v0s, rings.v);
         }
-        for (int x = 0; x < va; ++x)
-          tma_store_4d(&mapO, smem + rv.slot * slot_bytes + x * DA_ATOM, v0 + 64 * x, w.h,
-                       w.t0 + 128 * g, w.b);
-        bulk_commit_group();
-        bulk_wait_group_read<0>();
-        mbar_arrive(&empty[rv.slot]);
-        mbar_arrive(&stored[g & 1]);
+        if (g >= 0) {
+          if (!got(&staged[g & 1], g >> 1, 1150)) break;
+          if (lane == 0) {
+            for (int x = 0; x < va; ++x)
+              tma_store_4d(&mapO, smem + ro.slot * slot_bytes + x * DA_ATOM, v0 + 64 * x, w.h,
+                           w.t0 + 128 * g, w.b);
+            bulk_commit_group();
+            bulk_wait_group_read<0>();
+            mbar_arrive(&empty[ro.slot]);
+            mbar_arrive(&stored[g & 1]);
+          }
+          __syncwarp();
+          ro.step(v0s, rings.v);
+        }
       }
-      bulk_wait_group<0>();
+      if (lane == 0) bulk_wait_group<0>();
     }
   } else if (!LOCAL && warp < DA_KEY_WARP) {
     // =========================== P and the outputs: a row and 64 columns a thread
@@ -484,6 +545,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       __syncwarp();
       tc_fence_after();
       wait(&d_full[g & 1], g >> 1, 1132);  // D has read v too
+      wait(&v_ready[g & 1], g >> 1, 1133);
       if (g > 1) wait(&stored[g & 1], (g >> 1) - 1, 1131);
       // Through v's place in the ring, which its products have left, and out by TMA: 32-byte
       // stores from the registers hold the SM's other shared memory traffic up for 1800 of
@@ -506,6 +568,12 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4 *>(out + sw128_offset((uint32_t)row, 2u * c + 16u * j)) =
                 make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        }
+        if (wild[g & 1] != 0 && in) {
+#pragma unroll 1
+          for (int c = 0; c < 64; ++c)
+            if (row >= wild_row[g & 1][64 * half + c])
+              *reinterpret_cast<uint16_t *>(out + sw128_offset((uint32_t)row, 2u * c)) = 0x7FFFu;
         }
         fence_proxy_async_smem();
       }
@@ -542,7 +610,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (!LOCAL && lane == 0) mbar_arrive(&v_ready);
+      if (!LOCAL && lane == 0) mbar_arrive(&v_ready[g & 1]);
 #pragma unroll 1
       for (int qt = group; 32 * qt < n; qt += GROUPS, ++xn) {
         const int buf = LOCAL ? group : xn & 1, use = LOCAL ? xn : xn >> 1;

@@ -231,3 +231,68 @@ def test_lengths_change_under_a_captured_call():
         p, t = fm.decay_attention(q, k, v, ld, lengths=lengths)
         settled()
         assert torch.equal(o, p) and torch.equal(s, t)
+
+
+@pytest.mark.parametrize("dtype,T,dk,dv", [(BF16, 200, 64, 64), (BF16, 300, 128, 200),
+                                           (BF16, 2000, 16, 72), (F32, 150, 20, 70)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_values_that_are_not_finite_reach_no_earlier_row(dtype, T, dk, dv, bad):
+    """An infinity or NaN in a token's q, k or v reaches its own and later rows alone, one
+    in v its own column alone: all others are as without it, bit for bit."""
+    q, k, v = rand(2, T, 2, dk, dtype=dtype), rand(2, T, 2, dk, dtype=dtype, seed=1), \
+        rand(2, T, 2, dv, dtype=dtype, seed=2)
+    ld = torch.tensor([-0.02, -0.5]).cuda()
+    want, ws = fm.decay_attention(q, k, v, ld)
+    for t, c in ((T - 1, 0), (T // 2 + 3, dv - 1), (5, 9), (127, 33), (128, 63), (1, 15)):
+        x = v.clone()
+        x[0, t, 1, c] = bad
+        o, s = fm.decay_attention(q, k, x, ld)
+        settled()
+        hit = torch.zeros_like(o, dtype=torch.bool)
+        hit[0, t:, 1, c] = True
+        assert torch.equal(o[~hit], want[~hit])
+        assert not torch.isfinite(o[0, t, 1, c])
+        hit = torch.zeros_like(s, dtype=torch.bool)
+        hit[0, 1, :, c] = True
+        assert torch.equal(s[~hit], ws[~hit]) and not torch.isfinite(s[hit]).any()
+    # two columns and three rows of one, at once
+    x = v.clone()
+    x[0, 40, 0, 2], x[0, 60, 0, 2], x[1, 90, 1, 3], x[0, 50, 0, 3] = bad, 1.0, bad, bad
+    o, _ = fm.decay_attention(q, k, x, ld)
+    settled()
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[0, 40:, 0, 2] = hit[1, 90:, 1, 3] = hit[0, 50:, 0, 3] = hit[0, 60:, 0, 2] = True
+    assert torch.equal(o[~hit], want[~hit])
+    for t in (0, 77, 128, T - 1):
+        x = k.clone()
+        x[1, t, 0, dk - 1] = bad
+        o, s = fm.decay_attention(q, x, v, ld)
+        settled()
+        assert torch.equal(o[0], want[0]) and torch.equal(s[0], ws[0])
+        assert torch.equal(o[1, :, 1], want[1, :, 1])
+        assert torch.equal(o[1, :t, 0], want[1, :t, 0])
+        assert not torch.isfinite(o[1, t, 0]).any()
+        x = q.clone()
+        x[1, t, 0, 0] = bad
+        o, s = fm.decay_attention(x, k, v, ld)
+        settled()
+        rest = torch.ones_like(o, dtype=torch.bool)
+        rest[1, t, 0] = False
+        assert torch.equal(o[rest], want[rest]) and torch.equal(s, ws)
+
+
+def test_the_longest_row_of_logits():
+    V = 2 ** 31 - 1
+    z = torch.zeros(1, 1, V, dtype=BF16, device="cuda")
+    at = [V - 1, 2 ** 30 + 5, 3]
+    z[0, 0, at] = torch.tensor([9.0, 8.0, 8.0], dtype=BF16, device="cuda")
+    score, parent, token = fm.beam_select(z, torch.zeros(1, 1, device="cuda"), 4)
+    settled()
+    assert token.tolist() == [[V - 1, 3, 2 ** 30 + 5, 0]] and not parent.any()
+    lse = math.log(V - 3 + math.exp(9.0) + 2 * math.exp(8.0))
+    # a sum of V equal terms of 1 by lanes, warps and blocks: 32 lanes' and 32 places' sums
+    # are exact up to 2^24, what is added to them late loses at most half a step of 2^31 / 2^24
+    # each (2^-24 of it), over V / 1024 / 8 / 8 turns of a warp of 64
+    turns = V / 1024 / 64
+    got = torch.tensor([9.0, 8.0, 8.0, 0.0], dtype=torch.float64) - lse
+    assert ((score[0].cpu().double() - got).abs() <= (turns + 70) * 2.0 ** -24 + 2.0 ** -19).all()
