@@ -114,11 +114,30 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// Two bf16 times 0, plus `sum`: 0 until one is infinite or a NaN.
-__device__ __forceinline__ uint32_t zero_unless_wild(uint32_t x, uint32_t sum) {
-  uint32_t y;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0u), "r"(sum));
-  return y;
+// Two products of bf16, plus `sum`: finite only if all are.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t x, uint32_t y, uint32_t sum) {
+  uint32_t z;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(z) : "r"(x), "r"(y), "r"(sum));
+  return z;
+}
+__device__ __forceinline__ bool wild_lo(uint32_t x) { return (x & 0x7F80u) == 0x7F80u; }
+__device__ __forceinline__ bool wild_hi(uint32_t x) { return (x & 0x7F800000u) == 0x7F800000u; }
+
+// By one warp: what is not finite in a tile of n rows of 64 columns becomes 0, and
+// row[0 .. 63] each column's first row with such a value (128: none).
+__device__ __noinline__ void tame(uint8_t *tile, int n, uint8_t *row, int lane) {
+  int at[2] = {128, 128};
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    uint32_t *const p = reinterpret_cast<uint32_t *>(tile + sw128_offset(i, 4u * lane));
+    const uint32_t y = *p;
+    const bool lo = wild_lo(y), hi = wild_hi(y);
+    if (lo && at[0] > i) at[0] = i;
+    if (hi && at[1] > i) at[1] = i;
+    if (lo || hi) *p = y & (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
+  }
+  row[2 * lane] = (uint8_t)at[0];
+  row[2 * lane + 1] = (uint8_t)at[1];
 }
 
 // Two keys times w as three bf16 terms.
@@ -419,36 +438,26 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           if (!got(&full[rv.slot], rv.use, 1151)) break;
           uint8_t *const v = smem + rv.slot * slot_bytes;
           const int n = tokens(g + 1), buf = (g + 1) & 1;
-          uint32_t zero[4] = {};
-          for (int x = 0; x < va; ++x)
-#pragma unroll 8
-            for (int i = lane; i < 8 * n; i += 32) {
-              const uint4 y = *reinterpret_cast<const uint4 *>(v + x * DA_ATOM + 16 * i);
-              zero[0] = zero_unless_wild(y.x, zero[0]);
-              zero[1] = zero_unless_wild(y.y, zero[1]);
-              zero[2] = zero_unless_wild(y.z, zero[2]);
-              zero[3] = zero_unless_wild(y.w, zero[3]);
+          uint32_t sum[2] = {};
+          const uint8_t *p = v + 16 * lane;
+#pragma unroll 1
+          for (int i = 0; i < 4 * va; ++i, p += DA_ATOM / 4) {  // 32 rows of 64 columns
+            const int left = (n - 32 * (i & 3)) * 8 - lane;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint4 y = make_uint4(0u, 0u, 0u, 0u);
+              if (32 * j < left) y = *reinterpret_cast<const uint4 *>(p + 512 * j);
+              sum[0] = fma_bf16x2(y.x, y.y, sum[0]);
+              sum[1] = fma_bf16x2(y.z, y.w, sum[1]);
             }
-          const bool any = __any_sync(
-              0xFFFFFFFFu, ((zero[0] | zero[1] | zero[2] | zero[3]) & 0x7FFF7FFFu) != 0u);
+          }
+          // (or values whose products overflow: then there is nothing to take out)
+          const bool any = __any_sync(0xFFFFFFFFu, wild_lo(sum[0]) || wild_hi(sum[0]) ||
+                                                       wild_lo(sum[1]) || wild_hi(sum[1]));
           if (any) {
             if (!got(&d_full[buf], (g + 1) >> 1, 1152)) break;
 #pragma unroll 1
-            for (int x = 0; x < va; ++x) {  // two columns a lane
-              int at[2] = {128, 128};
-#pragma unroll 1
-              for (int i = 0; i < n; ++i) {
-                uint32_t *const p =
-                    reinterpret_cast<uint32_t *>(v + x * DA_ATOM + sw128_offset(i, 4u * lane));
-                const uint32_t y = *p;
-                const bool lo = (y & 0x7F80u) == 0x7F80u, hi = (y & 0x7F800000u) == 0x7F800000u;
-                if (lo && at[0] > i) at[0] = i;
-                if (hi && at[1] > i) at[1] = i;
-                if (lo || hi) *p = y & (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
-              }
-              wild_row[buf][64 * x + 2 * lane] = (uint8_t)at[0];
-              wild_row[buf][64 * x + 2 * lane + 1] = (uint8_t)at[1];
-            }
+            for (int x = 0; x < va; ++x) tame(v + x * DA_ATOM, n, &wild_row[buf][64 * x], lane);
             fence_proxy_async_smem();
           }
           if (lane == 0) wild[buf] = any;
@@ -541,11 +550,12 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_ready);
 
+      wait(&v_ready[g & 1], g >> 1, 1133);
+      const bool odd = wild[g & 1] != 0;
       wait(&o_full, g, 1130);
       __syncwarp();
       tc_fence_after();
       wait(&d_full[g & 1], g >> 1, 1132);  // D has read v too
-      wait(&v_ready[g & 1], g >> 1, 1133);
       if (g > 1) wait(&stored[g & 1], (g >> 1) - 1, 1131);
       // Through v's place in the ring, which its products have left, and out by TMA: 32-byte
       // stores from the registers hold the SM's other shared memory traffic up for 1800 of
@@ -569,7 +579,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
             *reinterpret_cast<uint4 *>(out + sw128_offset((uint32_t)row, 2u * c + 16u * j)) =
                 make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
         }
-        if (wild[g & 1] != 0 && in) {
+        if (odd && in) {
 #pragma unroll 1
           for (int c = 0; c < 64; ++c)
             if (row >= wild_row[g & 1][64 * half + c])
