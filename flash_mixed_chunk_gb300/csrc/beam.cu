@@ -358,7 +358,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         const int count = __shfl_sync(kAll, before, 31);
         before -= __popc(mask);
-        if (count <= 6) {  // one by one into their places
+        // one by one into their places: of a row that has been under way for long only a few
+        // get this far (64 x 8 beams of 32000 take 24.6 us, and 26.4 sorting them always)
+        if (count <= 6) {
           uint64_t mine = pop();
           for (unsigned act; (act = __ballot_sync(kAll, mine != 0)) != 0;) {
             const int from = __ffs(act) - 1;
@@ -538,12 +540,13 @@ int launch_beam_select(const void *logits, int64_t row, const float *scores,
                        int B, int K, int V, int n, int pad, int bf16, cudaStream_t stream) {
   SelectArgs a{logits, row, scores, finished, score, parent, token, K, V, n, pad, 0};
   // a beam's row has NT warps' work; as many blocks as run at once (two an SM), no more
-  // than have any
+  // than have any.  (One element of 4 beams of 32000: 10.0 us on 8 blocks, 20.7 on one.)
   const int64_t NT = ((int64_t)V + TASK - 1) / TASK;
   int NC = 1;
   while (NC < kBeamCluster && (int64_t)B * 2 * NC <= 2 * 152 && NC * kWarps < NT * K) NC *= 2;
   // warps that share a beam: a warp's first task of a row costs about twice the others'
-  // (its list begins)
+  // (its list begins).  64 x 8 beams of 32000: 24.6 us; 51.9 with one warp a beam, 35.7 with
+  // all of a cluster's warps on every beam.  1 x 32 of 50000: 59.9; 86 and 178.
   int64_t least = INT64_MAX;
   for (int group = 1; group <= NC * kWarps; group *= 2) {
     const int64_t groups = NC * kWarps / group;
@@ -555,7 +558,7 @@ int launch_beam_select(const void *logits, int64_t row, const float *scores,
   const auto fits = [&](int bytes) {
     return at % bytes == 0 && ((int64_t)V * el) % bytes == 0 && (row * el) % bytes == 0;
   };
-  if (bf16) {
+  if (bf16) {  // (64 x 8 beams of 32000: 24.6 us by 16 bytes, 25.4 by 4)
     if (fits(16)) return select<__nv_bfloat16, 16>(a, B, NC, stream);
     if (fits(4)) return select<__nv_bfloat16, 4>(a, B, NC, stream);
     return select<__nv_bfloat16, 2>(a, B, NC, stream);

@@ -340,7 +340,8 @@ int step(const DecayArgs &a, float *state, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)blocks(32));
     return cudaLaunchKernelEx(&cfg, decay_step<T, 1, 32>, a, state) == cudaSuccess ? 0 : 1;
   }
-  // the widest rows that leave two blocks an SM
+  // the widest rows that leave two blocks an SM (whole lines: 64 sequences of 16 heads of 128
+  // take 21.6 us with 128 columns a block, 23.5 with 32)
   auto *kern = decay_step<T, 4, 32>;
   int W = 128;
   if (blocks(128) < 2 * kDecaySms) kern = decay_step<T, 4, 16>, W = 64;

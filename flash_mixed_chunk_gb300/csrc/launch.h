@@ -441,7 +441,9 @@ struct DecayArgs {
 struct DecaySplit {
   int S, L, nvt;
 };
-// CUDA cores: about two units an SM, segments of 64 tokens at least and 64 at most.
+// CUDA cores: two blocks fit an SM, and there are as many segments as make so many units, of
+// 64 tokens at least (a segment's start costs about as much) and 64 of them at most.  3 x 517 tokens, 6 heads, dk 33: 31 us; 36 with segments for one
+// block an SM, 82 uncut.
 inline DecaySplit decay_split_simt(int B, int T, int H, int dv) {
   const int nvt = (dv + 63) / 64;
   const int64_t heads = (int64_t)B * H * nvt;
@@ -458,6 +460,9 @@ inline size_t decay_bytes_simt(int B, int T, int H, int dk, int dv) {
 // Tensor cores: tiles of 128 columns, chunks of 128 tokens; a slot of the workspace
 // holds a unit's state of 128 x 128.
 constexpr size_t kDecaySlot = 128 * 128;
+// What the maps of its loads take, and its shared memory (dk <= 128).  It is the faster one
+// from single tokens on: 12 heads of 64, 1 token 7.1 us against 7.8, 37 tokens 7.3 against 13.4,
+// 512 tokens 16 against 40; 2 x 8192 63 against 349.
 inline bool decay_tc(const DecayArgs &a) {
   if (!a.bf16 || a.dk % 8 || a.dv % 8 || a.dk > 128) return false;
   const auto fits = [](const void *p, const int64_t *s, int B, int T, int heads) {
@@ -469,8 +474,10 @@ inline bool decay_tc(const DecayArgs &a) {
   return fits(a.q, a.qs, a.B, a.T, a.Hq) && fits(a.k, a.ks, a.B, a.T, a.Hk) &&
          fits(a.v, a.vs, a.B, a.T, a.Hv) && reinterpret_cast<uintptr_t>(a.o) % 16 == 0;
 }
-// As many segments as make the two launches shortest, a chunk of the first (k and v
-// alone) counted as half of one of the second, a launch's start as three.
+// As many segments as make the two launches shortest, counted in halves of a chunk of the
+// second launch: a chunk of the first one (k and v alone) is one, its start four, the second's
+// start six.  12 heads of 128: 512 tokens in 4 segments 17.7 us, uncut 23.4; 1024 in 8 22.3 and
+// 38.3; 256 uncut 16.0, in two 15.8.  24 heads, 2 x 8192 tokens of 64 in 6 63, uncut 182.
 inline DecaySplit decay_split_tc(int B, int T, int H, int dv) {
   const int nvt = (dv + 127) / 128;
   const int64_t heads = (int64_t)B * H * nvt, chunks = ((int64_t)T + 127) / 128;
@@ -478,7 +485,7 @@ inline DecaySplit decay_split_tc(int B, int T, int H, int dv) {
   int64_t best = 1, least = 2 * waves(heads) * (chunks + 3);
   for (int64_t S = 2; S <= chunks && S <= 64 && heads * S < 4 * kDecaySms; ++S) {
     const int64_t L = (chunks + S - 1) / S;
-    const int64_t cost = waves(heads * (S - 1)) * (L + 6) + 2 * waves(heads * S) * (L + 3);
+    const int64_t cost = waves(heads * (S - 1)) * (L + 4) + 2 * waves(heads * S) * (L + 3);
     if (cost < least) least = cost, best = S;
   }
   const int64_t L = (chunks + best - 1) / best * 128;
