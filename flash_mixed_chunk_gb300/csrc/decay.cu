@@ -340,12 +340,12 @@ int step(const DecayArgs &a, float *state, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)blocks(32));
     return cudaLaunchKernelEx(&cfg, decay_step<T, 1, 32>, a, state) == cudaSuccess ? 0 : 1;
   }
-  // the widest rows that leave two blocks an SM (whole lines: 64 sequences of 16 heads of 128
-  // take 21.6 us with 128 columns a block, 23.5 with 32)
-  auto *kern = decay_step<T, 4, 32>;
-  int W = 128;
-  if (blocks(128) < 2 * kDecaySms) kern = decay_step<T, 4, 16>, W = 64;
-  if (blocks(64) < 2 * kDecaySms) kern = decay_step<T, 4, 8>, W = 32;
+  // 64 columns a block, two lines of every row; 32 where fewer than an SM's worth of blocks
+  // would do so.  64 sequences of 12 heads of 128: 16.5 us, with 32 columns 17.9, with 128 17.3;
+  // 16 sequences 5.7, 6.5, 6.2; 2 sequences (24 blocks) 2.9, with 32 2.55, with 128 3.9.
+  auto *kern = decay_step<T, 4, 16>;
+  int W = 64;
+  if (blocks(64) < kDecaySms) kern = decay_step<T, 4, 8>, W = 32;
   cfg.gridDim = dim3((unsigned)blocks(W));
   return cudaLaunchKernelEx(&cfg, kern, a, state) == cudaSuccess ? 0 : 1;
 }
