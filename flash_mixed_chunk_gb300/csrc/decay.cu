@@ -40,18 +40,8 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 
 // ------------------------------------------------------------------- prompts
 
-// dk in whole float4s (zeros behind it), and a row of q or k: an odd number of float4s,
-// so that the rows that eight threads read at once lie in different banks.
-__host__ __device__ constexpr int padded(int dk) { return (dk + 3) / 4 * 4; }
-__host__ __device__ constexpr int row_of(int dk) {
-  return padded(dk) + (padded(dk) / 4 % 2 ? 8 : 4);
-}
 constexpr int WS = C + 4;  // row of the weights
-// Shared memory, in floats: q and k [C][row_of(dk)], v [C][VS], the state
-// [padded(dk)][DVT], the chunk's weights [C][WS], the powers 0 .. C.
-__host__ __device__ constexpr int prompt_floats(int dk) {
-  return 2 * C * row_of(dk) + C * VS + padded(dk) * DVT + C * WS + C + 4;
-}
+static_assert(C == 32 && VS == 68 && WS == 36, "decay_floats counts these");
 __device__ __forceinline__ float4 &at4(float *p) { return *reinterpret_cast<float4 *>(p); }
 __device__ __forceinline__ void fma4(float x, const float4 &y, float4 &z) {
   z.x = fmaf(x, y.x, z.x), z.y = fmaf(x, y.y, z.y);
@@ -62,12 +52,12 @@ __device__ __forceinline__ void fma4(float x, const float4 &y, float4 &z) {
 // slots 1 .. S-1 of the workspace (segment 0 starts from the carried state, a copy
 // of which goes to slot 0: the second launch may overwrite it in place).
 template <typename T, bool LOCAL>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     decay_prompt(const __grid_constant__ DecayArgs a, const DecaySplit sp,
                  float *__restrict__ slots) {
   extern __shared__ float4 smem4[];
   float *sm = reinterpret_cast<float *>(smem4);
-  const int dk = a.dk, dkp = padded(dk), ks = row_of(dk);
+  const int dk = a.dk, dkp = decay_dk4(dk), ks = decay_row(dk);
   float *sq = sm, *sk = sq + C * ks, *sv = sk + C * ks, *st = sv + C * VS;
   float *sw = st + dkp * DVT, *pw = sw + C * WS;
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
@@ -352,11 +342,11 @@ int step(const DecayArgs &a, float *state, cudaStream_t stream) {
 
 template <typename T>
 int prompt(const DecayArgs &a, float *slots, cudaStream_t stream) {
-  const DecaySplit sp = decay_split_simt(a.B, a.T, a.H, a.dv);
-  const size_t smem = sizeof(float) * (size_t)prompt_floats(a.dk);
+  const DecaySplit sp = decay_split_simt(a.B, a.T, a.H, a.dk, a.dv);
+  const size_t smem = sizeof(float) * (size_t)decay_floats(a.dk);
   static OncePerDevice attrs;
   if (!attrs.run([] {
-        const int most = (int)sizeof(float) * prompt_floats(kDecayMaxK);
+        const int most = (int)sizeof(float) * decay_floats(kDecayMaxK);
         return cudaFuncSetAttribute(decay_prompt<T, true>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     most) == cudaSuccess &&

@@ -441,20 +441,33 @@ struct DecayArgs {
 struct DecaySplit {
   int S, L, nvt;
 };
-// CUDA cores: two blocks fit an SM, and there are as many segments as make so many units, of
-// 64 tokens at least (a segment's start costs about as much) and 64 of them at most.  3 x 517 tokens, 6 heads, dk 33: 31 us; 36 with segments for one
-// block an SM, 82 uncut.
-inline DecaySplit decay_split_simt(int B, int T, int H, int dv) {
+// CUDA cores: chunks of 32 tokens, tiles of 64 columns of dv.  Shared memory, in floats: q
+// and k [32][row], v [32][68], the state [dk in whole float4s][64], the chunk's weights
+// [32][36], the powers 0 .. 32.  A row of q or k is an odd number of float4s, so that the
+// rows that eight threads read at once lie in different banks.
+__host__ __device__ constexpr int decay_dk4(int dk) { return (dk + 3) / 4 * 4; }
+__host__ __device__ constexpr int decay_row(int dk) { return decay_dk4(dk) + (decay_dk4(dk) / 4 % 2 ? 8 : 4); }
+__host__ __device__ constexpr int decay_floats(int dk) {
+  return 2 * 32 * decay_row(dk) + 32 * 68 + decay_dk4(dk) * 64 + 32 * 36 + 32 + 4;
+}
+// As many segments as fill the blocks that the SMs hold (three each, or what their shared
+// memory has room for), of 64 tokens at least (a segment's start costs about as much) and 64
+// of them at most.  16-bit 2 x 8192 tokens, 12 heads of 33 x 65: 394 us, 500 with two blocks an
+// SM; 1 x 4000, 8 heads of 200 x 150, where one fits: 572 us, 710 cut for three; 3 x 517, 6
+// heads of 33, uncut: 82 us for 31.
+inline DecaySplit decay_split_simt(int B, int T, int H, int dk, int dv) {
   const int nvt = (dv + 63) / 64;
   const int64_t heads = (int64_t)B * H * nvt;
-  int64_t S = heads < 2 * kDecaySms ? 2 * kDecaySms / heads : 1;
+  const int fit = 232448 / (4 * decay_floats(dk) + 2048);
+  const int64_t room = (int64_t)(fit < 3 ? fit : 3) * kDecaySms;
+  int64_t S = heads < room ? room / heads : 1;
   const int64_t most = ((int64_t)T + 63) / 64 < 64 ? ((int64_t)T + 63) / 64 : 64;
   S = S < most ? S : most;
   const int64_t L = ((T + S - 1) / S + 31) / 32 * 32;
   return DecaySplit{(int)((T + L - 1) / L), (int)L, nvt};
 }
 inline size_t decay_bytes_simt(int B, int T, int H, int dk, int dv) {
-  const DecaySplit sp = decay_split_simt(B, T, H, dv);
+  const DecaySplit sp = decay_split_simt(B, T, H, dk, dv);
   return sp.S > 1 ? align256(sizeof(float) * (size_t)B * H * sp.nvt * sp.S * (size_t)dk * 64) : 0;
 }
 // Tensor cores: tiles of 128 columns, chunks of 128 tokens; a slot of the workspace
