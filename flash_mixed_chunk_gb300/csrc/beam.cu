@@ -16,10 +16,18 @@
 // Rows of one call are cut the same way, so that equal rows give equal sums and the
 // tie goes to the lower beam.
 //
+// Measured: one element, 4 beams of 32000 in bf16, 10.0 us (2 of the launch, the rest a chain:
+// a row's part, the lists of a block, of the cluster, of the beams); 64 x 8 of 50001 in fp32,
+// 16 candidates, a fifth finished, 37 us, 82 MB at 2.2 TB/s (33 % of a copy's rate): an SM
+// issues in half of its cycles, about 30 instructions a logit: 11 to load, compare and sum it,
+// the others for the lists, which a warp of 12 parts of a row changes in most of them.  Longer
+// rows pay less of that: 64 x 8 of 32000 in bf16 by 16 bytes 24.6 us.
+//
 // beam_reorder: rows of up to 16 arrays, t[b, k] = t[b, parent[b, k]] in place, one
 // launch.  A thread holds its bytes of every beam that changes in registers before
 // it writes the first: no second buffer, and beams that stay are neither read (but
-// as somebody's parent) nor written.
+// as somebody's parent) nor written.  Bound by the bytes: 64 rows of 4.7 MB, 448 MB read
+// and written, in 67 us: 6.7 TB/s, a copy's rate.
 //
 // Both are programmatic dependents of what runs ahead of them on the stream and wait
 // for it before they read or write.
@@ -38,7 +46,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int E = 32;           // logits of a lane
+constexpr int E = 32;           // logits of a lane (in registers twice: these and the next)
 constexpr int TASK = 32 * E;    // of a warp at a time
 constexpr int kPool = 256;      // keys that a warp gathers before it sorts them
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -444,7 +452,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         list_at[(warp - half) * 32 + lane] = where;
       }
       __syncthreads();
-      if (warp < half) merge_pairs(best, where, list_c[warp * 32 + lane], list_at[warp * 32 + lane], lane);
+      if (warp < half)
+        merge_pairs(best, where, list_c[warp * 32 + lane], list_at[warp * 32 + lane], lane);
     }
     if (warp == 0) {
       if (best != 0 && lane < n) {

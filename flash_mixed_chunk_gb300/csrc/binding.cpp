@@ -619,7 +619,8 @@ PyMethodDef kMethods[] = {
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding",
-                       "Wrappers of the training operators and of generation with states.", -1, kMethods};
+                       "Wrappers of the training operators and of generation with states.", -1,
+                       kMethods};
 
 }  // namespace
 

@@ -25,10 +25,23 @@
 // launch (LOCAL) forms only the segments' states, a second starts every segment from
 // the sum of those before it.
 //
-// Warps (768 threads): 0 TMA, 1 and 3 MMA issuers, 2 a look at v and the output stores; 4-11 P and the outputs; 12-15
-// K~'s terms, from K in place (the first term) and through two buffers of 32 tokens (the
-// others); 16-23 the state, from D in TMEM, and its bf16 copy in shared memory.  P takes
-// the columns of the scores that its own warp has read, of one of two buffers.
+// Warps (768 threads): 0 TMA, 1 and 3 MMA issuers, 2 a look at v and the output stores; 4-11 P
+// and the outputs; 12-15 K~'s terms, from K in place (the first term) and through two buffers
+// of 32 tokens (the others); 16-23 the state, from D in TMEM, and its bf16 copy in shared
+// memory.  P takes the columns of the scores that its own warp has read, of one of two
+// buffers.
+//
+// Measured: 2 x 8192 tokens of 12 heads of 128 81 us (201 MB: 2.5 TB/s, 38 % of a copy's rate;
+// under a profiler the states' launch 31 and the outputs' 61), 1 x 32768 of 16 191 us, 8 x
+// 1024 of 12 heads with one q and k 43 us, 37 tokens 7.1 us.  Not bound by memory (the same
+// from L2) nor by the products (the pipe is busy 26 % of the time): a chunk of the outputs'
+// launch takes about 3.8 us on an SM, in which the state goes once around (D, the sum in
+// registers, its bf16 copy, Q S) while 24 warps pass the tiles through shared memory: keys
+// read, three terms written, v looked at, the weights and both accumulators through registers.
+// Around them are 9 us: the start, the first copies, the last outputs.  So the cut: whole
+// heads of 128 columns, one unit an SM, as many segments as there are SMs, though k and v of
+// all but the last are read twice. Chunks of 128: the products' tile; the weights' work grows
+// with the chunk, the state's with the number of them, and at 128 x 128 x 128 they are equal.
 #pragma once
 
 #include "decay.cuh"
@@ -76,7 +89,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// A wait with a limit of turns (each suspends the thread for a while; about a second in
+// A wait with a limit of turns (each suspends the thread for up to a microsecond; seconds in
 // all), without a look at the clock: the roles' loops of a chunk share the instruction
 // caches, and what is not in a warp's nearest one costs it more than its products.
 __device__ __forceinline__ bool da_wait(uint64_t *bar, int use) {
@@ -424,8 +437,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     if (!LOCAL && warp == 2) {
       // =========================== a look at v a chunk ahead, and output stores
       // A weight of 0 keeps no infinity or NaN of a later token out of a row's sum.  So v is
-      // looked through; where it holds one, it is taken out once the state's product has had
-      // it, and the rows from there on become NaN.
+      // looked through (5 % of a chunk's time, by the reads of shared memory); where it holds
+      // one, it is taken out once the state's product has had it, and the rows from there on
+      // become NaN.
       RingAt rv(v0s), ro(v0s);
       const auto got = [&](uint64_t *bar, int use, int code) {
         if (__all_sync(0xFFFFFFFFu, da_wait(bar, use))) return true;
@@ -521,7 +535,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {  // (a power with an exponent below 0 is dropped)
             const float x = __uint_as_float(r[j]) * (a.scale * exp2_fast(rf * (float)(gap - j)));
-            const float y = __uint_as_float(r[j + 1]) * (a.scale * exp2_fast(rf * (float)(gap - j - 1)));
+            const float y =
+                __uint_as_float(r[j + 1]) * (a.scale * exp2_fast(rf * (float)(gap - j - 1)));
             p[j / 2] = pack_bf16x2(j <= gap ? x : 0.f, j < gap ? y : 0.f);
           }
         } else {
@@ -558,8 +573,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
       wait(&d_full[g & 1], g >> 1, 1132);  // D has read v too
       if (g > 1) wait(&stored[g & 1], (g >> 1) - 1, 1131);
       // Through v's place in the ring, which its products have left, and out by TMA: 32-byte
-      // stores from the registers hold the SM's other shared memory traffic up for 1800 of
-      // 10000 cycles a chunk.  Rows behind the end are zeros.
+      // stores from the registers hold the SM's other shared memory traffic up (for 1800 of the
+      // 10000 cycles that a chunk took with them).  Rows behind the end are zeros.
       const bool in = row < tokens(g);
       if (half < va) {
         uint8_t *const out = smem + rv.slot * slot_bytes + (uint32_t)half * DA_ATOM;
@@ -571,7 +586,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const uint32_t x = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            const uint32_t x =
+                pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
             r[j] = in ? x : 0u;
           }
 #pragma unroll

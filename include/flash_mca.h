@@ -498,10 +498,13 @@ fmca_status flash_mca_vocab_loss_backward(const void *X, const void *W, const in
  *            state_in NULL: zero; state_out NULL: not wanted, or state_in itself
  *   o        device [B][T][H][dv] of `dtype`, contiguous (a step: [B][H][dv])
  * States, sums and powers of the decay are held in 32 bits or more.  In a prompt of
- * FMCA_BF16 with dk and dv multiples of 8, dk <= 128 and strides (in elements) that
- * are multiples of 8, products run on the tensor cores: the weights of a chunk's
- * pairs of tokens and the state as an operand of its outputs are rounded to bf16,
- * the state itself is not.  Every other prompt runs in fp32 on the CUDA cores.
+ * FMCA_BF16 with dk and dv multiples of 8, dk <= 128, strides (in elements) that are
+ * multiples of 8 and not 0, and q, k, v and o aligned to 16 bytes, products run on the
+ * tensor cores: the weights of a chunk's pairs of tokens and the state as an operand of
+ * its outputs are rounded to bf16, the state itself is not.  Every other prompt runs
+ * in fp32 on the CUDA cores.  An infinity or NaN in a token's q, k or v reaches no
+ * earlier token's output, and one in v its own column alone; what it reaches is not
+ * finite, and may be NaN where the formula has an infinity.
  * Sizes: B, T, H >= 1; 1 <= dk <= 256; dv >= 1.  log_decay, lengths and states are
  * aligned to 4 bytes (states to 16 for a dv that is a multiple of 4), q, k, v and o
  * to their elements.  Outputs must not overlap inputs (but state_out state_in), the
