@@ -18,10 +18,10 @@
 //
 // Measured: one element, 4 beams of 32000 in bf16, 10.0 us (2 of the launch, the rest a chain:
 // a row's part, the lists of a block, of the cluster, of the beams); 64 x 8 of 50001 in fp32,
-// 16 candidates, a fifth finished, 37 us, 82 MB at 2.2 TB/s (33 % of a copy's rate): an SM
-// issues in half of its cycles, about 30 instructions a logit: 11 to load, compare and sum it,
-// the others for the lists, which a warp of 12 parts of a row changes in most of them.  Longer
-// rows pay less of that: 64 x 8 of 32000 in bf16 by 16 bytes 24.6 us.
+// 16 candidates, none finished, 34 us, 102 MB at 3.0 TB/s (45 % of a copy's rate): an SM with
+// work issues in half of its cycles, about 20 instructions a logit, half of them to load,
+// compare and sum it, half for the lists, which a warp of 12 parts of a row changes in most of
+// them; and 256 blocks do not spread evenly over 152 SMs.  64 x 8 of 32000 in bf16 23 us.
 //
 // beam_reorder: rows of up to 16 arrays, t[b, k] = t[b, parent[b, k]] in place, one
 // launch.  A thread holds its bytes of every beam that changes in registers before
@@ -49,6 +49,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int E = 32;           // logits of a lane (in registers twice: these and the next)
 constexpr int TASK = 32 * E;    // of a warp at a time
 constexpr int kPool = 256;      // keys that a warp gathers before it sorts them
+constexpr int kFew = 2;          // lanes that a warp goes through one by one
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -131,6 +132,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
   return m;
 }
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
 
 // The 32 largest of `count` lists of n keys, largest first each, `stride` keys apart:
 // short ones several at a time, as one sort of 32.
@@ -185,11 +191,16 @@ struct Task {
     __device__ Raw() {}
   } r[NV];
   __device__ __forceinline__ void load(const T *__restrict__ row, int V, int t, int lane) {
+    const int64_t first = (int64_t)t * TASK + lane * EV;
+    const raw_t *const p = reinterpret_cast<const raw_t *>(row + first);
+    if ((int64_t)(t + 1) * TASK <= V) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t at = (int64_t)t * TASK + (j * 32 + lane) * EV;
-      if (at < V) r[j].raw = __ldg(reinterpret_cast<const raw_t *>(row + at));
+      for (int j = 0; j < NV; ++j) r[j].raw = __ldg(p + j * 32);
+      return;
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (first + j * 32 * EV < V) r[j].raw = __ldg(p + j * 32);
   }
   // -inf behind the row's end
   __device__ __forceinline__ void get(int V, int t, int lane, float (&z)[E]) const {
@@ -307,9 +318,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         task.get(a.V, t, lane, z);
         // the next ones are on their way while these are gone through
         if (t + a.group < NT) task.load(row, a.V, t + a.group, lane);
-        float top = z[0];
+        float top = max_nan(z[0], z[1]);
 #pragma unroll
-        for (int i = 1; i < E; ++i) top = max_nan(top, z[i]);
+        for (int i = 2; i < E; i += 2) top = max_nan(top, z[i], z[i + 1]);
         float most = top;
 #pragma unroll
         for (int off = 16; off > 0; off /= 2)
@@ -343,6 +354,28 @@ __global__ void __launch_bounds__(kThreads, 2)
           v = fmaxf(v, __shfl_sync(kAll, sort32(top, lane), n - 1));
         }
         if (most < v) continue;
+        // one key into its place in the list
+        const auto put = [&](uint64_t &mine, int from) {
+          const uint64_t key = __shfl_sync(kAll, mine, from);
+          const uint64_t up = __shfl_up_sync(kAll, list, 1);
+          if (list < key) list = lane == 0 || up > key ? key : up;
+        };
+        // few lanes: the warp goes through each one's logits (read again: a register of a
+        // place known at run time is none).  (64 x 8 of 50001: 34.3 us; 35.2 without, 35.7 with
+        // up to 8 lanes.)
+        const unsigned who = __ballot_sync(kAll, top >= v);
+        if (last != 0 && __popc(who) <= kFew) {
+          for (unsigned w = who; w != 0; w &= w - 1) {
+            const uint32_t at = index_of<T, BYTES>(t, __ffs(w) - 1, lane);
+            const float x = at < (uint32_t)a.V ? to_f(__ldg(row + at)) : -kInf;
+            uint64_t mine = x >= v ? key_of(x, at) : 0;
+            for (unsigned act = __ballot_sync(kAll, mine != 0); act != 0; act &= act - 1)
+              put(mine, __ffs(act) - 1);
+          }
+          const uint64_t own = __shfl_sync(kAll, list, nth - 1);
+          if (lane == 0) tops[k * kWarps + warp] = (uint32_t)(own >> 32);
+          continue;
+        }
         uint32_t mask = 0;
 #pragma unroll
         for (int i = 0; i < E; ++i) mask |= z[i] >= v ? 1u << i : 0u;
@@ -366,15 +399,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         const int count = __shfl_sync(kAll, before, 31);
         before -= __popc(mask);
-        // one by one into their places: of a row that has been under way for long only a few
-        // get this far (64 x 8 beams of 32000 take 24.6 us, and 26.4 sorting them always)
+        // one by one into their places (64 x 8 beams of 32000 took 24.6 us, and 26.4 sorting
+        // them always)
         if (count <= 6) {
           uint64_t mine = pop();
           for (unsigned act; (act = __ballot_sync(kAll, mine != 0)) != 0;) {
             const int from = __ffs(act) - 1;
-            const uint64_t key = __shfl_sync(kAll, mine, from);
-            const uint64_t up = __shfl_up_sync(kAll, list, 1);
-            if (list < key) list = lane == 0 || up > key ? key : up;
+            put(mine, from);
             if (lane == from) mine = pop();
           }
         } else if (count <= kPool) {
