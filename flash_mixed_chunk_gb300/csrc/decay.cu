@@ -89,22 +89,29 @@ __global__ void __launch_bounds__(kThreads, 3)
   const size_t at = ((size_t)w.b * a.H + w.h) * dk * (size_t)a.dv + v0;
   __syncthreads();
   const int warp = tid / 32, lane = tid % 32;
-  for (int i = tid; i < dkp * DVT; i += kThreads) {
-    const int d = i / DVT, c = i % DVT;
-    float x = 0.f;
-    if (d >= dk) {
-    } else if (sp.S == 1 || (LOCAL && w.s == 0)) {
-      if (a.state_in != nullptr && c < nv) x = a.state_in[at + (size_t)d * a.dv + c];
-      if (LOCAL) own[i] = x;
-    } else if (!LOCAL) {
-      if (w.s == 0) {
-        x = own[i];
-      } else if (w.t0 < w.len) {
+  if (sp.S == 1 || (LOCAL && w.s == 0)) {
 #pragma unroll 4
-        for (int s = 1; s <= w.s; ++s) x = fmaf(from[s], own[s * slot + i], x);
-      }
+    for (int i = tid; i < dkp * DVT; i += kThreads) {
+      const int d = i / DVT, c = i % DVT;
+      const bool in = a.state_in != nullptr && d < dk && c < nv;
+      const float x = in ? a.state_in[at + (size_t)d * a.dv + c] : 0.f;
+      st[i] = x;
+      if (LOCAL && d < dk) own[i] = x;
     }
-    st[i] = x;
+  } else {
+    // four columns a thread, the loads of several segments on their way
+    const int last = !LOCAL && w.t0 < w.len ? w.s : 0;
+    const size_t slot4 = slot / 4;
+    for (int i = tid; i < dkp * DVT / 4; i += kThreads) {
+      const float4 *const p = reinterpret_cast<const float4 *>(own) + i;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < dk * DVT / 4) {
+        if (!LOCAL && w.s == 0) x = *p;
+#pragma unroll 8
+        for (int s = 1; s <= last; ++s) fma4(from[s], p[s * slot4], x);
+      }
+      at4(st + 4 * i) = x;
+    }
   }
   // a segment that nothing comes behind is nobody's start
   const int end = w.t1 < w.len ? w.t1 : w.len;
