@@ -17,9 +17,9 @@
 // All kernels are programmatic dependents of what runs ahead of them on the stream
 // and wait for it before they read or write.
 //
-// Measured: fp32 prompts of 3 x 777 tokens, 6 heads of 37 x 75, 54 us (under a profiler 17 for
-// the states, 42 for the outputs), 8 x 1024 of 12 heads of 64 158 us (15 TFLOP/s, of about 70).
-// Bound by the chunks' chain of barriers and trips to shared memory: an SM issues in 45 % of its
+// Measured: fp32 prompts of 3 x 777 tokens, 6 heads of 37 x 75, 51 us, 8 x 1024 of 12 heads of 64
+// 150 us (16 TFLOP/s, of about 70).  Bound by the chunks' chain of barriers and trips to shared
+// memory (100 tokens, four chunks in two launches: 23 us): an SM issues in under half of its
 // cycles with up to 24 warps, 40 % of them products.  32 tokens a chunk: the weights' share
 // of the work stays under the state's from dk 32 on.  A step of 64 sequences of 12 heads of 128
 // takes 16.5 us, 101 MB at 6.1 TB/s (91 % of a copy's rate); one sequence's 2.1 us on the
@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   extern __shared__ float4 smem4[];
   float *sm = reinterpret_cast<float *>(smem4);
   const int dk = a.dk, dkp = decay_dk4(dk), ks = decay_row(dk);
-  float *sq = sm, *sk = sq + C * ks, *sv = sk + C * ks, *st = sv + C * VS;
+  // q, k, k with its weights in the state, v, the state, the chunk's weights, the powers
+  float *sq = sm, *sk = sq + C * ks, *kw = sk + C * ks, *sv = kw + C * ks, *st = sv + C * VS;
   float *sw = st + dkp * DVT, *pw = sw + C * WS;
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
 
@@ -133,23 +134,28 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
     for (int i = 0; i < 2 * R; ++i) {
       const int r = warp + kThreads / 32 * (i % R), c = lane + 32 * (i / R);
-      if (r < n && c < nv) y[i] = v[(int64_t)(t + r) * a.vs[1] + c];
+      if (r < n && c < nv) y[i] = __ldg(v + (int64_t)(t + r) * a.vs[1] + c);
     }
+#pragma unroll 2
     for (int d = lane; d < dkp; d += 32) {
       T x[2 * R];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int r = warp + kThreads / 32 * i;
         if (r >= n || d >= dk) continue;
-        if (!LOCAL) x[i] = q[(int64_t)(t + r) * a.qs[1] + d];
-        x[R + i] = k[(int64_t)(t + r) * a.ks[1] + d];
+        if (!LOCAL) x[i] = __ldg(q + (int64_t)(t + r) * a.qs[1] + d);
+        x[R + i] = __ldg(k + (int64_t)(t + r) * a.ks[1] + d);
       }
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int r = warp + kThreads / 32 * i;
         const bool in = r < n && d < dk;
-        if (!LOCAL) sq[r * ks + d] = in ? to_f(x[i]) : 0.f;
-        sk[r * ks + d] = in ? to_f(x[R + i]) : 0.f;
+        const float key = in ? to_f(x[R + i]) : 0.f;
+        if (!LOCAL) {
+          sq[r * ks + d] = in ? to_f(x[i]) : 0.f;
+          sk[r * ks + d] = key;
+        }
+        kw[r * ks + d] = in ? key * pw[n - 1 - r] : 0.f;
       }
     }
 #pragma unroll
@@ -213,17 +219,14 @@ __global__ void __launch_bounds__(kThreads, 3)
           if (4 * tx + c < nv) put(row + 4 * tx + c, a.scale * fmaf(pw[r + 1], y[c], x[c]));
       }
     }
-    // k_j's weight in the state
-    for (int r = warp; r < n; r += kThreads / 32)
-      for (int d = lane; d < dk; d += 32) sk[r * ks + d] *= pw[n - 1 - r];
-    __syncthreads();
+    if (!LOCAL) __syncthreads();  // all have read the state
     const float2 g = n == C ? whole : make_float2(pw[n], 0.f);
     // places 4 ty .. 4 ty + 3 of dk, columns 4 tx .. 4 tx + 3
     for (int d = 4 * ty; d < dkp; d += 64) {
       float4 add[4] = {};
 #pragma unroll 4
       for (int j = 0; j < n; ++j) {
-        const float4 x = at4(sk + j * ks + d), y = at4(sv + j * VS + 4 * tx);
+        const float4 x = at4(kw + j * ks + d), y = at4(sv + j * VS + 4 * tx);
         fma4(x.x, y, add[0]);
         fma4(x.y, y, add[1]);
         fma4(x.z, y, add[2]);

@@ -441,20 +441,20 @@ struct DecayArgs {
 struct DecaySplit {
   int S, L, nvt;
 };
-// CUDA cores: chunks of 32 tokens, tiles of 64 columns of dv.  Shared memory, in floats: q
-// and k [32][row], v [32][68], the state [dk in whole float4s][64], the chunk's weights
+// CUDA cores: chunks of 32 tokens, tiles of 64 columns of dv.  Shared memory, in floats: q,
+// k and k weighted [32][row], v [32][68], the state [dk in whole float4s][64], the chunk's weights
 // [32][36], the powers 0 .. 32.  A row of q or k is an odd number of float4s, so that the
 // rows that eight threads read at once lie in different banks.
 __host__ __device__ constexpr int decay_dk4(int dk) { return (dk + 3) / 4 * 4; }
 __host__ __device__ constexpr int decay_row(int dk) { return decay_dk4(dk) + (decay_dk4(dk) / 4 % 2 ? 8 : 4); }
 __host__ __device__ constexpr int decay_floats(int dk) {
-  return 2 * 32 * decay_row(dk) + 32 * 68 + decay_dk4(dk) * 64 + 32 * 36 + 32 + 4;
+  return 3 * 32 * decay_row(dk) + 32 * 68 + decay_dk4(dk) * 64 + 32 * 36 + 32 + 4;
 }
 // As many segments as fill the blocks that the SMs hold (three each, or what their shared
 // memory has room for), of 64 tokens at least (a segment's start costs about as much) and 64
 // of them at most.  16-bit 2 x 8192 tokens, 12 heads of 33 x 65: 394 us, 500 with two blocks an
 // SM; 1 x 4000, 8 heads of 200 x 150, where one fits: 572 us, 710 cut for three; 3 x 517, 6
-// heads of 33, uncut: 82 us for 31.
+// heads of 33, uncut: 82 us for 31.  (Before the loads' later changes, both sides alike.)
 inline DecaySplit decay_split_simt(int B, int T, int H, int dk, int dv) {
   const int nvt = (dv + 63) / 64;
   const int64_t heads = (int64_t)B * H * nvt;
