@@ -31,11 +31,12 @@
 // memory.  P takes the columns of the scores that its own warp has read, of one of two
 // buffers.
 //
-// Measured: 2 x 8192 tokens of 12 heads of 128 81 us (201 MB: 2.5 TB/s, 38 % of a copy's rate;
-// under a profiler the states' launch 31 and the outputs' 61), 1 x 32768 of 16 191 us, 8 x
-// 1024 of 12 heads with one q and k 43 us, 37 tokens 7.1 us.  Not bound by memory (the same
-// from L2) nor by the products (the pipe is busy 26 % of the time): a chunk of the outputs'
-// launch takes about 3.8 us on an SM, in which the state goes once around (D, the sum in
+// Measured: 2 x 8192 tokens of 12 heads of 128 78 us (201 MB: 2.6 TB/s, 39 % of a copy's rate;
+// under a profiler the states' launch 31 and the outputs' 57), 1 x 32768 of 16 181 us, 8 x
+// 1024 of 12 heads with one q and k 41 us, 37 tokens 7.1 us; with a unit uncut on every SM, 2 x
+// 8192 of 75 heads, 253 us, 5.0 TB/s.  Not bound by memory (the same from L2) nor by the
+// products (the pipe is busy 26 % of the time): a chunk of the outputs' launch takes about 3.7
+// us on an SM, in which the state goes once around (D, the sum in
 // registers, its bf16 copy, Q S) while 24 warps pass the tiles through shared memory: keys
 // read, three terms written, v looked at, the weights and both accumulators through registers.
 // Around them are 9 us: the start, the first copies, the last outputs.  So the cut: whole
@@ -437,39 +438,53 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     if (!LOCAL && warp == 2) {
       // =========================== a look at v a chunk ahead, and output stores
       // A weight of 0 keeps no infinity or NaN of a later token out of a row's sum.  So v is
-      // looked through (5 % of a chunk's time, by the reads of shared memory); where it holds
-      // one, it is taken out once the state's product has had it, and the rows from there on
-      // become NaN.
+      // looked through (1 or 2 % of the time; with a bounds check at every read it was 10, as
+      // this warp's instructions hold up those of its quarter of the SM); where it holds one, it
+      // is taken out once the state's product has had it, and the rows from there on become NaN.
       RingAt rv(v0s), ro(v0s);
       const auto got = [&](uint64_t *bar, int use, int code) {
         if (__all_sync(0xFFFFFFFFu, da_wait(bar, use))) return true;
         if (lane == 0) record_timeout(code);
         return false;
       };
+      // whichever comes first, the next v or the next outputs (v two chunks ahead of them at
+      // most: so many buffers has `wild`)
+      int seen = 0, sent = 0;
 #pragma unroll 1
-      for (int g = -1; g < chunks; ++g) {
-        if (g + 1 < chunks) {
-          if (!got(&full[rv.slot], rv.use, 1151)) break;
+      for (int turns = 0; sent < chunks; ++turns) {
+        const bool look = seen < chunks && seen < sent + 2 &&
+                          __all_sync(0xFFFFFFFFu, mbar_try_wait_sleep(&full[rv.slot],
+                                                                      (uint32_t)rv.use & 1u, 100u));
+        if (look) {
           uint8_t *const v = smem + rv.slot * slot_bytes;
-          const int n = tokens(g + 1), buf = (g + 1) & 1;
+          const int n = tokens(seen), buf = seen & 1;
           uint32_t sum[2] = {};
+          // 32 rows of 64 columns at a time
           const uint8_t *p = v + 16 * lane;
+          const auto add = [&](const uint4 &y) {
+            sum[0] = fma_bf16x2(y.x, y.y, sum[0]);
+            sum[1] = fma_bf16x2(y.z, y.w, sum[1]);
+          };
+          if (n == 128) {
 #pragma unroll 1
-          for (int i = 0; i < 4 * va; ++i, p += DA_ATOM / 4) {  // 32 rows of 64 columns
-            const int left = (n - 32 * (i & 3)) * 8 - lane;
+            for (int i = 0; i < 4 * va; ++i, p += DA_ATOM / 4) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint4 y = make_uint4(0u, 0u, 0u, 0u);
-              if (32 * j < left) y = *reinterpret_cast<const uint4 *>(p + 512 * j);
-              sum[0] = fma_bf16x2(y.x, y.y, sum[0]);
-              sum[1] = fma_bf16x2(y.z, y.w, sum[1]);
+              for (int j = 0; j < 8; ++j) add(*reinterpret_cast<const uint4 *>(p + 512 * j));
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 4 * va; ++i, p += DA_ATOM / 4) {
+              const int left = (n - 32 * (i & 3)) * 8 - lane;
+#pragma unroll 1
+              for (int j = 0; 32 * j < left && j < 8; ++j)
+                add(*reinterpret_cast<const uint4 *>(p + 512 * j));
             }
           }
           // (or values whose products overflow: then there is nothing to take out)
           const bool any = __any_sync(0xFFFFFFFFu, wild_lo(sum[0]) || wild_hi(sum[0]) ||
                                                        wild_lo(sum[1]) || wild_hi(sum[1]));
           if (any) {
-            if (!got(&d_full[buf], (g + 1) >> 1, 1152)) break;
+            if (!got(&d_full[buf], seen >> 1, 1152)) break;
 #pragma unroll 1
             for (int x = 0; x < va; ++x) tame(v + x * DA_ATOM, n, &wild_row[buf][64 * x], lane);
             fence_proxy_async_smem();
@@ -478,20 +493,26 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&v_ready[buf]);
           rv.step(v0s, rings.v);
+          ++seen, turns = 0;
         }
-        if (g >= 0) {
-          if (!got(&staged[g & 1], g >> 1, 1150)) break;
+        if (sent < seen &&
+            __all_sync(0xFFFFFFFFu,
+                       mbar_try_wait_sleep(&staged[sent & 1], (uint32_t)(sent >> 1) & 1u, 100u))) {
           if (lane == 0) {
             for (int x = 0; x < va; ++x)
               tma_store_4d(&mapO, smem + ro.slot * slot_bytes + x * DA_ATOM, v0 + 64 * x, w.h,
-                           w.t0 + 128 * g, w.b);
+                           w.t0 + 128 * sent, w.b);
             bulk_commit_group();
             bulk_wait_group_read<0>();
             mbar_arrive(&empty[ro.slot]);
-            mbar_arrive(&stored[g & 1]);
+            mbar_arrive(&stored[sent & 1]);
           }
           __syncwarp();
           ro.step(v0s, rings.v);
+          ++sent, turns = 0;
+        } else if (turns > (1 << 23)) {
+          if (lane == 0) record_timeout(1150);
+          break;
         }
       }
       if (lane == 0) bulk_wait_group<0>();
