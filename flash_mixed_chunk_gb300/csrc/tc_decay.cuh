@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   __shared__ __align__(8) uint64_t full[DA_SLOTS], empty[DA_SLOTS], x_ready[2], x_free[2];
   __shared__ __align__(8) uint64_t staged[2], stored[2];
   __shared__ __align__(8) uint64_t sc_full[2], qs_full, p_ready, o_full, o_free, s_ready, d_full[2],
-      d_free[2], v_ready[2], mma_done[2];
+      d_free[2], v_ready[2], mma_done[2], whole_ready;
   __shared__ __align__(16) float back[16];  // lam^(15 - j)
   __shared__ float power[129];              // lam^j
   __shared__ float from[64];                // the segments' powers at this one's start
@@ -216,33 +216,59 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     return n < 128 ? n : 128;
   };
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < n_slots; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
+  // k, q and v (0, 1, 2) of chunk g into the place r
+  const auto load = [&](int g, int what, RingAt &r) {
+    const CUtensorMap *const map = what == 0 ? &mapK : what == 1 ? &mapQ : &mapV;
+    const int atoms = what == 2 ? va : ka, x0 = what == 2 ? v0 : 0;
+    const int head = w.h / (a.H / (what == 0 ? a.Hk : what == 1 ? a.Hq : a.Hv));
+    mbar_arrive_expect_tx(&full[r.slot], DA_ATOM * (uint32_t)atoms);
+#pragma unroll 1
+    for (int x = 0; x < atoms; ++x)
+      tma_load_4d(smem + r.slot * slot_bytes + x * DA_ATOM, map, &full[r.slot], x0 + 64 * x, head,
+                  w.t0 + 128 * g, w.b);
+    if (what == 0)
+      r.step(k0, rings.k);
+    else if (what == 1)
+      r.step(0, rings.q);
+    else
+      r.step(v0s, rings.v);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < n_slots; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], 1);
+      }
+      fence_mbar_init();
+      // the first chunk is on its way while the block gets ready
+      RingAt rq(0), rk(k0), rv(v0s);
+      if (chunks > 0) {
+        load(0, 0, rk);
+        if (!LOCAL) load(0, 1, rq);
+        load(0, 2, rv);
+      }
+    } else if (lane < 3) {
+      const int i = lane - 1;
       mbar_init(&x_ready[i], 4);
       mbar_init(&x_free[i], 1);
       mbar_init(&staged[i], 8);
       mbar_init(&stored[i], 1);
+      mbar_init(&sc_full[i], 1);
+      mbar_init(&d_full[i], 1);
+      mbar_init(&v_ready[i], 5);
+      mbar_init(&d_free[i], 8);
+      mbar_init(&mma_done[i], 1);
+      fence_mbar_init();
+    } else if (lane == 3) {
+      mbar_init(&qs_full, 1);
+      mbar_init(&p_ready, 8);
+      mbar_init(&o_full, 1);
+      mbar_init(&o_free, 8);
+      mbar_init(&s_ready, 8);
+      mbar_init(&whole_ready, 1);
+      fence_mbar_init();
     }
-    mbar_init(&sc_full[0], 1);
-    mbar_init(&sc_full[1], 1);
-    mbar_init(&qs_full, 1);
-    mbar_init(&p_ready, 8);
-    mbar_init(&o_full, 1);
-    mbar_init(&o_free, 8);
-    mbar_init(&s_ready, 8);
-    mbar_init(&d_full[0], 1);
-    mbar_init(&d_full[1], 1);
-    mbar_init(&v_ready[0], 5);
-    mbar_init(&v_ready[1], 5);
-    mbar_init(&d_free[0], 8);
-    mbar_init(&d_free[1], 8);
-    mbar_init(&mma_done[0], 1);
-    mbar_init(&mma_done[1], 1);
-    fence_mbar_init();
   }
   if (threadIdx.x >= 64 && threadIdx.x < 64 + 129) {
     const int j = (int)threadIdx.x - 64;
@@ -250,7 +276,6 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     power[j] = p;
     if (j < 16) back[15 - j] = p;
   }
-  if (warp == 12 && lane == 0) whole_s = decay_power2(rate, 128);
   if (!LOCAL && threadIdx.x >= 512 && (int)threadIdx.x - 512 <= w.s)
     from[threadIdx.x - 512] = decay_power(rate, w.t0 - ((int)threadIdx.x - 512) * sp.L);
   if (warp == 1) {
@@ -276,37 +301,31 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     regs_dec<DA_REG_ISSUE>();
     if (warp == 0 && lane == 0) {
       // =========================== TMA
-      if (!LOCAL) tma_prefetch_desc(&mapQ);
-      tma_prefetch_desc(&mapK);
-      tma_prefetch_desc(&mapV);
-      const int hq = w.h / (a.H / a.Hq), hk = w.h / (a.H / a.Hk), hv = w.h / (a.H / a.Hv);
       RingAt rq(0), rk(k0), rv(v0s);
+      if (chunks > 0) {  // (the first chunk's are issued)
+        if (!LOCAL) rq.step(0, rings.q);
+        rk.step(k0, rings.k);
+        rv.step(v0s, rings.v);
+      }
       bool ok = true;
 #pragma unroll 1
-      for (int g = 0; ok && g < chunks; ++g) {
-        const int t = w.t0 + 128 * g;
+      for (int g = 1; ok && g < chunks; ++g) {
 #pragma unroll 1
-        for (int i = 0; ok && i < (LOCAL ? 2 : 3); ++i) {  // k, (q,) v
-          const bool isk = i == 0, isv = i == (LOCAL ? 1 : 2), isq = !isk && !isv;
-          RingAt r = isv ? rv : isq ? rq : rk;
+        for (int i = 0; i < 3; ++i) {
+          if (LOCAL && i == 1) continue;
+          RingAt r = i == 2 ? rv : i == 1 ? rq : rk;
           if (r.use > 0 && !da_wait(&empty[r.slot], r.use - 1)) {
             record_timeout(1101);
             ok = false;
             break;
           }
-          const int atoms = isv ? va : ka;
-          mbar_arrive_expect_tx(&full[r.slot], DA_ATOM * (uint32_t)atoms);
-#pragma unroll 1
-          for (int x = 0; x < atoms; ++x)
-            tma_load_4d(smem + r.slot * slot_bytes + x * DA_ATOM, isv ? &mapV : isq ? &mapQ : &mapK,
-                        &full[r.slot], (isv ? v0 : 0) + 64 * x, isv ? hv : isq ? hq : hk, t, w.b);
-          r.step(isv ? v0s : isq ? 0 : k0, isv ? rings.v : isq ? rings.q : rings.k);
-          if (isv)
+          load(g, i, r);
+          if (i == 2)
             rv = r;
-          else if (isk)
-            rk = r;
-          else
+          else if (i == 1)
             rq = r;
+          else
+            rk = r;
         }
       }
       // the last copy issued into each place has landed
@@ -435,7 +454,12 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         got(&mma_done[1], 0, 1118);
       }
     }
+    if (warp == 2 && lane == 0) {  // (64-bit: a microsecond, which nobody else waits for)
+      whole_s = decay_power2(rate, 128);
+      mbar_arrive(&whole_ready);
+    }
     if (!LOCAL && warp == 2) {
+      __syncwarp();
       // =========================== a look at v a chunk ahead, and output stores
       // A weight of 0 keeps no infinity or NaN of a later token out of a row's sum.  So v is
       // looked through (1 or 2 % of the time; with a bounds check at every read it was 10, as
@@ -546,10 +570,14 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float4 d = *reinterpret_cast<const float4 *>(&back[j]);
-            p[j / 2] = pack_bf16x2(__uint_as_float(r[j]) * (f * d.x),
-                                   __uint_as_float(r[j + 1]) * (f * d.y));
-            p[j / 2 + 1] = pack_bf16x2(__uint_as_float(r[j + 2]) * (f * d.z),
-                                       __uint_as_float(r[j + 3]) * (f * d.w));
+            const float2 f2 = make_float2(f, f);
+            const float2 a2 = mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                   mul2(f2, make_float2(d.x, d.y)));
+            const float2 b2 =
+                mul2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                     mul2(f2, make_float2(d.z, d.w)));
+            p[j / 2] = pack_bf16x2(a2.x, a2.y);
+            p[j / 2 + 1] = pack_bf16x2(b2.x, b2.y);
           }
         } else if (at < 32) {
           const int gap = ln - at;
@@ -577,7 +605,11 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           tmem_ld16(ocol + (uint32_t)c, r);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * ahead);
+          for (int j = 0; j < 16; j += 2) {
+            const float2 y = mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                  make_float2(ahead, ahead));
+            r[j] = __float_as_uint(y.x), r[j + 1] = __float_as_uint(y.y);
+          }
           tmem_st16(ocol + (uint32_t)c, r);
         }
       }
@@ -737,6 +769,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         }
       }
     }
+    wait(&whole_ready, 0, 1146);
     const float2 whole = whole_s;
     const auto publish = [&]() {  // the operand of the next chunk's Q S
       if (row < 64 * ka && half < va) {
