@@ -31,18 +31,20 @@
 // memory.  P takes the columns of the scores that its own warp has read, of one of two
 // buffers.
 //
-// Measured: 2 x 8192 tokens of 12 heads of 128 78 us (201 MB: 2.6 TB/s, 39 % of a copy's rate;
-// under a profiler the states' launch 31 and the outputs' 57), 1 x 32768 of 16 181 us, 8 x
-// 1024 of 12 heads with one q and k 41 us, 37 tokens 7.1 us; with a unit uncut on every SM, 2 x
-// 8192 of 75 heads, 253 us, 5.0 TB/s.  Not bound by memory (the same from L2) nor by the
-// products (the pipe is busy 26 % of the time): a chunk of the outputs' launch takes about 3.7
-// us on an SM, in which the state goes once around (D, the sum in
+// Measured: 2 x 8192 tokens of 12 heads of 128 76 us (201 MB: 2.6 TB/s, 40 % of a copy's rate;
+// under a profiler the states' launch 31 and the outputs' 57), 1 x 32768 of 16 178 us, 8 x
+// 1024 of 12 heads with one q and k 41 us, 37 tokens 6.8 us; with a unit uncut on every SM, 2
+// x 8192 of 75 heads, 249 us, 5.1 TB/s, 76 % of a copy's rate. Not bound by memory (the same
+// from L2) nor by the products (the pipe is busy 26 % of the time): a chunk of the outputs'
+// launch takes about 3.7 us on an SM, in which the state goes once around (D, the sum in
 // registers, its bf16 copy, Q S) while 24 warps pass the tiles through shared memory: keys
 // read, three terms written, v looked at, the weights and both accumulators through registers.
-// Around them are 9 us: the start, the first copies, the last outputs.  So the cut: whole
-// heads of 128 columns, one unit an SM, as many segments as there are SMs, though k and v of
-// all but the last are read twice. Chunks of 128: the products' tile; the weights' work grows
-// with the chunk, the state's with the number of them, and at 128 x 128 x 128 they are equal.
+// Without the keys' terms a chunk takes 10 % less, without the weights 2 %, with one term's
+// products 2 %. Around the chunks are 8 us: the start, the first copies, the last outputs. So
+// the cut: whole heads of 128 columns, one unit an SM, as many segments as there are SMs,
+// though k and v of all but the last are read twice. Chunks of 128: the products' tile; the
+// weights' work grows with the chunk, the state's with the number of them, and at 128 x 128 x
+// 128 they are equal.
 #pragma once
 
 #include "decay.cuh"
