@@ -296,3 +296,29 @@ def test_the_longest_row_of_logits():
     turns = V / 1024 / 64
     got = torch.tensor([9.0, 8.0, 8.0, 0.0], dtype=torch.float64) - lse
     assert ((score[0].cpu().double() - got).abs() <= (turns + 70) * 2.0 ** -24 + 2.0 ** -19).all()
+
+
+def test_rows_that_overlap_and_other_orders():
+    """Tokens closer than their rows are long, heads inside one another, tokens innermost but
+    for the row, batches last: as contiguous copies of them, bit for bit."""
+    B, T, H, d = 2, 300, 3, 64
+    flat = rand(B * T * H * d)
+    views = [
+        torch.as_strided(flat, (B, T, H, d), (T * 8, 8, 16, 1)),
+        torch.as_strided(flat, (B, T, H, d), (8, 24, 64, 1)),
+        flat.view(B, H, T, d).transpose(1, 2),
+        flat.view(H, T, B, d).permute(2, 1, 0, 3),
+        flat.view(T, H, B, d).permute(2, 0, 1, 3),
+    ]
+    ld = torch.tensor([-0.01, -0.1, -0.7]).cuda()
+    for x in views:
+        for y in (views[2], x):
+            want = fm.decay_attention(x.contiguous(), x.contiguous(), y.contiguous(), ld)
+            got = fm.decay_attention(x, x, y, ld)
+            settled()
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+            s1, s2 = want[1].clone(), want[1].clone()
+            a = fm.decay_step(x[:, 3], x[:, 4], y[:, 5], ld, s1)
+            b = fm.decay_step(x[:, 3].contiguous(), x[:, 4].contiguous(), y[:, 5].contiguous(), ld,
+                              s2)
+            assert torch.equal(a, b) and torch.equal(s1, s2)
