@@ -31,12 +31,12 @@
 // memory.  P takes the columns of the scores that its own warp has read, of one of two
 // buffers.
 //
-// Measured: 2 x 8192 tokens of 12 heads of 128 76 us (201 MB: 2.6 TB/s, 40 % of a copy's rate;
-// under a profiler the states' launch 31 and the outputs' 57), 1 x 32768 of 16 178 us, 8 x
-// 1024 of 12 heads with one q and k 41 us, 37 tokens 6.8 us; with a unit uncut on every SM, 2
-// x 8192 of 75 heads, 249 us, 5.1 TB/s, 76 % of a copy's rate. Not bound by memory (the same
+// Measured: 2 x 8192 tokens of 12 heads of 128 75 us (201 MB: 2.7 TB/s, 40 % of a copy's rate;
+// under a profiler the states' launch 31 and the outputs' 57), 1 x 32768 of 16 176 us, 8 x
+// 1024 of 12 heads with one q and k 40 us, 37 tokens 6.8 us; with a unit uncut on every SM, 2
+// x 8192 of 75 heads, 245 us, 5.2 TB/s, 77 % of a copy's rate. Not bound by memory (the same
 // from L2) nor by the products (the pipe is busy 26 % of the time): a chunk of the outputs'
-// launch takes about 3.7 us on an SM, in which the state goes once around (D, the sum in
+// launch takes about 3.6 us on an SM, in which the state goes once around (D, the sum in
 // registers, its bf16 copy, Q S) while 24 warps pass the tiles through shared memory: keys
 // read, three terms written, v looked at, the weights and both accumulators through registers.
 // Without the keys' terms a chunk takes 10 % less, without the weights 2 %, with one term's
@@ -688,6 +688,11 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
           for (int x = 0; x < va; ++x)
             *reinterpret_cast<uint4 *>(v + x * DA_ATOM + n * 128 + i * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
+        // (of k this thread's own places)
+        for (int j = r; j < 128; j += 16)
+          for (int x = 0; j >= n && x < ka; ++x)
+            *reinterpret_cast<uint4 *>(k + x * DA_ATOM + j * 128 + p16) =
+                make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
       }
       __syncwarp();
@@ -698,7 +703,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         if (use > 0) wait(&x_free[buf], use - 1, 1143);
         uint8_t *const x = terms + (uint32_t)buf * 2 * (uint32_t)ka * 4096 + r * 128 + p16;
         uint8_t *const kp = k + (qt * 32 + r) * 128 + p16;
-#pragma unroll 1
+#pragma unroll
         for (int h = 0; h < 2; ++h) {  // 16 tokens
           const int j = qt * 32 + 16 * h + r;
           const float wj = j < n ? power[n - 1 - j] : 0.f;
@@ -707,7 +712,6 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < ka; ++i) {
             raw[i] = *reinterpret_cast<const uint4 *>(kp + i * DA_ATOM + h * 2048);
-            if (j >= n) raw[i] = make_uint4(0u, 0u, 0u, 0u);
           }
 #pragma unroll
           for (int i = 0; i < ka; ++i) {
