@@ -127,6 +127,25 @@ __device__ __forceinline__ float exp_below(float x) {
   return y;
 }
 
+// log(s) of a sum, s >= 1, to about 1e-9, where the sum itself is good to 1e-7: s = 2^e f, f
+// within a half power of 1, and log f = 2 atanh z, z = (f - 1) / (f + 1), as a float, its rest
+// and the series behind it.  (The double log took 1 us of the smallest call's 8, 4 of 34 at 64 x
+// 8 of 50001.)
+__device__ __forceinline__ double log_sum(float s) {
+  const uint32_t u = __float_as_uint(s);
+  int e = (int)(u >> 23) - 127;
+  float f = __uint_as_float((u & 0x007FFFFFu) | 0x3F800000u);
+  if (f > 1.41421356f) f *= 0.5f, ++e;
+  const float n = f - 1.f, d = f + 1.f, rest = f - (d - 1.f);  // (n is exact)
+  const float z = n / d;
+  const float z_rest = (fmaf(-z, d, n) - z * rest) / d;
+  const float y = z * z;
+  const float series =
+      y * fmaf(y, fmaf(y, fmaf(y, fmaf(y, 2.f / 11, 2.f / 9), 2.f / 7), 2.f / 5), 2.f / 3);
+  return fma((double)e, 0.693147180559945309,
+             2.0 * (double)z + (double)fmaf(z, series, 2.f * z_rest));
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {
   float m;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
@@ -469,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         flat = (uint64_t)k * a.V + a.pad;
       } else if (list != 0 && isfinite(sum.m)) {
         c = order_of((double)scores[k] +
-                     ((double)key_value(list) - ((double)sum.m + log((double)sum.s))));
+                     ((double)key_value(list) - ((double)sum.m + log_sum(sum.s))));
       }
       if (lane >= n) c = 0;
       merge_pairs(best, where, c, flat, lane);
