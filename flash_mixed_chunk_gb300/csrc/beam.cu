@@ -16,12 +16,12 @@
 // Rows of one call are cut the same way, so that equal rows give equal sums and the
 // tie goes to the lower beam.
 //
-// Measured: one element, 4 beams of 32000 in bf16, 10.0 us (2 of the launch, the rest a chain:
+// Measured: one element, 4 beams of 32000 in bf16, 9.3 us (2 of the launch, the rest a chain:
 // a row's part, the lists of a block, of the cluster, of the beams); 64 x 8 of 50001 in fp32,
-// 16 candidates, none finished, 34 us, 102 MB at 3.0 TB/s (45 % of a copy's rate): an SM with
+// 16 candidates, none finished, 31 us, 102 MB at 3.3 TB/s (49 % of a copy's rate): an SM with
 // work issues in half of its cycles, about 20 instructions a logit, half of them to load,
 // compare and sum it, half for the lists, which a warp of 12 parts of a row changes in most of
-// them; and 256 blocks do not spread evenly over 152 SMs.  64 x 8 of 32000 in bf16 23 us.
+// them; and 256 blocks do not spread evenly over 152 SMs.  64 x 8 of 32000 in bf16 20 us.
 //
 // beam_reorder: rows of up to 16 arrays, t[b, k] = t[b, parent[b, k]] in place, one
 // launch.  A thread holds its bytes of every beam that changes in registers before

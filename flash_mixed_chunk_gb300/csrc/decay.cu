@@ -17,7 +17,7 @@
 // All kernels are programmatic dependents of what runs ahead of them on the stream
 // and wait for it before they read or write.
 //
-// Measured: fp32 prompts of 3 x 777 tokens, 6 heads of 37 x 75, 51 us, 8 x 1024 of 12 heads of 64
+// Measured: fp32 prompts of 3 x 777 tokens, 6 heads of 37 x 75, 50 us, 8 x 1024 of 12 heads of 64
 // 150 us (16 TFLOP/s, of about 70).  Bound by the chunks' chain of barriers and trips to shared
 // memory (100 tokens, four chunks in two launches: 23 us): an SM issues in under half of its
 // cycles with up to 24 warps, 40 % of them products.  32 tokens a chunk: the weights' share

@@ -13,7 +13,7 @@ namespace {
 
 // log2 of a head's decay, as a sum of two floats: the exponent of a far position is a
 // product with up to 2^31.  (64-bit arithmetic, whose pipe is a trickle here, costs a
-// block whose warps all form powers microseconds.)  A log decay of -inf (nothing is kept)
+// block that forms powers microseconds.)  A log decay of -inf (nothing is kept)
 // becomes one whose first power is 0 already, so that the power 0 is 1 and not a NaN.
 struct DecayRate {
   float hi, lo;
@@ -37,13 +37,31 @@ __device__ __forceinline__ float decay_power(const DecayRate &r, int n) {
   const float p = exp2f(e);
   return isinf(e) ? p : fmaf(p, rest * 0.693147180559945f, p);
 }
-// The same as a sum of two floats: a state is multiplied by one power once a chunk,
-// and a factor in 32 bits would be off by half a step in every one of them.  (In 64 bits:
-// for one warp of a block.)
+// The same as a sum of two floats, n up to 128: a state is multiplied by one power once a
+// chunk, and a factor in 32 bits would be off by half a step in every one of them.  2^x = 2^k
+// (1 + m), 1 + m = exp(t)^32 with |t| <= ln(2) / 64: t and m in two floats each, m = t + t^2 / 2
+// + ..., and five times m = 2 m + m^2.  Off by under 2^-30 of itself times the exponent (of e),
+// so that all the chunks of which a state still holds something add up to less than one
+// rounding.  (A double exp2
+// takes its warp a microsecond, and a block's first barrier waits for it.)
 __device__ __forceinline__ float2 decay_power2(const DecayRate &r, int n) {
-  const double p = exp2(((double)r.hi + (double)r.lo) * (double)n);
-  const float hi = (float)p;
-  return make_float2(hi, isinf(hi) ? 0.f : (float)(p - (double)hi));
+  const float fn = (float)n, x = fn * r.hi, x_rest = fmaf(fn, r.hi, -x) + fn * r.lo;
+  if (!(x > -200.f && x < 128.f)) return make_float2(x < 0.f ? 0.f : exp2f(x), 0.f);
+  const float k = rintf(x), g = x - k;  // exactly
+  constexpr float kHi = 0.693147182464599609f / 32, kLo = -1.90465429995776804e-9f / 32;  // ln(2)
+  const float t = g * kHi, t_rest = fmaf(g, kHi, -t) + fmaf(g, kLo, x_rest * kHi);
+  const float q = fmaf(t * t, fmaf(t, fmaf(t, 1.f / 24, 1.f / 6), 0.5f), fmaf(t, t_rest, t_rest));
+  float m = t + q, low = q - (m - t);
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const float sq = m * m, sq_rest = fmaf(m, m, -sq) + 2.f * m * low;
+    const float h = 2.f * m + sq;
+    low = (sq - (h - 2.f * m)) + (2.f * low + sq_rest);
+    m = h;
+  }
+  const float h = 1.f + m, l = (m - (h - 1.f)) + low;
+  const float hi = h + l, lo = l - (hi - h);
+  return make_float2(ldexpf(hi, (int)k), ldexpf(lo, (int)k));
 }
 
 // A unit of work: one head of one sequence, a tile of dv, a segment of tokens.

@@ -33,7 +33,7 @@
 //
 // Measured: 2 x 8192 tokens of 12 heads of 128 75 us (201 MB: 2.7 TB/s, 40 % of a copy's rate;
 // under a profiler the states' launch 31 and the outputs' 57), 1 x 32768 of 16 176 us, 8 x
-// 1024 of 12 heads with one q and k 40 us, 37 tokens 6.8 us; with a unit uncut on every SM, 2
+// 1024 of 12 heads with one q and k 40 us, 37 tokens 6.6 us; with a unit uncut on every SM, 2
 // x 8192 of 75 heads, 245 us, 5.2 TB/s, 77 % of a copy's rate. Not bound by memory (the same
 // from L2) nor by the products (the pipe is busy 26 % of the time): a chunk of the outputs'
 // launch takes about 3.6 us on an SM, in which the state goes once around (D, the sum in
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         got(&mma_done[1], 0, 1118);
       }
     }
-    if (warp == 2 && lane == 0) {  // (64-bit: a microsecond, which nobody else waits for)
+    if (warp == 2 && lane == 0) {  // (only the state's warps wait for it, and late)
       whole_s = decay_power2(rate, 128);
       mbar_arrive(&whole_ready);
     }
