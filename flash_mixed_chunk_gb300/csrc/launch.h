@@ -446,7 +446,9 @@ struct DecaySplit {
 // [32][36], the powers 0 .. 32.  A row of q or k is an odd number of float4s, so that the
 // rows that eight threads read at once lie in different banks.
 __host__ __device__ constexpr int decay_dk4(int dk) { return (dk + 3) / 4 * 4; }
-__host__ __device__ constexpr int decay_row(int dk) { return decay_dk4(dk) + (decay_dk4(dk) / 4 % 2 ? 8 : 4); }
+__host__ __device__ constexpr int decay_row(int dk) {
+  return decay_dk4(dk) + (decay_dk4(dk) / 4 % 2 ? 8 : 4);
+}
 __host__ __device__ constexpr int decay_floats(int dk) {
   return 3 * 32 * decay_row(dk) + 32 * 68 + decay_dk4(dk) * 64 + 32 * 36 + 32 + 4;
 }
