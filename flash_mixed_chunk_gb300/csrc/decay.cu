@@ -19,7 +19,7 @@
 //
 // Measured: fp32 prompts of 3 x 777 tokens, 6 heads of 37 x 75, 50 us, 8 x 1024 of 12 heads of 64
 // 150 us (16 TFLOP/s, of about 70).  Bound by the chunks' chain of barriers and trips to shared
-// memory (100 tokens, four chunks in two launches: 23 us): an SM issues in under half of its
+// memory (100 tokens, four chunks in two launches: 21.5 us): an SM issues in under half of its
 // cycles with up to 24 warps, 40 % of them products.  32 tokens a chunk: the weights' share
 // of the work stays under the state's from dk 32 on.  A step of 64 sequences of 12 heads of 128
 // takes 16.5 us, 101 MB at 6.1 TB/s (91 % of a copy's rate); one sequence's 2.1 us on the
