@@ -963,6 +963,17 @@ def _row_stride(name, t, B, K) -> int:
     return t.stride(1)
 
 
+def _logit_row(logits, B, K) -> int:
+    """Elements between the rows of logits [B, K, V] or [B K, V]; of two dimensions the
+    first counts the beams, also where the second happens to be K."""
+    if logits.dim() == 2 and logits.shape[0] == B * K:
+        return _row_stride("logits", logits, B * K, 1)
+    if logits.dim() == 3 and logits.shape[:2] == (B, K):
+        return _row_stride("logits", logits, B, K)
+    raise ValueError(f"logits must be [B, K, V] or [B K, V] with scores [B, K] = {(B, K)}, got "
+                     f"{tuple(logits.shape)}")
+
+
 def flash_mca_beam_select(logits, scores, finished, score, parent, token, pad: int = 0,
                           stream=None) -> None:
     """Of the candidates scores[k] + log softmax(logits[k])[v] of every batch element the
@@ -976,9 +987,7 @@ def flash_mca_beam_select(logits, scores, finished, score, parent, token, pad: i
 
 def _beam_select(dev, ptr, logits, scores, finished, score, parent, token, pad):
     (B, K), (_, n) = _matrix("scores", scores), _matrix("score", score)
-    if logits.dim() not in (2, 3) or logits.dim() == 3 and logits.shape[:2] != (B, K):
-        raise ValueError("logits must be [B, K, V] or [B K, V] with scores [B, K]")
-    row, V = _row_stride("logits", logits, B, K), logits.shape[-1]
+    row, V = _logit_row(logits, B, K), logits.shape[-1]
     if V > _INT_MAX or not 0 <= pad <= _INT_MAX:
         raise ValueError("the vocabulary and pad must fit 32 bits")
     st = lib.flash_mca_beam_select(

@@ -538,11 +538,12 @@ PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const fmca_dtype dt = dtype_of(logits);
   const int64_t B = scores.size(0), K = scores.size(1);
   const float *ps = (const float *)on("scores", scores, at::kFloat, {B, K}, dev);
-  const int64_t row = row_stride("logits", logits, B, K);
-  const bool two = logits.dim() == 3;
-  if (!two && logits.dim() != 2) fail(PyExc_ValueError, "logits must be [B, K, V] or [B K, V]");
-  if (two && (logits.size(0) != B || logits.size(1) != K))
-    fail(PyExc_ValueError, "logits must be [B, K, V] with scores [B, K]");
+  // of two dimensions the first counts the beams, also where the second happens to be K
+  const bool flat = logits.dim() == 2 && logits.size(0) == B * K;
+  if (!flat && (logits.dim() != 3 || logits.size(0) != B || logits.size(1) != K))
+    fail(PyExc_ValueError, "logits must be [B, K, V] or [B K, V] with scores [B, K], got " +
+                               shape_text(logits.sizes()));
+  const int64_t row = row_stride("logits", logits, flat ? B * K : B, flat ? 1 : K);
   const int V = size_of("the vocabulary", logits.size(logits.dim() - 1));
   const int64_t n = a[2] == Py_None ? K : whole(a[2]), pad = whole(a[4]);
   if (n < 1 || n > INT32_MAX || pad < 0 || pad > INT32_MAX)
