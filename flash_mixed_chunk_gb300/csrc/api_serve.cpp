@@ -42,6 +42,8 @@ bool aligned(std::initializer_list<const void *> ptrs, uintptr_t to) {
 fmca_status done(int rc) { return rc == 0 ? FMCA_OK : FMCA_ERR_CUDA; }
 bool known(fmca_dtype t) { return t == FMCA_F32 || t == FMCA_BF16; }
 
+static_assert(FMCA_BEAM_MAX == kBeamMax, "the header's limit is the kernels'");
+
 // Every offset of an operand fits 62 bits: a size or stride beyond 2^40 is refused,
 // and so is an operand that would span 2^60 bytes.
 constexpr int64_t kMost = (int64_t)1 << 40, kSpan = (int64_t)1 << 60;

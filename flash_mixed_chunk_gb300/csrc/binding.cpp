@@ -548,6 +548,8 @@ PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   const int64_t n = a[2] == Py_None ? K : whole(a[2]), pad = whole(a[4]);
   if (n < 1 || n > INT32_MAX || pad < 0 || pad > INT32_MAX)
     fail(PyExc_ValueError, "n must be at least 1, pad a token");
+  // (ahead of the results, whose size it is)
+  if (n > FMCA_BEAM_MAX || K > FMCA_BEAM_MAX) check(FMCA_ERR_UNSUPPORTED, "flash_mca_beam_select");
   const uint8_t *pf =
       a[3] != Py_None ? (const uint8_t *)on("finished", a[3], at::kBool, {B, K}, dev) : nullptr;
   const void *pl = logits.data_ptr();

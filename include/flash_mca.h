@@ -548,6 +548,7 @@ fmca_status flash_mca_decay_step(const void *q, const void *k, const void *v,
  * Sizes: B, V >= 1, 1 <= K, n <= 32, 0 <= pad < V.  Arrays are aligned to their
  * elements; outputs must not overlap inputs or each other.
  */
+#define FMCA_BEAM_MAX 32 /* beams, and candidates, of a batch element */
 fmca_status flash_mca_beam_select(const void *logits, int64_t row, const float *scores,
                                   const uint8_t *finished, float *score, int64_t *parent,
                                   int64_t *token, int B, int K, int V, int n, int pad,

@@ -1,5 +1,5 @@
 """Calls of generation with states that are easily got wrong: strided logits of two
-dimensions."""
+dimensions, too many candidates."""
 import pytest
 import torch
 
@@ -24,3 +24,18 @@ def test_logits_of_two_dimensions_have_a_row_for_each_beam():
     assert got[2].flatten().tolist() == one.argmax(1).tolist()
     got = fm.beam_select(torch.randn(1, 1, device="cuda"), scores[:, :1])
     assert got[2].tolist() == [[0]]
+
+
+def test_too_many_candidates_are_refused_before_memory_is_taken():
+    logits, scores = torch.zeros(8, 4, 50, device="cuda"), torch.zeros(8, 4, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for n in (33, 10 ** 6, 2 ** 31 - 1):
+        with pytest.raises(fm.FmcaError):
+            fm.beam_select(logits, scores, n)
+    many = torch.zeros(1, 40, 5, device="cuda")  # 40 beams, and so 40 candidates by default
+    before += many.numel() * 4 + 2048
+    with pytest.raises(fm.FmcaError):
+        fm.beam_select(many, many[:, :, 0].contiguous())
+    assert torch.cuda.max_memory_allocated() <= before
