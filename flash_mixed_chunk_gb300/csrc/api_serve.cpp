@@ -126,12 +126,22 @@ size_t decay_bytes(const DecayArgs &a) {
   return s > t ? s : t;
 }
 
+// Whether one of the rows of a piece shares a byte with `n` bytes at p that come again every
+// `again` bytes (0: once).  Rows that are as far apart take the same places of every row, so
+// that column ranges of one buffer do not clash though the ranges of their addresses do.
+bool clash(const fmca_beam_piece &a, int64_t rows, const void *p, int64_t n, int64_t again) {
+  const Span all{a.base, (uint64_t)(rows - 1) * a.row + a.bytes};
+  if (!overlap(all, Span{p, (uint64_t)(again > 0 ? (rows - 1) * again : 0) + n})) return false;
+  if (again > 0 && again != a.row) return true;
+  const intptr_t gap = reinterpret_cast<intptr_t>(p) - reinterpret_cast<intptr_t>(a.base);
+  const int64_t at = (gap % a.row + a.row) % a.row;
+  return at < a.bytes || at + n > a.row;
+}
 fmca_status pieces_check(const fmca_beam_piece *p, int n, const int64_t *parent, int B, int K) {
   if (!p || n <= 0 || !parent || B <= 0 || K <= 0) return FMCA_ERR_INVALID_ARG;
   if (K > kBeamMax) return FMCA_ERR_UNSUPPORTED;
   if (!aligned({parent}, 8)) return FMCA_ERR_ALIGN;
   const int64_t rows = (int64_t)B * K;
-  const Span ps{parent, 8 * (uint64_t)rows};
   for (int i = 0; i < n; ++i) {
     if (p[i].bytes < 0 || p[i].row < p[i].bytes || p[i].row > kMost) return FMCA_ERR_SHAPE;
     if (p[i].bytes == 0) continue;
@@ -139,11 +149,9 @@ fmca_status pieces_check(const fmca_beam_piece *p, int n, const int64_t *parent,
     if ((double)rows * (double)p[i].row > (double)kSpan ||
         (double)B * ((double)p[i].bytes + 256) / 256 > 2e9)
       return FMCA_ERR_UNSUPPORTED;
-    const Span a{p[i].base, (uint64_t)(rows - 1) * p[i].row + p[i].bytes};
-    if (overlap(a, ps)) return FMCA_ERR_INVALID_ARG;
+    if (clash(p[i], rows, parent, 8 * rows, 0)) return FMCA_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
-      if (p[j].bytes > 0 &&
-          overlap(a, Span{p[j].base, (uint64_t)(rows - 1) * p[j].row + p[j].bytes}))
+      if (p[j].bytes > 0 && clash(p[i], rows, p[j].base, p[j].bytes, p[j].row))
         return FMCA_ERR_INVALID_ARG;
   }
   return FMCA_OK;

@@ -558,8 +558,9 @@ fmca_status flash_mca_beam_select(const void *logits, int64_t row, const float *
  * Rows of any arrays after a selection, in place: row (b, k) becomes what row
  * (b, parent[b][k]) was.  A piece is an array of B K rows of `bytes` bytes, `row`
  * bytes (>= bytes) apart; what lies between is not touched.  A parent outside
- * 0 .. K - 1 leaves its beam as it is.  One launch for up to 16 pieces; pieces must
- * not overlap each other or parent.  Sizes: B, n_pieces >= 1, 1 <= K <= 32.
+ * 0 .. K - 1 leaves its beam as it is.  One launch for up to 16 pieces; rows must
+ * not overlap another piece's rows or parent (rows inside one another's gaps, as column
+ * ranges of one buffer are, need the same `row`).  Sizes: B, n_pieces >= 1, 1 <= K <= 32.
  */
 typedef struct {
   void *base;

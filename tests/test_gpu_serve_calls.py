@@ -1,5 +1,5 @@
 """Calls of generation with states that are easily got wrong: strided logits of two
-dimensions, too many candidates."""
+dimensions, too many candidates, pieces whose rows lie inside one another."""
 import pytest
 import torch
 
@@ -39,3 +39,43 @@ def test_too_many_candidates_are_refused_before_memory_is_taken():
     with pytest.raises(fm.FmcaError):
         fm.beam_select(many, many[:, :, 0].contiguous())
     assert torch.cuda.max_memory_allocated() <= before
+
+
+@pytest.mark.parametrize("call", ["beam_reorder", "flash_mca_beam_reorder"])
+def test_rows_inside_one_another(call):
+    """Column ranges of one buffer are pieces that share no byte; parent may lie between
+    rows, too."""
+    g = torch.Generator().manual_seed(1)
+    parent = torch.tensor([[1, 1, 3, 0], [2, 2, 0, 3]], device="cuda")
+    rows = (parent + 4 * torch.arange(2, device="cuda")[:, None]).flatten()
+    reorder = getattr(fm, call)
+    buf = torch.randn(8, 200, generator=g).cuda()
+    want = buf[rows]
+    reorder([buf[:, :100], buf[:, 100:]], parent)
+    assert torch.equal(buf, want)
+    want = buf.clone()
+    want[:, 150:190], want[:, 3:77] = buf[rows, 150:190], buf[rows, 3:77]
+    reorder([buf[:, 150:190], buf[:, 3:50], buf[:, 50:77]], parent)
+    assert torch.equal(buf, want)
+    wrap = torch.randn(8 * 20 + 30, generator=g).cuda()  # the second piece a row further on
+    a, b = torch.as_strided(wrap, (8, 12), (20, 1), 0), torch.as_strided(wrap, (8, 8), (20, 1), 32)
+    wa, wb = a[rows], b[rows]
+    reorder([b, a], parent)
+    assert torch.equal(a, wa) and torch.equal(b, wb)
+    # parent between the rows of a piece, as 16 bytes of one beam in a buffer of 64-bit numbers
+    own = torch.zeros(4, 12, dtype=torch.int64, device="cuda")
+    own[:, 8:] = torch.arange(16, device="cuda").view(4, 4)
+    near = torch.as_strided(own, (1, 4), (48, 1), 0)
+    near.copy_(torch.tensor([[3, 2, 2, 0]]))
+    part = own[:, 4:]
+    wp = part[near[0]]
+    reorder([part], near)
+    assert torch.equal(part, wp) and near.tolist() == [[3, 2, 2, 0]]
+    for bad in ([own], [own[:, 3:5]]):
+        with pytest.raises(fm.FmcaError):
+            reorder(bad, near)
+    for bad in ([buf[:, :100], buf[:, 99:]], [buf[:, 50:60], buf[:, :51]], [buf, buf[:, 7:8]],
+                [a, torch.as_strided(wrap, (8, 9), (20, 1), 32)],
+                [buf[:, :100], torch.as_strided(buf, (8, 10), (150, 1), 100)]):
+        with pytest.raises(fm.FmcaError):
+            reorder(bad, parent)
