@@ -600,6 +600,14 @@ def _on_or_none(name, t, dtype, shape, dev):
     return None if t is None else _on(name, t, dtype, shape, dev)
 
 
+def _written(*tensors) -> None:
+    """Tells autograd of a write that it did not see: a tensor that a backward pass has
+    saved is an error there."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _placed(name, t, stream, fn, *args):
     """fn(device index, stream handle, *args) with the device of tensor `t`
     current; `stream` defaults to torch's current stream there."""
@@ -908,6 +916,7 @@ def _decay_attention(dev, ptr, q, k, v, log_decay, lengths, state_in, o, state_o
         None if ws is None else _on("workspace", ws, _U8, ws.shape, dev),
         0 if ws is None else ws.numel(), ptr)
     _check(st, "flash_mca_decay_attention")
+    _written(o, state_out)
 
 
 def decay_attention(q, k, v, log_decay, state=None, scale: float = 1.0, lengths=None,
@@ -934,6 +943,7 @@ def _decay_step(dev, ptr, q, k, v, log_decay, state, o, scale):
         _on("state", state, _FP32, (s.B, s.H, s.dk, s.dv), dev),
         _on("o", o, q.dtype, (s.B, s.H, s.dv), dev), ctypes.byref(s), scale, dt, ptr)
     _check(st, "flash_mca_decay_step")
+    _written(state, o)
 
 
 def decay_step(q, k, v, log_decay, state, scale: float = 1.0, stream=None):
@@ -996,6 +1006,7 @@ def _beam_select(dev, ptr, logits, scores, finished, score, parent, token, pad):
         _on("score", score, _FP32, (B, n), dev), _on("parent", parent, _I64, (B, n), dev),
         _on("token", token, _I64, (B, n), dev), B, K, V, n, pad, _dtype_code(logits), ptr)
     _check(st, "flash_mca_beam_select")
+    _written(score, parent, token)
 
 
 def beam_select(logits, scores, n: int | None = None, finished=None, pad: int = 0, stream=None):
@@ -1027,6 +1038,7 @@ def _beam_reorder(dev, ptr, tensors, parent):
     st = lib.flash_mca_beam_reorder(pieces, len(tensors), _on("parent", parent, _I64, (B, K), dev),
                                     B, K, ptr)
     _check(st, "flash_mca_beam_reorder")
+    _written(*tensors)
 
 
 def beam_reorder(tensors, parent, stream=None) -> None:
@@ -1055,6 +1067,7 @@ def _decode_reorder(dev, ptr, state, parent, s, e, C, t, dtype):
                                       _on("parent", parent, _I64, (B, K), dev), B, K, s, e, C, t,
                                       dtype, ptr)
     _check(st, "flash_mca_decode_reorder")
+    _written(state)
 
 
 def flash_mca_device_status(stream=None) -> tuple[int, int]:

@@ -389,6 +389,12 @@ PyObject *vocab_loss_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // ------------------------------------------------------- generation with states
 
+// Tells autograd of a write that it did not see: a tensor that a backward pass has saved is an
+// error there.  (Inference tensors have no version.)
+void written(const at::Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // The strides (batch, token, head) of q, k or v; `lead` dimensions ahead of (heads,
 // d): 2, or 1 without tokens.
 void strides_of(const char *name, const at::Tensor &t, int lead, int64_t *out) {
@@ -502,6 +508,7 @@ PyObject *decay_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                       stream_of(dev));
         }),
         "flash_mca_decay_step");
+  written(tensor("state", a[4]));
   return THPVariable_Wrap(t[o]);
   END_HANDLE_TH_ERRORS
 }
@@ -582,6 +589,7 @@ PyObject *beam_reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
   if (all == nullptr) throw python_error();
   std::unique_ptr<PyObject, void (*)(PyObject *)> held(all, [](PyObject *o) { Py_DECREF(o); });
   std::vector<fmca_beam_piece> pieces;
+  std::vector<at::Tensor> tensors;  // (another thread may change the list while this one queues)
   for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(all); ++i) {
     const std::string name = "tensor " + std::to_string(i);
     const at::Tensor &t = tensor(name.c_str(), PySequence_Fast_GET_ITEM(all, i));
@@ -590,6 +598,7 @@ PyObject *beam_reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     const int64_t rows = B * K;
     pieces.push_back(fmca_beam_piece{t.data_ptr(), row * el,
                                      rows > 0 ? t.numel() / rows * el : 0});
+    tensors.push_back(t);
   }
   if (pieces.empty()) fail(PyExc_ValueError, "no tensors");
   const int Bi = size_of("B", B), Ki = size_of("K", K);
@@ -601,6 +610,7 @@ PyObject *beam_reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     st = flash_mca_beam_reorder(pieces.data(), count, pp, Bi, Ki, stream_of(dev));
   }
   check(st, "flash_mca_beam_reorder");
+  for (const at::Tensor &t : tensors) written(t);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

@@ -1,5 +1,6 @@
 """Calls of generation with states that are easily got wrong: strided logits of two
-dimensions, too many candidates, pieces whose rows lie inside one another."""
+dimensions, too many candidates, pieces whose rows lie inside one another,
+tensors that autograd has saved."""
 import pytest
 import torch
 
@@ -79,3 +80,52 @@ def test_rows_inside_one_another(call):
                 [buf[:, :100], torch.as_strided(buf, (8, 10), (150, 1), 100)]):
         with pytest.raises(fm.FmcaError):
             reorder(bad, parent)
+
+
+def test_writes_are_seen_by_autograd():
+    """A tensor that a backward pass has saved and a call overwrites is an error there."""
+    B, K, H, d = 1, 4, 2, 16
+    q = torch.randn(B * K, H, d, device="cuda")
+    ld = torch.tensor([-0.1, -0.2], device="cuda")
+    parent = torch.tensor([[1, 0, 2, 2]], device="cuda")
+    x = torch.randn(B, K, 50, device="cuda")
+    scores = torch.zeros(B, K, device="cuda")
+    idx = lambda: torch.zeros(B, K, dtype=torch.int64, device="cuda")  # noqa: E731
+    core = torch.zeros(fm.flash_mca_decode_state_bytes(B * K, 8, 8, 16, fm.FMCA_F32),
+                       dtype=torch.uint8, device="cuda")
+    state = torch.randn(B * K, H, d, d, device="cuda")
+    o = torch.empty(B * K, H, d, device="cuda")
+    row = torch.randn(B * K, 30, device="cuda")
+    half = torch.randn(B * K, 30, device="cuda")
+    out = torch.empty(B, K, device="cuda"), idx(), idx()
+    prompt = [t[None] for t in (q, q, q)]
+    po, ps = torch.empty(1, B * K, H, d, device="cuda"), torch.empty(1, H, d, d, device="cuda")
+    for written, call in [
+            ([state], lambda: fm.decay_step(q, q, q, ld, state)),
+            ([state, o], lambda: fm.flash_mca_decay_step(q, q, q, ld, state, o)),
+            ([po, ps], lambda: fm.flash_mca_decay_attention(*prompt, ld, None, None, po, ps, None)),
+            ([po], lambda: fm.flash_mca_decay_attention(*prompt, ld, None, ps, po, None, None)),
+            ([row, half], lambda: fm.beam_reorder([row, half[:, :7]], parent)),
+            ([row, half], lambda: fm.flash_mca_beam_reorder([row, half[:, :7]], parent)),
+            (list(out), lambda: fm.flash_mca_beam_select(x, scores, None, *out)),
+            ([core], lambda: fm.flash_mca_decode_reorder(core, parent, 8, 8, 16, 3, fm.FMCA_F32))]:
+        before = [t._version for t in written]
+        call()
+        assert all(t._version > v for t, v in zip(written, before))
+    read = [q, ld, parent, x, scores]
+    assert not any(t._version for t in read)
+    w = torch.randn(B * K, H, d, d, device="cuda", requires_grad=True)
+    y = (w * state).sum()
+    fm.decay_step(q, q, q, ld, state)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    v = state._version
+    with pytest.raises(ValueError):
+        fm.decay_step(q, q, q, ld, state[:1])
+    assert state._version == v  # a call that is refused writes nothing
+    with torch.inference_mode():  # tensors without a version
+        s = torch.zeros_like(state)
+        fm.decay_step(q, q, q, ld, s)
+        fm.beam_reorder([s], parent)
+        fm.flash_mca_decay_step(q, q, q, ld, s, o)
+    torch.cuda.synchronize()
