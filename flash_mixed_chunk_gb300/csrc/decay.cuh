@@ -13,21 +13,22 @@ namespace {
 
 // log2 of a head's decay, as a sum of two floats: the exponent of a far position is a
 // product with up to 2^31.  (64-bit arithmetic, whose pipe is a trickle here, costs a
-// block that forms powers microseconds.)  A log decay of -inf (nothing is kept)
-// becomes one whose first power is 0 already, so that the power 0 is 1 and not a NaN.
+// block that forms powers microseconds.)  A log decay of -inf (nothing is kept) becomes one
+// whose first power is 0 already, and one of +inf one whose first power overflows, so that the
+// power 0 is 1 and not a NaN.
 struct DecayRate {
   float hi, lo;
 };
 __device__ __forceinline__ DecayRate decay_rate(float log_decay) {
-  const float x = log_decay < -1e6f ? -1e6f : log_decay;
+  const float x = log_decay < -1e6f ? -1e6f : log_decay > 1e6f ? 1e6f : log_decay;  // (or NaN)
   constexpr float kHi = 1.44269502162933349609f, kLo = 1.92596299112661746887e-8f;  // log2(e)
   DecayRate r;
   r.hi = x * kHi;
   r.lo = fmaf(x, kLo, fmaf(x, kHi, -r.hi));
-  if (isinf(r.hi)) r.lo = 0.f;
   return r;
 }
-// 2^(rate n), n >= 0: the exponent's rounding goes back in as a factor.
+// 2^(rate n), n >= 0: the exponent's rounding goes back in as a factor (not into an infinity,
+// which would become a NaN; a power overflows from a finite exponent on, 128).
 __device__ __forceinline__ float decay_power(const DecayRate &r, int n) {
   const float a = (float)(n & ~4095), b = (float)(n & 4095);  // exactly
   const float pa = a * r.hi, pb = b * r.hi;
@@ -35,7 +36,7 @@ __device__ __forceinline__ float decay_power(const DecayRate &r, int n) {
   const float rest = (pa - (e - back)) + (pb - back) + fmaf(a, r.hi, -pa) + fmaf(b, r.hi, -pb) +
                      (float)n * r.lo;
   const float p = exp2f(e);
-  return isinf(e) ? p : fmaf(p, rest * 0.693147180559945f, p);
+  return isinf(p) ? p : fmaf(p, rest * 0.693147180559945f, p);
 }
 // The same as a sum of two floats, n up to 128: a state is multiplied by one power once a
 // chunk, and a factor in 32 bits would be off by half a step in every one of them.  2^x = 2^k
