@@ -24,7 +24,6 @@
 // of the work stays under the state's from dk 32 on.  A step of 64 sequences of 12 heads of 128
 // takes 16.5 us, 101 MB at 6.1 TB/s (91 % of a copy's rate); one sequence's 2.1 us on the
 // device, a launch and three trips to memory.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -41,15 +40,11 @@ constexpr int C = 32;         // tokens of a chunk
 constexpr int DVT = 64;       // columns of v of a unit
 constexpr int VS = DVT + 4;   // row of the v tile in shared memory
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
 // ------------------------------------------------------------------- prompts
 
 constexpr int WS = C + 4;  // row of the weights
 static_assert(C == 32 && VS == 68 && WS == 36, "decay_floats counts these");
+static_assert(decay_floats(1) >= 4 * DVT + 2 * kThreads, "decay_tokens' state and sums");
 __device__ __forceinline__ float4 &at4(float *p) { return *reinterpret_cast<float4 *>(p); }
 __device__ __forceinline__ void fma4(float x, const float4 &y, float4 &z) {
   z.x = fmaf(x, y.x, z.x), z.y = fmaf(x, y.y, z.y);
@@ -79,6 +74,11 @@ __global__ void __launch_bounds__(kThreads, 3)
   const size_t slot = (size_t)dk * DVT;
   float *own = slots + (((size_t)w.b * a.H + w.h) * sp.nvt + w.vt) * sp.S * slot;
   const DecayRate rate = decay_rate(a.log_decay[w.h]);
+  if (decay_grows(rate, w.len)) {
+    if (!LOCAL && w.s == 0)
+      decay_tokens<T, kThreads, DVT>(a, w.b, w.h, w.vt, w.len, decay_power(rate, 1), sm);
+    return;
+  }
   if (tid <= C) pw[tid] = decay_power(rate, tid);
   __shared__ float2 whole;
   __shared__ float from[64];  // the segments' powers at this one's start

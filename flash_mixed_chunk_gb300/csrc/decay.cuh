@@ -2,6 +2,7 @@
 // a head's decay, the cut of a sequence into segments, and their workspace.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -94,6 +95,75 @@ __device__ __forceinline__ DecayUnit decay_unit(const DecayArgs &a, const DecayS
 // that is returned (a sequence without tokens: its first segment's).
 __device__ __forceinline__ bool decay_last(const DecayUnit &w, int L) {
   return w.s == (w.len == 0 ? 0 : (w.len - 1) / L);
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Whether a head grows so much over a sequence that the chunked form does not hold: it
+// multiplies by powers of up to the sequence's length, and one that leaves the range makes a NaN
+// of a state, key or score of 0 and an infinity of a small one, where the recurrence, whose
+// factors come one at a time, is finite.  Up to 2^100 the operands have 2^28 of room, and behind
+// it speed is not what counts: 2 x 8192 tokens of 12 heads of 128 take 36 ms a token at a time,
+// and 80 us in chunks.
+__device__ __forceinline__ bool decay_grows(const DecayRate &r, int len) {
+  return r.hi * (float)len > 100.f;
+}
+// The recurrence itself, for such a head: a whole sequence's unit by one block of NT threads, W
+// columns of v, from state_in to state_out, with zeros behind the end.  The state lies in shared
+// memory, sm: [dk][W], behind it the NT threads' sums of two tokens.  A thread has a column and every NT / W-th
+// row, the rows' sums are joined in a fixed order.
+template <typename T, int NT, int W>
+__device__ __noinline__ void decay_tokens(const DecayArgs &a, int b, int h, int vt, int len,
+                                          float lam, float *sm) {
+  constexpr int RG = NT / W, U = NT > 256 ? 4 : 2;  // (more cost the callers registers)
+  static_assert(NT % W == 0, "whole columns");
+  const int tid = threadIdx.x, c = tid % W, r0 = tid / W, col = vt * W + c;
+  const bool in = col < a.dv;
+  float *const st = sm + c, *part = sm + a.dk * W + c, *next = part + NT;
+  const size_t at = ((size_t)b * a.H + h) * a.dk * (size_t)a.dv + col;
+  for (int d = r0; d < a.dk; d += RG)
+    st[d * W] = in && a.state_in != nullptr ? a.state_in[at + (size_t)d * a.dv] : 0.f;
+  const T *q = static_cast<const T *>(a.q) + b * a.qs[0] + (h / (a.H / a.Hq)) * a.qs[2];
+  const T *k = static_cast<const T *>(a.k) + b * a.ks[0] + (h / (a.H / a.Hk)) * a.ks[2];
+  const T *v = static_cast<const T *>(a.v) + b * a.vs[0] + (h / (a.H / a.Hv)) * a.vs[2] + col;
+  T *o = static_cast<T *>(a.o) + ((size_t)b * a.T * a.H + h) * (size_t)a.dv + col;
+  for (int t = 0; t < len; ++t, q += a.qs[1], k += a.ks[1], v += a.vs[1]) {
+    const float x = in ? to_f(__ldg(v)) : 0.f;
+    float sum = 0.f;
+    for (int d0 = r0; d0 < a.dk; d0 += U * RG) {  // U rows' loads on their way at once
+      T key[U], ask[U];
+      float e[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (d0 + u * RG < a.dk) {
+          key[u] = __ldg(k + d0 + u * RG), ask[u] = __ldg(q + d0 + u * RG);
+          e[u] = st[(d0 + u * RG) * W];
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (d0 + u * RG < a.dk) {
+          e[u] = fmaf(lam, e[u], to_f(key[u]) * x);
+          st[(d0 + u * RG) * W] = e[u];
+          sum = fmaf(to_f(ask[u]), e[u], sum);
+        }
+    }
+    part[r0 * W] = sum;
+    __syncthreads();
+    if (r0 == 0 && in) {
+      float y = 0.f;
+      for (int i = 0; i < RG; ++i) y += part[i * W];
+      put(o + (size_t)t * a.H * a.dv, a.scale * y);
+    }
+    float *const last = part;
+    part = next, next = last;
+  }
+  if (!in) return;
+  for (int t = len + r0; t < a.T; t += RG) put(o + (size_t)t * a.H * a.dv, 0.f);
+  if (a.state_out != nullptr)
+    for (int d = r0; d < a.dk; d += RG) a.state_out[at + (size_t)d * a.dv] = st[d * W];
 }
 
 }  // namespace

@@ -73,6 +73,7 @@ __host__ __device__ inline uint32_t da_slot(int ka, int va) {
 __host__ __device__ inline uint32_t da_state_bytes(int ka, int va) {
   return 8192u * (uint32_t)(ka * va);
 }
+static_assert(4 * (128 * 128 + 2 * DA_THREADS) <= DA_SMEM, "decay_tokens' state and sums");
 __host__ __device__ inline uint32_t da_term_bytes(int ka) { return DA_ATOM * (uint32_t)ka; }
 // The places of a ring each of q, k and v tiles (LOCAL: of k and v, and no state tile).
 // One ring of all three in turn would have k wait for the place that outputs leave last.
@@ -207,6 +208,16 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
   uint8_t *const terms = smem + n_slots * slot_bytes;
   uint8_t *const s_tile = terms + da_term_bytes(ka);
   const DecayRate rate = decay_rate(a.log_decay[w.h]);
+  if (decay_grows(rate, w.len)) {
+    if (!first) {
+      griddep_wait();
+      if (!LOCAL) griddep_launch_dependents();
+    }
+    if (!LOCAL && w.s == 0)
+      decay_tokens<__nv_bfloat16, DA_THREADS, 128>(a, w.b, w.h, w.vt, w.len, decay_power(rate, 1),
+                                                   reinterpret_cast<float *>(smem));
+    return;
+  }
   const int end = w.t1 < w.len ? w.t1 : w.len;
   // (LOCAL: a segment that nothing comes behind is nobody's start)
   const int chunks = end <= w.t0 || (LOCAL && w.t1 >= w.len)

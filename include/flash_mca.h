@@ -489,8 +489,10 @@ fmca_status flash_mca_vocab_loss_backward(const void *X, const void *W, const in
  *            contiguous, the others at the strides that `shape` gives (columns of
  *            one projection's output, say; 0 and overlapping rows are allowed).
  *            Hq, Hk and Hv divide H: head h reads heads h / (H / Hq) and so on.
- *   log_decay  device float32 [H], <= 0 (-inf: nothing is kept; above 0 the state
- *            grows, and overflows as the formula does)
+ *   log_decay  device float32 [H], <= 0 (-inf: nothing is kept).  Above 0 the state
+ *            grows, and overflows where the recurrence in fp32 does, a token at a
+ *            time: a head whose powers over a sequence's tokens pass 2^100 is run so,
+ *            some microseconds a token
  *   lengths  device int32 [B] or NULL: sequence b has its first lengths[b] tokens
  *            (cut to 0 .. T); what lies behind, NaN included, reaches nothing, its
  *            outputs are 0, and the state is the one after lengths[b] tokens
