@@ -10,18 +10,21 @@
 // n largest as one sorted list across its lanes (64-bit keys: the value in an order
 // of unsigned numbers, then the complement of the index).  Within a beam the order
 // of the logits is that of the candidates, so no candidate is formed before the
-// last step, which compares the n best of every beam in 64 bits: in 32 the rounding
-// of c would decide between beams.  One launch: a cluster of blocks is one batch
-// element, and joins its lists through distributed shared memory, in a fixed order.
-// Rows of one call are cut the same way, so that equal rows give equal sums and the
-// tie goes to the lower beam.
+// last step, which compares the n best of every beam in 64 bits.  lse comes from fp32
+// sums first, good to some 1e-6; where candidates of two beams are closer than that, their
+// rows are summed once more, to 2^-29, before it decides (lse_near).  One launch: a
+// cluster of blocks is one batch element, and joins its lists through distributed shared
+// memory, in a fixed order.  Rows of one call are cut the same way, so that equal rows
+// give equal sums and the tie goes to the lower beam.
 //
-// Measured: one element, 4 beams of 32000 in bf16, 9.3 us (2 of the launch, the rest a chain:
-// a row's part, the lists of a block, of the cluster, of the beams); 64 x 8 of 50001 in fp32,
-// 16 candidates, none finished, 31 us, 102 MB at 3.3 TB/s (49 % of a copy's rate): an SM with
-// work issues in half of its cycles, about 20 instructions a logit, half of them to load,
-// compare and sum it, half for the lists, which a warp of 12 parts of a row changes in most of
-// them; and 256 blocks do not spread evenly over 152 SMs.  64 x 8 of 32000 in bf16 20 us.
+// Measured (calls replayed from a graph): one element, 4 beams of 32000 in bf16, 10.5 us (2 of
+// the launch, the rest a chain: a row's part, the lists of a block, of the cluster, of the beams,
+// 0.7 the look for close ones); 64 x 8 of 50001 in fp32, 16 candidates, a fifth of the beams
+// finished, 30.3 us, 82 MB at 2.7 TB/s (40 % of a copy's rate), and 44 where an element has
+// close candidates (4 of 60 inputs): an SM with work issues in half of its cycles, about 20
+// instructions a logit, half of them to load, compare and sum it, half for the lists, which a
+// warp of 12 parts of a row changes in most of them; and 256 blocks do not spread evenly over
+// 152 SMs.  64 x 8 of 32000 in bf16 20.6 us.
 //
 // beam_reorder: rows of up to 16 arrays, t[b, k] = t[b, parent[b, k]] in place, one
 // launch.  A thread holds its bytes of every beam that changes in registers before
@@ -35,6 +38,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "launch.h"
@@ -120,17 +124,16 @@ __device__ __forceinline__ void merge_pairs(uint64_t &c, uint64_t &at, uint64_t 
   }
 }
 
-// exp(x), x <= 0 (what is under 2^-126 is 0)
+// exp(x), x <= 2 (what is under 2^-126 is 0)
 __device__ __forceinline__ float exp_below(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
   return y;
 }
 
-// log(s) of a sum, s >= 1, to about 1e-9, where the sum itself is good to 1e-7: s = 2^e f, f
-// within a half power of 1, and log f = 2 atanh z, z = (f - 1) / (f + 1), as a float, its rest
-// and the series behind it.  (The double log took 1 us of the smallest call's 8, 4 of 34 at 64 x
-// 8 of 50001.)
+// log(s) of a sum, s >= 1/8, to about 1e-9: s = 2^e f, f within a half power of 1, and log f = 2
+// atanh z, z = (f - 1) / (f + 1), as a float, its rest and the series behind it.  (The double log
+// took 1 us of the smallest call's 8, 4 of 34 at 64 x 8 of 50001.)
 __device__ __forceinline__ double log_sum(float s) {
   const uint32_t u = __float_as_uint(s);
   int e = (int)(u >> 23) - 127;
@@ -173,16 +176,52 @@ __device__ __forceinline__ uint64_t merge_lists(const uint64_t *lists, int count
   return list;
 }
 
-// (maximum, sum of exp(z - maximum)) of two parts; a maximum that is -inf has
-// nothing, one that is +inf or NaN makes the row's NaN.
+// What a part of a row is measured from, m, and its sum of exp(z - m).  m is -inf where there is
+// nothing yet, and +inf or NaN where the row has no candidates; else the largest logit so far is
+// between m and m + kSlack.
 struct Part {
   float m, s;
 };
-__device__ __forceinline__ Part join(const Part &a, const Part &b) {
-  const float m = max_nan(a.m, b.m);
-  if (m == -kInf) return Part{m, 0.f};
-  return Part{m, a.s * expf(a.m - m) + b.s * expf(b.m - m)};
+constexpr float kSlack = 2.f;
+// Eight lanes' parts as one, in each of them: one factor for each, and the sums as a tree.
+__device__ __forceinline__ Part join8(const Part &p) {
+  float m = p.m;
+#pragma unroll
+  for (int off = 4; off > 0; off /= 2) m = max_nan(m, __shfl_xor_sync(kAll, m, off));
+  float s = p.m == -kInf ? 0.f : p.s * expf(p.m - m);
+#pragma unroll
+  for (int off = 4; off > 0; off /= 2) s += __shfl_xor_sync(kAll, s, off);
+  return Part{m, s};
 }
+static_assert(kWarps == 8 && kBeamCluster == 8, "parts that join8 joins");
+
+// s + x as a sum of two floats, the rest added to `rest`.
+__device__ __forceinline__ void add2(float &s, float &rest, float x) {
+  const float t = s + x, y = t - s;
+  rest += (s - (t - y)) + (x - y);
+  s = t;
+}
+// exp(z - m) of N logits from AT on, as a tree (one after the other, equal terms would all be
+// rounded to the same side).
+template <int AT, int N>
+__device__ __forceinline__ float sum_exp(const float (&z)[E], float m) {
+  if constexpr (N == 1)
+    return exp_below(z[AT] - m);
+  else
+    return sum_exp<AT, N / 2>(z, m) + sum_exp<AT + N / 2, N / 2>(z, m);
+}
+
+// How far a row's log sum of exponentials may be off, and what is done about it.  In u = 2^-24:
+// of a term the difference z - m, its product with log2(e) and that constant 2.22 |z - m|, and
+// ex2.approx 4; where m moves, by more than kSlack, 5 for the factor.  By its share of the sum a
+// row's term lies ln V under the maximum at most, on average (the entropy is at most ln V, and
+// the sum at least its largest term), so these are 2.22 (ln V + 6) + 4 + 5 (ln V / 2 + 2).  The
+// tree of a task 5, the tasks as two floats 1, the lanes 6, the joins of warps and of blocks 6.4
+// each.  In all under (54 + 5 ln V) u, 6.5e-6 at 50000.
+// That is too much between beams: candidates of different ones may lie closer.  So where two that
+// matter are within twice as much of each other, their beams' rows are summed again, to 2^-29
+// (exact_sum).
+inline double lse_near(int V) { return 2.0 * (54.0 + 5.0 * log((double)V)) / (1 << 24); }
 
 // ------------------------------------------------------------------- the logits
 
@@ -254,7 +293,99 @@ struct SelectArgs {
   int64_t *parent, *token;
   int K, V, n, pad;
   int group;  // warps of a cluster that share a beam (a power of 2)
+  double near;  // candidates of different beams that are closer may be in the wrong order
 };
+
+// sum exp(z - m) to 2^-29 over the logits from `first` on, `step` apart: exp(x) = 2^(N / 64)
+// exp(r), N = rint(64 x / ln 2), with x = z - m and r = x - N ln(2) / 64 as sums of two floats,
+// the powers from a table of two floats, the sum in two floats.  What is off: r by 2^-31, as p =
+// exp(r) - 1 and the power's product with it are.  m: within kSlack under the row's maximum.
+// (About 45 instructions a logit.)
+template <typename T>
+__device__ __forceinline__ double exact_sum(const T *__restrict__ row, int V, int first, int step,
+                                            float m, const float2 *powers) {
+  constexpr float kN = 92.3324826f, kA = 1420.f / 131072, kB = -3.3155381258556e-06f;
+  constexpr int U = 8;  // logits on their way while as many are gone through
+  float next[U], s = 0.f, rest = 0.f;
+  const auto load = [&](int64_t at) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      next[u] = at + u * step < V ? to_f(__ldg(row + at + u * step)) : -kInf;
+  };
+  load(first);
+  for (int64_t i = first; i < V; i += U * step) {
+    float z[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) z[u] = next[u];
+    load(i + U * step);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float d = z[u] - m, y = d - z[u], x = fmaxf(d, -60.f);  // 2^-86 of the sum: nothing
+      const float x_rest = d > -60.f ? (z[u] - (d - y)) - (m + y) : 0.f;
+      const float n = rintf(x * kN);
+      const float r = fmaf(-n, kB, fmaf(-n, kA, x)) + x_rest;  // (n kA has 24 bits)
+      const float p = fmaf(r * r, fmaf(r, fmaf(r, 1.f / 24, 1.f / 6), 0.5f), r);
+      const int k = (int)n;
+      const float2 w = powers[k & 63];
+      const float up = __int_as_float(((k >> 6) + 127) << 23);
+      const float hi = w.x * up, lo = fmaf(w.x, p, w.y) * up, term = hi + lo;
+      add2(s, rest, term);
+      rest += lo - (term - hi);
+    }
+  }
+  return (double)s + (double)rest;
+}
+
+// The two halves of a barrier over the cluster's threads (those that have ended do not
+// count); what was written before the first is there behind the second.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The log sums of the beams in `which`, again and to 2^-29, by all blocks of the cluster (behind
+// a barrier of theirs): into the first one's lse.  mem: 7 kPool words of every block's shared
+// memory.  Out of line: in it, the kernel's main path was 0.9 to 2.8 us longer.
+template <typename T>
+__device__ __noinline__ void settle(const SelectArgs &a, int64_t b, unsigned which,
+                                    const float *from, double *lse, uint64_t *mem, int rank,
+                                    int NC) {
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  double *const sums = reinterpret_cast<double *>(mem);  // [K][kBeamCluster], the first block's
+  double *const part = sums + kBeamMax * kBeamCluster;   // the warps'
+  float2 *const powers = reinterpret_cast<float2 *>(part + kWarps);
+  static_assert(kBeamMax * kBeamCluster + kWarps + 64 <= (kWarps - 1) * kPool, "mem");
+  if (tid < 64) {
+    const double p = exp2((double)tid / 64);
+    powers[tid] = make_float2((float)p, (float)(p - (double)(float)p));
+  }
+  __syncthreads();
+  for (unsigned w = which; w != 0; w &= w - 1) {
+    const int k = __ffs(w) - 1;
+    const T *row = static_cast<const T *>(a.logits) + (b * a.K + k) * a.row;
+    double sum = exact_sum<T>(row, a.V, rank * kThreads + tid, NC * kThreads, from[k], powers);
+#pragma unroll
+    for (int off = 16; off > 0; off /= 2) sum += __shfl_xor_sync(kAll, sum, off);
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      sum = 0.0;
+      for (int i = 0; i < kWarps; ++i) sum += part[i];
+      cg::this_cluster().map_shared_rank(sums, 0)[k * kBeamCluster + rank] = sum;
+    }
+    __syncthreads();
+  }
+  cluster_arrive();
+  if (rank != 0) return;
+  cluster_wait();
+  if (tid < a.K && which >> tid & 1) {
+    double sum = 0.0;
+    for (int r = 0; r < NC; ++r) sum += sums[tid * kBeamCluster + r];
+    lse[tid] = (double)from[tid] + log(sum);
+  }
+  __syncthreads();
+}
 
 // Shared memory of a block, in words of 64 bits: the n keys and the part of every (beam,
 // warp), the same of every (beam, block) in the cluster's first block, and the nth
@@ -274,14 +405,6 @@ __host__ __device__ inline SelectSmem select_smem(int K, int n) {
 }
 static_assert(kWarps * kPool >= 2 * (kWarps / 2) * 32, "half the warps' lists of pairs");
 
-// The two halves of a barrier over the cluster's threads (those that have ended do not
-// count); what was written before the first is there behind the second.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // The next float above v (finite).
 __device__ __forceinline__ float nextafter_up(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
@@ -293,6 +416,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     beam_select(const __grid_constant__ SelectArgs a) {
   extern __shared__ uint64_t sm64[];
   __shared__ uint64_t pool[kWarps][kPool];
+  // what the end needs of every beam: its log sum and what its row is measured from; the beams
+  // whose order is not sure, the values that are as close as that to the last place's, its beam
+  __shared__ double lse[kBeamMax];
+  __shared__ float from[kBeamMax];
+  __shared__ unsigned unsure;
+  __shared__ uint64_t border[2];
+  __shared__ int border_beam;
   const int K = a.K, n = a.n;
   const SelectSmem at = select_smem(K, n);
   uint64_t *keys = sm64 + at.keys;                               // [K][kWarps][n]
@@ -313,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     parts[i] = Part{-kInf, 0.f};
     tops[i] = 0;
   }
+  if (tid == 0) unsure = 0;
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
@@ -327,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   for (int k = me / a.group; k < K; k += groups) {
     uint64_t list = 0;  // 0: no key
-    Part sum{-kInf, 0.f};
+    float m = -kInf, s = 0.f, rest = 0.f;
     if (isfinite(scores[k]) && !(finished != nullptr && finished[k])) {
       const T *row = static_cast<const T *>(a.logits) + (b * K + k) * a.row;
       Task<T, BYTES> task;
@@ -344,17 +475,18 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int off = 16; off > 0; off /= 2)
           most = max_nan(most, __shfl_xor_sync(kAll, most, off));
-        const float m = max_nan(sum.m, most);
-        if (!(m < kInf)) {  // NaN or +inf: this row has no candidates
-          sum.m = m;
+        const float high = max_nan(m, most);
+        if (!(high < kInf)) {  // NaN or +inf: this row has no candidates
+          m = high;
           break;
         }
-        if (m == -kInf) continue;
-        float add = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) add += exp_below(z[i] - m);
-        sum.s = (sum.s == 0.f ? 0.f : sum.s * exp_below(sum.m - m)) + add;
-        sum.m = m;
+        if (high == -kInf) continue;
+        if (high > m + kSlack) {
+          const float f = exp_below(m - high);
+          s = __fmul_rn(s, f), rest = __fmul_rn(rest, f);
+          m = high;
+        }
+        add2(s, rest, sum_exp<0, E>(z, m));
 
         // What may enter the list: with a full one whatever is above its last (an
         // equal value here has a higher index); before that whatever reaches the
@@ -449,61 +581,117 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) tops[k * kWarps + warp] = (uint32_t)(own >> 32);
       }
     }
+    s += rest;
 #pragma unroll
-    for (int off = 16; off > 0; off /= 2) sum.s += __shfl_xor_sync(kAll, sum.s, off);
+    for (int off = 16; off > 0; off /= 2) s += __shfl_xor_sync(kAll, s, off);
     if (lane < n) keys[(k * kWarps + warp) * n + lane] = list;
-    if (lane == 0) parts[k * kWarps + warp] = sum;
+    if (lane == 0) parts[k * kWarps + warp] = Part{m, s};
   }
   __syncthreads();
   // the block's list of every beam, into the first block's memory
   cluster_wait();
   for (int k = warp; k < K; k += kWarps) {
     const uint64_t list = merge_lists(keys + (size_t)k * kWarps * n, kWarps, n, n, lane);
-    Part sum{-kInf, 0.f};
-    for (int w = 0; w < kWarps; ++w) {
-      const Part p = parts[k * kWarps + w];
-      if (p.m != -kInf) sum = join(sum, p);  // (else a warp without a part of this row)
-    }
+    const Part sum = join8(parts[k * kWarps + lane % kWarps]);
     if (lane < n)
       cluster.map_shared_rank(keys_got, 0)[(k * kBeamCluster + rank) * n + lane] = list;
     if (lane == 0) cluster.map_shared_rank(parts_got, 0)[k * kBeamCluster + rank] = sum;
   }
   __syncwarp();
   cluster_arrive();
-  if (rank != 0) return;  // nobody reads this block's memory
   cluster_wait();
-  {
-    // a warp's beams: the n best of each as candidates, and of them the n best
-    uint64_t best = 0, where = 0;  // a lane's place in the list, by value, then the lower index
+  // The first block joins the lists.  The others wait to hear that nothing is unsure, or help.
+  uint64_t *const lists = keys, *const found = keys + K * n;  // [K][n] each: keys, candidates
+  const auto done = [&](int k) { return finished != nullptr && finished[k]; };
+  if (rank == 0) {
     for (int k = warp; k < K; k += kWarps) {
       const uint64_t list = merge_lists(keys_got + (size_t)k * kBeamCluster * n, NC, n, n, lane);
-      Part sum{-kInf, 0.f};
-      for (int r = 0; r < NC; ++r) {
-        const Part p = parts_got[k * kBeamCluster + r];
-        if (p.m != -kInf) sum = join(sum, p);
+      const Part sum =
+          join8(lane % 8 < NC ? parts_got[k * kBeamCluster + lane % 8] : Part{-kInf, 0.f});
+      if (lane < n) lists[k * n + lane] = isfinite(sum.m) ? list : 0;
+      if (lane == 0) {
+        lse[k] = (double)sum.m + log_sum(sum.s);
+        from[k] = sum.m;
       }
-      uint64_t c = 0, flat = (uint64_t)k * a.V + key_index(list);
-      if (finished != nullptr && finished[k]) {
-        if (lane == 0 && isfinite(scores[k])) c = order_of((double)scores[k]);
-        flat = (uint64_t)k * a.V + a.pad;
-      } else if (list != 0 && isfinite(sum.m)) {
-        c = order_of((double)scores[k] +
-                     ((double)key_value(list) - ((double)sum.m + log_sum(sum.s))));
-      }
-      if (lane >= n) c = 0;
-      merge_pairs(best, where, c, flat, lane);
     }
-    // the warps' lists, pair by pair
-    uint64_t *list_c = &pool[0][0], *list_at = list_c + kWarps / 2 * 32;
-    for (int half = kWarps / 2; half > 0; half /= 2) {
-      __syncthreads();
-      if (warp >= half && warp < 2 * half) {
-        list_c[(warp - half) * 32 + lane] = best;
-        list_at[(warp - half) * 32 + lane] = where;
+    __syncwarp();
+  }
+  for (bool again = false;; again = true) {
+    uint64_t best = 0, where = 0;  // a lane's place in the list, by value, then the lower index
+    if (rank == 0) {
+      // a warp's beams: the n best of each as candidates, and of them the n best
+      for (int k = warp; k < K; k += kWarps) {
+        const uint64_t list = lane < n ? lists[k * n + lane] : 0;
+        uint64_t c = 0, flat = (uint64_t)k * a.V + key_index(list);
+        if (done(k)) {
+          if (lane == 0 && isfinite(scores[k])) c = order_of((double)scores[k]);
+          flat = (uint64_t)k * a.V + a.pad;
+        } else if (list != 0) {
+          c = order_of((double)scores[k] + ((double)key_value(list) - lse[k]));
+        }
+        if (lane < n) found[k * n + lane] = c;
+        merge_pairs(best, where, c, flat, lane);
       }
-      __syncthreads();
-      if (warp < half)
-        merge_pairs(best, where, list_c[warp * 32 + lane], list_at[warp * 32 + lane], lane);
+      // the warps' lists, pair by pair
+      uint64_t *list_c = &pool[0][0], *list_at = list_c + kWarps / 2 * 32;
+      for (int half = kWarps / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (warp >= half && warp < 2 * half) {
+          list_c[(warp - half) * 32 + lane] = best;
+          list_at[(warp - half) * 32 + lane] = where;
+        }
+        __syncthreads();
+        if (warp < half)
+          merge_pairs(best, where, list_c[warp * 32 + lane], list_at[warp * 32 + lane], lane);
+      }
+      if (!again && K > 1) {
+        // Neighbours of different beams in the list that are too close, and candidates of other
+        // beams that are too close to its last: both beams are unsure.  (Whatever else could
+        // change places has such a pair between.)
+        if (warp == 0) {
+          const int beam = (int)(where / (uint32_t)a.V);
+          const double c = value_of(best);
+          const uint64_t least = order_of(c - a.near), next = __shfl_down_sync(kAll, best, 1);
+          const int beam2 = __shfl_down_sync(kAll, beam, 1);
+          unsigned mask = 0;
+          if (lane + 1 < n && next != 0 && beam != beam2 && next >= least)
+            mask = (done(beam) ? 0u : 1u << beam) | (done(beam2) ? 0u : 1u << beam2);
+          mask = __reduce_or_sync(kAll, mask);
+          if (lane == 0) unsure = mask;
+          if (lane == n - 1) {
+            border[0] = least, border[1] = order_of(c + a.near);
+            border_beam = best != 0 ? beam : -1;  // an empty place: nothing is left out
+          }
+        }
+        __syncthreads();
+        unsigned mask = unsure;
+        if (border_beam >= 0 && lane < n)
+          for (int k = warp; k < K; k += kWarps) {
+            const uint64_t c = found[k * n + lane];
+            if (k != border_beam && c >= border[0] && c <= border[1])
+              mask |= (done(k) ? 0u : 1u << k) | (done(border_beam) ? 0u : 1u << border_beam);
+          }
+        if (__syncthreads_or((int)mask)) {
+          if (mask != 0) atomicOr(&unsure, mask);
+          __syncthreads();
+          for (int i = tid; i < NC * K; i += kThreads) {
+            if (i % K == 0) *cluster.map_shared_rank(&unsure, i / K) = unsure;
+            cluster.map_shared_rank(from, i / K)[i % K] = from[i % K];
+          }
+        }
+      }
+    }
+    if (!again) {
+      __syncwarp();
+      cluster_arrive();
+      if (rank != 0) cluster_wait();
+      if (unsure != 0) {
+        if (rank == 0) cluster_wait();
+        settle<T>(a, b, unsure, from, lse, &pool[1][0], rank, NC);
+        if (rank != 0) return;
+        continue;
+      }
+      if (rank != 0) return;
     }
     if (warp == 0) {
       if (best != 0 && lane < n) {
@@ -516,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         a.token[b * n + lane] = a.pad;
       }
     }
+    return;
   }
 }
 
@@ -597,7 +786,8 @@ int select(const SelectArgs &a, int B, int NC, cudaStream_t stream) {
 int launch_beam_select(const void *logits, int64_t row, const float *scores,
                        const uint8_t *finished, float *score, int64_t *parent, int64_t *token,
                        int B, int K, int V, int n, int pad, int bf16, cudaStream_t stream) {
-  SelectArgs a{logits, row, scores, finished, score, parent, token, K, V, n, pad, 0};
+  SelectArgs a{logits, row, scores, finished, score, parent, token, K, V, n, pad, 0,
+               lse_near(V)};
   // a beam's row has NT warps' work; as many blocks as run at once (two an SM), no more
   // than have any.  (One element of 4 beams of 32000: 10.0 us on 8 blocks, 20.7 on one.)
   const int64_t NT = ((int64_t)V + TASK - 1) / TASK;

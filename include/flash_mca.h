@@ -545,8 +545,12 @@ fmca_status flash_mca_decay_step(const void *q, const void *k, const void *v,
  *   score     device float32 [B][n];  parent, token  device int64 [B][n]
  * A beam whose score is not finite, or whose logits hold a NaN, +inf or nothing above
  * -inf, has no candidate, nor has a logit of -inf.  Places without a candidate (the
- * last ones) hold score -inf, parent (place mod K) and token `pad`.  Candidates are
- * compared in 64 bits.  One launch, nothing allocated; deterministic.
+ * last ones) hold score -inf, parent (place mod K) and token `pad`.  A row's logarithm
+ * is good to (54 + 5 ln V) 2^-24, and so is a score but for its own rounding; where
+ * candidates of two beams lie closer than twice that (equal ones too, as of equal
+ * rows), their rows' logarithms are formed again, to 2^-29, and the order is that of
+ * sums in 64 bits with these: 10 to 15 us more, and for many beams more than that.
+ * One launch, nothing allocated; deterministic.
  * Sizes: B, V >= 1, 1 <= K, n <= 32, 0 <= pad < V.  Arrays are aligned to their
  * elements; outputs must not overlap inputs or each other.
  */
