@@ -196,3 +196,29 @@ def test_close_rows_with_masks_and_in_a_captured_call():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, got))
+
+
+@pytest.mark.parametrize("B,K,V", [(1, 32, 3000), (7, 9, 2500), (60, 2, 4001), (100, 5, 900),
+                                   (200, 32, 1100)])
+def test_close_candidates_however_an_element_is_cut(B, K, V):
+    """All beams' best candidates within some 1e-6, on clusters of 8 blocks down to one."""
+    g = torch.Generator().manual_seed(B)
+    z = torch.randn(B, K, V + 3, generator=g).to(BF16)[:, :, 3:]
+    zd = z.double()
+    lse = torch.logsumexp(zd, 2)
+    top = zd.amax(2)
+    s = (lse - top + 1e-6 * torch.randn(B, K, generator=g).double()).float()
+    best, order = torch.sort(s.double() + (top - lse), 1, descending=True)
+    n = min(K, 4)
+    gap = best[:, :n] - torch.cat([best[:, 1:], torch.full((B, 1), -1.0)], 1)[:, :n]
+    # second candidates of a beam lie in between where a row has its maximum twice
+    alone = ((zd == top[..., None]).sum(2) == 1).all(1) & (gap > 2.5 * FINE).all(1)
+    assert alone.double().mean() > 0.5 or K > 8
+    wide = torch.zeros(B, K, V + 3, dtype=BF16, device="cuda")
+    wide[:, :, 3:] = z.cuda()
+    score, parent, token = fm.beam_select(wide[:, :, 3:], s.cuda(), n)
+    want = torch.gather(zd.argmax(2), 1, order)[:, :n]
+    assert torch.equal(parent.cpu()[alone], order[:, :n][alone])
+    assert torch.equal(token.cpu()[alone], want[alone])
+    err = (score.cpu().double() - best[:, :n]).abs()[alone]
+    assert alone.any() and (err <= bound(V)).all()
