@@ -21,10 +21,10 @@
 // the launch, the rest a chain: a row's part, the lists of a block, of the cluster, of the beams,
 // 0.7 the look for close ones); 64 x 8 of 50001 in fp32, 16 candidates, a fifth of the beams
 // finished, 30.3 us, 82 MB at 2.7 TB/s (40 % of a copy's rate), and 44 where an element has
-// close candidates (4 of 60 inputs): an SM with work issues in half of its cycles, about 20
+// close candidates (4 of 60 inputs): an SM with work issues in 35 % of its cycles, 17
 // instructions a logit, half of them to load, compare and sum it, half for the lists, which a
 // warp of 12 parts of a row changes in most of them; and 256 blocks do not spread evenly over
-// 152 SMs.  64 x 8 of 32000 in bf16 20.6 us.
+// 152 SMs.  64 x 8 of 32000 in bf16 20.6 us, 1 x 4 of 150000 16, 1 x 32 of 50000 52.
 //
 // beam_reorder: rows of up to 16 arrays, t[b, k] = t[b, parent[b, k]] in place, one
 // launch.  A thread holds its bytes of every beam that changes in registers before
@@ -512,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (list < key) list = lane == 0 || up > key ? key : up;
         };
         // few lanes: the warp goes through each one's logits (read again: a register of a
-        // place known at run time is none).  (64 x 8 of 50001: 34.3 us; 35.2 without, 35.7 with
-        // up to 8 lanes.)
+        // place known at run time is none).  (64 x 8 of 50001, 16 candidates: 32.1 us; 33.1
+        // without, 33.7 with up to 8 lanes.  1 x 32 of 50000: 51.2; 53.6 and 52.8.  1 x 4: alike.)
         const unsigned who = __ballot_sync(kAll, top >= v);
         if (last != 0 && __popc(who) <= kFew) {
           for (unsigned w = who; w != 0; w &= w - 1) {
@@ -550,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         const int count = __shfl_sync(kAll, before, 31);
         before -= __popc(mask);
-        // one by one into their places (64 x 8 beams of 32000 took 24.6 us, and 26.4 sorting
-        // them always)
+        // one by one into their places (64 x 8 beams of 50001 32.1 us, 32.5 sorting them
+        // always; of 32000 in bf16 20.1 and 20.5; 1 x 4 alike)
         if (count <= 6) {
           uint64_t mine = pop();
           for (unsigned act; (act = __ballot_sync(kAll, mine != 0)) != 0;) {
@@ -789,13 +789,14 @@ int launch_beam_select(const void *logits, int64_t row, const float *scores,
   SelectArgs a{logits, row, scores, finished, score, parent, token, K, V, n, pad, 0,
                lse_near(V)};
   // a beam's row has NT warps' work; as many blocks as run at once (two an SM), no more
-  // than have any.  (One element of 4 beams of 32000: 10.0 us on 8 blocks, 20.7 on one.)
+  // than have any.  (One element of 4 beams of 32000: 10.1 us on 8 blocks, 20.0 on one; 64 x 8
+  // 20.1 on 4 blocks each, 37.5 on one.)
   const int64_t NT = ((int64_t)V + TASK - 1) / TASK;
   int NC = 1;
   while (NC < kBeamCluster && (int64_t)B * 2 * NC <= 2 * 152 && NC * kWarps < NT * K) NC *= 2;
   // warps that share a beam: a warp's first task of a row costs about twice the others'
-  // (its list begins).  64 x 8 beams of 32000: 24.6 us; 51.9 with one warp a beam, 35.7 with
-  // all of a cluster's warps on every beam.  1 x 32 of 50000: 59.9; 86 and 178.
+  // (its list begins).  64 x 8 beams of 32000: 20.1 us; 45.3 with one warp a beam, 30.2 with
+  // all of a cluster's warps on every beam.  1 x 32 of 50000: 51.2; 77 and 172.
   int64_t least = INT64_MAX;
   for (int group = 1; group <= NC * kWarps; group *= 2) {
     const int64_t groups = NC * kWarps / group;
@@ -807,7 +808,7 @@ int launch_beam_select(const void *logits, int64_t row, const float *scores,
   const auto fits = [&](int bytes) {
     return at % bytes == 0 && ((int64_t)V * el) % bytes == 0 && (row * el) % bytes == 0;
   };
-  if (bf16) {  // (64 x 8 beams of 32000: 24.6 us by 16 bytes, 25.4 by 4)
+  if (bf16) {  // (64 x 8 beams of 32000: 20.1 us by 16 bytes, 20.6 by 4)
     if (fits(16)) return select<__nv_bfloat16, 16>(a, B, NC, stream);
     if (fits(4)) return select<__nv_bfloat16, 4>(a, B, NC, stream);
     return select<__nv_bfloat16, 2>(a, B, NC, stream);

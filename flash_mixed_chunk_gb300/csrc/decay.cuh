@@ -113,8 +113,8 @@ __device__ __forceinline__ bool decay_grows(const DecayRate &r, int len) {
 }
 // The recurrence itself, for such a head: a whole sequence's unit by one block of NT threads, W
 // columns of v, from state_in to state_out, with zeros behind the end.  The state lies in shared
-// memory, sm: [dk][W], behind it the NT threads' sums of two tokens.  A thread has a column and every NT / W-th
-// row, the rows' sums are joined in a fixed order.
+// memory, sm: [dk][W], behind it the NT threads' sums of two tokens.  A thread has a column and
+// every NT / W-th row, the rows' sums are joined in a fixed order.
 template <typename T, int NT, int W>
 __device__ __noinline__ void decay_tokens(const DecayArgs &a, int b, int h, int vt, int len,
                                           float lam, float *sm) {

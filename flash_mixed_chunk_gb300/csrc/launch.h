@@ -454,9 +454,9 @@ __host__ __device__ constexpr int decay_floats(int dk) {
 }
 // As many segments as fill the blocks that the SMs hold (three each, or what their shared
 // memory has room for), of 64 tokens at least (a segment's start costs about as much) and 64
-// of them at most.  16-bit 2 x 8192 tokens, 12 heads of 33 x 65: 394 us, 500 with two blocks an
-// SM; 1 x 4000, 8 heads of 200 x 150, where one fits: 572 us, 710 cut for three; 3 x 517, 6
-// heads of 33, uncut: 82 us for 31.  (Before the loads' later changes, both sides alike.)
+// of them at most.  16-bit 2 x 8192 tokens, 12 heads of 33 x 65: 397 us, 580 with two blocks an
+// SM, 1318 uncut; 1 x 4000, 8 heads of 200 x 150, where one fits: 471 us, 563 cut for three; 3 x
+// 517, 6 heads of 33, fp32: 25 us, uncut 76.
 inline DecaySplit decay_split_simt(int B, int T, int H, int dk, int dv) {
   const int nvt = (dv + 63) / 64;
   const int64_t heads = (int64_t)B * H * nvt;
@@ -476,8 +476,8 @@ inline size_t decay_bytes_simt(int B, int T, int H, int dk, int dv) {
 // holds a unit's state of 128 x 128.
 constexpr size_t kDecaySlot = 128 * 128;
 // What the maps of its loads take, and its shared memory (dk <= 128).  It is the faster one
-// from single tokens on: 12 heads of 64, 1 token 7.1 us against 7.8, 37 tokens 7.3 against 13.4,
-// 512 tokens 16 against 40; 2 x 8192 63 against 349.
+// from single tokens on: 12 heads of 64, 1 token 6.6 us against 7.0, 37 tokens 6.8 against 12.8,
+// 512 tokens 12.8 against 25.9; 2 x 8192 60 against 275 (calls replayed from a graph).
 inline bool decay_tc(const DecayArgs &a) {
   if (!a.bf16 || a.dk % 8 || a.dv % 8 || a.dk > 128) return false;
   const auto fits = [](const void *p, const int64_t *s, int B, int T, int heads) {
@@ -491,8 +491,8 @@ inline bool decay_tc(const DecayArgs &a) {
 }
 // As many segments as make the two launches shortest, counted in halves of a chunk of the
 // second launch: a chunk of the first one (k and v alone) is one, its start four, the second's
-// start six.  12 heads of 128: 512 tokens in 4 segments 17.7 us, uncut 23.4; 1024 in 8 22.3 and
-// 38.3; 256 uncut 16.0, in two 15.8.  24 heads, 2 x 8192 tokens of 64 in 6 63, uncut 182.
+// start six.  12 heads of 128: 512 tokens in 4 segments 15.4 us, uncut 21.0; 1024 in 8 21.4 and
+// 35.6; 256 uncut 13.8, in two 13.9.  24 heads, 2 x 8192 tokens of 64 in 6 60, uncut 172.
 inline DecaySplit decay_split_tc(int B, int T, int H, int dv) {
   const int nvt = (dv + 127) / 128;
   const int64_t heads = (int64_t)B * H * nvt, chunks = ((int64_t)T + 127) / 128;
