@@ -17,14 +17,14 @@
 // memory, in a fixed order.  Rows of one call are cut the same way, so that equal rows
 // give equal sums and the tie goes to the lower beam.
 //
-// Measured (calls replayed from a graph): one element, 4 beams of 32000 in bf16, 10.5 us (2 of
+// Measured (calls replayed from a graph): one element, 4 beams of 32000 in bf16, 10.3 us (2 of
 // the launch, the rest a chain: a row's part, the lists of a block, of the cluster, of the beams,
-// 0.7 the look for close ones); 64 x 8 of 50001 in fp32, 16 candidates, a fifth of the beams
-// finished, 30.3 us, 82 MB at 2.7 TB/s (40 % of a copy's rate), and 44 where an element has
+// 0.6 the look for close ones); 64 x 8 of 50001 in fp32, 16 candidates, a fifth of the beams
+// finished, 30.0 us, 82 MB at 2.7 TB/s (41 % of a copy's rate), and 44 where an element has
 // close candidates (4 of 60 inputs): an SM with work issues in 35 % of its cycles, 17
 // instructions a logit, half of them to load, compare and sum it, half for the lists, which a
 // warp of 12 parts of a row changes in most of them; and 256 blocks do not spread evenly over
-// 152 SMs.  64 x 8 of 32000 in bf16 20.6 us, 1 x 4 of 150000 16, 1 x 32 of 50000 52.
+// 152 SMs.  64 x 8 of 32000 in bf16 20.4 us, 1 x 4 of 150000 16, 1 x 32 of 50000 52.
 //
 // beam_reorder: rows of up to 16 arrays, t[b, k] = t[b, parent[b, k]] in place, one
 // launch.  A thread holds its bytes of every beam that changes in registers before
@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_launch_dependents();
 
   const float *scores = a.scores + b * K;
-  const uint8_t *finished = a.finished == nullptr ? nullptr : a.finished + b * K;
+  const unsigned finished =
+      a.finished == nullptr ? 0 : __ballot_sync(kAll, lane < K && a.finished[b * K + lane]);
   const int me = rank * kWarps + warp;
   const int groups = NC * kWarps / a.group, in_group = me % a.group;
   // the warps of this block that share a beam, and how many of its n a warp answers for
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int k = me / a.group; k < K; k += groups) {
     uint64_t list = 0;  // 0: no key
     float m = -kInf, s = 0.f, rest = 0.f;
-    if (isfinite(scores[k]) && !(finished != nullptr && finished[k])) {
+    if (isfinite(scores[k]) && !(finished >> k & 1)) {
       const T *row = static_cast<const T *>(a.logits) + (b * K + k) * a.row;
       Task<T, BYTES> task;
       if (in_group < NT) task.load(row, a.V, in_group, lane);
@@ -602,7 +603,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_wait();
   // The first block joins the lists.  The others wait to hear that nothing is unsure, or help.
   uint64_t *const lists = keys, *const found = keys + K * n;  // [K][n] each: keys, candidates
-  const auto done = [&](int k) { return finished != nullptr && finished[k]; };
   if (rank == 0) {
     for (int k = warp; k < K; k += kWarps) {
       const uint64_t list = merge_lists(keys_got + (size_t)k * kBeamCluster * n, NC, n, n, lane);
@@ -618,12 +618,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   for (bool again = false;; again = true) {
     uint64_t best = 0, where = 0;  // a lane's place in the list, by value, then the lower index
+    int beam = 0;                  // (of it, in the first warp)
     if (rank == 0) {
       // a warp's beams: the n best of each as candidates, and of them the n best
       for (int k = warp; k < K; k += kWarps) {
         const uint64_t list = lane < n ? lists[k * n + lane] : 0;
         uint64_t c = 0, flat = (uint64_t)k * a.V + key_index(list);
-        if (done(k)) {
+        if (finished >> k & 1) {
           if (lane == 0 && isfinite(scores[k])) c = order_of((double)scores[k]);
           flat = (uint64_t)k * a.V + a.pad;
         } else if (list != 0) {
@@ -644,18 +645,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (warp < half)
           merge_pairs(best, where, list_c[warp * 32 + lane], list_at[warp * 32 + lane], lane);
       }
+      if (warp == 0) beam = (int)(where / (uint32_t)a.V);
       if (!again && K > 1) {
         // Neighbours of different beams in the list that are too close, and candidates of other
         // beams that are too close to its last: both beams are unsure.  (Whatever else could
         // change places has such a pair between.)
         if (warp == 0) {
-          const int beam = (int)(where / (uint32_t)a.V);
           const double c = value_of(best);
           const uint64_t least = order_of(c - a.near), next = __shfl_down_sync(kAll, best, 1);
           const int beam2 = __shfl_down_sync(kAll, beam, 1);
           unsigned mask = 0;
           if (lane + 1 < n && next != 0 && beam != beam2 && next >= least)
-            mask = (done(beam) ? 0u : 1u << beam) | (done(beam2) ? 0u : 1u << beam2);
+            mask = (1u << beam | 1u << beam2) & ~finished;
           mask = __reduce_or_sync(kAll, mask);
           if (lane == 0) unsure = mask;
           if (lane == n - 1) {
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int k = warp; k < K; k += kWarps) {
             const uint64_t c = found[k * n + lane];
             if (k != border_beam && c >= border[0] && c <= border[1])
-              mask |= (done(k) ? 0u : 1u << k) | (done(border_beam) ? 0u : 1u << border_beam);
+              mask |= (1u << k | 1u << border_beam) & ~finished;
           }
         if (__syncthreads_or((int)mask)) {
           if (mask != 0) atomicOr(&unsure, mask);
@@ -696,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == 0) {
       if (best != 0 && lane < n) {
         a.score[b * n + lane] = (float)value_of(best);
-        a.parent[b * n + lane] = (int64_t)(where / (uint32_t)a.V);
-        a.token[b * n + lane] = (int64_t)(where % (uint32_t)a.V);
+        a.parent[b * n + lane] = beam;
+        a.token[b * n + lane] = (int64_t)(where - (uint64_t)beam * a.V);
       } else if (lane < n) {  // a place without a candidate
         a.score[b * n + lane] = -kInf;
         a.parent[b * n + lane] = lane % K;
